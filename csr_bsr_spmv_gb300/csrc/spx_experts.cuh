@@ -1,0 +1,105 @@
+// spx_experts.cuh -- what the routed-expert kernels share: element types and
+// their conversions, the tested row range of an expert, the alignment of rows.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "spx_internal.h"
+
+namespace spx_exp {
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+
+template <class V>
+__device__ __forceinline__ V from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) {
+    return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) {
+    return __float2half_rn(v);
+}
+
+// Rows [lo, hi) of expert e, whatever the offsets hold: inside [0, S], lo <= hi.
+__device__ __forceinline__ void expert_rows(const int* __restrict__ offsets, int e, int S, int& lo, int& hi) {
+    lo = min(max(__ldg(offsets + e), 0), S);
+    hi = min(max(__ldg(offsets + e + 1), lo), S);
+}
+
+inline size_t type_bytes(spx_type t) { return t == SPX_F32 ? 4 : t == SPX_I8 ? 1 : 2; }
+inline bool is_float_type(spx_type t) { return t == SPX_F32 || t == SPX_BF16 || t == SPX_F16; }
+inline bool is_half_type(spx_type t) { return t == SPX_BF16 || t == SPX_F16; }
+
+// Largest of 16, 8, ..., `least` bytes that divides all of them.
+inline int copy_width(uint64_t bits, int least) {
+    int v = 16;
+    while (v > least && bits % v) v >>= 1;
+    return v;
+}
+inline uint64_t addr(const void* p) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p)); }
+
+}  // namespace spx_exp
+
+namespace spx_exp {
+
+// Row tile `tile` of height TM over the experts' rows, experts in order, the
+// rows from offsets[E] on as one more "expert" E: which expert, its rows
+// [r0, hi).  False when there is no such tile.  One full warp.
+__device__ __forceinline__ bool warp_find_tile(const int* __restrict__ offsets, int E, int S, int TM, int tile, int& e,
+                                               int& r0, int& hi) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int e0 = 0; e0 <= E; e0 += 32) {
+        int lo = 0, up = 0;
+        if (e0 + lane < E) expert_rows(offsets, e0 + lane, S, lo, up);
+        else if (e0 + lane == E) lo = min(max(__ldg(offsets + E), 0), S), up = S;
+        const int n = (up - lo + TM - 1) / TM;
+        int inc = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        const unsigned at = __ballot_sync(0xffffffffu, tile < base + inc);
+        if (at) {
+            const int src = __ffs(at) - 1;
+            const int first = base + __shfl_sync(0xffffffffu, inc - n, src);
+            e = e0 + src;
+            r0 = __shfl_sync(0xffffffffu, lo, src) + (tile - first) * TM;
+            hi = __shfl_sync(0xffffffffu, up, src);
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return false;
+}
+
+// No more row tiles than this, whatever the offsets.
+inline long long max_row_tiles(int E, int S, int TM) { return (S + TM - 1) / TM + static_cast<long long>(E) + 1; }
+
+// Sums in plain CUDA-core arithmetic, for arrays the copy engine cannot read
+// (rows or bases off 16-byte boundaries): spx_experts_simt.cu.
+struct SimtGemm {
+    const void *L, *R;             // the factors: out[i, j] = sum_r L(i, r) * R(j, r)
+    long long li, lr, rj, rr, re;  // element strides; re: of R between experts
+    void* C;
+    long long ldc, ce;             // row pitch of C, and its stride between experts
+    const float *row_scale, *col_scale;  // 8-bit integers only: [S], [E * NJ]
+    const int* offsets;            // NULL: one expert with all S rows
+    int E, S, NI, NJ, NR;          // rows of experts run over i (by_rows) or over r
+    bool by_rows;
+};
+spx_status simt_gemm(const SimtGemm& g, spx_type type, spx_type c_type, cudaStream_t st);
+
+}  // namespace spx_exp

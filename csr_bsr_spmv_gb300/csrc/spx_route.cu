@@ -1,0 +1,562 @@
+// spx_route.cu -- routed experts: the tokens' slots sorted by expert, tokens
+// gathered into that order, the experts' rows returned weighted, and the
+// gradients of the return.
+//
+// The sort is a stable counting sort with E buckets.  Each warp owns a run of
+// consecutive slots: it counts them per expert (match_any finds the lanes of
+// one expert, one lane adds their number to the warp's own counters), the
+// counters of all warps before it give its first places, and a second pass
+// over the same slots hands them out in order.  Nothing is atomic, so places
+// do not depend on timing.
+//
+// Gather, return and gradient are bound by HBM: every row is one contiguous
+// copy.  All three are driven by the token, not by the sorted place: a token's
+// row (X, Y or dY) is then read or written exactly once and its k partners
+// are whole rows at scattered places, which cost no more than ordered ones
+// because a row is far longer than a DRAM burst.
+#include <algorithm>
+
+#include "spx_experts.cuh"
+
+using namespace spx_exp;
+
+namespace {
+
+// ---------------------------------------------------------------- the sort
+
+struct Ids {
+    const void* p;
+    long long lde;
+    int k, bytes;
+};
+
+// Expert of flat slot i, -1 when it is none.
+__device__ __forceinline__ int id_of(const Ids& x, int i, int E) {
+    const long long at = x.lde == x.k ? i : static_cast<long long>(i / x.k) * x.lde + i % x.k;
+    if (x.bytes == 4) {
+        const int e = __ldg(static_cast<const int*>(x.p) + at);
+        return e >= 0 && e < E ? e : -1;
+    }
+    const long long e = __ldg(static_cast<const long long*>(x.p) + at);
+    return e >= 0 && e < E ? static_cast<int>(e) : -1;
+}
+
+// This warp's run of the block's slots [b0, b1): whole groups of 32 lanes.
+__device__ __forceinline__ void warp_run(int b0, int b1, int& w0, int& w1) {
+    const int nw = blockDim.x >> 5, w = threadIdx.x >> 5;
+    const int per = ((b1 - b0 + 32 * nw - 1) / (32 * nw)) * 32;
+    w0 = min(b0 + w * per, b1);
+    w1 = min(w0 + per, b1);
+}
+
+// counts[w][e] = slots of expert e in warp w's run.
+__device__ __forceinline__ void count_run(const Ids& x, int E, int w0, int w1, int* wc) {
+    const int lane = threadIdx.x & 31;
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+        const int e = i < w1 ? id_of(x, i, E) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && lane == __ffs(same) - 1) wc[e] += __popc(same);
+        __syncwarp();
+    }
+}
+
+__global__ void route_count_kernel(Ids x, int S, int E, int per, int* __restrict__ hist) {
+    extern __shared__ int sm[];
+    const int nw = blockDim.x >> 5, w = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < nw * E; i += blockDim.x) sm[i] = 0;
+    __syncthreads();
+    const int b0 = blockIdx.x * per, b1 = min(S, b0 + per);
+    int w0, w1;
+    warp_run(b0, b1, w0, w1);
+    count_run(x, E, w0, w1, sm + w * E);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int n = 0;
+        for (int v = 0; v < nw; ++v) n += sm[v * E + e];
+        hist[blockIdx.x * E + e] = n;
+    }
+}
+
+// hist == NULL: one block holds all slots.
+__global__ void route_place_kernel(Ids x, int S, int E, int per, const int* __restrict__ hist,
+                                   int* __restrict__ offsets, int* __restrict__ slot, int* __restrict__ pos) {
+    extern __shared__ int sm[];  // counters of each warp, then E totals
+    const int nw = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* tot = sm + nw * E;
+    for (int i = threadIdx.x; i < nw * E; i += blockDim.x) sm[i] = 0;
+    __syncthreads();
+    const int b0 = blockIdx.x * per, b1 = min(S, b0 + per);
+    int w0, w1;
+    warp_run(b0, b1, w0, w1);
+    count_run(x, E, w0, w1, sm + w * E);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int before = 0, all = 0;  // the expert's slots in earlier blocks, in all blocks
+        if (hist) {
+            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+                const int n = __ldg(hist + b * E + e);
+                if (b < static_cast<int>(blockIdx.x)) before += n;
+                all += n;
+            }
+        }
+        int run = before;
+        for (int v = 0; v < nw; ++v) {
+            const int n = sm[v * E + e];
+            sm[v * E + e] = run;
+            run += n;
+        }
+        tot[e] = hist ? all : run;
+    }
+    __syncthreads();
+    if (w == 0) {  // totals -> offsets
+        int carry = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int n = e0 + lane < E ? tot[e0 + lane] : 0;
+            int inc = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += up;
+            }
+            if (e0 + lane < E) {
+                tot[e0 + lane] = carry + inc - n;
+                if (blockIdx.x == 0) offsets[e0 + lane] = carry + inc - n;
+            }
+            carry += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) {
+            tot[E] = carry;
+            if (blockIdx.x == 0) offsets[E] = carry;
+        }
+    }
+    __syncthreads();
+    int* wc = sm + w * E;
+    for (int i = w0 + lane; i - lane < w1; i += 32) {
+        const int e = i < w1 ? id_of(x, i, E) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        int p = -1;
+        if (e >= 0) p = tot[e] + wc[e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) wc[e] += __popc(same);
+        __syncwarp();
+        if (i < w1) {
+            pos[i] = p;
+            if (p >= 0) slot[p] = i;
+        }
+    }
+    for (int p = tot[E] + blockIdx.x * blockDim.x + threadIdx.x; p < S; p += gridDim.x * blockDim.x) slot[p] = -1;
+}
+
+// One CTA sorts up to this many slots; beyond, a counting launch comes first
+// and each CTA takes a share.
+constexpr int kOneBlockSlots = 8192;
+constexpr int kMaxBlocks = 304;
+
+int route_blocks(long long S) {
+    if (S <= kOneBlockSlots) return 1;
+    return static_cast<int>(std::min<long long>((S + 4095) / 4096, kMaxBlocks));
+}
+
+// ---------------------------------------------------------------- rows in pieces of VB bytes
+
+template <int VB>
+struct Piece;
+template <>
+struct Piece<16> {
+    using T = uint4;
+};
+template <>
+struct Piece<4> {
+    using T = uint32_t;
+};
+template <>
+struct Piece<2> {
+    using T = uint16_t;
+};
+template <>
+struct Piece<1> {
+    using T = uint8_t;
+};
+
+template <class P>
+__device__ __forceinline__ P zero_piece() {
+    P z;
+    memset(&z, 0, sizeof(P));
+    return z;
+}
+
+// The values of one piece as floats, and back (rounded once each).
+template <class V, class P>
+__device__ __forceinline__ void widen(const P& p, float (&f)[sizeof(P) / sizeof(V)]) {
+    V v[sizeof(P) / sizeof(V)];
+    memcpy(v, &p, sizeof(P));
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(P) / sizeof(V)); ++i) f[i] = to_f(v[i]);
+}
+template <class V, class P>
+__device__ __forceinline__ P narrow(const float (&f)[sizeof(P) / sizeof(V)]) {
+    V v[sizeof(P) / sizeof(V)];
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(P) / sizeof(V)); ++i) v[i] = from_f<V>(f[i]);
+    P p;
+    memcpy(&p, v, sizeof(P));
+    return p;
+}
+
+constexpr int kRowThreads = 256;
+
+// A group of G threads (G divides 256) works on one token; grid.y splits the
+// row among groups when there are few tokens.
+struct RowShape {
+    int T, k, np, G;           // tokens, slots a token, pieces a row, threads a group
+    long long a, b;            // row pitch in pieces of the token-ordered and of the sorted array
+};
+
+__device__ __forceinline__ int place(const int* __restrict__ pos, long long i, int S) {
+    const int p = __ldg(pos + i);
+    return p >= 0 && p < S ? p : -1;
+}
+
+// Zeros in the sorted array's rows from offsets[E] on: token t's group takes every T-th of them.
+template <class P>
+__device__ __forceinline__ void zero_tail(const RowShape& r, const int* __restrict__ end, int t, int v0, int dv, P* out) {
+    const int S = r.T * r.k;
+    for (long long p = min(max(__ldg(end), 0), S) + static_cast<long long>(t); p < S; p += r.T)
+        for (int v = v0; v < r.np; v += dv) out[p * r.b + v] = zero_piece<P>();
+}
+
+template <int VB>
+__global__ void __launch_bounds__(kRowThreads)
+    route_gather_kernel(RowShape r, const int* __restrict__ pos, const int* __restrict__ end,
+                        const typename Piece<VB>::T* __restrict__ X, typename Piece<VB>::T* __restrict__ Xs) {
+    using P = typename Piece<VB>::T;
+    const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
+    if (t >= r.T) return;
+    const int S = r.T * r.k, v0 = blockIdx.y * r.G + threadIdx.x % r.G, dv = gridDim.y * r.G;
+    const P* x = X + t * r.a;
+    for (int v = v0; v < r.np; v += dv) {
+        const P piece = __ldg(x + v);
+        for (int j = 0; j < r.k; ++j) {
+            const int p = place(pos, static_cast<long long>(t) * r.k + j, S);
+            if (p >= 0) __stcs(Xs + p * r.b + v, piece);
+        }
+    }
+    zero_tail<P>(r, end, t, v0, dv, Xs);
+}
+
+constexpr int kSlotsAtOnce = 4;  // rows of one token in flight in a thread
+
+template <class V, int VB>
+__global__ void __launch_bounds__(kRowThreads)
+    route_combine_kernel(RowShape r, const int* __restrict__ pos, const float* __restrict__ weight,
+                         const typename Piece<VB>::T* __restrict__ Ys, typename Piece<VB>::T* __restrict__ Y) {
+    using P = typename Piece<VB>::T;
+    constexpr int N = VB / sizeof(V);
+    const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
+    if (t >= r.T) return;
+    const int S = r.T * r.k, v0 = blockIdx.y * r.G + threadIdx.x % r.G, dv = gridDim.y * r.G;
+    const long long i0 = static_cast<long long>(t) * r.k;
+    for (int v = v0; v < r.np; v += dv) {
+        float acc[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+        for (int j0 = 0; j0 < r.k; j0 += kSlotsAtOnce) {
+            P piece[kSlotsAtOnce];
+            float w[kSlotsAtOnce];
+            bool on[kSlotsAtOnce];
+#pragma unroll
+            for (int u = 0; u < kSlotsAtOnce; ++u) {
+                const int p = j0 + u < r.k ? place(pos, i0 + j0 + u, S) : -1;
+                on[u] = p >= 0;
+                if (on[u]) {
+                    piece[u] = __ldcs(Ys + p * r.b + v);
+                    w[u] = weight ? __ldg(weight + i0 + j0 + u) : 1.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kSlotsAtOnce; ++u) {
+                if (!on[u]) continue;
+                float f[N];
+                widen<V, P>(piece[u], f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] = fmaf(w[u], f[i], acc[i]);
+            }
+        }
+        Y[t * r.a + v] = narrow<V, P>(acc);
+    }
+}
+
+// dweight: a thread's products in pieces order, then a fixed tree over the
+// group's lanes and warps.
+template <class V, int VB>
+__global__ void __launch_bounds__(kRowThreads)
+    route_combine_grad_kernel(RowShape r, const int* __restrict__ pos, const int* __restrict__ end,
+                              const float* __restrict__ weight, const typename Piece<VB>::T* __restrict__ dY,
+                              long long ldys, const typename Piece<VB>::T* __restrict__ Ys,
+                              typename Piece<VB>::T* __restrict__ dYs, float* __restrict__ dw) {
+    using P = typename Piece<VB>::T;
+    constexpr int N = VB / sizeof(V);
+    __shared__ float part[kRowThreads / 32][kSlotsAtOnce];
+    const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
+    const bool live = t < r.T;
+    const int S = r.T * r.k, v0 = threadIdx.x % r.G;
+    const long long i0 = static_cast<long long>(t) * r.k;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int j0 = 0; j0 < r.k; j0 += kSlotsAtOnce) {
+        float dot[kSlotsAtOnce], w[kSlotsAtOnce];
+        int at[kSlotsAtOnce];
+#pragma unroll
+        for (int u = 0; u < kSlotsAtOnce; ++u) {
+            dot[u] = 0.f;
+            at[u] = live && j0 + u < r.k ? place(pos, i0 + j0 + u, S) : -1;
+            w[u] = at[u] >= 0 && weight ? __ldg(weight + i0 + j0 + u) : 1.f;
+        }
+        if (live) {
+            for (int v = v0; v < r.np; v += r.G) {
+                const P g = __ldg(dY + t * r.a + v);
+                P y[kSlotsAtOnce];
+                if (dw) {
+#pragma unroll
+                    for (int u = 0; u < kSlotsAtOnce; ++u)
+                        if (at[u] >= 0) y[u] = __ldcs(Ys + at[u] * ldys + v);
+                }
+                float gf[N];
+                widen<V, P>(g, gf);
+#pragma unroll
+                for (int u = 0; u < kSlotsAtOnce; ++u) {
+                    if (at[u] < 0) continue;
+                    float f[N];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) f[i] = w[u] * gf[i];
+                    __stcs(dYs + at[u] * r.b + v, narrow<V, P>(f));
+                    if (dw) {
+                        widen<V, P>(y[u], f);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) dot[u] = fmaf(gf[i], f[i], dot[u]);
+                    }
+                }
+            }
+        }
+        if (dw) {
+#pragma unroll
+            for (int u = 0; u < kSlotsAtOnce; ++u)
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], d);
+            if (r.G > 32) {
+                if (lane == 0)
+#pragma unroll
+                    for (int u = 0; u < kSlotsAtOnce; ++u) part[warp][u] = dot[u];
+                __syncthreads();
+            }
+            if (live && v0 < kSlotsAtOnce && j0 + v0 < r.k) {
+                float s = 0.f;
+                if (r.G > 32) {
+                    for (int x = 0; x < r.G / 32; ++x) s += part[warp + x][v0];
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kSlotsAtOnce; ++u)
+                        if (u == v0) s = dot[u];
+                }
+                dw[i0 + j0 + v0] = place(pos, i0 + j0 + v0, S) >= 0 ? s : 0.f;
+            }
+            if (r.G > 32) __syncthreads();
+        }
+    }
+    if (live) zero_tail<P>(r, end, t, v0, r.G, dYs);
+}
+
+// ---------------------------------------------------------------- host side
+
+// Threads a group: enough that a row is one step, no more than a CTA; a warp
+// at least (the weights' gradient reduces over warps).
+RowShape row_shape(int T, int k, int64_t np) {
+    RowShape r{};
+    r.T = T;
+    r.k = k;
+    r.np = static_cast<int>(np);
+    r.G = 32;
+    while (r.G < kRowThreads && r.G < np) r.G <<= 1;
+    return r;
+}
+
+dim3 row_grid(const RowShape& r, bool split) {
+    const int bx = (r.T + kRowThreads / r.G - 1) / (kRowThreads / r.G);
+    // few tokens: their rows are cut so that a thread has one piece
+    const int steps = (r.np + r.G - 1) / r.G;
+    const int by = split && bx < 608 ? std::min(steps, 608 / bx + 1) : 1;
+    return dim3(bx, by);
+}
+
+spx_status check_rows(int32_t T, int32_t k, int32_t H) {
+    if (T < 0 || k <= 0 || H < 0) return SPX_ERR_ARG;
+    if (static_cast<int64_t>(T) * k > kI32Max) return SPX_ERR_INDEX_RANGE;
+    return SPX_OK;
+}
+
+template <class V>
+int piece_bytes(uint64_t bits) {
+    const int v = copy_width(bits, static_cast<int>(sizeof(V)));
+    return v == 8 ? 4 : v;  // the kernels come in 16-byte, 4-byte and element-wise pieces
+}
+
+template <class V, int VB>
+void combine_launch(RowShape r, const int32_t* pos, const float* weight, const void* Ys, void* Y, cudaStream_t st) {
+    using P = typename Piece<VB>::T;
+    route_combine_kernel<V, VB><<<row_grid(r, true), kRowThreads, 0, st>>>(r, pos, weight, static_cast<const P*>(Ys),
+                                                                          static_cast<P*>(Y));
+}
+
+template <class V>
+spx_status combine(int T, int k, int H, const int32_t* pos, const float* weight, const void* Ys, int64_t ldys, void* Y,
+                   int64_t ldy, cudaStream_t st) {
+    const uint64_t row = static_cast<uint64_t>(H) * sizeof(V), a = ldy * sizeof(V), b = ldys * sizeof(V);
+    const int vb = piece_bytes<V>(addr(Ys) | addr(Y) | row | a | b);
+    RowShape r = row_shape(T, k, static_cast<int64_t>(row / vb));
+    r.a = static_cast<long long>(a / vb);
+    r.b = static_cast<long long>(b / vb);
+    if (vb == 16) combine_launch<V, 16>(r, pos, weight, Ys, Y, st);
+    else if (vb == 4) combine_launch<V, 4>(r, pos, weight, Ys, Y, st);
+    else combine_launch<V, sizeof(V)>(r, pos, weight, Ys, Y, st);
+    spx_note_launches(1);
+    return spx_cuda_status(cudaGetLastError());
+}
+
+template <class V, int VB>
+void combine_grad_launch(RowShape r, const int32_t* pos, const int32_t* end, const float* weight, const void* dY,
+                         long long ldys, const void* Ys, void* dYs, float* dw, cudaStream_t st) {
+    using P = typename Piece<VB>::T;
+    route_combine_grad_kernel<V, VB><<<row_grid(r, false), kRowThreads, 0, st>>>(
+        r, pos, end, weight, static_cast<const P*>(dY), ldys, static_cast<const P*>(Ys), static_cast<P*>(dYs), dw);
+}
+
+template <class V>
+spx_status combine_grad(int T, int k, int H, const int32_t* pos, const int32_t* end, const float* weight,
+                        const void* dY, int64_t lddy, const void* Ys, int64_t ldys, void* dYs, int64_t lddys,
+                        float* dw, cudaStream_t st) {
+    const uint64_t row = static_cast<uint64_t>(H) * sizeof(V), a = lddy * sizeof(V), b = lddys * sizeof(V);
+    const uint64_t y = dw ? ldys * sizeof(V) : 0;
+    const int vb = piece_bytes<V>(addr(dY) | addr(dYs) | (dw ? addr(Ys) : 0) | row | a | b | y);
+    RowShape r = row_shape(T, k, static_cast<int64_t>(row / vb));
+    r.a = static_cast<long long>(a / vb);
+    r.b = static_cast<long long>(b / vb);
+    const long long ly = static_cast<long long>(y / vb);
+    if (vb == 16) combine_grad_launch<V, 16>(r, pos, end, weight, dY, ly, Ys, dYs, dw, st);
+    else if (vb == 4) combine_grad_launch<V, 4>(r, pos, end, weight, dY, ly, Ys, dYs, dw, st);
+    else combine_grad_launch<V, sizeof(V)>(r, pos, end, weight, dY, ly, Ys, dYs, dw, st);
+    spx_note_launches(1);
+    return spx_cuda_status(cudaGetLastError());
+}
+
+template <int VB>
+void gather_launch(RowShape r, const int32_t* pos, const int32_t* end, const void* X, void* Xs, cudaStream_t st) {
+    using P = typename Piece<VB>::T;
+    route_gather_kernel<VB><<<row_grid(r, true), kRowThreads, 0, st>>>(r, pos, end, static_cast<const P*>(X),
+                                                                      static_cast<P*>(Xs));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spx_route_scratch_bytes(int32_t T, int32_t k, int32_t E) {
+    if (T < 0 || k <= 0 || E <= 0) return 0;
+    const int nb = route_blocks(static_cast<int64_t>(T) * k);
+    return nb == 1 ? 0 : sizeof(int32_t) * static_cast<size_t>(nb) * static_cast<size_t>(E);
+}
+
+spx_status spx_route_build(int32_t T, int32_t k, int32_t E, const void* expert, int32_t id_bytes, int64_t lde,
+                           int32_t* offsets, int32_t* slot, int32_t* pos, void* scratch, size_t scratch_bytes,
+                           spx_stream_t stream) {
+    if (T < 0 || k <= 0 || E <= 0 || (id_bytes != 4 && id_bytes != 8)) return SPX_ERR_ARG;
+    if (E > SPX_MAX_EXPERTS) return SPX_ERR_UNSUPPORTED;
+    const int64_t S64 = static_cast<int64_t>(T) * k;
+    if (S64 > kI32Max - 1024) return SPX_ERR_INDEX_RANGE;  // the kernels step past the end by up to a CTA
+    if (!offsets || (S64 > 0 && (!expert || !slot || !pos || lde < k))) return SPX_ERR_ARG;
+    if (!spx_aligned(offsets, 4) || !spx_aligned(slot, 4) || !spx_aligned(pos, 4) ||
+        !spx_aligned(expert, static_cast<size_t>(id_bytes)))
+        return SPX_ERR_ALIGN;
+    const int S = static_cast<int>(S64), nb = route_blocks(S64);
+    const size_t need = spx_route_scratch_bytes(T, k, E);
+    if (need > 0 && (!scratch || scratch_bytes < need)) return SPX_ERR_ARG;
+    if (need > 0 && !spx_aligned(scratch, 4)) return SPX_ERR_ALIGN;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const Ids ids{expert, lde, k, id_bytes};
+    // warps a CTA: one for each 32 slots, as far as their counters fit 48 KB
+    const int per = nb == 1 ? S : static_cast<int>((S64 + nb - 1) / nb);
+    int nw = 1;
+    while (nw < 32 && 32 * nw < per && (2 * nw + 1) * (E + 1) * 4 <= 48 * 1024) nw *= 2;
+    const size_t smem = sizeof(int32_t) * (static_cast<size_t>(nw) * E + E + 1);
+    if (nb > 1) route_count_kernel<<<nb, 32 * nw, smem, st>>>(ids, S, E, per, static_cast<int*>(scratch));
+    route_place_kernel<<<nb, 32 * nw, smem, st>>>(ids, S, E, per, nb > 1 ? static_cast<const int*>(scratch) : nullptr,
+                                                  offsets, slot, pos);
+    spx_note_launches(nb > 1 ? 2 : 1);
+    return spx_cuda_status(cudaGetLastError());
+}
+
+spx_status spx_route_gather(int32_t T, int32_t k, int32_t H, spx_type type, const int32_t* pos,
+                            const int32_t* offsets_end, const void* X, int64_t ldx, void* Xs, int64_t ldxs,
+                            spx_stream_t stream) {
+    const spx_status c = check_rows(T, k, H);
+    if (c != SPX_OK) return c;
+    if (!is_float_type(type) && type != SPX_I8) return SPX_ERR_ARG;
+    if (T == 0 || H == 0) return SPX_OK;
+    if (!pos || !offsets_end || !X || !Xs || ldx < H || ldxs < H) return SPX_ERR_ARG;
+    const size_t eb = type_bytes(type);
+    if (!spx_aligned(pos, 4) || !spx_aligned(offsets_end, 4) || !spx_aligned(X, eb) || !spx_aligned(Xs, eb))
+        return SPX_ERR_ALIGN;
+    const uint64_t row = static_cast<uint64_t>(H) * eb, a = ldx * eb, b = ldxs * eb;
+    int vb = copy_width(addr(X) | addr(Xs) | row | a | b, static_cast<int>(eb));
+    if (vb == 8) vb = 4;
+    if (row / vb > static_cast<uint64_t>(kI32Max)) return SPX_ERR_INDEX_RANGE;
+    RowShape r = row_shape(T, k, static_cast<int64_t>(row / vb));
+    r.a = static_cast<long long>(a / vb);
+    r.b = static_cast<long long>(b / vb);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (vb == 16) gather_launch<16>(r, pos, offsets_end, X, Xs, st);
+    else if (vb == 4) gather_launch<4>(r, pos, offsets_end, X, Xs, st);
+    else if (vb == 2) gather_launch<2>(r, pos, offsets_end, X, Xs, st);
+    else gather_launch<1>(r, pos, offsets_end, X, Xs, st);
+    spx_note_launches(1);
+    return spx_cuda_status(cudaGetLastError());
+}
+
+spx_status spx_route_combine(int32_t T, int32_t k, int32_t H, spx_type type, const int32_t* pos, const float* weight,
+                             const void* Ys, int64_t ldys, void* Y, int64_t ldy, spx_stream_t stream) {
+    const spx_status c = check_rows(T, k, H);
+    if (c != SPX_OK) return c;
+    if (!is_float_type(type)) return SPX_ERR_ARG;
+    if (T == 0 || H == 0) return SPX_OK;
+    if (!pos || !Ys || !Y || ldys < H || ldy < H) return SPX_ERR_ARG;
+    const size_t eb = type_bytes(type);
+    if (!spx_aligned(pos, 4) || !spx_aligned(weight, 4) || !spx_aligned(Ys, eb) || !spx_aligned(Y, eb))
+        return SPX_ERR_ALIGN;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (type == SPX_F32) return combine<float>(T, k, H, pos, weight, Ys, ldys, Y, ldy, st);
+    if (type == SPX_BF16) return combine<__nv_bfloat16>(T, k, H, pos, weight, Ys, ldys, Y, ldy, st);
+    return combine<__half>(T, k, H, pos, weight, Ys, ldys, Y, ldy, st);
+}
+
+spx_status spx_route_combine_grad(int32_t T, int32_t k, int32_t H, spx_type type, const int32_t* pos,
+                                  const int32_t* offsets_end, const float* weight, const void* dY, int64_t lddy,
+                                  const void* Ys, int64_t ldys, void* dYs, int64_t lddys, float* dweight,
+                                  spx_stream_t stream) {
+    const spx_status c = check_rows(T, k, H);
+    if (c != SPX_OK) return c;
+    if (!is_float_type(type)) return SPX_ERR_ARG;
+    if (T == 0) return SPX_OK;
+    if (!pos || !offsets_end) return SPX_ERR_ARG;
+    if (H > 0 && (!dY || !dYs || lddy < H || lddys < H || (dweight && (!Ys || ldys < H)))) return SPX_ERR_ARG;
+    const size_t eb = type_bytes(type);
+    if (!spx_aligned(pos, 4) || !spx_aligned(offsets_end, 4) || !spx_aligned(weight, 4) || !spx_aligned(dweight, 4) ||
+        !spx_aligned(dY, eb) || !spx_aligned(dYs, eb) || (dweight && !spx_aligned(Ys, eb)))
+        return SPX_ERR_ALIGN;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (type == SPX_F32)
+        return combine_grad<float>(T, k, H, pos, offsets_end, weight, dY, lddy, Ys, ldys, dYs, lddys, dweight, st);
+    if (type == SPX_BF16)
+        return combine_grad<__nv_bfloat16>(T, k, H, pos, offsets_end, weight, dY, lddy, Ys, ldys, dYs, lddys, dweight,
+                                           st);
+    return combine_grad<__half>(T, k, H, pos, offsets_end, weight, dY, lddy, Ys, ldys, dYs, lddys, dweight, st);
+}
+
+}  // extern "C"

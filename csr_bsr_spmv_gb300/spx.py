@@ -187,6 +187,20 @@ def _load(path):
         "spx_spmm_bsr_planned_scratch_bytes": ([vp, i32], sz),
         "spx_spmm_bsr_planned": ([vp, i32, i32, i32, i32, i64, vp, vp, vp, i32, vp, i64, f32, f32, vp, i64, vp, sz,
                                   vp], ctypes.c_int),
+        "spx_route_scratch_bytes": ([i32, i32, i32], sz),
+        "spx_route_build": ([i32, i32, i32, vp, i32, i64, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+        "spx_route_gather": ([i32, i32, i32, ctypes.c_int, vp, vp, vp, i64, vp, i64, vp], ctypes.c_int),
+        "spx_route_combine": ([i32, i32, i32, ctypes.c_int, vp, vp, vp, i64, vp, i64, vp], ctypes.c_int),
+        "spx_route_combine_grad": ([i32, i32, i32, ctypes.c_int, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp],
+                                   ctypes.c_int),
+        "spx_gemm_grouped": ([i32, i32, i32, i32, vp, vp, i64, vp, i64, i64, ctypes.c_int, ctypes.c_int, vp, i64,
+                              ctypes.c_int, vp], ctypes.c_int),
+        "spx_gemm_grouped_wgrad": ([i32, i32, i32, i32, vp, vp, i64, vp, i64, ctypes.c_int, vp, i64, i64, ctypes.c_int,
+                                    vp], ctypes.c_int),
+        "spx_quant_rows_i8": ([i32, i32, ctypes.c_int, vp, i64, vp, i64, vp, vp], ctypes.c_int),
+        "spx_gemm_i8_scratch_bytes": ([i32, i32, i32, i32], sz),
+        "spx_gemm_i8": ([i32, i32, i32, i32, vp, vp, i64, vp, vp, i64, i64, vp, vp, i64, ctypes.c_int, vp, sz, vp],
+                        ctypes.c_int),
         "spx_gather_probe_blocks": ([], ctypes.c_int32),
         "spx_gather_probe": ([i64, vp, vp, vp, i32, vp, i32, vp], ctypes.c_int),
         "spx_last_device_error": ([vp], ctypes.c_int),
@@ -831,6 +845,229 @@ def spx_spmm_bsr(M: int, K: int, br: int, bc: int, bsr_row_ptr, bsr_col, bsr_val
     _check(_lib().spx_spmm_bsr(M, K, br, bc, nnzb, _ptr(bsr_row_ptr), _ptr(bsr_col), _ptr(bsr_val), N, _ptr(B),
                                B.stride(0), float(alpha), float(beta), _ptr(C), C.stride(0), _stream(stream)),
            "spx_spmm_bsr")
+    return C
+
+
+# ------------------------------------------------------------------ routed experts
+
+_SPX_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int8: 3}
+
+
+def _type(t: torch.Tensor) -> int:
+    code = _SPX_TYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{t.dtype}: float32, bfloat16, float16 or int8 is wanted")
+    return code
+
+
+def _new(shape, dtype, device, stream):
+    """An output or scratch tensor that belongs to the stream the call runs on, so that its memory is
+    not handed out again before that stream has passed the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t: torch.Tensor, what: str) -> int:
+    """Row pitch of a 2-D operand whose columns are adjacent."""
+    _require(t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1), f"{what} must be 2-D with unit column stride")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def _addr(t: torch.Tensor | None):
+    if t is None or not t.numel():
+        return None
+    _require(t.is_cuda, "the routed-expert calls take device tensors")
+    return t.data_ptr()
+
+
+@dataclass
+class Route:
+    """The slots of T tokens (k each) sorted by expert: int32 device tensors offsets[E + 1], slot[T * k]
+    (the flat slot at each sorted place, -1 past offsets[E]) and pos[T * k] (each slot's place, -1: dropped)."""
+    T: int
+    k: int
+    E: int
+    offsets: torch.Tensor
+    slot: torch.Tensor
+    pos: torch.Tensor
+
+    @property
+    def slots(self) -> int:
+        return self.T * self.k
+
+
+def spx_route_build(expert: torch.Tensor, E: int, stream=None, scratch: torch.Tensor | None = None) -> Route:
+    """Sort the slots of expert[T, k] (int32 or int64 ids; one outside [0, E), -1 say, is dropped) by expert."""
+    _require(expert.dtype in (torch.int32, torch.int64), "expert ids must be int32 or int64")
+    lde = _rows(expert, "expert")
+    T, k = expert.shape
+    lib, dev = _lib(), expert.device
+    S = T * k
+    block = _new(E + 1 + 2 * S, torch.int32, dev, stream)  # one allocation for the three arrays
+    offsets, slot, pos = block[:E + 1], block[E + 1:E + 1 + S], block[E + 1 + S:]
+    if scratch is None:
+        need = lib.spx_route_scratch_bytes(T, k, E)
+        if need:
+            scratch = _new(need // 4, torch.int32, dev, stream)
+    _check(lib.spx_route_build(T, k, E, _addr(expert), expert.element_size(), lde, offsets.data_ptr(), _addr(slot),
+                               _addr(pos), _addr(scratch), scratch.numel() * scratch.element_size() if scratch is not None else 0,
+                               _stream(stream)), "spx_route_build")
+    return Route(T, k, E, offsets, slot, pos)
+
+
+def _route_end(r: Route):
+    return r.offsets.data_ptr() + 4 * r.E
+
+
+def spx_route_gather(r: Route, X: torch.Tensor, Xs: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Xs[place of slot (t, j)] = X[t] (any of the four types), zeros past offsets[E]."""
+    ldx = _rows(X, "X")
+    _require(X.shape[0] == r.T, "X needs one row a token")
+    if Xs is None:
+        Xs = _new((r.slots, X.shape[1]), X.dtype, X.device, stream)
+    ldxs = _rows(Xs, "Xs")
+    _require(Xs.shape[0] == r.slots and Xs.shape[1] == X.shape[1] and Xs.dtype == X.dtype, "Xs needs one row a slot")
+    _check(_lib().spx_route_gather(r.T, r.k, X.shape[1], _type(X), _addr(r.pos), _route_end(r), _addr(X), ldx,
+                                   _addr(Xs), ldxs, _stream(stream)), "spx_route_gather")
+    return Xs
+
+
+def _weights(r: Route, weight):
+    if weight is None:
+        return None
+    _require(weight.dtype == torch.float32 and weight.is_contiguous() and weight.numel() == r.slots,
+             "weights must be float32, dense, one a slot")
+    return _addr(weight)
+
+
+def spx_route_combine(r: Route, Ys: torch.Tensor, weight: torch.Tensor | None = None, Y: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Y[t] = sum over t's kept slots of weight * Ys[place] (no weights: all ones, the gradient of spx_route_gather)."""
+    ldys = _rows(Ys, "Ys")
+    _require(Ys.shape[0] == r.slots, "Ys needs one row a slot")
+    if Y is None:
+        Y = _new((r.T, Ys.shape[1]), Ys.dtype, Ys.device, stream)
+    ldy = _rows(Y, "Y")
+    _require(Y.shape[0] == r.T and Y.shape[1] == Ys.shape[1] and Y.dtype == Ys.dtype, "Y needs one row a token")
+    _check(_lib().spx_route_combine(r.T, r.k, Ys.shape[1], _type(Ys), _addr(r.pos), _weights(r, weight), _addr(Ys),
+                                    ldys, _addr(Y), ldy, _stream(stream)), "spx_route_combine")
+    return Y
+
+
+def spx_route_combine_grad(r: Route, dY: torch.Tensor, Ys: torch.Tensor | None = None,
+                           weight: torch.Tensor | None = None, dYs: torch.Tensor | None = None, stream=None):
+    """Gradients of spx_route_combine: (dYs[T*k, H], dweight[T, k] fp32); without Ys only dYs (dweight None)."""
+    lddy = _rows(dY, "dY")
+    _require(dY.shape[0] == r.T, "dY needs one row a token")
+    ldys = 0
+    if Ys is not None:
+        ldys = _rows(Ys, "Ys")
+        _require(Ys.shape[0] == r.slots and Ys.shape[1] == dY.shape[1] and Ys.dtype == dY.dtype,
+                 "Ys needs one row a slot")
+    if dYs is None:
+        dYs = _new((r.slots, dY.shape[1]), dY.dtype, dY.device, stream)
+    lddys = _rows(dYs, "dYs")
+    _require(dYs.shape[0] == r.slots and dYs.shape[1] == dY.shape[1] and dYs.dtype == dY.dtype,
+             "dYs needs one row a slot")
+    dw = _new((r.T, r.k), torch.float32, dY.device, stream) if Ys is not None else None
+    _check(_lib().spx_route_combine_grad(r.T, r.k, dY.shape[1], _type(dY), _addr(r.pos), _route_end(r),
+                                         _weights(r, weight), _addr(dY), lddy, _addr(Ys), ldys, _addr(dYs), lddys,
+                                         _addr(dw), _stream(stream)), "spx_route_combine_grad")
+    return dYs, dw
+
+
+def _expert_weights(W: torch.Tensor, what: str):
+    _require(W.dim() == 3 and (W.stride(2) == 1 or W.shape[2] <= 1), f"{what} must be 3-D with unit stride in its last axis")
+    return (W.stride(1) if W.shape[1] > 1 else max(W.shape[2], W.stride(1))), (W.stride(0) if W.shape[0] > 1 else 0)
+
+
+def _offsets(offsets: torch.Tensor, E: int):
+    _require(offsets.dtype == torch.int32 and offsets.is_contiguous() and offsets.numel() == E + 1,
+             "offsets must be int32, dense, E + 1 of them")
+    return _addr(offsets)
+
+
+def spx_gemm_grouped(offsets: torch.Tensor, A: torch.Tensor, W: torch.Tensor, C: torch.Tensor | None = None,
+                     layout: str = "nk", dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """C[p] = A[p] times expert e's weights for its rows offsets[e] <= p < offsets[e+1], zeros past the last.
+    layout "nk": W[e] holds N output channels of K; "kn": K rows of N.  C in A's type or float32 (dtype)."""
+    lda = _rows(A, "A")
+    ldw, sw = _expert_weights(W, "W")
+    _require(layout in ("nk", "kn"), "layout must be 'nk' or 'kn'")
+    E, S = W.shape[0], A.shape[0]
+    N, K = (W.shape[1], W.shape[2]) if layout == "nk" else (W.shape[2], W.shape[1])
+    _require(A.shape[1] == K and W.dtype == A.dtype, "A and W do not fit")
+    if C is None:
+        C = _new((S, N), dtype or A.dtype, A.device, stream)
+    ldc = _rows(C, "C")
+    _require(C.shape[0] == S and C.shape[1] == N, "C must be S x N")
+    _check(_lib().spx_gemm_grouped(E, S, N, K, _offsets(offsets, E), _addr(A), lda, _addr(W), ldw, sw,
+                                   0 if layout == "nk" else 1, _type(A), _addr(C), ldc, _type(C), _stream(stream)),
+           "spx_gemm_grouped")
+    return C
+
+
+def spx_gemm_grouped_wgrad(offsets: torch.Tensor, G: torch.Tensor, A: torch.Tensor, dW: torch.Tensor | None = None,
+                           dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """dW[e] (N x K) = G_e^T A_e over expert e's rows of G (S x N) and A (S x K); A's type or float32 (dtype)."""
+    ldg, lda = _rows(G, "G"), _rows(A, "A")
+    E, S, N, K = offsets.numel() - 1, A.shape[0], G.shape[1], A.shape[1]
+    _require(G.shape[0] == S and G.dtype == A.dtype, "G and A do not fit")
+    if dW is None:
+        dW = _new((E, N, K), dtype or A.dtype, A.device, stream)
+    ldw, sw = _expert_weights(dW, "dW")
+    _require(dW.shape[0] == E and dW.shape[1] == N and dW.shape[2] == K, "dW must be E x N x K")
+    _check(_lib().spx_gemm_grouped_wgrad(E, S, N, K, _offsets(offsets, E), _addr(G), ldg, _addr(A), lda, _type(A),
+                                         _addr(dW), ldw, sw, _type(dW), _stream(stream)), "spx_gemm_grouped_wgrad")
+    return dW
+
+
+def spx_quant_rows_i8(X: torch.Tensor, Q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """(Q int8, scale fp32): each row divided by its largest magnitude / 127 and rounded to whole numbers."""
+    ldx = _rows(X, "X")
+    if Q is None:
+        Q = _new(X.shape, torch.int8, X.device, stream)
+    if scale is None:
+        scale = _new(X.shape[0], torch.float32, X.device, stream)
+    ldq = _rows(Q, "Q")
+    _require(Q.shape == X.shape and Q.dtype == torch.int8, "Q must be int8 of X's shape")
+    _require(scale.dtype == torch.float32 and scale.is_contiguous() and scale.numel() == X.shape[0],
+             "scale must be float32, dense, one a row")
+    _check(_lib().spx_quant_rows_i8(X.shape[0], X.shape[1], _type(X), _addr(X), ldx, _addr(Q), ldq, _addr(scale),
+                                    _stream(stream)), "spx_quant_rows_i8")
+    return Q, scale
+
+
+def spx_gemm_i8(Q: torch.Tensor, row_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
+                offsets: torch.Tensor | None = None, C: torch.Tensor | None = None, dtype: torch.dtype | None = None,
+                stream=None, scratch: torch.Tensor | None = None) -> torch.Tensor:
+    """C[p, n] = row_scale[p] * w_scale[n] * (Q[p] . W[n]), exact int32 sums.  W is N x K with w_scale[N], or with
+    offsets E x N x K with w_scale[E, N], each expert's weights for its rows.  C in dtype (default float32)."""
+    ldq = _rows(Q, "Q")
+    W3 = W if offsets is not None else W.unsqueeze(0)
+    ldw, sw = _expert_weights(W3, "W")
+    E, N, K = W3.shape
+    S = Q.shape[0]
+    _require(Q.dtype == torch.int8 and W.dtype == torch.int8 and Q.shape[1] == K, "Q and W must be int8 and fit")
+    _require(row_scale.dtype == torch.float32 and row_scale.is_contiguous() and row_scale.numel() == S,
+             "row_scale must be float32, dense, one a row")
+    _require(w_scale.dtype == torch.float32 and w_scale.is_contiguous() and w_scale.numel() == E * N,
+             "w_scale must be float32, dense, one a channel")
+    if C is None:
+        C = _new((S, N), dtype or torch.float32, Q.device, stream)
+    ldc = _rows(C, "C")
+    _require(C.shape[0] == S and C.shape[1] == N, "C must be S x N")
+    lib = _lib()
+    if scratch is None:
+        need = lib.spx_gemm_i8_scratch_bytes(E, S, N, K)
+        if need:
+            scratch = _new(need, torch.uint8, Q.device, stream)
+    _check(lib.spx_gemm_i8(E, S, N, K, _offsets(offsets, E) if offsets is not None else None, _addr(Q), ldq,
+                           _addr(row_scale), _addr(W), ldw, sw, _addr(w_scale), _addr(C), ldc, _type(C),
+                           _addr(scratch), scratch.numel() * scratch.element_size() if scratch is not None else 0,
+                           _stream(stream)), "spx_gemm_i8")
     return C
 
 

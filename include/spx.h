@@ -761,6 +761,154 @@ spx_status spx_spmm_wcsr_planned(const spx_wcsr_plan* plan, int32_t M, int32_t K
                                  const uint16_t* B, int64_t ldb, float alpha, float beta, float* C, int64_t ldc,
                                  void* scratch, size_t scratch_bytes, spx_stream_t stream);
 
+/* ------------------------------------------------------------ routed experts */
+
+/*
+ * A layer of routed experts is a sparse product: the routing matrix has k
+ * entries a token (one an expert the token is sent to), its transpose lists
+ * each expert's tokens, and the experts' weights form a block-diagonal matrix
+ * with blocks of unequal height.  The calls below sort the tokens' slots by
+ * expert, gather tokens into that order, multiply each expert's rows by its
+ * own weights (16-bit floats, or 8-bit integers with scales), return the rows
+ * weighted to their tokens, and give the gradients of all of it.
+ *
+ * Terms: T tokens with k slots each, S = T * k; flat slot i = t * k + j; E
+ * experts, at most SPX_MAX_EXPERTS (SPX_ERR_UNSUPPORTED beyond).  A slot whose
+ * expert id lies outside [0, E) -- -1 by convention -- is dropped: no expert
+ * sees it, it adds nothing to its token, its weight's gradient is 0.  Arrays
+ * of S rows sorted by expert hold the kept slots first; the rows past them
+ * (offsets[E] and on) are written as zeros by every call that writes such an
+ * array.  Offsets, places and slots read from device memory are tested
+ * against S before use, so wrong ones give wrong values but no access outside
+ * the arrays.  Pointers need only their elements' alignment unless a call
+ * says otherwise (16-byte aligned rows run on wider copies).  Nothing here
+ * synchronises or allocates; no floating-point atomics, so results are the
+ * same from run to run.
+ */
+#define SPX_MAX_EXPERTS 2048
+
+typedef enum spx_type {
+    SPX_F32 = 0,
+    SPX_BF16 = 1,
+    SPX_F16 = 2,
+    SPX_I8 = 3
+} spx_type;
+
+/*
+ * The stable counting sort of the slots by expert (COO -> CSR of the
+ * transposed routing matrix, [Formats] §3):
+ *   offsets[E+1]: offsets[e] = kept slots with an id below e;
+ *   pos[S]: the sorted place of flat slot i, -1 when dropped; slots of one
+ *     expert keep their order;
+ *   slot[S]: the flat slot at each sorted place, -1 past offsets[E].
+ *   expert: T x k ids, id_bytes 4 (int32) or 8 (int64) each, row t at
+ *     expert + t * lde elements (lde >= k).
+ *   scratch: spx_route_scratch_bytes(T, k, E) bytes (may be 0), 4-byte aligned.
+ * T * k must fit int32 (SPX_ERR_INDEX_RANGE).  Launches: 1, or 2 for more
+ * slots than one CTA sorts well.
+ */
+size_t spx_route_scratch_bytes(int32_t T, int32_t k, int32_t E);
+spx_status spx_route_build(int32_t T, int32_t k, int32_t E, const void* expert, int32_t id_bytes, int64_t lde,
+                           int32_t* offsets, int32_t* slot, int32_t* pos, void* scratch, size_t scratch_bytes,
+                           spx_stream_t stream);
+
+/*
+ * Xs[pos[t*k + j]] = X[t] for every kept slot (H values of `type` a row, any
+ * of the four), zeros in the rows past offsets[E]; offsets_end points to
+ * offsets[E].  Rows are copied, not computed.  Each token's row is read once.
+ * Its gradient is spx_route_combine without weights.  Launches: 1.
+ */
+spx_status spx_route_gather(int32_t T, int32_t k, int32_t H, spx_type type, const int32_t* pos,
+                            const int32_t* offsets_end, const void* X, int64_t ldx, void* Xs, int64_t ldxs,
+                            spx_stream_t stream);
+
+/*
+ * Y[t] = sum over the kept slots j of weight[t*k + j] * Ys[pos[t*k + j]]
+ * (weight fp32, NULL: all ones), summed in fp32 in slot order and rounded once
+ * to `type` (SPX_F32, SPX_BF16, SPX_F16); a token without a kept slot gets
+ * zeros.  Launches: 1.
+ */
+spx_status spx_route_combine(int32_t T, int32_t k, int32_t H, spx_type type, const int32_t* pos, const float* weight,
+                             const void* Ys, int64_t ldys, void* Y, int64_t ldy, spx_stream_t stream);
+
+/*
+ * The gradients of spx_route_combine for the gradient dY of its output:
+ *   dYs[pos[t*k + j]] = weight[t*k + j] * dY[t], zeros past offsets[E];
+ *   dweight[t*k + j]  = <dY[t], Ys[pos[t*k + j]]> (fp32), 0 when dropped.
+ * dY, Ys and dYs hold `type`; weight NULL: all ones; dweight NULL: not
+ * computed (Ys is then not read and may be NULL).  Launches: 1.
+ */
+spx_status spx_route_combine_grad(int32_t T, int32_t k, int32_t H, spx_type type, const int32_t* pos,
+                                  const int32_t* offsets_end, const float* weight, const void* dY, int64_t lddy,
+                                  const void* Ys, int64_t ldys, void* dYs, int64_t lddys, float* dweight,
+                                  spx_stream_t stream);
+
+/* How spx_gemm_grouped reads W_e: N rows of K (rows are output channels), or K rows of N. */
+typedef enum spx_w_layout {
+    SPX_W_NK = 0,
+    SPX_W_KN = 1
+} spx_w_layout;
+
+/*
+ * The experts' product: for the rows p of expert e, offsets[e] <= p <
+ * offsets[e+1],
+ *   C[p, n] = sum_k A[p, k] * W_e[n, k]   (SPX_W_NK)
+ *   C[p, n] = sum_k A[p, k] * W_e[k, n]   (SPX_W_KN)
+ * and C[p] = 0 for the rows from offsets[E] on.  A is S x K (lda), C is S x N
+ * (ldc), W_e starts at W + e * stride_w with rows ldw apart.  A and W hold
+ * `type` (SPX_BF16 or SPX_F16), products and sums are fp32, C holds `c_type`
+ * (`type` or SPX_F32) and is rounded once.  The gradient of the SPX_W_NK
+ * product with respect to A is the SPX_W_KN product of C's gradient with the
+ * same weights, and the other way round.  offsets (device, int32[E+1]) is not
+ * read on the host: nothing waits for the routing.  K == 0 gives zeros.
+ * Launches: 1 or 2.
+ */
+spx_status spx_gemm_grouped(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const void* A,
+                            int64_t lda, const void* W, int64_t ldw, int64_t stride_w, spx_w_layout layout,
+                            spx_type type, void* C, int64_t ldc, spx_type c_type, spx_stream_t stream);
+
+/*
+ * The weights' gradient of the experts' product: for every expert
+ *   dW_e[n, k] = sum over its rows p of G[p, n] * A[p, k],
+ * zeros for an expert without rows.  G is S x N (ldg), A is S x K (lda), both
+ * `type`; dW_e starts at dW + e * stride_w, N rows of K, rows ldw apart, in
+ * `w_type` (`type` or SPX_F32), rounded once from fp32.  For weights stored
+ * K x N swap G and A (and N and K).  Launches: 1.
+ */
+spx_status spx_gemm_grouped_wgrad(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const void* G,
+                                  int64_t ldg, const void* A, int64_t lda, spx_type type, void* dW, int64_t ldw,
+                                  int64_t stride_w, spx_type w_type, spx_stream_t stream);
+
+/*
+ * Rows to 8 bits: scale[m] = max_k |X[m, k]| / 127 and Q[m, k] = X[m, k] /
+ * scale[m] rounded to the nearest whole number (ties to even), both in fp32
+ * (IEEE division).  A row of zeros gets scale 0 and codes 0.  A row that holds
+ * an infinity or NaN gets scale NaN and codes 0, so its products are NaN.
+ * X holds SPX_F32, SPX_BF16 or SPX_F16.  Launches: 1.
+ */
+spx_status spx_quant_rows_i8(int32_t M, int32_t K, spx_type type, const void* X, int64_t ldx, int8_t* Q, int64_t ldq,
+                             float* scale, spx_stream_t stream);
+
+/*
+ * The product of 8-bit integers with a scale for each row (token) and output
+ * channel:
+ *   C[p, n] = row_scale[p] * w_scale[e*N + n] * sum_k Q[p, k] * W_e[n, k]
+ * for the rows p of expert e; offsets NULL (then E must be 1): all S rows
+ * belong to the one weight matrix.  The sum is the exact integer (K <=
+ * SPX_I8_MAX_K keeps it inside int32; SPX_ERR_UNSUPPORTED beyond), the scales
+ * are applied in fp32, C holds SPX_F32, SPX_BF16 or SPX_F16 and is rounded
+ * once; zeros in the rows from offsets[E] on.  Q is S x K (ldq), W_e starts
+ * at W + e * stride_w, N rows of K, ldw apart.
+ *   scratch: spx_gemm_i8_scratch_bytes(E, S, N, K) bytes, 256-byte aligned
+ *     (may be NULL when that is 0).
+ */
+#define SPX_I8_MAX_K 131071
+size_t spx_gemm_i8_scratch_bytes(int32_t E, int32_t S, int32_t N, int32_t K);
+spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const int8_t* Q,
+                       int64_t ldq, const float* row_scale, const int8_t* W, int64_t ldw, int64_t stride_w,
+                       const float* w_scale, void* C, int64_t ldc, spx_type c_type, void* scratch,
+                       size_t scratch_bytes, spx_stream_t stream);
+
 /* ------------------------------------------------------------ measurement */
 
 /*
