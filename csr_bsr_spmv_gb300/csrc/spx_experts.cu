@@ -31,6 +31,8 @@ spx_status spx_gemm_grouped(int32_t E, int32_t S, int32_t N, int32_t K, const in
     if (!spx_aligned(offsets, 4) || !spx_aligned(A, 2) || !spx_aligned(W, 2) || !spx_aligned(C, type_bytes(c_type)))
         return SPX_ERR_ALIGN;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (K > 0 && tc_product_fits(A, lda, W, ldw, stride_w, E))
+        return tc_product(E, S, N, K, offsets, A, lda, W, ldw, stride_w, layout, type, C, ldc, c_type, st);
     SimtGemm g{};
     g.L = A, g.li = lda, g.lr = 1;
     g.R = W, g.rj = nk ? ldw : 1, g.rr = nk ? 1 : ldw, g.re = stride_w;
@@ -51,6 +53,8 @@ spx_status spx_gemm_grouped_wgrad(int32_t E, int32_t S, int32_t N, int32_t K, co
     if (!spx_aligned(offsets, 4) || !spx_aligned(G, 2) || !spx_aligned(A, 2) || !spx_aligned(dW, type_bytes(w_type)))
         return SPX_ERR_ALIGN;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (S > 0 && tc_wgrad_fits(G, ldg, A, lda))
+        return tc_wgrad(E, S, N, K, offsets, G, ldg, A, lda, type, dW, ldw, stride_w, w_type, st);
     SimtGemm g{};
     g.L = G, g.li = 1, g.lr = ldg;
     g.R = A, g.rj = 1, g.rr = lda;

@@ -75,6 +75,7 @@ __device__ __forceinline__ bool warp_find_tile(const int* __restrict__ offsets, 
         if (at) {
             const int src = __ffs(at) - 1;
             const int first = base + __shfl_sync(0xffffffffu, inc - n, src);
+            if (tile < first) return false;  // only sums of wrong offsets that passed int32
             e = e0 + src;
             r0 = __shfl_sync(0xffffffffu, lo, src) + (tile - first) * TM;
             hi = __shfl_sync(0xffffffffu, up, src);
@@ -101,5 +102,18 @@ struct SimtGemm {
     bool by_rows;
 };
 spx_status simt_gemm(const SimtGemm& g, spx_type type, spx_type c_type, cudaStream_t st);
+
+// The tensor-core form (spx_experts_tc.cu) of the product and of the weights'
+// gradient, for rows the copy engine can read: 16-byte aligned bases, row
+// pitches and expert strides that are multiples of 8 values.
+bool tc_product_fits(const void* A, int64_t lda, const void* W, int64_t ldw, int64_t stride_w, int E);
+spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void* A, int64_t lda, const void* W,
+                      int64_t ldw, int64_t stride_w, spx_w_layout layout, spx_type type, void* C, int64_t ldc,
+                      spx_type c_type, cudaStream_t st);
+bool tc_wgrad_fits(const void* G, int64_t ldg, const void* A, int64_t lda);
+spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* G, int64_t ldg, const void* A,
+                    int64_t lda, spx_type type, void* dW, int64_t ldw, int64_t stride_w, spx_type w_type,
+                    cudaStream_t st);
+int experts_error_take();  // reads and clears the error word of those kernels: 0 or SPX_ERR_TIMEOUT
 
 }  // namespace spx_exp

@@ -1,0 +1,617 @@
+// spx_experts_tc.cu -- the experts' products and their weight gradients on the
+// sm_103a tensor cores (tcgen05 + TMEM, TMA-fed), 16-bit factors, fp32 sums.
+//
+// One kernel body, three ways the factors lie in memory:
+//   kNK  C[p, n] = sum_k A[p, k] W_e[n, k]      both with k contiguous (K-major)
+//   kKN  C[p, n] = sum_k A[p, k] W_e[k, n]      the weights with n contiguous (MN-major)
+//   kWG  dW_e[n, k] = sum_p G[p, n] A[p, k]     both MN-major, the reduction runs over the expert's rows
+// The MMA computes the transposed tile: its 128 lanes (256 for a CTA pair)
+// run along the output's contiguous axis -- n, or k for kWG -- and its columns
+// along the output's rows -- tokens, or n for kWG.  So each TMEM lane is one
+// output column and a warp's store of one accumulator column is one contiguous
+// run of an output row, whatever the row's alignment; and the ragged number of
+// an expert's rows is the MMA's N, which comes in steps of 16, so a short last
+// tile costs the time of its own rows, not of a whole tile, and a handful of
+// decoded tokens runs on the same kernel as a prefill batch.
+//
+// Persistent: each CTA (pair) walks a static list of tiles; a TMA warp keeps a
+// ring of 64-deep stages filled across tiles, one thread issues the MMAs into
+// one of two TMEM accumulators, four warps store the other one.  The tile list
+// comes from the offsets on the device: nothing waits for the host.
+//
+// Every mbarrier wait is bounded; on expiry the CTA records an error word
+// (read by spx_last_device_error), stops, waits (bounded) for its copies and
+// MMAs in flight, frees its TMEM and exits.
+#include <algorithm>
+
+#include "spx_experts.cuh"
+#include "spx_tc.cuh"
+
+using namespace spx_exp;
+using namespace spx_tc;
+
+namespace {
+
+enum Mode : int { kNK = 0, kKN = 1, kWG = 2 };
+
+constexpr int kThreads = 192;
+constexpr int kDepth = 64;                      // reduction length of a stage: one 128-byte swizzle row
+constexpr uint32_t kLaneBytes = 128 * kDepth * 2;  // a stage's lane factor: 128 lanes a CTA, 16 KB
+constexpr uint32_t kBox = 64 * kDepth * 2;      // an MN-major box: 64 long, 64 deep, 8 KB
+constexpr int kMaxStages = 12;
+constexpr int kBand = 8;                        // row tiles that run side by side before the next lane tile
+constexpr size_t kSmemMax = 224 * 1024;         // dynamic shared memory of a CTA
+constexpr long long kSpinLimit = 2000000000LL;  // cycles (~1 s): only a broken pipeline reaches it
+
+enum : int { kErrFull = 1, kErrEmpty = 2, kErrAcc = 3, kErrDrain = 4, kErrTmemFree = 5 };
+
+__device__ int g_experts_error;
+__device__ __forceinline__ void record_error(int code) { atomicCAS(&g_experts_error, 0, code); }
+
+struct TcArgs {
+    const int* offsets;
+    int E, S;
+    int NL;           // output columns: the lanes' axis
+    int NC;           // kWG: output rows
+    int NR;           // kNK, kKN: reduction length
+    int TN;           // output rows a tile: 32 to 256, a power of two
+    int max_tiles;    // kNK, kKN: more than any sound offsets give
+    int stages;
+    uint32_t col_bytes, stage_bytes, idesc;
+    int same_w;       // 1: every expert reads W_0
+    void* C;
+    long long ldc, ce;
+    spx_type c_type;
+};
+
+struct Item {
+    int e;            // expert (its weights' coordinate)
+    int lane0;        // first output column of the tile
+    int row0, rows;   // output rows [row0, row0 + rows)
+    int red0, red;    // reduction range [red0, red0 + red): k, or the expert's rows
+};
+
+// Tile t of the list.  kNK, kKN: `first` holds each expert's first tile, then
+// the first tile of the rows past the last expert's, then the count; an
+// expert's tiles go in bands of kBand row tiles, lane tiles within a band, row
+// tiles fastest, so that tiles that run together share both factors in L2.
+template <int MODE, int CG>
+__device__ __forceinline__ Item tile_item(const TcArgs& a, const int* first, int t) {
+    Item it;
+    const int nlt = (a.NL + 128 * CG - 1) / (128 * CG);
+    if (MODE == kWG) {
+        const int nct = (a.NC + a.TN - 1) / a.TN, per = nlt * nct;
+        it.e = t / per;
+        const int in = t % per;
+        it.lane0 = (in % nlt) * 128 * CG;
+        it.row0 = (in / nlt) * a.TN;
+        it.rows = min(a.TN, a.NC - it.row0);
+        int hi;
+        expert_rows(a.offsets, it.e, a.S, it.red0, hi);
+        it.red = hi - it.red0;
+        return it;
+    }
+    int lo = 0, up = a.E;  // the last expert whose first tile is <= t
+    while (lo < up) {
+        const int mid = (lo + up + 1) >> 1;
+        if (first[mid] <= t) lo = mid;
+        else up = mid - 1;
+    }
+    int r0 = 0, r1 = a.S;
+    if (a.offsets) {
+        if (lo < a.E) {
+            expert_rows(a.offsets, lo, a.S, r0, r1);
+        } else {
+            r0 = min(max(__ldg(a.offsets + a.E), 0), a.S);
+        }
+    }
+    const int in = t - first[lo], mt = (r1 - r0 + a.TN - 1) / a.TN;
+    const int band = in / (kBand * nlt), inb = in - band * kBand * nlt;
+    const int high = min(kBand, mt - band * kBand);
+    it.e = lo;
+    it.lane0 = (inb / high) * 128 * CG;
+    it.row0 = r0 + (band * kBand + inb % high) * a.TN;
+    it.rows = min(a.TN, r1 - it.row0);
+    it.red0 = 0;
+    it.red = lo < a.E ? a.NR : 0;  // the rows past the last expert's: zeros
+    return it;
+}
+
+template <int CG>
+__device__ __forceinline__ uint32_t leader_addr(uint32_t local) {
+    if (CG == 1) return local;
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(local));
+    return r;
+}
+
+template <int CG>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+            "[%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+            "{%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+            "%4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+            "{%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far have completed.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                     : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One accumulator column chunk (32 columns from c0) of this thread's output column.
+template <class O>
+__device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, O* col, int c0, const uint32_t (&v)[32]) {
+    O* q = col + static_cast<long long>(it.row0 + c0) * a.ldc;
+    if (c0 + 32 <= it.rows) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j, q += a.ldc) *q = from_f<O>(__uint_as_float(v[j]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j, q += a.ldc)
+            if (c0 + j < it.rows) *q = from_f<O>(__uint_as_float(v[j]));
+    }
+}
+
+template <int MODE, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    experts_tc_kernel(const __grid_constant__ CUtensorMap tm_lane, const __grid_constant__ CUtensorMap tm_col,
+                      const __grid_constant__ TcArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    __shared__ uint32_t s_issued, s_consumed;
+    __shared__ __align__(8) uint64_t s_bars[2 * kMaxStages + 5];
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t bars = smem_u32(s_bars);
+    auto full_bar = [&](uint32_t s) { return bars + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bars + 8u * (kMaxStages + s); };
+    auto tfull_bar = [&](int b) { return bars + 8u * (2 * kMaxStages + b); };
+    auto tempty_bar = [&](int b) { return bars + 8u * (2 * kMaxStages + 2 + b); };
+    const uint32_t fin_bar = bars + 8u * (2 * kMaxStages + 4);
+    const uint32_t NS = a.stages;
+    // the tile list, behind the ring
+    int* first = reinterpret_cast<int*>(smem_raw + (base - smem_u32(smem_raw)) + NS * a.stage_bytes);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank = 0;
+    if (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int G = static_cast<int>(gridDim.x) / CG, me = static_cast<int>(blockIdx.x) / CG;
+    const uint32_t tmem_cols = 2u * a.TN;  // two accumulators
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < NS; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), 4 * CG);  // one arrive per epilogue warp of the pair
+        }
+        mbar_init(fin_bar, 1);
+        s_abort = 0;
+        s_issued = 0;
+        s_consumed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 5) {
+        if (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                         "r"(tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                         "r"(tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
+    }
+    int ntiles = 0;
+    if (MODE == kWG) {
+        ntiles = a.E * ((a.NL + 128 * CG - 1) / (128 * CG)) * ((a.NC + a.TN - 1) / a.TN);
+    } else {
+        const int nlt = (a.NL + 128 * CG - 1) / (128 * CG);
+        for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+            int lo = 0, hi = a.S;
+            if (a.offsets) {
+                if (e < a.E) expert_rows(a.offsets, e, a.S, lo, hi);
+                else lo = min(max(__ldg(a.offsets + a.E), 0), a.S);
+            } else if (e == a.E) {
+                lo = hi;
+            }
+            first[e] = (hi - lo + a.TN - 1) / a.TN * nlt;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            long long carry = 0;
+            for (int e0 = 0; e0 <= a.E; e0 += 32) {
+                const int n = e0 + lane <= a.E ? first[e0 + lane] : 0;
+                long long inc = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const long long up = __shfl_up_sync(0xffffffffu, inc, d);
+                    if (lane >= d) inc += up;
+                }
+                if (e0 + lane <= a.E) first[e0 + lane] = static_cast<int>(carry + inc - n);
+                carry += __shfl_sync(0xffffffffu, inc, 31);
+            }
+            // offsets out of order can overlap and give more tiles than rows: then none is run
+            if (lane == 0) first[a.E + 1] = carry <= a.max_tiles ? static_cast<int>(carry) : 0;
+        }
+    }
+    tc_fence_before();
+    if (CG == 2) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    if (MODE != kWG) ntiles = first[a.E + 1];
+    const uint32_t buf_cols = tmem_cols / 2;
+
+    if (warp == 4) {
+        // ---------------- producer: this CTA's part of every stage
+        if (lane == 0) {
+            uint32_t g = 0;
+            bool stop = false;
+            for (int t = me; t < ntiles && !stop && !s_abort; t += G) {
+                const Item it = tile_item<MODE, CG>(a, first, t);
+                const int nb = (it.red + kDepth - 1) / kDepth;
+                const int ncols = (it.rows + 15) & ~15;  // the MMA's columns; a pair's CTA holds half of them
+                const int lane0 = it.lane0 + 128 * static_cast<int>(rank);
+                const int z = a.same_w ? 0 : it.e;
+                for (int b = 0; b < nb; ++b, ++g) {
+                    const uint32_t s = g % NS, ph = (g / NS) & 1u;
+                    if (!mbar_wait(empty_bar(s), ph ^ 1u, kSpinLimit) || s_abort) {
+                        record_error(kErrEmpty);
+                        s_abort = 1;
+                        stop = true;
+                        break;
+                    }
+                    if (rank == 0) mbar_expect_tx(full_bar(s), CG * a.stage_bytes);
+                    const uint32_t bar = leader_addr<CG>(full_bar(s));
+                    const uint32_t sl = base + s * a.stage_bytes, sc = sl + kLaneBytes;
+                    const int r = it.red0 + b * kDepth;
+                    if (MODE == kNK) {
+                        load_3d<CG>(sl, &tm_lane, r, lane0, z, bar);
+                        load_2d<CG>(sc, &tm_col, r, it.row0 + static_cast<int>(rank) * (ncols / 2), bar);
+                    } else if (MODE == kKN) {
+                        load_3d<CG>(sl, &tm_lane, lane0, r, z, bar);
+                        load_3d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, z, bar);
+                        load_2d<CG>(sc, &tm_col, r, it.row0 + static_cast<int>(rank) * (ncols / 2), bar);
+                    } else {
+                        load_2d<CG>(sl, &tm_lane, lane0, r, bar);
+                        load_2d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, bar);
+                        const int c0 = it.row0 + static_cast<int>(rank) * (a.TN / 2);
+                        for (int c = 0; c < a.TN / CG; c += 64) load_2d<CG>(sc + c / 64 * kBox, &tm_col, c0 + c, r, bar);
+                    }
+                }
+            }
+            s_issued = g;
+        }
+    } else if (warp == 5) {
+        // ---------------- MMA issuer (the pair's first CTA)
+        if (rank == 0) {
+            uint32_t g = 0;
+            int i = 0;
+            bool ok = true;
+            for (int t = me; t < ntiles && ok; t += G, ++i) {
+                const Item it = tile_item<MODE, CG>(a, first, t);
+                const int nb = (it.red + kDepth - 1) / kDepth;
+                const int buf = i & 1;
+                int go = 1;
+                if (lane == 0) go = mbar_wait(tempty_bar(buf), ((i >> 1) & 1u) ^ 1u, kSpinLimit) && !s_abort;
+                go = __shfl_sync(0xffffffffu, go, 0);
+                if (!go) {
+                    if (lane == 0) {
+                        record_error(kErrTmemFree);
+                        s_abort = 1;
+                    }
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + buf * buf_cols;
+                const uint32_t ncols = MODE == kWG ? a.TN : (it.rows + 15) & ~15;
+                const uint32_t idesc = a.idesc | ((ncols >> 3) << 17);
+                for (int b = 0; b < nb; ++b, ++g) {
+                    const uint32_t s = g % NS, ph = (g / NS) & 1u;
+                    if (lane == 0) go = mbar_wait(full_bar(s), ph, kSpinLimit);
+                    go = __shfl_sync(0xffffffffu, go, 0);
+                    if (!go) {
+                        if (lane == 0) {
+                            record_error(kErrFull);
+                            s_abort = 1;
+                        }
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sl = base + s * a.stage_bytes, sc = sl + kLaneBytes;
+                    const int depth = min(kDepth, it.red - b * kDepth);
+                    const int nks = (depth + 15) >> 4;
+                    if (MODE == kWG && (depth & 15)) {
+                        // rows of the next expert inside the last step of 16: zeros in both factors
+                        const int bad = nks * 16 - depth, boxes = 2 + a.TN / 64;
+                        for (int q = lane; q < bad * 8 * boxes; q += 32) {
+                            const uint32_t at = sl + (q / (bad * 8)) * kBox + (depth + q / 8 % bad) * 128 + q % 8 * 16;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                    }
+                    tc_fence_after();
+                    if (lane == 0) {
+                        for (int ks = 0; ks < nks; ++ks) {
+                            const uint64_t ad = MODE == kNK ? sw128_desc(sl + ks * 32u, 16u, 1024u)
+                                                            : sw128_desc(sl + ks * 2048u, kBox, 1024u);
+                            const uint64_t bd = MODE == kWG ? sw128_desc(sc + ks * 2048u, kBox, 1024u)
+                                                            : sw128_desc(sc + ks * 32u, 16u, 1024u);
+                            mma<CG>(d, ad, bd, idesc, (b > 0 || ks > 0) ? 1u : 0u);
+                        }
+                        commit<CG>(empty_bar(s));
+                    }
+                    __syncwarp();
+                }
+                if (ok && lane == 0) commit<CG>(tfull_bar(buf));
+            }
+            if (lane == 0) s_consumed = g;
+        }
+    } else {
+        // ---------------- epilogue warps 0..3: TMEM lane quarter = warp
+        int i = 0;
+        for (int t = me; t < ntiles; t += G, ++i) {
+            const Item it = tile_item<MODE, CG>(a, first, t);
+            const int buf = i & 1;
+            int ok = 1;
+            if (lane == 0) ok = (mbar_wait(tfull_bar(buf), (i >> 1) & 1u, kSpinLimit) && !s_abort) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) {
+                if (lane == 0) {
+                    record_error(kErrAcc);
+                    s_abort = 1;
+                }
+                break;
+            }
+            tc_fence_after();
+            const int x = it.lane0 + 128 * static_cast<int>(rank) + 32 * warp + lane;
+            const long long off = (MODE == kWG ? it.e * a.ce : 0) + x;
+            const uint32_t src = tmem + buf * buf_cols + (static_cast<uint32_t>(32 * warp) << 16);
+#pragma unroll 1
+            for (int c0 = 0; c0 < it.rows; c0 += 32) {
+                uint32_t v[32];
+                if (it.red > 0) {
+                    tmem_ld32(src + c0, v);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0u;
+                }
+                if (x < a.NL) {
+                    if (a.c_type == SPX_F32) store_chunk(a, it, static_cast<float*>(a.C) + off, c0, v);
+                    else if (a.c_type == SPX_BF16) store_chunk(a, it, static_cast<__nv_bfloat16*>(a.C) + off, c0, v);
+                    else store_chunk(a, it, static_cast<__half*>(a.C) + off, c0, v);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 1) mbar_arrive(tempty_bar(buf));
+                else
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                     leader_addr<CG>(tempty_bar(buf)))
+                                 : "memory");
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (CG == 2) cluster_sync();  // the peer's waits are over too
+    else __syncthreads();
+    if (s_abort && rank == 0) {
+        if (warp == 4 && lane == 0) {
+            // copies issued but never consumed: wait (bounded) until each has landed
+            for (uint32_t g = s_consumed; g < s_issued; ++g)
+                if (!mbar_wait(full_bar(g % NS), (g / NS) & 1u, kSpinLimit)) {
+                    record_error(kErrDrain);
+                    break;
+                }
+        } else if (warp == 5 && lane == 0) {
+            // MMAs in flight: one more commit, then wait (bounded) for it
+            commit<CG>(fin_bar);
+            if (!mbar_wait(fin_bar, 0, kSpinLimit)) record_error(kErrDrain);
+        }
+    }
+    __syncwarp();
+    if (CG == 2) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 5) {
+        if (CG == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols) : "memory");
+    }
+}
+
+// ------------------------------------------------------------ host side
+
+// 16-bit tensor map of up to three axes, 128-byte swizzle, a box of 64 x rows (x 1).
+bool make_map3(CUtensorMap* m, const void* base, spx_type type, uint64_t inner, uint64_t rows, uint64_t ld, uint64_t mats,
+               uint64_t stride, uint32_t box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {inner, rows, mats};
+    cuuint64_t strides[2] = {ld * 2, stride * 2};
+    cuuint32_t box[3] = {64, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, type == SPX_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, mats ? 3 : 2,
+               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+    static std::mutex mu;
+    static std::map<int, int> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = cache.find(dev);
+    if (it != cache.end()) return it->second;
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return cache[dev] = n;
+}
+
+bool rows_aligned(const void* p, int64_t ld) { return spx_aligned(p, 16) && ld % 8 == 0; }
+
+template <int MODE, int CG>
+spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long long max_tiles, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms <= 0) return SPX_ERR_CUDA;
+    const size_t list = sizeof(int) * (static_cast<size_t>(a.E) + 2);
+    a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemMax - 1024 - list) / a.stage_bytes));
+    const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + list;
+    if (set_smem_limit(experts_tc_kernel<MODE, CG>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
+    const int groups = static_cast<int>(std::min<long long>(max_tiles, sms / CG));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(groups * CG);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_tc_kernel<MODE, CG>, tl, tc, a);
+    spx_note_launches(1);
+    return spx_cuda_status(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+uint32_t idesc_of(spx_type type, int mode, int cg) {
+    uint32_t d = 1u << 4;                                 // fp32 sums
+    if (type == SPX_BF16) d |= (1u << 7) | (1u << 10);    // both factors bf16 (else fp16)
+    if (mode != kNK) d |= 1u << 15;                       // lane factor MN-major
+    if (mode == kWG) d |= 1u << 16;                       // column factor MN-major
+    return d | ((128u * cg >> 4) << 24);
+}
+
+}  // namespace
+
+namespace spx_exp {
+
+int experts_error_take() {
+    int h = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&h, g_experts_error, sizeof(int)) != cudaSuccess) return SPX_ERR_CUDA;
+    if (h != 0 && cudaMemcpyToSymbol(g_experts_error, &zero, sizeof(int)) != cudaSuccess) return SPX_ERR_CUDA;
+    return h ? static_cast<int>(SPX_ERR_TIMEOUT) : 0;
+}
+
+bool tc_product_fits(const void* A, int64_t lda, const void* W, int64_t ldw, int64_t stride_w, int E) {
+    return rows_aligned(A, lda) && rows_aligned(W, ldw) && (E == 1 || stride_w % 8 == 0);
+}
+
+spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void* A, int64_t lda, const void* W,
+                      int64_t ldw, int64_t stride_w, spx_w_layout layout, spx_type type, void* C, int64_t ldc,
+                      spx_type c_type, cudaStream_t st) {
+    const bool nk = layout == SPX_W_NK;
+    TcArgs a{};
+    a.offsets = offsets, a.E = E, a.S = S, a.NL = N, a.NR = K;
+    a.C = C, a.ldc = ldc, a.c_type = c_type;
+    a.same_w = E == 1 || stride_w == 0;
+    a.TN = 32;
+    while (a.TN < 256 && a.TN < 2 * ((S + E - 1) / E)) a.TN *= 2;
+    a.col_bytes = static_cast<uint32_t>(a.TN) * kDepth * 2;
+    a.stage_bytes = kLaneBytes + a.col_bytes;
+    a.idesc = idesc_of(type, nk ? kNK : kKN, 1);
+    CUtensorMap tl, tc;
+    const uint64_t mats = a.same_w ? 1 : E, sw = a.same_w ? static_cast<uint64_t>(ldw) * (nk ? N : K) : stride_w;
+    const bool ok = nk ? make_map3(&tl, W, type, K, N, ldw, mats, sw, 128) : make_map3(&tl, W, type, N, K, ldw, mats, sw, 64);
+    if (!ok || !make_map3(&tc, A, type, K, S, lda, 0, 0, a.TN)) return SPX_ERR_CUDA;
+    const long long nlt = (N + 127) / 128, tiles = max_row_tiles(E, S, a.TN) * nlt;
+    if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;  // the list's walk steps past its end by a grid
+    a.max_tiles = static_cast<int>(tiles);
+    return nk ? launch<kNK, 1>(tl, tc, a, tiles, st) : launch<kKN, 1>(tl, tc, a, tiles, st);
+}
+
+bool tc_wgrad_fits(const void* G, int64_t ldg, const void* A, int64_t lda) {
+    return rows_aligned(G, ldg) && rows_aligned(A, lda);
+}
+
+spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* G, int64_t ldg, const void* A,
+                    int64_t lda, spx_type type, void* dW, int64_t ldw, int64_t stride_w, spx_type w_type,
+                    cudaStream_t st) {
+    TcArgs a{};
+    a.offsets = offsets, a.E = E, a.S = S, a.NL = K, a.NC = N;
+    a.C = dW, a.ldc = ldw, a.ce = stride_w, a.c_type = w_type;
+    a.TN = N > 128 ? 256 : 128;
+    a.col_bytes = static_cast<uint32_t>(a.TN) * kDepth * 2;
+    a.stage_bytes = kLaneBytes + a.col_bytes;
+    a.idesc = idesc_of(type, kWG, 1);
+    CUtensorMap tl, tc;
+    if (!make_map3(&tl, A, type, K, S, lda, 0, 0, 64) || !make_map3(&tc, G, type, N, S, ldg, 0, 0, 64))
+        return SPX_ERR_CUDA;
+    const long long tiles = static_cast<long long>(E) * ((K + 127) / 128) * ((N + a.TN - 1) / a.TN);
+    if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;
+    return launch<kWG, 1>(tl, tc, a, tiles, st);
+}
+
+}  // namespace spx_exp

@@ -941,7 +941,8 @@ spx_status spx_wait_probe(int64_t limit_cycles, spx_stream_t stream);
 
 /*
  * Synchronises `stream`, then reads and clears the device-side error words:
- * SPX_ERR_TIMEOUT if a bounded wait of spx_spmm_bsr or spx_spmm_wcsr gave up, else the index
+ * SPX_ERR_TIMEOUT if a bounded wait of spx_spmm_bsr, spx_spmm_wcsr or an
+ * experts' product gave up, else the index
  * or ordering error spx_spmv_coo recorded, else SPX_OK.  The words are one
  * per device, shared by every stream: with calls still running on other
  * streams, the status read may come from any of them.
