@@ -57,7 +57,7 @@ struct TcArgs {
     int TN;           // output rows a tile: 32 to 256, a power of two
     int max_tiles;    // kNK, kKN: more than any sound offsets give
     int stages;
-    uint32_t col_bytes, stage_bytes, idesc;
+    uint32_t stage_bytes, idesc;
     int same_w;       // 1: every expert reads W_0
     void* C;
     long long ldc, ce;
@@ -175,6 +175,18 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t adesc, uint64_t bdesc, 
             : "memory");
 }
 
+// The ring position of a role: stage and phase, stepped without a division
+// (the roles are single threads whose instructions follow one another; with
+// the stage from a remainder, each stage cost them about 1000 cycles, twice
+// its MMAs).
+struct Ring {
+    uint32_t n, s = 0, ph = 0;
+    __device__ __forceinline__ explicit Ring(uint32_t stages) : n(stages) {}
+    __device__ __forceinline__ void next() {
+        if (++s == n) s = 0, ph ^= 1u;
+    }
+};
+
 // Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far have completed.
 template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -187,6 +199,32 @@ __device__ __forceinline__ void commit(uint32_t bar) {
                 bar),
             "h"(static_cast<uint16_t>(3))
             : "memory");
+}
+
+// The columns an MMA takes for `rows` output rows: steps of 16, of 32 for a pair.
+template <int CG>
+__device__ __forceinline__ int mma_cols(int rows) {
+    return (rows + 16 * CG - 1) / (16 * CG) * (16 * CG);
+}
+
+// Bounded wait for arrivals that may come from the other CTA of the pair.
+template <int CG>
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity) {
+    if (CG == 1) return mbar_wait(bar, parity, kSpinLimit);
+    long long t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (t0 == 0) t0 = clock64();
+        else if (clock64() - t0 > kSpinLimit) return false;
+    }
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -301,114 +339,129 @@ __global__ void __launch_bounds__(kThreads, 1)
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
+    const uint32_t full0 = leader_addr<CG>(full_bar(0));
     if (MODE != kWG) ntiles = first[a.E + 1];
     const uint32_t buf_cols = tmem_cols / 2;
 
     if (warp == 4) {
         // ---------------- producer: this CTA's part of every stage
         if (lane == 0) {
-            uint32_t g = 0;
+            Ring ring(NS);
+            uint32_t issued = 0;
             bool stop = false;
-            for (int t = me; t < ntiles && !stop && !s_abort; t += G) {
+            for (int t = me; t < ntiles && !stop; t += G) {
                 const Item it = tile_item<MODE, CG>(a, first, t);
-                const int nb = (it.red + kDepth - 1) / kDepth;
-                const int ncols = (it.rows + 15) & ~15;  // the MMA's columns; a pair's CTA holds half of them
+                const int ncols = mma_cols<CG>(it.rows);  // a pair's CTA holds half of them
                 const int lane0 = it.lane0 + 128 * static_cast<int>(rank);
-                const int z = a.same_w ? 0 : it.e;
-                for (int b = 0; b < nb; ++b, ++g) {
-                    const uint32_t s = g % NS, ph = (g / NS) & 1u;
-                    if (!mbar_wait(empty_bar(s), ph ^ 1u, kSpinLimit) || s_abort) {
+                const int col0 = it.row0 + static_cast<int>(rank) * (MODE == kWG ? a.TN : ncols) / 2;
+                const int z = a.same_w ? 0 : it.e, end = it.red0 + it.red;
+                for (int r = it.red0; r < end; r += kDepth, ring.next(), ++issued) {
+                    const uint32_t s8 = 8u * ring.s, sl = base + ring.s * a.stage_bytes, sc = sl + kLaneBytes;
+                    if (!mbar_wait(empty_bar(0) + s8, ring.ph ^ 1u, kSpinLimit) || s_abort) {
                         record_error(kErrEmpty);
                         s_abort = 1;
                         stop = true;
                         break;
                     }
-                    if (rank == 0) mbar_expect_tx(full_bar(s), CG * a.stage_bytes);
-                    const uint32_t bar = leader_addr<CG>(full_bar(s));
-                    const uint32_t sl = base + s * a.stage_bytes, sc = sl + kLaneBytes;
-                    const int r = it.red0 + b * kDepth;
+                    if (rank == 0) mbar_expect_tx(full_bar(0) + s8, CG * a.stage_bytes);
+                    const uint32_t bar = full0 + s8;
                     if (MODE == kNK) {
                         load_3d<CG>(sl, &tm_lane, r, lane0, z, bar);
-                        load_2d<CG>(sc, &tm_col, r, it.row0 + static_cast<int>(rank) * (ncols / 2), bar);
+                        load_2d<CG>(sc, &tm_col, r, col0, bar);
                     } else if (MODE == kKN) {
                         load_3d<CG>(sl, &tm_lane, lane0, r, z, bar);
                         load_3d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, z, bar);
-                        load_2d<CG>(sc, &tm_col, r, it.row0 + static_cast<int>(rank) * (ncols / 2), bar);
+                        load_2d<CG>(sc, &tm_col, r, col0, bar);
                     } else {
                         load_2d<CG>(sl, &tm_lane, lane0, r, bar);
                         load_2d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, bar);
-                        const int c0 = it.row0 + static_cast<int>(rank) * (a.TN / 2);
-                        for (int c = 0; c < a.TN / CG; c += 64) load_2d<CG>(sc + c / 64 * kBox, &tm_col, c0 + c, r, bar);
+                        for (int c = 0; c < a.TN / CG; c += 64) load_2d<CG>(sc + c / 64 * kBox, &tm_col, col0 + c, r, bar);
                     }
                 }
             }
-            s_issued = g;
+            s_issued = issued;
         }
     } else if (warp == 5) {
         // ---------------- MMA issuer (the pair's first CTA)
         if (rank == 0) {
-            uint32_t g = 0;
-            int i = 0;
+            // descriptors of stage 0; a stage or a step of 16 adds to their low words (16-byte units)
+            const uint64_t ad0 = MODE == kNK ? sw128_desc(base, 16u, 1024u) : sw128_desc(base, kBox, 1024u);
+            const uint64_t bd0 = MODE == kWG ? sw128_desc(base + kLaneBytes, kBox, 1024u)
+                                             : sw128_desc(base + kLaneBytes, 16u, 1024u);
+            constexpr uint32_t a_step = (MODE == kNK ? 32u : 2048u) >> 4, b_step = (MODE == kWG ? 2048u : 32u) >> 4;
+            const uint32_t stage_step = a.stage_bytes >> 4;
+            Ring ring(NS);
+            uint32_t consumed = 0, d = tmem, tph = 1;
+            int buf = 0;
             bool ok = true;
-            for (int t = me; t < ntiles && ok; t += G, ++i) {
+            for (int t = me; t < ntiles && ok; t += G) {
                 const Item it = tile_item<MODE, CG>(a, first, t);
-                const int nb = (it.red + kDepth - 1) / kDepth;
-                const int buf = i & 1;
-                int go = 1;
-                if (lane == 0) go = mbar_wait(tempty_bar(buf), ((i >> 1) & 1u) ^ 1u, kSpinLimit) && !s_abort;
-                go = __shfl_sync(0xffffffffu, go, 0);
-                if (!go) {
-                    if (lane == 0) {
-                        record_error(kErrTmemFree);
-                        s_abort = 1;
-                    }
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem + buf * buf_cols;
-                const uint32_t ncols = MODE == kWG ? a.TN : (it.rows + 15) & ~15;
+                const uint32_t ncols = MODE == kWG ? a.TN : mma_cols<CG>(it.rows);
                 const uint32_t idesc = a.idesc | ((ncols >> 3) << 17);
-                for (int b = 0; b < nb; ++b, ++g) {
-                    const uint32_t s = g % NS, ph = (g / NS) & 1u;
-                    if (lane == 0) go = mbar_wait(full_bar(s), ph, kSpinLimit);
-                    go = __shfl_sync(0xffffffffu, go, 0);
-                    if (!go) {
-                        if (lane == 0) {
+                const int whole = it.red / kDepth, tail = it.red % kDepth;
+                uint32_t acc = 0;
+                if (lane == 0) {
+                    ok = pair_wait<CG>(tempty_bar(buf), tph) && !s_abort;
+                    if (!ok) record_error(kErrTmemFree);
+                    tc_fence_after();
+                    for (int b = 0; ok && b < whole; ++b, ring.next(), ++consumed) {
+                        const uint32_t s8 = 8u * ring.s;
+                        if (!pair_wait<CG>(full_bar(0) + s8, ring.ph)) {
                             record_error(kErrFull);
-                            s_abort = 1;
+                            ok = false;
+                            break;
                         }
-                        ok = false;
-                        break;
+                        tc_fence_after();
+                        const uint64_t ad = ad0 + ring.s * stage_step, bd = bd0 + ring.s * stage_step;
+                        mma<CG>(d, ad, bd, idesc, acc);
+                        acc = 1;
+#pragma unroll
+                        for (uint32_t ks = 1; ks < kDepth / 16; ++ks)
+                            mma<CG>(d, ad + ks * a_step, bd + ks * b_step, idesc, 1u);
+                        commit<CG>(empty_bar(0) + s8);
                     }
-                    const uint32_t sl = base + s * a.stage_bytes, sc = sl + kLaneBytes;
-                    const int depth = min(kDepth, it.red - b * kDepth);
-                    const int nks = (depth + 15) >> 4;
-                    if (MODE == kWG && (depth & 15)) {
+                }
+                if (MODE == kWG) __syncwarp();
+                if (tail && (MODE == kWG || lane == 0)) {  // the reduction's last, short stage
+                    ring.s = MODE == kWG ? __shfl_sync(0xffffffffu, ring.s, 0) : ring.s;
+                    const uint32_t s8 = 8u * ring.s;
+                    if (lane == 0 && ok && !pair_wait<CG>(full_bar(0) + s8, ring.ph)) {
+                        record_error(kErrFull);
+                        ok = false;
+                    }
+                    if (MODE == kWG) ok = __shfl_sync(0xffffffffu, ok, 0);
+                    const int nks = (tail + 15) >> 4;
+                    if (MODE == kWG && ok && (tail & 15)) {
                         // rows of the next expert inside the last step of 16: zeros in both factors
-                        const int bad = nks * 16 - depth, boxes = 2 + a.TN / 64;
+                        const uint32_t sl = base + ring.s * a.stage_bytes;
+                        const int bad = nks * 16 - tail, boxes = 2 + a.TN / 64;
                         for (int q = lane; q < bad * 8 * boxes; q += 32) {
-                            const uint32_t at = sl + (q / (bad * 8)) * kBox + (depth + q / 8 % bad) * 128 + q % 8 * 16;
+                            const uint32_t at = sl + (q / (bad * 8)) * kBox + (tail + q / 8 % bad) * 128 + q % 8 * 16;
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
                         }
                         fence_proxy_async();
                         __syncwarp();
                     }
-                    tc_fence_after();
-                    if (lane == 0) {
-                        for (int ks = 0; ks < nks; ++ks) {
-                            const uint64_t ad = MODE == kNK ? sw128_desc(sl + ks * 32u, 16u, 1024u)
-                                                            : sw128_desc(sl + ks * 2048u, kBox, 1024u);
-                            const uint64_t bd = MODE == kWG ? sw128_desc(sc + ks * 2048u, kBox, 1024u)
-                                                            : sw128_desc(sc + ks * 32u, 16u, 1024u);
-                            mma<CG>(d, ad, bd, idesc, (b > 0 || ks > 0) ? 1u : 0u);
-                        }
-                        commit<CG>(empty_bar(s));
+                    if (lane == 0 && ok) {
+                        tc_fence_after();
+                        const uint64_t ad = ad0 + ring.s * stage_step, bd = bd0 + ring.s * stage_step;
+                        for (int ks = 0; ks < nks; ++ks, acc = 1)
+                            mma<CG>(d, ad + static_cast<uint32_t>(ks) * a_step, bd + static_cast<uint32_t>(ks) * b_step,
+                                    idesc, acc);
+                        commit<CG>(empty_bar(0) + s8);
+                        ring.next();
+                        ++consumed;
                     }
-                    __syncwarp();
                 }
-                if (ok && lane == 0) commit<CG>(tfull_bar(buf));
+                if (lane == 0 && ok) commit<CG>(tfull_bar(buf));
+                if (lane == 0 && !ok) s_abort = 1;
+                buf ^= 1;
+                d = tmem + buf * buf_cols;
+                if (buf == 0) tph ^= 1u;
+                __syncwarp();
+                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
-            if (lane == 0) s_consumed = g;
+            if (lane == 0) s_consumed = consumed;
         }
     } else {
         // ---------------- epilogue warps 0..3: TMEM lane quarter = warp
@@ -518,6 +571,23 @@ int sm_count() {
     return cache[dev] = n;
 }
 
+// Clusters of `kernel` the device holds at once, asked once per (kernel, device).
+int resident_pairs(const void* kernel, const cudaLaunchConfig_t& cfg) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, int> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_pair(kernel, dev);
+    auto it = cache.find(key);
+    if (it != cache.end()) return it->second;
+    cudaLaunchConfig_t most = cfg;
+    most.dynamicSmemBytes = kSmemMax;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &most) != cudaSuccess) return 0;
+    return cache[key] = n;
+}
+
 bool rows_aligned(const void* p, int64_t ld) { return spx_aligned(p, 16) && ld % 8 == 0; }
 
 template <int MODE, int CG>
@@ -528,9 +598,7 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemMax - 1024 - list) / a.stage_bytes));
     const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + list;
     if (set_smem_limit(experts_tc_kernel<MODE, CG>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
-    const int groups = static_cast<int>(std::min<long long>(max_tiles, sms / CG));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(groups * CG);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -540,6 +608,14 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG > 1 ? 1 : 0;
+    // as many CTAs as run at once: one an SM; pairs only where a GPC has two SMs left for them
+    int groups = sms;
+    if (CG > 1) {
+        cfg.gridDim = dim3(sms / CG * CG);
+        groups = resident_pairs(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG>), cfg);
+        if (groups <= 0) return SPX_ERR_CUDA;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(max_tiles, groups)) * CG);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_tc_kernel<MODE, CG>, tl, tc, a);
     spx_note_launches(1);
     return spx_cuda_status(e != cudaSuccess ? e : cudaGetLastError());
@@ -579,16 +655,17 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
     a.same_w = E == 1 || stride_w == 0;
     a.TN = 32;
     while (a.TN < 256 && a.TN < 2 * ((S + E - 1) / E)) a.TN *= 2;
-    a.col_bytes = static_cast<uint32_t>(a.TN) * kDepth * 2;
-    a.stage_bytes = kLaneBytes + a.col_bytes;
-    a.idesc = idesc_of(type, nk ? kNK : kKN, 1);
+    const int cg = a.TN == 256 && N > 128 ? 2 : 1;
+    a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
+    a.idesc = idesc_of(type, nk ? kNK : kKN, cg);
     CUtensorMap tl, tc;
     const uint64_t mats = a.same_w ? 1 : E, sw = a.same_w ? static_cast<uint64_t>(ldw) * (nk ? N : K) : stride_w;
     const bool ok = nk ? make_map3(&tl, W, type, K, N, ldw, mats, sw, 128) : make_map3(&tl, W, type, N, K, ldw, mats, sw, 64);
-    if (!ok || !make_map3(&tc, A, type, K, S, lda, 0, 0, a.TN)) return SPX_ERR_CUDA;
-    const long long nlt = (N + 127) / 128, tiles = max_row_tiles(E, S, a.TN) * nlt;
+    if (!ok || !make_map3(&tc, A, type, K, S, lda, 0, 0, a.TN / cg)) return SPX_ERR_CUDA;
+    const long long nlt = (N + 128 * cg - 1) / (128 * cg), tiles = max_row_tiles(E, S, a.TN) * nlt;
     if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;  // the list's walk steps past its end by a grid
     a.max_tiles = static_cast<int>(tiles);
+    if (cg == 2) return nk ? launch<kNK, 2>(tl, tc, a, tiles, st) : launch<kKN, 2>(tl, tc, a, tiles, st);
     return nk ? launch<kNK, 1>(tl, tc, a, tiles, st) : launch<kKN, 1>(tl, tc, a, tiles, st);
 }
 
@@ -603,8 +680,7 @@ spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* 
     a.offsets = offsets, a.E = E, a.S = S, a.NL = K, a.NC = N;
     a.C = dW, a.ldc = ldw, a.ce = stride_w, a.c_type = w_type;
     a.TN = N > 128 ? 256 : 128;
-    a.col_bytes = static_cast<uint32_t>(a.TN) * kDepth * 2;
-    a.stage_bytes = kLaneBytes + a.col_bytes;
+    a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN) * kDepth * 2;
     a.idesc = idesc_of(type, kWG, 1);
     CUtensorMap tl, tc;
     if (!make_map3(&tl, A, type, K, S, lda, 0, 0, 64) || !make_map3(&tc, G, type, N, S, ldg, 0, 0, 64))
