@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
-    __shared__ uint32_t s_issued, s_consumed;
-    __shared__ __align__(8) uint64_t s_bars[2 * kMaxStages + 5];
+    __shared__ uint32_t s_issued, s_consumed, s_tails_in, s_tails_done;
+    __shared__ __align__(8) uint64_t s_bars[4 * kMaxStages + 5];
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t bars = smem_u32(s_bars);
@@ -262,6 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tfull_bar = [&](int b) { return bars + 8u * (2 * kMaxStages + b); };
     auto tempty_bar = [&](int b) { return bars + 8u * (2 * kMaxStages + 2 + b); };
     const uint32_t fin_bar = bars + 8u * (2 * kMaxStages + 4);
+    // kWG: a last stage that ends inside a step of 16 rows lands on its own CTA's tail_bar; both CTAs clear the
+    // rows past the expert's and arrive on the first one's clear_bar.  One of each a ring stage: several short
+    // reductions can be in the ring at once, but a stage is not filled again before it was consumed.
+    auto tail_bar = [&](uint32_t s) { return bars + 8u * (2 * kMaxStages + 5 + s); };
+    auto clear_bar = [&](uint32_t s) { return bars + 8u * (3 * kMaxStages + 5 + s); };
     const uint32_t NS = a.stages;
     // the tile list, behind the ring
     int* first = reinterpret_cast<int*>(smem_raw + (base - smem_u32(smem_raw)) + NS * a.stage_bytes);
@@ -282,9 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(tempty_bar(b), 4 * CG);  // one arrive per epilogue warp of the pair
         }
         mbar_init(fin_bar, 1);
+        if (MODE == kWG)
+            for (uint32_t s = 0; s < NS; ++s) {
+                mbar_init(tail_bar(s), 1);
+                mbar_init(clear_bar(s), CG);
+            }
         s_abort = 0;
-        s_issued = 0;
-        s_consumed = 0;
+        s_issued = s_consumed = s_tails_in = s_tails_done = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- producer: this CTA's part of every stage
         if (lane == 0) {
             Ring ring(NS);
-            uint32_t issued = 0;
+            uint32_t issued = 0, tails = 0;
             bool stop = false;
             for (int t = me; t < ntiles && !stop; t += G) {
                 const Item it = tile_item<MODE, CG>(a, first, t);
@@ -363,8 +372,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         stop = true;
                         break;
                     }
-                    if (rank == 0) mbar_expect_tx(full_bar(0) + s8, CG * a.stage_bytes);
-                    const uint32_t bar = full0 + s8;
+                    uint32_t bar = full0 + s8;
+                    if (MODE == kWG && end - r < kDepth && (end - r) % 16) {
+                        if (rank == 0) mbar_arrive(full_bar(0) + s8);
+                        mbar_expect_tx(tail_bar(ring.s), a.stage_bytes);
+                        bar = tail_bar(ring.s);
+                        tails ^= 1u << ring.s;
+                    } else if (rank == 0) {
+                        mbar_expect_tx(full_bar(0) + s8, CG * a.stage_bytes);
+                    }
                     if (MODE == kNK) {
                         load_3d<CG>(sl, &tm_lane, r, lane0, z, bar);
                         load_2d<CG>(sc, &tm_col, r, col0, bar);
@@ -380,9 +396,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             s_issued = issued;
+            s_tails_in = tails;
         }
     } else if (warp == 5) {
         // ---------------- MMA issuer (the pair's first CTA)
+        uint32_t tails = 0;  // bit s: the phase of tail_bar(s) and clear_bar(s)
+        // The rows of the next expert inside the last step of 16 of ring stage s: zeros in both factors.  Both are
+        // cleared because a NaN or infinity there would survive a product with zero.
+        auto clear_tail = [&](uint32_t s, int tail) {
+            int got = 1;
+            if (lane == 0) got = mbar_wait(tail_bar(s), (tails >> s) & 1u, kSpinLimit);
+            if (!__shfl_sync(0xffffffffu, got, 0)) {
+                if (lane == 0) record_error(kErrFull);
+                return false;
+            }
+            tails ^= 1u << s;
+            const uint32_t sl = base + s * a.stage_bytes;
+            const int bad = (-tail) & 15, boxes = 2 + a.TN / CG / 64;
+            for (int q = lane; q < bad * 8 * boxes; q += 32) {
+                const uint32_t at = sl + (q / (bad * 8)) * kBox + (tail + q / 8 % bad) * 128 + q % 8 * 16;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                 leader_addr<CG>(clear_bar(s)))
+                             : "memory");
+            return true;
+        };
         if (rank == 0) {
             // descriptors of stage 0; a stage or a step of 16 adds to their low words (16-byte units)
             const uint64_t ad0 = MODE == kNK ? sw128_desc(base, 16u, 1024u) : sw128_desc(base, kBox, 1024u);
@@ -421,31 +463,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         commit<CG>(empty_bar(0) + s8);
                     }
                 }
-                if (MODE == kWG) __syncwarp();
-                if (tail && (MODE == kWG || lane == 0)) {  // the reduction's last, short stage
-                    ring.s = MODE == kWG ? __shfl_sync(0xffffffffu, ring.s, 0) : ring.s;
+                if (MODE == kWG) ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (MODE == kWG && ok && (tail & 15)) {
+                    ring.s = __shfl_sync(0xffffffffu, ring.s, 0);
+                    ok = clear_tail(ring.s, tail);
+                }
+                if (tail && lane == 0 && ok) {  // the reduction's last, short stage
                     const uint32_t s8 = 8u * ring.s;
-                    if (lane == 0 && ok && !pair_wait<CG>(full_bar(0) + s8, ring.ph)) {
-                        record_error(kErrFull);
-                        ok = false;
-                    }
-                    if (MODE == kWG) ok = __shfl_sync(0xffffffffu, ok, 0);
-                    const int nks = (tail + 15) >> 4;
-                    if (MODE == kWG && ok && (tail & 15)) {
-                        // rows of the next expert inside the last step of 16: zeros in both factors
-                        const uint32_t sl = base + ring.s * a.stage_bytes;
-                        const int bad = nks * 16 - tail, boxes = 2 + a.TN / 64;
-                        for (int q = lane; q < bad * 8 * boxes; q += 32) {
-                            const uint32_t at = sl + (q / (bad * 8)) * kBox + (tail + q / 8 % bad) * 128 + q % 8 * 16;
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-                        }
-                        fence_proxy_async();
-                        __syncwarp();
-                    }
-                    if (lane == 0 && ok) {
-                        tc_fence_after();
+                    ok = pair_wait<CG>(full_bar(0) + s8, ring.ph);
+                    if (MODE == kWG && ok && (tail & 15)) ok = pair_wait<CG>(clear_bar(ring.s), ((tails >> ring.s) & 1u) ^ 1u);
+                    if (!ok) record_error(kErrFull);
+                    tc_fence_after();
+                    if (ok) {
                         const uint64_t ad = ad0 + ring.s * stage_step, bd = bd0 + ring.s * stage_step;
-                        for (int ks = 0; ks < nks; ++ks, acc = 1)
+                        for (int ks = 0; ks < (tail + 15) >> 4; ++ks, acc = 1)
                             mma<CG>(d, ad + static_cast<uint32_t>(ks) * a_step, bd + static_cast<uint32_t>(ks) * b_step,
                                     idesc, acc);
                         commit<CG>(empty_bar(0) + s8);
@@ -462,7 +493,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __shfl_sync(0xffffffffu, ok, 0);
             }
             if (lane == 0) s_consumed = consumed;
+        } else if (MODE == kWG) {
+            // the pair's second CTA: only its part of clearing the tails
+            uint32_t at = 0;
+            for (int t = me; t < ntiles && !s_abort; t += G) {
+                const int red = tile_item<MODE, CG>(a, first, t).red;
+                if ((red & 15) && !clear_tail((at + red / kDepth) % NS, red % kDepth)) {
+                    if (lane == 0) s_abort = 1;
+                    break;
+                }
+                at = (at + (red + kDepth - 1) / kDepth) % NS;
+            }
         }
+        if (lane == 0) s_tails_done = tails;
     } else {
         // ---------------- epilogue warps 0..3: TMEM lane quarter = warp
         int i = 0;
@@ -515,6 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     if (CG == 2) cluster_sync();  // the peer's waits are over too
     else __syncthreads();
+    if (MODE == kWG && s_abort && warp == 4 && lane == 0)
+        for (uint32_t s = 0; s < NS; ++s)
+            if (((s_tails_in ^ s_tails_done) >> s & 1u) && !mbar_wait(tail_bar(s), (s_tails_done >> s) & 1u, kSpinLimit))
+                record_error(kErrDrain);
     if (s_abort && rank == 0) {
         if (warp == 4 && lane == 0) {
             // copies issued but never consumed: wait (bounded) until each has landed
@@ -680,14 +727,15 @@ spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* 
     a.offsets = offsets, a.E = E, a.S = S, a.NL = K, a.NC = N;
     a.C = dW, a.ldc = ldw, a.ce = stride_w, a.c_type = w_type;
     a.TN = N > 128 ? 256 : 128;
-    a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN) * kDepth * 2;
-    a.idesc = idesc_of(type, kWG, 1);
+    const int cg = a.TN == 256 && K > 128 ? 2 : 1;
+    a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
+    a.idesc = idesc_of(type, kWG, cg);
     CUtensorMap tl, tc;
     if (!make_map3(&tl, A, type, K, S, lda, 0, 0, 64) || !make_map3(&tc, G, type, N, S, ldg, 0, 0, 64))
         return SPX_ERR_CUDA;
-    const long long tiles = static_cast<long long>(E) * ((K + 127) / 128) * ((N + a.TN - 1) / a.TN);
+    const long long tiles = static_cast<long long>(E) * ((K + 128 * cg - 1) / (128 * cg)) * ((N + a.TN - 1) / a.TN);
     if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;
-    return launch<kWG, 1>(tl, tc, a, tiles, st);
+    return cg == 2 ? launch<kWG, 2>(tl, tc, a, tiles, st) : launch<kWG, 1>(tl, tc, a, tiles, st);
 }
 
 }  // namespace spx_exp

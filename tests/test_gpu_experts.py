@@ -274,7 +274,8 @@ def product_ref(off, A, W):
 PRODUCTS = [("spread", 4, 300, 128, 64), ("spread", 3, 1000, 1000, 776), ("gaps", 12, 700, 264, 520),
             ("one", 5, 600, 96, 200), ("single", 64, 40, 512, 1024), ("empty", 3, 20, 72, 40),
             ("spread", 1, 1, 8, 8), ("spread", 2, 5, 1, 16), ("gaps", 40, 4097, 136, 72), ("spread", 8, 2000, 513, 257),
-            ("spread", 300, 90, 40, 24), ("one", 2, 257, 256, 4096)]
+            ("spread", 300, 90, 40, 24), ("one", 2, 257, 256, 4096),
+            ("spread", 200, 900, 200, 264), ("gaps", 7, 5000, 392, 648)]
 
 
 @pytest.mark.parametrize("load,E,S,N,K", PRODUCTS)
