@@ -34,7 +34,7 @@ namespace {
 
 enum Mode : int { kNK = 0, kKN = 1, kWG = 2 };
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;  // 4 epilogue warps, the lane factor's copies, the MMAs, the column factor's copies
 constexpr int kDepth = 64;                      // reduction length of a stage: one 128-byte swizzle row
 constexpr uint32_t kLaneBytes = 128 * kDepth * 2;  // a stage's lane factor: 128 lanes a CTA, 16 KB
 constexpr uint32_t kBox = 64 * kDepth * 2;      // an MN-major box: 64 long, 64 deep, 8 KB
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
-    __shared__ uint32_t s_issued, s_consumed, s_tails_in, s_tails_done;
+    __shared__ uint32_t s_issued, s_issued_col, s_consumed, s_tails_in, s_tails_done;
     __shared__ __align__(8) uint64_t s_bars[4 * kMaxStages + 5];
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(clear_bar(s), CG);
             }
         s_abort = 0;
-        s_issued = s_consumed = s_tails_in = s_tails_done = 0;
+        s_issued = s_issued_col = s_consumed = s_tails_in = s_tails_done = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -352,8 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (MODE != kWG) ntiles = first[a.E + 1];
     const uint32_t buf_cols = tmem_cols / 2;
 
-    if (warp == 4) {
-        // ---------------- producer: this CTA's part of every stage
+    if (warp == 4 || warp == 6) {
+        // ---------------- producers: this CTA's part of every stage, one thread for each factor (a thread takes
+        // about 250 cycles from one copy to the next, so one alone would hold up the MMAs)
+        const bool lanes = warp == 4;
         if (lane == 0) {
             Ring ring(NS);
             uint32_t issued = 0, tails = 0;
@@ -374,29 +376,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint32_t bar = full0 + s8;
                     if (MODE == kWG && end - r < kDepth && (end - r) % 16) {
-                        if (rank == 0) mbar_arrive(full_bar(0) + s8);
-                        mbar_expect_tx(tail_bar(ring.s), a.stage_bytes);
+                        if (lanes && rank == 0) mbar_arrive(full_bar(0) + s8);
+                        if (lanes) mbar_expect_tx(tail_bar(ring.s), a.stage_bytes);
                         bar = tail_bar(ring.s);
                         tails ^= 1u << ring.s;
-                    } else if (rank == 0) {
+                    } else if (lanes && rank == 0) {
                         mbar_expect_tx(full_bar(0) + s8, CG * a.stage_bytes);
                     }
-                    if (MODE == kNK) {
-                        load_3d<CG>(sl, &tm_lane, r, lane0, z, bar);
-                        load_2d<CG>(sc, &tm_col, r, col0, bar);
-                    } else if (MODE == kKN) {
-                        load_3d<CG>(sl, &tm_lane, lane0, r, z, bar);
-                        load_3d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, z, bar);
-                        load_2d<CG>(sc, &tm_col, r, col0, bar);
-                    } else {
-                        load_2d<CG>(sl, &tm_lane, lane0, r, bar);
-                        load_2d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, bar);
+                    if (lanes) {
+                        if (MODE == kNK) {
+                            load_3d<CG>(sl, &tm_lane, r, lane0, z, bar);
+                        } else if (MODE == kKN) {
+                            load_3d<CG>(sl, &tm_lane, lane0, r, z, bar);
+                            load_3d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, z, bar);
+                        } else {
+                            load_2d<CG>(sl, &tm_lane, lane0, r, bar);
+                            load_2d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, bar);
+                        }
+                    } else if (MODE == kWG) {
                         for (int c = 0; c < a.TN / CG; c += 64) load_2d<CG>(sc + c / 64 * kBox, &tm_col, col0 + c, r, bar);
+                    } else {
+                        load_2d<CG>(sc, &tm_col, r, col0, bar);
                     }
                 }
             }
-            s_issued = issued;
-            s_tails_in = tails;
+            (lanes ? s_issued : s_issued_col) = issued;
+            if (lanes) s_tails_in = tails;
         }
     } else if (warp == 5) {
         // ---------------- MMA issuer (the pair's first CTA)
@@ -564,8 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 record_error(kErrDrain);
     if (s_abort && rank == 0) {
         if (warp == 4 && lane == 0) {
-            // copies issued but never consumed: wait (bounded) until each has landed
-            for (uint32_t g = s_consumed; g < s_issued; ++g)
+            // copies issued but never consumed: wait (bounded) until each has landed (a stage that only one factor's
+            // copies were issued for runs into the limit, by which time they have)
+            for (uint32_t g = s_consumed; g < max(s_issued, s_issued_col); ++g)
                 if (!mbar_wait(full_bar(g % NS), (g / NS) & 1u, kSpinLimit)) {
                     record_error(kErrDrain);
                     break;
