@@ -849,6 +849,8 @@ def spx_spmm_bsr(M: int, K: int, br: int, bc: int, bsr_row_ptr, bsr_col, bsr_val
 
 
 # ------------------------------------------------------------------ routed experts
+# A decoded token's calls run for a few microseconds each, so these bindings ask torch for as little as
+# they can: one shape, one stride, one address an operand, and the stream's raw handle.
 
 _SPX_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int8: 3}
 
@@ -860,26 +862,48 @@ def _type(t: torch.Tensor) -> int:
     return code
 
 
-def _new(shape, dtype, device, stream):
+def _new(shape, dtype, like, stream):
     """An output or scratch tensor that belongs to the stream the call runs on, so that its memory is
     not handed out again before that stream has passed the call."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _rows(t: torch.Tensor, what: str) -> int:
-    """Row pitch of a 2-D operand whose columns are adjacent."""
-    _require(t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1), f"{what} must be 2-D with unit column stride")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+def _raw_stream(like: torch.Tensor, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(like.get_device()) or None
+    return stream.cuda_stream or None
 
 
-def _addr(t: torch.Tensor | None):
-    if t is None or not t.numel():
-        return None
-    _require(t.is_cuda, "the routed-expert calls take device tensors")
-    return t.data_ptr()
+def _mat(t: torch.Tensor, what: str):
+    """(rows, columns, row pitch, address) of a 2-D device operand whose columns are adjacent."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D device tensor")
+    n, m = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and m > 1:
+        raise ValueError(f"{what} must have unit column stride")
+    return n, m, ld if n > 1 else max(m, ld), t.data_ptr() if n and m else None
+
+
+def _vec(t: torch.Tensor, n: int, dtype, what: str):
+    """Address of a dense device array of n values of a type."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what} must be a dense device tensor of {n} {dtype}")
+    return t.data_ptr() if n else None
+
+
+def _out(t, n: int, m: int, dtype, like, what: str, stream):
+    """The caller's output operand, or a new one: (tensor, row pitch, address)."""
+    if t is None:
+        t = _new((n, m), dtype, like, stream)
+        return t, m, t.data_ptr() if n and m else None
+    rows, cols, ld, at = _mat(t, what)
+    if rows != n or cols != m or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be {n} x {m} {dtype or ''}")
+    return t, ld, at
 
 
 @dataclass
@@ -897,114 +921,104 @@ class Route:
     def slots(self) -> int:
         return self.T * self.k
 
+    def _places(self):
+        """Addresses of pos and of offsets[E]."""
+        return (_vec(self.pos, self.T * self.k, torch.int32, "pos"),
+                _vec(self.offsets, self.E + 1, torch.int32, "offsets") + 4 * self.E)
+
 
 def spx_route_build(expert: torch.Tensor, E: int, stream=None, scratch: torch.Tensor | None = None) -> Route:
     """Sort the slots of expert[T, k] (int32 or int64 ids; one outside [0, E), -1 say, is dropped) by expert."""
-    _require(expert.dtype in (torch.int32, torch.int64), "expert ids must be int32 or int64")
-    lde = _rows(expert, "expert")
-    T, k = expert.shape
-    lib, dev = _lib(), expert.device
+    dt = expert.dtype
+    if dt != torch.int32 and dt != torch.int64:
+        raise ValueError("expert ids must be int32 or int64")
+    T, k, lde, at = _mat(expert, "expert")
+    lib = _lib()
     S = T * k
-    block = _new(E + 1 + 2 * S, torch.int32, dev, stream)  # one allocation for the three arrays
-    offsets, slot, pos = block[:E + 1], block[E + 1:E + 1 + S], block[E + 1 + S:]
-    if scratch is None:
-        need = lib.spx_route_scratch_bytes(T, k, E)
-        if need:
-            scratch = _new(need // 4, torch.int32, dev, stream)
-    _check(lib.spx_route_build(T, k, E, _addr(expert), expert.element_size(), lde, offsets.data_ptr(), _addr(slot),
-                               _addr(pos), _addr(scratch), scratch.numel() * scratch.element_size() if scratch is not None else 0,
-                               _stream(stream)), "spx_route_build")
+    offsets, slot, pos = (_new(n, torch.int32, expert, stream) for n in (E + 1, S, S))
+    need = lib.spx_route_scratch_bytes(T, k, E)
+    if need and scratch is None:
+        scratch = _new(need // 4, torch.int32, expert, stream)
+    _check(lib.spx_route_build(T, k, E, at, 4 if dt == torch.int32 else 8, lde, offsets.data_ptr(),
+                               slot.data_ptr() if S else None, pos.data_ptr() if S else None, scratch.data_ptr() if need else None,
+                               scratch.numel() * scratch.element_size() if need else 0, _raw_stream(expert, stream)),
+           "spx_route_build")
     return Route(T, k, E, offsets, slot, pos)
-
-
-def _route_end(r: Route):
-    return r.offsets.data_ptr() + 4 * r.E
 
 
 def spx_route_gather(r: Route, X: torch.Tensor, Xs: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Xs[place of slot (t, j)] = X[t] (any of the four types), zeros past offsets[E]."""
-    ldx = _rows(X, "X")
-    _require(X.shape[0] == r.T, "X needs one row a token")
-    if Xs is None:
-        Xs = _new((r.slots, X.shape[1]), X.dtype, X.device, stream)
-    ldxs = _rows(Xs, "Xs")
-    _require(Xs.shape[0] == r.slots and Xs.shape[1] == X.shape[1] and Xs.dtype == X.dtype, "Xs needs one row a slot")
-    _check(_lib().spx_route_gather(r.T, r.k, X.shape[1], _type(X), _addr(r.pos), _route_end(r), _addr(X), ldx,
-                                   _addr(Xs), ldxs, _stream(stream)), "spx_route_gather")
+    T, H, ldx, at = _mat(X, "X")
+    if T != r.T:
+        raise ValueError("X needs one row a token")
+    Xs, ldxs, to = _out(Xs, r.slots, H, X.dtype, X, "Xs", stream)
+    pos, end = r._places()
+    _check(_lib().spx_route_gather(T, r.k, H, _type(X), pos, end, at, ldx, to, ldxs, _raw_stream(X, stream)),
+           "spx_route_gather")
     return Xs
-
-
-def _weights(r: Route, weight):
-    if weight is None:
-        return None
-    _require(weight.dtype == torch.float32 and weight.is_contiguous() and weight.numel() == r.slots,
-             "weights must be float32, dense, one a slot")
-    return _addr(weight)
 
 
 def spx_route_combine(r: Route, Ys: torch.Tensor, weight: torch.Tensor | None = None, Y: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
     """Y[t] = sum over t's kept slots of weight * Ys[place] (no weights: all ones, the gradient of spx_route_gather)."""
-    ldys = _rows(Ys, "Ys")
-    _require(Ys.shape[0] == r.slots, "Ys needs one row a slot")
-    if Y is None:
-        Y = _new((r.T, Ys.shape[1]), Ys.dtype, Ys.device, stream)
-    ldy = _rows(Y, "Y")
-    _require(Y.shape[0] == r.T and Y.shape[1] == Ys.shape[1] and Y.dtype == Ys.dtype, "Y needs one row a token")
-    _check(_lib().spx_route_combine(r.T, r.k, Ys.shape[1], _type(Ys), _addr(r.pos), _weights(r, weight), _addr(Ys),
-                                    ldys, _addr(Y), ldy, _stream(stream)), "spx_route_combine")
+    S, H, ldys, at = _mat(Ys, "Ys")
+    if S != r.slots:
+        raise ValueError("Ys needs one row a slot")
+    w = _vec(weight, S, torch.float32, "weight") if weight is not None else None
+    Y, ldy, to = _out(Y, r.T, H, Ys.dtype, Ys, "Y", stream)
+    _check(_lib().spx_route_combine(r.T, r.k, H, _type(Ys), r._places()[0], w, at, ldys, to, ldy, _raw_stream(Ys, stream)),
+           "spx_route_combine")
     return Y
 
 
 def spx_route_combine_grad(r: Route, dY: torch.Tensor, Ys: torch.Tensor | None = None,
                            weight: torch.Tensor | None = None, dYs: torch.Tensor | None = None, stream=None):
     """Gradients of spx_route_combine: (dYs[T*k, H], dweight[T, k] fp32); without Ys only dYs (dweight None)."""
-    lddy = _rows(dY, "dY")
-    _require(dY.shape[0] == r.T, "dY needs one row a token")
-    ldys = 0
+    T, H, lddy, at = _mat(dY, "dY")
+    if T != r.T:
+        raise ValueError("dY needs one row a token")
+    S, ldys, ys, dw, dwp = r.slots, 0, None, None, None
     if Ys is not None:
-        ldys = _rows(Ys, "Ys")
-        _require(Ys.shape[0] == r.slots and Ys.shape[1] == dY.shape[1] and Ys.dtype == dY.dtype,
-                 "Ys needs one row a slot")
-    if dYs is None:
-        dYs = _new((r.slots, dY.shape[1]), dY.dtype, dY.device, stream)
-    lddys = _rows(dYs, "dYs")
-    _require(dYs.shape[0] == r.slots and dYs.shape[1] == dY.shape[1] and dYs.dtype == dY.dtype,
-             "dYs needs one row a slot")
-    dw = _new((r.T, r.k), torch.float32, dY.device, stream) if Ys is not None else None
-    _check(_lib().spx_route_combine_grad(r.T, r.k, dY.shape[1], _type(dY), _addr(r.pos), _route_end(r),
-                                         _weights(r, weight), _addr(dY), lddy, _addr(Ys), ldys, _addr(dYs), lddys,
-                                         _addr(dw), _stream(stream)), "spx_route_combine_grad")
+        n, m, ldys, ys = _mat(Ys, "Ys")
+        if n != S or m != H or Ys.dtype != dY.dtype:
+            raise ValueError("Ys needs one row a slot")
+        dw = _new((T, r.k), torch.float32, dY, stream)
+        dwp = dw.data_ptr() if S else None
+    w = _vec(weight, S, torch.float32, "weight") if weight is not None else None
+    dYs, lddys, to = _out(dYs, S, H, dY.dtype, dY, "dYs", stream)
+    pos, end = r._places()
+    _check(_lib().spx_route_combine_grad(T, r.k, H, _type(dY), pos, end, w, at, lddy, ys, ldys, to, lddys, dwp,
+                                         _raw_stream(dY, stream)), "spx_route_combine_grad")
     return dYs, dw
 
 
-def _expert_weights(W: torch.Tensor, what: str):
-    _require(W.dim() == 3 and (W.stride(2) == 1 or W.shape[2] <= 1), f"{what} must be 3-D with unit stride in its last axis")
-    return (W.stride(1) if W.shape[1] > 1 else max(W.shape[2], W.stride(1))), (W.stride(0) if W.shape[0] > 1 else 0)
-
-
-def _offsets(offsets: torch.Tensor, E: int):
-    _require(offsets.dtype == torch.int32 and offsets.is_contiguous() and offsets.numel() == E + 1,
-             "offsets must be int32, dense, E + 1 of them")
-    return _addr(offsets)
+def _experts(W: torch.Tensor, what: str):
+    """(experts, rows, columns, row pitch, expert stride, address) of a 3-D device operand."""
+    if W.dim() != 3 or not W.is_cuda:
+        raise ValueError(f"{what} must be a 3-D device tensor")
+    E, n, m = W.shape
+    se, ld, unit = W.stride()
+    if unit != 1 and m > 1:
+        raise ValueError(f"{what} must have unit stride in its last axis")
+    return E, n, m, ld if n > 1 else max(m, ld), se if E > 1 else 0, W.data_ptr() if E and n and m else None
 
 
 def spx_gemm_grouped(offsets: torch.Tensor, A: torch.Tensor, W: torch.Tensor, C: torch.Tensor | None = None,
                      layout: str = "nk", dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
     """C[p] = A[p] times expert e's weights for its rows offsets[e] <= p < offsets[e+1], zeros past the last.
     layout "nk": W[e] holds N output channels of K; "kn": K rows of N.  C in A's type or float32 (dtype)."""
-    lda = _rows(A, "A")
-    ldw, sw = _expert_weights(W, "W")
-    _require(layout in ("nk", "kn"), "layout must be 'nk' or 'kn'")
-    E, S = W.shape[0], A.shape[0]
-    N, K = (W.shape[1], W.shape[2]) if layout == "nk" else (W.shape[2], W.shape[1])
-    _require(A.shape[1] == K and W.dtype == A.dtype, "A and W do not fit")
-    if C is None:
-        C = _new((S, N), dtype or A.dtype, A.device, stream)
-    ldc = _rows(C, "C")
-    _require(C.shape[0] == S and C.shape[1] == N, "C must be S x N")
-    _check(_lib().spx_gemm_grouped(E, S, N, K, _offsets(offsets, E), _addr(A), lda, _addr(W), ldw, sw,
-                                   0 if layout == "nk" else 1, _type(A), _addr(C), ldc, _type(C), _stream(stream)),
+    S, K, lda, a = _mat(A, "A")
+    E, N, k, ldw, sw, w = _experts(W, "W")
+    if layout == "kn":
+        N, k = k, N
+    elif layout != "nk":
+        raise ValueError("layout must be 'nk' or 'kn'")
+    dt = A.dtype
+    if k != K or W.dtype != dt:
+        raise ValueError("A and W do not fit")
+    C, ldc, c = _out(C, S, N, (dtype or dt) if C is None else dtype, A, "C", stream)
+    _check(_lib().spx_gemm_grouped(E, S, N, K, _vec(offsets, E + 1, torch.int32, "offsets"), a, lda, w, ldw, sw,
+                                   0 if layout == "nk" else 1, _type(A), c, ldc, _type(C), _raw_stream(A, stream)),
            "spx_gemm_grouped")
     return C
 
@@ -1012,31 +1026,30 @@ def spx_gemm_grouped(offsets: torch.Tensor, A: torch.Tensor, W: torch.Tensor, C:
 def spx_gemm_grouped_wgrad(offsets: torch.Tensor, G: torch.Tensor, A: torch.Tensor, dW: torch.Tensor | None = None,
                            dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
     """dW[e] (N x K) = G_e^T A_e over expert e's rows of G (S x N) and A (S x K); A's type or float32 (dtype)."""
-    ldg, lda = _rows(G, "G"), _rows(A, "A")
-    E, S, N, K = offsets.numel() - 1, A.shape[0], G.shape[1], A.shape[1]
-    _require(G.shape[0] == S and G.dtype == A.dtype, "G and A do not fit")
+    n, N, ldg, g = _mat(G, "G")
+    S, K, lda, a = _mat(A, "A")
+    E = offsets.numel() - 1
+    if n != S or G.dtype != A.dtype:
+        raise ValueError("G and A do not fit")
     if dW is None:
-        dW = _new((E, N, K), dtype or A.dtype, A.device, stream)
-    ldw, sw = _expert_weights(dW, "dW")
-    _require(dW.shape[0] == E and dW.shape[1] == N and dW.shape[2] == K, "dW must be E x N x K")
-    _check(_lib().spx_gemm_grouped_wgrad(E, S, N, K, _offsets(offsets, E), _addr(G), ldg, _addr(A), lda, _type(A),
-                                         _addr(dW), ldw, sw, _type(dW), _stream(stream)), "spx_gemm_grouped_wgrad")
+        dW = _new((E, N, K), dtype or A.dtype, A, stream)
+    e, n, k, ldw, sw, w = _experts(dW, "dW")
+    if e != E or n != N or k != K:
+        raise ValueError(f"dW must be {E} x {N} x {K}")
+    _check(_lib().spx_gemm_grouped_wgrad(E, S, N, K, _vec(offsets, E + 1, torch.int32, "offsets"), g, ldg, a, lda,
+                                         _type(A), w, ldw, sw, _type(dW), _raw_stream(A, stream)),
+           "spx_gemm_grouped_wgrad")
     return dW
 
 
 def spx_quant_rows_i8(X: torch.Tensor, Q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
     """(Q int8, scale fp32): each row divided by its largest magnitude / 127 and rounded to whole numbers."""
-    ldx = _rows(X, "X")
-    if Q is None:
-        Q = _new(X.shape, torch.int8, X.device, stream)
+    M, K, ldx, x = _mat(X, "X")
+    Q, ldq, q = _out(Q, M, K, torch.int8, X, "Q", stream)
     if scale is None:
-        scale = _new(X.shape[0], torch.float32, X.device, stream)
-    ldq = _rows(Q, "Q")
-    _require(Q.shape == X.shape and Q.dtype == torch.int8, "Q must be int8 of X's shape")
-    _require(scale.dtype == torch.float32 and scale.is_contiguous() and scale.numel() == X.shape[0],
-             "scale must be float32, dense, one a row")
-    _check(_lib().spx_quant_rows_i8(X.shape[0], X.shape[1], _type(X), _addr(X), ldx, _addr(Q), ldq, _addr(scale),
-                                    _stream(stream)), "spx_quant_rows_i8")
+        scale = _new(M, torch.float32, X, stream)
+    _check(_lib().spx_quant_rows_i8(M, K, _type(X), x, ldx, q, ldq, _vec(scale, M, torch.float32, "scale"),
+                                    _raw_stream(X, stream)), "spx_quant_rows_i8")
     return Q, scale
 
 
@@ -1045,29 +1058,24 @@ def spx_gemm_i8(Q: torch.Tensor, row_scale: torch.Tensor, W: torch.Tensor, w_sca
                 stream=None, scratch: torch.Tensor | None = None) -> torch.Tensor:
     """C[p, n] = row_scale[p] * w_scale[n] * (Q[p] . W[n]), exact int32 sums.  W is N x K with w_scale[N], or with
     offsets E x N x K with w_scale[E, N], each expert's weights for its rows.  C in dtype (default float32)."""
-    ldq = _rows(Q, "Q")
-    W3 = W if offsets is not None else W.unsqueeze(0)
-    ldw, sw = _expert_weights(W3, "W")
-    E, N, K = W3.shape
-    S = Q.shape[0]
-    _require(Q.dtype == torch.int8 and W.dtype == torch.int8 and Q.shape[1] == K, "Q and W must be int8 and fit")
-    _require(row_scale.dtype == torch.float32 and row_scale.is_contiguous() and row_scale.numel() == S,
-             "row_scale must be float32, dense, one a row")
-    _require(w_scale.dtype == torch.float32 and w_scale.is_contiguous() and w_scale.numel() == E * N,
-             "w_scale must be float32, dense, one a channel")
-    if C is None:
-        C = _new((S, N), dtype or torch.float32, Q.device, stream)
-    ldc = _rows(C, "C")
-    _require(C.shape[0] == S and C.shape[1] == N, "C must be S x N")
+    S, K, ldq, q = _mat(Q, "Q")
+    if offsets is None:
+        E, sw = 1, 0
+        N, k, ldw, w = _mat(W, "W")
+    else:
+        E, N, k, ldw, sw, w = _experts(W, "W")
+    if Q.dtype != torch.int8 or W.dtype != torch.int8 or k != K:
+        raise ValueError("Q and W must be int8 and fit")
+    rs, ws = _vec(row_scale, S, torch.float32, "row_scale"), _vec(w_scale, E * N, torch.float32, "w_scale")
+    C, ldc, c = _out(C, S, N, (dtype or torch.float32) if C is None else dtype, Q, "C", stream)
     lib = _lib()
-    if scratch is None:
-        need = lib.spx_gemm_i8_scratch_bytes(E, S, N, K)
-        if need:
-            scratch = _new(need, torch.uint8, Q.device, stream)
-    _check(lib.spx_gemm_i8(E, S, N, K, _offsets(offsets, E) if offsets is not None else None, _addr(Q), ldq,
-                           _addr(row_scale), _addr(W), ldw, sw, _addr(w_scale), _addr(C), ldc, _type(C),
-                           _addr(scratch), scratch.numel() * scratch.element_size() if scratch is not None else 0,
-                           _stream(stream)), "spx_gemm_i8")
+    need = lib.spx_gemm_i8_scratch_bytes(E, S, N, K)
+    if need and scratch is None:
+        scratch = _new(need, torch.uint8, Q, stream)
+    _check(lib.spx_gemm_i8(E, S, N, K, _vec(offsets, E + 1, torch.int32, "offsets") if offsets is not None else None,
+                           q, ldq, rs, w, ldw, sw, ws, c, ldc, _type(C), scratch.data_ptr() if need else None,
+                           scratch.numel() * scratch.element_size() if need else 0, _raw_stream(Q, stream)),
+           "spx_gemm_i8")
     return C
 
 
