@@ -96,7 +96,6 @@ struct SimtGemm {
     long long li, lr, rj, rr, re;  // element strides; re: of R between experts
     void* C;
     long long ldc, ce;             // row pitch of C, and its stride between experts
-    const float *row_scale, *col_scale;  // 8-bit integers only: [S], [E * NJ]
     const int* offsets;            // NULL: one expert with all S rows
     int E, S, NI, NJ, NR;          // rows of experts run over i (by_rows) or over r
     bool by_rows;
@@ -110,6 +109,9 @@ bool tc_product_fits(const void* A, int64_t lda, const void* W, int64_t ldw, int
 spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void* A, int64_t lda, const void* W,
                       int64_t ldw, int64_t stride_w, spx_w_layout layout, spx_type type, void* C, int64_t ldc,
                       spx_type c_type, cudaStream_t st);
+spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const void* Q, int64_t ldq,
+                         const float* row_scale, const void* W, int64_t ldw, int64_t mats, const float* col_scale,
+                         void* C, int64_t ldc, spx_type c_type, cudaStream_t st);
 bool tc_wgrad_fits(const void* G, int64_t ldg, const void* A, int64_t lda);
 spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* G, int64_t ldg, const void* A,
                     int64_t lda, spx_type type, void* dW, int64_t ldw, int64_t stride_w, spx_type w_type,

@@ -34,11 +34,21 @@ namespace {
 
 enum Mode : int { kNK = 0, kKN = 1, kWG = 2 };
 
-constexpr int kThreads = 224;  // 4 epilogue warps, the lane factor's copies, the MMAs, the column factor's copies
+// Warps: 4 that store (8 for 8-bit integers, each with half of the tile's
+// rows), one for the lane factor's copies, one for the MMAs, one for the
+// column factor's copies.
+template <bool I8>
+constexpr int kStoreWarps = I8 ? 8 : 4;
+template <bool I8>
+constexpr int kThreads = 32 * (kStoreWarps<I8> + 3);
 constexpr int kDepth = 64;                      // reduction length of a stage: one 128-byte swizzle row
 constexpr uint32_t kLaneBytes = 128 * kDepth * 2;  // a stage's lane factor: 128 lanes a CTA, 16 KB
 constexpr uint32_t kBox = 64 * kDepth * 2;      // an MN-major box: 64 long, 64 deep, 8 KB
 constexpr int kMaxStages = 12;
+// 8-bit codes are held as fp16, exactly; a product is at most 2^14 and an fp32
+// sum of 1024 of them at most 2^24, so every partial sum up to there is an
+// exact whole number.  Longer sums go to int32 registers every 1024 terms.
+constexpr int kExact = 1024;
 constexpr int kBand = 8;                        // row tiles that run side by side before the next lane tile
 constexpr size_t kSmemMax = 224 * 1024;         // dynamic shared memory of a CTA
 constexpr long long kSpinLimit = 2000000000LL;  // cycles (~1 s): only a broken pipeline reaches it
@@ -62,6 +72,8 @@ struct TcArgs {
     void* C;
     long long ldc, ce;
     spx_type c_type;
+    bool wide_c;      // 16-bit output with rows on 16-byte boundaries, NL a multiple of 8
+    const float *row_scale, *col_scale;  // 8-bit integers: [S], [E * NL]
 };
 
 struct Item {
@@ -231,22 +243,95 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One accumulator column chunk (32 columns from c0) of this thread's output column.
+// Two floats as a pair of 16-bit values, `lo` in the low half.
 template <class O>
-__device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, O* col, int c0, const uint32_t (&v)[32]) {
-    O* q = col + static_cast<long long>(it.row0 + c0) * a.ldc;
-    if (c0 + 32 <= it.rows) {
+__device__ __forceinline__ uint32_t pack(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// 32 accumulator columns (output rows) of a warp's 32 lanes (output columns)
+// as matrix fragments: thread t's value (h, q, i) -- v[16 h + 4 q + i] -- is
+// lane 16 h + t / 4 + 8 (i / 2), column 8 q + 2 (t % 4) + i % 2.
+__device__ __forceinline__ void load_frag(uint32_t taddr, uint32_t (&v)[32]) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j, q += a.ldc) *q = from_f<O>(__uint_as_float(v[j]));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j, q += a.ldc)
-            if (c0 + j < it.rows) *q = from_f<O>(__uint_as_float(v[j]));
+    for (int h = 0; h < 2; ++h) {
+        uint32_t* r = v + 16 * h;
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16)));
     }
 }
 
-template <int MODE, int CG>
-__global__ void __launch_bounds__(kThreads, 1)
+// Row pitch of a warp's transpose buffer: 64 bytes of a row and 16 of slack,
+// so that neither the matrices' rows nor the reads of whole rows share banks.
+constexpr uint32_t kPatchPitch = 80, kPatchBytes = 32 * kPatchPitch;
+
+// Stores 32 output rows from it.row0 + c0 on of the output columns x .. x + 31.
+// 16-bit rows on 16-byte boundaries (`wide`) go through the warp's patch of
+// shared memory: stmatrix transposes 8 x 8 blocks, and each store then covers
+// eight rows of 64 bytes (about 50 instructions for the 1024 values against
+// 160 for storing each by itself; one storing warp a scheduler issues them, so
+// their number is what the stores cost).
+template <class O>
+__device__ __forceinline__ void store_rows(const TcArgs& a, const Item& it, O* C, int x, int lane, bool wide,
+                                           uint32_t patch, int c0, const float (&v)[32]) {
+    C += static_cast<long long>(it.row0 + c0) * a.ldc + x;
+    const int rows = it.rows - c0, cols = a.NL - x;
+    if constexpr (sizeof(O) == 2) {
+        if (wide) {
+#pragma unroll
+            for (int hg = 0; hg < 4; ++hg) {
+                const float* f = v + 16 * (hg >> 1) + 2 * (hg & 1);
+                asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 patch + lane * kPatchPitch + 16 * hg),
+                             "r"(pack<O>(f[0], f[1])), "r"(pack<O>(f[4], f[5])), "r"(pack<O>(f[8], f[9])),
+                             "r"(pack<O>(f[12], f[13]))
+                             : "memory");
+            }
+            __syncwarp();
+            const int r = lane >> 2, p = lane & 3;
+            O* q = C + r * a.ldc + 8 * p;
+#pragma unroll
+            for (int u = 0; u < 4; ++u, q += 8 * a.ldc) {
+                uint4 w;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                             : "r"(patch + (r + 8 * u) * kPatchPitch + 16 * p)
+                             : "memory");
+                if (r + 8 * u < rows && 8 * p < cols) *reinterpret_cast<uint4*>(q) = w;
+            }
+            __syncwarp();
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const int n = 16 * (i >> 4) + (lane >> 2) + 8 * ((i >> 1) & 1), r = 8 * ((i >> 2) & 3) + 2 * (lane & 3) + (i & 1);
+        if (n < cols && r < rows) C[r * a.ldc + n] = from_f<O>(v[i]);
+    }
+}
+
+__device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, long long off, int x, int lane,
+                                            uint32_t patch, int c0, const float (&v)[32]) {
+    if (a.c_type == SPX_F32) store_rows(a, it, static_cast<float*>(a.C) + off, x, lane, false, patch, c0, v);
+    else if (a.c_type == SPX_BF16)
+        store_rows(a, it, static_cast<__nv_bfloat16*>(a.C) + off, x, lane, a.wide_c, patch, c0, v);
+    else store_rows(a, it, static_cast<__half*>(a.C) + off, x, lane, a.wide_c, patch, c0, v);
+}
+
+template <int MODE, int CG, bool I8>
+__global__ void __launch_bounds__(kThreads<I8>, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tm_lane, const __grid_constant__ CUtensorMap tm_col,
                       const __grid_constant__ TcArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -268,9 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tail_bar = [&](uint32_t s) { return bars + 8u * (2 * kMaxStages + 5 + s); };
     auto clear_bar = [&](uint32_t s) { return bars + 8u * (3 * kMaxStages + 5 + s); };
     const uint32_t NS = a.stages;
-    // the tile list, behind the ring
-    int* first = reinterpret_cast<int*>(smem_raw + (base - smem_u32(smem_raw)) + NS * a.stage_bytes);
+    // the storing warps' patches, then the tile list, behind the ring
+    int* first = reinterpret_cast<int*>(smem_raw + (base - smem_u32(smem_raw)) + NS * a.stage_bytes +
+                                        kStoreWarps<I8> * kPatchBytes);
 
+    constexpr int SW = kStoreWarps<I8>, LOAD = SW, MMA = SW + 1, LOAD2 = SW + 2;  // the roles' warps
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank = 0;
     if (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -284,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), 4 * CG);  // one arrive per epilogue warp of the pair
+            mbar_init(tempty_bar(b), SW * CG);  // one arrive per storing warp of the pair
         }
         mbar_init(fin_bar, 1);
         if (MODE == kWG)
@@ -297,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 5) {
+    if (warp == MMA) {
         if (CG == 1) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                          "r"(tmem_cols)
@@ -315,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ntiles = a.E * ((a.NL + 128 * CG - 1) / (128 * CG)) * ((a.NC + a.TN - 1) / a.TN);
     } else {
         const int nlt = (a.NL + 128 * CG - 1) / (128 * CG);
-        for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+        for (int e = threadIdx.x; e <= a.E; e += kThreads<I8>) {
             int lo = 0, hi = a.S;
             if (a.offsets) {
                 if (e < a.E) expert_rows(a.offsets, e, a.S, lo, hi);
@@ -352,10 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (MODE != kWG) ntiles = first[a.E + 1];
     const uint32_t buf_cols = tmem_cols / 2;
 
-    if (warp == 4 || warp == 6) {
+    if (warp == LOAD || warp == LOAD2) {
         // ---------------- producers: this CTA's part of every stage, one thread for each factor (a thread takes
         // about 250 cycles from one copy to the next, so one alone would hold up the MMAs)
-        const bool lanes = warp == 4;
+        const bool lanes = warp == LOAD;
         if (lane == 0) {
             Ring ring(NS);
             uint32_t issued = 0, tails = 0;
@@ -403,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             (lanes ? s_issued : s_issued_col) = issued;
             if (lanes) s_tails_in = tails;
         }
-    } else if (warp == 5) {
+    } else if (warp == MMA) {
         // ---------------- MMA issuer (the pair's first CTA)
         uint32_t tails = 0;  // bit s: the phase of tail_bar(s) and clear_bar(s)
         // The rows of the next expert inside the last step of 16 of ring stage s: zeros in both factors.  Both are
@@ -445,7 +532,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Item it = tile_item<MODE, CG>(a, first, t);
                 const uint32_t ncols = MODE == kWG ? a.TN : mma_cols<CG>(it.rows);
                 const uint32_t idesc = a.idesc | ((ncols >> 3) << 17);
-                const int whole = it.red / kDepth, tail = it.red % kDepth;
+                int left = it.red;
+                do {  // one accumulator's worth: the whole reduction, or kExact terms of it
+                const int now = I8 ? min(left, kExact) : left;
+                left -= now;
+                const int whole = now / kDepth, tail = now % kDepth;
                 uint32_t acc = 0;
                 if (lane == 0) {
                     ok = pair_wait<CG>(tempty_bar(buf), tph) && !s_abort;
@@ -496,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (buf == 0) tph ^= 1u;
                 __syncwarp();
                 ok = __shfl_sync(0xffffffffu, ok, 0);
+                } while (I8 && left > 0 && ok);
             }
             if (lane == 0) s_consumed = consumed;
         } else if (MODE == kWG) {
@@ -512,42 +604,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) s_tails_done = tails;
     } else {
-        // ---------------- epilogue warps 0..3: TMEM lane quarter = warp
-        int i = 0;
-        for (int t = me; t < ntiles; t += G, ++i) {
-            const Item it = tile_item<MODE, CG>(a, first, t);
-            const int buf = i & 1;
+        // ---------------- storing warps: TMEM lane quarter = warp % 4
+        int buf = 0;
+        uint32_t tph = 0;
+        auto acc_wait = [&]() {
             int ok = 1;
-            if (lane == 0) ok = (mbar_wait(tfull_bar(buf), (i >> 1) & 1u, kSpinLimit) && !s_abort) ? 1 : 0;
+            if (lane == 0) ok = (mbar_wait(tfull_bar(buf), tph, kSpinLimit) && !s_abort) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) {
-                if (lane == 0) {
-                    record_error(kErrAcc);
-                    s_abort = 1;
-                }
-                break;
+            if (!ok && lane == 0) {
+                record_error(kErrAcc);
+                s_abort = 1;
             }
             tc_fence_after();
-            const int x = it.lane0 + 128 * static_cast<int>(rank) + 32 * warp + lane;
-            const long long off = (MODE == kWG ? it.e * a.ce : 0) + x;
-            const uint32_t src = tmem + buf * buf_cols + (static_cast<uint32_t>(32 * warp) << 16);
-#pragma unroll 1
-            for (int c0 = 0; c0 < it.rows; c0 += 32) {
-                uint32_t v[32];
-                if (it.red > 0) {
-                    tmem_ld32(src + c0, v);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;
-                }
-                if (x < a.NL) {
-                    if (a.c_type == SPX_F32) store_chunk(a, it, static_cast<float*>(a.C) + off, c0, v);
-                    else if (a.c_type == SPX_BF16) store_chunk(a, it, static_cast<__nv_bfloat16*>(a.C) + off, c0, v);
-                    else store_chunk(a, it, static_cast<__half*>(a.C) + off, c0, v);
-                }
-                __syncwarp();
-            }
+            return ok != 0;
+        };
+        auto acc_free = [&]() {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -557,18 +628,100 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      leader_addr<CG>(tempty_bar(buf)))
                                  : "memory");
             }
+            buf ^= 1;
+            if (buf == 0) tph ^= 1u;
+        };
+        const uint32_t patch = base + NS * a.stage_bytes + warp * kPatchBytes;
+        const uint32_t quarter = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        for (int t = me; t < ntiles; t += G) {
+            const Item it = tile_item<MODE, CG>(a, first, t);
+            const int x = it.lane0 + 128 * static_cast<int>(rank) + 32 * (warp & 3);
+            const long long off = MODE == kWG ? it.e * a.ce : 0;
+            if (!I8) {
+                if (!acc_wait()) break;
+                const uint32_t src = tmem + buf * buf_cols + quarter;
+#pragma unroll 1
+                for (int c0 = 0; c0 < it.rows; c0 += 32) {
+                    uint32_t v[32];
+                    if (it.red > 0) {
+                        load_frag(src + c0, v);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    }
+                    float f[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+                    store_chunk(a, it, off, x, lane, patch, c0, f);
+                }
+                acc_free();
+                continue;
+            }
+            // 8-bit integers: the exact partial sums are added in int32, scaled at the end
+            const int half = warp >> 2;  // this warp's rows: [128 half, 128 half + 128) of the tile
+            int sum[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[q][j] = 0;
+            bool ok = true;
+            int left = it.red;
+            do {
+                left -= min(left, kExact);
+                ok = acc_wait();
+                if (!ok) break;
+                const uint32_t src = tmem + buf * buf_cols + quarter;
+                if (it.red > 0) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int c0 = 128 * half + 32 * q;
+                        if (c0 >= it.rows) break;
+                        uint32_t v[32];
+                        load_frag(src + c0, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[q][j] += __float2int_rn(__uint_as_float(v[j]));
+                    }
+                }
+                acc_free();
+            } while (left > 0);
+            if (!ok) break;
+            float cs[4];  // of this thread's four lanes
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int n = x + 8 * g + (lane >> 2);
+                cs[g] = it.e < a.E && n < a.NL ? __ldg(a.col_scale + static_cast<long long>(it.e) * a.NL + n) : 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c0 = 128 * half + 32 * q;
+                if (c0 >= it.rows) break;
+                float f[32];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {  // this thread's eight rows of the 32
+                    const int row = 8 * (r >> 1) + 2 * (lane & 3) + (r & 1);
+                    const float rs = __ldg(a.row_scale + min(it.row0 + c0 + row, a.S - 1));
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int i = 16 * (g >> 1) + 4 * (r >> 1) + 2 * (g & 1) + (r & 1);
+                        f[i] = it.e < a.E ? static_cast<float>(sum[q][i]) * (rs * cs[g]) : 0.f;
+                    }
+                }
+                store_chunk(a, it, off, x, lane, patch, c0, f);
+            }
         }
     }
     __syncwarp();
     tc_fence_before();
     if (CG == 2) cluster_sync();  // the peer's waits are over too
     else __syncthreads();
-    if (MODE == kWG && s_abort && warp == 4 && lane == 0)
+    if (MODE == kWG && s_abort && warp == LOAD && lane == 0)
         for (uint32_t s = 0; s < NS; ++s)
             if (((s_tails_in ^ s_tails_done) >> s & 1u) && !mbar_wait(tail_bar(s), (s_tails_done >> s) & 1u, kSpinLimit))
                 record_error(kErrDrain);
     if (s_abort && rank == 0) {
-        if (warp == 4 && lane == 0) {
+        if (warp == LOAD && lane == 0) {
             // copies issued but never consumed: wait (bounded) until each has landed (a stage that only one factor's
             // copies were issued for runs into the limit, by which time they have)
             for (uint32_t g = s_consumed; g < max(s_issued, s_issued_col); ++g)
@@ -576,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     record_error(kErrDrain);
                     break;
                 }
-        } else if (warp == 5 && lane == 0) {
+        } else if (warp == MMA && lane == 0) {
             // MMAs in flight: one more commit, then wait (bounded) for it
             commit<CG>(fin_bar);
             if (!mbar_wait(fin_bar, 0, kSpinLimit)) record_error(kErrDrain);
@@ -586,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (CG == 2) cluster_sync();
     else __syncthreads();
     tc_fence_after();
-    if (warp == 5) {
+    if (warp == MMA) {
         if (CG == 1)
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols) : "memory");
         else
@@ -643,16 +796,17 @@ int resident_pairs(const void* kernel, const cudaLaunchConfig_t& cfg) {
 
 bool rows_aligned(const void* p, int64_t ld) { return spx_aligned(p, 16) && ld % 8 == 0; }
 
-template <int MODE, int CG>
+template <int MODE, int CG, bool I8 = false>
 spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long long max_tiles, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return SPX_ERR_CUDA;
-    const size_t list = sizeof(int) * (static_cast<size_t>(a.E) + 2);
+    a.wide_c = spx_aligned(a.C, 16) && a.ldc % 8 == 0 && a.ce % 8 == 0 && a.NL % 8 == 0;
+    const size_t list = kStoreWarps<I8> * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.E) + 2);
     a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemMax - 1024 - list) / a.stage_bytes));
     const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + list;
-    if (set_smem_limit(experts_tc_kernel<MODE, CG>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
+    if (set_smem_limit(experts_tc_kernel<MODE, CG, I8>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads<I8>);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -665,11 +819,11 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     int groups = sms;
     if (CG > 1) {
         cfg.gridDim = dim3(sms / CG * CG);
-        groups = resident_pairs(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG>), cfg);
+        groups = resident_pairs(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG, I8>), cfg);
         if (groups <= 0) return SPX_ERR_CUDA;
     }
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(max_tiles, groups)) * CG);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_tc_kernel<MODE, CG>, tl, tc, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_tc_kernel<MODE, CG, I8>, tl, tc, a);
     spx_note_launches(1);
     return spx_cuda_status(e != cudaSuccess ? e : cudaGetLastError());
 }
@@ -720,6 +874,29 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
     a.max_tiles = static_cast<int>(tiles);
     if (cg == 2) return nk ? launch<kNK, 2>(tl, tc, a, tiles, st) : launch<kKN, 2>(tl, tc, a, tiles, st);
     return nk ? launch<kNK, 1>(tl, tc, a, tiles, st) : launch<kKN, 1>(tl, tc, a, tiles, st);
+}
+
+// The 8-bit product on codes held as fp16: Q is S x K (lda), W is mats x N x K
+// (ldw rows, N * ldw apart), both 16-byte aligned.
+spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const void* Q, int64_t ldq,
+                         const float* row_scale, const void* W, int64_t ldw, int64_t mats, const float* col_scale,
+                         void* C, int64_t ldc, spx_type c_type, cudaStream_t st) {
+    TcArgs a{};
+    a.offsets = offsets, a.E = E, a.S = S, a.NL = N, a.NR = K;
+    a.C = C, a.ldc = ldc, a.c_type = c_type;
+    a.row_scale = row_scale, a.col_scale = col_scale;
+    a.same_w = mats == 1;
+    a.TN = 256;
+    const int cg = N > 128 ? 2 : 1;
+    a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
+    a.idesc = idesc_of(SPX_F16, kNK, cg);
+    CUtensorMap tl, tc;
+    if (!make_map3(&tl, W, SPX_F16, K, N, ldw, mats, ldw * N, 128) || !make_map3(&tc, Q, SPX_F16, K, S, ldq, 0, 0, a.TN / cg))
+        return SPX_ERR_CUDA;
+    const long long nlt = (N + 128 * cg - 1) / (128 * cg), tiles = max_row_tiles(E, S, a.TN) * nlt;
+    if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;
+    a.max_tiles = static_cast<int>(tiles);
+    return cg == 2 ? launch<kNK, 2, true>(tl, tc, a, tiles, st) : launch<kNK, 1, true>(tl, tc, a, tiles, st);
 }
 
 bool tc_wgrad_fits(const void* G, int64_t ldg, const void* A, int64_t lda) {

@@ -1,5 +1,12 @@
 // spx_int8.cu -- rows quantised to 8 bits and the product of 8-bit integers
 // with a scale for each row and output channel.
+//
+// This chip has no fast 8-bit integer matrix rate, but fp16 holds every code
+// exactly and the fp16 tensor cores sum their products exactly in fp32 up to
+// 2^24, so the product runs on the experts' tensor-core kernel with codes
+// widened to fp16, and its integer sums stay exact (see kExact there).  A few
+// rows (decoded tokens) are bound by the weights' bytes: they run on the CUDA
+// cores' four-way byte dot product straight from the 8-bit weights.
 #include <algorithm>
 
 #include "spx_experts.cuh"
@@ -8,24 +15,49 @@ using namespace spx_exp;
 
 namespace {
 
-// One CTA a row: its largest magnitude, then the codes.  Bound by HBM: the
-// second read of the row comes from L1 / L2.
-constexpr int kQThreads = 256;
+// ---------------------------------------------------------------- quantisation
 
-template <class V>
+// One CTA a row: its largest magnitude, then the codes.  Bound by HBM.  A row
+// of up to kQHeld pieces a thread stays in registers between the two; a longer
+// one is read again (from L2).
+constexpr int kQThreads = 256, kQHeld = 4;
+
+template <class V, int N>
+struct alignas(N * sizeof(V) >= 16 ? 16 : N * sizeof(V)) Pack {
+    V v[N];
+};
+
+// N values a piece: 16 bytes of X where rows are aligned, else 1 value.
+template <class V, int N>
 __global__ void __launch_bounds__(kQThreads)
     quant_rows_kernel(int K, const V* __restrict__ X, long long ldx, int8_t* __restrict__ Q, long long ldq,
                       float* __restrict__ scale) {
+    using P = Pack<V, N>;
+    using B = Pack<int8_t, N>;
     __shared__ float s_max[kQThreads / 32];
-    const V* x = X + blockIdx.x * ldx;
-    int8_t* q = Q + blockIdx.x * ldq;
+    const P* x = reinterpret_cast<const P*>(X + blockIdx.x * ldx);
+    B* q = reinterpret_cast<B*>(Q + blockIdx.x * ldq);
+    const int np = K / N;
     // a NaN or infinity anywhere makes `bad` NaN: v * 0 is 0 for every other value
     float m = 0.f, bad = 0.f;
-    for (int k = threadIdx.x; k < K; k += kQThreads) {
-        const float v = to_f(x[k]);
-        m = fmaxf(m, fabsf(v));
-        bad = fmaf(v, 0.f, bad);
+    P held[kQHeld];
+    auto look = [&](const P& p) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float v = to_f(p.v[i]);
+            m = fmaxf(m, fabsf(v));
+            bad = fmaf(v, 0.f, bad);
+        }
+    };
+#pragma unroll
+    for (int h = 0; h < kQHeld; ++h) {
+        const int k = threadIdx.x + h * kQThreads;
+        if (k < np) held[h] = x[k];
     }
+#pragma unroll
+    for (int h = 0; h < kQHeld; ++h)
+        if (threadIdx.x + h * kQThreads < np) look(held[h]);
+    for (int k = threadIdx.x + kQHeld * kQThreads; k < np; k += kQThreads) look(x[k]);
     if (bad != bad) m = __int_as_float(0x7f800000);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -37,11 +69,224 @@ __global__ void __launch_bounds__(kQThreads)
     const bool fine = m < __int_as_float(0x7f800000);
     const float s = m / 127.f;
     if (threadIdx.x == 0) scale[blockIdx.x] = fine ? s : __int_as_float(0x7fffffff);
-    for (int k = threadIdx.x; k < K; k += kQThreads) {
-        // a subnormal scale is coarse, so the quotient may pass 127
-        const float v = fine && s > 0.f ? rintf(to_f(x[k]) / s) : 0.f;
-        q[k] = static_cast<int8_t>(fminf(fmaxf(v, -127.f), 127.f));
+    auto code = [&](const P& p) {
+        B b;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // a subnormal scale is coarse, so the quotient may pass 127
+            const float v = fine && s > 0.f ? rintf(to_f(p.v[i]) / s) : 0.f;
+            b.v[i] = static_cast<int8_t>(fminf(fmaxf(v, -127.f), 127.f));
+        }
+        return b;
+    };
+#pragma unroll
+    for (int h = 0; h < kQHeld; ++h) {
+        const int k = threadIdx.x + h * kQThreads;
+        if (k < np) q[k] = code(held[h]);
     }
+    for (int k = threadIdx.x + kQHeld * kQThreads; k < np; k += kQThreads) q[k] = code(x[k]);
+}
+
+template <class V>
+void quant_launch(int M, int K, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, cudaStream_t st) {
+    constexpr int N = 16 / sizeof(V);
+    const V* x = static_cast<const V*>(X);
+    if (spx_aligned(X, 16) && spx_aligned(Q, N) && ldx % N == 0 && ldq % N == 0 && K % N == 0)
+        quant_rows_kernel<V, N><<<M, kQThreads, 0, st>>>(K, x, ldx, Q, ldq, scale);
+    else
+        quant_rows_kernel<V, 1><<<M, kQThreads, 0, st>>>(K, x, ldx, Q, ldq, scale);
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Up to kFew rows of one expert against all its channels: a warp takes kChan
+// channels, its lanes 16 codes of each at a time, so every weight is read
+// once, in 16-byte pieces; the rows' codes come from L1.  Bound by the
+// weights' bytes.
+constexpr int kFew = 8, kChan = 2, kFewThreads = 128;
+
+struct FewArgs {
+    const int* offsets;
+    int E, S, N, K;
+    const int8_t* Q;
+    long long ldq;
+    const float* row_scale;
+    const int8_t* W;
+    long long ldw, stride_w;
+    const float* col_scale;
+    void* C;
+    long long ldc;
+    spx_type c_type;
+};
+
+template <int R>
+__device__ __forceinline__ void few_rows(const FewArgs& a, int e, int r0, int n0, int (&sum)[kFew][kChan]) {
+    const int lane = threadIdx.x & 31, np = a.K / 16;
+    const int4* w[kChan];
+#pragma unroll
+    for (int c = 0; c < kChan; ++c)
+        w[c] = reinterpret_cast<const int4*>(a.W + e * a.stride_w + static_cast<long long>(min(n0 + c, a.N - 1)) * a.ldw);
+    const int4* q = reinterpret_cast<const int4*>(a.Q + r0 * a.ldq);
+    const long long dq = a.ldq / 16;
+    constexpr int U = R <= 2 ? 4 : 2;  // pieces in flight
+    for (int p0 = 0; p0 < np; p0 += 32 * U) {
+        int4 y[U][kChan];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int c = 0; c < kChan; ++c) {
+                const int p = p0 + 32 * u + lane;
+                y[u][c] = p < np ? __ldcs(w[c] + p) : make_int4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = p0 + 32 * u + lane;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int4 x = p < np ? __ldg(q + r * dq + p) : make_int4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < kChan; ++c) {
+                    sum[r][c] = __dp4a(x.x, y[u][c].x, sum[r][c]);
+                    sum[r][c] = __dp4a(x.y, y[u][c].y, sum[r][c]);
+                    sum[r][c] = __dp4a(x.z, y[u][c].z, sum[r][c]);
+                    sum[r][c] = __dp4a(x.w, y[u][c].w, sum[r][c]);
+                }
+            }
+        }
+    }
+}
+
+template <class O>
+__device__ __forceinline__ void few_store(const FewArgs& a, long long i, float v) {
+    static_cast<O*>(a.C)[i] = from_f<O>(v);
+}
+
+__global__ void __launch_bounds__(kFewThreads) i8_few_kernel(FewArgs a) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int e = 0, r0 = 0, hi = a.S;
+    if (a.offsets) {
+        if (!warp_find_tile(a.offsets, a.E, a.S, kFew, blockIdx.y, e, r0, hi)) return;
+    } else {
+        r0 = blockIdx.y * kFew;
+    }
+    const int R = min(kFew, hi - r0);
+    const int n0 = (blockIdx.x * (kFewThreads / 32) + warp) * kChan;
+    if (n0 >= a.N || R <= 0) return;
+    int sum[kFew][kChan];
+#pragma unroll
+    for (int r = 0; r < kFew; ++r)
+#pragma unroll
+        for (int c = 0; c < kChan; ++c) sum[r][c] = 0;
+    if (e < a.E) {
+        if (R == 1) few_rows<1>(a, e, r0, n0, sum);
+        else if (R == 2) few_rows<2>(a, e, r0, n0, sum);
+        else if (R <= 4) {
+            if (R == 3) few_rows<3>(a, e, r0, n0, sum);
+            else few_rows<4>(a, e, r0, n0, sum);
+        } else {
+            switch (R) {
+                case 5: few_rows<5>(a, e, r0, n0, sum); break;
+                case 6: few_rows<6>(a, e, r0, n0, sum); break;
+                case 7: few_rows<7>(a, e, r0, n0, sum); break;
+                default: few_rows<8>(a, e, r0, n0, sum);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kFew; ++r) {
+        if (r >= R) break;
+#pragma unroll
+        for (int c = 0; c < kChan; ++c)
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum[r][c] += __shfl_xor_sync(0xffffffffu, sum[r][c], d);
+    }
+    // lane r * kChan + c stores row r of channel n0 + c
+#pragma unroll
+    for (int r = 0; r < kFew; ++r)
+#pragma unroll
+        for (int c = 0; c < kChan; ++c) {
+            if (lane != r * kChan + c || r >= R || n0 + c >= a.N) continue;
+            const float v = e < a.E ? static_cast<float>(sum[r][c]) *
+                                          (__ldg(a.row_scale + r0 + r) * __ldg(a.col_scale + static_cast<long long>(e) * a.N + n0 + c))
+                                    : 0.f;
+            const long long i = (r0 + r) * a.ldc + n0 + c;
+            if (a.c_type == SPX_F32) few_store<float>(a, i, v);
+            else if (a.c_type == SPX_BF16) few_store<__nv_bfloat16>(a, i, v);
+            else few_store<__half>(a, i, v);
+        }
+}
+
+// ---------------------------------------------------------------- codes to fp16
+
+// Four codes (bytes of w) to fp16: 0x6400 | u is 1024 + u for a byte u, and
+// u = code + 128 after flipping its top bit, so one subtraction is exact.
+__device__ __forceinline__ uint2 widen_codes(uint32_t w) {
+    w ^= 0x80808080u;
+    const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// The rows of Q and of every expert that has rows, as fp16 with a row pitch of
+// Kp (a multiple of 8) values; what lies between K and Kp is never read.
+// blockIdx.y: 0 for Q, 1 + e for W_e.
+constexpr int kWidenThreads = 256;
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(kWidenThreads)
+    widen_kernel(const int* __restrict__ offsets, int S, int N, int K, int Kp, const int8_t* __restrict__ Q,
+                 long long ldq, const int8_t* __restrict__ W, long long ldw, long long stride_w,
+                 __half* __restrict__ Q16, __half* __restrict__ W16, bool same_w) {
+    const int8_t* src = Q;
+    __half* dst = Q16;
+    long long ld = ldq;
+    int rows = S;
+    if (blockIdx.y > 0) {
+        const int e = blockIdx.y - 1;
+        if (offsets && !same_w) {
+            int lo, hi;
+            expert_rows(offsets, e, S, lo, hi);
+            if (lo == hi) return;
+        }
+        src = W + e * stride_w, ld = ldw, rows = N;
+        dst = W16 + static_cast<long long>(e) * N * Kp;
+    }
+    const int np = (K + 15) / 16;
+    const long long total = static_cast<long long>(rows) * np;
+    for (long long i = blockIdx.x * static_cast<long long>(kWidenThreads) + threadIdx.x; i < total;
+         i += static_cast<long long>(gridDim.x) * kWidenThreads) {
+        const int r = static_cast<int>(i / np), k = static_cast<int>(i % np) * 16;
+        const int8_t* s = src + r * ld + k;
+        uint32_t w[4];
+        if (ALIGNED && k + 16 <= K) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(s));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                w[b] = 0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (k + 4 * b + c < K) w[b] |= static_cast<uint32_t>(static_cast<uint8_t>(s[4 * b + c])) << (8 * c);
+            }
+        }
+        uint4* d = reinterpret_cast<uint4*>(dst + static_cast<long long>(r) * Kp + k);
+        const uint2 h0 = widen_codes(w[0]), h1 = widen_codes(w[1]), h2 = widen_codes(w[2]), h3 = widen_codes(w[3]);
+        d[0] = make_uint4(h0.x, h0.y, h1.x, h1.y);
+        if (k + 8 < Kp) d[1] = make_uint4(h2.x, h2.y, h3.x, h3.y);
+    }
+}
+
+// Rows in all up to which the few-rows kernel is taken.
+constexpr int kFewRows = 8;
+
+int pitch16(int K) { return (K + 7) / 8 * 8; }
+
+bool few_fits(int S, const int8_t* Q, int64_t ldq, const int8_t* W, int64_t ldw, int64_t stride_w, int K) {
+    return S <= kFewRows && K % 16 == 0 && spx_aligned(Q, 16) && spx_aligned(W, 16) && ldq % 16 == 0 && ldw % 16 == 0 &&
+           stride_w % 16 == 0;
 }
 
 }  // namespace
@@ -55,18 +300,19 @@ spx_status spx_quant_rows_i8(int32_t M, int32_t K, spx_type type, const void* X,
     if (!scale || (K > 0 && (!X || !Q || ldx < K || ldq < K))) return SPX_ERR_ARG;
     if (!spx_aligned(X, type_bytes(type)) || !spx_aligned(scale, 4)) return SPX_ERR_ALIGN;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (type == SPX_F32)
-        quant_rows_kernel<float><<<M, kQThreads, 0, st>>>(K, static_cast<const float*>(X), ldx, Q, ldq, scale);
-    else if (type == SPX_BF16)
-        quant_rows_kernel<__nv_bfloat16>
-            <<<M, kQThreads, 0, st>>>(K, static_cast<const __nv_bfloat16*>(X), ldx, Q, ldq, scale);
-    else
-        quant_rows_kernel<__half><<<M, kQThreads, 0, st>>>(K, static_cast<const __half*>(X), ldx, Q, ldq, scale);
+    if (type == SPX_F32) quant_launch<float>(M, K, X, ldx, Q, ldq, scale, st);
+    else if (type == SPX_BF16) quant_launch<__nv_bfloat16>(M, K, X, ldx, Q, ldq, scale, st);
+    else quant_launch<__half>(M, K, X, ldx, Q, ldq, scale, st);
     spx_note_launches(1);
     return spx_cuda_status(cudaGetLastError());
 }
 
-size_t spx_gemm_i8_scratch_bytes(int32_t E, int32_t S, int32_t N, int32_t K) { return 0; }
+size_t spx_gemm_i8_scratch_bytes(int32_t E, int32_t S, int32_t N, int32_t K) {
+    if (E <= 0 || S <= 0 || N <= 0 || K <= 0) return 0;
+    const size_t row = 2 * static_cast<size_t>(pitch16(K));
+    const size_t q = (row * S + 255) / 256 * 256;
+    return q + row * N * static_cast<size_t>(E);
+}
 
 spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const int8_t* Q,
                        int64_t ldq, const float* row_scale, const int8_t* W, int64_t ldw, int64_t stride_w,
@@ -81,17 +327,37 @@ spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t
     if (!spx_aligned(offsets, 4) || !spx_aligned(row_scale, 4) || !spx_aligned(w_scale, 4) ||
         !spx_aligned(C, type_bytes(c_type)))
         return SPX_ERR_ALIGN;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const size_t cb = type_bytes(c_type);
+    if (K == 0)
+        return spx_cuda_status(cudaMemset2DAsync(C, static_cast<size_t>(ldc) * cb, 0, static_cast<size_t>(N) * cb,
+                                                 static_cast<size_t>(S), st));
+    if (few_fits(S, Q, ldq, W, ldw, stride_w, K)) {
+        const FewArgs a{offsets, E, S, N, K, Q, ldq, row_scale, W, ldw, stride_w, w_scale, C, ldc, c_type};
+        const long long ty = offsets ? std::min<long long>(max_row_tiles(E, S, kFew), S + 1) : (S + kFew - 1) / kFew;
+        i8_few_kernel<<<dim3((N + kFewThreads / 32 * kChan - 1) / (kFewThreads / 32 * kChan), static_cast<unsigned>(ty)),
+                        kFewThreads, 0, st>>>(a);
+        spx_note_launches(1);
+        return spx_cuda_status(cudaGetLastError());
+    }
     const size_t need = spx_gemm_i8_scratch_bytes(E, S, N, K);
     if (need > 0 && (!scratch || scratch_bytes < need)) return SPX_ERR_ARG;
     if (need > 0 && !spx_aligned(scratch, 256)) return SPX_ERR_ALIGN;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    SimtGemm g{};
-    g.L = Q, g.li = ldq, g.lr = 1;
-    g.R = W, g.rj = ldw, g.rr = 1, g.re = stride_w;
-    g.C = C, g.ldc = ldc;
-    g.row_scale = row_scale, g.col_scale = w_scale;
-    g.offsets = offsets, g.E = E, g.S = S, g.NI = S, g.NJ = N, g.NR = K, g.by_rows = true;
-    return simt_gemm(g, SPX_I8, c_type, st);
+    const bool same_w = E == 1 || stride_w == 0;
+    const int Kp = pitch16(K), mats = same_w ? 1 : E;
+    __half* Q16 = static_cast<__half*>(scratch);
+    __half* W16 = Q16 + (static_cast<size_t>(Kp) * S + 127) / 128 * 128;
+    {
+        const bool aligned = spx_aligned(Q, 16) && spx_aligned(W, 16) && ldq % 16 == 0 && ldw % 16 == 0 && stride_w % 16 == 0;
+        const long long most = static_cast<long long>(std::max(S, N)) * ((K + 15) / 16);
+        const dim3 grid(static_cast<unsigned>(std::min<long long>((most + kWidenThreads - 1) / kWidenThreads, 1216)), 1 + mats);
+        if (aligned)
+            widen_kernel<true><<<grid, kWidenThreads, 0, st>>>(offsets, S, N, K, Kp, Q, ldq, W, ldw, stride_w, Q16, W16, same_w);
+        else
+            widen_kernel<false><<<grid, kWidenThreads, 0, st>>>(offsets, S, N, K, Kp, Q, ldq, W, ldw, stride_w, Q16, W16, same_w);
+        spx_note_launches(1);
+    }
+    return tc_product_i8(E, S, N, K, offsets, Q16, Kp, row_scale, W16, Kp, mats, w_scale, C, ldc, c_type, st);
 }
 
 }  // extern "C"

@@ -900,7 +900,9 @@ spx_status spx_quant_rows_i8(int32_t M, int32_t K, spx_type type, const void* X,
  * once; zeros in the rows from offsets[E] on.  Q is S x K (ldq), W_e starts
  * at W + e * stride_w, N rows of K, ldw apart.
  *   scratch: spx_gemm_i8_scratch_bytes(E, S, N, K) bytes, 256-byte aligned
- *     (may be NULL when that is 0).
+ *     (may be NULL when that is 0): the codes as 16-bit floats, which hold them
+ *     exactly.  S <= 8 with rows on 16-byte boundaries runs without it.
+ * K == 0 gives zeros.  Launches: 1 or 2.
  */
 #define SPX_I8_MAX_K 131071
 size_t spx_gemm_i8_scratch_bytes(int32_t E, int32_t S, int32_t N, int32_t K);
