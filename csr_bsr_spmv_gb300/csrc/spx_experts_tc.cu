@@ -34,13 +34,11 @@ namespace {
 
 enum Mode : int { kNK = 0, kKN = 1, kWG = 2 };
 
-// Warps: 4 that store (8 for 8-bit integers, each with half of the tile's
-// rows), one for the lane factor's copies, one for the MMAs, one for the
-// column factor's copies.
-template <bool I8>
-constexpr int kStoreWarps = I8 ? 8 : 4;
-template <bool I8>
-constexpr int kThreads = 32 * (kStoreWarps<I8> + 3);
+// Warps: 8 that store (two for each quarter of the lanes, taking turns at the
+// tile's rows), one for the lane factor's copies, one for the MMAs, one for
+// the column factor's copies.
+constexpr int kStoreWarps = 8;
+constexpr int kThreads = 32 * (kStoreWarps + 3);
 constexpr int kDepth = 64;                      // reduction length of a stage: one 128-byte swizzle row
 constexpr uint32_t kLaneBytes = 128 * kDepth * 2;  // a stage's lane factor: 128 lanes a CTA, 16 KB
 constexpr uint32_t kBox = 64 * kDepth * 2;      // an MN-major box: 64 long, 64 deep, 8 KB
@@ -53,10 +51,24 @@ constexpr int kBand = 8;                        // row tiles that run side by si
 constexpr size_t kSmemMax = 224 * 1024;         // dynamic shared memory of a CTA
 constexpr long long kSpinLimit = 2000000000LL;  // cycles (~1 s): only a broken pipeline reaches it
 
-enum : int { kErrFull = 1, kErrEmpty = 2, kErrAcc = 3, kErrDrain = 4, kErrTmemFree = 5 };
+enum : int { kErrFull = 1, kErrEmpty = 2, kErrAcc = 3, kErrDrain = 4 };
 
 __device__ int g_experts_error;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_experts_error, 0, code); }
+
+// Division of 0 <= n < 2^31 by a number known at the launch: a multiply, an
+// add and a shift (m = 2^32 (2^s - d) / d + 1 rounded down, s = ceil(log2 d)).
+struct Divisor {
+    uint32_t d = 1, m = 1, s = 0;
+    Divisor() = default;
+    explicit Divisor(uint32_t v) : d(v) {
+        while ((1ull << s) < v) ++s;
+        m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - v)) / v + 1);
+    }
+    __device__ __forceinline__ int of(int n) const {
+        return static_cast<int>((__umulhi(static_cast<uint32_t>(n), m) + static_cast<uint32_t>(n)) >> s);
+    }
+};
 
 struct TcArgs {
     const int* offsets;
@@ -64,11 +76,12 @@ struct TcArgs {
     int NL;           // output columns: the lanes' axis
     int NC;           // kWG: output rows
     int NR;           // kNK, kKN: reduction length
-    int TN;           // output rows a tile: 32 to 256, a power of two
-    int max_tiles;    // kNK, kKN: more than any sound offsets give
+    int TN, log_tn;   // output rows a tile: 32 to 256, a power of two
+    int max_tiles;    // kWG: the tiles; else no fewer than sound offsets give
     int stages;
     uint32_t stage_bytes, idesc;
     int same_w;       // 1: every expert reads W_0
+    Divisor by_lane, by_group;  // lane tiles; kNK, kKN: tiles of a full band, kWG: tiles of an expert
     void* C;
     long long ldc, ce;
     spx_type c_type;
@@ -83,46 +96,45 @@ struct Item {
     int red0, red;    // reduction range [red0, red0 + red): k, or the expert's rows
 };
 
-// Tile t of the list.  kNK, kKN: `first` holds each expert's first tile, then
-// the first tile of the rows past the last expert's, then the count; an
-// expert's tiles go in bands of kBand row tiles, lane tiles within a band, row
-// tiles fastest, so that tiles that run together share both factors in L2.
+// The tile list in shared memory, E + 1 entries each: an expert's first row and
+// the row after its last, and (kNK, kKN) its first tile; the last entry stands
+// for the rows past the last expert's, and one more first tile is the count.
+struct List {
+    int *lo, *hi, *first;
+};
+inline size_t list_bytes(int E) { return sizeof(int) * (3 * static_cast<size_t>(E) + 4); }
+
+// Tile t of the list.  kNK, kKN: an expert's tiles go in bands of kBand row
+// tiles, lane tiles within a band, row tiles fastest, so that tiles that run
+// together share both factors in L2.  No division and no global read: the
+// thread that issues the MMAs does this between tiles.
 template <int MODE, int CG>
-__device__ __forceinline__ Item tile_item(const TcArgs& a, const int* first, int t) {
+__device__ __forceinline__ Item tile_item(const TcArgs& a, const List& list, int t) {
     Item it;
-    const int nlt = (a.NL + 128 * CG - 1) / (128 * CG);
     if (MODE == kWG) {
-        const int nct = (a.NC + a.TN - 1) / a.TN, per = nlt * nct;
-        it.e = t / per;
-        const int in = t % per;
-        it.lane0 = (in % nlt) * 128 * CG;
-        it.row0 = (in / nlt) * a.TN;
+        it.e = a.by_group.of(t);
+        const int in = t - it.e * static_cast<int>(a.by_group.d), c = a.by_lane.of(in);
+        it.lane0 = (in - c * static_cast<int>(a.by_lane.d)) * 128 * CG;
+        it.row0 = c * a.TN;
         it.rows = min(a.TN, a.NC - it.row0);
-        int hi;
-        expert_rows(a.offsets, it.e, a.S, it.red0, hi);
-        it.red = hi - it.red0;
+        it.red0 = list.lo[it.e];
+        it.red = list.hi[it.e] - it.red0;
         return it;
     }
     int lo = 0, up = a.E;  // the last expert whose first tile is <= t
     while (lo < up) {
         const int mid = (lo + up + 1) >> 1;
-        if (first[mid] <= t) lo = mid;
+        if (list.first[mid] <= t) lo = mid;
         else up = mid - 1;
     }
-    int r0 = 0, r1 = a.S;
-    if (a.offsets) {
-        if (lo < a.E) {
-            expert_rows(a.offsets, lo, a.S, r0, r1);
-        } else {
-            r0 = min(max(__ldg(a.offsets + a.E), 0), a.S);
-        }
-    }
-    const int in = t - first[lo], mt = (r1 - r0 + a.TN - 1) / a.TN;
-    const int band = in / (kBand * nlt), inb = in - band * kBand * nlt;
+    const int r0 = list.lo[lo], r1 = list.hi[lo];
+    const int in = t - list.first[lo], mt = (r1 - r0 + a.TN - 1) >> a.log_tn;
+    const int band = a.by_group.of(in), inb = in - band * static_cast<int>(a.by_group.d);
     const int high = min(kBand, mt - band * kBand);
+    const int nt = high == kBand ? inb / kBand : inb / high;
     it.e = lo;
-    it.lane0 = (inb / high) * 128 * CG;
-    it.row0 = r0 + (band * kBand + inb % high) * a.TN;
+    it.lane0 = nt * 128 * CG;
+    it.row0 = r0 + (band * kBand + inb - nt * high) * a.TN;
     it.rows = min(a.TN, r1 - it.row0);
     it.red0 = 0;
     it.red = lo < a.E ? a.NR : 0;  // the rows past the last expert's: zeros
@@ -187,10 +199,13 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t adesc, uint64_t bdesc, 
             : "memory");
 }
 
-// The ring position of a role: stage and phase, stepped without a division
-// (the roles are single threads whose instructions follow one another; with
-// the stage from a remainder, each stage cost them about 1000 cycles, twice
-// its MMAs).
+// The ring position of a role: stage and phase, stepped without a division.
+// The warps that issue copies and MMAs run their loops with all lanes and
+// elect one for the instruction itself: what they compute then stays in
+// uniform registers, where those instructions take their operands from.  (A
+// stage's MMAs take 512 cycles on a whole tile.  With the ring's stage from a
+// remainder a stage cost the issuing thread about 1000 cycles, with a single
+// lane's loop about 650.)
 struct Ring {
     uint32_t n, s = 0, ph = 0;
     __device__ __forceinline__ explicit Ring(uint32_t stages) : n(stages) {}
@@ -237,6 +252,23 @@ __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity) {
         if (t0 == 0) t0 = clock64();
         else if (clock64() - t0 > kSpinLimit) return false;
     }
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Bounded wait by a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kSpinLimit));
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -331,7 +363,7 @@ __device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, lon
 }
 
 template <int MODE, int CG, bool I8>
-__global__ void __launch_bounds__(kThreads<I8>, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tm_lane, const __grid_constant__ CUtensorMap tm_col,
                       const __grid_constant__ TcArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -354,12 +386,15 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
     auto clear_bar = [&](uint32_t s) { return bars + 8u * (3 * kMaxStages + 5 + s); };
     const uint32_t NS = a.stages;
     // the storing warps' patches, then the tile list, behind the ring
-    int* first = reinterpret_cast<int*>(smem_raw + (base - smem_u32(smem_raw)) + NS * a.stage_bytes +
-                                        kStoreWarps<I8> * kPatchBytes);
+    List list;
+    list.lo = reinterpret_cast<int*>(smem_raw + (base - smem_u32(smem_raw)) + NS * a.stage_bytes +
+                                     kStoreWarps * kPatchBytes);
+    list.hi = list.lo + a.E + 1;
+    list.first = list.hi + a.E + 1;
 
-    constexpr int SW = kStoreWarps<I8>, LOAD = SW, MMA = SW + 1, LOAD2 = SW + 2;  // the roles' warps
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t rank = 0;
+    constexpr int SW = kStoreWarps, LOAD = SW, MMA = SW + 1, LOAD2 = SW + 2;  // the roles' warps
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    int rank = 0;
     if (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const int G = static_cast<int>(gridDim.x) / CG, me = static_cast<int>(blockIdx.x) / CG;
     const uint32_t tmem_cols = 2u * a.TN;  // two accumulators
@@ -397,95 +432,97 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         }
     }
-    int ntiles = 0;
-    if (MODE == kWG) {
-        ntiles = a.E * ((a.NL + 128 * CG - 1) / (128 * CG)) * ((a.NC + a.TN - 1) / a.TN);
-    } else {
-        const int nlt = (a.NL + 128 * CG - 1) / (128 * CG);
-        for (int e = threadIdx.x; e <= a.E; e += kThreads<I8>) {
-            int lo = 0, hi = a.S;
-            if (a.offsets) {
-                if (e < a.E) expert_rows(a.offsets, e, a.S, lo, hi);
-                else lo = min(max(__ldg(a.offsets + a.E), 0), a.S);
-            } else if (e == a.E) {
-                lo = hi;
-            }
-            first[e] = (hi - lo + a.TN - 1) / a.TN * nlt;
+    int ntiles = a.max_tiles;  // kWG: every expert's tiles, rows or not
+    for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+        int lo = 0, hi = a.S;
+        if (a.offsets) {
+            if (e < a.E) expert_rows(a.offsets, e, a.S, lo, hi);
+            else lo = min(max(__ldg(a.offsets + a.E), 0), a.S);
+        } else if (e == a.E) {
+            lo = hi;
         }
+        list.lo[e] = lo;
+        list.hi[e] = hi;
+    }
+    if (MODE != kWG) {
         __syncthreads();
         if (warp == 0) {
             long long carry = 0;
             for (int e0 = 0; e0 <= a.E; e0 += 32) {
-                const int n = e0 + lane <= a.E ? first[e0 + lane] : 0;
+                const int e = e0 + lane;
+                const long long n = e <= a.E ? ((list.hi[e] - list.lo[e] + a.TN - 1) >> a.log_tn) * static_cast<long long>(a.by_lane.d) : 0;
                 long long inc = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const long long up = __shfl_up_sync(0xffffffffu, inc, d);
                     if (lane >= d) inc += up;
                 }
-                if (e0 + lane <= a.E) first[e0 + lane] = static_cast<int>(carry + inc - n);
+                if (e <= a.E) list.first[e] = static_cast<int>(carry + inc - n);
                 carry += __shfl_sync(0xffffffffu, inc, 31);
             }
             // offsets out of order can overlap and give more tiles than rows: then none is run
-            if (lane == 0) first[a.E + 1] = carry <= a.max_tiles ? static_cast<int>(carry) : 0;
+            if (lane == 0) list.first[a.E + 1] = carry <= a.max_tiles ? static_cast<int>(carry) : 0;
         }
     }
     tc_fence_before();
     if (CG == 2) cluster_sync();
     else __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = uniform(s_tmem);
     const uint32_t full0 = leader_addr<CG>(full_bar(0));
-    if (MODE != kWG) ntiles = first[a.E + 1];
+    if (MODE != kWG) ntiles = uniform(list.first[a.E + 1]);
     const uint32_t buf_cols = tmem_cols / 2;
 
     if (warp == LOAD || warp == LOAD2) {
         // ---------------- producers: this CTA's part of every stage, one thread for each factor (a thread takes
         // about 250 cycles from one copy to the next, so one alone would hold up the MMAs)
         const bool lanes = warp == LOAD;
-        if (lane == 0) {
-            Ring ring(NS);
-            uint32_t issued = 0, tails = 0;
-            bool stop = false;
-            for (int t = me; t < ntiles && !stop; t += G) {
-                const Item it = tile_item<MODE, CG>(a, first, t);
-                const int ncols = mma_cols<CG>(it.rows);  // a pair's CTA holds half of them
-                const int lane0 = it.lane0 + 128 * static_cast<int>(rank);
-                const int col0 = it.row0 + static_cast<int>(rank) * (MODE == kWG ? a.TN : ncols) / 2;
-                const int z = a.same_w ? 0 : it.e, end = it.red0 + it.red;
-                for (int r = it.red0; r < end; r += kDepth, ring.next(), ++issued) {
-                    const uint32_t s8 = 8u * ring.s, sl = base + ring.s * a.stage_bytes, sc = sl + kLaneBytes;
-                    if (!mbar_wait(empty_bar(0) + s8, ring.ph ^ 1u, kSpinLimit) || s_abort) {
-                        record_error(kErrEmpty);
-                        s_abort = 1;
-                        stop = true;
-                        break;
-                    }
-                    uint32_t bar = full0 + s8;
-                    if (MODE == kWG && end - r < kDepth && (end - r) % 16) {
-                        if (lanes && rank == 0) mbar_arrive(full_bar(0) + s8);
-                        if (lanes) mbar_expect_tx(tail_bar(ring.s), a.stage_bytes);
-                        bar = tail_bar(ring.s);
-                        tails ^= 1u << ring.s;
-                    } else if (lanes && rank == 0) {
+        Ring ring(NS);
+        uint32_t issued = 0, tails = 0;
+        bool ok = true;
+        for (int t = me; t < ntiles && ok; t += G) {
+            const Item it = tile_item<MODE, CG>(a, list, t);
+            const int cols = MODE == kWG ? a.TN : mma_cols<CG>(it.rows);  // a pair's CTA holds half of them
+            const int lane0 = uniform(it.lane0) + 128 * rank, col0 = uniform(it.row0 + rank * cols / 2);
+            const int z = a.same_w ? 0 : uniform(it.e), r0 = uniform(it.red0), end = r0 + uniform(it.red);
+            for (int r = r0; r < end; r += kDepth, ring.next(), ++issued) {
+                const uint32_t s8 = 8u * ring.s, sl = base + ring.s * a.stage_bytes, sc = sl + kLaneBytes;
+                ok = warp_wait(empty_bar(0) + s8, ring.ph ^ 1u) && !s_abort;
+                if (!ok) break;
+                uint32_t bar = full0 + s8;
+                const bool ragged = MODE == kWG && end - r < kDepth && (end - r) % 16;
+                if (ragged) {
+                    bar = tail_bar(ring.s);
+                    tails ^= 1u << ring.s;
+                }
+                if (!elect()) continue;
+                if (lanes) {
+                    if (ragged) {
+                        if (rank == 0) mbar_arrive(full_bar(0) + s8);
+                        mbar_expect_tx(bar, a.stage_bytes);
+                    } else if (rank == 0) {
                         mbar_expect_tx(full_bar(0) + s8, CG * a.stage_bytes);
                     }
-                    if (lanes) {
-                        if (MODE == kNK) {
-                            load_3d<CG>(sl, &tm_lane, r, lane0, z, bar);
-                        } else if (MODE == kKN) {
-                            load_3d<CG>(sl, &tm_lane, lane0, r, z, bar);
-                            load_3d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, z, bar);
-                        } else {
-                            load_2d<CG>(sl, &tm_lane, lane0, r, bar);
-                            load_2d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, bar);
-                        }
-                    } else if (MODE == kWG) {
-                        for (int c = 0; c < a.TN / CG; c += 64) load_2d<CG>(sc + c / 64 * kBox, &tm_col, col0 + c, r, bar);
+                    if (MODE == kNK) {
+                        load_3d<CG>(sl, &tm_lane, r, lane0, z, bar);
+                    } else if (MODE == kKN) {
+                        load_3d<CG>(sl, &tm_lane, lane0, r, z, bar);
+                        load_3d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, z, bar);
                     } else {
-                        load_2d<CG>(sc, &tm_col, r, col0, bar);
+                        load_2d<CG>(sl, &tm_lane, lane0, r, bar);
+                        load_2d<CG>(sl + kBox, &tm_lane, lane0 + 64, r, bar);
                     }
+                } else if (MODE == kWG) {
+                    for (int c = 0; c < a.TN / CG; c += 64) load_2d<CG>(sc + c / 64 * kBox, &tm_col, col0 + c, r, bar);
+                } else {
+                    load_2d<CG>(sc, &tm_col, r, col0, bar);
                 }
+            }
+        }
+        if (lane == 0) {
+            if (!ok) {
+                record_error(kErrEmpty);
+                s_abort = 1;
             }
             (lanes ? s_issued : s_issued_col) = issued;
             if (lanes) s_tails_in = tails;
@@ -496,12 +533,7 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
         // The rows of the next expert inside the last step of 16 of ring stage s: zeros in both factors.  Both are
         // cleared because a NaN or infinity there would survive a product with zero.
         auto clear_tail = [&](uint32_t s, int tail) {
-            int got = 1;
-            if (lane == 0) got = mbar_wait(tail_bar(s), (tails >> s) & 1u, kSpinLimit);
-            if (!__shfl_sync(0xffffffffu, got, 0)) {
-                if (lane == 0) record_error(kErrFull);
-                return false;
-            }
+            if (!warp_wait(tail_bar(s), (tails >> s) & 1u)) return false;
             tails ^= 1u << s;
             const uint32_t sl = base + s * a.stage_bytes;
             const int bad = (-tail) & 15, boxes = 2 + a.TN / CG / 64;
@@ -529,74 +561,64 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
             int buf = 0;
             bool ok = true;
             for (int t = me; t < ntiles && ok; t += G) {
-                const Item it = tile_item<MODE, CG>(a, first, t);
-                const uint32_t ncols = MODE == kWG ? a.TN : mma_cols<CG>(it.rows);
-                const uint32_t idesc = a.idesc | ((ncols >> 3) << 17);
-                int left = it.red;
+                const Item it = tile_item<MODE, CG>(a, list, t);
+                const uint32_t idesc = a.idesc | (uniform(MODE == kWG ? a.TN : mma_cols<CG>(it.rows)) >> 3 << 17);
+                int left = uniform(it.red);
                 do {  // one accumulator's worth: the whole reduction, or kExact terms of it
-                const int now = I8 ? min(left, kExact) : left;
-                left -= now;
-                const int whole = now / kDepth, tail = now % kDepth;
-                uint32_t acc = 0;
-                if (lane == 0) {
-                    ok = pair_wait<CG>(tempty_bar(buf), tph) && !s_abort;
-                    if (!ok) record_error(kErrTmemFree);
+                    const int now = I8 ? min(left, kExact) : left;
+                    left -= now;
+                    ok = warp_wait(tempty_bar(buf), tph) && !s_abort;
+                    if (!ok) break;
                     tc_fence_after();
-                    for (int b = 0; ok && b < whole; ++b, ring.next(), ++consumed) {
-                        const uint32_t s8 = 8u * ring.s;
-                        if (!pair_wait<CG>(full_bar(0) + s8, ring.ph)) {
-                            record_error(kErrFull);
-                            ok = false;
-                            break;
+                    uint32_t acc = 0;
+                    for (int k = now; k > 0; k -= kDepth) {
+                        if (MODE == kWG && k < kDepth && (k & 15)) {
+                            ok = clear_tail(ring.s, k) &&
+                                 __all_sync(0xffffffffu, pair_wait<CG>(clear_bar(ring.s), ((tails >> ring.s) & 1u) ^ 1u));
+                            if (!ok) break;
                         }
+                        ok = warp_wait(full_bar(0) + 8u * ring.s, ring.ph);
+                        if (!ok) break;
                         tc_fence_after();
                         const uint64_t ad = ad0 + ring.s * stage_step, bd = bd0 + ring.s * stage_step;
-                        mma<CG>(d, ad, bd, idesc, acc);
-                        acc = 1;
+                        if (elect()) {
+                            mma<CG>(d, ad, bd, idesc, acc);
+                            if (k > kDepth - 16) {
 #pragma unroll
-                        for (uint32_t ks = 1; ks < kDepth / 16; ++ks)
-                            mma<CG>(d, ad + ks * a_step, bd + ks * b_step, idesc, 1u);
-                        commit<CG>(empty_bar(0) + s8);
-                    }
-                }
-                if (MODE == kWG) ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (MODE == kWG && ok && (tail & 15)) {
-                    ring.s = __shfl_sync(0xffffffffu, ring.s, 0);
-                    ok = clear_tail(ring.s, tail);
-                }
-                if (tail && lane == 0 && ok) {  // the reduction's last, short stage
-                    const uint32_t s8 = 8u * ring.s;
-                    ok = pair_wait<CG>(full_bar(0) + s8, ring.ph);
-                    if (MODE == kWG && ok && (tail & 15)) ok = pair_wait<CG>(clear_bar(ring.s), ((tails >> ring.s) & 1u) ^ 1u);
-                    if (!ok) record_error(kErrFull);
-                    tc_fence_after();
-                    if (ok) {
-                        const uint64_t ad = ad0 + ring.s * stage_step, bd = bd0 + ring.s * stage_step;
-                        for (int ks = 0; ks < (tail + 15) >> 4; ++ks, acc = 1)
-                            mma<CG>(d, ad + static_cast<uint32_t>(ks) * a_step, bd + static_cast<uint32_t>(ks) * b_step,
-                                    idesc, acc);
-                        commit<CG>(empty_bar(0) + s8);
+                                for (uint32_t ks = 1; ks < kDepth / 16; ++ks)
+                                    mma<CG>(d, ad + ks * a_step, bd + ks * b_step, idesc, 1u);
+                            } else {  // the reduction's last stage: the steps that hold something
+                                for (uint32_t ks = 1; 16 * static_cast<int>(ks) < k; ++ks)
+                                    mma<CG>(d, ad + ks * a_step, bd + ks * b_step, idesc, 1u);
+                            }
+                            commit<CG>(empty_bar(0) + 8u * ring.s);
+                        }
+                        acc = 1;
                         ring.next();
                         ++consumed;
                     }
-                }
-                if (lane == 0 && ok) commit<CG>(tfull_bar(buf));
-                if (lane == 0 && !ok) s_abort = 1;
-                buf ^= 1;
-                d = tmem + buf * buf_cols;
-                if (buf == 0) tph ^= 1u;
-                __syncwarp();
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                } while (I8 && left > 0 && ok);
+                    if (!ok) break;
+                    if (elect()) commit<CG>(tfull_bar(buf));
+                    buf ^= 1;
+                    d = tmem + buf * buf_cols;
+                    if (buf == 0) tph ^= 1u;
+                } while (I8 && left > 0);
+            }
+            if (!ok && lane == 0) {
+                record_error(kErrFull);
+                s_abort = 1;
             }
             if (lane == 0) s_consumed = consumed;
         } else if (MODE == kWG) {
             // the pair's second CTA: only its part of clearing the tails
             uint32_t at = 0;
             for (int t = me; t < ntiles && !s_abort; t += G) {
-                const int red = tile_item<MODE, CG>(a, first, t).red;
+                const int red = tile_item<MODE, CG>(a, list, t).red;
                 if ((red & 15) && !clear_tail((at + red / kDepth) % NS, red % kDepth)) {
-                    if (lane == 0) s_abort = 1;
+                    if (lane == 0) {
+                        record_error(kErrFull);
+                        s_abort = 1;
+                    }
                     break;
                 }
                 at = (at + (red + kDepth - 1) / kDepth) % NS;
@@ -608,15 +630,13 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
         int buf = 0;
         uint32_t tph = 0;
         auto acc_wait = [&]() {
-            int ok = 1;
-            if (lane == 0) ok = (mbar_wait(tfull_bar(buf), tph, kSpinLimit) && !s_abort) ? 1 : 0;
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            const bool ok = warp_wait(tfull_bar(buf), tph) && !s_abort;
             if (!ok && lane == 0) {
                 record_error(kErrAcc);
                 s_abort = 1;
             }
             tc_fence_after();
-            return ok != 0;
+            return ok;
         };
         auto acc_free = [&]() {
             tc_fence_before();
@@ -624,7 +644,9 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
             if (lane == 0) {
                 if (CG == 1) mbar_arrive(tempty_bar(buf));
                 else
-                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                    // relaxed: a release would wait for this warp's stores to the output (1200 cycles and more);
+                    // all that has to come before it are the accumulator's loads, which are complete
+                    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                                      leader_addr<CG>(tempty_bar(buf)))
                                  : "memory");
             }
@@ -634,14 +656,15 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
         const uint32_t patch = base + NS * a.stage_bytes + warp * kPatchBytes;
         const uint32_t quarter = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         for (int t = me; t < ntiles; t += G) {
-            const Item it = tile_item<MODE, CG>(a, first, t);
-            const int x = it.lane0 + 128 * static_cast<int>(rank) + 32 * (warp & 3);
+            const Item it = tile_item<MODE, CG>(a, list, t);
+            const int x = it.lane0 + 128 * rank + 32 * (warp & 3);
             const long long off = MODE == kWG ? it.e * a.ce : 0;
             if (!I8) {
                 if (!acc_wait()) break;
                 const uint32_t src = tmem + buf * buf_cols + quarter;
+                bool held = true;
 #pragma unroll 1
-                for (int c0 = 0; c0 < it.rows; c0 += 32) {
+                for (int c0 = 32 * (warp >> 2); c0 < it.rows; c0 += 64) {
                     uint32_t v[32];
                     if (it.red > 0) {
                         load_frag(src + c0, v);
@@ -650,16 +673,20 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0u;
                     }
+                    if (c0 + 64 >= it.rows) {  // this warp's last look at the accumulator
+                        acc_free();
+                        held = false;
+                    }
                     float f[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
                     store_chunk(a, it, off, x, lane, patch, c0, f);
                 }
-                acc_free();
+                if (held) acc_free();
                 continue;
             }
             // 8-bit integers: the exact partial sums are added in int32, scaled at the end
-            const int half = warp >> 2;  // this warp's rows: [128 half, 128 half + 128) of the tile
+            const int half = warp >> 2;  // this warp's rows: every other 32 of the tile
             int sum[4][32];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -675,7 +702,7 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
                 if (it.red > 0) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int c0 = 128 * half + 32 * q;
+                        const int c0 = 64 * q + 32 * half;
                         if (c0 >= it.rows) break;
                         uint32_t v[32];
                         load_frag(src + c0, v);
@@ -695,7 +722,7 @@ __global__ void __launch_bounds__(kThreads<I8>, 1)
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int c0 = 128 * half + 32 * q;
+                const int c0 = 64 * q + 32 * half;
                 if (c0 >= it.rows) break;
                 float f[32];
 #pragma unroll
@@ -801,12 +828,14 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     const int sms = sm_count();
     if (sms <= 0) return SPX_ERR_CUDA;
     a.wide_c = spx_aligned(a.C, 16) && a.ldc % 8 == 0 && a.ce % 8 == 0 && a.NL % 8 == 0;
-    const size_t list = kStoreWarps<I8> * kPatchBytes + sizeof(int) * (static_cast<size_t>(a.E) + 2);
+    a.log_tn = 0;
+    while ((1 << a.log_tn) < a.TN) ++a.log_tn;
+    const size_t list = kStoreWarps * kPatchBytes + list_bytes(a.E);
     a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemMax - 1024 - list) / a.stage_bytes));
     const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + list;
     if (set_smem_limit(experts_tc_kernel<MODE, CG, I8>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads<I8>);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -872,6 +901,8 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
     const long long nlt = (N + 128 * cg - 1) / (128 * cg), tiles = max_row_tiles(E, S, a.TN) * nlt;
     if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;  // the list's walk steps past its end by a grid
     a.max_tiles = static_cast<int>(tiles);
+    a.by_lane = Divisor(static_cast<uint32_t>(nlt));
+    a.by_group = Divisor(static_cast<uint32_t>(kBand * nlt));
     if (cg == 2) return nk ? launch<kNK, 2>(tl, tc, a, tiles, st) : launch<kKN, 2>(tl, tc, a, tiles, st);
     return nk ? launch<kNK, 1>(tl, tc, a, tiles, st) : launch<kKN, 1>(tl, tc, a, tiles, st);
 }
@@ -896,6 +927,8 @@ spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const v
     const long long nlt = (N + 128 * cg - 1) / (128 * cg), tiles = max_row_tiles(E, S, a.TN) * nlt;
     if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;
     a.max_tiles = static_cast<int>(tiles);
+    a.by_lane = Divisor(static_cast<uint32_t>(nlt));
+    a.by_group = Divisor(static_cast<uint32_t>(kBand * nlt));
     return cg == 2 ? launch<kNK, 2, true>(tl, tc, a, tiles, st) : launch<kNK, 1, true>(tl, tc, a, tiles, st);
 }
 
@@ -916,8 +949,11 @@ spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* 
     CUtensorMap tl, tc;
     if (!make_map3(&tl, A, type, K, S, lda, 0, 0, 64) || !make_map3(&tc, G, type, N, S, ldg, 0, 0, 64))
         return SPX_ERR_CUDA;
-    const long long tiles = static_cast<long long>(E) * ((K + 128 * cg - 1) / (128 * cg)) * ((N + a.TN - 1) / a.TN);
+    const long long nlt = (K + 128 * cg - 1) / (128 * cg), per = nlt * ((N + a.TN - 1) / a.TN), tiles = E * per;
     if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;
+    a.max_tiles = static_cast<int>(tiles);
+    a.by_lane = Divisor(static_cast<uint32_t>(nlt));
+    a.by_group = Divisor(static_cast<uint32_t>(per));
     return cg == 2 ? launch<kWG, 2>(tl, tc, a, tiles, st) : launch<kWG, 1>(tl, tc, a, tiles, st);
 }
 
