@@ -23,6 +23,7 @@
 // (read by spx_last_device_error), stops, waits (bounded) for its copies and
 // MMAs in flight, frees its TMEM and exits.
 #include <algorithm>
+#include <tuple>
 
 #include "spx_experts.cuh"
 #include "spx_tc.cuh"
@@ -79,12 +80,14 @@ struct TcArgs {
     int TN, log_tn;   // output rows a tile: 32 to 256, a power of two
     int max_tiles;    // kWG: the tiles; else no fewer than sound offsets give
     int stages;
-    uint32_t stage_bytes, idesc;
+    uint32_t stage_bytes, idesc, part_off;  // part_off: the shared partial tile, behind the tile list
+    int split, split_red;  // CTAs that share a tile's reduction, and the length of a share (a multiple of kDepth)
     int same_w;       // 1: every expert reads W_0
     Divisor by_lane, by_group;  // lane tiles; kNK, kKN: tiles of a full band, kWG: tiles of an expert
     void* C;
     long long ldc, ce;
     spx_type c_type;
+    bool wide_f;      // fp32 output with rows on 16-byte boundaries, NL a multiple of 4
     bool wide_c;      // 16-bit output with rows on 16-byte boundaries, NL a multiple of 8
     const float *row_scale, *col_scale;  // 8-bit integers: [S], [E * NL]
 };
@@ -354,6 +357,25 @@ __device__ __forceinline__ void store_rows(const TcArgs& a, const Item& it, O* C
     }
 }
 
+// Pitch of a shared partial tile: a row of 128 sums and four words of slack,
+// so that a fragment's stores touch every bank once.
+constexpr uint32_t kPartPitch = 132 * 4;
+
+// Four sums of this lane's columns of one output row (shared reductions).
+template <class O>
+__device__ __forceinline__ void store_four(const TcArgs& a, long long row, int x, const float (&f)[4]) {
+    O* q = static_cast<O*>(a.C) + row * a.ldc + x;
+    if (a.wide_c || (sizeof(O) == 4 && a.wide_f)) {
+        if (x + 4 > a.NL) return;
+        if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(q) = make_uint2(pack<O>(f[0], f[1]), pack<O>(f[2], f[3]));
+        else *reinterpret_cast<float4*>(q) = make_float4(f[0], f[1], f[2], f[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (x + i < a.NL) q[i] = from_f<O>(f[i]);
+}
+
 __device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, long long off, int x, int lane,
                                             uint32_t patch, int c0, const float (&v)[32]) {
     if (a.c_type == SPX_F32) store_rows(a, it, static_cast<float*>(a.C) + off, x, lane, false, patch, c0, v);
@@ -362,7 +384,10 @@ __device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, lon
     else store_rows(a, it, static_cast<__half*>(a.C) + off, x, lane, a.wide_c, patch, c0, v);
 }
 
-template <int MODE, int CG, bool I8>
+// SPLIT: a cluster of a.split CTAs shares each tile, every one the products of
+// its part of the reduction; the partial tiles meet in shared memory, where
+// CTA r adds the parts of its share of the rows in rank order.
+template <int MODE, int CG, bool I8, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tm_lane, const __grid_constant__ CUtensorMap tm_col,
                       const __grid_constant__ TcArgs a) {
@@ -370,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_issued, s_issued_col, s_consumed, s_tails_in, s_tails_done;
-    __shared__ __align__(8) uint64_t s_bars[4 * kMaxStages + 5];
+    __shared__ __align__(8) uint64_t s_bars[4 * kMaxStages + 7];
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t bars = smem_u32(s_bars);
@@ -384,6 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // reductions can be in the ring at once, but a stage is not filled again before it was consumed.
     auto tail_bar = [&](uint32_t s) { return bars + 8u * (2 * kMaxStages + 5 + s); };
     auto clear_bar = [&](uint32_t s) { return bars + 8u * (3 * kMaxStages + 5 + s); };
+    // SPLIT: every part of a tile is in place; everybody has read this CTA's
+    const uint32_t ready_bar = bars + 8u * (4 * kMaxStages + 5), done_bar = bars + 8u * (4 * kMaxStages + 6);
     const uint32_t NS = a.stages;
     // the storing warps' patches, then the tile list, behind the ring
     List list;
@@ -394,9 +421,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     constexpr int SW = kStoreWarps, LOAD = SW, MMA = SW + 1, LOAD2 = SW + 2;  // the roles' warps
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    int rank = 0;
+    int rank = 0, part = 0;  // place in the pair, share of the reduction
     if (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    const int G = static_cast<int>(gridDim.x) / CG, me = static_cast<int>(blockIdx.x) / CG;
+    if (SPLIT) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(part));
+    const int team = SPLIT ? a.split : CG;
+    const int G = static_cast<int>(gridDim.x) / team, me = static_cast<int>(blockIdx.x) / team;
+    // this CTA's part of a tile's reduction
+    auto share = [&](Item it) {
+        if (SPLIT) {
+            it.red0 = part * a.split_red;
+            it.red = max(0, min(it.red - it.red0, a.split_red));
+        }
+        return it;
+    };
     const uint32_t tmem_cols = 2u * a.TN;  // two accumulators
 
     if (threadIdx.x == 0) {
@@ -409,6 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(tempty_bar(b), SW * CG);  // one arrive per storing warp of the pair
         }
         mbar_init(fin_bar, 1);
+        if (SPLIT) {
+            mbar_init(ready_bar, kStoreWarps * a.split);
+            mbar_init(done_bar, kStoreWarps * a.split);
+        }
         if (MODE == kWG)
             for (uint32_t s = 0; s < NS; ++s) {
                 mbar_init(tail_bar(s), 1);
@@ -465,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     tc_fence_before();
-    if (CG == 2) cluster_sync();
+    if (CG == 2 || SPLIT) cluster_sync();
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(s_tmem);
@@ -481,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t issued = 0, tails = 0;
         bool ok = true;
         for (int t = me; t < ntiles && ok; t += G) {
-            const Item it = tile_item<MODE, CG>(a, list, t);
+            const Item it = share(tile_item<MODE, CG>(a, list, t));
             const int cols = MODE == kWG ? a.TN : mma_cols<CG>(it.rows);  // a pair's CTA holds half of them
             const int lane0 = uniform(it.lane0) + 128 * rank, col0 = uniform(it.row0 + rank * cols / 2);
             const int z = a.same_w ? 0 : uniform(it.e), r0 = uniform(it.red0), end = r0 + uniform(it.red);
@@ -561,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int buf = 0;
             bool ok = true;
             for (int t = me; t < ntiles && ok; t += G) {
-                const Item it = tile_item<MODE, CG>(a, list, t);
+                const Item it = share(tile_item<MODE, CG>(a, list, t));
                 const uint32_t idesc = a.idesc | (uniform(MODE == kWG ? a.TN : mma_cols<CG>(it.rows)) >> 3 << 17);
                 int left = uniform(it.red);
                 do {  // one accumulator's worth: the whole reduction, or kExact terms of it
@@ -655,10 +696,107 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const uint32_t patch = base + NS * a.stage_bytes + warp * kPatchBytes;
         const uint32_t quarter = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        // A tile whose reduction the cluster shares: this CTA's sums to its shared partial tile, then its rows of all.
+        uint32_t pph = 0;  // tiles so far, mod 2
+        auto tell_all = [&](uint32_t bar) {
+            __syncwarp();
+            if (lane < a.split) {
+                uint32_t there;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(bar), "r"(lane));
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
+            }
+        };
+        auto meet = [&](uint32_t bar, uint32_t parity) {
+            const bool ok = __all_sync(0xffffffffu, pair_wait<2>(bar, parity)) && !s_abort;
+            if (!ok && lane == 0) {
+                record_error(kErrAcc);
+                s_abort = 1;
+            }
+            return ok;
+        };
+        auto shared_tile = [&](const Item& it) {
+            const Item mine = share(it);
+            const uint32_t part0 = base + NS * a.stage_bytes + kStoreWarps * kPatchBytes + a.part_off;
+            if (!meet(done_bar, pph ^ 1u)) return false;
+            int left = mine.red;
+            bool fresh = true;
+            do {
+                left -= I8 ? min(left, kExact) : left;
+                if (!acc_wait()) return false;
+                const uint32_t src = tmem + buf * buf_cols + quarter;
+#pragma unroll 1
+                for (int c0 = 32 * (warp >> 2); c0 < it.rows; c0 += 64) {
+                    uint32_t v[32];
+                    if (mine.red > 0) {
+                        load_frag(src + c0, v);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int n = 32 * (warp & 3) + 16 * (i >> 4) + (lane >> 2) + 8 * ((i >> 1) & 1);
+                        const int r = c0 + 8 * ((i >> 2) & 3) + 2 * (lane & 3) + (i & 1);
+                        const uint32_t at = part0 + r * kPartPitch + 4 * n;
+                        uint32_t w = v[i];
+                        if (I8) {
+                            int whole = __float2int_rn(__uint_as_float(v[i]));
+                            if (!fresh) {
+                                int before;
+                                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(before) : "r"(at) : "memory");
+                                whole += before;
+                            }
+                            w = static_cast<uint32_t>(whole);
+                        }
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
+                    }
+                }
+                acc_free();
+                fresh = false;
+            } while (left > 0);
+            tell_all(ready_bar);
+            if (!meet(ready_bar, pph)) return false;
+            const int per = a.TN / a.split, col = it.lane0 + 4 * lane;
+            float cs[4] = {0.f, 0.f, 0.f, 0.f};
+            if (I8 && it.e < a.E)
+                for (int i = 0; i < 4; ++i)
+                    if (col + i < a.NL) cs[i] = __ldg(a.col_scale + static_cast<long long>(it.e) * a.NL + col + i);
+            for (int r = part * per + warp; r < min((part + 1) * per, it.rows); r += kStoreWarps) {
+                uint32_t v[4], sum[4] = {0u, 0u, 0u, 0u};
+                for (int p = 0; p < a.split; ++p) {
+                    uint32_t there;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(part0 + r * kPartPitch + 16 * lane), "r"(p));
+                    asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                 : "r"(there)
+                                 : "memory");
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sum[i] = I8 ? sum[i] + v[i] : __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
+                }
+                float f[4];
+                const float rs = I8 ? __ldg(a.row_scale + it.row0 + r) : 1.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[i] = !I8 ? __uint_as_float(sum[i])
+                               : it.e < a.E ? static_cast<float>(static_cast<int>(sum[i])) * (rs * cs[i]) : 0.f;
+                if (a.c_type == SPX_F32) store_four<float>(a, it.row0 + r, col, f);
+                else if (a.c_type == SPX_BF16) store_four<__nv_bfloat16>(a, it.row0 + r, col, f);
+                else store_four<__half>(a, it.row0 + r, col, f);
+            }
+            tell_all(done_bar);
+            pph ^= 1u;
+            return true;
+        };
         for (int t = me; t < ntiles; t += G) {
             const Item it = tile_item<MODE, CG>(a, list, t);
             const int x = it.lane0 + 128 * rank + 32 * (warp & 3);
             const long long off = MODE == kWG ? it.e * a.ce : 0;
+            if constexpr (SPLIT) {
+                if (!shared_tile(it)) break;
+                continue;
+            }
             if (!I8) {
                 if (!acc_wait()) break;
                 const uint32_t src = tmem + buf * buf_cols + quarter;
@@ -741,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     tc_fence_before();
-    if (CG == 2) cluster_sync();  // the peer's waits are over too
+    if (CG == 2 || SPLIT) cluster_sync();  // the peer's waits are over too
     else __syncthreads();
     if (MODE == kWG && s_abort && warp == LOAD && lane == 0)
         for (uint32_t s = 0; s < NS; ++s)
@@ -763,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
-    if (CG == 2) cluster_sync();
+    if (CG == 2 || SPLIT) cluster_sync();
     else __syncthreads();
     tc_fence_after();
     if (warp == MMA) {
@@ -804,14 +942,14 @@ int sm_count() {
     return cache[dev] = n;
 }
 
-// Clusters of `kernel` the device holds at once, asked once per (kernel, device).
-int resident_pairs(const void* kernel, const cudaLaunchConfig_t& cfg) {
+// Clusters of `team` CTAs of `kernel` the device holds at once, asked once per (kernel, size, device).
+int resident_teams(const void* kernel, int team, const cudaLaunchConfig_t& cfg) {
     static std::mutex mu;
-    static std::map<std::pair<const void*, int>, int> cache;
+    static std::map<std::tuple<const void*, int, int>, int> cache;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_pair(kernel, dev);
+    const auto key = std::make_tuple(kernel, team, dev);
     auto it = cache.find(key);
     if (it != cache.end()) return it->second;
     cudaLaunchConfig_t most = cfg;
@@ -821,38 +959,85 @@ int resident_pairs(const void* kernel, const cudaLaunchConfig_t& cfg) {
     return cache[key] = n;
 }
 
+// The tile (a.TN rows of 128 or, for a pair, 256 columns) and the CTAs that
+// share a tile's reduction (a.split, a.split_red), by the least modelled time;
+// returns the CTAs of a tile, 1 or 2.  Cycles of a 64-deep stage, measured on
+// products of 512 to 16384 rows: small tiles are bound by what issuing a stage
+// takes, single CTAs with large ones by the L2 reads of their factors, pairs
+// come near the tensor rate.  A tile's stores (12 cycles a row) run beside the
+// next tile's MMAs; rounds of tiles count whole.  Sharing a reduction costs
+// about 1500 cycles a CTA for the exchange.  512 rows x 4096 x 4096: 128-row
+// tiles 19 us, 256-row pairs 25, 64-row tiles 30; 16 rows: one CTA a tile 16.5
+// us, two 13.0, four 11.6, eight 16.1.  `mean` rows (kWG: terms) an expert.
+int choose_tile(TcArgs& a, bool wgrad, bool may_split) {
+    struct Shape {
+        int tn, cg, stage;
+    };
+    constexpr Shape shapes[] = {{256, 2, 615}, {256, 1, 725}, {128, 2, 435}, {128, 1, 460}, {64, 1, 390}, {32, 1, 350}};
+    const double mean = static_cast<double>(a.S) / a.E, used = std::min(a.E, a.S);
+    const int sms = sm_count();
+    double best = 0;
+    Shape pick = shapes[0];
+    a.split = 1;
+    for (const Shape& sh : shapes) {
+        if (wgrad && sh.tn < 128) continue;                    // boxes of 64 columns, two lanes a stage
+        if (sh.cg == 2 && a.NL <= 128) continue;
+        const int most = wgrad ? a.NC : a.S;
+        if (sh.tn > 64 && sh.tn / 2 >= most) continue;
+        const double lanes = (a.NL + 128 * sh.cg - 1) / (128 * sh.cg);
+        // row tiles: an expert's last one is half full on average, unless one holds all its rows
+        const double rows = wgrad      ? static_cast<double>(a.E) * ((a.NC + sh.tn - 1) / sh.tn)
+                            : a.E == 1 ? (a.S + sh.tn - 1) / sh.tn
+                                       : used * (2 * mean > sh.tn ? mean / sh.tn + 0.5 : 1.0);
+        const double tiles = rows * lanes, slots = sms / sh.cg;
+        const double stages = wgrad ? mean / kDepth + 0.5 : (a.NR + kDepth - 1) / kDepth;
+        for (int split = 1; split <= 8; split *= 2) {
+            if (split > 1 && (!may_split || sh.cg > 1 || sh.tn > 128 || tiles * split > slots)) break;
+            const double rounds = tiles * split <= slots ? 1 : tiles / slots < 4 ? static_cast<int>(tiles / slots + 0.99) : tiles / slots;
+            const double cycles = rounds * (std::max(stages / split * sh.stage, 12.0 * sh.tn) + 600) + (split > 1 ? 1500 * split : 0);
+            if (best == 0 || cycles < best) best = cycles, pick = sh, a.split = split;
+        }
+    }
+    a.TN = pick.tn;
+    a.split_red = ((a.NR + kDepth - 1) / kDepth + a.split - 1) / a.split * kDepth;
+    return pick.cg;
+}
+
 bool rows_aligned(const void* p, int64_t ld) { return spx_aligned(p, 16) && ld % 8 == 0; }
 
-template <int MODE, int CG, bool I8 = false>
+template <int MODE, int CG, bool I8 = false, bool SPLIT = false>
 spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long long max_tiles, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return SPX_ERR_CUDA;
     a.wide_c = spx_aligned(a.C, 16) && a.ldc % 8 == 0 && a.ce % 8 == 0 && a.NL % 8 == 0;
     a.log_tn = 0;
     while ((1 << a.log_tn) < a.TN) ++a.log_tn;
-    const size_t list = kStoreWarps * kPatchBytes + list_bytes(a.E);
+    a.wide_f = spx_aligned(a.C, 16) && a.ldc % 4 == 0 && a.NL % 4 == 0;
+    const int team = SPLIT ? a.split : CG;  // CTAs that work on one tile
+    a.part_off = static_cast<uint32_t>((list_bytes(a.E) + 15) / 16 * 16);
+    const size_t list = kStoreWarps * kPatchBytes + a.part_off + (SPLIT ? a.TN * kPartPitch : 0);
     a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemMax - 1024 - list) / a.stage_bytes));
     const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + list;
-    if (set_smem_limit(experts_tc_kernel<MODE, CG, I8>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
+    if (set_smem_limit(experts_tc_kernel<MODE, CG, I8, SPLIT>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.x = team;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 1 : 0;
-    // as many CTAs as run at once: one an SM; pairs only where a GPC has two SMs left for them
+    cfg.numAttrs = team > 1 ? 1 : 0;
+    // as many CTAs as run at once: one an SM; teams only where a GPC has the SMs left for them
     int groups = sms;
-    if (CG > 1) {
-        cfg.gridDim = dim3(sms / CG * CG);
-        groups = resident_pairs(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG, I8>), cfg);
+    if (team > 1) {
+        cfg.gridDim = dim3(sms / team * team);
+        groups = resident_teams(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG, I8, SPLIT>), team, cfg);
         if (groups <= 0) return SPX_ERR_CUDA;
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(max_tiles, groups)) * CG);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_tc_kernel<MODE, CG, I8>, tl, tc, a);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(max_tiles, groups)) * team);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_tc_kernel<MODE, CG, I8, SPLIT>, tl, tc, a);
     spx_note_launches(1);
     return spx_cuda_status(e != cudaSuccess ? e : cudaGetLastError());
 }
@@ -889,9 +1074,7 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
     a.offsets = offsets, a.E = E, a.S = S, a.NL = N, a.NR = K;
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.same_w = E == 1 || stride_w == 0;
-    a.TN = 32;
-    while (a.TN < 256 && a.TN < 2 * ((S + E - 1) / E)) a.TN *= 2;
-    const int cg = a.TN == 256 && N > 128 ? 2 : 1;
+    const int cg = choose_tile(a, false, true);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(type, nk ? kNK : kKN, cg);
     CUtensorMap tl, tc;
@@ -903,6 +1086,8 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
     a.max_tiles = static_cast<int>(tiles);
     a.by_lane = Divisor(static_cast<uint32_t>(nlt));
     a.by_group = Divisor(static_cast<uint32_t>(kBand * nlt));
+    if (a.split > 1)
+        return nk ? launch<kNK, 1, false, true>(tl, tc, a, tiles, st) : launch<kKN, 1, false, true>(tl, tc, a, tiles, st);
     if (cg == 2) return nk ? launch<kNK, 2>(tl, tc, a, tiles, st) : launch<kKN, 2>(tl, tc, a, tiles, st);
     return nk ? launch<kNK, 1>(tl, tc, a, tiles, st) : launch<kKN, 1>(tl, tc, a, tiles, st);
 }
@@ -917,8 +1102,7 @@ spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const v
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.row_scale = row_scale, a.col_scale = col_scale;
     a.same_w = mats == 1;
-    a.TN = 256;
-    const int cg = N > 128 ? 2 : 1;
+    const int cg = choose_tile(a, false, true);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(SPX_F16, kNK, cg);
     CUtensorMap tl, tc;
@@ -929,6 +1113,7 @@ spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const v
     a.max_tiles = static_cast<int>(tiles);
     a.by_lane = Divisor(static_cast<uint32_t>(nlt));
     a.by_group = Divisor(static_cast<uint32_t>(kBand * nlt));
+    if (a.split > 1) return launch<kNK, 1, true, true>(tl, tc, a, tiles, st);
     return cg == 2 ? launch<kNK, 2, true>(tl, tc, a, tiles, st) : launch<kNK, 1, true>(tl, tc, a, tiles, st);
 }
 
@@ -942,8 +1127,7 @@ spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* 
     TcArgs a{};
     a.offsets = offsets, a.E = E, a.S = S, a.NL = K, a.NC = N;
     a.C = dW, a.ldc = ldw, a.ce = stride_w, a.c_type = w_type;
-    a.TN = N > 128 ? 256 : 128;
-    const int cg = a.TN == 256 && K > 128 ? 2 : 1;
+    const int cg = choose_tile(a, true, false);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(type, kWG, cg);
     CUtensorMap tl, tc;

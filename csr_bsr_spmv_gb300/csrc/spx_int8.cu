@@ -8,6 +8,7 @@
 // rows (decoded tokens) are bound by the weights' bytes: they run on the CUDA
 // cores' four-way byte dot product straight from the 8-bit weights.
 #include <algorithm>
+#include <type_traits>
 
 #include "spx_experts.cuh"
 
@@ -17,74 +18,184 @@ namespace {
 
 // ---------------------------------------------------------------- quantisation
 
-// One CTA a row: its largest magnitude, then the codes.  Bound by HBM.  A row
-// of up to kQHeld pieces a thread stays in registers between the two; a longer
-// one is read again (from L2).
-constexpr int kQThreads = 256, kQHeld = 4;
+// A row's largest magnitude, then its codes.  Bound by HBM.  A group of G
+// threads takes a row: a warp where there are rows enough to fill the SMs (16384
+// rows x 2048 bf16: MEASURE us, a CTA a row 52), a CTA otherwise.  Up to kQHeld
+// pieces a thread stay in registers between the two; a longer row is read again
+// (from L2).
+constexpr int kQThreads = 256, kQHeld = 8;
+constexpr int kQWarpRows = 1216;  // rows from which a warp takes one: eight a CTA, one CTA an SM
 
 template <class V, int N>
 struct alignas(N * sizeof(V) >= 16 ? 16 : N * sizeof(V)) Pack {
     V v[N];
 };
 
-// N values a piece: 16 bytes of X where rows are aligned, else 1 value.
+// A piece is read and written as one word of its size.
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> {
+    using T = uint4;
+};
+template <>
+struct Word<8> {
+    using T = uint2;
+};
+template <>
+struct Word<4> {
+    using T = uint32_t;
+};
+template <>
+struct Word<2> {
+    using T = uint16_t;
+};
+template <>
+struct Word<1> {
+    using T = uint8_t;
+};
+template <class P>
+__device__ __forceinline__ P read_piece(const P* p) {
+    using T = typename Word<sizeof(P)>::T;
+    const T w = __ldcs(reinterpret_cast<const T*>(p));
+    P r;
+    memcpy(&r, &w, sizeof(P));
+    return r;
+}
+template <class P>
+__device__ __forceinline__ void write_piece(P* p, const P& v) {
+    using T = typename Word<sizeof(P)>::T;
+    T w;
+    memcpy(&w, &v, sizeof(P));
+    *reinterpret_cast<T*>(p) = w;
+}
+
+// The largest magnitude seen, as fp32 bits: those of an infinity or NaN are
+// above every number's, so one of them anywhere shows in the result.
 template <class V, int N>
-__global__ void __launch_bounds__(kQThreads)
-    quant_rows_kernel(int K, const V* __restrict__ X, long long ldx, int8_t* __restrict__ Q, long long ldq,
+struct Largest {
+    uint32_t m = 0;
+    __device__ __forceinline__ void look(const Pack<V, N>& p) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(to_f(p.v[i])) & 0x7fffffffu);
+    }
+    __device__ __forceinline__ uint32_t bits() const { return m; }
+};
+// 16-bit values two at a time.
+__device__ __forceinline__ __nv_bfloat162 max_abs(__nv_bfloat162 m, __nv_bfloat162 x) { return __hmax2_nan(m, __habs2(x)); }
+__device__ __forceinline__ __half2 max_abs(__half2 m, __half2 x) { return __hmax2_nan(m, __habs2(x)); }
+template <class V>
+struct Largest<V, 8> {
+    using V2 = typename std::conditional<std::is_same<V, __half>::value, __half2, __nv_bfloat162>::type;
+    uint32_t m = 0;  // two zeros
+    __device__ __forceinline__ void look(const Pack<V, 8>& p) {
+        V2 x[4], y;
+        memcpy(x, &p, 16);
+        memcpy(&y, &m, 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y = max_abs(y, x[i]);
+        memcpy(&m, &y, 4);
+    }
+    __device__ __forceinline__ uint32_t bits() const {
+        V v[2];
+        memcpy(v, &m, 4);
+        return max(__float_as_uint(to_f(v[0])) & 0x7fffffffu, __float_as_uint(to_f(v[1])) & 0x7fffffffu);
+    }
+};
+
+// Low bytes of N words.
+template <int N>
+__device__ __forceinline__ void low_bytes(const uint32_t (&t)[N], Pack<int8_t, N>& b) {
+    if constexpr (N == 1) {
+        b.v[0] = static_cast<int8_t>(t[0]);
+    } else {
+        uint32_t w[N / 4];
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            w[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040), __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040), 0x5410);
+        memcpy(&b, w, N);
+    }
+}
+
+// The codes of a piece by division; a call, so that this rare path costs the
+// kernel no registers.
+template <class V, int N>
+__device__ __noinline__ Pack<int8_t, N> divided_codes(Pack<V, N> p, float s) {
+    Pack<int8_t, N> b;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float v = s > 0.f ? rintf(to_f(p.v[i]) / s) : 0.f;
+        b.v[i] = static_cast<int8_t>(fminf(fmaxf(v, -127.f), 127.f));
+    }
+    return b;
+}
+
+// N values a piece: 16 bytes of X where rows are aligned, else 1 value.
+template <class V, int N, int G>
+__global__ void __launch_bounds__(kQThreads, 4)
+    quant_rows_kernel(int M, int K, const V* __restrict__ X, long long ldx, int8_t* __restrict__ Q, long long ldq,
                       float* __restrict__ scale) {
     using P = Pack<V, N>;
     using B = Pack<int8_t, N>;
-    __shared__ float s_max[kQThreads / 32];
-    const P* x = reinterpret_cast<const P*>(X + blockIdx.x * ldx);
-    B* q = reinterpret_cast<B*>(Q + blockIdx.x * ldq);
+    __shared__ uint32_t s_max[kQThreads / 32];
+    const int row = blockIdx.x * (kQThreads / G) + threadIdx.x / G, at = threadIdx.x % G;
+    if (row >= M) return;  // a whole group; G == kQThreads: never
+    const P* x = reinterpret_cast<const P*>(X + row * ldx);
+    B* q = reinterpret_cast<B*>(Q + row * ldq);
     const int np = K / N;
-    // a NaN or infinity anywhere makes `bad` NaN: v * 0 is 0 for every other value
-    float m = 0.f, bad = 0.f;
+    Largest<V, N> big;
     P held[kQHeld];
-    auto look = [&](const P& p) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float v = to_f(p.v[i]);
-            m = fmaxf(m, fabsf(v));
-            bad = fmaf(v, 0.f, bad);
-        }
-    };
-#pragma unroll
-    for (int h = 0; h < kQHeld; ++h) {
-        const int k = threadIdx.x + h * kQThreads;
-        if (k < np) held[h] = x[k];
-    }
 #pragma unroll
     for (int h = 0; h < kQHeld; ++h)
-        if (threadIdx.x + h * kQThreads < np) look(held[h]);
-    for (int k = threadIdx.x + kQHeld * kQThreads; k < np; k += kQThreads) look(x[k]);
-    if (bad != bad) m = __int_as_float(0x7f800000);
+        if (at + h * G < np) held[h] = read_piece(x + at + h * G);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = s_max[0];
+    for (int h = 0; h < kQHeld; ++h)
+        if (at + h * G < np) big.look(held[h]);
+    for (int k = at + kQHeld * G; k < np; k += G) big.look(read_piece(x + k));
+    uint32_t m = big.bits();
 #pragma unroll
-    for (int w = 1; w < kQThreads / 32; ++w) m = fmaxf(m, s_max[w]);
-    const bool fine = m < __int_as_float(0x7f800000);
-    const float s = m / 127.f;
-    if (threadIdx.x == 0) scale[blockIdx.x] = fine ? s : __int_as_float(0x7fffffff);
+    for (int d = 16; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (G > 32) {
+        if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+        __syncthreads();
+        m = s_max[0];
+#pragma unroll
+        for (int w = 1; w < kQThreads / 32; ++w) m = max(m, s_max[w]);
+    }
+    const bool fine = m < 0x7f800000u;
+    const float s = __uint_as_float(m) / 127.f;
+    if (at == 0) scale[row] = fine ? s : __int_as_float(0x7fffffff);
+    // The quotient x / s from the rounded reciprocal: a first quotient, its exact remainder (one fused multiply-add),
+    // and a correction, which rounds it correctly (Markstein, "Computation of elementary functions on the IBM RISC
+    // System/6000 processor", 1990).  In bf16 rows quotients that lie exactly between two whole numbers are common
+    // (0.2% of them), so nothing less exact than the division itself would give its codes.  Subnormal scales, whose
+    // reciprocal may not exist, divide; they are coarse, so the quotient may pass 127.
+    const bool plain = fine && s >= 1e-30f;
+    const float inv = plain ? 1.f / s : 0.f;
+    constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
     auto code = [&](const P& p) {
+        if (!plain) return divided_codes<V, N>(p, fine ? s : 0.f);
         B b;
+        uint32_t t[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            // a subnormal scale is coarse, so the quotient may pass 127
-            const float v = fine && s > 0.f ? rintf(to_f(p.v[i]) / s) : 0.f;
-            b.v[i] = static_cast<int8_t>(fminf(fmaxf(v, -127.f), 127.f));
+            const float x = to_f(p.v[i]), q0 = x * inv;
+            t[i] = __float_as_uint(fmaf(fmaf(-q0, s, x), inv, q0) + kWhole);
         }
+        low_bytes<N>(t, b);
         return b;
     };
 #pragma unroll
-    for (int h = 0; h < kQHeld; ++h) {
-        const int k = threadIdx.x + h * kQThreads;
-        if (k < np) q[k] = code(held[h]);
-    }
-    for (int k = threadIdx.x + kQHeld * kQThreads; k < np; k += kQThreads) q[k] = code(x[k]);
+    for (int h = 0; h < kQHeld; ++h)
+        if (at + h * G < np) write_piece(q + at + h * G, code(held[h]));
+    for (int k = at + kQHeld * G; k < np; k += G) write_piece(q + k, code(read_piece(x + k)));
+}
+
+template <class V, int N>
+void quant_grid(int M, int K, const V* x, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, cudaStream_t st) {
+    constexpr int per = kQThreads / 32;
+    if (M >= kQWarpRows) quant_rows_kernel<V, N, 32><<<(M + per - 1) / per, kQThreads, 0, st>>>(M, K, x, ldx, Q, ldq, scale);
+    else quant_rows_kernel<V, N, kQThreads><<<M, kQThreads, 0, st>>>(M, K, x, ldx, Q, ldq, scale);
 }
 
 template <class V>
@@ -92,9 +203,9 @@ void quant_launch(int M, int K, const void* X, int64_t ldx, int8_t* Q, int64_t l
     constexpr int N = 16 / sizeof(V);
     const V* x = static_cast<const V*>(X);
     if (spx_aligned(X, 16) && spx_aligned(Q, N) && ldx % N == 0 && ldq % N == 0 && K % N == 0)
-        quant_rows_kernel<V, N><<<M, kQThreads, 0, st>>>(K, x, ldx, Q, ldq, scale);
+        quant_grid<V, N>(M, K, x, ldx, Q, ldq, scale, st);
     else
-        quant_rows_kernel<V, 1><<<M, kQThreads, 0, st>>>(K, x, ldx, Q, ldq, scale);
+        quant_grid<V, 1>(M, K, x, ldx, Q, ldq, scale, st);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -253,39 +364,47 @@ __global__ void __launch_bounds__(kWidenThreads)
         src = W + e * stride_w, ld = ldw, rows = N;
         dst = W16 + static_cast<long long>(e) * N * Kp;
     }
-    const int np = (K + 15) / 16;
-    const long long total = static_cast<long long>(rows) * np;
-    for (long long i = blockIdx.x * static_cast<long long>(kWidenThreads) + threadIdx.x; i < total;
-         i += static_cast<long long>(gridDim.x) * kWidenThreads) {
-        const int r = static_cast<int>(i / np), k = static_cast<int>(i % np) * 16;
-        const int8_t* s = src + r * ld + k;
-        uint32_t w[4];
-        if (ALIGNED && k + 16 <= K) {
-            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(s));
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else {
+    // eight codes a piece: a warp's loads and stores are both contiguous
+    const int np = (K + 7) / 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int U = 4;  // pieces in flight
+    for (int r = blockIdx.x * (kWidenThreads / 32) + warp; r < rows; r += gridDim.x * (kWidenThreads / 32)) {
+        const int8_t* s = src + r * ld;
+        __half* d = dst + static_cast<long long>(r) * Kp;
+        for (int p0 = lane; p0 < np; p0 += 32 * U) {
+            uint2 w[U];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                w[b] = 0;
+            for (int u = 0; u < U; ++u) {
+                const int k = 8 * (p0 + 32 * u);
+                w[u] = make_uint2(0u, 0u);
+                if (ALIGNED && k + 8 <= K) {
+                    w[u] = __ldcs(reinterpret_cast<const uint2*>(s + k));
+                } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (k + 4 * b + c < K) w[b] |= static_cast<uint32_t>(static_cast<uint8_t>(s[4 * b + c])) << (8 * c);
+                    for (int c = 0; c < 8; ++c)
+                        if (k + c < K)
+                            (c < 4 ? w[u].x : w[u].y) |= static_cast<uint32_t>(static_cast<uint8_t>(s[k + c])) << (8 * (c & 3));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = p0 + 32 * u;
+                const uint2 lo = widen_codes(w[u].x), hi = widen_codes(w[u].y);
+                if (p < np) reinterpret_cast<uint4*>(d)[p] = make_uint4(lo.x, lo.y, hi.x, hi.y);
             }
         }
-        uint4* d = reinterpret_cast<uint4*>(dst + static_cast<long long>(r) * Kp + k);
-        const uint2 h0 = widen_codes(w[0]), h1 = widen_codes(w[1]), h2 = widen_codes(w[2]), h3 = widen_codes(w[3]);
-        d[0] = make_uint4(h0.x, h0.y, h1.x, h1.y);
-        if (k + 8 < Kp) d[1] = make_uint4(h2.x, h2.y, h3.x, h3.y);
     }
 }
 
-// Rows in all up to which the few-rows kernel is taken.
-constexpr int kFewRows = 8;
+// The few-rows kernel is taken up to kFewEach rows an expert on average and
+// kFewMore in all besides: 64 experts of 2048 x 2048, 64 rows 41 us (146 through
+// 16-bit codes), 512 rows 141 (219), 1024 rows 244 (215); one of 4096 x 4096, 16
+// rows 14 us (22), 32 rows 24 (22).
+constexpr int kFewEach = 8, kFewMore = 8;
 
 int pitch16(int K) { return (K + 7) / 8 * 8; }
 
-bool few_fits(int S, const int8_t* Q, int64_t ldq, const int8_t* W, int64_t ldw, int64_t stride_w, int K) {
-    return S <= kFewRows && K % 16 == 0 && spx_aligned(Q, 16) && spx_aligned(W, 16) && ldq % 16 == 0 && ldw % 16 == 0 &&
+bool few_fits(int E, int S, const int8_t* Q, int64_t ldq, const int8_t* W, int64_t ldw, int64_t stride_w, int K) {
+    return S <= kFewEach * static_cast<int64_t>(E) + kFewMore && K % 16 == 0 && spx_aligned(Q, 16) && spx_aligned(W, 16) && ldq % 16 == 0 && ldw % 16 == 0 &&
            stride_w % 16 == 0;
 }
 
@@ -332,9 +451,9 @@ spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t
     if (K == 0)
         return spx_cuda_status(cudaMemset2DAsync(C, static_cast<size_t>(ldc) * cb, 0, static_cast<size_t>(N) * cb,
                                                  static_cast<size_t>(S), st));
-    if (few_fits(S, Q, ldq, W, ldw, stride_w, K)) {
+    if (few_fits(E, S, Q, ldq, W, ldw, stride_w, K)) {
         const FewArgs a{offsets, E, S, N, K, Q, ldq, row_scale, W, ldw, stride_w, w_scale, C, ldc, c_type};
-        const long long ty = offsets ? std::min<long long>(max_row_tiles(E, S, kFew), S + 1) : (S + kFew - 1) / kFew;
+        const long long ty = offsets ? std::min<long long>(max_row_tiles(E, S, kFew), static_cast<long long>(S) + 1) : (S + kFew - 1) / kFew;
         i8_few_kernel<<<dim3((N + kFewThreads / 32 * kChan - 1) / (kFewThreads / 32 * kChan), static_cast<unsigned>(ty)),
                         kFewThreads, 0, st>>>(a);
         spx_note_launches(1);
@@ -348,9 +467,9 @@ spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t
     __half* Q16 = static_cast<__half*>(scratch);
     __half* W16 = Q16 + (static_cast<size_t>(Kp) * S + 127) / 128 * 128;
     {
-        const bool aligned = spx_aligned(Q, 16) && spx_aligned(W, 16) && ldq % 16 == 0 && ldw % 16 == 0 && stride_w % 16 == 0;
-        const long long most = static_cast<long long>(std::max(S, N)) * ((K + 15) / 16);
-        const dim3 grid(static_cast<unsigned>(std::min<long long>((most + kWidenThreads - 1) / kWidenThreads, 1216)), 1 + mats);
+        const bool aligned = spx_aligned(Q, 8) && spx_aligned(W, 8) && ldq % 8 == 0 && ldw % 8 == 0 && stride_w % 8 == 0;
+        constexpr int per = kWidenThreads / 32;  // a row a warp
+        const dim3 grid(std::min((std::max(S, N) + per - 1) / per, 1216), 1 + mats);
         if (aligned)
             widen_kernel<true><<<grid, kWidenThreads, 0, st>>>(offsets, S, N, K, Kp, Q, ldq, W, ldw, stride_w, Q16, W16, same_w);
         else
