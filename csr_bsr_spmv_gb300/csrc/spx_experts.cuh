@@ -31,6 +31,17 @@ __device__ __forceinline__ __half from_f<__half>(float v) {
     return __float2half_rn(v);
 }
 
+// Four 8-bit codes (bytes of w) as fp16: 0x6400 | u is 1024 + u for a byte u,
+// and u = code + 128 after flipping its top bit, so one subtraction is exact.
+__device__ __forceinline__ uint2 widen_codes(uint32_t w) {
+    w ^= 0x80808080u;
+    const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
 // Rows [lo, hi) of expert e, whatever the offsets hold: inside [0, S], lo <= hi.
 __device__ __forceinline__ void expert_rows(const int* __restrict__ offsets, int e, int S, int& lo, int& hi) {
     lo = min(max(__ldg(offsets + e), 0), S);
@@ -59,12 +70,18 @@ namespace spx_exp {
 __device__ __forceinline__ bool warp_find_tile(const int* __restrict__ offsets, int E, int S, int TM, int tile, int& e,
                                                int& r0, int& hi) {
     const int lane = threadIdx.x & 31;
+    constexpr int P = 4;  // experts a lane looks at in a round, their offsets read side by side
     int base = 0;
-    for (int e0 = 0; e0 <= E; e0 += 32) {
-        int lo = 0, up = 0;
-        if (e0 + lane < E) expert_rows(offsets, e0 + lane, S, lo, up);
-        else if (e0 + lane == E) lo = min(max(__ldg(offsets + E), 0), S), up = S;
-        const int n = (up - lo + TM - 1) / TM;
+    for (int e0 = 0; e0 <= E; e0 += 32 * P) {
+        int lo[P], up[P], n = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int x = e0 + lane * P + i;
+            lo[i] = up[i] = 0;
+            if (x < E) expert_rows(offsets, x, S, lo[i], up[i]);
+            else if (x == E) lo[i] = min(max(__ldg(offsets + E), 0), S), up[i] = S;
+            n += (up[i] - lo[i] + TM - 1) / TM;
+        }
         int inc = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -74,12 +91,22 @@ __device__ __forceinline__ bool warp_find_tile(const int* __restrict__ offsets, 
         const unsigned at = __ballot_sync(0xffffffffu, tile < base + inc);
         if (at) {
             const int src = __ffs(at) - 1;
-            const int first = base + __shfl_sync(0xffffffffu, inc - n, src);
-            if (tile < first) return false;  // only sums of wrong offsets that passed int32
-            e = e0 + src;
-            r0 = __shfl_sync(0xffffffffu, lo, src) + (tile - first) * TM;
-            hi = __shfl_sync(0xffffffffu, up, src);
-            return true;
+            int first = base + inc - n, x = e0 + lane * P, r = 0, h = 0;  // the answer is that of lane src
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int m = (up[i] - lo[i] + TM - 1) / TM;
+                if (h == 0 && tile < first + m) {
+                    r = lo[i] + (tile - first) * TM;
+                    h = up[i];
+                    x = e0 + lane * P + i;
+                    if (tile < first) r = h = 0;  // only sums of wrong offsets that passed int32
+                }
+                first += m;
+            }
+            e = __shfl_sync(0xffffffffu, x, src);
+            r0 = __shfl_sync(0xffffffffu, r, src);
+            hi = __shfl_sync(0xffffffffu, h, src);
+            return r0 < hi;
         }
         base += __shfl_sync(0xffffffffu, inc, 31);
     }
@@ -112,6 +139,11 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
 spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const void* Q, int64_t ldq,
                          const float* row_scale, const void* W, int64_t ldw, int64_t mats, const float* col_scale,
                          void* C, int64_t ldc, spx_type c_type, cudaStream_t st);
+// The same from the 8-bit codes themselves, for rows on 16-byte boundaries.
+bool tc_codes_fit(const int8_t* Q, int64_t ldq, const int8_t* W, int64_t ldw, int64_t stride_w);
+spx_status tc_product_codes(int E, int S, int N, int K, const int* offsets, const int8_t* Q, int64_t ldq,
+                            const float* row_scale, const int8_t* W, int64_t ldw, int64_t stride_w,
+                            const float* col_scale, void* C, int64_t ldc, spx_type c_type, cudaStream_t st);
 bool tc_wgrad_fits(const void* G, int64_t ldg, const void* A, int64_t lda);
 spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* G, int64_t ldg, const void* A,
                     int64_t lda, spx_type type, void* dW, int64_t ldw, int64_t stride_w, spx_type w_type,

@@ -39,7 +39,10 @@ enum Mode : int { kNK = 0, kKN = 1, kWG = 2 };
 // tile's rows), one for the lane factor's copies, one for the MMAs, one for
 // the column factor's copies.
 constexpr int kStoreWarps = 8;
-constexpr int kThreads = 32 * (kStoreWarps + 3);
+constexpr int kWidenWarps = 8;  // FUSE
+template <bool FUSE>
+constexpr int kThreadsOf = 32 * (kStoreWarps + 3 + (FUSE ? kWidenWarps : 0));
+constexpr int kRawDepth = 128;  // FUSE: reduction length of a raw stage, one 128-byte row
 constexpr int kDepth = 64;                      // reduction length of a stage: one 128-byte swizzle row
 constexpr uint32_t kLaneBytes = 128 * kDepth * 2;  // a stage's lane factor: 128 lanes a CTA, 16 KB
 constexpr uint32_t kBox = 64 * kDepth * 2;      // an MN-major box: 64 long, 64 deep, 8 KB
@@ -80,6 +83,8 @@ struct TcArgs {
     int TN, log_tn;   // output rows a tile: 32 to 256, a power of two
     int max_tiles;    // kWG: the tiles; else no fewer than sound offsets give
     int stages;
+    int raw_stages;   // FUSE
+    uint32_t raw_bytes;
     uint32_t stage_bytes, idesc, part_off;  // part_off: the shared partial tile, behind the tile list
     int split, split_red;  // CTAs that share a tile's reduction, and the length of a share (a multiple of kDepth)
     int same_w;       // 1: every expert reads W_0
@@ -384,18 +389,23 @@ __device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, lon
     else store_rows(a, it, static_cast<__half*>(a.C) + off, x, lane, a.wide_c, patch, c0, v);
 }
 
+// FUSE: the factors are 8-bit codes.  Their bytes arrive in a ring of raw
+// stages, and eight more warps widen them to fp16 into the ring the MMAs read.
+// The weights then cost one byte each wherever they come from, against five
+// through a widened copy in memory; but every stage passes through shared
+// memory twice more, which bounds it at 470 to 800 cycles a stage.
 // SPLIT: a cluster of a.split CTAs shares each tile, every one the products of
 // its part of the reduction; the partial tiles meet in shared memory, where
 // CTA r adds the parts of its share of the rows in rank order.
-template <int MODE, int CG, bool I8, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int MODE, int CG, bool I8, bool SPLIT, bool FUSE>
+__global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tm_lane, const __grid_constant__ CUtensorMap tm_col,
                       const __grid_constant__ TcArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_issued, s_issued_col, s_consumed, s_tails_in, s_tails_done;
-    __shared__ __align__(8) uint64_t s_bars[4 * kMaxStages + 7];
+    __shared__ __align__(8) uint64_t s_bars[6 * kMaxStages + 7];
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t bars = smem_u32(s_bars);
@@ -411,11 +421,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto clear_bar = [&](uint32_t s) { return bars + 8u * (3 * kMaxStages + 5 + s); };
     // SPLIT: every part of a tile is in place; everybody has read this CTA's
     const uint32_t ready_bar = bars + 8u * (4 * kMaxStages + 5), done_bar = bars + 8u * (4 * kMaxStages + 6);
-    const uint32_t NS = a.stages;
+    // FUSE: a raw stage has arrived, has been read
+    auto raw_full = [&](uint32_t s) { return bars + 8u * (4 * kMaxStages + 7 + s); };
+    auto raw_empty = [&](uint32_t s) { return bars + 8u * (5 * kMaxStages + 7 + s); };
+    const uint32_t NS = a.stages, NR = a.raw_stages;
     // the storing warps' patches, then the tile list, behind the ring
     List list;
-    list.lo = reinterpret_cast<int*>(smem_raw + (base - smem_u32(smem_raw)) + NS * a.stage_bytes +
-                                     kStoreWarps * kPatchBytes);
+    const uint32_t raw0 = base + NS * a.stage_bytes;  // FUSE: the raw ring
+    const uint32_t behind = raw0 + (FUSE ? NR * a.raw_bytes : 0);
+    list.lo = reinterpret_cast<int*>(smem_raw + (behind - smem_u32(smem_raw)) + (SPLIT ? 0 : kStoreWarps * kPatchBytes));
     list.hi = list.lo + a.E + 1;
     list.first = list.hi + a.E + 1;
 
@@ -438,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < NS; ++s) {
-            mbar_init(full_bar(s), 1);
+            mbar_init(full_bar(s), FUSE ? kWidenWarps / 2 : 1);
             mbar_init(empty_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -450,6 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(ready_bar, kStoreWarps * a.split);
             mbar_init(done_bar, kStoreWarps * a.split);
         }
+        if (FUSE)
+            for (uint32_t s = 0; s < NR; ++s) {
+                mbar_init(raw_full(s), 1);
+                mbar_init(raw_empty(s), kWidenWarps);
+            }
         if (MODE == kWG)
             for (uint32_t s = 0; s < NS; ++s) {
                 mbar_init(tail_bar(s), 1);
@@ -474,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     int ntiles = a.max_tiles;  // kWG: every expert's tiles, rows or not
-    for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+    for (int e = threadIdx.x; e <= a.E; e += kThreadsOf<FUSE>) {
         int lo = 0, hi = a.S;
         if (a.offsets) {
             if (e < a.E) expert_rows(a.offsets, e, a.S, lo, hi);
@@ -518,18 +537,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- producers: this CTA's part of every stage, one thread for each factor (a thread takes
         // about 250 cycles from one copy to the next, so one alone would hold up the MMAs)
         const bool lanes = warp == LOAD;
-        Ring ring(NS);
+        Ring ring(FUSE ? NR : NS);
         uint32_t issued = 0, tails = 0;
         bool ok = true;
+        constexpr int depth = FUSE ? kRawDepth : kDepth;
         for (int t = me; t < ntiles && ok; t += G) {
             const Item it = share(tile_item<MODE, CG>(a, list, t));
             const int cols = MODE == kWG ? a.TN : mma_cols<CG>(it.rows);  // a pair's CTA holds half of them
             const int lane0 = uniform(it.lane0) + 128 * rank, col0 = uniform(it.row0 + rank * cols / 2);
             const int z = a.same_w ? 0 : uniform(it.e), r0 = uniform(it.red0), end = r0 + uniform(it.red);
-            for (int r = r0; r < end; r += kDepth, ring.next(), ++issued) {
-                const uint32_t s8 = 8u * ring.s, sl = base + ring.s * a.stage_bytes, sc = sl + kLaneBytes;
-                ok = warp_wait(empty_bar(0) + s8, ring.ph ^ 1u) && !s_abort;
+            for (int r = r0; r < end; r += depth, ring.next(), ++issued) {
+                const uint32_t s8 = 8u * ring.s, sl = FUSE ? raw0 + ring.s * a.raw_bytes : base + ring.s * a.stage_bytes;
+                const uint32_t sc = sl + (FUSE ? 128 * kRawDepth : kLaneBytes);
+                ok = warp_wait((FUSE ? raw_empty(0) : empty_bar(0)) + s8, ring.ph ^ 1u) && !s_abort;
                 if (!ok) break;
+                if (FUSE) {
+                    if (!elect()) continue;
+                    if (lanes) {
+                        mbar_expect_tx(raw_full(0) + s8, a.raw_bytes);
+                        load_3d<CG>(sl, &tm_lane, r, lane0, z, raw_full(0) + s8);
+                    } else {
+                        load_2d<CG>(sc, &tm_col, r, col0, raw_full(0) + s8);
+                    }
+                    continue;
+                }
                 uint32_t bar = full0 + s8;
                 const bool ragged = MODE == kWG && end - r < kDepth && (end - r) % 16;
                 if (ragged) {
@@ -567,6 +598,77 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             (lanes ? s_issued : s_issued_col) = issued;
             if (lanes) s_tails_in = tails;
+        }
+    } else if (FUSE && warp > LOAD2) {
+        // ---------------- widening: raw bytes to the swizzled fp16 stages
+        // four warps take the first half of every raw stage, four the second: two stages are in the making at once
+        const int h = (warp - LOAD2 - 1) >> 2, w = (warp - LOAD2 - 1) & 3;
+        Ring raw(NR), ring(NS);
+        uint32_t taken = 0;
+        bool ok = true;
+        // eight rows of four 16-byte pieces a step; a quarter of a warp takes rows q and q + 4, and the two rows' halves
+        // are stored in opposite order, so that neither the reads nor the stores of the swizzled rows share banks
+        const int piece = lane & 3, odd = lane >> 2 & 1, row8 = odd * 4 + (lane >> 3);
+        for (int t = me; t < ntiles && ok; t += G) {
+            const Item it = share(tile_item<MODE, CG>(a, list, t));
+            const int rows = 128 + uniform(mma_cols<CG>(it.rows));  // the lanes' rows, then the columns'
+            for (int left = uniform(it.red); left > 0; left -= kRawDepth, raw.next(), ++taken) {
+                ok = warp_wait(raw_full(raw.s), raw.ph) && !s_abort;
+                if (!ok) break;
+                const int halves = left > 64 ? 2 : 1;
+                if (h < halves) {
+                    const uint32_t src = raw0 + raw.s * a.raw_bytes;
+                    Ring mine = ring;
+                    if (h) mine.next();
+                    const uint32_t dst = base + mine.s * a.stage_bytes;
+                    for (int i0 = 0; 8 * (w + 4 * i0) < rows; i0 += 4) {
+                        uint4 c[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 8 * (w + 4 * (i0 + i)) + row8;
+                            if (r < rows)
+                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(c[i].x), "=r"(c[i].y), "=r"(c[i].z), "=r"(c[i].w)
+                                             : "r"(src + 128 * r + 16 * ((4 * h + piece) ^ (r & 7)))
+                                             : "memory");
+                        }
+                        if (i0 == 0) {
+                            ok = warp_wait(empty_bar(mine.s), mine.ph ^ 1u) && !s_abort;
+                            if (!ok) break;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 8 * (w + 4 * (i0 + i)) + row8;
+                            if (r >= rows) break;
+                            const uint2 h0 = widen_codes(c[i].x), h1 = widen_codes(c[i].y), h2 = widen_codes(c[i].z),
+                                        h3 = widen_codes(c[i].w);
+                            const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
+                            const uint4 a1 = odd ? hi : lo, a2 = odd ? lo : hi;
+                            const uint32_t q = dst + 128 * r, i1 = (2 * piece + odd) ^ (r & 7), i2 = i1 ^ 1;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q + 16 * i1), "r"(a1.x),
+                                         "r"(a1.y), "r"(a1.z), "r"(a1.w)
+                                         : "memory");
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q + 16 * i2), "r"(a2.x),
+                                         "r"(a2.y), "r"(a2.z), "r"(a2.w)
+                                         : "memory");
+                        }
+                    }
+                    if (!ok) break;
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full_bar(mine.s));
+                }
+                if (lane == 0) mbar_arrive(raw_empty(raw.s));
+                ring.next();
+                if (halves == 2) ring.next();
+            }
+        }
+        if (lane == 0) {
+            if (!ok) {
+                record_error(kErrFull);
+                s_abort = 1;
+            }
+            if (w == 0 && h == 0) s_consumed = taken;
         }
     } else if (warp == MMA) {
         // ---------------- MMA issuer (the pair's first CTA)
@@ -649,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 record_error(kErrFull);
                 s_abort = 1;
             }
-            if (lane == 0) s_consumed = consumed;
+            if (lane == 0 && !FUSE) s_consumed = consumed;
         } else if (MODE == kWG) {
             // the pair's second CTA: only its part of clearing the tails
             uint32_t at = 0;
@@ -666,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (lane == 0) s_tails_done = tails;
-    } else {
+    } else if (warp < SW) {
         // ---------------- storing warps: TMEM lane quarter = warp % 4
         int buf = 0;
         uint32_t tph = 0;
@@ -694,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             buf ^= 1;
             if (buf == 0) tph ^= 1u;
         };
-        const uint32_t patch = base + NS * a.stage_bytes + warp * kPatchBytes;
+        const uint32_t patch = behind + warp * kPatchBytes;
         const uint32_t quarter = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         // A tile whose reduction the cluster shares: this CTA's sums to its shared partial tile, then its rows of all.
         uint32_t pph = 0;  // tiles so far, mod 2
@@ -716,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto shared_tile = [&](const Item& it) {
             const Item mine = share(it);
-            const uint32_t part0 = base + NS * a.stage_bytes + kStoreWarps * kPatchBytes + a.part_off;
+            const uint32_t part0 = behind + a.part_off;
             if (!meet(done_bar, pph ^ 1u)) return false;
             int left = mine.red;
             bool fresh = true;
@@ -890,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // copies issued but never consumed: wait (bounded) until each has landed (a stage that only one factor's
             // copies were issued for runs into the limit, by which time they have)
             for (uint32_t g = s_consumed; g < max(s_issued, s_issued_col); ++g)
-                if (!mbar_wait(full_bar(g % NS), (g / NS) & 1u, kSpinLimit)) {
+                if (!mbar_wait(FUSE ? raw_full(g % NR) : full_bar(g % NS), (g / (FUSE ? NR : NS)) & 1u, kSpinLimit)) {
                     record_error(kErrDrain);
                     break;
                 }
@@ -914,16 +1016,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------ host side
 
-// 16-bit tensor map of up to three axes, 128-byte swizzle, a box of 64 x rows (x 1).
+// Tensor map of up to three axes, 128-byte swizzle, a box of 128 bytes x rows (x 1).
 bool make_map3(CUtensorMap* m, const void* base, spx_type type, uint64_t inner, uint64_t rows, uint64_t ld, uint64_t mats,
                uint64_t stride, uint32_t box_rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
+    const uint32_t size = static_cast<uint32_t>(type_bytes(type));
     cuuint64_t dims[3] = {inner, rows, mats};
-    cuuint64_t strides[2] = {ld * 2, stride * 2};
-    cuuint32_t box[3] = {64, box_rows, 1};
+    cuuint64_t strides[2] = {ld * size, stride * size};
+    cuuint32_t box[3] = {128 / size, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    return enc(m, type == SPX_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, mats ? 3 : 2,
+    return enc(m,
+               type == SPX_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+               : type == SPX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+               mats ? 3 : 2,
                const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -959,6 +1066,8 @@ int resident_teams(const void* kernel, int team, const cudaLaunchConfig_t& cfg) 
     return cache[key] = n;
 }
 
+enum Kind { kProduct, kGradient, kCodes };  // kCodes: 8-bit factors widened on the way (FUSE)
+
 // The tile (a.TN rows of 128 or, for a pair, 256 columns) and the CTAs that
 // share a tile's reduction (a.split, a.split_red), by the least modelled time;
 // returns the CTAs of a tile, 1 or 2.  Cycles of a 64-deep stage, measured on
@@ -969,17 +1078,21 @@ int resident_teams(const void* kernel, int team, const cudaLaunchConfig_t& cfg) 
 // about 1500 cycles a CTA for the exchange.  512 rows x 4096 x 4096: 128-row
 // tiles 19 us, 256-row pairs 25, 64-row tiles 30; 16 rows: one CTA a tile 16.5
 // us, two 13.0, four 11.6, eight 16.1.  `mean` rows (kWG: terms) an expert.
-int choose_tile(TcArgs& a, bool wgrad, bool may_split) {
+int choose_tile(TcArgs& a, Kind kind) {
+    const bool wgrad = kind == kGradient, fused = kind == kCodes;
     struct Shape {
         int tn, cg, stage;
     };
     constexpr Shape shapes[] = {{256, 2, 615}, {256, 1, 725}, {128, 2, 435}, {128, 1, 460}, {64, 1, 390}, {32, 1, 350}};
+    constexpr Shape codes[] = {{128, 1, 800}, {64, 1, 570}, {32, 1, 470}};  // FUSE
+    const Shape *from = fused ? codes : shapes, *to = fused ? codes + 3 : shapes + 6;
     const double mean = static_cast<double>(a.S) / a.E, used = std::min(a.E, a.S);
     const int sms = sm_count();
     double best = 0;
-    Shape pick = shapes[0];
+    Shape pick = *from;
     a.split = 1;
-    for (const Shape& sh : shapes) {
+    for (; from != to; ++from) {
+        const Shape sh = *from;
         if (wgrad && sh.tn < 128) continue;                    // boxes of 64 columns, two lanes a stage
         if (sh.cg == 2 && a.NL <= 128) continue;
         const int most = wgrad ? a.NC : a.S;
@@ -992,20 +1105,21 @@ int choose_tile(TcArgs& a, bool wgrad, bool may_split) {
         const double tiles = rows * lanes, slots = sms / sh.cg;
         const double stages = wgrad ? mean / kDepth + 0.5 : (a.NR + kDepth - 1) / kDepth;
         for (int split = 1; split <= 8; split *= 2) {
-            if (split > 1 && (!may_split || sh.cg > 1 || sh.tn > 128 || tiles * split > slots)) break;
+            if (split > 1 && (wgrad || sh.cg > 1 || sh.tn > 128 || tiles * split > slots)) break;
             const double rounds = tiles * split <= slots ? 1 : tiles / slots < 4 ? static_cast<int>(tiles / slots + 0.99) : tiles / slots;
             const double cycles = rounds * (std::max(stages / split * sh.stage, 12.0 * sh.tn) + 600) + (split > 1 ? 1500 * split : 0);
             if (best == 0 || cycles < best) best = cycles, pick = sh, a.split = split;
         }
     }
     a.TN = pick.tn;
-    a.split_red = ((a.NR + kDepth - 1) / kDepth + a.split - 1) / a.split * kDepth;
+    const int unit = fused ? kRawDepth : kDepth;
+    a.split_red = ((a.NR + unit - 1) / unit + a.split - 1) / a.split * unit;
     return pick.cg;
 }
 
 bool rows_aligned(const void* p, int64_t ld) { return spx_aligned(p, 16) && ld % 8 == 0; }
 
-template <int MODE, int CG, bool I8 = false, bool SPLIT = false>
+template <int MODE, int CG, bool I8 = false, bool SPLIT = false, bool FUSE = false>
 spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long long max_tiles, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return SPX_ERR_CUDA;
@@ -1015,12 +1129,21 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     a.wide_f = spx_aligned(a.C, 16) && a.ldc % 4 == 0 && a.NL % 4 == 0;
     const int team = SPLIT ? a.split : CG;  // CTAs that work on one tile
     a.part_off = static_cast<uint32_t>((list_bytes(a.E) + 15) / 16 * 16);
-    const size_t list = kStoreWarps * kPatchBytes + a.part_off + (SPLIT ? a.TN * kPartPitch : 0);
-    a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemMax - 1024 - list) / a.stage_bytes));
-    const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + list;
-    if (set_smem_limit(experts_tc_kernel<MODE, CG, I8, SPLIT>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
+    const size_t list = a.part_off + (SPLIT ? a.TN * kPartPitch : kStoreWarps * kPatchBytes);
+    size_t room = kSmemMax - 1024 - list;
+    if (FUSE) {  // stages for the MMAs, more than the widening warps fill at once where there is room, and raw ones
+        a.stages = a.TN > 64 ? 2 : 4;
+        room -= a.stages * a.stage_bytes;
+        a.raw_stages = static_cast<int>(std::min<size_t>(kMaxStages, room / a.raw_bytes));
+        room = a.raw_stages * a.raw_bytes;
+    } else {
+        a.stages = static_cast<int>(std::min<size_t>(kMaxStages, room / a.stage_bytes));
+        room = 0;
+    }
+    const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + room + list;
+    if (set_smem_limit(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreadsOf<FUSE>);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1033,11 +1156,11 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     int groups = sms;
     if (team > 1) {
         cfg.gridDim = dim3(sms / team * team);
-        groups = resident_teams(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG, I8, SPLIT>), team, cfg);
+        groups = resident_teams(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE>), team, cfg);
         if (groups <= 0) return SPX_ERR_CUDA;
     }
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(max_tiles, groups)) * team);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_tc_kernel<MODE, CG, I8, SPLIT>, tl, tc, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE>, tl, tc, a);
     spx_note_launches(1);
     return spx_cuda_status(e != cudaSuccess ? e : cudaGetLastError());
 }
@@ -1074,7 +1197,7 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
     a.offsets = offsets, a.E = E, a.S = S, a.NL = N, a.NR = K;
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.same_w = E == 1 || stride_w == 0;
-    const int cg = choose_tile(a, false, true);
+    const int cg = choose_tile(a, kProduct);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(type, nk ? kNK : kKN, cg);
     CUtensorMap tl, tc;
@@ -1102,7 +1225,7 @@ spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const v
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.row_scale = row_scale, a.col_scale = col_scale;
     a.same_w = mats == 1;
-    const int cg = choose_tile(a, false, true);
+    const int cg = choose_tile(a, kProduct);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(SPX_F16, kNK, cg);
     CUtensorMap tl, tc;
@@ -1117,6 +1240,34 @@ spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const v
     return cg == 2 ? launch<kNK, 2, true>(tl, tc, a, tiles, st) : launch<kNK, 1, true>(tl, tc, a, tiles, st);
 }
 
+bool tc_codes_fit(const int8_t* Q, int64_t ldq, const int8_t* W, int64_t ldw, int64_t stride_w) {
+    return spx_aligned(Q, 16) && spx_aligned(W, 16) && ldq % 16 == 0 && ldw % 16 == 0 && stride_w % 16 == 0;
+}
+
+spx_status tc_product_codes(int E, int S, int N, int K, const int* offsets, const int8_t* Q, int64_t ldq,
+                            const float* row_scale, const int8_t* W, int64_t ldw, int64_t stride_w,
+                            const float* col_scale, void* C, int64_t ldc, spx_type c_type, cudaStream_t st) {
+    TcArgs a{};
+    a.offsets = offsets, a.E = E, a.S = S, a.NL = N, a.NR = K;
+    a.C = C, a.ldc = ldc, a.c_type = c_type;
+    a.row_scale = row_scale, a.col_scale = col_scale;
+    a.same_w = E == 1 || stride_w == 0;
+    choose_tile(a, kCodes);
+    a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN) * kDepth * 2;
+    a.raw_bytes = static_cast<uint32_t>(128 + a.TN) * kRawDepth;
+    a.idesc = idesc_of(SPX_F16, kNK, 1);
+    const uint64_t mats = a.same_w ? 1 : E, sw = a.same_w ? static_cast<uint64_t>(ldw) * N : stride_w;
+    CUtensorMap tl, tc;
+    if (!make_map3(&tl, W, SPX_I8, K, N, ldw, mats, sw, 128) || !make_map3(&tc, Q, SPX_I8, K, S, ldq, 0, 0, a.TN))
+        return SPX_ERR_CUDA;
+    const long long nlt = (N + 127) / 128, tiles = max_row_tiles(E, S, a.TN) * nlt;
+    if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;
+    a.max_tiles = static_cast<int>(tiles);
+    a.by_lane = Divisor(static_cast<uint32_t>(nlt));
+    a.by_group = Divisor(static_cast<uint32_t>(kBand * nlt));
+    return launch<kNK, 1, true, true, true>(tl, tc, a, tiles, st);
+}
+
 bool tc_wgrad_fits(const void* G, int64_t ldg, const void* A, int64_t lda) {
     return rows_aligned(G, ldg) && rows_aligned(A, lda);
 }
@@ -1127,7 +1278,7 @@ spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* 
     TcArgs a{};
     a.offsets = offsets, a.E = E, a.S = S, a.NL = K, a.NC = N;
     a.C = dW, a.ldc = ldw, a.ce = stride_w, a.c_type = w_type;
-    const int cg = choose_tile(a, true, false);
+    const int cg = choose_tile(a, kGradient);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(type, kWG, cg);
     CUtensorMap tl, tc;

@@ -4,9 +4,10 @@
 // This chip has no fast 8-bit integer matrix rate, but fp16 holds every code
 // exactly and the fp16 tensor cores sum their products exactly in fp32 up to
 // 2^24, so the product runs on the experts' tensor-core kernel with codes
-// widened to fp16, and its integer sums stay exact (see kExact there).  A few
-// rows (decoded tokens) are bound by the weights' bytes: they run on the CUDA
-// cores' four-way byte dot product straight from the 8-bit weights.
+// widened to fp16, and its integer sums stay exact (see kExact there): widened
+// by a pass of their own where there are rows enough to pay for it, on their
+// way through shared memory where the weights' bytes count.  A few rows
+// (decoded tokens) stream the weights straight into matrix fragments.
 #include <algorithm>
 #include <type_traits>
 
@@ -210,15 +211,22 @@ void quant_launch(int M, int K, const void* X, int64_t ldx, int8_t* Q, int64_t l
 
 // ---------------------------------------------------------------- few rows
 
-// Up to kFew rows of one expert against all its channels: a warp takes kChan
-// channels, its lanes 16 codes of each at a time, so every weight is read
-// once, in 16-byte pieces; the rows' codes come from L1.  Bound by the
-// weights' bytes.
-constexpr int kFew = 8, kChan = 2, kFewThreads = 128;
+// Up to 8 NB rows of one expert against its channels, bound by the weights'
+// bytes: a warp owns 16 MT channels and streams their codes from memory
+// straight into matrix fragments.  The order of the reduction is free, so a
+// lane's 16 neighbouring codes of a channel and the same 16 of a row are the
+// operands of four m16n8k16 products, widened to fp16 in registers; up to eight
+// rows they are those of two integer m16n8k32 products as they are (which run
+// at a quarter of the fp16 form's rate here, 151 against 601 Tops, but eight
+// rows need no more, and widening costs 60 of a chunk's 75 instructions).  a.ks warps of a CTA share a channel block's reduction, in
+// turns of 64 terms, where there are few blocks; their sums meet in shared
+// memory.  A warp's fp32 sums go to int32 every 1024 terms, so they are exact.
+
+constexpr long long kFewEnough = 152 * 64;  // warps that keep the memory busy
 
 struct FewArgs {
     const int* offsets;
-    int E, S, N, K;
+    int E, S, N, K, ks;
     const int8_t* Q;
     long long ldq;
     const float* row_scale;
@@ -230,115 +238,238 @@ struct FewArgs {
     spx_type c_type;
 };
 
-template <int R>
-__device__ __forceinline__ void few_rows(const FewArgs& a, int e, int r0, int n0, int (&sum)[kFew][kChan]) {
-    const int lane = threadIdx.x & 31, np = a.K / 16;
-    const int4* w[kChan];
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void few_store(const FewArgs& a, long long i, float v) {
+    if (a.c_type == SPX_F32) static_cast<float*>(a.C)[i] = v;
+    else if (a.c_type == SPX_BF16) static_cast<__nv_bfloat16*>(a.C)[i] = from_f<__nv_bfloat16>(v);
+    else static_cast<__half*>(a.C)[i] = from_f<__half>(v);
+}
+
+template <int NB, int MT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) i8_few_kernel(FewArgs a) {
+    constexpr int TM = 8 * NB, CH = 16 * MT;
+    __shared__ int part[WARPS][TM * CH];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    int e = 0, r0 = blockIdx.y * TM, hi = a.S;
+    if (a.offsets && !warp_find_tile(a.offsets, a.E, a.S, TM, blockIdx.y, e, r0, hi)) return;
+    const int R = min(TM, hi - r0);
+    const int n0 = (blockIdx.x * (WARPS / a.ks) + warp / a.ks) * CH, turn = warp % a.ks;
+    const bool on = n0 < a.N && R > 0;  // the same for the warps that share a block
+    int* mine = part[warp];
 #pragma unroll
-    for (int c = 0; c < kChan; ++c)
-        w[c] = reinterpret_cast<const int4*>(a.W + e * a.stride_w + static_cast<long long>(min(n0 + c, a.N - 1)) * a.ldw);
-    const int4* q = reinterpret_cast<const int4*>(a.Q + r0 * a.ldq);
-    const long long dq = a.ldq / 16;
-    constexpr int U = R <= 2 ? 4 : 2;  // pieces in flight
-    for (int p0 = 0; p0 < np; p0 += 32 * U) {
-        int4 y[U][kChan];
+    for (int i = 0; i < TM * CH / 32; ++i) mine[lane + 32 * i] = 0;
+    __syncwarp();
+    if (on && e < a.E) {
+        const int8_t* w[2 * MT];
+        const int8_t* q[NB];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int m = 0; m < 2 * MT; ++m)
+            w[m] = a.W + e * a.stride_w + static_cast<long long>(min(n0 + 8 * m + g, a.N - 1)) * a.ldw + 16 * t;
 #pragma unroll
-            for (int c = 0; c < kChan; ++c) {
-                const int p = p0 + 32 * u + lane;
-                y[u][c] = p < np ? __ldcs(w[c] + p) : make_int4(0, 0, 0, 0);
+        for (int b = 0; b < NB; ++b) q[b] = a.Q + static_cast<long long>(min(r0 + 8 * b + g, a.S - 1)) * a.ldq + 16 * t;
+        constexpr bool INT = NB == 1;
+        using Acc = typename std::conditional<INT, int, float>::type;
+        Acc acc[MT][NB][4];
+        auto clear = [&]() {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][b][i] = Acc(0);
+        };
+        // value i of (m, b) is channel 16 m + g + 8 (i / 2), row 8 b + 2 t + i % 2
+        auto flush = [&]() {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mine[(8 * b + 2 * t + (i & 1)) * CH + 16 * m + g + 8 * (i >> 1)] += INT ? static_cast<int>(acc[m][b][i]) : __float2int_rn(static_cast<float>(acc[m][b][i]));
+        };
+        constexpr int U = MT * NB > 4 ? 2 : 4;  // chunks of 64 terms whose weights are in flight
+        const int step = 64 * a.ks;
+        int done = 0;
+        clear();
+        for (int k0 = 64 * turn; k0 < a.K; k0 += step * U) {
+            int4 x[U][2 * MT];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * step;
+                const bool in = k + 16 * t < a.K;  // K is a multiple of 16
+#pragma unroll
+                for (int m = 0; m < 2 * MT; ++m)
+                    x[u][m] = in ? __ldcs(reinterpret_cast<const int4*>(w[m] + k)) : make_int4(0, 0, 0, 0);
             }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int p = p0 + 32 * u + lane;
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * step;
+                if (k >= a.K) break;
+                const bool in = k + 16 * t < a.K;
+                if constexpr (INT) {
+                    const int4 y = in ? __ldg(reinterpret_cast<const int4*>(q[0] + k)) : make_int4(0, 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int4 x = p < np ? __ldg(q + r * dq + p) : make_int4(0, 0, 0, 0);
+                    for (int m = 0; m < MT; ++m) {
+                        const int4 &lo = x[u][2 * m], &up = x[u][2 * m + 1];
+                        mma16832(acc[m][0], lo.x, up.x, lo.y, up.y, y.x, y.y);
+                        mma16832(acc[m][0], lo.z, up.z, lo.w, up.w, y.z, y.w);
+                    }
+                    continue;
+                } else {
+                uint2 f[2 * MT][4];
 #pragma unroll
-                for (int c = 0; c < kChan; ++c) {
-                    sum[r][c] = __dp4a(x.x, y[u][c].x, sum[r][c]);
-                    sum[r][c] = __dp4a(x.y, y[u][c].y, sum[r][c]);
-                    sum[r][c] = __dp4a(x.z, y[u][c].z, sum[r][c]);
-                    sum[r][c] = __dp4a(x.w, y[u][c].w, sum[r][c]);
+                for (int m = 0; m < 2 * MT; ++m) {
+                    f[m][0] = widen_codes(x[u][m].x), f[m][1] = widen_codes(x[u][m].y);
+                    f[m][2] = widen_codes(x[u][m].z), f[m][3] = widen_codes(x[u][m].w);
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int4 y = in ? __ldg(reinterpret_cast<const int4*>(q[b] + k)) : make_int4(0, 0, 0, 0);
+                    const uint2 h[4] = {widen_codes(y.x), widen_codes(y.y), widen_codes(y.z), widen_codes(y.w)};
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            mma16816(acc[m][b], f[2 * m][s].x, f[2 * m + 1][s].x, f[2 * m][s].y, f[2 * m + 1][s].y, h[s].x,
+                                     h[s].y);
+                }
+                }
+            }
+            done += 64 * U;
+            if (!INT && done == 1024) {  // U divides 16
+                flush();
+                clear();
+                done = 0;
+            }
+        }
+        flush();
+    }
+    if (a.ks > 1) __syncthreads();
+    else __syncwarp();
+    if (!on) return;
+    // the sharing warps' sums, each warp a part of the rows
+    const int first = warp - turn;
+    for (int i = 32 * turn + lane; i < TM * CH; i += 32 * a.ks) {
+        const int r = i / CH, n = n0 + i % CH;
+        if (r >= R || n >= a.N) continue;
+        int sum = 0;
+        for (int p = 0; p < a.ks; ++p) sum += part[first + p][i];
+        const float v = e < a.E ? static_cast<float>(sum) * (__ldg(a.row_scale + r0 + r) *
+                                                             __ldg(a.col_scale + static_cast<long long>(e) * a.N + n))
+                                : 0.f;
+        few_store(a, (r0 + r) * a.ldc + n, v);
+    }
+}
+
+template <int NB, int MT, int WARPS>
+void few_grid(FewArgs a, long long blocks, long long row_tiles, cudaStream_t st) {
+    const long long per = WARPS / a.ks;
+    i8_few_kernel<NB, MT, WARPS><<<dim3(static_cast<unsigned>((blocks + per - 1) / per), static_cast<unsigned>(row_tiles)),
+                                   32 * WARPS, 0, st>>>(a);
+}
+
+// A block's reduction is shared among warps until there are warps enough for the memory's latency: by the four of a
+// small CTA, or by MOST of a large one where even that leaves few (8 rows x 4096 x 4096: 7.0 us, 8.3 with four).
+template <int NB, int MT, int MOST>
+void few_launch(FewArgs a, long long row_tiles, cudaStream_t st) {
+    const long long blocks = (a.N + 16 * MT - 1) / (16 * MT);
+    const long long tiles = a.E == 1 ? (a.S + 8 * NB - 1) / (8 * NB) : std::min(a.E, a.S);
+    a.ks = 1;
+    while (a.ks < 4 && blocks * tiles * a.ks < kFewEnough && 64 * 2 * a.ks < a.K) a.ks *= 2;
+    while (a.ks >= 4 && a.ks < MOST && blocks * tiles * a.ks < kFewEnough / 4 && 64 * 2 * a.ks < a.K) a.ks *= 2;
+    if (a.ks <= 4) few_grid<NB, MT, 4>(a, blocks, row_tiles, st);
+    else few_grid<NB, MT, MOST>(a, blocks, row_tiles, st);
+}
+
+// One row (blockIdx.y) against its expert's channels, on the CUDA cores' byte
+// dot product: a warp takes kChan channels, its lanes 16 codes of each at a
+// time, so the reduction is split over the lanes and needs no shared memory.
+// One row x 4096 x 4096 4.4 us, 6.4 with matrix fragments; at four rows 8.5 and 7.0.
+constexpr int kRowChan = 2, kRowThreads = 128, kRowMost = 2;
+
+__global__ void __launch_bounds__(kRowThreads) i8_row_kernel(FewArgs a) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int e = 0, p = blockIdx.y, hi = a.S;
+    if (a.offsets && !warp_find_tile(a.offsets, a.E, a.S, 1, blockIdx.y, e, p, hi)) return;
+    const int n0 = (blockIdx.x * (kRowThreads / 32) + warp) * kRowChan, np = a.K / 16;
+    if (n0 >= a.N) return;
+    int sum[kRowChan] = {};
+    if (e < a.E) {
+        const int4* w[kRowChan];
+#pragma unroll
+        for (int c = 0; c < kRowChan; ++c)
+            w[c] = reinterpret_cast<const int4*>(a.W + e * a.stride_w + static_cast<long long>(min(n0 + c, a.N - 1)) * a.ldw);
+        const int4* q = reinterpret_cast<const int4*>(a.Q + p * a.ldq);
+        constexpr int U = 4;  // pieces in flight
+        for (int p0 = lane; p0 < np; p0 += 32 * U) {
+            int4 y[U][kRowChan];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < kRowChan; ++c)
+                    y[u][c] = p0 + 32 * u < np ? __ldcs(w[c] + p0 + 32 * u) : make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int4 x = p0 + 32 * u < np ? __ldg(q + p0 + 32 * u) : make_int4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < kRowChan; ++c) {
+                    sum[c] = __dp4a(x.x, y[u][c].x, sum[c]);
+                    sum[c] = __dp4a(x.y, y[u][c].y, sum[c]);
+                    sum[c] = __dp4a(x.z, y[u][c].z, sum[c]);
+                    sum[c] = __dp4a(x.w, y[u][c].w, sum[c]);
                 }
             }
         }
     }
+#pragma unroll
+    for (int c = 0; c < kRowChan; ++c) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], d);
+        if (lane == c && n0 + c < a.N)
+            few_store(a, p * a.ldc + n0 + c,
+                      e < a.E ? static_cast<float>(sum[c]) *
+                                    (__ldg(a.row_scale + p) * __ldg(a.col_scale + static_cast<long long>(e) * a.N + n0 + c))
+                              : 0.f);
+    }
 }
 
-template <class O>
-__device__ __forceinline__ void few_store(const FewArgs& a, long long i, float v) {
-    static_cast<O*>(a.C)[i] = from_f<O>(v);
-}
-
-__global__ void __launch_bounds__(kFewThreads) i8_few_kernel(FewArgs a) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int e = 0, r0 = 0, hi = a.S;
-    if (a.offsets) {
-        if (!warp_find_tile(a.offsets, a.E, a.S, kFew, blockIdx.y, e, r0, hi)) return;
-    } else {
-        r0 = blockIdx.y * kFew;
+// Row tiles of 8, 16 or 32 rows, by an expert's average: most experts are one tile.
+spx_status few_product(const FewArgs& a, cudaStream_t st) {
+    if (a.S <= kRowMost) {
+        constexpr int per = kRowThreads / 32 * kRowChan;
+        i8_row_kernel<<<dim3((a.N + per - 1) / per, a.S), kRowThreads, 0, st>>>(a);
+        spx_note_launches(1);
+        return spx_cuda_status(cudaGetLastError());
     }
-    const int R = min(kFew, hi - r0);
-    const int n0 = (blockIdx.x * (kFewThreads / 32) + warp) * kChan;
-    if (n0 >= a.N || R <= 0) return;
-    int sum[kFew][kChan];
-#pragma unroll
-    for (int r = 0; r < kFew; ++r)
-#pragma unroll
-        for (int c = 0; c < kChan; ++c) sum[r][c] = 0;
-    if (e < a.E) {
-        if (R == 1) few_rows<1>(a, e, r0, n0, sum);
-        else if (R == 2) few_rows<2>(a, e, r0, n0, sum);
-        else if (R <= 4) {
-            if (R == 3) few_rows<3>(a, e, r0, n0, sum);
-            else few_rows<4>(a, e, r0, n0, sum);
-        } else {
-            switch (R) {
-                case 5: few_rows<5>(a, e, r0, n0, sum); break;
-                case 6: few_rows<6>(a, e, r0, n0, sum); break;
-                case 7: few_rows<7>(a, e, r0, n0, sum); break;
-                default: few_rows<8>(a, e, r0, n0, sum);
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < kFew; ++r) {
-        if (r >= R) break;
-#pragma unroll
-        for (int c = 0; c < kChan; ++c)
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum[r][c] += __shfl_xor_sync(0xffffffffu, sum[r][c], d);
-    }
-    // lane r * kChan + c stores row r of channel n0 + c
-#pragma unroll
-    for (int r = 0; r < kFew; ++r)
-#pragma unroll
-        for (int c = 0; c < kChan; ++c) {
-            if (lane != r * kChan + c || r >= R || n0 + c >= a.N) continue;
-            const float v = e < a.E ? static_cast<float>(sum[r][c]) *
-                                          (__ldg(a.row_scale + r0 + r) * __ldg(a.col_scale + static_cast<long long>(e) * a.N + n0 + c))
-                                    : 0.f;
-            const long long i = (r0 + r) * a.ldc + n0 + c;
-            if (a.c_type == SPX_F32) few_store<float>(a, i, v);
-            else if (a.c_type == SPX_BF16) few_store<__nv_bfloat16>(a, i, v);
-            else few_store<__half>(a, i, v);
-        }
+    const long long avg = (a.S + a.E - 1) / a.E, most = a.E == 1 ? avg : 3 * avg / 2;
+    const int nb = most <= 8 ? 1 : most <= 16 ? 2 : 4;
+    const long long ty = a.offsets ? std::min<long long>(max_row_tiles(a.E, a.S, 8 * nb), static_cast<long long>(a.S) + 1)
+                                   : (a.S + 8 * nb - 1) / (8 * nb);
+    if (ty > 65535) return SPX_ERR_UNSUPPORTED;
+    if (nb == 1) few_launch<1, 1, 16>(a, ty, st);
+    else if (nb == 2) few_launch<2, 1, 16>(a, ty, st);
+    else few_launch<4, 2, 8>(a, ty, st);
+    spx_note_launches(1);
+    return spx_cuda_status(cudaGetLastError());
 }
 
 // ---------------------------------------------------------------- codes to fp16
-
-// Four codes (bytes of w) to fp16: 0x6400 | u is 1024 + u for a byte u, and
-// u = code + 128 after flipping its top bit, so one subtraction is exact.
-__device__ __forceinline__ uint2 widen_codes(uint32_t w) {
-    w ^= 0x80808080u;
-    const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
-    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
-    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
-    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
-    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
 
 // The rows of Q and of every expert that has rows, as fp16 with a row pitch of
 // Kp (a multiple of 8) values; what lies between K and Kp is never read.
@@ -395,18 +526,15 @@ __global__ void __launch_bounds__(kWidenThreads)
     }
 }
 
-// The few-rows kernel is taken up to kFewEach rows an expert on average and
-// kFewMore in all besides: 64 experts of 2048 x 2048, 64 rows 41 us (146 through
-// 16-bit codes), 512 rows 141 (219), 1024 rows 244 (215); one of 4096 x 4096, 16
-// rows 14 us (22), 32 rows 24 (22).
-constexpr int kFewEach = 8, kFewMore = 8;
+// Which kernel, by an expert's average rows (us, few rows / widened on the way / through widened copies):
+//   64 experts of 2048 x 2048: 4 rows 50/108/197, 16 rows 101/110/211, 64 rows -/134/219
+//   8 of 4096 x 2048: 8 rows 26/36/56, 32 rows 50/39/58, 128 rows 133/66/65
+//   one of 4096 x 4096: 16 rows 8/14/17, 32 rows 14/15/18, 64 rows 16/16/18, 128 rows 28/18/20
+constexpr int kFewRows = 16, kWidenRows = 128;
+
+int64_t avg_rows(int E, int S) { return (static_cast<int64_t>(S) + E - 1) / E; }
 
 int pitch16(int K) { return (K + 7) / 8 * 8; }
-
-bool few_fits(int E, int S, const int8_t* Q, int64_t ldq, const int8_t* W, int64_t ldw, int64_t stride_w, int K) {
-    return S <= kFewEach * static_cast<int64_t>(E) + kFewMore && K % 16 == 0 && spx_aligned(Q, 16) && spx_aligned(W, 16) && ldq % 16 == 0 && ldw % 16 == 0 &&
-           stride_w % 16 == 0;
-}
 
 }  // namespace
 
@@ -426,8 +554,8 @@ spx_status spx_quant_rows_i8(int32_t M, int32_t K, spx_type type, const void* X,
     return spx_cuda_status(cudaGetLastError());
 }
 
-size_t spx_gemm_i8_scratch_bytes(int32_t E, int32_t S, int32_t N, int32_t K) {
-    if (E <= 0 || S <= 0 || N <= 0 || K <= 0) return 0;
+size_t spx_gemm_i8_scratch_bytes(int32_t E, int32_t S, int32_t N, int32_t K, int32_t wide) {
+    if (E <= 0 || S <= 0 || N <= 0 || K <= 0 || (wide && avg_rows(E, S) <= kWidenRows)) return 0;
     const size_t row = 2 * static_cast<size_t>(pitch16(K));
     const size_t q = (row * S + 255) / 256 * 256;
     return q + row * N * static_cast<size_t>(E);
@@ -451,15 +579,13 @@ spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t
     if (K == 0)
         return spx_cuda_status(cudaMemset2DAsync(C, static_cast<size_t>(ldc) * cb, 0, static_cast<size_t>(N) * cb,
                                                  static_cast<size_t>(S), st));
-    if (few_fits(E, S, Q, ldq, W, ldw, stride_w, K)) {
-        const FewArgs a{offsets, E, S, N, K, Q, ldq, row_scale, W, ldw, stride_w, w_scale, C, ldc, c_type};
-        const long long ty = offsets ? std::min<long long>(max_row_tiles(E, S, kFew), static_cast<long long>(S) + 1) : (S + kFew - 1) / kFew;
-        i8_few_kernel<<<dim3((N + kFewThreads / 32 * kChan - 1) / (kFewThreads / 32 * kChan), static_cast<unsigned>(ty)),
-                        kFewThreads, 0, st>>>(a);
-        spx_note_launches(1);
-        return spx_cuda_status(cudaGetLastError());
-    }
-    const size_t need = spx_gemm_i8_scratch_bytes(E, S, N, K);
+    const int64_t rows = avg_rows(E, S);
+    const bool wide = tc_codes_fit(Q, ldq, W, ldw, stride_w);  // rows on 16-byte boundaries
+    if (wide && K % 16 == 0 && rows <= kFewRows)
+        return few_product(FewArgs{offsets, E, S, N, K, 1, Q, ldq, row_scale, W, ldw, stride_w, w_scale, C, ldc, c_type}, st);
+    if (wide && rows <= kWidenRows)
+        return tc_product_codes(E, S, N, K, offsets, Q, ldq, row_scale, W, ldw, stride_w, w_scale, C, ldc, c_type, st);
+    const size_t need = spx_gemm_i8_scratch_bytes(E, S, N, K, wide);
     if (need > 0 && (!scratch || scratch_bytes < need)) return SPX_ERR_ARG;
     if (need > 0 && !spx_aligned(scratch, 256)) return SPX_ERR_ALIGN;
     const bool same_w = E == 1 || stride_w == 0;

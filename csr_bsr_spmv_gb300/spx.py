@@ -198,7 +198,7 @@ def _load(path):
         "spx_gemm_grouped_wgrad": ([i32, i32, i32, i32, vp, vp, i64, vp, i64, ctypes.c_int, vp, i64, i64, ctypes.c_int,
                                     vp], ctypes.c_int),
         "spx_quant_rows_i8": ([i32, i32, ctypes.c_int, vp, i64, vp, i64, vp, vp], ctypes.c_int),
-        "spx_gemm_i8_scratch_bytes": ([i32, i32, i32, i32], sz),
+        "spx_gemm_i8_scratch_bytes": ([i32, i32, i32, i32, i32], sz),
         "spx_gemm_i8": ([i32, i32, i32, i32, vp, vp, i64, vp, vp, i64, i64, vp, vp, i64, ctypes.c_int, vp, sz, vp],
                         ctypes.c_int),
         "spx_gather_probe_blocks": ([], ctypes.c_int32),
@@ -1069,7 +1069,7 @@ def spx_gemm_i8(Q: torch.Tensor, row_scale: torch.Tensor, W: torch.Tensor, w_sca
     rs, ws = _vec(row_scale, S, torch.float32, "row_scale"), _vec(w_scale, E * N, torch.float32, "w_scale")
     C, ldc, c = _out(C, S, N, (dtype or torch.float32) if C is None else dtype, Q, "C", stream)
     lib = _lib()
-    need = lib.spx_gemm_i8_scratch_bytes(E, S, N, K)
+    need = lib.spx_gemm_i8_scratch_bytes(E, S, N, K, ((q or 0) | (w or 0) | ldq | ldw | sw) % 16 == 0)
     if need and scratch is None:
         scratch = _new(need, torch.uint8, Q, stream)
     _check(lib.spx_gemm_i8(E, S, N, K, _vec(offsets, E + 1, torch.int32, "offsets") if offsets is not None else None,

@@ -899,13 +899,15 @@ spx_status spx_quant_rows_i8(int32_t M, int32_t K, spx_type type, const void* X,
  * are applied in fp32, C holds SPX_F32, SPX_BF16 or SPX_F16 and is rounded
  * once; zeros in the rows from offsets[E] on.  Q is S x K (ldq), W_e starts
  * at W + e * stride_w, N rows of K, ldw apart.
- *   scratch: spx_gemm_i8_scratch_bytes(E, S, N, K) bytes, 256-byte aligned
- *     (may be NULL when that is 0): the codes as 16-bit floats, which hold them
- *     exactly.  S <= 8 with rows on 16-byte boundaries runs without it.
+ *   scratch: spx_gemm_i8_scratch_bytes(E, S, N, K, wide) bytes, 256-byte
+ *     aligned (may be NULL when that is 0): the codes as 16-bit floats, which
+ *     hold them exactly.  wide: not 0 when Q and W and their rows (ldq, ldw,
+ *     stride_w) lie on 16-byte boundaries; none is needed then up to 128 rows an
+ *     expert on average.
  * K == 0 gives zeros.  Launches: 1 or 2.
  */
 #define SPX_I8_MAX_K 131071
-size_t spx_gemm_i8_scratch_bytes(int32_t E, int32_t S, int32_t N, int32_t K);
+size_t spx_gemm_i8_scratch_bytes(int32_t E, int32_t S, int32_t N, int32_t K, int32_t wide);
 spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const int8_t* Q,
                        int64_t ldq, const float* row_scale, const int8_t* W, int64_t ldw, int64_t stride_w,
                        const float* w_scale, void* C, int64_t ldc, spx_type c_type, void* scratch,

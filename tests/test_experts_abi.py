@@ -163,3 +163,12 @@ def test_binding_refuses_layouts_and_host_tensors():
             call()
     with pytest.raises(TypeError):
         spx._type(torch.zeros(2, dtype=torch.float64))
+
+
+def test_gemm_i8_scratch_bytes():
+    lib = spx._lib()
+    assert lib.spx_gemm_i8_scratch_bytes(8, 0, 64, 64, 0) == 0
+    assert lib.spx_gemm_i8_scratch_bytes(8, 8 * 128, 64, 64, 1) == 0       # wide rows, few an expert
+    assert lib.spx_gemm_i8_scratch_bytes(8, 8 * 128, 64, 64, 0) == 2 * 64 * (8 * 128 + 8 * 64)
+    assert lib.spx_gemm_i8_scratch_bytes(8, 8 * 128 + 1, 64, 57, 1) == (2 * 64 * (8 * 128 + 1) + 255) // 256 * 256 + 2 * 64 * 8 * 64
+    assert lib.spx_gemm_i8_scratch_bytes(2048, 1 << 20, 1 << 14, 1 << 14, 1) > 1 << 40  # past 32 bits
