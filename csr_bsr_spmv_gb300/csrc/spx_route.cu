@@ -3,11 +3,15 @@
 // gradients of the return.
 //
 // The sort is a stable counting sort with E buckets.  Each warp owns a run of
-// consecutive slots: it counts them per expert (match_any finds the lanes of
-// one expert, one lane adds their number to the warp's own counters), the
-// counters of all warps before it give its first places, and a second pass
-// over the same slots hands them out in order.  Nothing is atomic, so places
-// do not depend on timing.
+// consecutive slots, whose ids its lanes hold in registers: the warp counts them
+// per expert (match_any finds the lanes of one expert, one lane adds their
+// number to the warp's own counters), which also gives every slot its rank in
+// the run; the counters of all warps before it give the run's first places.
+// Nothing is atomic but integer sums, so places do not depend on timing.  Up to
+// 2048 slots are one CTA, up to 16384 a cluster of CTAs that read each other's
+// counts in shared memory; more take a counting launch first.  (More slots a
+// CTA take longer: their scattered writes to `slot` pass one SM.)  Bound by
+// latency: 8 slots LAT1 us, 3711 LAT2, 65536 LAT3.
 //
 // Gather, return and gradient are bound by HBM: every row is one contiguous
 // copy.  All three are driven by the token, not by the sorted place: a token's
@@ -41,71 +45,125 @@ __device__ __forceinline__ int id_of(const Ids& x, int i, int E) {
     return e >= 0 && e < E ? static_cast<int>(e) : -1;
 }
 
-// This warp's run of the block's slots [b0, b1): whole groups of 32 lanes.
-__device__ __forceinline__ void warp_run(int b0, int b1, int& w0, int& w1) {
-    const int nw = blockDim.x >> 5, w = threadIdx.x >> 5;
-    const int per = ((b1 - b0 + 32 * nw - 1) / (32 * nw)) * 32;
-    w0 = min(b0 + w * per, b1);
-    w1 = min(w0 + per, b1);
-}
+constexpr int kHeld = 4;              // ids a lane holds
+constexpr int kRun = 32 * kHeld;      // slots of a warp
+constexpr int kMostWarps = 16, kMostCluster = 8, kMaxBlocks = 304;
 
-// counts[w][e] = slots of expert e in warp w's run.
-__device__ __forceinline__ void count_run(const Ids& x, int E, int w0, int w1, int* wc) {
+// Ids of this warp's run, -1 past the end and for dropped slots; done[w][e] = slots of expert e in the run; rank[i] =
+// those before this lane's i-th.  Slot i of a lane is w0 + 32 i + lane.
+__device__ __forceinline__ void rank_run(const Ids& x, int E, int w0, int end, int (&id)[kHeld], int (&rank)[kHeld],
+                                         int* done) {
     const int lane = threadIdx.x & 31;
-    for (int i = w0 + lane; i - lane < w1; i += 32) {
-        const int e = i < w1 ? id_of(x, i, E) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(same) - 1) wc[e] += __popc(same);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) id[i] = w0 + 32 * i + lane < end ? id_of(x, w0 + 32 * i + lane, E) : -1;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        if (w0 + 32 * i >= end) break;
+        const unsigned same = __match_any_sync(0xffffffffu, id[i]);
+        const unsigned before = same & ((1u << lane) - 1u);
+        if (id[i] >= 0) rank[i] = done[id[i]] + __popc(before);
+        __syncwarp();
+        if (id[i] >= 0 && before == 0) done[id[i]] += __popc(same);
         __syncwarp();
     }
 }
 
-__global__ void route_count_kernel(Ids x, int S, int E, int per, int* __restrict__ hist) {
+// The block's slots of each expert, for the sort of more slots than a cluster holds.
+__global__ void __launch_bounds__(32 * kMostWarps)
+    route_count_kernel(Ids x, int S, int E, int runs, int* __restrict__ hist) {
     extern __shared__ int sm[];
-    const int nw = blockDim.x >> 5, w = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < nw * E; i += blockDim.x) sm[i] = 0;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) sm[e] = 0;
     __syncthreads();
-    const int b0 = blockIdx.x * per, b1 = min(S, b0 + per);
-    int w0, w1;
-    warp_run(b0, b1, w0, w1);
-    count_run(x, E, w0, w1, sm + w * E);
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int n = 0;
-        for (int v = 0; v < nw; ++v) n += sm[v * E + e];
-        hist[blockIdx.x * E + e] = n;
+    const int per = runs * blockDim.x * kHeld, b0 = blockIdx.x * per, b1 = min(S, b0 + per);
+    for (int i = b0 + threadIdx.x; i < b1; i += blockDim.x) {
+        const int e = id_of(x, i, E);
+        if (e >= 0) atomicAdd(sm + e, 1);
     }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[blockIdx.x * E + e] = sm[e];
 }
 
-// hist == NULL: one block holds all slots.
-__global__ void route_place_kernel(Ids x, int S, int E, int per, const int* __restrict__ hist,
-                                   int* __restrict__ offsets, int* __restrict__ slot, int* __restrict__ pos) {
-    extern __shared__ int sm[];  // counters of each warp, then E totals
-    const int nw = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int* tot = sm + nw * E;
-    for (int i = threadIdx.x; i < nw * E; i += blockDim.x) sm[i] = 0;
+// A block places `runs` rounds of blockDim.x * kHeld consecutive slots.  The other blocks' counts come from `hist`
+// (counted before, any number of blocks), or (hist NULL) from the other CTAs of the cluster that the grid is.
+__global__ void __launch_bounds__(32 * kMostWarps)
+    route_place_kernel(Ids x, int S, int E, int runs, const int* __restrict__ hist, int* __restrict__ offsets,
+                       int* __restrict__ slot, int* __restrict__ pos) {
+    extern __shared__ int sm[];  // counters of each warp (ES apart), E + 1 totals, E places before this block, E counts of it
+    const int nw = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = gridDim.x, b = blockIdx.x;
+    const int ES = E | 1;  // odd: a column of the counters touches every bank
+    int *tot = sm + nw * ES, *before = tot + E + 1, *own = before + E;
+    for (int i = threadIdx.x; i < nw * ES + 3 * E + 1; i += blockDim.x) sm[i] = 0;
     __syncthreads();
-    const int b0 = blockIdx.x * per, b1 = min(S, b0 + per);
-    int w0, w1;
-    warp_run(b0, b1, w0, w1);
-    count_run(x, E, w0, w1, sm + w * E);
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int before = 0, all = 0;  // the expert's slots in earlier blocks, in all blocks
-        if (hist) {
-            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-                const int n = __ldg(hist + b * E + e);
-                if (b < static_cast<int>(blockIdx.x)) before += n;
+    const int per = runs * blockDim.x * kHeld, b0 = b * per, b1 = min(S, b0 + per);
+    int id[kHeld], rank[kHeld];
+    // the warps' counters of a round become places within it; the round's counts go to `own`
+    auto scan_warps = [&]() {
+        __syncthreads();
+        if (nw <= 4) {  // a thread an expert
+            for (int e = threadIdx.x; e < E; e += blockDim.x) {
+                int sum = 0;
+                for (int v = 0; v < nw; ++v) {
+                    const int n = sm[v * ES + e];
+                    sm[v * ES + e] = sum;
+                    sum += n;
+                }
+                own[e] = sum;
+            }
+            __syncthreads();
+            return;
+        }
+        for (int e = w; e < E; e += nw) {  // a warp an expert
+            const int n = lane < nw ? sm[lane * ES + e] : 0;
+            int inc = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += up;
+            }
+            if (lane < nw) sm[lane * ES + e] = inc - n;
+            if (lane == 31) own[e] = inc;
+        }
+        __syncthreads();
+    };
+    if (runs == 1) {
+        rank_run(x, E, b0 + w * kRun, b1, id, rank, sm + w * ES);
+        scan_warps();
+    }
+    if (hist) {  // all blocks' counts: thread i takes expert i % E of every (blockDim.x / E)-th block
+        const int parts = max(1, static_cast<int>(blockDim.x) / E);
+        for (int i = threadIdx.x; i < E * parts; i += blockDim.x) {
+            const int e = i % E;
+            int all = 0, lower = 0;
+#pragma unroll 4
+            for (int o = i / E; o < nb; o += parts) {
+                const int n = __ldg(hist + static_cast<long long>(o) * E + e);
                 all += n;
+                lower += o < b ? n : 0;
+            }
+            atomicAdd(tot + e, all);
+            atomicAdd(before + e, lower);
+        }
+    } else {
+        if (nb == 1) {
+            for (int e = threadIdx.x; e < E; e += blockDim.x) tot[e] = own[e];
+        } else {
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            for (int e = threadIdx.x; e < E; e += blockDim.x) {
+                int all = 0, lower = 0;
+                for (int o = 0; o < nb; ++o) {
+                    uint32_t there;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                                 : "=r"(there)
+                                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(own + e))), "r"(o));
+                    int n;
+                    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(n) : "r"(there) : "memory");
+                    all += n;
+                    lower += o < b ? n : 0;
+                }
+                tot[e] = all;
+                before[e] = lower;
             }
         }
-        int run = before;
-        for (int v = 0; v < nw; ++v) {
-            const int n = sm[v * E + e];
-            sm[v * E + e] = run;
-            run += n;
-        }
-        tot[e] = hist ? all : run;
     }
     __syncthreads();
     if (w == 0) {  // totals -> offsets
@@ -119,42 +177,63 @@ __global__ void route_place_kernel(Ids x, int S, int E, int per, const int* __re
                 if (lane >= d) inc += up;
             }
             if (e0 + lane < E) {
-                tot[e0 + lane] = carry + inc - n;
-                if (blockIdx.x == 0) offsets[e0 + lane] = carry + inc - n;
+                before[e0 + lane] += carry + inc - n;
+                if (b == 0) offsets[e0 + lane] = carry + inc - n;
             }
             carry += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (lane == 0) {
             tot[E] = carry;
-            if (blockIdx.x == 0) offsets[E] = carry;
+            if (b == 0) offsets[E] = carry;
         }
     }
     __syncthreads();
-    int* wc = sm + w * E;
-    for (int i = w0 + lane; i - lane < w1; i += 32) {
-        const int e = i < w1 ? id_of(x, i, E) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        int p = -1;
-        if (e >= 0) p = tot[e] + wc[e] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(same) - 1) wc[e] += __popc(same);
-        __syncwarp();
-        if (i < w1) {
-            pos[i] = p;
-            if (p >= 0) slot[p] = i;
+    for (int round = 0; round < runs; ++round) {
+        const int w0 = b0 + (round * nw + w) * kRun;
+        if (runs > 1) {
+            for (int i = threadIdx.x; i < nw * ES; i += blockDim.x) sm[i] = 0;
+            __syncthreads();
+            rank_run(x, E, w0, b1, id, rank, sm + w * ES);
+            scan_warps();
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int at = w0 + 32 * i + lane;
+            if (at >= b1) break;
+            const int p = id[i] >= 0 ? before[id[i]] + sm[w * ES + id[i]] + rank[i] : -1;
+            pos[at] = p;
+            if (p >= 0) slot[p] = at;
+        }
+        if (runs > 1) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < E; e += blockDim.x) before[e] += own[e];
         }
     }
-    for (int p = tot[E] + blockIdx.x * blockDim.x + threadIdx.x; p < S; p += gridDim.x * blockDim.x) slot[p] = -1;
+    for (int p = tot[E] + b * blockDim.x + threadIdx.x; p < S; p += nb * blockDim.x) slot[p] = -1;
+    if (!hist && nb > 1)  // nobody leaves while its counts may be read
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One CTA sorts up to this many slots; beyond, a counting launch comes first
-// and each CTA takes a share.
-constexpr int kOneBlockSlots = 8192;
-constexpr int kMaxBlocks = 304;
-
-int route_blocks(long long S) {
-    if (S <= kOneBlockSlots) return 1;
-    return static_cast<int>(std::min<long long>((S + 4095) / 4096, kMaxBlocks));
+// Warps a CTA, CTAs and rounds for S slots: the warps' counters fit 48 KB.
+struct SortShape {
+    int warps, blocks, runs;
+    bool counted;  // a counting launch comes first
+    size_t smem;
+};
+SortShape sort_shape(long long S, int E) {
+    SortShape r{};
+    r.warps = 1;
+    while (r.warps < kMostWarps && static_cast<long long>(r.warps) * kRun < S && (2 * r.warps + 3) * (E + 2) * 4 <= 48 * 1024)
+        r.warps *= 2;
+    const long long one = static_cast<long long>(r.warps) * kRun;
+    const long long blocks = std::max(1LL, (S + one - 1) / one);
+    r.counted = blocks > kMostCluster;
+    r.runs = r.counted ? static_cast<int>((blocks + kMaxBlocks - 1) / kMaxBlocks) : 1;
+    r.blocks = static_cast<int>((blocks + r.runs - 1) / r.runs);
+    if (!r.counted)
+        while (r.blocks & (r.blocks - 1)) ++r.blocks;  // a cluster of 1, 2, 4 or 8
+    r.smem = sizeof(int) * (static_cast<size_t>(r.warps) * (E | 1) + 3 * static_cast<size_t>(E) + 1);
+    return r;
 }
 
 // ---------------------------------------------------------------- rows in pieces of VB bytes
@@ -460,8 +539,8 @@ extern "C" {
 
 size_t spx_route_scratch_bytes(int32_t T, int32_t k, int32_t E) {
     if (T < 0 || k <= 0 || E <= 0) return 0;
-    const int nb = route_blocks(static_cast<int64_t>(T) * k);
-    return nb == 1 ? 0 : sizeof(int32_t) * static_cast<size_t>(nb) * static_cast<size_t>(E);
+    const SortShape h = sort_shape(static_cast<int64_t>(T) * k, E);
+    return h.counted ? sizeof(int32_t) * static_cast<size_t>(h.blocks) * static_cast<size_t>(E) : 0;
 }
 
 spx_status spx_route_build(int32_t T, int32_t k, int32_t E, const void* expert, int32_t id_bytes, int64_t lde,
@@ -470,27 +549,35 @@ spx_status spx_route_build(int32_t T, int32_t k, int32_t E, const void* expert, 
     if (T < 0 || k <= 0 || E <= 0 || (id_bytes != 4 && id_bytes != 8)) return SPX_ERR_ARG;
     if (E > SPX_MAX_EXPERTS) return SPX_ERR_UNSUPPORTED;
     const int64_t S64 = static_cast<int64_t>(T) * k;
-    if (S64 > kI32Max - 1024) return SPX_ERR_INDEX_RANGE;  // the kernels step past the end by up to a CTA
+    if (S64 > kI32Max - (1 << 23)) return SPX_ERR_INDEX_RANGE;  // the kernels step past the end by up to a CTA's slots
     if (!offsets || (S64 > 0 && (!expert || !slot || !pos || lde < k))) return SPX_ERR_ARG;
     if (!spx_aligned(offsets, 4) || !spx_aligned(slot, 4) || !spx_aligned(pos, 4) ||
         !spx_aligned(expert, static_cast<size_t>(id_bytes)))
         return SPX_ERR_ALIGN;
-    const int S = static_cast<int>(S64), nb = route_blocks(S64);
+    const int S = static_cast<int>(S64);
+    const SortShape h = sort_shape(S64, E);
     const size_t need = spx_route_scratch_bytes(T, k, E);
     if (need > 0 && (!scratch || scratch_bytes < need)) return SPX_ERR_ARG;
     if (need > 0 && !spx_aligned(scratch, 4)) return SPX_ERR_ALIGN;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const Ids ids{expert, lde, k, id_bytes};
-    // warps a CTA: one for each 32 slots, as far as their counters fit 48 KB
-    const int per = nb == 1 ? S : static_cast<int>((S64 + nb - 1) / nb);
-    int nw = 1;
-    while (nw < 32 && 32 * nw < per && (2 * nw + 1) * (E + 1) * 4 <= 48 * 1024) nw *= 2;
-    const size_t smem = sizeof(int32_t) * (static_cast<size_t>(nw) * E + E + 1);
-    if (nb > 1) route_count_kernel<<<nb, 32 * nw, smem, st>>>(ids, S, E, per, static_cast<int*>(scratch));
-    route_place_kernel<<<nb, 32 * nw, smem, st>>>(ids, S, E, per, nb > 1 ? static_cast<const int*>(scratch) : nullptr,
-                                                  offsets, slot, pos);
-    spx_note_launches(nb > 1 ? 2 : 1);
-    return spx_cuda_status(cudaGetLastError());
+    int* hist = h.counted ? static_cast<int*>(scratch) : nullptr;
+    if (h.counted) route_count_kernel<<<h.blocks, 32 * h.warps, sizeof(int) * E, st>>>(ids, S, E, h.runs, hist);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(h.blocks);
+    cfg.blockDim = dim3(32 * h.warps);
+    cfg.dynamicSmemBytes = h.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(h.blocks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = !h.counted && h.blocks > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, route_place_kernel, ids, S, E, h.runs, static_cast<const int*>(hist),
+                                             offsets, slot, pos);
+    spx_note_launches(h.counted ? 2 : 1);
+    return spx_cuda_status(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 spx_status spx_route_gather(int32_t T, int32_t k, int32_t H, spx_type type, const int32_t* pos,

@@ -804,8 +804,8 @@ typedef enum spx_type {
  *   expert: T x k ids, id_bytes 4 (int32) or 8 (int64) each, row t at
  *     expert + t * lde elements (lde >= k).
  *   scratch: spx_route_scratch_bytes(T, k, E) bytes (may be 0), 4-byte aligned.
- * T * k must fit int32 (SPX_ERR_INDEX_RANGE).  Launches: 1, or 2 for more
- * slots than one CTA sorts well.
+ * T * k may be up to 2^31 - 2^23 - 1 (SPX_ERR_INDEX_RANGE).  Launches: 1, or 2
+ * for more slots than a cluster of CTAs holds (16384, fewer with hundreds of experts).
  */
 size_t spx_route_scratch_bytes(int32_t T, int32_t k, int32_t E);
 spx_status spx_route_build(int32_t T, int32_t k, int32_t E, const void* expert, int32_t id_bytes, int64_t lde,
