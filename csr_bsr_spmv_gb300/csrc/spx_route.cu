@@ -11,7 +11,7 @@
 // 2048 slots are one CTA, up to 16384 a cluster of CTAs that read each other's
 // counts in shared memory; more take a counting launch first.  (More slots a
 // CTA take longer: their scattered writes to `slot` pass one SM.)  Bound by
-// latency: 8 slots LAT1 us, 3711 LAT2, 65536 LAT3.
+// latency: 8 slots 3.0 us, 3711 6.3, 65536 8.8.
 //
 // Gather, return and gradient are bound by HBM: every row is one contiguous
 // copy.  All three are driven by the token, not by the sorted place: a token's
@@ -252,17 +252,6 @@ template <>
 struct Piece<2> {
     using T = uint16_t;
 };
-template <>
-struct Piece<1> {
-    using T = uint8_t;
-};
-
-template <class P>
-__device__ __forceinline__ P zero_piece() {
-    P z;
-    memset(&z, 0, sizeof(P));
-    return z;
-}
 
 // The values of one piece as floats, and back (rounded once each).
 template <class V, class P>
@@ -285,7 +274,7 @@ __device__ __forceinline__ P narrow(const float (&f)[sizeof(P) / sizeof(V)]) {
 constexpr int kRowThreads = 256;
 
 // A group of G threads (G divides 256) works on one token; grid.y splits the
-// row among groups when there are few tokens.
+// row among groups when there are few tokens.  Pieces are values in the gather.
 struct RowShape {
     int T, k, np, G;           // tokens, slots a token, pieces a row, threads a group
     long long a, b;            // row pitch in pieces of the token-ordered and of the sorted array
@@ -301,26 +290,74 @@ template <class P>
 __device__ __forceinline__ void zero_tail(const RowShape& r, const int* __restrict__ end, int t, int v0, int dv, P* out) {
     const int S = r.T * r.k;
     for (long long p = min(max(__ldg(end), 0), S) + static_cast<long long>(t); p < S; p += r.T)
-        for (int v = v0; v < r.np; v += dv) out[p * r.b + v] = zero_piece<P>();
+        for (int v = v0; v < r.np; v += dv) memset(out + p * r.b + v, 0, sizeof(P));
 }
 
-template <int VB>
+// The 16 bytes at p (aligned to the element) out of the two aligned pieces
+// around them, or value by value where those would leave the array [lo, hi).
+template <class V>
+__device__ __forceinline__ uint4 read16(const char* p, const char* lo, const char* hi) {
+    const int m = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    const char* at = p - m;
+    if (m == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+    if (at < lo || at + 32 > hi) {
+        V v[16 / sizeof(V)];
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(16 / sizeof(V)); ++i) v[i] = reinterpret_cast<const V*>(p)[i];
+        uint4 w;
+        memcpy(&w, v, 16);
+        return w;
+    }
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(at)), y = __ldg(reinterpret_cast<const uint4*>(at) + 1);
+    const bool two = m & 8, one = m & 4;
+    const uint32_t t0 = two ? x.z : x.x, t1 = two ? x.w : x.y, t2 = two ? y.x : x.z, t3 = two ? y.y : x.w,
+                   t4 = two ? y.z : y.x, t5 = two ? y.w : y.y;
+    const uint32_t u0 = one ? t1 : t0, u1 = one ? t2 : t1, u2 = one ? t3 : t2, u3 = one ? t4 : t3, u4 = one ? t5 : t4;
+    const int sh = (m & 3) * 8;
+    return make_uint4(__funnelshift_r(u0, u1, sh), __funnelshift_r(u1, u2, sh), __funnelshift_r(u2, u3, sh),
+                      __funnelshift_r(u3, u4, sh));
+}
+
+// V: the copied values' type, or any of their size.  Rows off 16-byte
+// boundaries: each written row is cut at its own boundaries -- a head of single
+// values, aligned pieces, a tail -- so that wide stores fill whole sectors, and
+// the token's row, which L1 holds, is read around them (96008 rows of 4095 fp32:
+// 295 us, 438 with 4-byte stores where they fall).
+template <class V, bool ALIGNED>
 __global__ void __launch_bounds__(kRowThreads)
-    route_gather_kernel(RowShape r, const int* __restrict__ pos, const int* __restrict__ end,
-                        const typename Piece<VB>::T* __restrict__ X, typename Piece<VB>::T* __restrict__ Xs) {
-    using P = typename Piece<VB>::T;
+    route_gather_kernel(RowShape r, const int* __restrict__ pos, const int* __restrict__ end, const V* __restrict__ X,
+                        V* __restrict__ Xs) {
     const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
     if (t >= r.T) return;
     const int S = r.T * r.k, v0 = blockIdx.y * r.G + threadIdx.x % r.G, dv = gridDim.y * r.G;
-    const P* x = X + t * r.a;
-    for (int v = v0; v < r.np; v += dv) {
-        const P piece = __ldg(x + v);
+    const long long i0 = static_cast<long long>(t) * r.k;
+    constexpr int N = 16 / sizeof(V);
+    const V* x = X + t * r.a;
+    if (ALIGNED) {
+        for (int v = v0; v < r.np / N; v += dv) {
+            const uint4 piece = __ldg(reinterpret_cast<const uint4*>(x) + v);
+            for (int j = 0; j < r.k; ++j) {
+                const int p = place(pos, i0 + j, S);
+                if (p >= 0) __stcs(reinterpret_cast<uint4*>(Xs + p * r.b) + v, piece);
+            }
+        }
+    } else {
+        const char *lo = reinterpret_cast<const char*>(X), *hi = reinterpret_cast<const char*>(X + (r.T - 1) * r.a + r.np);
         for (int j = 0; j < r.k; ++j) {
-            const int p = place(pos, static_cast<long long>(t) * r.k + j, S);
-            if (p >= 0) __stcs(Xs + p * r.b + v, piece);
+            const int p = place(pos, i0 + j, S);
+            if (p < 0) continue;
+            V* q = Xs + p * r.b;
+            const int head = min(r.np, static_cast<int>((-reinterpret_cast<intptr_t>(q) & 15) / sizeof(V)));
+            const int pieces = (r.np - head) / N, rest = r.np - head - pieces * N;
+            for (int v = v0; v < pieces; v += dv)
+                __stcs(reinterpret_cast<uint4*>(q + head) + v, read16<V>(reinterpret_cast<const char*>(x + head) + 16LL * v, lo, hi));
+            for (int i = v0; i < head + rest; i += dv) {
+                const int at = i < head ? i : i + pieces * N;
+                q[at] = x[at];
+            }
         }
     }
-    zero_tail<P>(r, end, t, v0, dv, Xs);
+    zero_tail(r, end, t, v0, dv, Xs);
 }
 
 constexpr int kSlotsAtOnce = 4;  // rows of one token in flight in a thread
@@ -366,13 +403,12 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // dweight: a thread's products in pieces order, then a fixed tree over the
-// group's lanes and warps.
+// group's lanes and warps.  Pitches in bytes.
 template <class V, int VB>
 __global__ void __launch_bounds__(kRowThreads)
     route_combine_grad_kernel(RowShape r, const int* __restrict__ pos, const int* __restrict__ end,
-                              const float* __restrict__ weight, const typename Piece<VB>::T* __restrict__ dY,
-                              long long ldys, const typename Piece<VB>::T* __restrict__ Ys,
-                              typename Piece<VB>::T* __restrict__ dYs, float* __restrict__ dw) {
+                              const float* __restrict__ weight, const char* __restrict__ dY, long long ldys,
+                              const char* __restrict__ Ys, char* __restrict__ dYs, float* __restrict__ dw) {
     using P = typename Piece<VB>::T;
     constexpr int N = VB / sizeof(V);
     __shared__ float part[kRowThreads / 32][kSlotsAtOnce];
@@ -381,6 +417,7 @@ __global__ void __launch_bounds__(kRowThreads)
     const int S = r.T * r.k, v0 = threadIdx.x % r.G;
     const long long i0 = static_cast<long long>(t) * r.k;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const char* g = dY + t * r.a;
     for (int j0 = 0; j0 < r.k; j0 += kSlotsAtOnce) {
         float dot[kSlotsAtOnce], w[kSlotsAtOnce];
         int at[kSlotsAtOnce];
@@ -391,23 +428,24 @@ __global__ void __launch_bounds__(kRowThreads)
             w[u] = at[u] >= 0 && weight ? __ldg(weight + i0 + j0 + u) : 1.f;
         }
         if (live) {
+#pragma unroll 1  // 12001 tokens x 8 x 4095 fp32 679 us, 720 unrolled
             for (int v = v0; v < r.np; v += r.G) {
-                const P g = __ldg(dY + t * r.a + v);
+                const P gp = __ldg(reinterpret_cast<const P*>(g) + v);
                 P y[kSlotsAtOnce];
                 if (dw) {
 #pragma unroll
                     for (int u = 0; u < kSlotsAtOnce; ++u)
-                        if (at[u] >= 0) y[u] = __ldcs(Ys + at[u] * ldys + v);
+                        if (at[u] >= 0) y[u] = __ldcs(reinterpret_cast<const P*>(Ys + at[u] * ldys) + v);
                 }
                 float gf[N];
-                widen<V, P>(g, gf);
+                widen<V, P>(gp, gf);
 #pragma unroll
                 for (int u = 0; u < kSlotsAtOnce; ++u) {
                     if (at[u] < 0) continue;
                     float f[N];
 #pragma unroll
                     for (int i = 0; i < N; ++i) f[i] = w[u] * gf[i];
-                    __stcs(dYs + at[u] * r.b + v, narrow<V, P>(f));
+                    __stcs(reinterpret_cast<P*>(dYs + at[u] * r.b) + v, narrow<V, P>(f));
                     if (dw) {
                         widen<V, P>(y[u], f);
 #pragma unroll
@@ -441,27 +479,35 @@ __global__ void __launch_bounds__(kRowThreads)
             if (r.G > 32) __syncthreads();
         }
     }
-    if (live) zero_tail<P>(r, end, t, v0, r.G, dYs);
+    if (live) {
+        for (long long p = min(max(__ldg(end), 0), S) + static_cast<long long>(t); p < S; p += r.T)
+            for (int v = v0; v < r.np; v += r.G) memset(dYs + p * r.b + v * static_cast<long long>(VB), 0, VB);
+    }
 }
 
 // ---------------------------------------------------------------- host side
 
-// Threads a group: enough that a row is one step, no more than a CTA; a warp
-// at least (the weights' gradient reduces over warps).
-RowShape row_shape(int T, int k, int64_t np) {
+// Threads a group: enough that a row of `steps` pieces is one step, no more
+// than a CTA; a warp at least (the weights' gradient reduces over warps).  The
+// gradient's groups of several warps meet at a barrier for every four slots, so
+// it takes one warp a token (`warps`) where the tokens fill the SMs: 12001
+// tokens x 8 x 130 fp32 22 us, 65 with a CTA each.
+constexpr int kWarpTokens = 152 * 16;
+
+RowShape row_shape(int T, int k, int64_t np, int64_t steps, bool warps) {
     RowShape r{};
     r.T = T;
     r.k = k;
     r.np = static_cast<int>(np);
     r.G = 32;
-    while (r.G < kRowThreads && r.G < np) r.G <<= 1;
+    while (r.G < kRowThreads && r.G < steps && !(warps && T >= kWarpTokens)) r.G <<= 1;
     return r;
 }
 
-dim3 row_grid(const RowShape& r, bool split) {
+dim3 row_grid(const RowShape& r, int64_t pieces, bool split) {
     const int bx = (r.T + kRowThreads / r.G - 1) / (kRowThreads / r.G);
     // few tokens: their rows are cut so that a thread has one piece
-    const int steps = (r.np + r.G - 1) / r.G;
+    const int steps = static_cast<int>((pieces + r.G - 1) / r.G);
     const int by = split && bx < 608 ? std::min(steps, 608 / bx + 1) : 1;
     return dim3(bx, by);
 }
@@ -481,7 +527,7 @@ int piece_bytes(uint64_t bits) {
 template <class V, int VB>
 void combine_launch(RowShape r, const int32_t* pos, const float* weight, const void* Ys, void* Y, cudaStream_t st) {
     using P = typename Piece<VB>::T;
-    route_combine_kernel<V, VB><<<row_grid(r, true), kRowThreads, 0, st>>>(r, pos, weight, static_cast<const P*>(Ys),
+    route_combine_kernel<V, VB><<<row_grid(r, r.np, true), kRowThreads, 0, st>>>(r, pos, weight, static_cast<const P*>(Ys),
                                                                           static_cast<P*>(Y));
 }
 
@@ -490,7 +536,7 @@ spx_status combine(int T, int k, int H, const int32_t* pos, const float* weight,
                    int64_t ldy, cudaStream_t st) {
     const uint64_t row = static_cast<uint64_t>(H) * sizeof(V), a = ldy * sizeof(V), b = ldys * sizeof(V);
     const int vb = piece_bytes<V>(addr(Ys) | addr(Y) | row | a | b);
-    RowShape r = row_shape(T, k, static_cast<int64_t>(row / vb));
+    RowShape r = row_shape(T, k, static_cast<int64_t>(row / vb), static_cast<int64_t>(row / vb), false);
     r.a = static_cast<long long>(a / vb);
     r.b = static_cast<long long>(b / vb);
     if (vb == 16) combine_launch<V, 16>(r, pos, weight, Ys, Y, st);
@@ -500,14 +546,6 @@ spx_status combine(int T, int k, int H, const int32_t* pos, const float* weight,
     return spx_cuda_status(cudaGetLastError());
 }
 
-template <class V, int VB>
-void combine_grad_launch(RowShape r, const int32_t* pos, const int32_t* end, const float* weight, const void* dY,
-                         long long ldys, const void* Ys, void* dYs, float* dw, cudaStream_t st) {
-    using P = typename Piece<VB>::T;
-    route_combine_grad_kernel<V, VB><<<row_grid(r, false), kRowThreads, 0, st>>>(
-        r, pos, end, weight, static_cast<const P*>(dY), ldys, static_cast<const P*>(Ys), static_cast<P*>(dYs), dw);
-}
-
 template <class V>
 spx_status combine_grad(int T, int k, int H, const int32_t* pos, const int32_t* end, const float* weight,
                         const void* dY, int64_t lddy, const void* Ys, int64_t ldys, void* dYs, int64_t lddys,
@@ -515,22 +553,35 @@ spx_status combine_grad(int T, int k, int H, const int32_t* pos, const int32_t* 
     const uint64_t row = static_cast<uint64_t>(H) * sizeof(V), a = lddy * sizeof(V), b = lddys * sizeof(V);
     const uint64_t y = dw ? ldys * sizeof(V) : 0;
     const int vb = piece_bytes<V>(addr(dY) | addr(dYs) | (dw ? addr(Ys) : 0) | row | a | b | y);
-    RowShape r = row_shape(T, k, static_cast<int64_t>(row / vb));
-    r.a = static_cast<long long>(a / vb);
-    r.b = static_cast<long long>(b / vb);
-    const long long ly = static_cast<long long>(y / vb);
-    if (vb == 16) combine_grad_launch<V, 16>(r, pos, end, weight, dY, ly, Ys, dYs, dw, st);
-    else if (vb == 4) combine_grad_launch<V, 4>(r, pos, end, weight, dY, ly, Ys, dYs, dw, st);
-    else combine_grad_launch<V, sizeof(V)>(r, pos, end, weight, dY, ly, Ys, dYs, dw, st);
+    const int64_t np = static_cast<int64_t>(row / vb);
+    RowShape r = row_shape(T, k, np, np, vb == 16 || np <= 512);
+    r.a = static_cast<long long>(a);
+    r.b = static_cast<long long>(b);
+    const long long ly = static_cast<long long>(y);
+    const dim3 grid = row_grid(r, np, false);
+    const char *dy = static_cast<const char*>(dY), *ys = static_cast<const char*>(Ys);
+    char* out = static_cast<char*>(dYs);
+    if (vb == 16) route_combine_grad_kernel<V, 16><<<grid, kRowThreads, 0, st>>>(r, pos, end, weight, dy, ly, ys, out, dw);
+    else if (vb == 4) route_combine_grad_kernel<V, 4><<<grid, kRowThreads, 0, st>>>(r, pos, end, weight, dy, ly, ys, out, dw);
+    else route_combine_grad_kernel<V, sizeof(V)><<<grid, kRowThreads, 0, st>>>(r, pos, end, weight, dy, ly, ys, out, dw);
     spx_note_launches(1);
     return spx_cuda_status(cudaGetLastError());
 }
 
-template <int VB>
-void gather_launch(RowShape r, const int32_t* pos, const int32_t* end, const void* X, void* Xs, cudaStream_t st) {
-    using P = typename Piece<VB>::T;
-    route_gather_kernel<VB><<<row_grid(r, true), kRowThreads, 0, st>>>(r, pos, end, static_cast<const P*>(X),
-                                                                      static_cast<P*>(Xs));
+template <class V>
+spx_status gather(int T, int k, int H, const int32_t* pos, const int32_t* end, const void* X, int64_t ldx, void* Xs,
+                  int64_t ldxs, cudaStream_t st) {
+    const int64_t pieces = (H + 16 / sizeof(V) - 1) / (16 / sizeof(V));
+    RowShape r = row_shape(T, k, H, pieces, false);
+    r.a = ldx;
+    r.b = ldxs;
+    const V* x = static_cast<const V*>(X);
+    V* xs = static_cast<V*>(Xs);
+    const uint64_t bits = addr(X) | addr(Xs) | (static_cast<uint64_t>(H) | ldx | ldxs) * sizeof(V);
+    if (bits % 16 == 0) route_gather_kernel<V, true><<<row_grid(r, pieces, true), kRowThreads, 0, st>>>(r, pos, end, x, xs);
+    else route_gather_kernel<V, false><<<row_grid(r, pieces, true), kRowThreads, 0, st>>>(r, pos, end, x, xs);
+    spx_note_launches(1);
+    return spx_cuda_status(cudaGetLastError());
 }
 
 }  // namespace
@@ -591,20 +642,10 @@ spx_status spx_route_gather(int32_t T, int32_t k, int32_t H, spx_type type, cons
     const size_t eb = type_bytes(type);
     if (!spx_aligned(pos, 4) || !spx_aligned(offsets_end, 4) || !spx_aligned(X, eb) || !spx_aligned(Xs, eb))
         return SPX_ERR_ALIGN;
-    const uint64_t row = static_cast<uint64_t>(H) * eb, a = ldx * eb, b = ldxs * eb;
-    int vb = copy_width(addr(X) | addr(Xs) | row | a | b, static_cast<int>(eb));
-    if (vb == 8) vb = 4;
-    if (row / vb > static_cast<uint64_t>(kI32Max)) return SPX_ERR_INDEX_RANGE;
-    RowShape r = row_shape(T, k, static_cast<int64_t>(row / vb));
-    r.a = static_cast<long long>(a / vb);
-    r.b = static_cast<long long>(b / vb);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (vb == 16) gather_launch<16>(r, pos, offsets_end, X, Xs, st);
-    else if (vb == 4) gather_launch<4>(r, pos, offsets_end, X, Xs, st);
-    else if (vb == 2) gather_launch<2>(r, pos, offsets_end, X, Xs, st);
-    else gather_launch<1>(r, pos, offsets_end, X, Xs, st);
-    spx_note_launches(1);
-    return spx_cuda_status(cudaGetLastError());
+    if (eb == 4) return gather<uint32_t>(T, k, H, pos, offsets_end, X, ldx, Xs, ldxs, st);
+    if (eb == 2) return gather<uint16_t>(T, k, H, pos, offsets_end, X, ldx, Xs, ldxs, st);
+    return gather<uint8_t>(T, k, H, pos, offsets_end, X, ldx, Xs, ldxs, st);
 }
 
 spx_status spx_route_combine(int32_t T, int32_t k, int32_t H, spx_type type, const int32_t* pos, const float* weight,
