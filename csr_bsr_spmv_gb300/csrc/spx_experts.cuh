@@ -48,6 +48,35 @@ __device__ __forceinline__ void expert_rows(const int* __restrict__ offsets, int
     hi = min(max(__ldg(offsets + e + 1), lo), S);
 }
 
+// The calls of a layer follow one another on a stream and run for a few
+// microseconds each, so every kernel waits for the one before -- all of it --
+// only when it is about to touch global memory, and the short ones let the next
+// be scheduled early (programmatic dependent launch): the launch and the set-up
+// overlap the kernel before (sort, gather and return of 16384 x 4 x 2048 bf16
+// 125 -> 118 us).
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st,
+                         A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 inline size_t type_bytes(spx_type t) { return t == SPX_F32 ? 4 : t == SPX_I8 ? 1 : 2; }
 inline bool is_float_type(spx_type t) { return t == SPX_F32 || t == SPX_BF16 || t == SPX_F16; }
 inline bool is_half_type(spx_type t) { return t == SPX_BF16 || t == SPX_F16; }

@@ -30,6 +30,8 @@ template <class V, class O>
 __global__ void __launch_bounds__(kThreads) experts_simt_kernel(SimtGemm g) {
     __shared__ float sl[kR][kT + 1], sr[kR][kT + 1];
     __shared__ int s_e, s_lo, s_hi;
+    let_next_start();
+    wait_for_previous();
     const V *L = static_cast<const V*>(g.L), *R = static_cast<const V*>(g.R);
     O* C = static_cast<O*>(g.C);
     const int j0 = blockIdx.y * kT;
@@ -102,11 +104,11 @@ spx_status launch(const SimtGemm& g, spx_type c_type, cudaStream_t st) {
         grid = dim3((g.NI + kT - 1) / kT, (g.NJ + kT - 1) / kT, g.E);
     }
     if (grid.y > 65535) return SPX_ERR_UNSUPPORTED;
-    if (c_type == SPX_F32) experts_simt_kernel<V, float><<<grid, kThreads, 0, st>>>(g);
-    else if (c_type == SPX_BF16) experts_simt_kernel<V, __nv_bfloat16><<<grid, kThreads, 0, st>>>(g);
-    else experts_simt_kernel<V, __half><<<grid, kThreads, 0, st>>>(g);
     spx_note_launches(1);
-    return spx_cuda_status(cudaGetLastError());
+    return spx_cuda_status(launch_early(c_type == SPX_F32    ? experts_simt_kernel<V, float>
+                                        : c_type == SPX_BF16 ? experts_simt_kernel<V, __nv_bfloat16>
+                                                             : experts_simt_kernel<V, __half>,
+                                        grid, kThreads, 0, 1, st, g));
 }
 
 }  // namespace

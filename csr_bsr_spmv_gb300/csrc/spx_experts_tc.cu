@@ -492,6 +492,9 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         }
     }
+    // (The next kernel is not let in early: its blocks beside this one's cost more than its launch, 224 us for the 8-bit
+    // prefill product against 215.)
+    wait_for_previous();
     int ntiles = a.max_tiles;  // kWG: every expert's tiles, rows or not
     for (int e = threadIdx.x; e <= a.E; e += kThreadsOf<FUSE>) {
         int lo = 0, hi = a.S;
@@ -1150,8 +1153,8 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = team;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = team > 1 ? 1 : 0;
+    cfg.attrs = attr;  // for the question below
+    cfg.numAttrs = 1;
     // as many CTAs as run at once: one an SM; teams only where a GPC has the SMs left for them
     int groups = sms;
     if (team > 1) {
@@ -1159,10 +1162,10 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
         groups = resident_teams(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE>), team, cfg);
         if (groups <= 0) return SPX_ERR_CUDA;
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(max_tiles, groups)) * team);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE>, tl, tc, a);
     spx_note_launches(1);
-    return spx_cuda_status(e != cudaSuccess ? e : cudaGetLastError());
+    return spx_cuda_status(launch_early(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE>,
+                                        dim3(static_cast<unsigned>(std::min<long long>(max_tiles, groups)) * team),
+                                        kThreadsOf<FUSE>, smem, team, st, tl, tc, a));
 }
 
 uint32_t idesc_of(spx_type type, int mode, int cg) {

@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(kQThreads, 4)
     using P = Pack<V, N>;
     using B = Pack<int8_t, N>;
     __shared__ uint32_t s_max[kQThreads / 32];
+    let_next_start();
+    wait_for_previous();
     const int row = blockIdx.x * (kQThreads / G) + threadIdx.x / G, at = threadIdx.x % G;
     if (row >= M) return;  // a whole group; G == kQThreads: never
     const P* x = reinterpret_cast<const P*>(X + row * ldx);
@@ -193,20 +195,21 @@ __global__ void __launch_bounds__(kQThreads, 4)
 }
 
 template <class V, int N>
-void quant_grid(int M, int K, const V* x, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, cudaStream_t st) {
+cudaError_t quant_grid(int M, int K, const V* x, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, cudaStream_t st) {
     constexpr int per = kQThreads / 32;
-    if (M >= kQWarpRows) quant_rows_kernel<V, N, 32><<<(M + per - 1) / per, kQThreads, 0, st>>>(M, K, x, ldx, Q, ldq, scale);
-    else quant_rows_kernel<V, N, kQThreads><<<M, kQThreads, 0, st>>>(M, K, x, ldx, Q, ldq, scale);
+    return M >= kQWarpRows ? launch_early(quant_rows_kernel<V, N, 32>, dim3((M + per - 1) / per), kQThreads, 0, 1, st, M, K, x,
+                                          ldx, Q, ldq, scale)
+                           : launch_early(quant_rows_kernel<V, N, kQThreads>, dim3(M), kQThreads, 0, 1, st, M, K, x, ldx, Q,
+                                          ldq, scale);
 }
 
 template <class V>
-void quant_launch(int M, int K, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, cudaStream_t st) {
+cudaError_t quant_launch(int M, int K, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, cudaStream_t st) {
     constexpr int N = 16 / sizeof(V);
     const V* x = static_cast<const V*>(X);
     if (spx_aligned(X, 16) && spx_aligned(Q, N) && ldx % N == 0 && ldq % N == 0 && K % N == 0)
-        quant_grid<V, N>(M, K, x, ldx, Q, ldq, scale, st);
-    else
-        quant_grid<V, 1>(M, K, x, ldx, Q, ldq, scale, st);
+        return quant_grid<V, N>(M, K, x, ldx, Q, ldq, scale, st);
+    return quant_grid<V, 1>(M, K, x, ldx, Q, ldq, scale, st);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -264,6 +267,8 @@ template <int NB, int MT, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) i8_few_kernel(FewArgs a) {
     constexpr int TM = 8 * NB, CH = 16 * MT;
     __shared__ int part[WARPS][TM * CH];
+    let_next_start();
+    wait_for_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int e = 0, r0 = blockIdx.y * TM, hi = a.S;
     if (a.offsets && !warp_find_tile(a.offsets, a.E, a.S, TM, blockIdx.y, e, r0, hi)) return;
@@ -378,23 +383,23 @@ __global__ void __launch_bounds__(32 * WARPS) i8_few_kernel(FewArgs a) {
 }
 
 template <int NB, int MT, int WARPS>
-void few_grid(FewArgs a, long long blocks, long long row_tiles, cudaStream_t st) {
+cudaError_t few_grid(FewArgs a, long long blocks, long long row_tiles, cudaStream_t st) {
     const long long per = WARPS / a.ks;
-    i8_few_kernel<NB, MT, WARPS><<<dim3(static_cast<unsigned>((blocks + per - 1) / per), static_cast<unsigned>(row_tiles)),
-                                   32 * WARPS, 0, st>>>(a);
+    return launch_early(i8_few_kernel<NB, MT, WARPS>,
+                        dim3(static_cast<unsigned>((blocks + per - 1) / per), static_cast<unsigned>(row_tiles)), 32 * WARPS, 0,
+                        1, st, a);
 }
 
 // A block's reduction is shared among warps until there are warps enough for the memory's latency: by the four of a
 // small CTA, or by MOST of a large one where even that leaves few (8 rows x 4096 x 4096: 7.0 us, 8.3 with four).
 template <int NB, int MT, int MOST>
-void few_launch(FewArgs a, long long row_tiles, cudaStream_t st) {
+cudaError_t few_launch(FewArgs a, long long row_tiles, cudaStream_t st) {
     const long long blocks = (a.N + 16 * MT - 1) / (16 * MT);
     const long long tiles = a.E == 1 ? (a.S + 8 * NB - 1) / (8 * NB) : std::min(a.E, a.S);
     a.ks = 1;
     while (a.ks < 4 && blocks * tiles * a.ks < kFewEnough && 64 * 2 * a.ks < a.K) a.ks *= 2;
     while (a.ks >= 4 && a.ks < MOST && blocks * tiles * a.ks < kFewEnough / 4 && 64 * 2 * a.ks < a.K) a.ks *= 2;
-    if (a.ks <= 4) few_grid<NB, MT, 4>(a, blocks, row_tiles, st);
-    else few_grid<NB, MT, MOST>(a, blocks, row_tiles, st);
+    return a.ks <= 4 ? few_grid<NB, MT, 4>(a, blocks, row_tiles, st) : few_grid<NB, MT, MOST>(a, blocks, row_tiles, st);
 }
 
 // One row (blockIdx.y) against its expert's channels, on the CUDA cores' byte
@@ -404,6 +409,8 @@ void few_launch(FewArgs a, long long row_tiles, cudaStream_t st) {
 constexpr int kRowChan = 2, kRowThreads = 128, kRowMost = 2;
 
 __global__ void __launch_bounds__(kRowThreads) i8_row_kernel(FewArgs a) {
+    let_next_start();
+    wait_for_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int e = 0, p = blockIdx.y, hi = a.S;
     if (a.offsets && !warp_find_tile(a.offsets, a.E, a.S, 1, blockIdx.y, e, p, hi)) return;
@@ -453,20 +460,18 @@ __global__ void __launch_bounds__(kRowThreads) i8_row_kernel(FewArgs a) {
 spx_status few_product(const FewArgs& a, cudaStream_t st) {
     if (a.S <= kRowMost) {
         constexpr int per = kRowThreads / 32 * kRowChan;
-        i8_row_kernel<<<dim3((a.N + per - 1) / per, a.S), kRowThreads, 0, st>>>(a);
         spx_note_launches(1);
-        return spx_cuda_status(cudaGetLastError());
+        return spx_cuda_status(launch_early(i8_row_kernel, dim3((a.N + per - 1) / per, a.S), kRowThreads, 0, 1, st, a));
     }
     const long long avg = (a.S + a.E - 1) / a.E, most = a.E == 1 ? avg : 3 * avg / 2;
     const int nb = most <= 8 ? 1 : most <= 16 ? 2 : 4;
     const long long ty = a.offsets ? std::min<long long>(max_row_tiles(a.E, a.S, 8 * nb), static_cast<long long>(a.S) + 1)
                                    : (a.S + 8 * nb - 1) / (8 * nb);
     if (ty > 65535) return SPX_ERR_UNSUPPORTED;
-    if (nb == 1) few_launch<1, 1, 16>(a, ty, st);
-    else if (nb == 2) few_launch<2, 1, 16>(a, ty, st);
-    else few_launch<4, 2, 8>(a, ty, st);
     spx_note_launches(1);
-    return spx_cuda_status(cudaGetLastError());
+    return spx_cuda_status(nb == 1   ? few_launch<1, 1, 16>(a, ty, st)
+                           : nb == 2 ? few_launch<2, 1, 16>(a, ty, st)
+                                     : few_launch<4, 2, 8>(a, ty, st));
 }
 
 // ---------------------------------------------------------------- codes to fp16
@@ -481,6 +486,8 @@ __global__ void __launch_bounds__(kWidenThreads)
     widen_kernel(const int* __restrict__ offsets, int S, int N, int K, int Kp, const int8_t* __restrict__ Q,
                  long long ldq, const int8_t* __restrict__ W, long long ldw, long long stride_w,
                  __half* __restrict__ Q16, __half* __restrict__ W16, bool same_w) {
+    let_next_start();
+    wait_for_previous();
     const int8_t* src = Q;
     __half* dst = Q16;
     long long ld = ldq;
@@ -547,11 +554,10 @@ spx_status spx_quant_rows_i8(int32_t M, int32_t K, spx_type type, const void* X,
     if (!scale || (K > 0 && (!X || !Q || ldx < K || ldq < K))) return SPX_ERR_ARG;
     if (!spx_aligned(X, type_bytes(type)) || !spx_aligned(scale, 4)) return SPX_ERR_ALIGN;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (type == SPX_F32) quant_launch<float>(M, K, X, ldx, Q, ldq, scale, st);
-    else if (type == SPX_BF16) quant_launch<__nv_bfloat16>(M, K, X, ldx, Q, ldq, scale, st);
-    else quant_launch<__half>(M, K, X, ldx, Q, ldq, scale, st);
     spx_note_launches(1);
-    return spx_cuda_status(cudaGetLastError());
+    return spx_cuda_status(type == SPX_F32    ? quant_launch<float>(M, K, X, ldx, Q, ldq, scale, st)
+                           : type == SPX_BF16 ? quant_launch<__nv_bfloat16>(M, K, X, ldx, Q, ldq, scale, st)
+                                              : quant_launch<__half>(M, K, X, ldx, Q, ldq, scale, st));
 }
 
 size_t spx_gemm_i8_scratch_bytes(int32_t E, int32_t S, int32_t N, int32_t K, int32_t wide) {
@@ -596,10 +602,9 @@ spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t
         const bool aligned = spx_aligned(Q, 8) && spx_aligned(W, 8) && ldq % 8 == 0 && ldw % 8 == 0 && stride_w % 8 == 0;
         constexpr int per = kWidenThreads / 32;  // a row a warp
         const dim3 grid(std::min((std::max(S, N) + per - 1) / per, 1216), 1 + mats);
-        if (aligned)
-            widen_kernel<true><<<grid, kWidenThreads, 0, st>>>(offsets, S, N, K, Kp, Q, ldq, W, ldw, stride_w, Q16, W16, same_w);
-        else
-            widen_kernel<false><<<grid, kWidenThreads, 0, st>>>(offsets, S, N, K, Kp, Q, ldq, W, ldw, stride_w, Q16, W16, same_w);
+        const cudaError_t e = launch_early(aligned ? widen_kernel<true> : widen_kernel<false>, grid, kWidenThreads, 0, 1, st,
+                                           offsets, S, N, K, Kp, Q, ldq, W, ldw, stride_w, Q16, W16, same_w);
+        if (e != cudaSuccess) return spx_cuda_status(e);
         spx_note_launches(1);
     }
     return tc_product_i8(E, S, N, K, offsets, Q16, Kp, row_scale, W16, Kp, mats, w_scale, C, ldc, c_type, st);

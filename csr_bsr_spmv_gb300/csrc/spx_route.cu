@@ -72,6 +72,8 @@ __device__ __forceinline__ void rank_run(const Ids& x, int E, int w0, int end, i
 __global__ void __launch_bounds__(32 * kMostWarps)
     route_count_kernel(Ids x, int S, int E, int runs, int* __restrict__ hist) {
     extern __shared__ int sm[];
+    let_next_start();
+    wait_for_previous();
     for (int e = threadIdx.x; e < E; e += blockDim.x) sm[e] = 0;
     __syncthreads();
     const int per = runs * blockDim.x * kHeld, b0 = blockIdx.x * per, b1 = min(S, b0 + per);
@@ -92,7 +94,9 @@ __global__ void __launch_bounds__(32 * kMostWarps)
     const int nw = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = gridDim.x, b = blockIdx.x;
     const int ES = E | 1;  // odd: a column of the counters touches every bank
     int *tot = sm + nw * ES, *before = tot + E + 1, *own = before + E;
+    let_next_start();
     for (int i = threadIdx.x; i < nw * ES + 3 * E + 1; i += blockDim.x) sm[i] = 0;
+    wait_for_previous();
     __syncthreads();
     const int per = runs * blockDim.x * kHeld, b0 = b * per, b1 = min(S, b0 + per);
     int id[kHeld], rank[kHeld];
@@ -327,6 +331,8 @@ template <class V, bool ALIGNED>
 __global__ void __launch_bounds__(kRowThreads)
     route_gather_kernel(RowShape r, const int* __restrict__ pos, const int* __restrict__ end, const V* __restrict__ X,
                         V* __restrict__ Xs) {
+    let_next_start();
+    wait_for_previous();
     const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
     if (t >= r.T) return;
     const int S = r.T * r.k, v0 = blockIdx.y * r.G + threadIdx.x % r.G, dv = gridDim.y * r.G;
@@ -368,6 +374,8 @@ __global__ void __launch_bounds__(kRowThreads)
                          const typename Piece<VB>::T* __restrict__ Ys, typename Piece<VB>::T* __restrict__ Y) {
     using P = typename Piece<VB>::T;
     constexpr int N = VB / sizeof(V);
+    let_next_start();
+    wait_for_previous();
     const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
     if (t >= r.T) return;
     const int S = r.T * r.k, v0 = blockIdx.y * r.G + threadIdx.x % r.G, dv = gridDim.y * r.G;
@@ -412,6 +420,8 @@ __global__ void __launch_bounds__(kRowThreads)
     using P = typename Piece<VB>::T;
     constexpr int N = VB / sizeof(V);
     __shared__ float part[kRowThreads / 32][kSlotsAtOnce];
+    let_next_start();
+    wait_for_previous();
     const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
     const bool live = t < r.T;
     const int S = r.T * r.k, v0 = threadIdx.x % r.G;
@@ -525,10 +535,10 @@ int piece_bytes(uint64_t bits) {
 }
 
 template <class V, int VB>
-void combine_launch(RowShape r, const int32_t* pos, const float* weight, const void* Ys, void* Y, cudaStream_t st) {
+cudaError_t combine_launch(RowShape r, const int32_t* pos, const float* weight, const void* Ys, void* Y, cudaStream_t st) {
     using P = typename Piece<VB>::T;
-    route_combine_kernel<V, VB><<<row_grid(r, r.np, true), kRowThreads, 0, st>>>(r, pos, weight, static_cast<const P*>(Ys),
-                                                                          static_cast<P*>(Y));
+    return launch_early(route_combine_kernel<V, VB>, row_grid(r, r.np, true), kRowThreads, 0, 1, st, r, pos, weight,
+                        static_cast<const P*>(Ys), static_cast<P*>(Y));
 }
 
 template <class V>
@@ -539,11 +549,10 @@ spx_status combine(int T, int k, int H, const int32_t* pos, const float* weight,
     RowShape r = row_shape(T, k, static_cast<int64_t>(row / vb), static_cast<int64_t>(row / vb), false);
     r.a = static_cast<long long>(a / vb);
     r.b = static_cast<long long>(b / vb);
-    if (vb == 16) combine_launch<V, 16>(r, pos, weight, Ys, Y, st);
-    else if (vb == 4) combine_launch<V, 4>(r, pos, weight, Ys, Y, st);
-    else combine_launch<V, sizeof(V)>(r, pos, weight, Ys, Y, st);
     spx_note_launches(1);
-    return spx_cuda_status(cudaGetLastError());
+    return spx_cuda_status(vb == 16  ? combine_launch<V, 16>(r, pos, weight, Ys, Y, st)
+                           : vb == 4 ? combine_launch<V, 4>(r, pos, weight, Ys, Y, st)
+                                     : combine_launch<V, sizeof(V)>(r, pos, weight, Ys, Y, st));
 }
 
 template <class V>
@@ -561,11 +570,11 @@ spx_status combine_grad(int T, int k, int H, const int32_t* pos, const int32_t* 
     const dim3 grid = row_grid(r, np, false);
     const char *dy = static_cast<const char*>(dY), *ys = static_cast<const char*>(Ys);
     char* out = static_cast<char*>(dYs);
-    if (vb == 16) route_combine_grad_kernel<V, 16><<<grid, kRowThreads, 0, st>>>(r, pos, end, weight, dy, ly, ys, out, dw);
-    else if (vb == 4) route_combine_grad_kernel<V, 4><<<grid, kRowThreads, 0, st>>>(r, pos, end, weight, dy, ly, ys, out, dw);
-    else route_combine_grad_kernel<V, sizeof(V)><<<grid, kRowThreads, 0, st>>>(r, pos, end, weight, dy, ly, ys, out, dw);
     spx_note_launches(1);
-    return spx_cuda_status(cudaGetLastError());
+    auto launch = [&](auto kernel) { return launch_early(kernel, grid, kRowThreads, 0, 1, st, r, pos, end, weight, dy, ly, ys, out, dw); };
+    return spx_cuda_status(vb == 16  ? launch(route_combine_grad_kernel<V, 16>)
+                           : vb == 4 ? launch(route_combine_grad_kernel<V, 4>)
+                                     : launch(route_combine_grad_kernel<V, sizeof(V)>));
 }
 
 template <class V>
@@ -578,10 +587,9 @@ spx_status gather(int T, int k, int H, const int32_t* pos, const int32_t* end, c
     const V* x = static_cast<const V*>(X);
     V* xs = static_cast<V*>(Xs);
     const uint64_t bits = addr(X) | addr(Xs) | (static_cast<uint64_t>(H) | ldx | ldxs) * sizeof(V);
-    if (bits % 16 == 0) route_gather_kernel<V, true><<<row_grid(r, pieces, true), kRowThreads, 0, st>>>(r, pos, end, x, xs);
-    else route_gather_kernel<V, false><<<row_grid(r, pieces, true), kRowThreads, 0, st>>>(r, pos, end, x, xs);
     spx_note_launches(1);
-    return spx_cuda_status(cudaGetLastError());
+    return spx_cuda_status(launch_early(bits % 16 == 0 ? route_gather_kernel<V, true> : route_gather_kernel<V, false>,
+                                        row_grid(r, pieces, true), kRowThreads, 0, 1, st, r, pos, end, x, xs));
 }
 
 }  // namespace
@@ -613,22 +621,14 @@ spx_status spx_route_build(int32_t T, int32_t k, int32_t E, const void* expert, 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const Ids ids{expert, lde, k, id_bytes};
     int* hist = h.counted ? static_cast<int*>(scratch) : nullptr;
-    if (h.counted) route_count_kernel<<<h.blocks, 32 * h.warps, sizeof(int) * E, st>>>(ids, S, E, h.runs, hist);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(h.blocks);
-    cfg.blockDim = dim3(32 * h.warps);
-    cfg.dynamicSmemBytes = h.smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(h.blocks);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = !h.counted && h.blocks > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, route_place_kernel, ids, S, E, h.runs, static_cast<const int*>(hist),
-                                             offsets, slot, pos);
     spx_note_launches(h.counted ? 2 : 1);
-    return spx_cuda_status(e != cudaSuccess ? e : cudaGetLastError());
+    cudaError_t e = cudaSuccess;
+    if (h.counted)
+        e = launch_early(route_count_kernel, dim3(h.blocks), 32 * h.warps, sizeof(int) * E, 1, st, ids, S, E, h.runs, hist);
+    if (e == cudaSuccess)
+        e = launch_early(route_place_kernel, dim3(h.blocks), 32 * h.warps, h.smem, h.counted ? 1 : h.blocks, st, ids, S, E,
+                         h.runs, hist, offsets, slot, pos);
+    return spx_cuda_status(e);
 }
 
 spx_status spx_route_gather(int32_t T, int32_t k, int32_t H, spx_type type, const int32_t* pos,
