@@ -20,12 +20,13 @@ namespace {
 // ---------------------------------------------------------------- quantisation
 
 // A row's largest magnitude, then its codes.  Bound by HBM.  A group of G
-// threads takes a row: a warp where there are rows enough to fill the SMs (16384
-// rows x 2048 bf16: MEASURE us, a CTA a row 52), a CTA otherwise.  Up to kQHeld
-// pieces a thread stay in registers between the two; a longer row is read again
-// (from L2).
-constexpr int kQThreads = 256, kQHeld = 8;
-constexpr int kQWarpRows = 1216;  // rows from which a warp takes one: eight a CTA, one CTA an SM
+// threads takes a row: a warp where there are rows enough to fill the SMs and
+// they are short (16384 rows x 2048 bf16: 20 us, 26 with a CTA a row; x 4096 51
+// and 42), a CTA otherwise.  Up to kQHeld pieces a thread stay in registers
+// between the two, a longer row is read again from L2: more of them held cost
+// more in resident warps (eight: 27 us) than the reads.
+constexpr int kQThreads = 128, kQHeld = 4;
+constexpr int kQWarpRows = 1216;  // rows that fill the SMs with a warp each: eight an SM
 
 template <class V, int N>
 struct alignas(N * sizeof(V) >= 16 ? 16 : N * sizeof(V)) Pack {
@@ -133,7 +134,7 @@ __device__ __noinline__ Pack<int8_t, N> divided_codes(Pack<V, N> p, float s) {
 
 // N values a piece: 16 bytes of X where rows are aligned, else 1 value.
 template <class V, int N, int G>
-__global__ void __launch_bounds__(kQThreads, 4)
+__global__ void __launch_bounds__(kQThreads, 10)
     quant_rows_kernel(int M, int K, const V* __restrict__ X, long long ldx, int8_t* __restrict__ Q, long long ldq,
                       float* __restrict__ scale) {
     using P = Pack<V, N>;
@@ -197,7 +198,8 @@ __global__ void __launch_bounds__(kQThreads, 4)
 template <class V, int N>
 cudaError_t quant_grid(int M, int K, const V* x, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, cudaStream_t st) {
     constexpr int per = kQThreads / 32;
-    return M >= kQWarpRows ? launch_early(quant_rows_kernel<V, N, 32>, dim3((M + per - 1) / per), kQThreads, 0, 1, st, M, K, x,
+    const bool warps = M >= kQWarpRows && K <= (N == 1 ? 2048 : 256 * N);
+    return warps ? launch_early(quant_rows_kernel<V, N, 32>, dim3((M + per - 1) / per), kQThreads, 0, 1, st, M, K, x,
                                           ldx, Q, ldq, scale)
                            : launch_early(quant_rows_kernel<V, N, kQThreads>, dim3(M), kQThreads, 0, 1, st, M, K, x, ldx, Q,
                                           ldq, scale);

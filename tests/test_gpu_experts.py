@@ -74,7 +74,8 @@ def close(got, ref, bound, n, what=""):
 # ---------------------------------------------------------------- the sort
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (5, 3, 2), (31, 1, 7), (33, 2, 2048), (1000, 8, 3),
-                                   (2731, 3, 60), (8192, 1, 64), (8193, 1, 64), (20000, 6, 129), (70001, 4, 2048)])
+                                   (2731, 3, 60), (8192, 1, 64), (8193, 1, 64), (20000, 6, 129), (70001, 4, 2048),
+                                   (512, 4, 64), (513, 4, 64), (4096, 4, 33), (4097, 4, 33), (200000, 4, 50)])
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 def test_route_build_is_the_stable_sort(T, k, E, dtype):
     ids = ids_of(T, k, E, T + E, dtype=dtype)
@@ -275,7 +276,9 @@ PRODUCTS = [("spread", 4, 300, 128, 64), ("spread", 3, 1000, 1000, 776), ("gaps"
             ("one", 5, 600, 96, 200), ("single", 64, 40, 512, 1024), ("empty", 3, 20, 72, 40),
             ("spread", 1, 1, 8, 8), ("spread", 2, 5, 1, 16), ("gaps", 40, 4097, 136, 72), ("spread", 8, 2000, 513, 257),
             ("spread", 300, 90, 40, 24), ("one", 2, 257, 256, 4096),
-            ("spread", 200, 900, 200, 264), ("gaps", 7, 5000, 392, 648)]
+            ("spread", 200, 900, 200, 264), ("gaps", 7, 5000, 392, 648),
+            # few tiles and a long reduction: shared by two, four and eight CTAs
+            ("spread", 1, 16, 512, 8192), ("spread", 1, 100, 640, 4104), ("gaps", 2, 33, 384, 6000)]
 
 
 @pytest.mark.parametrize("load,E,S,N,K", PRODUCTS)
@@ -399,6 +402,30 @@ def test_product_past_32_bit_offsets():
         close(C[lo:lo + 64], a @ w.T, a.abs() @ w.abs().T, K, "far rows")
 
 
+def test_weights_past_32_bit_offsets():
+    E, N, K = 36, 8192, 8192  # 2.4e9 weights
+    W = torch.empty(E, N, K, device="cuda", dtype=BF16)
+    for e in range(E):
+        W[e].normal_(generator=gen(200 + e))
+    S = 3 * E
+    A = torch.randn(S, K, device="cuda", generator=gen(201)).to(BF16)
+    off = torch.arange(0, S + 1, 3, dtype=torch.int32, device="cuda")
+    G = torch.randn(S, N, device="cuda", generator=gen(202)).to(BF16)
+    C, dA = spx.spx_gemm_grouped(off, A, W), spx.spx_gemm_grouped(off, G, W, layout="kn")
+    W8 = torch.randint(-127, 128, (E, N, K), device="cuda", generator=gen(203), dtype=torch.int8)
+    Q, rs = spx.spx_quant_rows_i8(A)
+    ws = torch.rand(E, N, device="cuda", generator=gen(204))
+    C8 = spx.spx_gemm_i8(Q, rs, W8, ws, offsets=off)
+    dW = spx.spx_gemm_grouped_wgrad(off, G, A)
+    for e in (0, 31, 32, 35):
+        a, g, w = A[3 * e:3 * e + 3].double(), G[3 * e:3 * e + 3].double(), W[e].double()
+        close(C[3 * e:3 * e + 3], a @ w.T, a.abs() @ w.abs().T, K, "far weights")
+        close(dA[3 * e:3 * e + 3], g @ w, g.abs() @ w.abs(), N, "far weights")
+        close(dW[e], g.T @ a, g.abs().T @ a.abs(), 3, "far gradient")
+        acc = (Q[3 * e:3 * e + 3].double() @ W8[e].double().T).long()
+        assert torch.equal(C8[3 * e:3 * e + 3], acc.float() * (rs[3 * e:3 * e + 3, None] * ws[e]))
+
+
 def test_experts_on_another_stream():
     """Calls on a side stream, their outputs read there, while the main stream reuses memory."""
     T, k, E, H, N = 600, 2, 6, 256, 384
@@ -494,6 +521,10 @@ def i8_ref(off, Q, rs, W, ws, out):
 
 I8 = [("spread", 1, 1, 4096, 4096), ("spread", 1, 5, 100, 300), ("spread", 1, 64, 256, 512), ("spread", 1, 300, 1000, 776),
       ("spread", 4, 500, 264, 1040), ("gaps", 12, 800, 128, 96), ("single", 64, 40, 512, 256), ("one", 3, 400, 513, 129),
+      # one or two rows in all, up to 8, 16 and 32 an expert, and on to 128: each with long and short reductions
+      ("one", 3, 2, 72, 4096), ("spread", 1, 2, 1030, 208), ("spread", 1, 8, 300, 4112), ("spread", 1, 16, 520, 9216),
+      ("spread", 40, 200, 136, 2048), ("gaps", 40, 480, 100, 1040), ("spread", 1, 24, 512, 4096),
+      ("spread", 5, 170, 260, 4112), ("gaps", 6, 300, 264, 2320), ("spread", 2, 250, 640, 3000), ("one", 4, 100, 136, 520),
       ("empty", 3, 20, 72, 40), ("spread", 2, 17, 1, 1), ("spread", 1, 2, 40, 5000), ("spread", 3, 900, 272, 2064)]
 
 
