@@ -606,3 +606,18 @@ def test_layer_end_to_end():
     assert torch.equal(Y.double(), out.detach())
     for got, p in ((dX, P[0]), (dW1, P[1]), (dW2, P[2]), (dwt, P[3])):
         assert torch.equal(got.double(), p.grad)
+
+
+def test_example_trains_and_serves():
+    """examples/routed_experts.py: the loss falls, and 8-bit experts stay within 5% of the bf16 layer (codes of
+    7 bits a value round by about 0.5% of a row's largest, four roundings in a row)."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "routed_experts.py")
+    spec = importlib.util.spec_from_file_location("routed_experts", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses, off = m.main(tokens=512, width=128, inner=256, experts=8, k=2, steps=30, say=lambda *_: None)
+    assert losses[-1] < 0.8 * losses[0]
+    assert all(v < 0.05 for v in off.values())
