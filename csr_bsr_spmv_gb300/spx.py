@@ -8,6 +8,7 @@ fallback: if libspx.so is missing, loading raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
@@ -849,10 +850,11 @@ def spx_spmm_bsr(M: int, K: int, br: int, bc: int, bsr_row_ptr, bsr_col, bsr_val
 
 
 # ------------------------------------------------------------------ routed experts
-# A decoded token's calls run for a few microseconds each, so these bindings ask torch for as little as
-# they can: one shape, one stride, one address an operand, and the stream's raw handle.
+# A decoded token's calls run for a few microseconds each, so these bindings look at an operand once --
+# shape, strides, type, address -- and go straight to the call; the library checks the rest.
 
 _SPX_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int8: 3}
+_F32, _I32, _I8, _empty = torch.float32, torch.int32, torch.int8, torch.empty
 
 
 def _type(t: torch.Tensor) -> int:
@@ -866,25 +868,26 @@ def _new(shape, dtype, like, stream):
     """An output or scratch tensor that belongs to the stream the call runs on, so that its memory is
     not handed out again before that stream has passed the call."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype=dtype, device=like.device)
 
 
 def _raw_stream(like: torch.Tensor, stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(like.get_device()) or None
-    return stream.cuda_stream or None
+        return torch._C._cuda_getCurrentRawStream(like.get_device())
+    return stream.cuda_stream
 
 
 def _mat(t: torch.Tensor, what: str):
     """(rows, columns, row pitch, address) of a 2-D device operand whose columns are adjacent."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{what} must be a 2-D device tensor")
-    n, m = t.shape
+    try:
+        n, m = t.shape
+    except ValueError:
+        raise ValueError(f"{what} must be 2-D") from None
     ld, unit = t.stride()
-    if unit != 1 and m > 1:
-        raise ValueError(f"{what} must have unit column stride")
+    if (unit != 1 and m > 1) or not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor with unit column stride")
     return n, m, ld if n > 1 else max(m, ld), t.data_ptr() if n and m else None
 
 
@@ -906,43 +909,68 @@ def _out(t, n: int, m: int, dtype, like, what: str, stream):
     return t, ld, at
 
 
-@dataclass
+@functools.lru_cache(maxsize=4096)
+def _route_scratch(lib, T: int, k: int, E: int) -> int:
+    return lib.spx_route_scratch_bytes(T, k, E)
+
+
+@functools.lru_cache(maxsize=4096)
+def _i8_scratch(lib, E: int, S: int, N: int, K: int, wide: bool) -> int:
+    return lib.spx_gemm_i8_scratch_bytes(E, S, N, K, wide)
+
+
 class Route:
     """The slots of T tokens (k each) sorted by expert: int32 device tensors offsets[E + 1], slot[T * k]
-    (the flat slot at each sorted place, -1 past offsets[E]) and pos[T * k] (each slot's place, -1: dropped)."""
-    T: int
-    k: int
-    E: int
-    offsets: torch.Tensor
-    slot: torch.Tensor
-    pos: torch.Tensor
+    (the flat slot at each sorted place, -1 past offsets[E]) and pos[T * k] (each slot's place, -1: dropped).
+    The arrays are looked at here, once; their contents may change, the tensors are not to be resized."""
+    __slots__ = ("T", "k", "E", "slots", "_offsets", "_slot", "_pos")
 
-    @property
-    def slots(self) -> int:
-        return self.T * self.k
+    def __init__(self, T: int, k: int, E: int, offsets: torch.Tensor, slot: torch.Tensor, pos: torch.Tensor):
+        S = T * k
+        for t, n, what in ((offsets, E + 1, "offsets"), (slot, S, "slot"), (pos, S, "pos")):
+            if t.dtype != _I32 or t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{what} must be a dense tensor of {n} int32")
+        self.T, self.k, self.E, self.slots = T, k, E, S
+        self._offsets, self._slot, self._pos = offsets, slot, pos
+
+    offsets = property(lambda self: self._offsets)
+    slot = property(lambda self: self._slot)
+    pos = property(lambda self: self._pos)
+
+    def __repr__(self):
+        return f"Route(T={self.T}, k={self.k}, E={self.E})"
 
     def _places(self):
         """Addresses of pos and of offsets[E]."""
-        return (_vec(self.pos, self.T * self.k, torch.int32, "pos"),
-                _vec(self.offsets, self.E + 1, torch.int32, "offsets") + 4 * self.E)
+        pos, offsets = self._pos, self._offsets
+        if not (pos.is_cuda and offsets.is_cuda):
+            raise ValueError("the route's arrays must be device tensors")
+        return pos.data_ptr(), offsets.data_ptr() + 4 * self.E
 
 
 def spx_route_build(expert: torch.Tensor, E: int, stream=None, scratch: torch.Tensor | None = None) -> Route:
     """Sort the slots of expert[T, k] (int32 or int64 ids; one outside [0, E), -1 say, is dropped) by expert."""
     dt = expert.dtype
-    if dt != torch.int32 and dt != torch.int64:
+    if dt != torch.int64 and dt != _I32:
         raise ValueError("expert ids must be int32 or int64")
     T, k, lde, at = _mat(expert, "expert")
     lib = _lib()
     S = T * k
-    offsets, slot, pos = (_new(n, torch.int32, expert, stream) for n in (E + 1, S, S))
-    need = lib.spx_route_scratch_bytes(T, k, E)
-    if need and scratch is None:
-        scratch = _new(need // 4, torch.int32, expert, stream)
-    _check(lib.spx_route_build(T, k, E, at, 4 if dt == torch.int32 else 8, lde, offsets.data_ptr(),
-                               slot.data_ptr() if S else None, pos.data_ptr() if S else None, scratch.data_ptr() if need else None,
-                               scratch.numel() * scratch.element_size() if need else 0, _raw_stream(expert, stream)),
-           "spx_route_build")
+    if stream is None:
+        dev = expert.device
+        offsets, slot, pos = _empty(E + 1, dtype=_I32, device=dev), _empty(S, dtype=_I32, device=dev), _empty(S, dtype=_I32, device=dev)
+    else:
+        offsets, slot, pos = (_new(n, _I32, expert, stream) for n in (E + 1, S, S))
+    need = _route_scratch(lib, T, k, E)
+    work, size = None, 0
+    if need:
+        if scratch is None:
+            scratch = _new(need // 4, _I32, expert, stream)
+        work, size = scratch.data_ptr(), scratch.numel() * scratch.element_size()
+    rc = lib.spx_route_build(T, k, E, at, 4 if dt == _I32 else 8, lde, offsets.data_ptr(), slot.data_ptr(),
+                             pos.data_ptr(), work, size, _raw_stream(expert, stream))
+    if rc:
+        raise SpxError(rc, "spx_route_build")
     return Route(T, k, E, offsets, slot, pos)
 
 
@@ -951,10 +979,12 @@ def spx_route_gather(r: Route, X: torch.Tensor, Xs: torch.Tensor | None = None, 
     T, H, ldx, at = _mat(X, "X")
     if T != r.T:
         raise ValueError("X needs one row a token")
+    code = _type(X)
     Xs, ldxs, to = _out(Xs, r.slots, H, X.dtype, X, "Xs", stream)
     pos, end = r._places()
-    _check(_lib().spx_route_gather(T, r.k, H, _type(X), pos, end, at, ldx, to, ldxs, _raw_stream(X, stream)),
-           "spx_route_gather")
+    rc = _lib().spx_route_gather(T, r.k, H, code, pos, end, at, ldx, to, ldxs, _raw_stream(X, stream))
+    if rc:
+        raise SpxError(rc, "spx_route_gather")
     return Xs
 
 
@@ -964,10 +994,12 @@ def spx_route_combine(r: Route, Ys: torch.Tensor, weight: torch.Tensor | None = 
     S, H, ldys, at = _mat(Ys, "Ys")
     if S != r.slots:
         raise ValueError("Ys needs one row a slot")
-    w = _vec(weight, S, torch.float32, "weight") if weight is not None else None
+    code = _type(Ys)
+    w = _vec(weight, S, _F32, "weight") if weight is not None else None
     Y, ldy, to = _out(Y, r.T, H, Ys.dtype, Ys, "Y", stream)
-    _check(_lib().spx_route_combine(r.T, r.k, H, _type(Ys), r._places()[0], w, at, ldys, to, ldy, _raw_stream(Ys, stream)),
-           "spx_route_combine")
+    rc = _lib().spx_route_combine(r.T, r.k, H, code, r._places()[0], w, at, ldys, to, ldy, _raw_stream(Ys, stream))
+    if rc:
+        raise SpxError(rc, "spx_route_combine")
     return Y
 
 
@@ -977,29 +1009,33 @@ def spx_route_combine_grad(r: Route, dY: torch.Tensor, Ys: torch.Tensor | None =
     T, H, lddy, at = _mat(dY, "dY")
     if T != r.T:
         raise ValueError("dY needs one row a token")
+    code = _type(dY)
     S, ldys, ys, dw, dwp = r.slots, 0, None, None, None
     if Ys is not None:
         n, m, ldys, ys = _mat(Ys, "Ys")
         if n != S or m != H or Ys.dtype != dY.dtype:
             raise ValueError("Ys needs one row a slot")
-        dw = _new((T, r.k), torch.float32, dY, stream)
+        dw = _new((T, r.k), _F32, dY, stream)
         dwp = dw.data_ptr() if S else None
-    w = _vec(weight, S, torch.float32, "weight") if weight is not None else None
+    w = _vec(weight, S, _F32, "weight") if weight is not None else None
     dYs, lddys, to = _out(dYs, S, H, dY.dtype, dY, "dYs", stream)
     pos, end = r._places()
-    _check(_lib().spx_route_combine_grad(T, r.k, H, _type(dY), pos, end, w, at, lddy, ys, ldys, to, lddys, dwp,
-                                         _raw_stream(dY, stream)), "spx_route_combine_grad")
+    rc = _lib().spx_route_combine_grad(T, r.k, H, code, pos, end, w, at, lddy, ys, ldys, to, lddys, dwp,
+                                       _raw_stream(dY, stream))
+    if rc:
+        raise SpxError(rc, "spx_route_combine_grad")
     return dYs, dw
 
 
 def _experts(W: torch.Tensor, what: str):
     """(experts, rows, columns, row pitch, expert stride, address) of a 3-D device operand."""
-    if W.dim() != 3 or not W.is_cuda:
-        raise ValueError(f"{what} must be a 3-D device tensor")
-    E, n, m = W.shape
+    try:
+        E, n, m = W.shape
+    except ValueError:
+        raise ValueError(f"{what} must be 3-D") from None
     se, ld, unit = W.stride()
-    if unit != 1 and m > 1:
-        raise ValueError(f"{what} must have unit stride in its last axis")
+    if (unit != 1 and m > 1) or not W.is_cuda:
+        raise ValueError(f"{what} must be a device tensor with unit stride in its last axis")
     return E, n, m, ld if n > 1 else max(m, ld), se if E > 1 else 0, W.data_ptr() if E and n and m else None
 
 
@@ -1009,17 +1045,20 @@ def spx_gemm_grouped(offsets: torch.Tensor, A: torch.Tensor, W: torch.Tensor, C:
     layout "nk": W[e] holds N output channels of K; "kn": K rows of N.  C in A's type or float32 (dtype)."""
     S, K, lda, a = _mat(A, "A")
     E, N, k, ldw, sw, w = _experts(W, "W")
+    kn = 0
     if layout == "kn":
-        N, k = k, N
+        N, k, kn = k, N, 1
     elif layout != "nk":
         raise ValueError("layout must be 'nk' or 'kn'")
     dt = A.dtype
     if k != K or W.dtype != dt:
         raise ValueError("A and W do not fit")
+    code = _type(A)
     C, ldc, c = _out(C, S, N, (dtype or dt) if C is None else dtype, A, "C", stream)
-    _check(_lib().spx_gemm_grouped(E, S, N, K, _vec(offsets, E + 1, torch.int32, "offsets"), a, lda, w, ldw, sw,
-                                   0 if layout == "nk" else 1, _type(A), c, ldc, _type(C), _raw_stream(A, stream)),
-           "spx_gemm_grouped")
+    rc = _lib().spx_gemm_grouped(E, S, N, K, _vec(offsets, E + 1, _I32, "offsets"), a, lda, w, ldw, sw, kn, code, c, ldc,
+                                 _type(C), _raw_stream(A, stream))
+    if rc:
+        raise SpxError(rc, "spx_gemm_grouped")
     return C
 
 
@@ -1031,25 +1070,32 @@ def spx_gemm_grouped_wgrad(offsets: torch.Tensor, G: torch.Tensor, A: torch.Tens
     E = offsets.numel() - 1
     if n != S or G.dtype != A.dtype:
         raise ValueError("G and A do not fit")
+    code = _type(A)
     if dW is None:
         dW = _new((E, N, K), dtype or A.dtype, A, stream)
     e, n, k, ldw, sw, w = _experts(dW, "dW")
     if e != E or n != N or k != K:
         raise ValueError(f"dW must be {E} x {N} x {K}")
-    _check(_lib().spx_gemm_grouped_wgrad(E, S, N, K, _vec(offsets, E + 1, torch.int32, "offsets"), g, ldg, a, lda,
-                                         _type(A), w, ldw, sw, _type(dW), _raw_stream(A, stream)),
-           "spx_gemm_grouped_wgrad")
+    rc = _lib().spx_gemm_grouped_wgrad(E, S, N, K, _vec(offsets, E + 1, _I32, "offsets"), g, ldg, a, lda, code, w, ldw, sw,
+                                       _type(dW), _raw_stream(A, stream))
+    if rc:
+        raise SpxError(rc, "spx_gemm_grouped_wgrad")
     return dW
 
 
 def spx_quant_rows_i8(X: torch.Tensor, Q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
     """(Q int8, scale fp32): each row divided by its largest magnitude / 127 and rounded to whole numbers."""
     M, K, ldx, x = _mat(X, "X")
-    Q, ldq, q = _out(Q, M, K, torch.int8, X, "Q", stream)
+    code = _type(X)
+    Q, ldq, q = _out(Q, M, K, _I8, X, "Q", stream)
     if scale is None:
-        scale = _new(M, torch.float32, X, stream)
-    _check(_lib().spx_quant_rows_i8(M, K, _type(X), x, ldx, q, ldq, _vec(scale, M, torch.float32, "scale"),
-                                    _raw_stream(X, stream)), "spx_quant_rows_i8")
+        scale = _new(M, _F32, X, stream)
+        to = scale.data_ptr() if M else None
+    else:
+        to = _vec(scale, M, _F32, "scale")
+    rc = _lib().spx_quant_rows_i8(M, K, code, x, ldx, q, ldq, to, _raw_stream(X, stream))
+    if rc:
+        raise SpxError(rc, "spx_quant_rows_i8")
     return Q, scale
 
 
@@ -1060,22 +1106,25 @@ def spx_gemm_i8(Q: torch.Tensor, row_scale: torch.Tensor, W: torch.Tensor, w_sca
     offsets E x N x K with w_scale[E, N], each expert's weights for its rows.  C in dtype (default float32)."""
     S, K, ldq, q = _mat(Q, "Q")
     if offsets is None:
-        E, sw = 1, 0
+        E, sw, off = 1, 0, None
         N, k, ldw, w = _mat(W, "W")
     else:
         E, N, k, ldw, sw, w = _experts(W, "W")
-    if Q.dtype != torch.int8 or W.dtype != torch.int8 or k != K:
+        off = _vec(offsets, E + 1, _I32, "offsets")
+    if Q.dtype != _I8 or W.dtype != _I8 or k != K:
         raise ValueError("Q and W must be int8 and fit")
-    rs, ws = _vec(row_scale, S, torch.float32, "row_scale"), _vec(w_scale, E * N, torch.float32, "w_scale")
-    C, ldc, c = _out(C, S, N, (dtype or torch.float32) if C is None else dtype, Q, "C", stream)
+    rs, ws = _vec(row_scale, S, _F32, "row_scale"), _vec(w_scale, E * N, _F32, "w_scale")
+    C, ldc, c = _out(C, S, N, (dtype or _F32) if C is None else dtype, Q, "C", stream)
     lib = _lib()
-    need = lib.spx_gemm_i8_scratch_bytes(E, S, N, K, ((q or 0) | (w or 0) | ldq | ldw | sw) % 16 == 0)
-    if need and scratch is None:
-        scratch = _new(need, torch.uint8, Q, stream)
-    _check(lib.spx_gemm_i8(E, S, N, K, _vec(offsets, E + 1, torch.int32, "offsets") if offsets is not None else None,
-                           q, ldq, rs, w, ldw, sw, ws, c, ldc, _type(C), scratch.data_ptr() if need else None,
-                           scratch.numel() * scratch.element_size() if need else 0, _raw_stream(Q, stream)),
-           "spx_gemm_i8")
+    need = _i8_scratch(lib, E, S, N, K, ((q or 0) | (w or 0) | ldq | ldw | sw) % 16 == 0)
+    work, size = None, 0
+    if need:
+        if scratch is None:
+            scratch = _new(need, torch.uint8, Q, stream)
+        work, size = scratch.data_ptr(), scratch.numel() * scratch.element_size()
+    rc = lib.spx_gemm_i8(E, S, N, K, off, q, ldq, rs, w, ldw, sw, ws, c, ldc, _type(C), work, size, _raw_stream(Q, stream))
+    if rc:
+        raise SpxError(rc, "spx_gemm_i8")
     return C
 
 
