@@ -249,6 +249,10 @@ struct Piece<16> {
     using T = uint4;
 };
 template <>
+struct Piece<8> {
+    using T = uint2;
+};
+template <>
 struct Piece<4> {
     using T = uint32_t;
 };
@@ -368,6 +372,9 @@ __global__ void __launch_bounds__(kRowThreads)
 
 constexpr int kSlotsAtOnce = 4;  // rows of one token in flight in a thread
 
+// VB: the widest piece, of 16 bytes down to a value, that all rows are aligned
+// to (12001 tokens x 8 x 4094 fp32: 278 us in 8-byte pieces, 385 in 4-byte ones;
+// pieces put together from aligned neighbours, as the gather does, took 440).
 template <class V, int VB>
 __global__ void __launch_bounds__(kRowThreads)
     route_combine_kernel(RowShape r, const int* __restrict__ pos, const float* __restrict__ weight,
@@ -500,8 +507,9 @@ __global__ void __launch_bounds__(kRowThreads)
 // Threads a group: enough that a row of `steps` pieces is one step, no more
 // than a CTA; a warp at least (the weights' gradient reduces over warps).  The
 // gradient's groups of several warps meet at a barrier for every four slots, so
-// it takes one warp a token (`warps`) where the tokens fill the SMs: 12001
-// tokens x 8 x 130 fp32 22 us, 65 with a CTA each.
+// it takes one warp a token (`warps`: rows of wide pieces, or short ones) where
+// the tokens fill the SMs: 12001 tokens x 8 x 130 fp32 18 us, 65 with a CTA
+// each; 3001 x 3 x 1002 fp32, in 8-byte pieces, 24 and 19.
 constexpr int kWarpTokens = 152 * 16;
 
 RowShape row_shape(int T, int k, int64_t np, int64_t steps, bool warps) {
@@ -530,8 +538,7 @@ spx_status check_rows(int32_t T, int32_t k, int32_t H) {
 
 template <class V>
 int piece_bytes(uint64_t bits) {
-    const int v = copy_width(bits, static_cast<int>(sizeof(V)));
-    return v == 8 ? 4 : v;  // the kernels come in 16-byte, 4-byte and element-wise pieces
+    return copy_width(bits, static_cast<int>(sizeof(V)));
 }
 
 template <class V, int VB>
@@ -551,6 +558,7 @@ spx_status combine(int T, int k, int H, const int32_t* pos, const float* weight,
     r.b = static_cast<long long>(b / vb);
     spx_note_launches(1);
     return spx_cuda_status(vb == 16  ? combine_launch<V, 16>(r, pos, weight, Ys, Y, st)
+                           : vb == 8 ? combine_launch<V, 8>(r, pos, weight, Ys, Y, st)
                            : vb == 4 ? combine_launch<V, 4>(r, pos, weight, Ys, Y, st)
                                      : combine_launch<V, sizeof(V)>(r, pos, weight, Ys, Y, st));
 }
@@ -563,7 +571,7 @@ spx_status combine_grad(int T, int k, int H, const int32_t* pos, const int32_t* 
     const uint64_t y = dw ? ldys * sizeof(V) : 0;
     const int vb = piece_bytes<V>(addr(dY) | addr(dYs) | (dw ? addr(Ys) : 0) | row | a | b | y);
     const int64_t np = static_cast<int64_t>(row / vb);
-    RowShape r = row_shape(T, k, np, np, vb == 16 || np <= 512);
+    RowShape r = row_shape(T, k, np, np, vb == 16 || row <= 2048);
     r.a = static_cast<long long>(a);
     r.b = static_cast<long long>(b);
     const long long ly = static_cast<long long>(y);
@@ -573,6 +581,7 @@ spx_status combine_grad(int T, int k, int H, const int32_t* pos, const int32_t* 
     spx_note_launches(1);
     auto launch = [&](auto kernel) { return launch_early(kernel, grid, kRowThreads, 0, 1, st, r, pos, end, weight, dy, ly, ys, out, dw); };
     return spx_cuda_status(vb == 16  ? launch(route_combine_grad_kernel<V, 16>)
+                           : vb == 8 ? launch(route_combine_grad_kernel<V, 8>)
                            : vb == 4 ? launch(route_combine_grad_kernel<V, 4>)
                                      : launch(route_combine_grad_kernel<V, sizeof(V)>));
 }
