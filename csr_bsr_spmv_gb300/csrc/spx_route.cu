@@ -326,12 +326,16 @@ __device__ __forceinline__ uint4 read16(const char* p, const char* lo, const cha
                       __funnelshift_r(u3, u4, sh));
 }
 
-// V: the copied values' type, or any of their size.  Rows off 16-byte
-// boundaries: each written row is cut at its own boundaries -- a head of single
-// values, aligned pieces, a tail -- so that wide stores fill whole sectors, and
-// the token's row, which L1 holds, is read around them (96008 rows of 4095 fp32:
-// 295 us, 438 with 4-byte stores where they fall).
-template <class V, bool ALIGNED>
+// V: the copied values' type, or any of their size.  VB: rows on boundaries of
+// 16 or 8 bytes move in pieces of that; 0: each written row is cut at its own
+// 16-byte boundaries -- a head of single values, aligned pieces, a tail -- so
+// that wide stores fill whole sectors, and the token's row, which L1 holds, is
+// read around them.  12001 tokens x 8 fp32: rows of 4095 285 us so, 438 with
+// 4-byte stores where they fall; of 4094 286 so and 344 in 8-byte pieces; of 130
+// 20 and 12: rows on 8-byte boundaries are cut from kCutRow bytes on.
+constexpr long long kCutRow = 8192;
+
+template <class V, int VB>
 __global__ void __launch_bounds__(kRowThreads)
     route_gather_kernel(RowShape r, const int* __restrict__ pos, const int* __restrict__ end, const V* __restrict__ X,
                         V* __restrict__ Xs) {
@@ -341,17 +345,18 @@ __global__ void __launch_bounds__(kRowThreads)
     if (t >= r.T) return;
     const int S = r.T * r.k, v0 = blockIdx.y * r.G + threadIdx.x % r.G, dv = gridDim.y * r.G;
     const long long i0 = static_cast<long long>(t) * r.k;
-    constexpr int N = 16 / sizeof(V);
     const V* x = X + t * r.a;
-    if (ALIGNED) {
-        for (int v = v0; v < r.np / N; v += dv) {
-            const uint4 piece = __ldg(reinterpret_cast<const uint4*>(x) + v);
+    if constexpr (VB > 0) {
+        using P = typename Piece<VB>::T;
+        for (int v = v0; v < r.np / static_cast<int>(VB / sizeof(V)); v += dv) {
+            const P piece = __ldg(reinterpret_cast<const P*>(x) + v);
             for (int j = 0; j < r.k; ++j) {
                 const int p = place(pos, i0 + j, S);
-                if (p >= 0) __stcs(reinterpret_cast<uint4*>(Xs + p * r.b) + v, piece);
+                if (p >= 0) __stcs(reinterpret_cast<P*>(Xs + p * r.b) + v, piece);
             }
         }
     } else {
+        constexpr int N = 16 / sizeof(V);
         const char *lo = reinterpret_cast<const char*>(X), *hi = reinterpret_cast<const char*>(X + (r.T - 1) * r.a + r.np);
         for (int j = 0; j < r.k; ++j) {
             const int p = place(pos, i0 + j, S);
@@ -589,15 +594,18 @@ spx_status combine_grad(int T, int k, int H, const int32_t* pos, const int32_t* 
 template <class V>
 spx_status gather(int T, int k, int H, const int32_t* pos, const int32_t* end, const void* X, int64_t ldx, void* Xs,
                   int64_t ldxs, cudaStream_t st) {
-    const int64_t pieces = (H + 16 / sizeof(V) - 1) / (16 / sizeof(V));
+    const uint64_t bits = addr(X) | addr(Xs) | (static_cast<uint64_t>(H) | ldx | ldxs) * sizeof(V);
+    const int vb = bits % 16 == 0 ? 16 : bits % 8 == 0 && H * static_cast<long long>(sizeof(V)) < kCutRow ? 8 : 0;
+    const int64_t per = (vb ? vb : 16) / sizeof(V), pieces = (H + per - 1) / per;
     RowShape r = row_shape(T, k, H, pieces, false);
     r.a = ldx;
     r.b = ldxs;
     const V* x = static_cast<const V*>(X);
     V* xs = static_cast<V*>(Xs);
-    const uint64_t bits = addr(X) | addr(Xs) | (static_cast<uint64_t>(H) | ldx | ldxs) * sizeof(V);
     spx_note_launches(1);
-    return spx_cuda_status(launch_early(bits % 16 == 0 ? route_gather_kernel<V, true> : route_gather_kernel<V, false>,
+    return spx_cuda_status(launch_early(vb == 16  ? route_gather_kernel<V, 16>
+                                        : vb == 8 ? route_gather_kernel<V, 8>
+                                                  : route_gather_kernel<V, 0>,
                                         row_grid(r, pieces, true), kRowThreads, 0, 1, st, r, pos, end, x, xs));
 }
 
