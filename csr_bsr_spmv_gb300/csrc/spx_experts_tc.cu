@@ -8,16 +8,24 @@
 // The MMA computes the transposed tile: its 128 lanes (256 for a CTA pair)
 // run along the output's contiguous axis -- n, or k for kWG -- and its columns
 // along the output's rows -- tokens, or n for kWG.  So each TMEM lane is one
-// output column and a warp's store of one accumulator column is one contiguous
-// run of an output row, whatever the row's alignment; and the ragged number of
-// an expert's rows is the MMA's N, which comes in steps of 16, so a short last
-// tile costs the time of its own rows, not of a whole tile, and a handful of
-// decoded tokens runs on the same kernel as a prefill batch.
+// output column; and the ragged number of an expert's rows is the MMA's N, which
+// comes in steps of 16, so a short last tile costs the time of its own rows, not
+// of a whole tile, and a handful of decoded tokens runs on the same kernel as a
+// prefill batch.
 //
-// Persistent: each CTA (pair) walks a static list of tiles; a TMA warp keeps a
-// ring of 64-deep stages filled across tiles, one thread issues the MMAs into
-// one of two TMEM accumulators, four warps store the other one.  The tile list
+// Persistent: each CTA (pair) walks a static list of tiles; two TMA warps keep
+// a ring of 64-deep stages filled across tiles, one thread issues the MMAs into
+// one of two TMEM accumulators, eight warps store the other one.  The tile list
 // comes from the offsets on the device: nothing waits for the host.
+//
+// What bounds it, measured: whole 256 x 256 tiles of a CTA pair run at the
+// tensor rate (32768 rows x 2048 x 4096 over 16 experts, even: 287 us, 1913
+// TFLOP/s; tensor pipe 91% active in ncu on the uneven case), for seconds on end
+// at the power limit (335 us; a library product of the same size 313).  Few rows
+// are bound by the weights' bytes (32 rows, 23 experts of 2048 x 2048 hit: 34 us,
+// 5.6 TB/s), the smallest by a fixed cost (16 rows x 128 x 64: 3.8 us), a weight
+// gradient over few rows by its stores (537 MB of gradients in 157 us; filling
+// that memory takes 141).
 //
 // Every mbarrier wait is bounded; on expiry the CTA records an error word
 // (read by spx_last_device_error), stops, waits (bounded) for its copies and
@@ -49,7 +57,8 @@ constexpr uint32_t kBox = 64 * kDepth * 2;      // an MN-major box: 64 long, 64 
 constexpr int kMaxStages = 12;
 // 8-bit codes are held as fp16, exactly; a product is at most 2^14 and an fp32
 // sum of 1024 of them at most 2^24, so every partial sum up to there is an
-// exact whole number.  Longer sums go to int32 registers every 1024 terms.
+// exact whole number.  Longer sums go to int32 every 1024 terms, in
+// registers or, with a shared reduction, in shared memory.
 constexpr int kExact = 1024;
 constexpr int kBand = 8;                        // row tiles that run side by side before the next lane tile
 constexpr size_t kSmemMax = 224 * 1024;         // dynamic shared memory of a CTA
@@ -320,9 +329,8 @@ constexpr uint32_t kPatchPitch = 80, kPatchBytes = 32 * kPatchPitch;
 // Stores 32 output rows from it.row0 + c0 on of the output columns x .. x + 31.
 // 16-bit rows on 16-byte boundaries (`wide`) go through the warp's patch of
 // shared memory: stmatrix transposes 8 x 8 blocks, and each store then covers
-// eight rows of 64 bytes (about 50 instructions for the 1024 values against
-// 160 for storing each by itself; one storing warp a scheduler issues them, so
-// their number is what the stores cost).
+// eight rows of 64 bytes (weight gradients of 64 experts of 2048 x 2048: 170 us,
+// 182 with each value stored by itself).
 template <class O>
 __device__ __forceinline__ void store_rows(const TcArgs& a, const Item& it, O* C, int x, int lane, bool wide,
                                            uint32_t patch, int c0, const float (&v)[32]) {
@@ -392,8 +400,8 @@ __device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, lon
 // FUSE: the factors are 8-bit codes.  Their bytes arrive in a ring of raw
 // stages, and eight more warps widen them to fp16 into the ring the MMAs read.
 // The weights then cost one byte each wherever they come from, against five
-// through a widened copy in memory; but every stage passes through shared
-// memory twice more, which bounds it at 470 to 800 cycles a stage.
+// through a widened copy in memory; but the widening bounds a stage: 900 cycles
+// with 32 rows, 985 with 64, 1165 with 128 (from the time's slope over K).
 // SPLIT: a cluster of a.split CTAs shares each tile, every one the products of
 // its part of the reduction; the partial tiles meet in shared memory, where
 // CTA r adds the parts of its share of the rows in rank order.
@@ -1080,14 +1088,14 @@ enum Kind { kProduct, kGradient, kCodes };  // kCodes: 8-bit factors widened on 
 // next tile's MMAs; rounds of tiles count whole.  Sharing a reduction costs
 // about 1500 cycles a CTA for the exchange.  512 rows x 4096 x 4096: 128-row
 // tiles 19 us, 256-row pairs 25, 64-row tiles 30; 16 rows: one CTA a tile 16.5
-// us, two 13.0, four 11.6, eight 16.1.  `mean` rows (kWG: terms) an expert.
+// us, two 13.0, four 11.6, eight 16.1.
 int choose_tile(TcArgs& a, Kind kind) {
     const bool wgrad = kind == kGradient, fused = kind == kCodes;
     struct Shape {
         int tn, cg, stage;
     };
     constexpr Shape shapes[] = {{256, 2, 615}, {256, 1, 725}, {128, 2, 435}, {128, 1, 460}, {64, 1, 390}, {32, 1, 350}};
-    constexpr Shape codes[] = {{128, 1, 800}, {64, 1, 570}, {32, 1, 470}};  // FUSE
+    constexpr Shape codes[] = {{128, 1, 1165}, {64, 1, 985}, {32, 1, 900}};  // FUSE, measured
     const Shape *from = fused ? codes : shapes, *to = fused ? codes + 3 : shapes + 6;
     const double mean = static_cast<double>(a.S) / a.E, used = std::min(a.E, a.S);
     const int sms = sm_count();

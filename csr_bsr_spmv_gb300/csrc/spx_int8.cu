@@ -223,9 +223,9 @@ cudaError_t quant_launch(int M, int K, const void* X, int64_t ldx, int8_t* Q, in
 // operands of four m16n8k16 products, widened to fp16 in registers; up to eight
 // rows they are those of two integer m16n8k32 products as they are (which run
 // at a quarter of the fp16 form's rate here, 151 against 601 Tops, but eight
-// rows need no more, and widening costs 60 of a chunk's 75 instructions).  a.ks warps of a CTA share a channel block's reduction, in
-// turns of 64 terms, where there are few blocks; their sums meet in shared
-// memory.  A warp's fp32 sums go to int32 every 1024 terms, so they are exact.
+// rows need no more, and there is nothing to widen).  a.ks warps of a CTA share
+// a channel block's reduction, in turns of 64 terms, where there are few blocks;
+// their sums meet in shared memory.  A warp's fp32 sums go to int32 every 1024 terms, so they are exact.
 
 constexpr long long kFewEnough = 152 * 64;  // warps that keep the memory busy
 
@@ -339,23 +339,23 @@ __global__ void __launch_bounds__(32 * WARPS) i8_few_kernel(FewArgs a) {
                     }
                     continue;
                 } else {
-                uint2 f[2 * MT][4];
+                    uint2 f[2 * MT][4];
 #pragma unroll
-                for (int m = 0; m < 2 * MT; ++m) {
-                    f[m][0] = widen_codes(x[u][m].x), f[m][1] = widen_codes(x[u][m].y);
-                    f[m][2] = widen_codes(x[u][m].z), f[m][3] = widen_codes(x[u][m].w);
-                }
+                    for (int m = 0; m < 2 * MT; ++m) {
+                        f[m][0] = widen_codes(x[u][m].x), f[m][1] = widen_codes(x[u][m].y);
+                        f[m][2] = widen_codes(x[u][m].z), f[m][3] = widen_codes(x[u][m].w);
+                    }
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int4 y = in ? __ldg(reinterpret_cast<const int4*>(q[b] + k)) : make_int4(0, 0, 0, 0);
-                    const uint2 h[4] = {widen_codes(y.x), widen_codes(y.y), widen_codes(y.z), widen_codes(y.w)};
+                    for (int b = 0; b < NB; ++b) {
+                        const int4 y = in ? __ldg(reinterpret_cast<const int4*>(q[b] + k)) : make_int4(0, 0, 0, 0);
+                        const uint2 h[4] = {widen_codes(y.x), widen_codes(y.y), widen_codes(y.z), widen_codes(y.w)};
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                        for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            mma16816(acc[m][b], f[2 * m][s].x, f[2 * m + 1][s].x, f[2 * m][s].y, f[2 * m + 1][s].y, h[s].x,
-                                     h[s].y);
-                }
+                            for (int s = 0; s < 4; ++s)
+                                mma16816(acc[m][b], f[2 * m][s].x, f[2 * m + 1][s].x, f[2 * m][s].y, f[2 * m + 1][s].y, h[s].x,
+                                         h[s].y);
+                    }
                 }
             }
             done += 64 * U;

@@ -861,7 +861,7 @@ typedef enum spx_w_layout {
  * product with respect to A is the SPX_W_KN product of C's gradient with the
  * same weights, and the other way round.  offsets (device, int32[E+1]) is not
  * read on the host: nothing waits for the routing.  K == 0 gives zeros.
- * Launches: 1 or 2.
+ * Launches: 1.
  */
 spx_status spx_gemm_grouped(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const void* A,
                             int64_t lda, const void* W, int64_t ldw, int64_t stride_w, spx_w_layout layout,
