@@ -20,7 +20,7 @@
 //
 // What bounds it, measured: whole 256 x 256 tiles of a CTA pair run at the
 // tensor rate (32768 rows x 2048 x 4096 over 16 experts, even: 287 us, 1913
-// TFLOP/s; tensor pipe 91% active in ncu on the uneven case), for seconds on end
+// TFLOP/s; tensor pipe 85% active in ncu, uneven, 304 us), for seconds on end
 // at the power limit (335 us; a library product of the same size 313).  Few rows
 // are bound by the weights' bytes (32 rows, 23 experts of 2048 x 2048 hit: 34 us,
 // 5.6 TB/s), the smallest by a fixed cost (16 rows x 128 x 64: 3.8 us), a weight
