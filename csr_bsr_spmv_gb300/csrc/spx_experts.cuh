@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "spx_internal.h"
 
@@ -42,12 +43,6 @@ __device__ __forceinline__ uint2 widen_codes(uint32_t w) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Rows [lo, hi) of expert e, whatever the offsets hold: inside [0, S], lo <= hi.
-__device__ __forceinline__ void expert_rows(const int* __restrict__ offsets, int e, int S, int& lo, int& hi) {
-    lo = min(max(__ldg(offsets + e), 0), S);
-    hi = min(max(__ldg(offsets + e + 1), lo), S);
-}
-
 // The calls of a layer follow one another on a stream and run for a few
 // microseconds each, so every kernel waits for the one before -- all of it --
 // only when it is about to touch global memory, and the short ones let the next
@@ -56,6 +51,53 @@ __device__ __forceinline__ void expert_rows(const int* __restrict__ offsets, int
 // 125 -> 118 us).
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Such a kernel is on its SM while the calls before it still write what it is
+// going to read.  The read-only path (__ldg, const __restrict__) is for memory
+// that nobody writes during the kernel's life, so every read of an array goes
+// through the coherent loads below, volatile so that none moves above
+// wait_for_previous().  load_once: a hint that the data is not read again.
+#define SPX_EXP_LOAD(name, op)                                                                            \
+    template <class T>                                                                                    \
+    __device__ __forceinline__ T name(const T* p) {                                                       \
+        static_assert(sizeof(T) == 1 || sizeof(T) == 2 || sizeof(T) == 4 || sizeof(T) == 8 || sizeof(T) == 16); \
+        const size_t at = __cvta_generic_to_global(p);                                                    \
+        T v;                                                                                              \
+        if constexpr (sizeof(T) == 16) {                                                                  \
+            uint4 w;                                                                                      \
+            asm volatile(op ".v4.b32 {%0, %1, %2, %3}, [%4];"                                             \
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)                                     \
+                         : "l"(at));                                                                      \
+            memcpy(&v, &w, 16);                                                                           \
+        } else if constexpr (sizeof(T) == 8) {                                                            \
+            uint2 w;                                                                                      \
+            asm volatile(op ".v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(at));                  \
+            memcpy(&v, &w, 8);                                                                            \
+        } else if constexpr (sizeof(T) == 4) {                                                            \
+            uint32_t w;                                                                                   \
+            asm volatile(op ".b32 %0, [%1];" : "=r"(w) : "l"(at));                                        \
+            memcpy(&v, &w, 4);                                                                            \
+        } else if constexpr (sizeof(T) == 2) {                                                            \
+            uint16_t w;                                                                                   \
+            asm volatile(op ".b16 %0, [%1];" : "=h"(w) : "l"(at));                                        \
+            memcpy(&v, &w, 2);                                                                            \
+        } else {                                                                                          \
+            uint32_t w;                                                                                   \
+            asm volatile(op ".u8 %0, [%1];" : "=r"(w) : "l"(at));                                         \
+            const uint8_t b = static_cast<uint8_t>(w);                                                    \
+            memcpy(&v, &b, 1);                                                                            \
+        }                                                                                                 \
+        return v;                                                                                         \
+    }
+SPX_EXP_LOAD(load, "ld.global")
+SPX_EXP_LOAD(load_once, "ld.global.cs")
+#undef SPX_EXP_LOAD
+
+// Rows [lo, hi) of expert e, whatever the offsets hold: inside [0, S], lo <= hi.
+__device__ __forceinline__ void expert_rows(const int* offsets, int e, int S, int& lo, int& hi) {
+    lo = min(max(load(offsets + e), 0), S);
+    hi = min(max(load(offsets + e + 1), lo), S);
+}
 
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st,
@@ -96,7 +138,7 @@ namespace spx_exp {
 // Row tile `tile` of height TM over the experts' rows, experts in order, the
 // rows from offsets[E] on as one more "expert" E: which expert, its rows
 // [r0, hi).  False when there is no such tile.  One full warp.
-__device__ __forceinline__ bool warp_find_tile(const int* __restrict__ offsets, int E, int S, int TM, int tile, int& e,
+__device__ __forceinline__ bool warp_find_tile(const int* offsets, int E, int S, int TM, int tile, int& e,
                                                int& r0, int& hi) {
     const int lane = threadIdx.x & 31;
     constexpr int P = 4;  // experts a lane looks at in a round, their offsets read side by side
@@ -108,7 +150,7 @@ __device__ __forceinline__ bool warp_find_tile(const int* __restrict__ offsets, 
             const int x = e0 + lane * P + i;
             lo[i] = up[i] = 0;
             if (x < E) expert_rows(offsets, x, S, lo[i], up[i]);
-            else if (x == E) lo[i] = min(max(__ldg(offsets + E), 0), S), up[i] = S;
+            else if (x == E) lo[i] = min(max(load(offsets + E), 0), S), up[i] = S;
             n += (up[i] - lo[i] + TM - 1) / TM;
         }
         int inc = n;

@@ -17,12 +17,12 @@ constexpr int kT = 64, kR = 32, kThreads = 256;
 // 64 x 32 elements (x, r) of M at base + x * sx + r * sr, zeros outside [0, nx) x [0, nr); neighbouring
 // threads take neighbouring addresses.
 template <class V>
-__device__ __forceinline__ void stage(float (*s)[kT + 1], const V* __restrict__ M, long long sx, long long sr, int nx,
+__device__ __forceinline__ void stage(float (*s)[kT + 1], const V* M, long long sx, long long sr, int nx,
                                       int nr) {
     const bool along_r = sr == 1;
     for (int i = threadIdx.x; i < kT * kR; i += kThreads) {
         const int x = along_r ? i / kR : i % kT, r = along_r ? i % kR : i / kT;
-        s[r][x] = x < nx && r < nr ? to_f(M[x * sx + r * sr]) : 0.f;
+        s[r][x] = x < nx && r < nr ? to_f(load(M + x * sx + r * sr)) : 0.f;
     }
 }
 

@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
         int lo = 0, hi = a.S;
         if (a.offsets) {
             if (e < a.E) expert_rows(a.offsets, e, a.S, lo, hi);
-            else lo = min(max(__ldg(a.offsets + a.E), 0), a.S);
+            else lo = min(max(load(a.offsets + a.E), 0), a.S);
         } else if (e == a.E) {
             lo = hi;
         }
@@ -874,7 +874,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             float cs[4] = {0.f, 0.f, 0.f, 0.f};
             if (I8 && it.e < a.E)
                 for (int i = 0; i < 4; ++i)
-                    if (col + i < a.NL) cs[i] = __ldg(a.col_scale + static_cast<long long>(it.e) * a.NL + col + i);
+                    if (col + i < a.NL) cs[i] = load(a.col_scale + static_cast<long long>(it.e) * a.NL + col + i);
             for (int r = part * per + warp; r < min((part + 1) * per, it.rows); r += kStoreWarps) {
                 uint32_t v[4], sum[4] = {0u, 0u, 0u, 0u};
                 for (int p = 0; p < a.split; ++p) {
@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                         sum[i] = I8 ? sum[i] + v[i] : __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
                 }
                 float f[4];
-                const float rs = I8 ? __ldg(a.row_scale + it.row0 + r) : 1.f;
+                const float rs = I8 ? load(a.row_scale + it.row0 + r) : 1.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     f[i] = !I8 ? __uint_as_float(sum[i])
@@ -969,7 +969,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int n = x + 8 * g + (lane >> 2);
-                cs[g] = it.e < a.E && n < a.NL ? __ldg(a.col_scale + static_cast<long long>(it.e) * a.NL + n) : 0.f;
+                cs[g] = it.e < a.E && n < a.NL ? load(a.col_scale + static_cast<long long>(it.e) * a.NL + n) : 0.f;
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -979,7 +979,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {  // this thread's eight rows of the 32
                     const int row = 8 * (r >> 1) + 2 * (lane & 3) + (r & 1);
-                    const float rs = __ldg(a.row_scale + min(it.row0 + c0 + row, a.S - 1));
+                    const float rs = load(a.row_scale + min(it.row0 + c0 + row, a.S - 1));
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const int i = 16 * (g >> 1) + 4 * (r >> 1) + 2 * (g & 1) + (r & 1);

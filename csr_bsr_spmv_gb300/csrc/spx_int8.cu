@@ -33,7 +33,7 @@ struct alignas(N * sizeof(V) >= 16 ? 16 : N * sizeof(V)) Pack {
     V v[N];
 };
 
-// A piece is read and written as one word of its size.
+// A piece is written as one word of its size.
 template <int BYTES>
 struct Word;
 template <>
@@ -56,14 +56,6 @@ template <>
 struct Word<1> {
     using T = uint8_t;
 };
-template <class P>
-__device__ __forceinline__ P read_piece(const P* p) {
-    using T = typename Word<sizeof(P)>::T;
-    const T w = __ldcs(reinterpret_cast<const T*>(p));
-    P r;
-    memcpy(&r, &w, sizeof(P));
-    return r;
-}
 template <class P>
 __device__ __forceinline__ void write_piece(P* p, const P& v) {
     using T = typename Word<sizeof(P)>::T;
@@ -135,8 +127,7 @@ __device__ __noinline__ Pack<int8_t, N> divided_codes(Pack<V, N> p, float s) {
 // N values a piece: 16 bytes of X where rows are aligned, else 1 value.
 template <class V, int N, int G>
 __global__ void __launch_bounds__(kQThreads, 10)
-    quant_rows_kernel(int M, int K, const V* __restrict__ X, long long ldx, int8_t* __restrict__ Q, long long ldq,
-                      float* __restrict__ scale) {
+    quant_rows_kernel(int M, int K, const V* X, long long ldx, int8_t* Q, long long ldq, float* scale) {
     using P = Pack<V, N>;
     using B = Pack<int8_t, N>;
     __shared__ uint32_t s_max[kQThreads / 32];
@@ -151,11 +142,11 @@ __global__ void __launch_bounds__(kQThreads, 10)
     P held[kQHeld];
 #pragma unroll
     for (int h = 0; h < kQHeld; ++h)
-        if (at + h * G < np) held[h] = read_piece(x + at + h * G);
+        if (at + h * G < np) held[h] = load_once(x + at + h * G);
 #pragma unroll
     for (int h = 0; h < kQHeld; ++h)
         if (at + h * G < np) big.look(held[h]);
-    for (int k = at + kQHeld * G; k < np; k += G) big.look(read_piece(x + k));
+    for (int k = at + kQHeld * G; k < np; k += G) big.look(load_once(x + k));
     uint32_t m = big.bits();
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -192,7 +183,7 @@ __global__ void __launch_bounds__(kQThreads, 10)
 #pragma unroll
     for (int h = 0; h < kQHeld; ++h)
         if (at + h * G < np) write_piece(q + at + h * G, code(held[h]));
-    for (int k = at + kQHeld * G; k < np; k += G) write_piece(q + k, code(read_piece(x + k)));
+    for (int k = at + kQHeld * G; k < np; k += G) write_piece(q + k, code(load_once(x + k)));
 }
 
 template <class V, int N>
@@ -322,7 +313,7 @@ __global__ void __launch_bounds__(32 * WARPS) i8_few_kernel(FewArgs a) {
                 const bool in = k + 16 * t < a.K;  // K is a multiple of 16
 #pragma unroll
                 for (int m = 0; m < 2 * MT; ++m)
-                    x[u][m] = in ? __ldcs(reinterpret_cast<const int4*>(w[m] + k)) : make_int4(0, 0, 0, 0);
+                    x[u][m] = in ? load_once(reinterpret_cast<const int4*>(w[m] + k)) : make_int4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -330,7 +321,7 @@ __global__ void __launch_bounds__(32 * WARPS) i8_few_kernel(FewArgs a) {
                 if (k >= a.K) break;
                 const bool in = k + 16 * t < a.K;
                 if constexpr (INT) {
-                    const int4 y = in ? __ldg(reinterpret_cast<const int4*>(q[0] + k)) : make_int4(0, 0, 0, 0);
+                    const int4 y = in ? load(reinterpret_cast<const int4*>(q[0] + k)) : make_int4(0, 0, 0, 0);
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         const int4 &lo = x[u][2 * m], &up = x[u][2 * m + 1];
@@ -347,7 +338,7 @@ __global__ void __launch_bounds__(32 * WARPS) i8_few_kernel(FewArgs a) {
                     }
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        const int4 y = in ? __ldg(reinterpret_cast<const int4*>(q[b] + k)) : make_int4(0, 0, 0, 0);
+                        const int4 y = in ? load(reinterpret_cast<const int4*>(q[b] + k)) : make_int4(0, 0, 0, 0);
                         const uint2 h[4] = {widen_codes(y.x), widen_codes(y.y), widen_codes(y.z), widen_codes(y.w)};
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
@@ -377,8 +368,8 @@ __global__ void __launch_bounds__(32 * WARPS) i8_few_kernel(FewArgs a) {
         if (r >= R || n >= a.N) continue;
         int sum = 0;
         for (int p = 0; p < a.ks; ++p) sum += part[first + p][i];
-        const float v = e < a.E ? static_cast<float>(sum) * (__ldg(a.row_scale + r0 + r) *
-                                                             __ldg(a.col_scale + static_cast<long long>(e) * a.N + n))
+        const float v = e < a.E ? static_cast<float>(sum) * (load(a.row_scale + r0 + r) *
+                                                             load(a.col_scale + static_cast<long long>(e) * a.N + n))
                                 : 0.f;
         few_store(a, (r0 + r) * a.ldc + n, v);
     }
@@ -432,10 +423,10 @@ __global__ void __launch_bounds__(kRowThreads) i8_row_kernel(FewArgs a) {
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int c = 0; c < kRowChan; ++c)
-                    y[u][c] = p0 + 32 * u < np ? __ldcs(w[c] + p0 + 32 * u) : make_int4(0, 0, 0, 0);
+                    y[u][c] = p0 + 32 * u < np ? load_once(w[c] + p0 + 32 * u) : make_int4(0, 0, 0, 0);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int4 x = p0 + 32 * u < np ? __ldg(q + p0 + 32 * u) : make_int4(0, 0, 0, 0);
+                const int4 x = p0 + 32 * u < np ? load(q + p0 + 32 * u) : make_int4(0, 0, 0, 0);
 #pragma unroll
                 for (int c = 0; c < kRowChan; ++c) {
                     sum[c] = __dp4a(x.x, y[u][c].x, sum[c]);
@@ -453,7 +444,7 @@ __global__ void __launch_bounds__(kRowThreads) i8_row_kernel(FewArgs a) {
         if (lane == c && n0 + c < a.N)
             few_store(a, p * a.ldc + n0 + c,
                       e < a.E ? static_cast<float>(sum[c]) *
-                                    (__ldg(a.row_scale + p) * __ldg(a.col_scale + static_cast<long long>(e) * a.N + n0 + c))
+                                    (load(a.row_scale + p) * load(a.col_scale + static_cast<long long>(e) * a.N + n0 + c))
                               : 0.f);
     }
 }
@@ -485,9 +476,8 @@ constexpr int kWidenThreads = 256;
 
 template <bool ALIGNED>
 __global__ void __launch_bounds__(kWidenThreads)
-    widen_kernel(const int* __restrict__ offsets, int S, int N, int K, int Kp, const int8_t* __restrict__ Q,
-                 long long ldq, const int8_t* __restrict__ W, long long ldw, long long stride_w,
-                 __half* __restrict__ Q16, __half* __restrict__ W16, bool same_w) {
+    widen_kernel(const int* offsets, int S, int N, int K, int Kp, const int8_t* Q, long long ldq, const int8_t* W,
+                 long long ldw, long long stride_w, __half* Q16, __half* W16, bool same_w) {
     let_next_start();
     wait_for_previous();
     const int8_t* src = Q;
@@ -517,12 +507,12 @@ __global__ void __launch_bounds__(kWidenThreads)
                 const int k = 8 * (p0 + 32 * u);
                 w[u] = make_uint2(0u, 0u);
                 if (ALIGNED && k + 8 <= K) {
-                    w[u] = __ldcs(reinterpret_cast<const uint2*>(s + k));
+                    w[u] = load_once(reinterpret_cast<const uint2*>(s + k));
                 } else {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         if (k + c < K)
-                            (c < 4 ? w[u].x : w[u].y) |= static_cast<uint32_t>(static_cast<uint8_t>(s[k + c])) << (8 * (c & 3));
+                            (c < 4 ? w[u].x : w[u].y) |= static_cast<uint32_t>(static_cast<uint8_t>(load(s + k + c))) << (8 * (c & 3));
                 }
             }
 #pragma unroll

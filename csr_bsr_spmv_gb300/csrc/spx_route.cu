@@ -38,10 +38,10 @@ struct Ids {
 __device__ __forceinline__ int id_of(const Ids& x, int i, int E) {
     const long long at = x.lde == x.k ? i : static_cast<long long>(i / x.k) * x.lde + i % x.k;
     if (x.bytes == 4) {
-        const int e = __ldg(static_cast<const int*>(x.p) + at);
+        const int e = load(static_cast<const int*>(x.p) + at);
         return e >= 0 && e < E ? e : -1;
     }
-    const long long e = __ldg(static_cast<const long long*>(x.p) + at);
+    const long long e = load(static_cast<const long long*>(x.p) + at);
     return e >= 0 && e < E ? static_cast<int>(e) : -1;
 }
 
@@ -70,7 +70,7 @@ __device__ __forceinline__ void rank_run(const Ids& x, int E, int w0, int end, i
 
 // The block's slots of each expert, for the sort of more slots than a cluster holds.
 __global__ void __launch_bounds__(32 * kMostWarps)
-    route_count_kernel(Ids x, int S, int E, int runs, int* __restrict__ hist) {
+    route_count_kernel(Ids x, int S, int E, int runs, int* hist) {
     extern __shared__ int sm[];
     let_next_start();
     wait_for_previous();
@@ -88,8 +88,7 @@ __global__ void __launch_bounds__(32 * kMostWarps)
 // A block places `runs` rounds of blockDim.x * kHeld consecutive slots.  The other blocks' counts come from `hist`
 // (counted before, any number of blocks), or (hist NULL) from the other CTAs of the cluster that the grid is.
 __global__ void __launch_bounds__(32 * kMostWarps)
-    route_place_kernel(Ids x, int S, int E, int runs, const int* __restrict__ hist, int* __restrict__ offsets,
-                       int* __restrict__ slot, int* __restrict__ pos) {
+    route_place_kernel(Ids x, int S, int E, int runs, const int* hist, int* offsets, int* slot, int* pos) {
     extern __shared__ int sm[];  // counters of each warp (ES apart), E + 1 totals, E places before this block, E counts of it
     const int nw = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = gridDim.x, b = blockIdx.x;
     const int ES = E | 1;  // odd: a column of the counters touches every bank
@@ -140,7 +139,7 @@ __global__ void __launch_bounds__(32 * kMostWarps)
             int all = 0, lower = 0;
 #pragma unroll 4
             for (int o = i / E; o < nb; o += parts) {
-                const int n = __ldg(hist + static_cast<long long>(o) * E + e);
+                const int n = load(hist + static_cast<long long>(o) * E + e);
                 all += n;
                 lower += o < b ? n : 0;
             }
@@ -288,16 +287,16 @@ struct RowShape {
     long long a, b;            // row pitch in pieces of the token-ordered and of the sorted array
 };
 
-__device__ __forceinline__ int place(const int* __restrict__ pos, long long i, int S) {
-    const int p = __ldg(pos + i);
+__device__ __forceinline__ int place(const int* pos, long long i, int S) {
+    const int p = load(pos + i);
     return p >= 0 && p < S ? p : -1;
 }
 
 // Zeros in the sorted array's rows from offsets[E] on: token t's group takes every T-th of them.
 template <class P>
-__device__ __forceinline__ void zero_tail(const RowShape& r, const int* __restrict__ end, int t, int v0, int dv, P* out) {
+__device__ __forceinline__ void zero_tail(const RowShape& r, const int* end, int t, int v0, int dv, P* out) {
     const int S = r.T * r.k;
-    for (long long p = min(max(__ldg(end), 0), S) + static_cast<long long>(t); p < S; p += r.T)
+    for (long long p = min(max(load(end), 0), S) + static_cast<long long>(t); p < S; p += r.T)
         for (int v = v0; v < r.np; v += dv) memset(out + p * r.b + v, 0, sizeof(P));
 }
 
@@ -307,16 +306,16 @@ template <class V>
 __device__ __forceinline__ uint4 read16(const char* p, const char* lo, const char* hi) {
     const int m = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
     const char* at = p - m;
-    if (m == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+    if (m == 0) return load(reinterpret_cast<const uint4*>(p));
     if (at < lo || at + 32 > hi) {
         V v[16 / sizeof(V)];
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(16 / sizeof(V)); ++i) v[i] = reinterpret_cast<const V*>(p)[i];
+        for (int i = 0; i < static_cast<int>(16 / sizeof(V)); ++i) v[i] = load(reinterpret_cast<const V*>(p) + i);
         uint4 w;
         memcpy(&w, v, 16);
         return w;
     }
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(at)), y = __ldg(reinterpret_cast<const uint4*>(at) + 1);
+    const uint4 x = load(reinterpret_cast<const uint4*>(at)), y = load(reinterpret_cast<const uint4*>(at) + 1);
     const bool two = m & 8, one = m & 4;
     const uint32_t t0 = two ? x.z : x.x, t1 = two ? x.w : x.y, t2 = two ? y.x : x.z, t3 = two ? y.y : x.w,
                    t4 = two ? y.z : y.x, t5 = two ? y.w : y.y;
@@ -337,8 +336,7 @@ constexpr long long kCutRow = 8192;
 
 template <class V, int VB>
 __global__ void __launch_bounds__(kRowThreads)
-    route_gather_kernel(RowShape r, const int* __restrict__ pos, const int* __restrict__ end, const V* __restrict__ X,
-                        V* __restrict__ Xs) {
+    route_gather_kernel(RowShape r, const int* pos, const int* end, const V* X, V* Xs) {
     let_next_start();
     wait_for_previous();
     const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
@@ -349,7 +347,7 @@ __global__ void __launch_bounds__(kRowThreads)
     if constexpr (VB > 0) {
         using P = typename Piece<VB>::T;
         for (int v = v0; v < r.np / static_cast<int>(VB / sizeof(V)); v += dv) {
-            const P piece = __ldg(reinterpret_cast<const P*>(x) + v);
+            const P piece = load(reinterpret_cast<const P*>(x) + v);
             for (int j = 0; j < r.k; ++j) {
                 const int p = place(pos, i0 + j, S);
                 if (p >= 0) __stcs(reinterpret_cast<P*>(Xs + p * r.b) + v, piece);
@@ -368,7 +366,7 @@ __global__ void __launch_bounds__(kRowThreads)
                 __stcs(reinterpret_cast<uint4*>(q + head) + v, read16<V>(reinterpret_cast<const char*>(x + head) + 16LL * v, lo, hi));
             for (int i = v0; i < head + rest; i += dv) {
                 const int at = i < head ? i : i + pieces * N;
-                q[at] = x[at];
+                q[at] = load(x + at);
             }
         }
     }
@@ -382,8 +380,8 @@ constexpr int kSlotsAtOnce = 4;  // rows of one token in flight in a thread
 // pieces put together from aligned neighbours, as the gather does, took 440).
 template <class V, int VB>
 __global__ void __launch_bounds__(kRowThreads)
-    route_combine_kernel(RowShape r, const int* __restrict__ pos, const float* __restrict__ weight,
-                         const typename Piece<VB>::T* __restrict__ Ys, typename Piece<VB>::T* __restrict__ Y) {
+    route_combine_kernel(RowShape r, const int* pos, const float* weight, const typename Piece<VB>::T* Ys,
+                         typename Piece<VB>::T* Y) {
     using P = typename Piece<VB>::T;
     constexpr int N = VB / sizeof(V);
     let_next_start();
@@ -405,8 +403,8 @@ __global__ void __launch_bounds__(kRowThreads)
                 const int p = j0 + u < r.k ? place(pos, i0 + j0 + u, S) : -1;
                 on[u] = p >= 0;
                 if (on[u]) {
-                    piece[u] = __ldcs(Ys + p * r.b + v);
-                    w[u] = weight ? __ldg(weight + i0 + j0 + u) : 1.f;
+                    piece[u] = load_once(Ys + p * r.b + v);
+                    w[u] = weight ? load(weight + i0 + j0 + u) : 1.f;
                 }
             }
 #pragma unroll
@@ -426,9 +424,8 @@ __global__ void __launch_bounds__(kRowThreads)
 // group's lanes and warps.  Pitches in bytes.
 template <class V, int VB>
 __global__ void __launch_bounds__(kRowThreads)
-    route_combine_grad_kernel(RowShape r, const int* __restrict__ pos, const int* __restrict__ end,
-                              const float* __restrict__ weight, const char* __restrict__ dY, long long ldys,
-                              const char* __restrict__ Ys, char* __restrict__ dYs, float* __restrict__ dw) {
+    route_combine_grad_kernel(RowShape r, const int* pos, const int* end, const float* weight, const char* dY,
+                              long long ldys, const char* Ys, char* dYs, float* dw) {
     using P = typename Piece<VB>::T;
     constexpr int N = VB / sizeof(V);
     __shared__ float part[kRowThreads / 32][kSlotsAtOnce];
@@ -447,17 +444,17 @@ __global__ void __launch_bounds__(kRowThreads)
         for (int u = 0; u < kSlotsAtOnce; ++u) {
             dot[u] = 0.f;
             at[u] = live && j0 + u < r.k ? place(pos, i0 + j0 + u, S) : -1;
-            w[u] = at[u] >= 0 && weight ? __ldg(weight + i0 + j0 + u) : 1.f;
+            w[u] = at[u] >= 0 && weight ? load(weight + i0 + j0 + u) : 1.f;
         }
         if (live) {
 #pragma unroll 1  // 12001 tokens x 8 x 4095 fp32 679 us, 720 unrolled
             for (int v = v0; v < r.np; v += r.G) {
-                const P gp = __ldg(reinterpret_cast<const P*>(g) + v);
+                const P gp = load(reinterpret_cast<const P*>(g) + v);
                 P y[kSlotsAtOnce];
                 if (dw) {
 #pragma unroll
                     for (int u = 0; u < kSlotsAtOnce; ++u)
-                        if (at[u] >= 0) y[u] = __ldcs(reinterpret_cast<const P*>(Ys + at[u] * ldys) + v);
+                        if (at[u] >= 0) y[u] = load_once(reinterpret_cast<const P*>(Ys + at[u] * ldys) + v);
                 }
                 float gf[N];
                 widen<V, P>(gp, gf);
@@ -502,7 +499,7 @@ __global__ void __launch_bounds__(kRowThreads)
         }
     }
     if (live) {
-        for (long long p = min(max(__ldg(end), 0), S) + static_cast<long long>(t); p < S; p += r.T)
+        for (long long p = min(max(load(end), 0), S) + static_cast<long long>(t); p < S; p += r.T)
             for (int v = v0; v < r.np; v += r.G) memset(dYs + p * r.b + v * static_cast<long long>(VB), 0, VB);
     }
 }

@@ -1,0 +1,32 @@
+"""What the routed-expert kernels' sources have to keep to, read as text (no GPU): faults that would show on
+hardware only once in a long while, or by hanging it, are refused here."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "csr_bsr_spmv_gb300", "csrc")
+FILES = ["spx_route.cu", "spx_int8.cu", "spx_experts.cu", "spx_experts.cuh", "spx_experts_simt.cu", "spx_experts_tc.cu"]
+
+
+def code(name):
+    """The file without its comments."""
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_kernels_launched_early_read_no_memory_as_read_only(name):
+    """A kernel launched with programmatic serialisation is resident while the calls before it write its inputs,
+    and the read-only path is defined only for memory that nobody writes during the kernel's life."""
+    assert not re.search(r"\b__ldg\b|\b__ldcs\b|\b__restrict__\b|ld\.global\.nc", code(name))
+
+
+def test_every_kernel_launched_early_waits_before_it_reads():
+    for name in FILES:
+        text = code(name)
+        kernels = re.findall(r"__global__.*?\n}", text, flags=re.S)
+        for k in kernels:
+            assert "wait_for_previous();" in k, k[:200]
+            first = re.search(r"\bload(_once)?(<[^;(]*>)?\(|\bexpert_rows\(|\bwarp_find_tile\(", k)
+            assert first is None or k.index("wait_for_previous();") < first.start(), k[:200]
