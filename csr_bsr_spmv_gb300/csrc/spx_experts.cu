@@ -10,6 +10,7 @@ namespace {
 spx_status check_sizes(int32_t E, int32_t S, int32_t N, int32_t K) {
     if (E <= 0 || S < 0 || N < 0 || K < 0) return SPX_ERR_ARG;
     if (E > SPX_MAX_EXPERTS) return SPX_ERR_UNSUPPORTED;
+    if (S > kMostIndex || N > kMostIndex || K > kMostIndex) return SPX_ERR_INDEX_RANGE;
     return SPX_OK;
 }
 

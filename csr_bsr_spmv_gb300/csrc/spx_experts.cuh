@@ -119,6 +119,10 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Slots, rows and row lengths stay below 2^31 by more than a grid's threads or
+// a CTA's slots, so that an int index that steps past its end does not wrap.
+constexpr int64_t kMostIndex = kI32Max - (1 << 23);
+
 inline size_t type_bytes(spx_type t) { return t == SPX_F32 ? 4 : t == SPX_I8 ? 1 : 2; }
 inline bool is_float_type(spx_type t) { return t == SPX_F32 || t == SPX_BF16 || t == SPX_F16; }
 inline bool is_half_type(spx_type t) { return t == SPX_BF16 || t == SPX_F16; }

@@ -542,6 +542,7 @@ extern "C" {
 spx_status spx_quant_rows_i8(int32_t M, int32_t K, spx_type type, const void* X, int64_t ldx, int8_t* Q, int64_t ldq,
                              float* scale, spx_stream_t stream) {
     if (M < 0 || K < 0 || !is_float_type(type)) return SPX_ERR_ARG;
+    if (M > kMostIndex || K > kMostIndex) return SPX_ERR_INDEX_RANGE;
     if (M == 0) return SPX_OK;
     if (!scale || (K > 0 && (!X || !Q || ldx < K || ldq < K))) return SPX_ERR_ARG;
     if (!spx_aligned(X, type_bytes(type)) || !spx_aligned(scale, 4)) return SPX_ERR_ALIGN;
@@ -566,6 +567,7 @@ spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t
     if (E <= 0 || S < 0 || N < 0 || K < 0 || !is_float_type(c_type)) return SPX_ERR_ARG;
     if (!offsets && E != 1) return SPX_ERR_ARG;
     if (E > SPX_MAX_EXPERTS || K > SPX_I8_MAX_K) return SPX_ERR_UNSUPPORTED;
+    if (S > kMostIndex || N > kMostIndex) return SPX_ERR_INDEX_RANGE;
     if (S == 0 || N == 0) return SPX_OK;
     if (!row_scale || !w_scale || !C || ldc < N || (K > 0 && (!Q || !W || ldq < K || ldw < K || stride_w < 0)))
         return SPX_ERR_ARG;

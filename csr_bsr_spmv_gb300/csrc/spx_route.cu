@@ -534,7 +534,7 @@ dim3 row_grid(const RowShape& r, int64_t pieces, bool split) {
 
 spx_status check_rows(int32_t T, int32_t k, int32_t H) {
     if (T < 0 || k <= 0 || H < 0) return SPX_ERR_ARG;
-    if (static_cast<int64_t>(T) * k > kI32Max) return SPX_ERR_INDEX_RANGE;
+    if (static_cast<int64_t>(T) * k > kMostIndex || H > kMostIndex) return SPX_ERR_INDEX_RANGE;
     return SPX_OK;
 }
 
@@ -622,7 +622,7 @@ spx_status spx_route_build(int32_t T, int32_t k, int32_t E, const void* expert, 
     if (T < 0 || k <= 0 || E <= 0 || (id_bytes != 4 && id_bytes != 8)) return SPX_ERR_ARG;
     if (E > SPX_MAX_EXPERTS) return SPX_ERR_UNSUPPORTED;
     const int64_t S64 = static_cast<int64_t>(T) * k;
-    if (S64 > kI32Max - (1 << 23)) return SPX_ERR_INDEX_RANGE;  // the kernels step past the end by up to a CTA's slots
+    if (S64 > kMostIndex) return SPX_ERR_INDEX_RANGE;
     if (!offsets || (S64 > 0 && (!expert || !slot || !pos || lde < k))) return SPX_ERR_ARG;
     if (!spx_aligned(offsets, 4) || !spx_aligned(slot, 4) || !spx_aligned(pos, 4) ||
         !spx_aligned(expert, static_cast<size_t>(id_bytes)))

@@ -773,7 +773,9 @@ spx_status spx_spmm_wcsr_planned(const spx_wcsr_plan* plan, int32_t M, int32_t K
  * weighted to their tokens, and give the gradients of all of it.
  *
  * Terms: T tokens with k slots each, S = T * k; flat slot i = t * k + j; E
- * experts, at most SPX_MAX_EXPERTS (SPX_ERR_UNSUPPORTED beyond).  A slot whose
+ * experts, at most SPX_MAX_EXPERTS (SPX_ERR_UNSUPPORTED beyond).  Numbers of
+ * slots and rows and lengths of rows (S, H, N, K, M) may be up to 2^31 - 2^23
+ * - 1 (SPX_ERR_INDEX_RANGE beyond).  A slot whose
  * expert id lies outside [0, E) -- -1 by convention -- is dropped: no expert
  * sees it, it adds nothing to its token, its weight's gradient is 0.  Arrays
  * of S rows sorted by expert hold the kept slots first; the rows past them
@@ -804,8 +806,7 @@ typedef enum spx_type {
  *   expert: T x k ids, id_bytes 4 (int32) or 8 (int64) each, row t at
  *     expert + t * lde elements (lde >= k).
  *   scratch: spx_route_scratch_bytes(T, k, E) bytes (may be 0), 4-byte aligned.
- * T * k may be up to 2^31 - 2^23 - 1 (SPX_ERR_INDEX_RANGE).  Launches: 1, or 2
- * for more slots than a cluster of CTAs holds (16384, fewer with hundreds of experts).
+ * Launches: 1, or 2 for more slots than a cluster of CTAs holds (16384, fewer with hundreds of experts).
  */
 size_t spx_route_scratch_bytes(int32_t T, int32_t k, int32_t E);
 spx_status spx_route_build(int32_t T, int32_t k, int32_t E, const void* expert, int32_t id_bytes, int64_t lde,
