@@ -448,6 +448,11 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
     if (SPLIT) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(part));
     const int team = SPLIT ? a.split : CG;
     const int G = static_cast<int>(gridDim.x) / team, me = static_cast<int>(blockIdx.x) / team;
+    // A warp's wait that also ends when another warp gave up.  The flag is part of the vote: lanes may look at it at
+    // different times, and a warp that left its loop in part would hang at the next vote or election.
+    auto warp_wait_live = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, kSpinLimit) && !s_abort) != 0;
+    };
     // this CTA's part of a tile's reduction
     auto share = [&](Item it) {
         if (SPLIT) {
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             for (int r = r0; r < end; r += depth, ring.next(), ++issued) {
                 const uint32_t s8 = 8u * ring.s, sl = FUSE ? raw0 + ring.s * a.raw_bytes : base + ring.s * a.stage_bytes;
                 const uint32_t sc = sl + (FUSE ? 128 * kRawDepth : kLaneBytes);
-                ok = warp_wait((FUSE ? raw_empty(0) : empty_bar(0)) + s8, ring.ph ^ 1u) && !s_abort;
+                ok = warp_wait_live((FUSE ? raw_empty(0) : empty_bar(0)) + s8, ring.ph ^ 1u);
                 if (!ok) break;
                 if (FUSE) {
                     if (!elect()) continue;
@@ -624,7 +629,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             const Item it = share(tile_item<MODE, CG>(a, list, t));
             const int rows = 128 + uniform(mma_cols<CG>(it.rows));  // the lanes' rows, then the columns'
             for (int left = uniform(it.red); left > 0; left -= kRawDepth, raw.next(), ++taken) {
-                ok = warp_wait(raw_full(raw.s), raw.ph) && !s_abort;
+                ok = warp_wait_live(raw_full(raw.s), raw.ph);
                 if (!ok) break;
                 const int halves = left > 64 ? 2 : 1;
                 if (h < halves) {
@@ -644,7 +649,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                                              : "memory");
                         }
                         if (i0 == 0) {
-                            ok = warp_wait(empty_bar(mine.s), mine.ph ^ 1u) && !s_abort;
+                            ok = warp_wait_live(empty_bar(mine.s), mine.ph ^ 1u);
                             if (!ok) break;
                         }
 #pragma unroll
@@ -721,7 +726,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                 do {  // one accumulator's worth: the whole reduction, or kExact terms of it
                     const int now = I8 ? min(left, kExact) : left;
                     left -= now;
-                    ok = warp_wait(tempty_bar(buf), tph) && !s_abort;
+                    ok = warp_wait_live(tempty_bar(buf), tph);
                     if (!ok) break;
                     tc_fence_after();
                     uint32_t acc = 0;
@@ -766,7 +771,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
         } else if (MODE == kWG) {
             // the pair's second CTA: only its part of clearing the tails
             uint32_t at = 0;
-            for (int t = me; t < ntiles && !s_abort; t += G) {
+            for (int t = me; t < ntiles && __all_sync(0xffffffffu, !s_abort); t += G) {
                 const int red = tile_item<MODE, CG>(a, list, t).red;
                 if ((red & 15) && !clear_tail((at + red / kDepth) % NS, red % kDepth)) {
                     if (lane == 0) {
@@ -784,7 +789,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
         int buf = 0;
         uint32_t tph = 0;
         auto acc_wait = [&]() {
-            const bool ok = warp_wait(tfull_bar(buf), tph) && !s_abort;
+            const bool ok = warp_wait_live(tfull_bar(buf), tph);
             if (!ok && lane == 0) {
                 record_error(kErrAcc);
                 s_abort = 1;
@@ -820,7 +825,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             }
         };
         auto meet = [&](uint32_t bar, uint32_t parity) {
-            const bool ok = __all_sync(0xffffffffu, pair_wait<2>(bar, parity)) && !s_abort;
+            const bool ok = __all_sync(0xffffffffu, pair_wait<2>(bar, parity) && !s_abort) != 0;
             if (!ok && lane == 0) {
                 record_error(kErrAcc);
                 s_abort = 1;

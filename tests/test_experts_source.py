@@ -30,3 +30,15 @@ def test_every_kernel_launched_early_waits_before_it_reads():
             assert "wait_for_previous();" in k, k[:200]
             first = re.search(r"\bload(_once)?(<[^;(]*>)?\(|\bexpert_rows\(|\bwarp_find_tile\(", k)
             assert first is None or k.index("wait_for_previous();") < first.start(), k[:200]
+
+
+def test_the_abort_flag_is_read_in_a_vote():
+    """Lanes of a warp may read the flag at different times: unless they vote on it, part of a warp can leave a loop
+    whose next whole-warp instruction the rest then waits at for ever."""
+    text = code("spx_experts_tc.cu")
+    reads = [m.start() for m in re.finditer(r"!\s*s_abort", text)]
+    assert reads
+    for at in reads:
+        statement = text[max(text.rfind(c, 0, at) for c in ";{}"):at]
+        vote = statement.rfind("__all_sync(")
+        assert vote >= 0 and statement[vote:].count("(") > statement[vote:].count(")"), statement
