@@ -62,7 +62,11 @@ constexpr int kMaxStages = 12;
 constexpr int kExact = 1024;
 constexpr int kBand = 8;                        // row tiles that run side by side before the next lane tile
 constexpr size_t kSmemMax = 224 * 1024;         // dynamic shared memory of a CTA
-constexpr long long kSpinLimit = 2000000000LL;  // cycles (~1 s): only a broken pipeline reaches it
+// Cycles of a wait, about a second; and as some waits last as long as a tile's
+// reduction (the storing warps', a pair's second CTA's for the last stage, those
+// of CTAs that share a reduction for each other), so many more for each of its
+// stages, which take 350 to 1165.  Only a broken pipeline reaches the sum.
+constexpr long long kSpinLimit = 2000000000LL, kStageLimit = 8192;
 
 enum : int { kErrFull = 1, kErrEmpty = 2, kErrAcc = 3, kErrDrain = 4 };
 
@@ -97,6 +101,7 @@ struct TcArgs {
     uint32_t stage_bytes, idesc, part_off;  // part_off: the shared partial tile, behind the tile list
     int split, split_red;  // CTAs that share a tile's reduction, and the length of a share (a multiple of kDepth)
     int same_w;       // 1: every expert reads W_0
+    long long spin_limit;  // cycles of a wait
     Divisor by_lane, by_group;  // lane tiles; kNK, kKN: tiles of a full band, kWG: tiles of an expert
     void* C;
     long long ldc, ce;
@@ -253,8 +258,8 @@ __device__ __forceinline__ int mma_cols(int rows) {
 
 // Bounded wait for arrivals that may come from the other CTA of the pair.
 template <int CG>
-__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity) {
-    if (CG == 1) return mbar_wait(bar, parity, kSpinLimit);
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, long long limit) {
+    if (CG == 1) return mbar_wait(bar, parity, limit);
     long long t0 = 0;
     for (;;) {
         uint32_t ok;
@@ -267,7 +272,7 @@ __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity) {
             : "memory");
         if (ok) return true;
         if (t0 == 0) t0 = clock64();
-        else if (clock64() - t0 > kSpinLimit) return false;
+        else if (clock64() - t0 > limit) return false;
     }
 }
 
@@ -282,11 +287,6 @@ __device__ __forceinline__ bool elect() {
     return p != 0;
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// Bounded wait by a whole warp, with one answer for all lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kSpinLimit));
-}
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -448,10 +448,14 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
     if (SPLIT) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(part));
     const int team = SPLIT ? a.split : CG;
     const int G = static_cast<int>(gridDim.x) / team, me = static_cast<int>(blockIdx.x) / team;
-    // A warp's wait that also ends when another warp gave up.  The flag is part of the vote: lanes may look at it at
+    // Bounded wait by a whole warp, with one answer for all lanes.
+    auto warp_wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.spin_limit)) != 0;
+    };
+    // The same, that also ends when another warp gave up.  The flag is part of the vote: lanes may look at it at
     // different times, and a warp that left its loop in part would hang at the next vote or election.
     auto warp_wait_live = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, kSpinLimit) && !s_abort) != 0;
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.spin_limit) && !s_abort) != 0;
     };
     // this CTA's part of a tile's reduction
     auto share = [&](Item it) {
@@ -733,7 +737,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                     for (int k = now; k > 0; k -= kDepth) {
                         if (MODE == kWG && k < kDepth && (k & 15)) {
                             ok = clear_tail(ring.s, k) &&
-                                 __all_sync(0xffffffffu, pair_wait<CG>(clear_bar(ring.s), ((tails >> ring.s) & 1u) ^ 1u));
+                                 __all_sync(0xffffffffu, pair_wait<CG>(clear_bar(ring.s), ((tails >> ring.s) & 1u) ^ 1u, a.spin_limit));
                             if (!ok) break;
                         }
                         ok = warp_wait(full_bar(0) + 8u * ring.s, ring.ph);
@@ -825,7 +829,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             }
         };
         auto meet = [&](uint32_t bar, uint32_t parity) {
-            const bool ok = __all_sync(0xffffffffu, pair_wait<2>(bar, parity) && !s_abort) != 0;
+            const bool ok = __all_sync(0xffffffffu, pair_wait<2>(bar, parity, a.spin_limit) && !s_abort) != 0;
             if (!ok && lane == 0) {
                 record_error(kErrAcc);
                 s_abort = 1;
@@ -1140,6 +1144,7 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     const int sms = sm_count();
     if (sms <= 0) return SPX_ERR_CUDA;
     a.wide_c = spx_aligned(a.C, 16) && a.ldc % 8 == 0 && a.ce % 8 == 0 && a.NL % 8 == 0;
+    a.spin_limit = kSpinLimit + kStageLimit * ((MODE == kWG ? a.S : a.NR) / kDepth + 1);
     a.log_tn = 0;
     while ((1 << a.log_tn) < a.TN) ++a.log_tn;
     a.wide_f = spx_aligned(a.C, 16) && a.ldc % 4 == 0 && a.NL % 4 == 0;
