@@ -34,6 +34,7 @@
 #include <tuple>
 
 #include "spx_experts.cuh"
+#include "spx_experts_tile.h"
 #include "spx_tc.cuh"
 
 using namespace spx_exp;
@@ -50,8 +51,6 @@ constexpr int kStoreWarps = 8;
 constexpr int kWidenWarps = 8;  // FUSE
 template <bool FUSE>
 constexpr int kThreadsOf = 32 * (kStoreWarps + 3 + (FUSE ? kWidenWarps : 0));
-constexpr int kRawDepth = 128;  // FUSE: reduction length of a raw stage, one 128-byte row
-constexpr int kDepth = 64;                      // reduction length of a stage: one 128-byte swizzle row
 constexpr uint32_t kLaneBytes = 128 * kDepth * 2;  // a stage's lane factor: 128 lanes a CTA, 16 KB
 constexpr uint32_t kBox = 64 * kDepth * 2;      // an MN-major box: 64 long, 64 deep, 8 KB
 constexpr int kMaxStages = 12;
@@ -1086,55 +1085,13 @@ int resident_teams(const void* kernel, int team, const cudaLaunchConfig_t& cfg) 
     return cache[key] = n;
 }
 
-enum Kind { kProduct, kGradient, kCodes };  // kCodes: 8-bit factors widened on the way (FUSE)
-
-// The tile (a.TN rows of 128 or, for a pair, 256 columns) and the CTAs that
-// share a tile's reduction (a.split, a.split_red), by the least modelled time;
-// returns the CTAs of a tile, 1 or 2.  Cycles of a 64-deep stage, measured on
-// products of 512 to 16384 rows: small tiles are bound by what issuing a stage
-// takes, single CTAs with large ones by the L2 reads of their factors, pairs
-// come near the tensor rate.  A tile's stores (12 cycles a row) run beside the
-// next tile's MMAs; rounds of tiles count whole.  Sharing a reduction costs
-// about 1500 cycles a CTA for the exchange.  512 rows x 4096 x 4096: 128-row
-// tiles 19 us, 256-row pairs 25, 64-row tiles 30; 16 rows: one CTA a tile 16.5
-// us, two 13.0, four 11.6, eight 16.1.
-int choose_tile(TcArgs& a, Kind kind) {
-    const bool wgrad = kind == kGradient, fused = kind == kCodes;
-    struct Shape {
-        int tn, cg, stage;
-    };
-    constexpr Shape shapes[] = {{256, 2, 615}, {256, 1, 725}, {128, 2, 435}, {128, 1, 460}, {64, 1, 390}, {32, 1, 350}};
-    constexpr Shape codes[] = {{128, 1, 1165}, {64, 1, 985}, {32, 1, 900}};  // FUSE, measured
-    const Shape *from = fused ? codes : shapes, *to = fused ? codes + 3 : shapes + 6;
-    const double mean = static_cast<double>(a.S) / a.E, used = std::min(a.E, a.S);
-    const int sms = sm_count();
-    double best = 0;
-    Shape pick = *from;
-    a.split = 1;
-    for (; from != to; ++from) {
-        const Shape sh = *from;
-        if (wgrad && sh.tn < 128) continue;                    // boxes of 64 columns, two lanes a stage
-        if (sh.cg == 2 && a.NL <= 128) continue;
-        const int most = wgrad ? a.NC : a.S;
-        if (sh.tn > 64 && sh.tn / 2 >= most) continue;
-        const double lanes = (a.NL + 128 * sh.cg - 1) / (128 * sh.cg);
-        // row tiles: an expert's last one is half full on average, unless one holds all its rows
-        const double rows = wgrad      ? static_cast<double>(a.E) * ((a.NC + sh.tn - 1) / sh.tn)
-                            : a.E == 1 ? (a.S + sh.tn - 1) / sh.tn
-                                       : used * (2 * mean > sh.tn ? mean / sh.tn + 0.5 : 1.0);
-        const double tiles = rows * lanes, slots = sms / sh.cg;
-        const double stages = wgrad ? mean / kDepth + 0.5 : (a.NR + kDepth - 1) / kDepth;
-        for (int split = 1; split <= 8; split *= 2) {
-            if (split > 1 && (wgrad || sh.cg > 1 || sh.tn > 128 || tiles * split > slots)) break;
-            const double rounds = tiles * split <= slots ? 1 : tiles / slots < 4 ? static_cast<int>(tiles / slots + 0.99) : tiles / slots;
-            const double cycles = rounds * (std::max(stages / split * sh.stage, 12.0 * sh.tn) + 600) + (split > 1 ? 1500 * split : 0);
-            if (best == 0 || cycles < best) best = cycles, pick = sh, a.split = split;
-        }
-    }
-    a.TN = pick.tn;
-    const int unit = fused ? kRawDepth : kDepth;
-    a.split_red = ((a.NR + unit - 1) / unit + a.split - 1) / a.split * unit;
-    return pick.cg;
+// Takes the tile for a's sizes; returns the CTAs of a tile, 1 or 2.
+int take_tile(TcArgs& a, Kind kind) {
+    const Tile t = choose_tile(kind, a.E, a.S, a.NL, a.NC, a.NR, sm_count());
+    a.TN = t.tn;
+    a.split = t.split;
+    a.split_red = t.split_red;
+    return t.cg;
 }
 
 bool rows_aligned(const void* p, int64_t ld) { return spx_aligned(p, 16) && ld % 8 == 0; }
@@ -1218,7 +1175,7 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
     a.offsets = offsets, a.E = E, a.S = S, a.NL = N, a.NR = K;
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.same_w = E == 1 || stride_w == 0;
-    const int cg = choose_tile(a, kProduct);
+    const int cg = take_tile(a, kProduct);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(type, nk ? kNK : kKN, cg);
     CUtensorMap tl, tc;
@@ -1246,7 +1203,7 @@ spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const v
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.row_scale = row_scale, a.col_scale = col_scale;
     a.same_w = mats == 1;
-    const int cg = choose_tile(a, kProduct);
+    const int cg = take_tile(a, kProduct);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(SPX_F16, kNK, cg);
     CUtensorMap tl, tc;
@@ -1273,7 +1230,7 @@ spx_status tc_product_codes(int E, int S, int N, int K, const int* offsets, cons
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.row_scale = row_scale, a.col_scale = col_scale;
     a.same_w = E == 1 || stride_w == 0;
-    choose_tile(a, kCodes);
+    take_tile(a, kCodes);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN) * kDepth * 2;
     a.raw_bytes = static_cast<uint32_t>(128 + a.TN) * kRawDepth;
     a.idesc = idesc_of(SPX_F16, kNK, 1);
@@ -1299,7 +1256,7 @@ spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* 
     TcArgs a{};
     a.offsets = offsets, a.E = E, a.S = S, a.NL = K, a.NC = N;
     a.C = dW, a.ldc = ldw, a.ce = stride_w, a.c_type = w_type;
-    const int cg = choose_tile(a, kGradient);
+    const int cg = take_tile(a, kGradient);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(type, kWG, cg);
     CUtensorMap tl, tc;

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from csr_bsr_spmv_gb300 import spx
+from test_gpu_experts import close, counts_case, gen, padded
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +27,21 @@ def test_a_gradient_over_hundreds_of_millions_of_rows_is_waited_for():
     dW = spx.spx_gemm_grouped_wgrad(off, G, A, dtype=torch.float32)
     assert spx.spx_last_device_error() == 0
     assert torch.equal(dW[0].double(), G[rows].double().T @ A[rows].double())
+
+
+@pytest.mark.parametrize("E,S,N,K", [(1, 700, 8, 2048), (8, 3000, 16, 1024), (5, 900, 64, 128), (3, 500, 1, 72), (60, 4000, 40, 264),
+                                     (4, 1000, 65, 520)])
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (torch.float16, torch.float32)])
+def test_gradients_of_few_output_rows(E, S, N, K, dtype, out):
+    """dW of N <= 64 rows (adapters of low rank): one 128-row tile, on a single CTA where K is short."""
+    off = counts_case("spread", E, S, N)
+    g = gen(N + K)
+    G = torch.randn(S, N, device="cuda", generator=g).to(dtype)
+    A = torch.randn(S, K, device="cuda", generator=g).to(dtype)
+    p = (-N) % 8  # rows the copy engine can read
+    dW = spx.spx_gemm_grouped_wgrad(off, padded(G, p), A, dtype=out)
+    o = off.tolist()
+    for e in range(E):
+        ge, ae = G[o[e]:o[e + 1]].double(), A[o[e]:o[e + 1]].double()
+        close(dW[e], ge.T @ ae, ge.abs().T @ ae.abs(), S, "gradient")
+    assert spx.spx_last_device_error() == 0
