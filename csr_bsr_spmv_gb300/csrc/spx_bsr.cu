@@ -50,7 +50,6 @@
 #include <type_traits>
 
 #include "spx_check.cuh"
-#include "spx_experts.cuh"
 #include "spx_internal.h"
 #include "spx_tc.cuh"
 
@@ -880,10 +879,12 @@ spx_status spx_last_device_error(spx_stream_t stream) {
     if (e != cudaSuccess) return SPX_ERR_CUDA;
     const int coo = spx_coo_error_take();
     const int wcsr = spx_wcsr_error_take();
-    const int experts = spx_exp::experts_error_take();
+    const int experts = spx_experts_error_take();
     // the checked build's index errors (always 0 in the product build, which reads no word for them)
     const int checked[] = {spx_check_take(g_bsr_check), spx_spmv_check_take(), spx_spmm_check_take(),
-                           spx_sell_check_take(), spx_wcsr_check_take(), spx_bsrg_check_take()};
+                           spx_sell_check_take(), spx_wcsr_check_take(), spx_bsrg_check_take(),
+                           spx_route_check_take(), spx_experts_check_take(), spx_experts_simt_check_take(),
+                           spx_int8_check_take()};
     if (h || wcsr == SPX_ERR_TIMEOUT || experts == SPX_ERR_TIMEOUT) return SPX_ERR_TIMEOUT;
     if (wcsr == SPX_ERR_CUDA || experts == SPX_ERR_CUDA) return SPX_ERR_CUDA;
     for (int c : checked)

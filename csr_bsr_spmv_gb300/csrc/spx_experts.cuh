@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "spx_check.cuh"
 #include "spx_internal.h"
 
 namespace spx_exp {
@@ -93,10 +94,16 @@ SPX_EXP_LOAD(load, "ld.global")
 SPX_EXP_LOAD(load_once, "ld.global.cs")
 #undef SPX_EXP_LOAD
 
+// The checked build's error word, one in every translation unit with kernels.
+static __device__ int g_experts_check;
+static __device__ __forceinline__ void check_fail() { atomicExch(&g_experts_check, 1); }
+
 // Rows [lo, hi) of expert e, whatever the offsets hold: inside [0, S], lo <= hi.
 __device__ __forceinline__ void expert_rows(const int* offsets, int e, int S, int& lo, int& hi) {
-    lo = min(max(load(offsets + e), 0), S);
-    hi = min(max(load(offsets + e + 1), lo), S);
+    const int a = load(offsets + e), b = load(offsets + e + 1);
+    if (SPX_CHECKED && !(0 <= a && a <= b && b <= S)) check_fail();
+    lo = min(max(a, 0), S);
+    hi = min(max(b, lo), S);
 }
 
 template <class... P, class... A>
@@ -223,6 +230,5 @@ bool tc_wgrad_fits(const void* G, int64_t ldg, const void* A, int64_t lda);
 spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* G, int64_t ldg, const void* A,
                     int64_t lda, spx_type type, void* dW, int64_t ldw, int64_t stride_w, spx_type w_type,
                     cudaStream_t st);
-int experts_error_take();  // reads and clears the error word of those kernels: 0 or SPX_ERR_TIMEOUT
 
 }  // namespace spx_exp

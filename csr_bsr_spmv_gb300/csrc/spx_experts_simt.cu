@@ -113,6 +113,8 @@ spx_status launch(const SimtGemm& g, spx_type c_type, cudaStream_t st) {
 
 }  // namespace
 
+int spx_experts_simt_check_take() { return spx_check_take(g_experts_check); }
+
 namespace spx_exp {
 
 spx_status simt_gemm(const SimtGemm& g, spx_type type, spx_type c_type, cudaStream_t st) {

@@ -1153,15 +1153,17 @@ uint32_t idesc_of(spx_type type, int mode, int cg) {
 
 }  // namespace
 
-namespace spx_exp {
-
-int experts_error_take() {
+int spx_experts_error_take() {
     int h = 0;
     const int zero = 0;
     if (cudaMemcpyFromSymbol(&h, g_experts_error, sizeof(int)) != cudaSuccess) return SPX_ERR_CUDA;
     if (h != 0 && cudaMemcpyToSymbol(g_experts_error, &zero, sizeof(int)) != cudaSuccess) return SPX_ERR_CUDA;
     return h ? static_cast<int>(SPX_ERR_TIMEOUT) : 0;
 }
+
+int spx_experts_check_take() { return spx_check_take(g_experts_check); }
+
+namespace spx_exp {
 
 bool tc_product_fits(const void* A, int64_t lda, const void* W, int64_t ldw, int64_t stride_w, int E) {
     return rows_aligned(A, lda) && rows_aligned(W, ldw) && (E == 1 || stride_w % 8 == 0);

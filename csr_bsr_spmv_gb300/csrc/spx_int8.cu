@@ -537,6 +537,8 @@ int pitch16(int K) { return (K + 7) / 8 * 8; }
 
 }  // namespace
 
+int spx_int8_check_take() { return spx_check_take(g_experts_check); }
+
 extern "C" {
 
 spx_status spx_quant_rows_i8(int32_t M, int32_t K, spx_type type, const void* X, int64_t ldx, int8_t* Q, int64_t ldq,

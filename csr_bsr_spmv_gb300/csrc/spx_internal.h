@@ -39,6 +39,9 @@ int spx_coo_error_take();
 // Reads and clears the error word of the WCSR kernel: 0 or SPX_ERR_TIMEOUT.
 int spx_wcsr_error_take();
 
+// Reads and clears the error word of the experts' products: 0 or SPX_ERR_TIMEOUT.
+int spx_experts_error_take();
+
 // The checked build (-DSPX_CHECK): read and clear the index-error word of each
 // translation unit's kernels, 0 or SPX_ERR_INDEX_RANGE (0 without reading
 // anything in the product build).
@@ -47,6 +50,10 @@ int spx_spmm_check_take();
 int spx_sell_check_take();
 int spx_wcsr_check_take();
 int spx_bsrg_check_take();
+int spx_route_check_take();
+int spx_experts_check_take();
+int spx_experts_simt_check_take();
+int spx_int8_check_take();
 
 // BSR SpMM for block shapes other than 64 x 64 (spx_bsr_simt.cu): the
 // arguments of spx_spmm_bsr, validated by it (ldb even; bsr_val 2-, B and C

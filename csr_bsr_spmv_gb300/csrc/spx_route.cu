@@ -289,14 +289,22 @@ struct RowShape {
 
 __device__ __forceinline__ int place(const int* pos, long long i, int S) {
     const int p = load(pos + i);
+    if (SPX_CHECKED && (p < -1 || p >= S)) check_fail();
     return p >= 0 && p < S ? p : -1;
+}
+
+// The first sorted row past the last expert's, offsets[E].
+__device__ __forceinline__ int rows_end(const int* end, int S) {
+    const int p = load(end);
+    if (SPX_CHECKED && !(0 <= p && p <= S)) check_fail();
+    return min(max(p, 0), S);
 }
 
 // Zeros in the sorted array's rows from offsets[E] on: token t's group takes every T-th of them.
 template <class P>
 __device__ __forceinline__ void zero_tail(const RowShape& r, const int* end, int t, int v0, int dv, P* out) {
     const int S = r.T * r.k;
-    for (long long p = min(max(load(end), 0), S) + static_cast<long long>(t); p < S; p += r.T)
+    for (long long p = rows_end(end, S) + static_cast<long long>(t); p < S; p += r.T)
         for (int v = v0; v < r.np; v += dv) memset(out + p * r.b + v, 0, sizeof(P));
 }
 
@@ -499,7 +507,7 @@ __global__ void __launch_bounds__(kRowThreads)
         }
     }
     if (live) {
-        for (long long p = min(max(load(end), 0), S) + static_cast<long long>(t); p < S; p += r.T)
+        for (long long p = rows_end(end, S) + static_cast<long long>(t); p < S; p += r.T)
             for (int v = v0; v < r.np; v += r.G) memset(dYs + p * r.b + v * static_cast<long long>(VB), 0, VB);
     }
 }
@@ -607,6 +615,8 @@ spx_status gather(int T, int k, int H, const int32_t* pos, const int32_t* end, c
 }
 
 }  // namespace
+
+int spx_route_check_take() { return spx_check_take(g_experts_check); }
 
 extern "C" {
 

@@ -782,7 +782,8 @@ spx_status spx_spmm_wcsr_planned(const spx_wcsr_plan* plan, int32_t M, int32_t K
  * (offsets[E] and on) are written as zeros by every call that writes such an
  * array.  Offsets, places and slots read from device memory are tested
  * against S before use, so wrong ones give wrong values but no access outside
- * the arrays.  Pointers need only their elements' alignment unless a call
+ * the arrays (the bounds-checked build reports them as SPX_ERR_INDEX_RANGE
+ * through spx_last_device_error).  Pointers need only their elements' alignment unless a call
  * says otherwise (16-byte aligned rows run on wider copies).  Nothing here
  * synchronises or allocates; no floating-point atomics, so results are the
  * same from run to run.
