@@ -873,9 +873,17 @@ def _new(shape, dtype, like, stream):
         return _empty(shape, dtype=dtype, device=like.device)
 
 
-def _raw_stream(like: torch.Tensor, stream):
+def _raw_stream(stream, like: torch.Tensor, *others):
+    """The handle of the stream a call runs on.  The library launches on the current device, so the operands
+    (None: absent) and the stream must belong to it."""
+    dev = like.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the operands must be on one device")
+    if dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
+        raise ValueError("the operands and the stream must belong to the current device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(like.get_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream
 
 
@@ -968,7 +976,7 @@ def spx_route_build(expert: torch.Tensor, E: int, stream=None, scratch: torch.Te
             scratch = _new(need // 4, _I32, expert, stream)
         work, size = scratch.data_ptr(), scratch.numel() * scratch.element_size()
     rc = lib.spx_route_build(T, k, E, at, 4 if dt == _I32 else 8, lde, offsets.data_ptr(), slot.data_ptr(),
-                             pos.data_ptr(), work, size, _raw_stream(expert, stream))
+                             pos.data_ptr(), work, size, _raw_stream(stream, expert, scratch))
     if rc:
         raise SpxError(rc, "spx_route_build")
     return Route(T, k, E, offsets, slot, pos)
@@ -982,7 +990,8 @@ def spx_route_gather(r: Route, X: torch.Tensor, Xs: torch.Tensor | None = None, 
     code = _type(X)
     Xs, ldxs, to = _out(Xs, r.slots, H, X.dtype, X, "Xs", stream)
     pos, end = r._places()
-    rc = _lib().spx_route_gather(T, r.k, H, code, pos, end, at, ldx, to, ldxs, _raw_stream(X, stream))
+    rc = _lib().spx_route_gather(T, r.k, H, code, pos, end, at, ldx, to, ldxs,
+                                 _raw_stream(stream, X, Xs, r._pos, r._offsets))
     if rc:
         raise SpxError(rc, "spx_route_gather")
     return Xs
@@ -997,7 +1006,8 @@ def spx_route_combine(r: Route, Ys: torch.Tensor, weight: torch.Tensor | None = 
     code = _type(Ys)
     w = _vec(weight, S, _F32, "weight") if weight is not None else None
     Y, ldy, to = _out(Y, r.T, H, Ys.dtype, Ys, "Y", stream)
-    rc = _lib().spx_route_combine(r.T, r.k, H, code, r._places()[0], w, at, ldys, to, ldy, _raw_stream(Ys, stream))
+    rc = _lib().spx_route_combine(r.T, r.k, H, code, r._places()[0], w, at, ldys, to, ldy,
+                                  _raw_stream(stream, Ys, Y, weight, r._pos))
     if rc:
         raise SpxError(rc, "spx_route_combine")
     return Y
@@ -1021,7 +1031,7 @@ def spx_route_combine_grad(r: Route, dY: torch.Tensor, Ys: torch.Tensor | None =
     dYs, lddys, to = _out(dYs, S, H, dY.dtype, dY, "dYs", stream)
     pos, end = r._places()
     rc = _lib().spx_route_combine_grad(T, r.k, H, code, pos, end, w, at, lddy, ys, ldys, to, lddys, dwp,
-                                       _raw_stream(dY, stream))
+                                       _raw_stream(stream, dY, Ys, dYs, weight, r._pos, r._offsets))
     if rc:
         raise SpxError(rc, "spx_route_combine_grad")
     return dYs, dw
@@ -1056,7 +1066,7 @@ def spx_gemm_grouped(offsets: torch.Tensor, A: torch.Tensor, W: torch.Tensor, C:
     code = _type(A)
     C, ldc, c = _out(C, S, N, (dtype or dt) if C is None else dtype, A, "C", stream)
     rc = _lib().spx_gemm_grouped(E, S, N, K, _vec(offsets, E + 1, _I32, "offsets"), a, lda, w, ldw, sw, kn, code, c, ldc,
-                                 _type(C), _raw_stream(A, stream))
+                                 _type(C), _raw_stream(stream, A, W, C, offsets))
     if rc:
         raise SpxError(rc, "spx_gemm_grouped")
     return C
@@ -1077,7 +1087,7 @@ def spx_gemm_grouped_wgrad(offsets: torch.Tensor, G: torch.Tensor, A: torch.Tens
     if e != E or n != N or k != K:
         raise ValueError(f"dW must be {E} x {N} x {K}")
     rc = _lib().spx_gemm_grouped_wgrad(E, S, N, K, _vec(offsets, E + 1, _I32, "offsets"), g, ldg, a, lda, code, w, ldw, sw,
-                                       _type(dW), _raw_stream(A, stream))
+                                       _type(dW), _raw_stream(stream, A, G, dW, offsets))
     if rc:
         raise SpxError(rc, "spx_gemm_grouped_wgrad")
     return dW
@@ -1093,7 +1103,7 @@ def spx_quant_rows_i8(X: torch.Tensor, Q: torch.Tensor | None = None, scale: tor
         to = scale.data_ptr() if M else None
     else:
         to = _vec(scale, M, _F32, "scale")
-    rc = _lib().spx_quant_rows_i8(M, K, code, x, ldx, q, ldq, to, _raw_stream(X, stream))
+    rc = _lib().spx_quant_rows_i8(M, K, code, x, ldx, q, ldq, to, _raw_stream(stream, X, Q, scale))
     if rc:
         raise SpxError(rc, "spx_quant_rows_i8")
     return Q, scale
@@ -1122,7 +1132,8 @@ def spx_gemm_i8(Q: torch.Tensor, row_scale: torch.Tensor, W: torch.Tensor, w_sca
         if scratch is None:
             scratch = _new(need, torch.uint8, Q, stream)
         work, size = scratch.data_ptr(), scratch.numel() * scratch.element_size()
-    rc = lib.spx_gemm_i8(E, S, N, K, off, q, ldq, rs, w, ldw, sw, ws, c, ldc, _type(C), work, size, _raw_stream(Q, stream))
+    rc = lib.spx_gemm_i8(E, S, N, K, off, q, ldq, rs, w, ldw, sw, ws, c, ldc, _type(C), work, size,
+                         _raw_stream(stream, Q, W, C, row_scale, w_scale, offsets, scratch))
     if rc:
         raise SpxError(rc, "spx_gemm_i8")
     return C
