@@ -6,6 +6,8 @@ import subprocess
 
 import pytest
 
+import experts_forms
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "csr_bsr_spmv_gb300", "csrc")
 PRODUCT, GRADIENT, CODES = 0, 1, 2
@@ -50,3 +52,20 @@ def test_every_choice_is_one_the_kernel_has(rule, E):
                 tn, cg, split, _ = rule(GRADIENT, E, R, NL, m, 0)
                 assert tn in (128, 256) and split == 1 and (cg == 1 or NL > 128), (E, R, NL, m)
                 assert tn == 128 or m > 128, "a gradient of few rows on a tile that is mostly empty"
+
+
+def forms(rule, kind, cases):
+    if kind == GRADIENT:
+        return {rule(kind, E, S, K, N, 0)[:3] for _, E, S, N, K in cases}
+    return {rule(kind, E, S, N, 0, K)[:3] for _, E, S, N, K in cases}
+
+
+def test_the_gpu_tests_reach_every_form(rule):
+    shared = {(tn, 1, split) for tn in (32, 64, 128) for split in (1, 2, 4, 8)}
+    pairs = {(128, 2, 1), (256, 2, 1)}
+    assert forms(rule, PRODUCT, experts_forms.PRODUCTS) == shared | pairs | {(256, 1, 1)}
+    assert forms(rule, GRADIENT, experts_forms.GRADIENTS) == pairs | {(128, 1, 1), (256, 1, 1)}
+    assert forms(rule, CODES, experts_forms.WIDENED) == shared
+    assert forms(rule, PRODUCT, experts_forms.COPIED) >= pairs | {(tn, 1, s) for tn in (64, 128) for s in (1, 2, 4)}
+    assert all(S > 128 * E for _, E, S, _, _ in experts_forms.COPIED)
+    assert all(16 * E < S <= 128 * E for _, E, S, _, _ in experts_forms.WIDENED)
