@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kThreads) experts_simt_kernel(SimtGemm g) {
     __shared__ int s_e, s_lo, s_hi;
     let_next_start();
     wait_for_previous();
-    const V *L = static_cast<const V*>(g.L), *R = static_cast<const V*>(g.R);
+    const V *L = static_cast<const V*>(behind_wait(g.L)), *R = static_cast<const V*>(behind_wait(g.R));
     O* C = static_cast<O*>(g.C);
     const int j0 = blockIdx.y * kT;
     int e, i0, i1, r0 = 0, r1 = g.NR;

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
         int lo = 0, hi = a.S;
         if (a.offsets) {
             if (e < a.E) expert_rows(a.offsets, e, a.S, lo, hi);
-            else lo = min(max(load(a.offsets + a.E), 0), a.S);
+            else lo = min(max(load(behind_wait(a.offsets) + a.E), 0), a.S);
         } else if (e == a.E) {
             lo = hi;
         }
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             const Item it = share(tile_item<MODE, CG>(a, list, t));
             const int rows = 128 + uniform(mma_cols<CG>(it.rows));  // the lanes' rows, then the columns'
             for (int left = uniform(it.red); left > 0; left -= kRawDepth, raw.next(), ++taken) {
-                ok = warp_wait_live(raw_full(raw.s), raw.ph);
+                ok = warp_wait(raw_full(raw.s), raw.ph);
                 if (!ok) break;
                 const int halves = left > 64 ? 2 : 1;
                 if (h < halves) {
@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             float cs[4] = {0.f, 0.f, 0.f, 0.f};
             if (I8 && it.e < a.E)
                 for (int i = 0; i < 4; ++i)
-                    if (col + i < a.NL) cs[i] = load(a.col_scale + static_cast<long long>(it.e) * a.NL + col + i);
+                    if (col + i < a.NL) cs[i] = load(behind_wait(a.col_scale) + static_cast<long long>(it.e) * a.NL + col + i);
             for (int r = part * per + warp; r < min((part + 1) * per, it.rows); r += kStoreWarps) {
                 uint32_t v[4], sum[4] = {0u, 0u, 0u, 0u};
                 for (int p = 0; p < a.split; ++p) {
@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                         sum[i] = I8 ? sum[i] + v[i] : __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
                 }
                 float f[4];
-                const float rs = I8 ? load(a.row_scale + it.row0 + r) : 1.f;
+                const float rs = I8 ? load(behind_wait(a.row_scale) + it.row0 + r) : 1.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     f[i] = !I8 ? __uint_as_float(sum[i])
@@ -977,7 +977,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int n = x + 8 * g + (lane >> 2);
-                cs[g] = it.e < a.E && n < a.NL ? load(a.col_scale + static_cast<long long>(it.e) * a.NL + n) : 0.f;
+                cs[g] = it.e < a.E && n < a.NL ? load(behind_wait(a.col_scale) + static_cast<long long>(it.e) * a.NL + n) : 0.f;
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -987,7 +987,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {  // this thread's eight rows of the 32
                     const int row = 8 * (r >> 1) + 2 * (lane & 3) + (r & 1);
-                    const float rs = load(a.row_scale + min(it.row0 + c0 + row, a.S - 1));
+                    const float rs = load(behind_wait(a.row_scale) + min(it.row0 + c0 + row, a.S - 1));
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const int i = 16 * (g >> 1) + 4 * (r >> 1) + 2 * (g & 1) + (r & 1);

@@ -34,28 +34,6 @@ struct alignas(N * sizeof(V) >= 16 ? 16 : N * sizeof(V)) Pack {
 };
 
 // A piece is written as one word of its size.
-template <int BYTES>
-struct Word;
-template <>
-struct Word<16> {
-    using T = uint4;
-};
-template <>
-struct Word<8> {
-    using T = uint2;
-};
-template <>
-struct Word<4> {
-    using T = uint32_t;
-};
-template <>
-struct Word<2> {
-    using T = uint16_t;
-};
-template <>
-struct Word<1> {
-    using T = uint8_t;
-};
 template <class P>
 __device__ __forceinline__ void write_piece(P* p, const P& v) {
     using T = typename Word<sizeof(P)>::T;
@@ -133,6 +111,7 @@ __global__ void __launch_bounds__(kQThreads, 10)
     __shared__ uint32_t s_max[kQThreads / 32];
     let_next_start();
     wait_for_previous();
+    X = behind_wait(X);
     const int row = blockIdx.x * (kQThreads / G) + threadIdx.x / G, at = threadIdx.x % G;
     if (row >= M) return;  // a whole group; G == kQThreads: never
     const P* x = reinterpret_cast<const P*>(X + row * ldx);
@@ -262,6 +241,7 @@ __global__ void __launch_bounds__(32 * WARPS) i8_few_kernel(FewArgs a) {
     __shared__ int part[WARPS][TM * CH];
     let_next_start();
     wait_for_previous();
+    a.Q = behind_wait(a.Q), a.W = behind_wait(a.W), a.row_scale = behind_wait(a.row_scale), a.col_scale = behind_wait(a.col_scale);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int e = 0, r0 = blockIdx.y * TM, hi = a.S;
     if (a.offsets && !warp_find_tile(a.offsets, a.E, a.S, TM, blockIdx.y, e, r0, hi)) return;
@@ -404,6 +384,7 @@ constexpr int kRowChan = 2, kRowThreads = 128, kRowMost = 2;
 __global__ void __launch_bounds__(kRowThreads) i8_row_kernel(FewArgs a) {
     let_next_start();
     wait_for_previous();
+    a.Q = behind_wait(a.Q), a.W = behind_wait(a.W), a.row_scale = behind_wait(a.row_scale), a.col_scale = behind_wait(a.col_scale);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int e = 0, p = blockIdx.y, hi = a.S;
     if (a.offsets && !warp_find_tile(a.offsets, a.E, a.S, 1, blockIdx.y, e, p, hi)) return;
@@ -480,6 +461,7 @@ __global__ void __launch_bounds__(kWidenThreads)
                  long long ldw, long long stride_w, __half* Q16, __half* W16, bool same_w) {
     let_next_start();
     wait_for_previous();
+    offsets = behind_wait(offsets), Q = behind_wait(Q), W = behind_wait(W);
     const int8_t* src = Q;
     __half* dst = Q16;
     long long ld = ldq;

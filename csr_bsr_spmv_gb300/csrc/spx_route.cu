@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(32 * kMostWarps)
     extern __shared__ int sm[];
     let_next_start();
     wait_for_previous();
+    x.p = behind_wait(x.p);
     for (int e = threadIdx.x; e < E; e += blockDim.x) sm[e] = 0;
     __syncthreads();
     const int per = runs * blockDim.x * kHeld, b0 = blockIdx.x * per, b1 = min(S, b0 + per);
@@ -96,6 +97,8 @@ __global__ void __launch_bounds__(32 * kMostWarps)
     let_next_start();
     for (int i = threadIdx.x; i < nw * ES + 3 * E + 1; i += blockDim.x) sm[i] = 0;
     wait_for_previous();
+    x.p = behind_wait(x.p);
+    hist = behind_wait(hist);
     __syncthreads();
     const int per = runs * blockDim.x * kHeld, b0 = b * per, b1 = min(S, b0 + per);
     int id[kHeld], rank[kHeld];
@@ -241,25 +244,6 @@ SortShape sort_shape(long long S, int E) {
 
 // ---------------------------------------------------------------- rows in pieces of VB bytes
 
-template <int VB>
-struct Piece;
-template <>
-struct Piece<16> {
-    using T = uint4;
-};
-template <>
-struct Piece<8> {
-    using T = uint2;
-};
-template <>
-struct Piece<4> {
-    using T = uint32_t;
-};
-template <>
-struct Piece<2> {
-    using T = uint16_t;
-};
-
 // The values of one piece as floats, and back (rounded once each).
 template <class V, class P>
 __device__ __forceinline__ void widen(const P& p, float (&f)[sizeof(P) / sizeof(V)]) {
@@ -347,13 +331,14 @@ __global__ void __launch_bounds__(kRowThreads)
     route_gather_kernel(RowShape r, const int* pos, const int* end, const V* X, V* Xs) {
     let_next_start();
     wait_for_previous();
+    pos = behind_wait(pos), end = behind_wait(end), X = behind_wait(X);
     const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
     if (t >= r.T) return;
     const int S = r.T * r.k, v0 = blockIdx.y * r.G + threadIdx.x % r.G, dv = gridDim.y * r.G;
     const long long i0 = static_cast<long long>(t) * r.k;
     const V* x = X + t * r.a;
     if constexpr (VB > 0) {
-        using P = typename Piece<VB>::T;
+        using P = typename Word<VB>::T;
         for (int v = v0; v < r.np / static_cast<int>(VB / sizeof(V)); v += dv) {
             const P piece = load(reinterpret_cast<const P*>(x) + v);
             for (int j = 0; j < r.k; ++j) {
@@ -388,12 +373,13 @@ constexpr int kSlotsAtOnce = 4;  // rows of one token in flight in a thread
 // pieces put together from aligned neighbours, as the gather does, took 440).
 template <class V, int VB>
 __global__ void __launch_bounds__(kRowThreads)
-    route_combine_kernel(RowShape r, const int* pos, const float* weight, const typename Piece<VB>::T* Ys,
-                         typename Piece<VB>::T* Y) {
-    using P = typename Piece<VB>::T;
+    route_combine_kernel(RowShape r, const int* pos, const float* weight, const typename Word<VB>::T* Ys,
+                         typename Word<VB>::T* Y) {
+    using P = typename Word<VB>::T;
     constexpr int N = VB / sizeof(V);
     let_next_start();
     wait_for_previous();
+    pos = behind_wait(pos), weight = behind_wait(weight), Ys = behind_wait(Ys);
     const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
     if (t >= r.T) return;
     const int S = r.T * r.k, v0 = blockIdx.y * r.G + threadIdx.x % r.G, dv = gridDim.y * r.G;
@@ -434,11 +420,12 @@ template <class V, int VB>
 __global__ void __launch_bounds__(kRowThreads)
     route_combine_grad_kernel(RowShape r, const int* pos, const int* end, const float* weight, const char* dY,
                               long long ldys, const char* Ys, char* dYs, float* dw) {
-    using P = typename Piece<VB>::T;
+    using P = typename Word<VB>::T;
     constexpr int N = VB / sizeof(V);
     __shared__ float part[kRowThreads / 32][kSlotsAtOnce];
     let_next_start();
     wait_for_previous();
+    pos = behind_wait(pos), end = behind_wait(end), weight = behind_wait(weight), dY = behind_wait(dY), Ys = behind_wait(Ys);
     const int t = blockIdx.x * (kRowThreads / r.G) + threadIdx.x / r.G;
     const bool live = t < r.T;
     const int S = r.T * r.k, v0 = threadIdx.x % r.G;
@@ -553,7 +540,7 @@ int piece_bytes(uint64_t bits) {
 
 template <class V, int VB>
 cudaError_t combine_launch(RowShape r, const int32_t* pos, const float* weight, const void* Ys, void* Y, cudaStream_t st) {
-    using P = typename Piece<VB>::T;
+    using P = typename Word<VB>::T;
     return launch_early(route_combine_kernel<V, VB>, row_grid(r, r.np, true), kRowThreads, 0, 1, st, r, pos, weight,
                         static_cast<const P*>(Ys), static_cast<P*>(Y));
 }

@@ -19,17 +19,31 @@ def code(name):
 def test_kernels_launched_early_read_no_memory_as_read_only(name):
     """A kernel launched with programmatic serialisation is resident while the calls before it write its inputs,
     and the read-only path is defined only for memory that nobody writes during the kernel's life."""
-    assert not re.search(r"\b__ldg\b|\b__ldcs\b|\b__restrict__\b|ld\.global\.nc", code(name))
+    assert not re.search(r"\b__ldg\b|\b__restrict__\b|ld\.global\.nc", code(name))
 
 
 def test_every_kernel_launched_early_waits_before_it_reads():
     for name in FILES:
         text = code(name)
-        kernels = re.findall(r"__global__.*?\n}", text, flags=re.S)
-        for k in kernels:
+        for k in re.findall(r"__global__.*?\n}", text, flags=re.S):
             assert "wait_for_previous();" in k, k[:200]
             first = re.search(r"\bload(_once)?(<[^;(]*>)?\(|\bexpert_rows\(|\bwarp_find_tile\(", k)
             assert first is None or k.index("wait_for_previous();") < first.start(), k[:200]
+
+
+def test_addresses_are_taken_behind_the_wait():
+    """A load whose address is known at the kernel's start may be moved above the wait: every pointer that a kernel
+    reads through passes behind_wait() first, parameters right after the wait."""
+    for name in FILES:
+        text = code(name)
+        for k in re.findall(r"__global__.*?\n}", text, flags=re.S):
+            params, body = k[:k.index("{")], k[k.index("wait_for_previous();"):]
+            for p in re.findall(r"const [\w:<> ]+\* (\w+)", params):
+                assert re.search(r"\b%s = behind_wait\(%s\)" % (p, p), body), (name, p, params[:200])
+            for field in re.findall(r"\bload(?:_once)?\((a\.\w+|g\.\w+|x\.p)", body):
+                assert "%s = behind_wait(%s)" % (field, field) in body, (name, field)
+        for field in re.findall(r"\bload(?:_once)?\((a\.\w+)", text):
+            assert "%s = behind_wait(%s)" % (field, field) in text, (name, field)
 
 
 def test_the_abort_flag_is_read_in_a_vote():
