@@ -219,7 +219,7 @@ struct SimtGemm {
     long long li, lr, rj, rr, re;  // element strides; re: of R between experts
     void* C;
     long long ldc, ce;             // row pitch of C, and its stride between experts
-    const int* offsets;            // NULL: one expert with all S rows
+    const int* offsets;
     int E, S, NI, NJ, NR;          // rows of experts run over i (by_rows) or over r
     bool by_rows;
 };

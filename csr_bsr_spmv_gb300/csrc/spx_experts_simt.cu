@@ -39,12 +39,7 @@ __global__ void __launch_bounds__(kThreads) experts_simt_kernel(SimtGemm g) {
     if (g.by_rows) {
         if (threadIdx.x < 32) {
             int te = 0, lo = 0, hi = 0;
-            if (!g.offsets) {
-                lo = blockIdx.x * kT;
-                hi = g.S;
-            } else if (!warp_find_tile(g.offsets, g.E, g.S, kT, blockIdx.x, te, lo, hi)) {
-                lo = hi = 0;
-            }
+            if (!warp_find_tile(g.offsets, g.E, g.S, kT, blockIdx.x, te, lo, hi)) lo = hi = 0;
             if (threadIdx.x == 0) s_e = te, s_lo = lo, s_hi = hi;
         }
         __syncthreads();
@@ -98,8 +93,7 @@ template <class V>
 spx_status launch(const SimtGemm& g, spx_type c_type, cudaStream_t st) {
     dim3 grid;
     if (g.by_rows) {
-        const long long nt = g.offsets ? max_row_tiles(g.E, g.S, kT) : (static_cast<long long>(g.S) + kT - 1) / kT;
-        grid = dim3(static_cast<unsigned>(nt), (g.NJ + kT - 1) / kT);
+        grid = dim3(static_cast<unsigned>(max_row_tiles(g.E, g.S, kT)), (g.NJ + kT - 1) / kT);
     } else {
         grid = dim3((g.NI + kT - 1) / kT, (g.NJ + kT - 1) / kT, g.E);
     }

@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kRowThreads) i8_row_kernel(FewArgs a) {
     }
 }
 
-// Row tiles of 8, 16 or 32 rows, by an expert's average: most experts are one tile.
+// Row tiles of 8, 16 or 32 rows, by an expert's average (at most kFewRows): most experts are one tile.
 spx_status few_product(const FewArgs& a, cudaStream_t st) {
     if (a.S <= kRowMost) {
         constexpr int per = kRowThreads / 32 * kRowChan;
@@ -441,7 +441,6 @@ spx_status few_product(const FewArgs& a, cudaStream_t st) {
     const int nb = most <= 8 ? 1 : most <= 16 ? 2 : 4;
     const long long ty = a.offsets ? std::min<long long>(max_row_tiles(a.E, a.S, 8 * nb), static_cast<long long>(a.S) + 1)
                                    : (a.S + 8 * nb - 1) / (8 * nb);
-    if (ty > 65535) return SPX_ERR_UNSUPPORTED;
     spx_note_launches(1);
     return spx_cuda_status(nb == 1   ? few_launch<1, 1, 16>(a, ty, st)
                            : nb == 2 ? few_launch<2, 1, 16>(a, ty, st)
