@@ -744,6 +744,16 @@ bool make_map_box(CUtensorMap* m, const void* base, uint64_t inner, uint64_t out
 
 }  // namespace
 
+int spx_bsr_error_take() {
+    int h = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&h, g_bsr_error, sizeof(int)) != cudaSuccess) return SPX_ERR_CUDA;
+    if (h != 0 && cudaMemcpyToSymbol(g_bsr_error, &zero, sizeof(int)) != cudaSuccess) return SPX_ERR_CUDA;
+    return h ? static_cast<int>(SPX_ERR_TIMEOUT) : 0;
+}
+
+int spx_bsr_check_take() { return spx_check_take(g_bsr_check); }
+
 extern "C" {
 
 spx_status spx_spmm_bsr(int32_t M, int32_t K, int32_t br, int32_t bc, int64_t nnzb, const int32_t* bsr_row_ptr,
@@ -867,32 +877,6 @@ spx_status spx_wait_probe(int64_t limit_cycles, spx_stream_t stream) {
     wait_probe_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(limit_cycles);
     spx_note_launches(1);
     return spx_cuda_status(cudaGetLastError());
-}
-
-spx_status spx_last_device_error(spx_stream_t stream) {
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    int h = 0;
-    const int zero = 0;
-    cudaError_t e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&h, g_bsr_error, sizeof(int));
-    if (e == cudaSuccess && h != 0) e = cudaMemcpyToSymbol(g_bsr_error, &zero, sizeof(int));
-    if (e != cudaSuccess) return SPX_ERR_CUDA;
-    const int coo = spx_coo_error_take();
-    const int wcsr = spx_wcsr_error_take();
-    const int experts = spx_experts_error_take();
-    // the checked build's index errors (always 0 in the product build, which reads no word for them)
-    const int checked[] = {spx_check_take(g_bsr_check), spx_spmv_check_take(), spx_spmm_check_take(),
-                           spx_sell_check_take(), spx_wcsr_check_take(), spx_bsrg_check_take(),
-                           spx_route_check_take(), spx_experts_check_take(), spx_experts_simt_check_take(),
-                           spx_int8_check_take()};
-    if (h || wcsr == SPX_ERR_TIMEOUT || experts == SPX_ERR_TIMEOUT) return SPX_ERR_TIMEOUT;
-    if (wcsr == SPX_ERR_CUDA || experts == SPX_ERR_CUDA) return SPX_ERR_CUDA;
-    for (int c : checked)
-        if (c == SPX_ERR_CUDA) return SPX_ERR_CUDA;
-    if (coo) return static_cast<spx_status>(coo);
-    for (int c : checked)
-        if (c) return static_cast<spx_status>(c);
-    return SPX_OK;
 }
 
 }  // extern "C"

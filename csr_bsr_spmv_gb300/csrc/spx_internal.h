@@ -36,6 +36,9 @@ spx_status spx_cuda_status(int cuda_error);
 // Reads and clears the error word of the COO kernel: 0 or a negative spx_status.
 int spx_coo_error_take();
 
+// Reads and clears the error word of the BSR kernels: 0 or SPX_ERR_TIMEOUT.
+int spx_bsr_error_take();
+
 // Reads and clears the error word of the WCSR kernel: 0 or SPX_ERR_TIMEOUT.
 int spx_wcsr_error_take();
 
@@ -49,6 +52,7 @@ int spx_spmv_check_take();
 int spx_spmm_check_take();
 int spx_sell_check_take();
 int spx_wcsr_check_take();
+int spx_bsr_check_take();
 int spx_bsrg_check_take();
 int spx_route_check_take();
 int spx_experts_check_take();
