@@ -5,7 +5,8 @@
 // R(j, r) with any strides.  A CTA owns a 64 x 64 tile of the output; 32 terms
 // at a time go through shared memory, each thread holds 4 x 4 fp32 sums.
 // Bound by the FMA rate and the shared-memory reads that feed it (8 words for
-// 16 FMAs): 32768 x 2048 x 4096 in 24.2 ms, 23 TFLOP/s.
+// 16 FMAs): 32768 x 2047 x 4095 in 23.5 ms, 23 TFLOP/s, against 0.29 ms of
+// 32768 x 2048 x 4096 on the tensor cores and 21.5 ms of a plain fp32 product.
 #include "spx_experts.cuh"
 
 using namespace spx_exp;

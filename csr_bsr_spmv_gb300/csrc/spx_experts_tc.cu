@@ -19,13 +19,15 @@
 // comes from the offsets on the device: nothing waits for the host.
 //
 // What bounds it, measured: whole 256 x 256 tiles of a CTA pair run at the
-// tensor rate (32768 rows x 2048 x 4096 over 16 experts, even: 287 us, 1913
-// TFLOP/s; tensor pipe 85% active in ncu, uneven, 304 us), for seconds on end
-// at the power limit (335 us; a library product of the same size 313).  Few rows
-// are bound by the weights' bytes (32 rows, 23 experts of 2048 x 2048 hit: 34 us,
-// 5.6 TB/s), the smallest by a fixed cost (16 rows x 128 x 64: 3.8 us), a weight
-// gradient over few rows by its stores (537 MB of gradients in 157 us; filling
-// that memory takes 141).
+// tensor rate (32768 rows x 2048 x 4096 over 16 experts, even: 286 us, 1922
+// TFLOP/s; tensor pipe 85 to 88% active in ncu, uneven, 298 us), repeated for
+// tens of milliseconds at the power limit (335 us, 8192^3 566 rested and 650 to
+// 680 repeated).  Few rows are bound by the weights' bytes (32 rows, 23 experts
+// of 2048 x 2048 hit: 34 us, 5.6 TB/s), the smallest by a fixed cost (16 rows x
+// 128 x 64: 4.6 us), a weight gradient over few rows by its stores (64 experts of
+// 2048 x 2048, 16 or 32 rows each: 537 MB of gradients in 107 us; filling that
+// memory takes 132), or by clearing what a last step of 16 rows does not hold (12
+// rows each 111, 8 130, 1 155).
 //
 // Every mbarrier wait is bounded; on expiry the CTA records an error word
 // (read by spx_last_device_error), stops, waits (bounded) for its copies and
@@ -127,8 +129,9 @@ inline size_t list_bytes(int E) { return sizeof(int) * (3 * static_cast<size_t>(
 
 // Tile t of the list.  kNK, kKN: an expert's tiles go in bands of kBand row
 // tiles, lane tiles within a band, row tiles fastest, so that tiles that run
-// together share both factors in L2.  No division and no global read: the
-// thread that issues the MMAs does this between tiles.
+// together share both factors in L2.  No global read, and no division but the
+// one in an expert's last, shorter band: the thread that issues the MMAs does
+// this between tiles.
 template <int MODE, int CG>
 __device__ __forceinline__ Item tile_item(const TcArgs& a, const List& list, int t) {
     Item it;

@@ -21,10 +21,11 @@ namespace {
 
 // A row's largest magnitude, then its codes.  Bound by HBM.  A group of G
 // threads takes a row: a warp where there are rows enough to fill the SMs and
-// they are short (16384 rows x 2048 bf16: 20 us, 26 with a CTA a row; x 4096 51
-// and 42), a CTA otherwise.  Up to kQHeld pieces a thread stay in registers
+// they are short (16384 rows x 2048 bf16: 21 us, 24 with a CTA a row; x 4096 53
+// and 37), a CTA otherwise.  Up to kQHeld pieces a thread stay in registers
 // between the two, a longer row is read again from L2: more of them held cost
-// more in resident warps (eight: 27 us) than the reads.
+// more in resident warps (eight: 38 us) than the reads.  Rows that are not on
+// 16-byte boundaries go value by value (16384 x 2047 bf16: 47 us).
 constexpr int kQThreads = 128, kQHeld = 4;
 constexpr int kQWarpRows = 1216;  // rows that fill the SMs with a warp each: eight an SM
 
@@ -506,10 +507,10 @@ __global__ void __launch_bounds__(kWidenThreads)
     }
 }
 
-// Which kernel, by an expert's average rows (us, few rows / widened on the way / through widened copies):
-//   64 experts of 2048 x 2048: 4 rows 50/108/197, 16 rows 101/110/211, 64 rows -/134/219
-//   8 of 4096 x 2048: 8 rows 26/36/56, 32 rows 50/39/58, 128 rows 133/66/65
-//   one of 4096 x 4096: 16 rows 8/14/17, 32 rows 14/15/18, 64 rows 16/16/18, 128 rows 28/18/20
+// Which kernel, by an expert's average rows (us, few rows / widened on the way / through widened copies; unevenly routed):
+//   64 experts of 2048 x 2048: 4 rows 50/103/206, 16 rows 104/118/215, 64 rows (evenly) 190/124/217
+//   8 of 4096 x 2048: 8 rows 26/35/54, 32 rows 41/39/56, 128 rows 101/65/64
+//   one of 4096 x 4096: 16 rows 10/13/15, 32 rows 13/14/16, 64 rows 14/15/16, 128 rows 26/18/18
 constexpr int kFewRows = 16, kWidenRows = 128;
 
 int64_t avg_rows(int E, int S) { return (static_cast<int64_t>(S) + E - 1) / E; }

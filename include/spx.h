@@ -864,6 +864,9 @@ typedef enum spx_w_layout {
  * same weights, and the other way round.  offsets (device, int32[E+1]) is not
  * read on the host: nothing waits for the routing.  K == 0 gives zeros.
  * Launches: 1.
+ * The tensor cores run when A and W lie on 16-byte boundaries and lda, ldw and
+ * (E > 1) stride_w are multiples of 8 (N and K may be any); all else runs on
+ * the CUDA cores, which take about 80 times as long on large products.
  */
 spx_status spx_gemm_grouped(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const void* A,
                             int64_t lda, const void* W, int64_t ldw, int64_t stride_w, spx_w_layout layout,
@@ -876,6 +879,8 @@ spx_status spx_gemm_grouped(int32_t E, int32_t S, int32_t N, int32_t K, const in
  * `type`; dW_e starts at dW + e * stride_w, N rows of K, rows ldw apart, in
  * `w_type` (`type` or SPX_F32), rounded once from fp32.  For weights stored
  * K x N swap G and A (and N and K).  Launches: 1.
+ * Alignment as above, for G and A: 16-byte bases, ldg and lda multiples of 8
+ * for the tensor cores.
  */
 spx_status spx_gemm_grouped_wgrad(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const void* G,
                                   int64_t ldg, const void* A, int64_t lda, spx_type type, void* dW, int64_t ldw,
@@ -903,7 +908,8 @@ spx_status spx_quant_rows_i8(int32_t M, int32_t K, spx_type type, const void* X,
  * at W + e * stride_w, N rows of K, ldw apart.
  *   scratch: spx_gemm_i8_scratch_bytes(E, S, N, K, wide) bytes, 256-byte
  *     aligned (may be NULL when that is 0): the codes as 16-bit floats, which
- *     hold them exactly.  wide: not 0 when Q and W and their rows (ldq, ldw,
+ *     hold them exactly (rows off 16-byte boundaries always take these copies,
+ *     of Q and of every expert that has rows).  wide: not 0 when Q and W and their rows (ldq, ldw,
  *     stride_w) lie on 16-byte boundaries; none is needed then up to 128 rows an
  *     expert on average.
  * K == 0 gives zeros.  Launches: 1 or 2.

@@ -277,7 +277,7 @@ PRODUCTS = [("spread", 4, 300, 128, 64), ("spread", 3, 1000, 1000, 776), ("gaps"
             ("spread", 1, 1, 8, 8), ("spread", 2, 5, 1, 16), ("gaps", 40, 4097, 136, 72), ("spread", 8, 2000, 513, 257),
             ("spread", 300, 90, 40, 24), ("one", 2, 257, 256, 4096),
             ("spread", 200, 900, 200, 264), ("gaps", 7, 5000, 392, 648),
-            # few tiles and a long reduction: shared by two, four and eight CTAs
+            # few tiles and a long reduction: shared by four CTAs
             ("spread", 1, 16, 512, 8192), ("spread", 1, 100, 640, 4104), ("gaps", 2, 33, 384, 6000)]
 
 
