@@ -58,8 +58,8 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 // that nobody writes during the kernel's life, so every read of an array is a
 // coherent load, from an address that passed behind_wait() after
 // wait_for_previous(): the compiler cannot know that address sooner, and may
-// still batch and move the loads (volatile ones took 55 us for 41 in the
-// quantisation of 16384 x 4096 bf16, 8.9 for 6.2 in the 8-bit product of 8 rows
+// still batch and move the loads (volatile ones took 55 us for 36 in the
+// quantisation of 16384 x 4096 bf16, 8.9 for 6.1 in the 8-bit product of 8 rows
 // x 4096 x 4096).
 template <class T>
 __device__ __forceinline__ T* behind_wait(T* p) {
