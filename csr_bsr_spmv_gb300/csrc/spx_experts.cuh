@@ -223,7 +223,10 @@ struct SimtGemm {
     int E, S, NI, NJ, NR;          // rows of experts run over i (by_rows) or over r
     bool by_rows;
 };
+struct Gate;
 spx_status simt_gemm(const SimtGemm& g, spx_type type, spx_type c_type, cudaStream_t st);
+// The same with a gate (spx_act.cuh) between the sums and what is stored; kGate: R holds 2 NJ rows, kGateGrad: C may be NULL.
+spx_status simt_gated(const SimtGemm& g, const Gate& gate, spx_type type, spx_type c_type, cudaStream_t st);
 
 // The tensor-core form (spx_experts_tc.cu) of the product and of the weights'
 // gradient, for rows the copy engine can read: 16-byte aligned bases, row

@@ -202,6 +202,21 @@ def _load(path):
         "spx_gemm_i8_scratch_bytes": ([i32, i32, i32, i32, i32], sz),
         "spx_gemm_i8": ([i32, i32, i32, i32, vp, vp, i64, vp, vp, i64, i64, vp, vp, i64, ctypes.c_int, vp, sz, vp],
                         ctypes.c_int),
+        "spx_rms_norm": ([i32, i32, ctypes.c_int, vp, i64, vp, i64, vp, ctypes.c_int, f32, vp, i64, vp, i64, vp, vp],
+                         ctypes.c_int),
+        "spx_rms_norm_i8": ([i32, i32, ctypes.c_int, vp, i64, vp, i64, vp, ctypes.c_int, f32, vp, i64, vp, i64, vp, vp],
+                            ctypes.c_int),
+        "spx_rms_norm_grad_scratch_bytes": ([i32, i32], sz),
+        "spx_rms_norm_grad": ([i32, i32, ctypes.c_int, vp, i64, vp, i64, vp, vp, ctypes.c_int, vp, i64, vp, i64, vp, vp,
+                               sz, vp], ctypes.c_int),
+        "spx_gemm_grouped_gated": ([i32, i32, i32, i32, vp, vp, i64, vp, i64, i64, ctypes.c_int, ctypes.c_int, vp, i64, vp,
+                                    i64, ctypes.c_int, vp], ctypes.c_int),
+        "spx_gemm_grouped_gated_grad": ([i32, i32, i32, i32, vp, vp, i64, vp, i64, i64, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_int, vp, i64, vp, i64, vp, i64, vp], ctypes.c_int),
+        "spx_embed": ([i32, i32, i32, ctypes.c_int, vp, i32, vp, i64, f32, vp, i64, vp], ctypes.c_int),
+        "spx_embed_grad_scratch_bytes": ([i32, i32], sz),
+        "spx_embed_grad": ([i32, i32, i32, ctypes.c_int, vp, i32, i32, f32, vp, i64, vp, i64, ctypes.c_int, i32, vp, sz, vp],
+                           ctypes.c_int),
         "spx_gather_probe_blocks": ([], ctypes.c_int32),
         "spx_gather_probe": ([i64, vp, vp, vp, i32, vp, i32, vp], ctypes.c_int),
         "spx_last_device_error": ([vp], ctypes.c_int),
@@ -1137,6 +1152,233 @@ def spx_gemm_i8(Q: torch.Tensor, row_scale: torch.Tensor, W: torch.Tensor, w_sca
     if rc:
         raise SpxError(rc, "spx_gemm_i8")
     return C
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_scratch(lib, M: int, H: int) -> int:
+    return lib.spx_rms_norm_grad_scratch_bytes(M, H)
+
+
+@functools.lru_cache(maxsize=4096)
+def _embed_scratch(lib, T: int, H: int) -> int:
+    return lib.spx_embed_grad_scratch_bytes(T, H)
+
+
+def _norm_weight(weight, H: int, X: torch.Tensor):
+    """(address, type code) of a norm's weights, of the rows' type or float32; None: all ones."""
+    if weight is None:
+        return None, _SPX_TYPE[_F32]
+    if weight.dtype != X.dtype and weight.dtype != _F32:
+        raise ValueError(f"weight must be {X.dtype} or float32")
+    return _vec(weight, H, weight.dtype, "weight"), _type(weight)
+
+
+def _norm_sum(X: torch.Tensor, R, S, M: int, H: int, stream):
+    """The residual and the sum's operand: (R's pitch, address, S or None, S's pitch, address)."""
+    if R is None:
+        if S is None:
+            return 0, None, None, 0, None
+        ldr, r = 0, None
+    else:
+        n, m, ldr, r = _mat(R, "R")
+        if n != M or m != H or R.dtype != X.dtype:
+            raise ValueError(f"R must be {M} x {H} {X.dtype}")
+    S, lds, s = _out(S, M, H, X.dtype, X, "S", stream)
+    return ldr, r, S, lds, s
+
+
+def spx_rms_norm(X: torch.Tensor, weight: torch.Tensor | None = None, R: torch.Tensor | None = None, eps: float = 1e-6,
+                 Y: torch.Tensor | None = None, S: torch.Tensor | None = None, grad: bool = False, stream=None):
+    """(Y, S, rstd) with S = X + R (None without R), Y = S / sqrt(mean(S^2) + eps) * weight in X's type, and, with grad,
+    rstd[M] in float32 for spx_rms_norm_grad (else None).  S may be X or R; Y may be any of the three."""
+    M, H, ldx, x = _mat(X, "X")
+    code = _type(X)
+    w, w_code = _norm_weight(weight, H, X)
+    ldr, r, S, lds, s = _norm_sum(X, R, S, M, H, stream)
+    Y, ldy, y = _out(Y, M, H, X.dtype, X, "Y", stream)
+    rstd = _new(M, _F32, X, stream) if grad else None
+    rc = _lib().spx_rms_norm(M, H, code, x, ldx, r, ldr, w, w_code, eps, s, lds, y, ldy,
+                             rstd.data_ptr() if grad and M else None, _raw_stream(stream, X, R, weight, S, Y))
+    if rc:
+        raise SpxError(rc, "spx_rms_norm")
+    return Y, S, rstd
+
+
+def spx_rms_norm_i8(X: torch.Tensor, weight: torch.Tensor | None = None, R: torch.Tensor | None = None, eps: float = 1e-6,
+                    Q: torch.Tensor | None = None, scale: torch.Tensor | None = None, S: torch.Tensor | None = None,
+                    stream=None):
+    """(Q int8, scale fp32, S): the norm's rows divided by their largest magnitude / 127 and rounded to whole numbers, as
+    spx_gemm_i8 reads them; S = X + R (None without R)."""
+    M, H, ldx, x = _mat(X, "X")
+    code = _type(X)
+    w, w_code = _norm_weight(weight, H, X)
+    ldr, r, S, lds, s = _norm_sum(X, R, S, M, H, stream)
+    Q, ldq, q = _out(Q, M, H, _I8, X, "Q", stream)
+    if scale is None:
+        scale = _new(M, _F32, X, stream)
+        to = scale.data_ptr() if M else None
+    else:
+        to = _vec(scale, M, _F32, "scale")
+    rc = _lib().spx_rms_norm_i8(M, H, code, x, ldx, r, ldr, w, w_code, eps, s, lds, q, ldq, to,
+                                _raw_stream(stream, X, R, weight, S, Q, scale))
+    if rc:
+        raise SpxError(rc, "spx_rms_norm_i8")
+    return Q, scale, S
+
+
+def spx_rms_norm_grad(dY: torch.Tensor, S: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor | None = None,
+                      dS: torch.Tensor | None = None, dX: torch.Tensor | None = None, dweight: bool = True, stream=None,
+                      scratch: torch.Tensor | None = None):
+    """Gradients of spx_rms_norm: (dX, dweight[H] fp32, None if not wanted).  S: the sum (X without a residual); dS: what
+    arrives at the sum from elsewhere.  dX is the gradient of X and of R; it may be dY, S or dS."""
+    M, H, lddy, dy = _mat(dY, "dY")
+    code = _type(dY)
+    w, w_code = _norm_weight(weight, H, dY)
+    n, m, lds, s = _mat(S, "S")
+    if n != M or m != H or S.dtype != dY.dtype:
+        raise ValueError(f"S must be {M} x {H} {dY.dtype}")
+    ldr, r = 0, None
+    if dS is not None:
+        n, m, ldr, r = _mat(dS, "dS")
+        if n != M or m != H or dS.dtype != dY.dtype:
+            raise ValueError(f"dS must be {M} x {H} {dY.dtype}")
+    dX, lddx, dx = _out(dX, M, H, dY.dtype, dY, "dX", stream)
+    lib = _lib()
+    dw, dwp, work, size = None, None, None, 0
+    if dweight:
+        dw = _new(H, _F32, dY, stream)
+        dwp = dw.data_ptr() if H else None
+        need = _norm_scratch(lib, M, H)
+        if need:
+            if scratch is None:
+                scratch = _new(need // 4, _F32, dY, stream)
+            work, size = scratch.data_ptr(), scratch.numel() * scratch.element_size()
+    rc = lib.spx_rms_norm_grad(M, H, code, dy, lddy, s, lds, _vec(rstd, M, _F32, "rstd"), w, w_code, r, ldr, dx, lddx, dwp,
+                               work, size, _raw_stream(stream, dY, S, rstd, weight, dS, dX, scratch))
+    if rc:
+        raise SpxError(rc, "spx_rms_norm_grad")
+    return dX, dw
+
+
+_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _act(name: str) -> int:
+    code = _ACT.get(name)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(_ACT)}")
+    return code
+
+
+def spx_gemm_grouped_gated(offsets: torch.Tensor | None, A: torch.Tensor, W: torch.Tensor, act: str = "silu",
+                           C: torch.Tensor | None = None, H: torch.Tensor | None = None, grad: bool = False,
+                           dtype: torch.dtype | None = None, stream=None):
+    """(C, H): C[p] = act(A[p] Wg_e^T) * (A[p] Wu_e^T) for expert e's rows, W[e] = the gate's F rows, then the other
+    factor's; with grad (or H given) H[S, 2F] holds both factors before the activation, for
+    spx_gemm_grouped_gated_grad.  offsets None: W is 2F x K and takes all rows.  C in A's type or float32 (dtype)."""
+    S, K, lda, a = _mat(A, "A")
+    if offsets is None:
+        E, sw, off = 1, 0, None
+        two, k, ldw, w = _mat(W, "W")
+    else:
+        E, two, k, ldw, sw, w = _experts(W, "W")
+        off = _vec(offsets, E + 1, _I32, "offsets")
+    dt = A.dtype
+    if k != K or W.dtype != dt or two % 2:
+        raise ValueError("A and W do not fit")
+    F = two // 2
+    code, kind = _type(A), _act(act)
+    C, ldc, c = _out(C, S, F, (dtype or dt) if C is None else dtype, A, "C", stream)
+    ldh, h = 0, None
+    if grad or H is not None:
+        H, ldh, h = _out(H, S, two, dt, A, "H", stream)
+    rc = _lib().spx_gemm_grouped_gated(E, S, F, K, off, a, lda, w, ldw, sw, kind, code, h, ldh, c, ldc, _type(C),
+                                       _raw_stream(stream, A, W, C, H, offsets))
+    if rc:
+        raise SpxError(rc, "spx_gemm_grouped_gated")
+    return C, H
+
+
+def spx_gemm_grouped_gated_grad(offsets: torch.Tensor | None, dY: torch.Tensor, W: torch.Tensor, H: torch.Tensor,
+                                act: str = "silu", layout: str = "kn", dH: torch.Tensor | None = None,
+                                C: torch.Tensor | None = None, product: bool = True, stream=None):
+    """(dH, C): the gradient of both factors H (S x 2F) through the experts' second weights W, N rows of F ("kn", what
+    spx_gemm_grouped takes as "nk") or F rows of N ("nk"), from dY (S x N); and, unless product is False, C = act(G) * U
+    once more, for the second weights' gradient.  offsets None: W is 2-D and takes all rows.  dH may be H."""
+    S, N, lddy, dy = _mat(dY, "dY")
+    if offsets is None:
+        E, sw, off = 1, 0, None
+        n, F, ldw, w = _mat(W, "W")
+    else:
+        E, n, F, ldw, sw, w = _experts(W, "W")
+        off = _vec(offsets, E + 1, _I32, "offsets")
+    kn = 1
+    if layout == "nk":
+        n, F, kn = F, n, 0
+    elif layout != "kn":
+        raise ValueError("layout must be 'nk' or 'kn'")
+    dt = dY.dtype
+    if n != N or W.dtype != dt:
+        raise ValueError("dY and W do not fit")
+    rows, two, ldh, h = _mat(H, "H")
+    if rows != S or two != 2 * F or H.dtype != dt:
+        raise ValueError(f"H must be {S} x {2 * F} {dt}")
+    code, kind = _type(dY), _act(act)
+    dH, lddh, dh = _out(dH, S, two, dt, dY, "dH", stream)
+    ldc, c = 0, None
+    if product or C is not None:
+        C, ldc, c = _out(C, S, F, dt, dY, "C", stream)
+    rc = _lib().spx_gemm_grouped_gated_grad(E, S, F, N, off, dy, lddy, w, ldw, sw, kn, kind, code, h, ldh, dh, lddh, c, ldc,
+                                            _raw_stream(stream, dY, W, H, dH, C, offsets))
+    if rc:
+        raise SpxError(rc, "spx_gemm_grouped_gated_grad")
+    return dH, C
+
+
+def _ids(ids: torch.Tensor):
+    """(tokens, address, bytes an id) of a dense device array of ids of any shape."""
+    dt = ids.dtype
+    if dt != torch.int64 and dt != _I32:
+        raise ValueError("token ids must be int32 or int64")
+    T = ids.numel()
+    return T, _vec(ids, T, dt, "ids"), 4 if dt == _I32 else 8
+
+
+def spx_embed(ids: torch.Tensor, W: torch.Tensor, scale: float = 1.0, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y[t] = scale * W[ids[t]] (T x H, W's type), T the number of ids, of any shape; an id outside W's rows gives zeros."""
+    T, at, size = _ids(ids)
+    V, H, ldw, w = _mat(W, "W")
+    code = _type(W)
+    Y, ldy, y = _out(Y, T, H, W.dtype, W, "Y", stream)
+    rc = _lib().spx_embed(T, H, V, code, at, size, w, ldw, scale, y, ldy, _raw_stream(stream, W, ids, Y))
+    if rc:
+        raise SpxError(rc, "spx_embed")
+    return Y
+
+
+def spx_embed_grad(ids: torch.Tensor, dY: torch.Tensor, V: int, scale: float = 1.0, padding: int | None = None,
+                   dW: torch.Tensor | None = None, dtype: torch.dtype | None = None, accumulate: bool = False, stream=None,
+                   scratch: torch.Tensor | None = None) -> torch.Tensor:
+    """dW[v] = scale * sum of dY[t] over the tokens with ids[t] == v, in dY's type or float32 (dtype), V rows; the id
+    `padding` adds nothing.  accumulate: the sums are added to dW."""
+    T, at, size = _ids(ids)
+    n, H, lddy, dy = _mat(dY, "dY")
+    if n != T:
+        raise ValueError("dY needs one row a token")
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs dW")
+    code = _type(dY)
+    dW, lddw, dw = _out(dW, V, H, (dtype or dY.dtype) if dW is None else dtype, dY, "dW", stream)
+    lib = _lib()
+    need = _embed_scratch(lib, T, H)
+    if scratch is None:
+        scratch = _new(need, torch.uint8, dY, stream)
+    rc = lib.spx_embed_grad(T, H, V, code, at, size, -1 if padding is None else padding, scale, dy, lddy, dw, lddw,
+                            _type(dW), int(accumulate), scratch.data_ptr(), scratch.numel() * scratch.element_size(),
+                            _raw_stream(stream, dY, ids, dW, scratch))
+    if rc:
+        raise SpxError(rc, "spx_embed_grad")
+    return dW
 
 
 def spx_gather_probe(A: Csr, x: torch.Tensor, partials: torch.Tensor | None = None, stream=None) -> torch.Tensor:

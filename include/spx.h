@@ -921,6 +921,131 @@ spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t
                        const float* w_scale, void* C, int64_t ldc, spx_type c_type, void* scratch,
                        size_t scratch_bytes, spx_stream_t stream);
 
+/* ------------------------------------------------------------ a block around routed experts */
+
+/*
+ * What a block of a language model has around and inside its routed experts:
+ * rows of a table by token id, the norm before the router and the experts, and
+ * experts with a gate, each with its gradient.  As above, nothing here
+ * synchronises or allocates, sums are fp32 in an order that does not depend on
+ * timing, and pointers need only their elements' alignment (16-byte aligned
+ * rows run on wider copies).
+ */
+
+/*
+ * The root-mean-square norm of rows, after the residual's addition:
+ *   s = X[m] + R[m]  (R NULL: X[m]),  S[m] = s,
+ *   rstd[m] = 1 / sqrt(mean(s^2) + eps),  Y[m] = s * rstd[m] * weight
+ * with s, the mean and Y in fp32; S and Y are rounded once each to `type`
+ * (SPX_F32, SPX_BF16, SPX_F16), Y from the s that was not rounded.  weight
+ * (H values of `type` or fp32) may be NULL: all ones; S and rstd (fp32, for the
+ * gradient) may be NULL.  S may be X or R, and Y may be any of the three, with
+ * the same row pitch.  Rows of 1 to SPX_NORM_MAX_H values
+ * (SPX_ERR_UNSUPPORTED beyond).  Squares whose mean passes fp32's range give
+ * zeros.  Launches: 1.
+ */
+#define SPX_NORM_MAX_H 32768
+spx_status spx_rms_norm(int32_t M, int32_t H, spx_type type, const void* X, int64_t ldx, const void* R, int64_t ldr,
+                        const void* weight, spx_type w_type, float eps, void* S, int64_t lds, void* Y, int64_t ldy,
+                        float* rstd, spx_stream_t stream);
+
+/*
+ * The same with an output that spx_gemm_i8 reads: scale[m] = max_h |Y[m, h]| /
+ * 127 and Q[m, h] = Y[m, h] / scale[m] rounded to the nearest whole number
+ * (ties to even), from the fp32 Y that was not rounded.  A row of zeros gets
+ * scale 0 and codes 0; a row whose Y holds an infinity or NaN gets scale NaN
+ * and codes 0, as in spx_quant_rows_i8.  Launches: 1.
+ */
+spx_status spx_rms_norm_i8(int32_t M, int32_t H, spx_type type, const void* X, int64_t ldx, const void* R, int64_t ldr,
+                           const void* weight, spx_type w_type, float eps, void* S, int64_t lds, int8_t* Q, int64_t ldq,
+                           float* scale, spx_stream_t stream);
+
+/*
+ * The gradients of spx_rms_norm.  For dY, the gradient of Y, and dS, what
+ * arrives at S from elsewhere (the residual stream; NULL: nothing), with
+ * g = dY[m] * weight and n = S[m] * rstd[m]:
+ *   dX[m] = rstd[m] * (g - n * mean(g * n)) + dS[m]   (X's gradient, and R's)
+ *   dweight = sum over m of dY[m] * n                 (fp32; NULL: not computed)
+ * S is what the forward pass stored (X itself without a residual), rstd what
+ * it returned.  dX may be dY, S or dS with the same row pitch.  M == 0 sets
+ * dweight to zeros.
+ *   scratch: spx_rms_norm_grad_scratch_bytes(M, H) bytes (0 without dweight),
+ *     4-byte aligned.
+ * Launches: 1, or 2 with dweight.
+ */
+size_t spx_rms_norm_grad_scratch_bytes(int32_t M, int32_t H);
+spx_status spx_rms_norm_grad(int32_t M, int32_t H, spx_type type, const void* dY, int64_t lddy, const void* S, int64_t lds,
+                             const float* rstd, const void* weight, spx_type w_type, const void* dS, int64_t ldds, void* dX,
+                             int64_t lddx, float* dweight, void* scratch, size_t scratch_bytes, spx_stream_t stream);
+
+/* Activations: x sigmoid(x); x Phi(x) with the normal distribution's Phi; x sigmoid(2 sqrt(2 / pi) (x + 0.044715 x^3)). */
+typedef enum spx_act {
+    SPX_ACT_SILU = 0,
+    SPX_ACT_GELU = 1,
+    SPX_ACT_GELU_TANH = 2
+} spx_act;
+
+/*
+ * The product of experts with a gate: W_e holds 2 F rows of K, the gate's F
+ * rows and then those of the other factor.  For the rows p of expert e
+ *   G[p] = A[p] Wg_e^T,  U[p] = A[p] Wu_e^T,  C[p, f] = act(G[p, f]) * U[p, f]
+ * in fp32, rounded once: C (S x F) to c_type (`type` or SPX_F32), and, where H
+ * is not NULL, H (S x 2 F, `type`) = G beside U, which the gradient reads.
+ * C comes from the G and U that were not rounded.  Zeros in the rows from
+ * offsets[E] on.  offsets NULL (then E must be 1): all S rows belong to the one
+ * weight matrix.  type is SPX_BF16 or SPX_F16.  K == 0 gives zeros.  Launches:
+ * 1.  Alignment for the tensor cores as in spx_gemm_grouped.
+ */
+spx_status spx_gemm_grouped_gated(int32_t E, int32_t S, int32_t F, int32_t K, const int32_t* offsets, const void* A,
+                                  int64_t lda, const void* W, int64_t ldw, int64_t stride_w, spx_act act, spx_type type,
+                                  void* H, int64_t ldh, void* C, int64_t ldc, spx_type c_type, spx_stream_t stream);
+
+/*
+ * Its gradient, through the experts' second product: dY (S x N) is the
+ * gradient of Y[p] = C[p] times expert e's second weights W_e, N rows of F
+ * (SPX_W_KN, the product that spx_gemm_grouped takes as SPX_W_NK) or F rows of
+ * N (SPX_W_NK), and H what spx_gemm_grouped_gated stored.  In fp32,
+ *   dC[p, f] = sum_n dY[p, n] W_e[n, f],  a = act(G[p, f]),  U = U[p, f]
+ *   dH[p, f] = dC U act'(G[p, f]),  dH[p, F + f] = dC a,  C[p, f] = a U
+ * each rounded once to `type`; C (NULL: not computed) is what the second
+ * weights' gradient needs, spx_gemm_grouped_wgrad(dY, C), so the forward pass
+ * need not keep it.  The first weights' gradient is spx_gemm_grouped_wgrad(dH,
+ * A), A's is the SPX_W_KN product of dH with the first weights.  Rows from
+ * offsets[E] on are zeros, whatever H holds there.  dH may be H with the same
+ * row pitch.  offsets NULL as above.  Launches: 1.
+ */
+spx_status spx_gemm_grouped_gated_grad(int32_t E, int32_t S, int32_t F, int32_t N, const int32_t* offsets, const void* dY,
+                                       int64_t lddy, const void* W, int64_t ldw, int64_t stride_w, spx_w_layout layout,
+                                       spx_act act, spx_type type, const void* H, int64_t ldh, void* dH, int64_t lddh,
+                                       void* C, int64_t ldc, spx_stream_t stream);
+
+/*
+ * Rows of a table by token id, a product with a sparse matrix of one entry a
+ * row: Y[t] = scale * W[ids[t]], in fp32, rounded once.  W is V x H (ldw), Y is
+ * T x H (ldy), both `type` (SPX_F32, SPX_BF16, SPX_F16); ids holds T int32 or
+ * int64 values (id_bytes 4 or 8).  An id outside [0, V) gives zeros.
+ * Launches: 1.
+ */
+spx_status spx_embed(int32_t T, int32_t H, int32_t V, spx_type type, const void* ids, int32_t id_bytes, const void* W,
+                     int64_t ldw, float scale, void* Y, int64_t ldy, spx_stream_t stream);
+
+/*
+ * The table's gradient, the product with that matrix's transpose: the tokens
+ * are sorted by id (stable), then
+ *   dW[v] = scale * sum over the tokens t with ids[t] == v of dY[t]
+ * summed in fp32 in an order that is the same from run to run, rounded once to
+ * w_type (`type` or SPX_F32).  Ids outside [0, V), and the id `padding` (-1:
+ * none), add nothing.  accumulate 0: every row of dW is written, zeros where no
+ * token has its id; 1: the sums are added to dW, whose other rows are not
+ * touched.
+ *   scratch: spx_embed_grad_scratch_bytes(T, H) bytes, 16-byte aligned.
+ * Launches: 3 (none for T == 0 with accumulate).
+ */
+size_t spx_embed_grad_scratch_bytes(int32_t T, int32_t H);
+spx_status spx_embed_grad(int32_t T, int32_t H, int32_t V, spx_type type, const void* ids, int32_t id_bytes, int32_t padding,
+                          float scale, const void* dY, int64_t lddy, void* dW, int64_t lddw, spx_type w_type,
+                          int32_t accumulate, void* scratch, size_t scratch_bytes, spx_stream_t stream);
+
 /* ------------------------------------------------------------ measurement */
 
 /*
