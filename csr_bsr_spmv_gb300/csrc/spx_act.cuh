@@ -13,7 +13,7 @@ enum Epilogue : int { kNone = 0, kGate = 1, kGateGrad = 2 };
 // wanted; kGateGrad the sums are dC, and dH and (where wanted) C come from H.
 struct Gate {
     Epilogue epi = kNone;
-    int act = 0, F = 0;
+    int act = 0;
     void* H = nullptr;  // kGate: written, NULL: not; kGateGrad: read
     long long ldh = 0;
     void* dH = nullptr;

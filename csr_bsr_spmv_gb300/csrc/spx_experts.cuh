@@ -235,6 +235,11 @@ bool tc_product_fits(const void* A, int64_t lda, const void* W, int64_t ldw, int
 spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void* A, int64_t lda, const void* W,
                       int64_t ldw, int64_t stride_w, spx_w_layout layout, spx_type type, void* C, int64_t ldc,
                       spx_type c_type, cudaStream_t st);
+// The product with a gate behind its sums, and its gradient (spx_act.cuh).
+spx_status tc_gated(int E, int S, int F, int K, const int* offsets, const void* A, int64_t lda, const void* W, int64_t ldw, int64_t stride_w,
+                    const Gate& gate, spx_type type, void* C, int64_t ldc, spx_type c_type, cudaStream_t st);
+spx_status tc_gated_grad(int E, int S, int F, int N, const int* offsets, const void* dY, int64_t lddy, const void* W, int64_t ldw,
+                         int64_t stride_w, spx_w_layout layout, const Gate& gate, spx_type type, void* C, int64_t ldc, cudaStream_t st);
 spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const void* Q, int64_t ldq,
                          const float* row_scale, const void* W, int64_t ldw, int64_t mats, const float* col_scale,
                          void* C, int64_t ldc, spx_type c_type, cudaStream_t st);

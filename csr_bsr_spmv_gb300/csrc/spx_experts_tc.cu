@@ -5,6 +5,8 @@
 //   kNK  C[p, n] = sum_k A[p, k] W_e[n, k]      both with k contiguous (K-major)
 //   kKN  C[p, n] = sum_k A[p, k] W_e[k, n]      the weights with n contiguous (MN-major)
 //   kWG  dW_e[n, k] = sum_p G[p, n] A[p, k]     both MN-major, the reduction runs over the expert's rows
+// and three that the sums are stored: as they are, through the experts' gate,
+// or through its gradient (Epilogue in spx_act.cuh).
 // The MMA computes the transposed tile: its 128 lanes (256 for a CTA pair)
 // run along the output's contiguous axis -- n, or k for kWG -- and its columns
 // along the output's rows -- tokens, or n for kWG.  So each TMEM lane is one
@@ -35,6 +37,7 @@
 #include <algorithm>
 #include <tuple>
 
+#include "spx_act.cuh"
 #include "spx_experts.cuh"
 #include "spx_experts_tile.h"
 #include "spx_tc.cuh"
@@ -110,6 +113,10 @@ struct TcArgs {
     bool wide_f;      // fp32 output with rows on 16-byte boundaries, NL a multiple of 4
     bool wide_c;      // 16-bit output with rows on 16-byte boundaries, NL a multiple of 8
     const float *row_scale, *col_scale;  // 8-bit integers: [S], [E * NL]
+    Gate gate;        // kGate, kGateGrad
+    spx_type h_type;
+    bool wide_h;      // H and dH with rows and halves on 16-byte boundaries
+    bool by16;        // kGate: F a multiple of 16, one copy a stage
 };
 
 struct Item {
@@ -202,6 +209,36 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, in
             "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
             "{%2, %3, %4}], [%5];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+}
+
+// The gate's weights (kGate): 16 rows of the gate and the same 16 of the other factor, in turn.
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar, bool pair) {
+    if (!pair)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+            "%5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+            "{%2, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+            : "memory");
+}
+__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, int v, uint32_t bar, bool pair) {
+    if (!pair)
+        asm volatile(
+            "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+            "%5, %6}], [%7];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+            "{%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
             : "memory");
 }
 
@@ -372,23 +409,287 @@ __device__ __forceinline__ void store_rows(const TcArgs& a, const Item& it, O* C
     }
 }
 
+// ---------------- the gate between the sums and what is stored
+//
+// Forward (kGate), a warp's 32 lanes hold 16 columns of the gate and then the
+// same 16 of the other factor, so that a thread's fragments have both sums of
+// an output: v[i] and v[16 + i].  A tile of 128 lanes then gives 64 columns.
+
+// Column group hg (eight columns of a row's 32) of a warp's 32 rows to its patch, transposed.
+__device__ __forceinline__ void patch_in(uint32_t patch, int lane, int hg, uint32_t q0, uint32_t q1, uint32_t q2, uint32_t q3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(patch + lane * kPatchPitch + 16 * hg),
+                 "r"(q0), "r"(q1), "r"(q2), "r"(q3)
+                 : "memory");
+}
+__device__ __forceinline__ void patch_out(uint32_t patch, int lane, int hg, uint32_t (&q)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+                 : "r"(patch + lane * kPatchPitch + 16 * hg)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 patch_row(uint32_t patch, int r, int p) {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(patch + r * kPatchPitch + 16 * p)
+                 : "memory");
+    return w;
+}
+
+// 32 rows from it.row0 + c0 on of the 16 columns from x on: H, and C in its type.
+template <class V>
+__device__ __forceinline__ void store_factors(const TcArgs& a, const Item& it, int x, int lane, uint32_t patch, int c0, const float (&v)[32]) {
+    const int rows = it.rows - c0, cols = a.NL - x;
+    V* H = static_cast<V*>(a.gate.H) + (it.row0 + c0) * a.gate.ldh + x;
+    if (a.wide_h) {
+#pragma unroll
+        for (int hg = 0; hg < 4; ++hg) {
+            const float* f = v + 16 * (hg >> 1) + 2 * (hg & 1);
+            patch_in(patch, lane, hg, pack<V>(f[0], f[1]), pack<V>(f[4], f[5]), pack<V>(f[8], f[9]), pack<V>(f[12], f[13]));
+        }
+        __syncwarp();
+        const int r = lane >> 2, p = lane & 3, c = 8 * (p & 1);
+        V* q = H + r * a.gate.ldh + c + (p >> 1) * static_cast<long long>(a.NL);
+#pragma unroll
+        for (int u = 0; u < 4; ++u, q += 8 * a.gate.ldh) {
+            const uint4 w = patch_row(patch, r + 8 * u, p);
+            if (r + 8 * u < rows && c < cols) *reinterpret_cast<uint4*>(q) = w;
+        }
+        __syncwarp();
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const int n = (lane >> 2) + 8 * ((i >> 1) & 1), r = 8 * ((i >> 2) & 3) + 2 * (lane & 3) + (i & 1);
+        if (n < cols && r < rows) H[r * a.gate.ldh + n + (i >> 4) * static_cast<long long>(a.NL)] = from_f<V>(v[i]);
+    }
+}
+
+template <class O>
+__device__ __forceinline__ void store_gated(const TcArgs& a, const Item& it, int x, int lane, uint32_t patch, int c0, const float (&v)[32]) {
+    const int rows = it.rows - c0, cols = a.NL - x;
+    O* C = static_cast<O*>(a.C) + (it.row0 + c0) * a.ldc + x;
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = act_of(a.gate.act, v[i]) * v[16 + i];
+    if constexpr (sizeof(O) == 2) {
+        if (a.wide_c) {
+#pragma unroll
+            for (int hg = 0; hg < 2; ++hg) {
+                const float* g = f + 2 * hg;
+                patch_in(patch, lane, hg, pack<O>(g[0], g[1]), pack<O>(g[4], g[5]), pack<O>(g[8], g[9]), pack<O>(g[12], g[13]));
+            }
+            __syncwarp();
+            const int r = lane >> 1, p = lane & 1;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint4 w = patch_row(patch, r + 16 * u, p);
+                if (r + 16 * u < rows && 8 * p < cols) *reinterpret_cast<uint4*>(C + (r + 16 * u) * a.ldc + 8 * p) = w;
+            }
+            __syncwarp();
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int n = (lane >> 2) + 8 * ((i >> 1) & 1), r = 8 * ((i >> 2) & 3) + 2 * (lane & 3) + (i & 1);
+        if (n < cols && r < rows) C[r * a.ldc + n] = from_f<O>(f[i]);
+    }
+}
+
+__device__ __forceinline__ void store_gate(const TcArgs& a, const Item& it, int x, int lane, uint32_t patch, int c0, const float (&v)[32]) {
+    if (a.gate.H) {
+        if (a.h_type == SPX_BF16) store_factors<__nv_bfloat16>(a, it, x, lane, patch, c0, v);
+        else store_factors<__half>(a, it, x, lane, patch, c0, v);
+    }
+    if (a.c_type == SPX_F32) store_gated<float>(a, it, x, lane, patch, c0, v);
+    else if (a.c_type == SPX_BF16) store_gated<__nv_bfloat16>(a, it, x, lane, patch, c0, v);
+    else store_gated<__half>(a, it, x, lane, patch, c0, v);
+}
+
+// Gradient (kGateGrad): the sums are dC; both factors come from H, dH and C go out.  On wide rows H's 32 rows x 32
+// columns are fetched in whole pieces ahead of the sums and reach the fragments' order through the warp's patch.
+struct Factors {
+    uint4 g[4], u[4];  // thread (r = lane / 4, p = lane % 4): rows r + 8 i, columns 8 p to 8 p + 7
+};
+
+__device__ __forceinline__ void fetch_factors(const TcArgs& a, const Item& it, int x, int lane, int c0, Factors& h) {
+    const int r = lane >> 2, p = lane & 3;
+    const uint16_t* H = behind_wait(static_cast<const uint16_t*>(a.gate.H)) + (it.row0 + c0 + r) * a.gate.ldh + x + 8 * p;
+    const bool on = it.e < a.E && 8 * p < a.NL - x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, H += 8 * a.gate.ldh) {
+        h.g[i] = h.u[i] = make_uint4(0, 0, 0, 0);
+        if (on && r + 8 * i < it.rows - c0) {
+            h.g[i] = load_once(reinterpret_cast<const uint4*>(H));
+            h.u[i] = load_once(reinterpret_cast<const uint4*>(H + a.NL));
+        }
+    }
+}
+
+// A thread's pieces of a 32 x 32 block to fragments: q[4 hg + j] holds rows 8 j + 2 (lane % 4) and the next of column
+// 8 hg + lane / 4; and back.
+__device__ __forceinline__ void to_fragments(uint32_t patch, int lane, const uint4 (&w)[4], uint32_t (&q)[16]) {
+    const int r = lane >> 2, p = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + (r + 8 * i) * kPatchPitch + 16 * p), "r"(w[i].x), "r"(w[i].y),
+                     "r"(w[i].z), "r"(w[i].w)
+                     : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int hg = 0; hg < 4; ++hg) {
+        uint32_t t[4];
+        patch_out(patch, lane, hg, t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[4 * hg + j] = t[j];
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void store_fragments(uint32_t patch, int lane, const uint32_t (&q)[16], uint16_t* out, long long ld, int rows, int cols) {
+#pragma unroll
+    for (int hg = 0; hg < 4; ++hg) patch_in(patch, lane, hg, q[4 * hg], q[4 * hg + 1], q[4 * hg + 2], q[4 * hg + 3]);
+    __syncwarp();
+    const int r = lane >> 2, p = lane & 3;
+    out += r * ld + 8 * p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, out += 8 * ld) {
+        const uint4 w = patch_row(patch, r + 8 * i, p);
+        if (r + 8 * i < rows && 8 * p < cols) *reinterpret_cast<uint4*>(out) = w;
+    }
+    __syncwarp();
+}
+
+template <class V>
+__device__ __forceinline__ float2 unpack(uint32_t w) {
+    V v[2];
+    memcpy(v, &w, 4);
+    return make_float2(to_f(v[0]), to_f(v[1]));
+}
+
+// dG, dU and C of one output; all zeros in the rows past the last expert's, whatever H holds there.
+__device__ __forceinline__ void gate_grad(const TcArgs& a, bool live, float dc, float g, float u, float& dg, float& du, float& c) {
+    float slope;
+    const float act = act_of(a.gate.act, g, slope);
+    dg = live ? dc * u * slope : 0.f;
+    du = live ? dc * act : 0.f;
+    c = live ? act * u : 0.f;
+}
+
+template <class V>
+__device__ __forceinline__ void store_gate_grad(const TcArgs& a, const Item& it, int x, int lane, uint32_t patch, int c0,
+                                                const uint32_t (&v)[32], Factors& h, bool more) {
+    const int rows = it.rows - c0, cols = a.NL - x;
+    const bool live = it.e < a.E;
+    const long long row = it.row0 + c0;
+    V* dH = static_cast<V*>(a.gate.dH) + row * a.gate.lddh + x;
+    V* C = static_cast<V*>(a.C) + row * a.ldc + x;
+    if (a.wide_h) {
+        uint32_t g[16], u[16];
+        to_fragments(patch, lane, h.g, g);
+        to_fragments(patch, lane, h.u, u);
+        if (more) fetch_factors(a, it, x, lane, c0 + 64, h);
+        uint32_t dg[16], du[16], c[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int i = 16 * (j >> 3) + 2 * (j >> 2 & 1) + 4 * (j & 3);  // v's index of this pair
+            const float2 fg = unpack<V>(g[j]), fu = unpack<V>(u[j]);
+            float2 a0, a1, a2;
+            gate_grad(a, live, __uint_as_float(v[i]), fg.x, fu.x, a0.x, a1.x, a2.x);
+            gate_grad(a, live, __uint_as_float(v[i + 1]), fg.y, fu.y, a0.y, a1.y, a2.y);
+            dg[j] = pack<V>(a0.x, a0.y), du[j] = pack<V>(a1.x, a1.y), c[j] = pack<V>(a2.x, a2.y);
+        }
+        store_fragments(patch, lane, dg, reinterpret_cast<uint16_t*>(dH), a.gate.lddh, rows, cols);
+        store_fragments(patch, lane, du, reinterpret_cast<uint16_t*>(dH + a.NL), a.gate.lddh, rows, cols);
+        if (a.C) store_fragments(patch, lane, c, reinterpret_cast<uint16_t*>(C), a.ldc, rows, cols);
+        return;
+    }
+    const V* H = behind_wait(static_cast<const V*>(a.gate.H)) + row * a.gate.ldh + x;
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i) {
+        const int n = 16 * (i >> 4) + (lane >> 2) + 8 * ((i >> 1) & 1), r = 8 * ((i >> 2) & 3) + 2 * (lane & 3) + (i & 1);
+        if (n >= cols || r >= rows) continue;
+        float dc = 0.f, dg, du, c;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j == i) dc = __uint_as_float(v[j]);
+        const V* p = H + r * a.gate.ldh + n;
+        gate_grad(a, live, dc, to_f(load(p)), to_f(load(p + a.NL)), dg, du, c);
+        V* d = dH + r * a.gate.lddh + n;
+        d[0] = from_f<V>(dg);
+        d[a.NL] = from_f<V>(du);
+        if (a.C) C[r * a.ldc + n] = from_f<V>(c);
+    }
+}
+
 // Pitch of a shared partial tile: a row of 128 sums and four words of slack,
 // so that a fragment's stores touch every bank once.
 constexpr uint32_t kPartPitch = 132 * 4;
 
-// Four sums of this lane's columns of one output row (shared reductions).
+// Four values of neighbouring columns, `left` of them inside the row.
 template <class O>
-__device__ __forceinline__ void store_four(const TcArgs& a, long long row, int x, const float (&f)[4]) {
-    O* q = static_cast<O*>(a.C) + row * a.ldc + x;
-    if (a.wide_c || (sizeof(O) == 4 && a.wide_f)) {
-        if (x + 4 > a.NL) return;
+__device__ __forceinline__ void put_four(O* q, int left, bool wide, const float (&f)[4]) {
+    if (wide) {
+        if (left < 4) return;
         if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(q) = make_uint2(pack<O>(f[0], f[1]), pack<O>(f[2], f[3]));
         else *reinterpret_cast<float4*>(q) = make_float4(f[0], f[1], f[2], f[3]);
         return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (x + i < a.NL) q[i] = from_f<O>(f[i]);
+        if (i < left) q[i] = from_f<O>(f[i]);
+}
+
+// Four sums of this lane's columns of one output row (shared reductions).
+template <class O>
+__device__ __forceinline__ void store_four(const TcArgs& a, long long row, int x, const float (&f)[4]) {
+    put_four(static_cast<O*>(a.C) + row * a.ldc + x, a.NL - x, a.wide_c || (sizeof(O) == 4 && a.wide_f), f);
+}
+
+// The same through the gate: lanes 8 i to 8 i + 3 of a warp hold 16 columns of the gate, the next four those of the other factor.
+__device__ __forceinline__ void gate_four(const TcArgs& a, const Item& it, int r, int lane, const float (&f)[4]) {
+    const long long row = it.row0 + r;
+    const int x = it.lane0 / 2 + 16 * (lane >> 3) + 4 * (lane & 3);
+    const bool up = lane & 4;
+    float c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float u = __shfl_xor_sync(0xffffffffu, f[i], 4);
+        c[i] = up ? 0.f : act_of(a.gate.act, f[i]) * u;
+    }
+    if (a.gate.H) {
+        const long long at = row * a.gate.ldh + x + (up ? a.NL : 0);
+        if (a.h_type == SPX_BF16) put_four(static_cast<__nv_bfloat16*>(a.gate.H) + at, a.NL - x, a.wide_h, f);
+        else put_four(static_cast<__half*>(a.gate.H) + at, a.NL - x, a.wide_h, f);
+    }
+    if (up) return;
+    if (a.c_type == SPX_F32) store_four<float>(a, row, x, c);
+    else if (a.c_type == SPX_BF16) store_four<__nv_bfloat16>(a, row, x, c);
+    else store_four<__half>(a, row, x, c);
+}
+
+template <class V>
+__device__ __forceinline__ void gate_grad_four(const TcArgs& a, const Item& it, int r, int lane, const float (&f)[4]) {
+    const long long row = it.row0 + r;
+    const int x = it.lane0 + 4 * lane, left = a.NL - x;
+    const V* H = behind_wait(static_cast<const V*>(a.gate.H)) + row * a.gate.ldh + x;
+    float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f}, dg[4], du[4], c[4];
+    const bool live = it.e < a.E;
+    if (live && a.wide_h && left >= 4) {
+        const uint2 wg = load(reinterpret_cast<const uint2*>(H)), wu = load(reinterpret_cast<const uint2*>(H + a.NL));
+        const float2 g0 = unpack<V>(wg.x), g1 = unpack<V>(wg.y), u0 = unpack<V>(wu.x), u1 = unpack<V>(wu.y);
+        g[0] = g0.x, g[1] = g0.y, g[2] = g1.x, g[3] = g1.y, u[0] = u0.x, u[1] = u0.y, u[2] = u1.x, u[3] = u1.y;
+    } else if (live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) g[i] = to_f(load(H + i)), u[i] = to_f(load(H + a.NL + i));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gate_grad(a, live, f[i], g[i], u[i], dg[i], du[i], c[i]);
+    V* d = static_cast<V*>(a.gate.dH) + row * a.gate.lddh + x;
+    put_four(d, left, a.wide_h, dg);
+    put_four(d + a.NL, left, a.wide_h, du);
+    if (a.C) put_four(static_cast<V*>(a.C) + row * a.ldc + x, left, a.wide_c, c);
 }
 
 __device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, long long off, int x, int lane,
@@ -407,7 +708,7 @@ __device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, lon
 // SPLIT: a cluster of a.split CTAs shares each tile, every one the products of
 // its part of the reduction; the partial tiles meet in shared memory, where
 // CTA r adds the parts of its share of the rows in rank order.
-template <int MODE, int CG, bool I8, bool SPLIT, bool FUSE>
+template <int MODE, int CG, bool I8, bool SPLIT, bool FUSE, int EPI>
 __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tm_lane, const __grid_constant__ CUtensorMap tm_col,
                       const __grid_constant__ TcArgs a) {
@@ -597,7 +898,15 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                     } else if (rank == 0) {
                         mbar_expect_tx(full_bar(0) + s8, CG * a.stage_bytes);
                     }
-                    if (MODE == kNK) {
+                    if (EPI == kGate) {
+                        const int f0 = lane0 / 2;  // lane0 counts both factors
+                        if (a.by16) {
+                            load_5d(sl, &tm_lane, r, 0, 0, f0 / 16, z, bar, CG == 2);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) load_4d(sl + i * (kLaneBytes / 4), &tm_lane, r, f0 + 16 * i, 0, z, bar, CG == 2);
+                        }
+                    } else if (MODE == kNK) {
                         load_3d<CG>(sl, &tm_lane, r, lane0, z, bar);
                     } else if (MODE == kKN) {
                         load_3d<CG>(sl, &tm_lane, lane0, r, z, bar);
@@ -905,7 +1214,12 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                 for (int i = 0; i < 4; ++i)
                     f[i] = !I8 ? __uint_as_float(sum[i])
                                : it.e < a.E ? static_cast<float>(static_cast<int>(sum[i])) * (rs * cs[i]) : 0.f;
-                if (a.c_type == SPX_F32) store_four<float>(a, it.row0 + r, col, f);
+                if constexpr (EPI == kGate) gate_four(a, it, r, lane, f);
+                else if constexpr (EPI == kGateGrad) {
+                    if (a.h_type == SPX_BF16) gate_grad_four<__nv_bfloat16>(a, it, r, lane, f);
+                    else gate_grad_four<__half>(a, it, r, lane, f);
+                }
+                else if (a.c_type == SPX_F32) store_four<float>(a, it.row0 + r, col, f);
                 else if (a.c_type == SPX_BF16) store_four<__nv_bfloat16>(a, it.row0 + r, col, f);
                 else store_four<__half>(a, it.row0 + r, col, f);
             }
@@ -922,6 +1236,9 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                 continue;
             }
             if (!I8) {
+                Factors h;
+                if constexpr (EPI == kGateGrad)
+                    if (a.wide_h) fetch_factors(a, it, x, lane, 32 * (warp >> 2), h);
                 if (!acc_wait()) break;
                 const uint32_t src = tmem + buf * buf_cols + quarter;
                 bool held = true;
@@ -939,10 +1256,17 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                         acc_free();
                         held = false;
                     }
-                    float f[32];
+                    if constexpr (EPI == kGateGrad) {
+                        const bool more = c0 + 64 < it.rows;
+                        if (a.h_type == SPX_BF16) store_gate_grad<__nv_bfloat16>(a, it, x, lane, patch, c0, v, h, more);
+                        else store_gate_grad<__half>(a, it, x, lane, patch, c0, v, h, more);
+                    } else {
+                        float f[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-                    store_chunk(a, it, off, x, lane, patch, c0, f);
+                        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+                        if constexpr (EPI == kGate) store_gate(a, it, (it.lane0 + 128 * rank) / 2 + 16 * (warp & 3), lane, patch, c0, f);
+                        else store_chunk(a, it, off, x, lane, patch, c0, f);
+                    }
                 }
                 if (held) acc_free();
                 continue;
@@ -1058,6 +1382,21 @@ bool make_map3(CUtensorMap* m, const void* base, spx_type type, uint64_t inner, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The gate's weights, F rows of each factor: (K, 16 rows, factor, groups of 16 rows, matrix), or, where F is no multiple
+// of 16, (K, F rows, factor, matrix), whose groups end with the factor.  A box is 16 rows of each factor, or four such.
+bool make_gate_map(CUtensorMap* m, const void* base, spx_type type, uint64_t K, uint64_t F, uint64_t ld, uint64_t mats, uint64_t stride,
+                   bool by16) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[5] = {K, by16 ? 16 : F, 2, by16 ? F / 16 : mats, mats};
+    cuuint64_t strides[4] = {ld * 2, F * ld * 2, by16 ? 16 * ld * 2 : stride * 2, stride * 2};
+    cuuint32_t box[5] = {kDepth, 16, 2, by16 ? 4u : 1u, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(m, type == SPX_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, by16 ? 5 : 4,
+               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
     static std::mutex mu;
     static std::map<int, int> cache;
@@ -1089,8 +1428,8 @@ int resident_teams(const void* kernel, int team, const cudaLaunchConfig_t& cfg) 
 }
 
 // Takes the tile for a's sizes; returns the CTAs of a tile, 1 or 2.
-int take_tile(TcArgs& a, Kind kind) {
-    const Tile t = choose_tile(kind, a.E, a.S, a.NL, a.NC, a.NR, sm_count());
+int take_tile(TcArgs& a, Kind kind, int lanes) {
+    const Tile t = choose_tile(kind, a.E, a.S, lanes, a.NC, a.NR, sm_count());
     a.TN = t.tn;
     a.split = t.split;
     a.split_red = t.split_red;
@@ -1099,7 +1438,7 @@ int take_tile(TcArgs& a, Kind kind) {
 
 bool rows_aligned(const void* p, int64_t ld) { return spx_aligned(p, 16) && ld % 8 == 0; }
 
-template <int MODE, int CG, bool I8 = false, bool SPLIT = false, bool FUSE = false>
+template <int MODE, int CG, bool I8 = false, bool SPLIT = false, bool FUSE = false, int EPI = kNone>
 spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long long max_tiles, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return SPX_ERR_CUDA;
@@ -1122,7 +1461,7 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
         room = 0;
     }
     const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + room + list;
-    if (set_smem_limit(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
+    if (set_smem_limit(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE, EPI>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreadsOf<FUSE>);
     cfg.dynamicSmemBytes = smem;
@@ -1137,11 +1476,11 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     int groups = sms;
     if (team > 1) {
         cfg.gridDim = dim3(sms / team * team);
-        groups = resident_teams(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE>), team, cfg);
+        groups = resident_teams(reinterpret_cast<const void*>(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE, EPI>), team, cfg);
         if (groups <= 0) return SPX_ERR_CUDA;
     }
     spx_note_launches(1);
-    return spx_cuda_status(launch_early(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE>,
+    return spx_cuda_status(launch_early(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE, EPI>,
                                         dim3(static_cast<unsigned>(std::min<long long>(max_tiles, groups)) * team),
                                         kThreadsOf<FUSE>, smem, team, st, tl, tc, a));
 }
@@ -1180,7 +1519,7 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
     a.offsets = offsets, a.E = E, a.S = S, a.NL = N, a.NR = K;
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.same_w = E == 1 || stride_w == 0;
-    const int cg = take_tile(a, kProduct);
+    const int cg = take_tile(a, kProduct, N);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(type, nk ? kNK : kKN, cg);
     CUtensorMap tl, tc;
@@ -1198,6 +1537,58 @@ spx_status tc_product(int E, int S, int N, int K, const int* offsets, const void
     return nk ? launch<kNK, 1>(tl, tc, a, tiles, st) : launch<kKN, 1>(tl, tc, a, tiles, st);
 }
 
+spx_status tc_gated(int E, int S, int F, int K, const int* offsets, const void* A, int64_t lda, const void* W, int64_t ldw, int64_t stride_w,
+                    const Gate& gate, spx_type type, void* C, int64_t ldc, spx_type c_type, cudaStream_t st) {
+    TcArgs a{};
+    a.offsets = offsets, a.E = E, a.S = S, a.NL = F, a.NR = K;
+    a.C = C, a.ldc = ldc, a.c_type = c_type;
+    a.gate = gate, a.h_type = type;
+    a.wide_h = gate.H && rows_aligned(gate.H, gate.ldh) && F % 8 == 0;
+    a.by16 = F % 16 == 0;
+    a.same_w = E == 1 || stride_w == 0;
+    const int cg = take_tile(a, kProduct, 2 * F);
+    a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
+    a.idesc = idesc_of(type, kNK, cg);
+    CUtensorMap tl, tc;
+    const uint64_t mats = a.same_w ? 1 : E, sw = a.same_w ? 2 * static_cast<uint64_t>(ldw) * F : stride_w;
+    if (!make_gate_map(&tl, W, type, K, F, ldw, mats, sw, a.by16) || !make_map3(&tc, A, type, K, S, lda, 0, 0, a.TN / cg)) return SPX_ERR_CUDA;
+    const long long nlt = (F + 64 * cg - 1) / (64 * cg), tiles = max_row_tiles(E, S, a.TN) * nlt;
+    if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;
+    a.max_tiles = static_cast<int>(tiles);
+    a.by_lane = Divisor(static_cast<uint32_t>(nlt));
+    a.by_group = Divisor(static_cast<uint32_t>(kBand * nlt));
+    if (a.split > 1) return launch<kNK, 1, false, true, false, kGate>(tl, tc, a, tiles, st);
+    return cg == 2 ? launch<kNK, 2, false, false, false, kGate>(tl, tc, a, tiles, st) : launch<kNK, 1, false, false, false, kGate>(tl, tc, a, tiles, st);
+}
+
+spx_status tc_gated_grad(int E, int S, int F, int N, const int* offsets, const void* dY, int64_t lddy, const void* W, int64_t ldw,
+                         int64_t stride_w, spx_w_layout layout, const Gate& gate, spx_type type, void* C, int64_t ldc, cudaStream_t st) {
+    const bool nk = layout == SPX_W_NK;
+    TcArgs a{};
+    a.offsets = offsets, a.E = E, a.S = S, a.NL = F, a.NR = N;
+    a.C = C, a.ldc = ldc, a.c_type = type;
+    a.gate = gate, a.h_type = type;
+    a.wide_h = rows_aligned(gate.H, gate.ldh) && rows_aligned(gate.dH, gate.lddh) && F % 8 == 0 && (!C || rows_aligned(C, ldc));
+    a.same_w = E == 1 || stride_w == 0;
+    const int cg = take_tile(a, kProduct, F);
+    a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
+    a.idesc = idesc_of(type, nk ? kNK : kKN, cg);
+    CUtensorMap tl, tc;
+    const uint64_t mats = a.same_w ? 1 : E, sw = a.same_w ? static_cast<uint64_t>(ldw) * (nk ? F : N) : stride_w;
+    const bool ok = nk ? make_map3(&tl, W, type, N, F, ldw, mats, sw, 128) : make_map3(&tl, W, type, F, N, ldw, mats, sw, 64);
+    if (!ok || !make_map3(&tc, dY, type, N, S, lddy, 0, 0, a.TN / cg)) return SPX_ERR_CUDA;
+    const long long nlt = (F + 128 * cg - 1) / (128 * cg), tiles = max_row_tiles(E, S, a.TN) * nlt;
+    if (tiles > kI32Max - 4096) return SPX_ERR_INDEX_RANGE;
+    a.max_tiles = static_cast<int>(tiles);
+    a.by_lane = Divisor(static_cast<uint32_t>(nlt));
+    a.by_group = Divisor(static_cast<uint32_t>(kBand * nlt));
+    if (a.split > 1)
+        return nk ? launch<kNK, 1, false, true, false, kGateGrad>(tl, tc, a, tiles, st) : launch<kKN, 1, false, true, false, kGateGrad>(tl, tc, a, tiles, st);
+    if (cg == 2)
+        return nk ? launch<kNK, 2, false, false, false, kGateGrad>(tl, tc, a, tiles, st) : launch<kKN, 2, false, false, false, kGateGrad>(tl, tc, a, tiles, st);
+    return nk ? launch<kNK, 1, false, false, false, kGateGrad>(tl, tc, a, tiles, st) : launch<kKN, 1, false, false, false, kGateGrad>(tl, tc, a, tiles, st);
+}
+
 // The 8-bit product on codes held as fp16: Q is S x K (lda), W is mats x N x K
 // (ldw rows, N * ldw apart), both 16-byte aligned.
 spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const void* Q, int64_t ldq,
@@ -1208,7 +1599,7 @@ spx_status tc_product_i8(int E, int S, int N, int K, const int* offsets, const v
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.row_scale = row_scale, a.col_scale = col_scale;
     a.same_w = mats == 1;
-    const int cg = take_tile(a, kProduct);
+    const int cg = take_tile(a, kProduct, N);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(SPX_F16, kNK, cg);
     CUtensorMap tl, tc;
@@ -1235,7 +1626,7 @@ spx_status tc_product_codes(int E, int S, int N, int K, const int* offsets, cons
     a.C = C, a.ldc = ldc, a.c_type = c_type;
     a.row_scale = row_scale, a.col_scale = col_scale;
     a.same_w = E == 1 || stride_w == 0;
-    take_tile(a, kCodes);
+    take_tile(a, kCodes, N);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN) * kDepth * 2;
     a.raw_bytes = static_cast<uint32_t>(128 + a.TN) * kRawDepth;
     a.idesc = idesc_of(SPX_F16, kNK, 1);
@@ -1261,7 +1652,7 @@ spx_status tc_wgrad(int E, int S, int N, int K, const int* offsets, const void* 
     TcArgs a{};
     a.offsets = offsets, a.E = E, a.S = S, a.NL = K, a.NC = N;
     a.C = dW, a.ldc = ldw, a.ce = stride_w, a.c_type = w_type;
-    const int cg = take_tile(a, kGradient);
+    const int cg = take_tile(a, kGradient, K);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(type, kWG, cg);
     CUtensorMap tl, tc;

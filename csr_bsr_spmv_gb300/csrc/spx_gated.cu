@@ -34,13 +34,16 @@ spx_status spx_gemm_grouped_gated(int32_t E, int32_t S, int32_t F, int32_t K, co
         !spx_aligned(C, type_bytes(c_type)))
         return SPX_ERR_ALIGN;
     Gate gate;
-    gate.epi = kGate, gate.act = act, gate.F = F, gate.H = H, gate.ldh = ldh;
+    gate.epi = kGate, gate.act = act, gate.H = H, gate.ldh = ldh;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (K > 0 && tc_product_fits(A, lda, W, ldw, stride_w, E))
+        return tc_gated(E, S, F, K, offsets, A, lda, W, ldw, stride_w, gate, type, C, ldc, c_type, st);
     SimtGemm g{};
     g.L = A, g.li = lda, g.lr = 1;
     g.R = W, g.rj = ldw, g.rr = 1, g.re = stride_w;
     g.C = C, g.ldc = ldc;
     g.offsets = offsets, g.E = E, g.S = S, g.NI = S, g.NJ = F, g.NR = K, g.by_rows = true;
-    return simt_gated(g, gate, type, c_type, reinterpret_cast<cudaStream_t>(stream));
+    return simt_gated(g, gate, type, c_type, st);
 }
 
 spx_status spx_gemm_grouped_gated_grad(int32_t E, int32_t S, int32_t F, int32_t N, const int32_t* offsets, const void* dY,
@@ -60,13 +63,16 @@ spx_status spx_gemm_grouped_gated_grad(int32_t E, int32_t S, int32_t F, int32_t 
         !spx_aligned(C, 2))
         return SPX_ERR_ALIGN;
     Gate gate;
-    gate.epi = kGateGrad, gate.act = act, gate.F = F, gate.H = const_cast<void*>(H), gate.ldh = ldh, gate.dH = dH, gate.lddh = lddh;
+    gate.epi = kGateGrad, gate.act = act, gate.H = const_cast<void*>(H), gate.ldh = ldh, gate.dH = dH, gate.lddh = lddh;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (N > 0 && tc_product_fits(dY, lddy, W, ldw, stride_w, E))
+        return tc_gated_grad(E, S, F, N, offsets, dY, lddy, W, ldw, stride_w, layout, gate, type, C, ldc, st);
     SimtGemm g{};
     g.L = dY, g.li = lddy, g.lr = 1;
     g.R = W, g.rj = kn ? 1 : ldw, g.rr = kn ? ldw : 1, g.re = stride_w;
     g.C = C, g.ldc = ldc;
     g.offsets = offsets, g.E = E, g.S = S, g.NI = S, g.NJ = F, g.NR = N, g.by_rows = true;
-    return simt_gated(g, gate, type, type, reinterpret_cast<cudaStream_t>(stream));
+    return simt_gated(g, gate, type, type, st);
 }
 
 }  // extern "C"
