@@ -1,5 +1,5 @@
 // spx_act.cuh -- the activations of the experts' gate and their derivatives, in
-// fp32 with CUDA's own functions.
+// fp32.
 #pragma once
 
 #include "spx_experts.cuh"
@@ -23,30 +23,56 @@ struct Gate {
 // act(x) and act'(x).  All three are x p(x) with p in [0, 1], which keeps the
 // small values far left of zero; the tanh form's p is the logistic function of
 // z = 2 sqrt(2 / pi) (x + 0.044715 x^3), since (1 + tanh(z / 2)) / 2 is that.
-// Beyond |x| = 100 p is 0 or 1 and the slope's other term 0 in fp32, so x is cut
-// there (and far below in x p) where an infinity would meet that zero.  NaN
-// passes through p.
+// NaN passes; infinities give the limits: x is cut far out, where p is 0 or 1
+// and the slope's other term 0 in fp32, before either could meet an infinity.
+__device__ __forceinline__ float at_least(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float at_most(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+// 1 / (1 + exp(-z)), z within +-88, where the exponential is finite, from the
+// hardware's 2^t and 1 / y (off by two and one units in the last place): the
+// rounding of t = z log2(e) is put back to first order, 2^(t + d) = 2^t (1 + d
+// ln 2).  Off by less than 2^-21 of itself, and 0 below 1e-38.
+__device__ __forceinline__ float logistic(float z) {
+    constexpr float L = 1.44269502f, rest = 1.92596303e-8f;  // log2(e) = L + rest
+    const float t = -z * L, d = fmaf(-z, rest, fmaf(-z, L, -t));
+    float e, p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = fmaf(e, d * 0.693147181f, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + e));
+    return p;
+}
+
+constexpr float kTanh1 = 1.5957691216f, kTanh3 = 0.07135481628f;  // 2 sqrt(2 / pi), and that times 0.044715
+
 __device__ __forceinline__ float act_of(int kind, float x) {
-    const float cut = fmaxf(x, -1e30f);
+    const float cut = at_least(x, -100.f);
     if (kind == SPX_ACT_GELU) return cut * normcdff(x);
-    float z = x;
-    if (kind == SPX_ACT_GELU_TANH) z = x * fmaf(0.07135481628f, fminf(x * x, 1e4f), 1.5957691216f);
-    return cut / (1.f + expf(-z));
+    float z = cut;
+    if (kind == SPX_ACT_GELU_TANH) z = cut * fmaf(kTanh3, fminf(x * x, 1e4f), kTanh1);
+    return cut * logistic(at_most(at_least(z, -88.f), 88.f));
 }
 __device__ __forceinline__ float act_of(int kind, float x, float& slope) {
-    const float cut = fmaxf(x, -1e30f), near = fminf(fmaxf(x, -100.f), 100.f);
+    const float cut = at_least(x, -100.f), near = at_most(cut, 100.f);
     if (kind == SPX_ACT_GELU) {
         const float p = normcdff(x);
         slope = fmaf(near * 0.3989422804f, expf(-0.5f * x * x), p);
         return cut * p;
     }
-    float z = x, dz = 1.f;
+    float z = near, dz = 1.f;
     if (kind == SPX_ACT_GELU_TANH) {
-        const float xx = fminf(x * x, 1e4f);
-        z = x * fmaf(0.07135481628f, xx, 1.5957691216f);
-        dz = fmaf(3.f * 0.07135481628f, xx, 1.5957691216f);
+        const float xx = near * near;
+        z = near * fmaf(kTanh3, xx, kTanh1);
+        dz = fmaf(3.f * kTanh3, xx, kTanh1);
     }
-    const float p = 1.f / (1.f + expf(-z));
+    const float p = logistic(at_most(at_least(z, -88.f), 88.f));
     slope = p * fmaf(near * dz, 1.f - p, 1.f);
     return cut * p;
 }
