@@ -2,6 +2,8 @@
 // fp32.
 #pragma once
 
+#include <type_traits>
+
 #include "spx_experts.cuh"
 
 namespace spx_exp {
@@ -52,14 +54,16 @@ __device__ __forceinline__ float logistic(float z) {
 
 constexpr float kTanh1 = 1.5957691216f, kTanh3 = 0.07135481628f;  // 2 sqrt(2 / pi), and that times 0.044715
 
-__device__ __forceinline__ float act_of(int kind, float x) {
+template <int kind>
+__device__ __forceinline__ float act_of(float x) {
     const float cut = at_least(x, -100.f);
     if (kind == SPX_ACT_GELU) return cut * normcdff(x);
     float z = cut;
     if (kind == SPX_ACT_GELU_TANH) z = cut * fmaf(kTanh3, fminf(x * x, 1e4f), kTanh1);
     return cut * logistic(at_most(at_least(z, -88.f), 88.f));
 }
-__device__ __forceinline__ float act_of(int kind, float x, float& slope) {
+template <int kind>
+__device__ __forceinline__ float act_of(float x, float& slope) {
     const float cut = at_least(x, -100.f), near = at_most(cut, 100.f);
     if (kind == SPX_ACT_GELU) {
         const float p = normcdff(x);
@@ -75,6 +79,15 @@ __device__ __forceinline__ float act_of(int kind, float x, float& slope) {
     const float p = logistic(at_most(at_least(z, -88.f), 88.f));
     slope = p * fmaf(near * dz, 1.f - p, 1.f);
     return cut * p;
+}
+
+// f with the activation as a constant (a lambda over std::integral_constant): a chunk of values then runs one straight
+// piece of code.
+template <class F>
+__device__ __forceinline__ void with_act(int kind, F f) {
+    if (kind == SPX_ACT_SILU) f(std::integral_constant<int, SPX_ACT_SILU>{});
+    else if (kind == SPX_ACT_GELU) f(std::integral_constant<int, SPX_ACT_GELU>{});
+    else f(std::integral_constant<int, SPX_ACT_GELU_TANH>{});
 }
 
 }  // namespace spx_exp

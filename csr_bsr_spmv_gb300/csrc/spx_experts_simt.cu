@@ -89,40 +89,45 @@ __global__ void __launch_bounds__(kThreads) experts_simt_kernel(SimtGemm g, Gate
         __syncthreads();
     }
     O* Ce = C + (g.by_rows ? 0 : e * g.ce);
+    auto put = [&](auto kind) {
+        constexpr int ACT = decltype(kind)::value;
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        const int i = i0 + ty + 16 * a;
-        if (i >= i1) continue;
+        for (int a = 0; a < 4; ++a) {
+            const int i = i0 + ty + 16 * a;
+            if (i >= i1) continue;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int j = tx + 16 * b;
-            if (j >= nj) continue;
-            O* c = Ce + i * g.ldc + j0 + j;
-            if constexpr (EPI == kNone) {
-                *c = from_f<O>(acc[a][b]);
-            } else if constexpr (EPI == kGate) {
-                *c = from_f<O>(e < g.E ? act_of(gate.act, acc[a][b]) * up[a][b] : 0.f);
-                if (gate.H) {
-                    V* h = static_cast<V*>(gate.H) + i * gate.ldh + j0 + j;
-                    h[0] = from_f<V>(acc[a][b]);
-                    h[g.NJ] = from_f<V>(up[a][b]);
+            for (int b = 0; b < 4; ++b) {
+                const int j = tx + 16 * b;
+                if (j >= nj) continue;
+                O* c = Ce + i * g.ldc + j0 + j;
+                if constexpr (EPI == kNone) {
+                    *c = from_f<O>(acc[a][b]);
+                } else if constexpr (EPI == kGate) {
+                    *c = from_f<O>(e < g.E ? act_of<ACT>(acc[a][b]) * up[a][b] : 0.f);
+                    if (gate.H) {
+                        V* h = static_cast<V*>(gate.H) + i * gate.ldh + j0 + j;
+                        h[0] = from_f<V>(acc[a][b]);
+                        h[g.NJ] = from_f<V>(up[a][b]);
+                    }
+                } else {
+                    const V* h = behind_wait(static_cast<const V*>(gate.H)) + i * gate.ldh + j0 + j;
+                    float dg = 0.f, du = 0.f, out = 0.f;
+                    if (e < g.E) {  // rows past the last expert's are zeros, whatever H holds there
+                        const float u = to_f(load(h + g.NJ));
+                        float slope;
+                        const float act = act_of<ACT>(to_f(load(h)), slope);
+                        dg = acc[a][b] * u * slope, du = acc[a][b] * act, out = act * u;
+                    }
+                    V* d = static_cast<V*>(gate.dH) + i * gate.lddh + j0 + j;
+                    d[0] = from_f<V>(dg);
+                    d[g.NJ] = from_f<V>(du);
+                    if (g.C) *c = from_f<O>(out);
                 }
-            } else {
-                const V* h = behind_wait(static_cast<const V*>(gate.H)) + i * gate.ldh + j0 + j;
-                float dg = 0.f, du = 0.f, out = 0.f;
-                if (e < g.E) {  // rows past the last expert's are zeros, whatever H holds there
-                    const float u = to_f(load(h + g.NJ));
-                    float slope;
-                    const float act = act_of(gate.act, to_f(load(h)), slope);
-                    dg = acc[a][b] * u * slope, du = acc[a][b] * act, out = act * u;
-                }
-                V* d = static_cast<V*>(gate.dH) + i * gate.lddh + j0 + j;
-                d[0] = from_f<V>(dg);
-                d[g.NJ] = from_f<V>(du);
-                if (g.C) *c = from_f<O>(out);
             }
         }
-    }
+    };
+    if constexpr (EPI == kNone) put(std::integral_constant<int, 0>{});
+    else with_act(gate.act, put);
 }
 
 template <class V, int EPI>

@@ -51,11 +51,13 @@ enum Mode : int { kNK = 0, kKN = 1, kWG = 2 };
 
 // Warps: 8 that store (two for each quarter of the lanes, taking turns at the
 // tile's rows), one for the lane factor's copies, one for the MMAs, one for
-// the column factor's copies.
-constexpr int kStoreWarps = 8;
+// the column factor's copies.  The gate's gradient, which reads two values and
+// writes three for every sum, takes 16 storing warps to hide their latency.
 constexpr int kWidenWarps = 8;  // FUSE
-template <bool FUSE>
-constexpr int kThreadsOf = 32 * (kStoreWarps + 3 + (FUSE ? kWidenWarps : 0));
+template <bool SPLIT, int EPI>
+constexpr int kStoreWarpsOf = EPI == kGateGrad && !SPLIT ? 16 : 8;
+template <bool SPLIT, bool FUSE, int EPI>
+constexpr int kThreadsOf = 32 * (kStoreWarpsOf<SPLIT, EPI> + 3 + (FUSE ? kWidenWarps : 0));
 constexpr uint32_t kLaneBytes = 128 * kDepth * 2;  // a stage's lane factor: 128 lanes a CTA, 16 KB
 constexpr uint32_t kBox = 64 * kDepth * 2;      // an MN-major box: 64 long, 64 deep, 8 KB
 constexpr int kMaxStages = 12;
@@ -421,12 +423,6 @@ __device__ __forceinline__ void patch_in(uint32_t patch, int lane, int hg, uint3
                  "r"(q0), "r"(q1), "r"(q2), "r"(q3)
                  : "memory");
 }
-__device__ __forceinline__ void patch_out(uint32_t patch, int lane, int hg, uint32_t (&q)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-                 : "r"(patch + lane * kPatchPitch + 16 * hg)
-                 : "memory");
-}
 __device__ __forceinline__ uint4 patch_row(uint32_t patch, int r, int p) {
     uint4 w;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -470,8 +466,10 @@ __device__ __forceinline__ void store_gated(const TcArgs& a, const Item& it, int
     const int rows = it.rows - c0, cols = a.NL - x;
     O* C = static_cast<O*>(a.C) + (it.row0 + c0) * a.ldc + x;
     float f[16];
+    with_act(a.gate.act, [&](auto kind) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = act_of(a.gate.act, v[i]) * v[16 + i];
+        for (int i = 0; i < 16; ++i) f[i] = act_of<decltype(kind)::value>(v[i]) * v[16 + i];
+    });
     if constexpr (sizeof(O) == 2) {
         if (a.wide_c) {
 #pragma unroll
@@ -507,57 +505,61 @@ __device__ __forceinline__ void store_gate(const TcArgs& a, const Item& it, int 
     else store_gated<__half>(a, it, x, lane, patch, c0, v);
 }
 
-// Gradient (kGateGrad): the sums are dC; both factors come from H, dH and C go out.  On wide rows H's 32 rows x 32
-// columns are fetched in whole pieces ahead of the sums and reach the fragments' order through the warp's patch.
-struct Factors {
-    uint4 g[4], u[4];  // thread (r = lane / 4, p = lane % 4): rows r + 8 i, columns 8 p to 8 p + 7
-};
+// Gradient (kGateGrad): the sums are dC; both factors come from H, dH and C go
+// out.  A warp takes 16 rows of its 32 columns at a time.  On wide rows both
+// factors are copied ahead of the sums into the warp's two patches of shared
+// memory, reach the fragments' order by ldmatrix, and what goes out takes the
+// same way back.
+constexpr uint32_t kFactorBytes = 16 * kPatchPitch;
 
-__device__ __forceinline__ void fetch_factors(const TcArgs& a, const Item& it, int x, int lane, int c0, Factors& h) {
+__device__ __forceinline__ void fetch_factors(const TcArgs& a, const Item& it, int x, int lane, uint32_t patch, int c0) {
     const int r = lane >> 2, p = lane & 3;
-    const uint16_t* H = behind_wait(static_cast<const uint16_t*>(a.gate.H)) + (it.row0 + c0 + r) * a.gate.ldh + x + 8 * p;
-    const bool on = it.e < a.E && 8 * p < a.NL - x;
+    const uint16_t* H = behind_wait(static_cast<const uint16_t*>(a.gate.H));
 #pragma unroll
-    for (int i = 0; i < 4; ++i, H += 8 * a.gate.ldh) {
-        h.g[i] = h.u[i] = make_uint4(0, 0, 0, 0);
-        if (on && r + 8 * i < it.rows - c0) {
-            h.g[i] = load_once(reinterpret_cast<const uint4*>(H));
-            h.u[i] = load_once(reinterpret_cast<const uint4*>(H + a.NL));
-        }
+    for (int i = 0; i < 2; ++i) {
+        const bool on = it.e < a.E && 8 * p < a.NL - x && r + 8 * i < it.rows - c0;
+        const uint16_t* q = on ? H + (it.row0 + c0 + r + 8 * i) * a.gate.ldh + x + 8 * p : H;
+        const uint32_t to = patch + (r + 8 * i) * kPatchPitch + 16 * p, bytes = on ? 16 : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(q), "r"(bytes) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + kFactorBytes), "l"(q + (on ? a.NL : 0)), "r"(bytes) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// 16 rows of a warp's 32 lanes: thread t's v[8 h + 4 q + i] is lane 16 h + t / 4 + 8 (i / 2), row 8 q + 2 (t % 4) + i % 2.
+__device__ __forceinline__ void load_frag16(uint32_t taddr, uint32_t (&v)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t* r = v + 8 * h;
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16)));
     }
 }
 
-// A thread's pieces of a 32 x 32 block to fragments: q[4 hg + j] holds rows 8 j + 2 (lane % 4) and the next of column
-// 8 hg + lane / 4; and back.
-__device__ __forceinline__ void to_fragments(uint32_t patch, int lane, const uint4 (&w)[4], uint32_t (&q)[16]) {
-    const int r = lane >> 2, p = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + (r + 8 * i) * kPatchPitch + 16 * p), "r"(w[i].x), "r"(w[i].y),
-                     "r"(w[i].z), "r"(w[i].w)
-                     : "memory");
-    __syncwarp();
-#pragma unroll
-    for (int hg = 0; hg < 4; ++hg) {
-        uint32_t t[4];
-        patch_out(patch, lane, hg, t);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[4 * hg + j] = t[j];
-    }
-    __syncwarp();
+// Columns 16 h to 16 h + 15 of a patch's 16 rows as fragments, and back: q[m] holds rows 8 (m % 2) + 2 (t % 4) and the
+// next of column 16 h + 8 (m / 2) + t / 4.
+__device__ __forceinline__ uint32_t frag_addr(uint32_t patch, int lane, int h) {
+    return patch + ((lane >> 3 & 1) * 8 + (lane & 7)) * kPatchPitch + 32 * h + 16 * (lane >> 4);
 }
-__device__ __forceinline__ void store_fragments(uint32_t patch, int lane, const uint32_t (&q)[16], uint16_t* out, long long ld, int rows, int cols) {
-#pragma unroll
-    for (int hg = 0; hg < 4; ++hg) patch_in(patch, lane, hg, q[4 * hg], q[4 * hg + 1], q[4 * hg + 2], q[4 * hg + 3]);
-    __syncwarp();
+__device__ __forceinline__ void frag_out(uint32_t at, uint32_t (&q)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void frag_in(uint32_t at, const uint32_t (&q)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3])
+                 : "memory");
+}
+// A patch's 16 rows of 32 columns to memory.
+__device__ __forceinline__ void patch_rows(uint32_t patch, int lane, uint16_t* out, long long ld, int rows, int cols) {
     const int r = lane >> 2, p = lane & 3;
-    out += r * ld + 8 * p;
 #pragma unroll
-    for (int i = 0; i < 4; ++i, out += 8 * ld) {
+    for (int i = 0; i < 2; ++i) {
         const uint4 w = patch_row(patch, r + 8 * i, p);
-        if (r + 8 * i < rows && 8 * p < cols) *reinterpret_cast<uint4*>(out) = w;
+        if (r + 8 * i < rows && 8 * p < cols) *reinterpret_cast<uint4*>(out + (r + 8 * i) * ld + 8 * p) = w;
     }
-    __syncwarp();
 }
 
 template <class V>
@@ -568,53 +570,65 @@ __device__ __forceinline__ float2 unpack(uint32_t w) {
 }
 
 // dG, dU and C of one output; all zeros in the rows past the last expert's, whatever H holds there.
-__device__ __forceinline__ void gate_grad(const TcArgs& a, bool live, float dc, float g, float u, float& dg, float& du, float& c) {
+template <int ACT>
+__device__ __forceinline__ void gate_grad(bool live, float dc, float g, float u, float& dg, float& du, float& c) {
     float slope;
-    const float act = act_of(a.gate.act, g, slope);
+    const float act = act_of<ACT>(g, slope);
     dg = live ? dc * u * slope : 0.f;
     du = live ? dc * act : 0.f;
     c = live ? act * u : 0.f;
 }
 
-template <class V>
+template <class V, int ACT>
 __device__ __forceinline__ void store_gate_grad(const TcArgs& a, const Item& it, int x, int lane, uint32_t patch, int c0,
-                                                const uint32_t (&v)[32], Factors& h, bool more) {
+                                                const uint32_t (&v)[16]) {
     const int rows = it.rows - c0, cols = a.NL - x;
     const bool live = it.e < a.E;
     const long long row = it.row0 + c0;
     V* dH = static_cast<V*>(a.gate.dH) + row * a.gate.lddh + x;
     V* C = static_cast<V*>(a.C) + row * a.ldc + x;
     if (a.wide_h) {
-        uint32_t g[16], u[16];
-        to_fragments(patch, lane, h.g, g);
-        to_fragments(patch, lane, h.u, u);
-        if (more) fetch_factors(a, it, x, lane, c0 + 64, h);
-        uint32_t dg[16], du[16], c[16];
+        uint32_t c[2][4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int i = 16 * (j >> 3) + 2 * (j >> 2 & 1) + 4 * (j & 3);  // v's index of this pair
-            const float2 fg = unpack<V>(g[j]), fu = unpack<V>(u[j]);
-            float2 a0, a1, a2;
-            gate_grad(a, live, __uint_as_float(v[i]), fg.x, fu.x, a0.x, a1.x, a2.x);
-            gate_grad(a, live, __uint_as_float(v[i + 1]), fg.y, fu.y, a0.y, a1.y, a2.y);
-            dg[j] = pack<V>(a0.x, a0.y), du[j] = pack<V>(a1.x, a1.y), c[j] = pack<V>(a2.x, a2.y);
+        for (int h = 0; h < 2; ++h) {
+            uint32_t g[4], u[4];
+            const uint32_t at = frag_addr(patch, lane, h);
+            frag_out(at, g);
+            frag_out(at + kFactorBytes, u);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int i = 8 * h + 4 * (m & 1) + 2 * (m >> 1);
+                const float2 fg = unpack<V>(g[m]), fu = unpack<V>(u[m]);
+                float2 a0, a1, a2;
+                gate_grad<ACT>(live, __uint_as_float(v[i]), fg.x, fu.x, a0.x, a1.x, a2.x);
+                gate_grad<ACT>(live, __uint_as_float(v[i + 1]), fg.y, fu.y, a0.y, a1.y, a2.y);
+                g[m] = pack<V>(a0.x, a0.y), u[m] = pack<V>(a1.x, a1.y), c[h][m] = pack<V>(a2.x, a2.y);
+            }
+            __syncwarp();
+            frag_in(at, g);
+            frag_in(at + kFactorBytes, u);
         }
-        store_fragments(patch, lane, dg, reinterpret_cast<uint16_t*>(dH), a.gate.lddh, rows, cols);
-        store_fragments(patch, lane, du, reinterpret_cast<uint16_t*>(dH + a.NL), a.gate.lddh, rows, cols);
-        if (a.C) store_fragments(patch, lane, c, reinterpret_cast<uint16_t*>(C), a.ldc, rows, cols);
+        __syncwarp();
+        patch_rows(patch, lane, reinterpret_cast<uint16_t*>(dH), a.gate.lddh, rows, cols);
+        patch_rows(patch + kFactorBytes, lane, reinterpret_cast<uint16_t*>(dH + a.NL), a.gate.lddh, rows, cols);
+        __syncwarp();
+        if (a.C) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) frag_in(frag_addr(patch, lane, h), c[h]);
+            __syncwarp();
+            patch_rows(patch, lane, reinterpret_cast<uint16_t*>(C), a.ldc, rows, cols);
+            __syncwarp();
+        }
         return;
     }
     const V* H = behind_wait(static_cast<const V*>(a.gate.H)) + row * a.gate.ldh + x;
-#pragma unroll 4
-    for (int i = 0; i < 32; ++i) {
-        const int n = 16 * (i >> 4) + (lane >> 2) + 8 * ((i >> 1) & 1), r = 8 * ((i >> 2) & 3) + 2 * (lane & 3) + (i & 1);
-        if (n >= cols || r >= rows) continue;
-        float dc = 0.f, dg, du, c;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j == i) dc = __uint_as_float(v[j]);
+    for (int i = 0; i < 16; ++i) {
+        const int n = 16 * (i >> 3) + (lane >> 2) + 8 * ((i >> 1) & 1), r = 8 * ((i >> 2) & 1) + 2 * (lane & 3) + (i & 1);
+        if (n >= cols || r >= rows) continue;
+        float dg, du, c;
         const V* p = H + r * a.gate.ldh + n;
-        gate_grad(a, live, dc, to_f(load(p)), to_f(load(p + a.NL)), dg, du, c);
+        gate_grad<ACT>(live, __uint_as_float(v[i]), to_f(load(p)), to_f(load(p + a.NL)), dg, du, c);
         V* d = dH + r * a.gate.lddh + n;
         d[0] = from_f<V>(dg);
         d[a.NL] = from_f<V>(du);
@@ -651,12 +665,13 @@ __device__ __forceinline__ void gate_four(const TcArgs& a, const Item& it, int r
     const long long row = it.row0 + r;
     const int x = it.lane0 / 2 + 16 * (lane >> 3) + 4 * (lane & 3);
     const bool up = lane & 4;
-    float c[4];
+    float c[4], u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float u = __shfl_xor_sync(0xffffffffu, f[i], 4);
-        c[i] = up ? 0.f : act_of(a.gate.act, f[i]) * u;
-    }
+    for (int i = 0; i < 4; ++i) u[i] = __shfl_xor_sync(0xffffffffu, f[i], 4);
+    with_act(a.gate.act, [&](auto kind) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = act_of<decltype(kind)::value>(f[i]) * u[i];
+    });
     if (a.gate.H) {
         const long long at = row * a.gate.ldh + x + (up ? a.NL : 0);
         if (a.h_type == SPX_BF16) put_four(static_cast<__nv_bfloat16*>(a.gate.H) + at, a.NL - x, a.wide_h, f);
@@ -684,8 +699,10 @@ __device__ __forceinline__ void gate_grad_four(const TcArgs& a, const Item& it, 
         for (int i = 0; i < 4; ++i)
             if (i < left) g[i] = to_f(load(H + i)), u[i] = to_f(load(H + a.NL + i));
     }
+    with_act(a.gate.act, [&](auto kind) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) gate_grad(a, live, f[i], g[i], u[i], dg[i], du[i], c[i]);
+        for (int i = 0; i < 4; ++i) gate_grad<decltype(kind)::value>(live, f[i], g[i], u[i], dg[i], du[i], c[i]);
+    });
     V* d = static_cast<V*>(a.gate.dH) + row * a.gate.lddh + x;
     put_four(d, left, a.wide_h, dg);
     put_four(d + a.NL, left, a.wide_h, du);
@@ -709,7 +726,7 @@ __device__ __forceinline__ void store_chunk(const TcArgs& a, const Item& it, lon
 // its part of the reduction; the partial tiles meet in shared memory, where
 // CTA r adds the parts of its share of the rows in rank order.
 template <int MODE, int CG, bool I8, bool SPLIT, bool FUSE, int EPI>
-__global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
+__global__ void __launch_bounds__(kThreadsOf<SPLIT, FUSE, EPI>, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tm_lane, const __grid_constant__ CUtensorMap tm_col,
                       const __grid_constant__ TcArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -736,15 +753,17 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
     auto raw_full = [&](uint32_t s) { return bars + 8u * (4 * kMaxStages + 7 + s); };
     auto raw_empty = [&](uint32_t s) { return bars + 8u * (5 * kMaxStages + 7 + s); };
     const uint32_t NS = a.stages, NR = a.raw_stages;
+    constexpr int SW = kStoreWarpsOf<SPLIT, EPI>;
+    constexpr uint32_t PATCH = EPI == kGateGrad ? 2 * kFactorBytes : kPatchBytes;  // a storing warp's
     // the storing warps' patches, then the tile list, behind the ring
     List list;
     const uint32_t raw0 = base + NS * a.stage_bytes;  // FUSE: the raw ring
     const uint32_t behind = raw0 + (FUSE ? NR * a.raw_bytes : 0);
-    list.lo = reinterpret_cast<int*>(smem_raw + (behind - smem_u32(smem_raw)) + (SPLIT ? 0 : kStoreWarps * kPatchBytes));
+    list.lo = reinterpret_cast<int*>(smem_raw + (behind - smem_u32(smem_raw)) + (SPLIT ? 0 : SW * PATCH));
     list.hi = list.lo + a.E + 1;
     list.first = list.hi + a.E + 1;
 
-    constexpr int SW = kStoreWarps, LOAD = SW, MMA = SW + 1, LOAD2 = SW + 2;  // the roles' warps
+    constexpr int LOAD = SW, MMA = SW + 1, LOAD2 = SW + 2;  // the roles' warps
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     int rank = 0, part = 0;  // place in the pair, share of the reduction
     if (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -781,8 +800,8 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
         }
         mbar_init(fin_bar, 1);
         if (SPLIT) {
-            mbar_init(ready_bar, kStoreWarps * a.split);
-            mbar_init(done_bar, kStoreWarps * a.split);
+            mbar_init(ready_bar, SW * a.split);
+            mbar_init(done_bar, SW * a.split);
         }
         if (FUSE)
             for (uint32_t s = 0; s < NR; ++s) {
@@ -816,7 +835,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
     // prefill product against 215.)
     wait_for_previous();
     int ntiles = a.max_tiles;  // kWG: every expert's tiles, rows or not
-    for (int e = threadIdx.x; e <= a.E; e += kThreadsOf<FUSE>) {
+    for (int e = threadIdx.x; e <= a.E; e += kThreadsOf<SPLIT, FUSE, EPI>) {
         int lo = 0, hi = a.S;
         if (a.offsets) {
             if (e < a.E) expert_rows(a.offsets, e, a.S, lo, hi);
@@ -1127,7 +1146,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             buf ^= 1;
             if (buf == 0) tph ^= 1u;
         };
-        const uint32_t patch = behind + warp * kPatchBytes;
+        const uint32_t patch = behind + warp * PATCH;
         const uint32_t quarter = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         // A tile whose reduction the cluster shares: this CTA's sums to its shared partial tile, then its rows of all.
         uint32_t pph = 0;  // tiles so far, mod 2
@@ -1195,7 +1214,7 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             if (I8 && it.e < a.E)
                 for (int i = 0; i < 4; ++i)
                     if (col + i < a.NL) cs[i] = load(behind_wait(a.col_scale) + static_cast<long long>(it.e) * a.NL + col + i);
-            for (int r = part * per + warp; r < min((part + 1) * per, it.rows); r += kStoreWarps) {
+            for (int r = part * per + warp; r < min((part + 1) * per, it.rows); r += SW) {
                 uint32_t v[4], sum[4] = {0u, 0u, 0u, 0u};
                 for (int p = 0; p < a.split; ++p) {
                     uint32_t there;
@@ -1227,6 +1246,49 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
             pph ^= 1u;
             return true;
         };
+        if constexpr (EPI == kGateGrad && !SPLIT) {
+            const int first = 16 * (warp >> 2), x0 = 128 * rank + 32 * (warp & 3);
+            Item it{};
+            // the first rows' factors of the next tile, while this warp has none to wait for
+            auto begin = [&](int t) {
+                if (t >= ntiles) return;
+                it = tile_item<MODE, CG>(a, list, t);
+                if (a.wide_h && first < it.rows) fetch_factors(a, it, it.lane0 + x0, lane, patch, first);
+            };
+            begin(me);
+            for (int t = me; t < ntiles; t += G) {
+                if (!acc_wait()) break;
+                const uint32_t src = tmem + buf * buf_cols + quarter;
+                const int x = it.lane0 + x0;
+                bool held = true;
+#pragma unroll 1
+                for (int c0 = first; c0 < it.rows; c0 += 4 * SW) {
+                    uint32_t v[16];
+                    if (it.red > 0) {
+                        load_frag16(src + c0, v);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = 0u;
+                    }
+                    if (c0 + 4 * SW >= it.rows) {  // this warp's last look at the accumulator
+                        acc_free();
+                        held = false;
+                    }
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    __syncwarp();
+                    with_act(a.gate.act, [&](auto kind) {
+                        constexpr int ACT = decltype(kind)::value;
+                        if (a.h_type == SPX_BF16) store_gate_grad<__nv_bfloat16, ACT>(a, it, x, lane, patch, c0, v);
+                        else store_gate_grad<__half, ACT>(a, it, x, lane, patch, c0, v);
+                    });
+                    if (a.wide_h && c0 + 4 * SW < it.rows) fetch_factors(a, it, x, lane, patch, c0 + 4 * SW);
+                }
+                if (held) acc_free();
+                begin(t + G);
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        } else
         for (int t = me; t < ntiles; t += G) {
             const Item it = tile_item<MODE, CG>(a, list, t);
             const int x = it.lane0 + 128 * rank + 32 * (warp & 3);
@@ -1236,9 +1298,6 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                 continue;
             }
             if (!I8) {
-                Factors h;
-                if constexpr (EPI == kGateGrad)
-                    if (a.wide_h) fetch_factors(a, it, x, lane, 32 * (warp >> 2), h);
                 if (!acc_wait()) break;
                 const uint32_t src = tmem + buf * buf_cols + quarter;
                 bool held = true;
@@ -1256,17 +1315,11 @@ __global__ void __launch_bounds__(kThreadsOf<FUSE>, 1)
                         acc_free();
                         held = false;
                     }
-                    if constexpr (EPI == kGateGrad) {
-                        const bool more = c0 + 64 < it.rows;
-                        if (a.h_type == SPX_BF16) store_gate_grad<__nv_bfloat16>(a, it, x, lane, patch, c0, v, h, more);
-                        else store_gate_grad<__half>(a, it, x, lane, patch, c0, v, h, more);
-                    } else {
-                        float f[32];
+                    float f[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-                        if constexpr (EPI == kGate) store_gate(a, it, (it.lane0 + 128 * rank) / 2 + 16 * (warp & 3), lane, patch, c0, f);
-                        else store_chunk(a, it, off, x, lane, patch, c0, f);
-                    }
+                    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+                    if constexpr (EPI == kGate) store_gate(a, it, (it.lane0 + 128 * rank) / 2 + 16 * (warp & 3), lane, patch, c0, f);
+                    else store_chunk(a, it, off, x, lane, patch, c0, f);
                 }
                 if (held) acc_free();
                 continue;
@@ -1449,7 +1502,7 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     a.wide_f = spx_aligned(a.C, 16) && a.ldc % 4 == 0 && a.NL % 4 == 0;
     const int team = SPLIT ? a.split : CG;  // CTAs that work on one tile
     a.part_off = static_cast<uint32_t>((list_bytes(a.E) + 15) / 16 * 16);
-    const size_t list = a.part_off + (SPLIT ? a.TN * kPartPitch : kStoreWarps * kPatchBytes);
+    const size_t list = a.part_off + (SPLIT ? a.TN * kPartPitch : kStoreWarpsOf<SPLIT, EPI> * (EPI == kGateGrad ? 2 * kFactorBytes : kPatchBytes));
     size_t room = kSmemMax - 1024 - list;
     if (FUSE) {  // stages for the MMAs, more than the widening warps fill at once where there is room, and raw ones
         a.stages = a.TN > 64 ? 2 : 4;
@@ -1463,7 +1516,7 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + room + list;
     if (set_smem_limit(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE, EPI>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreadsOf<FUSE>);
+    cfg.blockDim = dim3(kThreadsOf<SPLIT, FUSE, EPI>);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1482,7 +1535,7 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     spx_note_launches(1);
     return spx_cuda_status(launch_early(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE, EPI>,
                                         dim3(static_cast<unsigned>(std::min<long long>(max_tiles, groups)) * team),
-                                        kThreadsOf<FUSE>, smem, team, st, tl, tc, a));
+                                        kThreadsOf<SPLIT, FUSE, EPI>, smem, team, st, tl, tc, a));
 }
 
 uint32_t idesc_of(spx_type type, int mode, int cg) {
