@@ -56,26 +56,29 @@ constexpr float kTanh1 = 1.5957691216f, kTanh3 = 0.07135481628f;  // 2 sqrt(2 / 
 
 template <int kind>
 __device__ __forceinline__ float act_of(float x) {
+    if (kind == SPX_ACT_SILU) {
+        const float cut = at_least(x, -88.f);
+        return cut * logistic(at_most(cut, 88.f));
+    }
     const float cut = at_least(x, -100.f);
     if (kind == SPX_ACT_GELU) return cut * normcdff(x);
-    float z = cut;
-    if (kind == SPX_ACT_GELU_TANH) z = cut * fmaf(kTanh3, fminf(x * x, 1e4f), kTanh1);
+    const float z = cut * fmaf(kTanh3, fminf(x * x, 1e4f), kTanh1);
     return cut * logistic(at_most(at_least(z, -88.f), 88.f));
 }
 template <int kind>
 __device__ __forceinline__ float act_of(float x, float& slope) {
-    const float cut = at_least(x, -100.f), near = at_most(cut, 100.f);
-    if (kind == SPX_ACT_GELU) {
-        const float p = normcdff(x);
-        slope = fmaf(near * 0.3989422804f, expf(-0.5f * x * x), p);
+    if (kind == SPX_ACT_SILU) {
+        const float cut = at_least(x, -88.f), z = at_most(cut, 88.f), p = logistic(z);
+        slope = p * fmaf(z, 1.f - p, 1.f);
         return cut * p;
     }
-    float z = near, dz = 1.f;
-    if (kind == SPX_ACT_GELU_TANH) {
-        const float xx = near * near;
-        z = near * fmaf(kTanh3, xx, kTanh1);
-        dz = fmaf(3.f * kTanh3, xx, kTanh1);
+    const float cut = at_least(x, -100.f), near = at_most(cut, 100.f), xx = near * near;
+    if (kind == SPX_ACT_GELU) {
+        const float p = normcdff(x);
+        slope = fmaf(near * 0.3989422804f, expf(-0.5f * xx), p);
+        return cut * p;
     }
+    const float z = near * fmaf(kTanh3, xx, kTanh1), dz = fmaf(3.f * kTanh3, xx, kTanh1);
     const float p = logistic(at_most(at_least(z, -88.f), 88.f));
     slope = p * fmaf(near * dz, 1.f - p, 1.f);
     return cut * p;

@@ -512,19 +512,47 @@ __device__ __forceinline__ void store_gate(const TcArgs& a, const Item& it, int 
 // same way back.
 constexpr uint32_t kFactorBytes = 16 * kPatchPitch;
 
-__device__ __forceinline__ void fetch_factors(const TcArgs& a, const Item& it, int x, int lane, uint32_t patch, int c0) {
-    const int r = lane >> 2, p = lane & 3;
-    const uint16_t* H = behind_wait(static_cast<const uint16_t*>(a.gate.H));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool on = it.e < a.E && 8 * p < a.NL - x && r + 8 * i < it.rows - c0;
-        const uint16_t* q = on ? H + (it.row0 + c0 + r + 8 * i) * a.gate.ldh + x + 8 * p : H;
-        const uint32_t to = patch + (r + 8 * i) * kPatchPitch + 16 * p, bytes = on ? 16 : 0;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(q), "r"(bytes) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + kFactorBytes), "l"(q + (on ? a.NL : 0)), "r"(bytes) : "memory");
+// Where a thread reads and writes whole pieces (r = lane / 4, p = lane % 4: rows r and r + 8, columns 8 p to 8 p + 7 of
+// a warp's chunk), stepped from chunk to chunk.
+struct Pieces {
+    const uint16_t* h;
+    uint16_t *d, *c;
+    int left;    // rows of the tile from r on; none where the columns end before these
+    bool live;   // rows of an expert
+    __device__ __forceinline__ void start(const TcArgs& a, const Item& it, int x, int lane, int c0) {
+        const int r = c0 + (lane >> 2), p = 8 * (lane & 3);
+        const long long row = it.row0 + r;
+        h = behind_wait(static_cast<const uint16_t*>(a.gate.H)) + row * a.gate.ldh + x + p;
+        d = static_cast<uint16_t*>(a.gate.dH) + row * a.gate.lddh + x + p;
+        c = static_cast<uint16_t*>(a.C) + row * a.ldc + x + p;
+        left = p < a.NL - x ? it.rows - r : 0;
+        live = it.e < a.E;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
+    __device__ __forceinline__ void step(const TcArgs& a, int by) {
+        h += by * a.gate.ldh, d += by * a.gate.lddh, c += by * a.ldc, left -= by;
+    }
+    // both factors to the warp's patches; what lies outside is not read
+    __device__ __forceinline__ void fetch(const TcArgs& a, uint32_t to) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (live && 8 * i < left) {
+                const uint16_t* q = h + i * 8 * a.gate.ldh;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 8 * kPatchPitch), "l"(q) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 8 * kPatchPitch + kFactorBytes), "l"(q + a.NL) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // a patch's rows to memory
+    __device__ __forceinline__ void put(uint32_t from, uint16_t* to, long long ld) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(from + i * 8 * kPatchPitch) : "memory");
+            if (8 * i < left) *reinterpret_cast<uint4*>(to + i * 8 * ld) = w;
+        }
+    }
+};
 
 // 16 rows of a warp's 32 lanes: thread t's v[8 h + 4 q + i] is lane 16 h + t / 4 + 8 (i / 2), row 8 q + 2 (t % 4) + i % 2.
 __device__ __forceinline__ void load_frag16(uint32_t taddr, uint32_t (&v)[16]) {
@@ -552,16 +580,6 @@ __device__ __forceinline__ void frag_in(uint32_t at, const uint32_t (&q)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3])
                  : "memory");
 }
-// A patch's 16 rows of 32 columns to memory.
-__device__ __forceinline__ void patch_rows(uint32_t patch, int lane, uint16_t* out, long long ld, int rows, int cols) {
-    const int r = lane >> 2, p = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 w = patch_row(patch, r + 8 * i, p);
-        if (r + 8 * i < rows && 8 * p < cols) *reinterpret_cast<uint4*>(out + (r + 8 * i) * ld + 8 * p) = w;
-    }
-}
-
 template <class V>
 __device__ __forceinline__ float2 unpack(uint32_t w) {
     V v[2];
@@ -569,58 +587,62 @@ __device__ __forceinline__ float2 unpack(uint32_t w) {
     return make_float2(to_f(v[0]), to_f(v[1]));
 }
 
-// dG, dU and C of one output; all zeros in the rows past the last expert's, whatever H holds there.
+// dG, dU and C of one output.
 template <int ACT>
-__device__ __forceinline__ void gate_grad(bool live, float dc, float g, float u, float& dg, float& du, float& c) {
+__device__ __forceinline__ void gate_grad(float dc, float g, float u, float& dg, float& du, float& c) {
     float slope;
     const float act = act_of<ACT>(g, slope);
-    dg = live ? dc * u * slope : 0.f;
-    du = live ? dc * act : 0.f;
-    c = live ? act * u : 0.f;
+    dg = dc * u * slope;
+    du = dc * act;
+    c = act * u;
 }
 
+// 16 rows on wide rows.  The rows past the last expert's are zeros: their sums are, and so is what stands for H.
 template <class V, int ACT>
-__device__ __forceinline__ void store_gate_grad(const TcArgs& a, const Item& it, int x, int lane, uint32_t patch, int c0,
-                                                const uint32_t (&v)[16]) {
+__device__ __forceinline__ void store_gate_grad(const TcArgs& a, const Pieces& at, int lane, uint32_t patch, const uint32_t (&v)[16]) {
+    const uint32_t piece = patch + (lane >> 2) * kPatchPitch + 16 * (lane & 3);
+    uint32_t c[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t g[4], u[4];
+        const uint32_t to = frag_addr(patch, lane, h);
+        frag_out(to, g);
+        frag_out(to + kFactorBytes, u);
+        if (!at.live) g[0] = g[1] = g[2] = g[3] = u[0] = u[1] = u[2] = u[3] = 0;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int i = 8 * h + 4 * (m & 1) + 2 * (m >> 1);
+            const float2 fg = unpack<V>(g[m]), fu = unpack<V>(u[m]);
+            float2 a0, a1, a2;
+            gate_grad<ACT>(__uint_as_float(v[i]), fg.x, fu.x, a0.x, a1.x, a2.x);
+            gate_grad<ACT>(__uint_as_float(v[i + 1]), fg.y, fu.y, a0.y, a1.y, a2.y);
+            g[m] = pack<V>(a0.x, a0.y), u[m] = pack<V>(a1.x, a1.y), c[h][m] = pack<V>(a2.x, a2.y);
+        }
+        __syncwarp();
+        frag_in(to, g);
+        frag_in(to + kFactorBytes, u);
+    }
+    __syncwarp();
+    at.put(piece, at.d, a.gate.lddh);
+    at.put(piece + kFactorBytes, at.d + a.NL, a.gate.lddh);
+    __syncwarp();
+    if (a.C) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) frag_in(frag_addr(patch, lane, h), c[h]);
+        __syncwarp();
+        at.put(piece, at.c, a.ldc);
+        __syncwarp();
+    }
+}
+
+// The same value by value.
+template <class V, int ACT>
+__device__ __forceinline__ void store_gate_grad_narrow(const TcArgs& a, const Item& it, int x, int lane, int c0, const uint32_t (&v)[16]) {
     const int rows = it.rows - c0, cols = a.NL - x;
     const bool live = it.e < a.E;
     const long long row = it.row0 + c0;
     V* dH = static_cast<V*>(a.gate.dH) + row * a.gate.lddh + x;
     V* C = static_cast<V*>(a.C) + row * a.ldc + x;
-    if (a.wide_h) {
-        uint32_t c[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t g[4], u[4];
-            const uint32_t at = frag_addr(patch, lane, h);
-            frag_out(at, g);
-            frag_out(at + kFactorBytes, u);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int i = 8 * h + 4 * (m & 1) + 2 * (m >> 1);
-                const float2 fg = unpack<V>(g[m]), fu = unpack<V>(u[m]);
-                float2 a0, a1, a2;
-                gate_grad<ACT>(live, __uint_as_float(v[i]), fg.x, fu.x, a0.x, a1.x, a2.x);
-                gate_grad<ACT>(live, __uint_as_float(v[i + 1]), fg.y, fu.y, a0.y, a1.y, a2.y);
-                g[m] = pack<V>(a0.x, a0.y), u[m] = pack<V>(a1.x, a1.y), c[h][m] = pack<V>(a2.x, a2.y);
-            }
-            __syncwarp();
-            frag_in(at, g);
-            frag_in(at + kFactorBytes, u);
-        }
-        __syncwarp();
-        patch_rows(patch, lane, reinterpret_cast<uint16_t*>(dH), a.gate.lddh, rows, cols);
-        patch_rows(patch + kFactorBytes, lane, reinterpret_cast<uint16_t*>(dH + a.NL), a.gate.lddh, rows, cols);
-        __syncwarp();
-        if (a.C) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) frag_in(frag_addr(patch, lane, h), c[h]);
-            __syncwarp();
-            patch_rows(patch, lane, reinterpret_cast<uint16_t*>(C), a.ldc, rows, cols);
-            __syncwarp();
-        }
-        return;
-    }
     const V* H = behind_wait(static_cast<const V*>(a.gate.H)) + row * a.gate.ldh + x;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -628,7 +650,7 @@ __device__ __forceinline__ void store_gate_grad(const TcArgs& a, const Item& it,
         if (n >= cols || r >= rows) continue;
         float dg, du, c;
         const V* p = H + r * a.gate.ldh + n;
-        gate_grad<ACT>(live, __uint_as_float(v[i]), to_f(load(p)), to_f(load(p + a.NL)), dg, du, c);
+        gate_grad<ACT>(__uint_as_float(v[i]), live ? to_f(load(p)) : 0.f, live ? to_f(load(p + a.NL)) : 0.f, dg, du, c);
         V* d = dH + r * a.gate.lddh + n;
         d[0] = from_f<V>(dg);
         d[a.NL] = from_f<V>(du);
@@ -701,7 +723,7 @@ __device__ __forceinline__ void gate_grad_four(const TcArgs& a, const Item& it, 
     }
     with_act(a.gate.act, [&](auto kind) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) gate_grad<decltype(kind)::value>(live, f[i], g[i], u[i], dg[i], du[i], c[i]);
+        for (int i = 0; i < 4; ++i) gate_grad<decltype(kind)::value>(f[i], g[i], u[i], dg[i], du[i], c[i]);
     });
     V* d = static_cast<V*>(a.gate.dH) + row * a.gate.lddh + x;
     put_four(d, left, a.wide_h, dg);
@@ -1248,12 +1270,26 @@ __global__ void __launch_bounds__(kThreadsOf<SPLIT, FUSE, EPI>, 1)
         };
         if constexpr (EPI == kGateGrad && !SPLIT) {
             const int first = 16 * (warp >> 2), x0 = 128 * rank + 32 * (warp & 3);
+            const uint32_t piece = patch + (lane >> 2) * kPatchPitch + 16 * (lane & 3);
             Item it{};
-            // the first rows' factors of the next tile, while this warp has none to wait for
+            Pieces at{};
+            // the first rows' factors of the next tile, while this warp has none to wait for; its other rows' to L2
             auto begin = [&](int t) {
                 if (t >= ntiles) return;
                 it = tile_item<MODE, CG>(a, list, t);
-                if (a.wide_h && first < it.rows) fetch_factors(a, it, it.lane0 + x0, lane, patch, first);
+                if (!a.wide_h || first >= it.rows) return;
+                at.start(a, it, it.lane0 + x0, lane, first);
+                at.fetch(a, piece);
+                if (at.live && (lane & 3) == 0)
+                    for (int i = 4 * SW; i < at.left; i += 4 * SW) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if (i + 8 * j >= at.left) break;
+                            const uint16_t* q = at.h + (i + 8 * j) * a.gate.ldh;
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(q + a.NL));
+                        }
+                    }
             };
             begin(me);
             for (int t = me; t < ntiles; t += G) {
@@ -1279,10 +1315,18 @@ __global__ void __launch_bounds__(kThreadsOf<SPLIT, FUSE, EPI>, 1)
                     __syncwarp();
                     with_act(a.gate.act, [&](auto kind) {
                         constexpr int ACT = decltype(kind)::value;
-                        if (a.h_type == SPX_BF16) store_gate_grad<__nv_bfloat16, ACT>(a, it, x, lane, patch, c0, v);
-                        else store_gate_grad<__half, ACT>(a, it, x, lane, patch, c0, v);
+                        if (a.wide_h) {
+                            if (a.h_type == SPX_BF16) store_gate_grad<__nv_bfloat16, ACT>(a, at, lane, patch, v);
+                            else store_gate_grad<__half, ACT>(a, at, lane, patch, v);
+                        } else {
+                            if (a.h_type == SPX_BF16) store_gate_grad_narrow<__nv_bfloat16, ACT>(a, it, x, lane, c0, v);
+                            else store_gate_grad_narrow<__half, ACT>(a, it, x, lane, c0, v);
+                        }
                     });
-                    if (a.wide_h && c0 + 4 * SW < it.rows) fetch_factors(a, it, x, lane, patch, c0 + 4 * SW);
+                    if (a.wide_h && c0 + 4 * SW < it.rows) {
+                        at.step(a, 4 * SW);
+                        at.fetch(a, piece);
+                    }
                 }
                 if (held) acc_free();
                 begin(t + G);
