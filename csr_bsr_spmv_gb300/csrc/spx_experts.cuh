@@ -33,6 +33,30 @@ __device__ __forceinline__ __half from_f<__half>(float v) {
     return __float2half_rn(v);
 }
 
+// A word of two 16-bit values, the lower half first, as floats, and back (rounded once each).
+template <class V>
+__device__ __forceinline__ float2 widen2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 widen2<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <class V>
+__device__ __forceinline__ uint32_t narrow2(float2 f);
+template <>
+__device__ __forceinline__ uint32_t narrow2<__nv_bfloat16>(float2 f) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+template <>
+__device__ __forceinline__ uint32_t narrow2<__half>(float2 f) {
+    const __half2 p = __floats2half2_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
 // Four 8-bit codes (bytes of w) as fp16: 0x6400 | u is 1024 + u for a byte u,
 // and u = code + 128 after flipping its top bit, so one subtraction is exact.
 __device__ __forceinline__ uint2 widen_codes(uint32_t w) {

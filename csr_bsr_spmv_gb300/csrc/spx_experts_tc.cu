@@ -335,16 +335,8 @@ __device__ __forceinline__ void cluster_sync() {
 
 // Two floats as a pair of 16-bit values, `lo` in the low half.
 template <class O>
-__device__ __forceinline__ uint32_t pack(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&p);
-}
-template <>
-__device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
-    const __half2 p = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&p);
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    return narrow2<O>(make_float2(lo, hi));
 }
 
 // 32 accumulator columns (output rows) of a warp's 32 lanes (output columns)
@@ -580,13 +572,6 @@ __device__ __forceinline__ void frag_in(uint32_t at, const uint32_t (&q)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3])
                  : "memory");
 }
-template <class V>
-__device__ __forceinline__ float2 unpack(uint32_t w) {
-    V v[2];
-    memcpy(v, &w, 4);
-    return make_float2(to_f(v[0]), to_f(v[1]));
-}
-
 // dG, dU and C of one output.
 template <int ACT>
 __device__ __forceinline__ void gate_grad(float dc, float g, float u, float& dg, float& du, float& c) {
@@ -612,7 +597,7 @@ __device__ __forceinline__ void store_gate_grad(const TcArgs& a, const Pieces& a
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const int i = 8 * h + 4 * (m & 1) + 2 * (m >> 1);
-            const float2 fg = unpack<V>(g[m]), fu = unpack<V>(u[m]);
+            const float2 fg = widen2<V>(g[m]), fu = widen2<V>(u[m]);
             float2 a0, a1, a2;
             gate_grad<ACT>(__uint_as_float(v[i]), fg.x, fu.x, a0.x, a1.x, a2.x);
             gate_grad<ACT>(__uint_as_float(v[i + 1]), fg.y, fu.y, a0.y, a1.y, a2.y);
@@ -714,7 +699,7 @@ __device__ __forceinline__ void gate_grad_four(const TcArgs& a, const Item& it, 
     const bool live = it.e < a.E;
     if (live && a.wide_h && left >= 4) {
         const uint2 wg = load(reinterpret_cast<const uint2*>(H)), wu = load(reinterpret_cast<const uint2*>(H + a.NL));
-        const float2 g0 = unpack<V>(wg.x), g1 = unpack<V>(wg.y), u0 = unpack<V>(wu.x), u1 = unpack<V>(wu.y);
+        const float2 g0 = widen2<V>(wg.x), g1 = widen2<V>(wg.y), u0 = widen2<V>(wu.x), u1 = widen2<V>(wu.y);
         g[0] = g0.x, g[1] = g0.y, g[2] = g1.x, g[3] = g1.y, u[0] = u0.x, u[1] = u0.y, u[2] = u1.x, u[3] = u1.y;
     } else if (live) {
 #pragma unroll

@@ -14,7 +14,15 @@ struct alignas(N * sizeof(V) >= 16 ? 16 : N * sizeof(V)) Pack {
     V v[N];
 };
 
-// A piece is written as one word of its size; `once`: it is not read again soon.
+// A piece is read (from shared memory) and written as one word of its size: its own copy would go value by value.
+// `once`: it is not read again soon.
+template <class P>
+__device__ __forceinline__ P read_piece(const P* p) {
+    const auto w = *reinterpret_cast<const typename Word<sizeof(P)>::T*>(p);
+    P v;
+    memcpy(&v, &w, sizeof(P));
+    return v;
+}
 template <class P>
 __device__ __forceinline__ void write_piece(P* p, const P& v) {
     using T = typename Word<sizeof(P)>::T;
@@ -30,22 +38,55 @@ __device__ __forceinline__ void write_once(P* p, const P& v) {
     __stcs(reinterpret_cast<T*>(p), w);
 }
 
+// A piece's values as fp32 in pairs (N == 1: one value and a zero), and back.
+template <int N>
+struct Floats {
+    float2 v[(N + 1) / 2];
+};
+template <class V, int N>
+__device__ __forceinline__ Floats<N> floats(const Pack<V, N>& p) {
+    Floats<N> f;
+    if constexpr (N == 1) {
+        f.v[0] = make_float2(to_f(p.v[0]), 0.f);
+    } else if constexpr (sizeof(V) == 2) {
+        uint32_t w[N / 2];
+        memcpy(w, &p, sizeof(p));
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) f.v[i] = widen2<V>(w[i]);
+    } else {
+        memcpy(&f, &p, sizeof(p));
+    }
+    return f;
+}
+template <class V, int N>
+__device__ __forceinline__ Pack<V, N> packed(const Floats<N>& f) {
+    Pack<V, N> p;
+    if constexpr (N == 1) {
+        p.v[0] = from_f<V>(f.v[0].x);
+    } else if constexpr (sizeof(V) == 2) {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = narrow2<V>(f.v[i]);
+        memcpy(&p, w, sizeof(p));
+    } else {
+        memcpy(&p, &f, sizeof(p));
+    }
+    return p;
+}
+
 // N values of type V or (wide) fp32, as fp32.
 template <class V, int N>
-__device__ __forceinline__ void load_floats(const void* p, bool wide, long long at, float (&f)[N]) {
-    if (wide) {
-        constexpr int Q = N < 4 ? N : 4;
+__device__ __forceinline__ Floats<N> load_floats(const void* p, bool wide, long long at) {
+    if (!wide) return floats(load(reinterpret_cast<const Pack<V, N>*>(static_cast<const V*>(p) + at)));
+    constexpr int Q = N < 4 ? N : 4;
+    Floats<N> f;
 #pragma unroll
-        for (int i = 0; i < N / Q; ++i) {
-            const Pack<float, Q> x = load(reinterpret_cast<const Pack<float, Q>*>(static_cast<const float*>(p) + at) + i);
+    for (int i = 0; i < N / Q; ++i) {
+        const Floats<Q> x = floats(load(reinterpret_cast<const Pack<float, Q>*>(static_cast<const float*>(p) + at) + i));
 #pragma unroll
-            for (int j = 0; j < Q; ++j) f[Q * i + j] = x.v[j];
-        }
-    } else {
-        const Pack<V, N> x = load(reinterpret_cast<const Pack<V, N>*>(static_cast<const V*>(p) + at));
-#pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = to_f(x.v[i]);
+        for (int j = 0; j < (Q + 1) / 2; ++j) f.v[(Q + 1) / 2 * i + j] = x.v[j];
     }
+    return f;
 }
 
 // Sum (or maximum, as unsigned numbers) over the G threads of a group, G a power of two; groups of several warps meet in

@@ -53,8 +53,8 @@ def test_rms_norm_grad_refuses(change, status):
 def test_rms_norm_grad_scratch_bytes():
     need = spx._lib().spx_rms_norm_grad_scratch_bytes
     assert need(1, 4096) == need(0, 64) == need(-1, 64) == need(64, 0) == need(64, 32769) == 0
-    assert 0 < need(100000, 4096) <= 608 * 4096 * 4
-    assert 0 < need(BIG - (1 << 23), 32768) <= 608 * 32768 * 4
+    assert 0 < need(100000, 4096) <= 304 * 4096 * 4
+    assert 0 < need(BIG - (1 << 23), 32768) <= 304 * 32768 * 4
 
 
 @pytest.mark.parametrize("change,status", [
