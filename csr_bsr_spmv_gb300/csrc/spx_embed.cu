@@ -60,10 +60,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int u = 0; u < kTokens; ++u) {
             if (t0 + u >= T) break;
-            Piece out;
+            Floats<N> f = floats(p[u]);
 #pragma unroll
-            for (int i = 0; i < N; ++i) out.v[i] = from_f<V>(id[u] >= 0 ? to_f(p[u].v[i]) * scale : 0.f);
-            write_once(reinterpret_cast<Piece*>(Y + (t0 + u) * ldy) + v, out);
+            for (int i = 0; i < (N + 1) / 2; ++i) f.v[i] = id[u] >= 0 ? __fmul2_rn(f.v[i], make_float2(scale, scale)) : make_float2(0.f, 0.f);
+            write_once(reinterpret_cast<Piece*>(Y + (t0 + u) * ldy) + v, packed<V, N>(f));
         }
     }
 }
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kOrderThreads, 2) embed_order_kernel(OrderArgs
 // ---------------------------------------------------------------- sums
 
 struct SumArgs {
-    int np, chunk;             // pieces a row, sorted tokens a chunk
+    int np, T, chunk;          // pieces a row, tokens, sorted tokens a chunk
     const int *order, *sid, *kept;
     const void* dY;
     long long lddy;
@@ -214,93 +214,123 @@ struct SumArgs {
 };
 
 template <class O, int N>
-__device__ __forceinline__ void write_sum(const SumArgs& a, int id, int v, const float (&acc)[N]) {
-    constexpr int Q = N * sizeof(O) > 16 ? 16 / sizeof(O) : N;
+__device__ __forceinline__ void write_sum(const SumArgs& a, int id, int v, const Floats<N>& acc) {
+    constexpr int Q = N * sizeof(O) > 16 ? 16 / sizeof(O) : N, X = (Q + 1) / 2;
     Pack<O, Q>* q = reinterpret_cast<Pack<O, Q>*>(static_cast<O*>(a.dW) + id * a.ldw + static_cast<long long>(v) * N);
+    const float2 c = make_float2(a.scale, a.scale);
 #pragma unroll
     for (int i = 0; i < N / Q; ++i) {
-        Pack<O, Q> p;
-        if (a.add) p = load(q + i);
+        Floats<Q> f;
+        if (a.add) f = floats(load(q + i));
 #pragma unroll
-        for (int j = 0; j < Q; ++j) p.v[j] = from_f<O>(a.add ? fmaf(acc[Q * i + j], a.scale, to_f(p.v[j])) : acc[Q * i + j] * a.scale);
-        write_piece(q + i, p);
+        for (int j = 0; j < X; ++j) f.v[j] = a.add ? __ffma2_rn(acc.v[X * i + j], c, f.v[j]) : __fmul2_rn(acc.v[X * i + j], c);
+        write_piece(q + i, packed<O, Q>(f));
     }
 }
 
 constexpr int kRows = 8;  // rows in flight
 
+// A warp's lanes hold the tokens and ids of 32 sorted places, the next 32 on their way.
 template <class V, class O, int N>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(SumArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) embed_sum_kernel(SumArgs a) {
+    constexpr int X = (N + 1) / 2;
     using Piece = Pack<V, N>;
     let_next_start();
     wait_for_previous();
-    const int n = load(behind_wait(a.kept));
     const int *order = behind_wait(a.order), *sid = behind_wait(a.sid);
-    const V* dY = behind_wait(static_cast<const V*>(a.dY));
-    const int v = blockIdx.y * kThreads + threadIdx.x;
+    const int lane = threadIdx.x & 31, v = min(static_cast<int>(blockIdx.y * kThreads + threadIdx.x), a.np - 1);
+    const bool mine = static_cast<int>(blockIdx.y * kThreads + threadIdx.x) < a.np;
     const long long first = static_cast<long long>(blockIdx.x) * a.chunk;
-    if (v >= a.np || first >= n) return;
-    const int p0 = static_cast<int>(first), p1 = static_cast<int>(min(first + a.chunk, static_cast<long long>(n)));
-    bool open = p0 > 0 && load(sid + p0 - 1) == load(sid + p0);  // the current id began before the chunk
-    float acc[N];
+    const int p0 = static_cast<int>(first), most = static_cast<int>(min(first + a.chunk, static_cast<long long>(a.T)));
+    // places past the last token's hold anything: they are looked at with the number of tokens in hand
+    int next_id = p0 + lane < most ? load(sid + p0 + lane) : -1, next_at = p0 + lane < most ? load(order + p0 + lane) : 0;
+    const int left = p0 > 0 ? load(sid + p0 - 1) : -1, right = most < a.T ? load(sid + most) : -1;
+    const int n = load(behind_wait(a.kept));
+    if (p0 >= n) return;
+    const int p1 = min(most, n);
+    const V* dY = behind_wait(static_cast<const V*>(a.dY)) + static_cast<long long>(v) * N;
+    int id = __shfl_sync(0xffffffffu, next_id, 0);
+    bool open = p0 > 0 && left == id;  // the current id began before the chunk
+    Floats<N> acc;
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    int id = load(sid + p0);
+    for (int i = 0; i < X; ++i) acc.v[i] = make_float2(0.f, 0.f);
     auto keep = [&](int which) {
-        float* q = a.part + (2LL * blockIdx.x + which) * a.ldp + static_cast<long long>(v) * N;
+        if (!mine) return;
+        constexpr int Q = N < 4 ? N : 4;
+        Pack<float, Q>* q = reinterpret_cast<Pack<float, Q>*>(a.part + (2LL * blockIdx.x + which) * a.ldp + static_cast<long long>(v) * N);
 #pragma unroll
-        for (int i = 0; i < N; ++i) q[i] = acc[i];
+        for (int i = 0; i < N / Q; ++i) {
+            Floats<Q> f;
+#pragma unroll
+            for (int j = 0; j < (Q + 1) / 2; ++j) f.v[j] = acc.v[(Q + 1) / 2 * i + j];
+            write_piece(q + i, packed<float, Q>(f));
+        }
     };
-    for (int p = p0; p < p1; p += kRows) {
-        Piece x[kRows];
-        int next[kRows];
+    for (int base = p0; base < p1; base += 32) {
+        const int my_id = next_id, my_at = next_at;
+        if (base + 32 + lane < p1) next_id = load(sid + base + 32 + lane), next_at = load(order + base + 32 + lane);
+        for (int u0 = 0; u0 < 32 && base + u0 < p1; u0 += kRows) {
+            Piece x[kRows];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u)
-            if (p + u < p1) {
-                next[u] = load(sid + p + u);
-                x[u] = load_once(reinterpret_cast<const Piece*>(dY + load(order + p + u) * a.lddy) + v);
+            for (int u = 0; u < kRows; ++u) {
+                const int t = __shfl_sync(0xffffffffu, my_at, u0 + u);
+                if (base + u0 + u < p1) x[u] = load_once(reinterpret_cast<const Piece*>(dY + t * a.lddy));
             }
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            if (p + u >= p1) break;
-            if (next[u] != id) {
-                if (open) keep(0);
-                else write_sum<O, N>(a, id, v, acc);
-                open = false;
-                id = next[u];
+            for (int u = 0; u < kRows; ++u) {
+                const int next = __shfl_sync(0xffffffffu, my_id, u0 + u);
+                if (base + u0 + u >= p1) continue;
+                if (next != id) {
+                    if (open) keep(0);
+                    else if (mine) write_sum<O, N>(a, id, v, acc);
+                    open = false;
+                    id = next;
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] = 0.f;
+                    for (int i = 0; i < X; ++i) acc.v[i] = make_float2(0.f, 0.f);
+                }
+                const Floats<N> f = floats(x[u]);
+#pragma unroll
+                for (int i = 0; i < X; ++i) acc.v[i] = __fadd2_rn(acc.v[i], f.v[i]);
             }
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] += to_f(x[u].v[i]);
         }
     }
     if (open) keep(0);
-    else if (p1 < n && load(sid + p1) == id) keep(1);
-    else write_sum<O, N>(a, id, v, acc);
+    else if (p1 < n && right == id) keep(1);
+    else if (mine) write_sum<O, N>(a, id, v, acc);
 }
 
 // One block for each chunk whose last id began in it and goes on after it.
 template <class O, int N>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(SumArgs a) {
+    constexpr int X = (N + 1) / 2;
     let_next_start();
     wait_for_previous();
-    const int n = load(behind_wait(a.kept));
     const int* sid = behind_wait(a.sid);
     const float* part = behind_wait(static_cast<const float*>(a.part));
     const int v = blockIdx.y * kThreads + threadIdx.x;
     const long long p0 = static_cast<long long>(blockIdx.x) * a.chunk, p1 = p0 + a.chunk;
-    if (v >= a.np || p1 >= n) return;
-    const int id = load(sid + p1 - 1);
-    if (load(sid + p1) != id || (p0 > 0 && load(sid + p0 - 1) == id)) return;
-    float acc[N];
+    if (p1 >= a.T) return;
+    // places past the last token's hold anything
+    const int n = load(behind_wait(a.kept)), id = load(sid + p1 - 1), after = load(sid + p1), before = p0 > 0 ? load(sid + p0 - 1) : -1;
+    if (p1 >= n || after != id || (p0 > 0 && before == id)) return;
+    // the chunks that the id goes on in, a thread a chunk
+    int chunks = 0;
+    for (;;) {
+        const long long p = p1 + (chunks + static_cast<long long>(threadIdx.x)) * a.chunk;
+        const int more = __syncthreads_count(p < n && load(sid + p) == id);
+        chunks += more;
+        if (more < kThreads) break;
+    }
+    if (v >= a.np) return;
+    Floats<N> acc;
     part += 2LL * blockIdx.x * a.ldp + static_cast<long long>(v) * N;
+    auto row = [&](const float* p) { return load_floats<float, N>(p, true, 0); };
+    acc = row(part + a.ldp);
+#pragma unroll 8
+    for (int c = 1; c <= chunks; ++c) {
+        const Floats<N> f = row(part + 2LL * c * a.ldp);
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = load(part + a.ldp + i);
-    for (long long p = p1; p < n && load(sid + p) == id; p += a.chunk) {
-        part += 2 * a.ldp;
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += load(part + i);
+        for (int i = 0; i < X; ++i) acc.v[i] = __fadd2_rn(acc.v[i], f.v[i]);
     }
     write_sum<O, N>(a, id, v, acc);
 }
@@ -333,8 +363,8 @@ spx_status embed(int T, int H, Ids x, const void* W, int64_t ldw, float scale, v
     return spx_cuda_status(embed_launch<V, 1>(T, H, x, W, ldw, scale, Y, ldy, st));
 }
 
-// Sorted tokens a chunk: 32, more where that would make over 4096 chunks.
-int chunk_of(int T) { return std::max(32, (T + 4095) / 4096); }
+// Sorted tokens a chunk: 8 to 32, so that the chunks fill the SMs, more where there would be over 4096 of them.
+int chunk_of(int T) { return std::max(std::min(32, (T / 512 + 7) / 8 * 8 + 8), (T + 4095) / 4096); }
 
 struct Scratch {
     size_t order, sid, list, kept, part, bytes;
@@ -434,7 +464,7 @@ spx_status spx_embed_grad(int32_t T, int32_t H, int32_t V, spx_type type, const 
                               : launch_early(embed_order_kernel<uint16_t>, grid, kOrderThreads, 0, 1, st, o);
     if (e != cudaSuccess || T == 0) return spx_cuda_status(e);
     SumArgs a{};
-    a.chunk = chunk_of(T);
+    a.chunk = chunk_of(T), a.T = T;
     a.order = o.order, a.sid = o.sid, a.kept = o.kept;
     a.dY = dY, a.lddy = lddy, a.dW = dW, a.ldw = lddw;
     a.part = reinterpret_cast<float*>(base + s.part), a.ldp = s.ldp;

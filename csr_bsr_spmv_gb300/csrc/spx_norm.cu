@@ -36,7 +36,7 @@ template <class V, class O, int N, int HELD, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1280 / MAXT) rms_norm_kernel(NormArgs a) {
     constexpr int P = HELD / N;
     using Piece = Pack<V, N>;
-    __shared__ float s_sum[MAXT / 32];
+    __shared__ __align__(16) float s_sum[MAXT / 32];
     __shared__ uint32_t s_max[MAXT / 32];
     let_next_start();
     wait_for_previous();
@@ -103,16 +103,41 @@ __global__ void __launch_bounds__(MAXT, 1280 / MAXT) rms_norm_kernel(NormArgs a)
         const float q = __uint_as_float(m) / 127.f;
         if (live && at == 0) a.scale[row] = fine ? q : __int_as_float(0x7fffffff);
         if (!live) return;
-        auto code = [&](float v) {  // subnormal scales are coarse: the quotient may pass 127
-            return static_cast<int8_t>(fine && q > 0.f ? fminf(fmaxf(rintf(v / q), -127.f), 127.f) : 0.f);
-        };
+        // The quotient from the rounded reciprocal: a first one, its exact remainder, and a correction that rounds it
+        // correctly (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
+        // Subnormal scales, whose reciprocal may not exist, divide; they are coarse, so the quotient may pass 127.
+        const bool plain = fine && q >= 1e-30f;
+        const float inv = plain ? 1.f / q : 0.f;
+        constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
+        const float2 inv2 = make_float2(inv, inv), q2 = make_float2(-q, -q), whole = make_float2(kWhole, kWhole);
         Pack<O, N>* y = reinterpret_cast<Pack<O, N>*>(static_cast<O*>(a.Y) + row * a.ldy);
 #pragma unroll
         for (int h = 0; h < P; ++h) {
             if (at + h * G >= np) break;
-            Pack<O, N> p;
+            uint32_t t[2 * X];
 #pragma unroll
-            for (int i = 0; i < N; ++i) p.v[i] = code(i & 1 ? s[h].v[i / 2].y : s[h].v[i / 2].x);
+            for (int i = 0; i < X; ++i) {
+                const float2 v = s[h].v[i], q0 = __fmul2_rn(v, inv2), c = __fadd2_rn(__ffma2_rn(__ffma2_rn(q0, q2, v), inv2, q0), whole);
+                t[2 * i] = __float_as_uint(c.x), t[2 * i + 1] = __float_as_uint(c.y);
+            }
+            if (!plain) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float v = i & 1 ? s[h].v[i / 2].y : s[h].v[i / 2].x;
+                    t[i] = fine && q > 0.f ? static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(v / q), -127.f), 127.f))) : 0u;
+                }
+            }
+            Pack<O, N> p;
+            if constexpr (N >= 4) {
+                uint32_t word[N / 4];
+#pragma unroll
+                for (int i = 0; i < N / 4; ++i)
+                    word[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040), __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040), 0x5410);
+                memcpy(&p, word, N);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) p.v[i] = static_cast<int8_t>(t[i]);
+            }
             write_piece(y + at + h * G, p);
         }
     } else {
@@ -128,18 +153,12 @@ __global__ void __launch_bounds__(MAXT, 1280 / MAXT) rms_norm_kernel(NormArgs a)
 
 // ---------------------------------------------------------------- gradient
 
-// A block takes a tile of R rows at a time into shared memory, the next tile's copies in flight beside it.  First each
-// warp sums dy w s over stretches of rows, 16 values a lane; then each thread goes over the tile with columns of its own,
-// writes d s and adds to its columns' d w.  The two ways through a tile keep what is done once a row -- the sums'
-// shuffles, the barriers, the addresses -- small beside what is done once a value, which at eight values a load is what
-// would bound it (a thread with its own columns for both, a row at a time: 48 instructions a value, 225 us for 16384 x
-// 4096 bf16).
+// A group of threads takes a row, each with columns of its own whose d w it sums over its rows.  A thread copies the
+// pieces it is going to need asynchronously into its own slots of shared memory, DEPTH rows ahead: it waits for nobody
+// else's copies, and they hold no registers.  Between the two looks at a row -- the sum of dy w s, then what is written --
+// only that sum crosses threads.
 struct GradArgs {
-    int M, H, R, tiles;
-    int log_c;       // log2 of the columns of threads, kGradThreads at most: the others take other rows of the tile
-    int log_l;       // log2 of the lanes that sum a stretch
-    int segs, dots;  // stretches a row, and that rounded up to a multiple of four
-    int pitch;       // bytes of a row in shared memory
+    int M, H, log_g;
     long long lddy, lds, lddr, lddx;
     const void *dY, *S, *w, *dR;
     const float* rstd;
@@ -148,196 +167,154 @@ struct GradArgs {
     bool wide_w;  // the weights are fp32
 };
 
-constexpr int kGradThreads = 256, kGradWarps = kGradThreads / 32, kGradBlocks = 304, kStageBytes = 49152, kMostRows = 64;
-constexpr int kLaneValues = 32;  // values a lane sums
-
-// A piece from memory to shared memory, asynchronously where there is a copy of its size.
 template <class P>
 __device__ __forceinline__ void copy_piece(P* to, const P* from) {
     const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
     if constexpr (sizeof(P) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
-    else if constexpr (sizeof(P) >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(sizeof(P)) : "memory");
-    else *to = load_once(from);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(sizeof(P) < 4 ? 4 : sizeof(P)) : "memory");
 }
 
-// HELD: values of a row that a thread holds sums for.
-template <class V, int N, int HELD>
-__global__ void __launch_bounds__(kGradThreads, 2) rms_norm_grad_kernel(GradArgs a) {
-    constexpr int K = HELD / N, X = (N + 1) / 2;
+// DEPTH 0 (pieces of 2 bytes, which no copy takes, and rows that leave no room): loaded where they are needed.
+template <class V, int N, int MAXT, int DEPTH>
+__global__ void __launch_bounds__(MAXT, MAXT == kThreads ? 3 : 1) rms_norm_grad_kernel(GradArgs a) {
+    constexpr int P = kHeld / N, X = (N + 1) / 2;
     using Piece = Pack<V, N>;
-    using Two = Floats<N>;
     extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ __align__(16) float s_sum[2][MAXT / 32];
     let_next_start();
     wait_for_previous();
-    const int np = a.H / N, arrays = a.dR ? 3 : 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = 1 << a.log_g, at = threadIdx.x & (G - 1), np = a.H / N;
+    const int groups = blockDim.x >> a.log_g, mine = threadIdx.x >> a.log_g, step = gridDim.x * groups;
     const V *dY = behind_wait(static_cast<const V*>(a.dY)), *S = behind_wait(static_cast<const V*>(a.S));
     const V* dR = behind_wait(static_cast<const V*>(a.dR));
     const float* rs = behind_wait(a.rstd);
     const void* w = behind_wait(a.w);
-    // two stages of R rows of each array, the weights as fp32, the stretches' sums of a tile, rstd of two tiles
-    const int bytes = a.R * a.pitch, stage = arrays * bytes;
-    float* sw = reinterpret_cast<float*>(sm + 2 * stage);
-    float* dots = sw + (a.H + 3) / 4 * 4;
-    float* srs = dots + a.R * a.dots;
-    // the copies: a warp a row, or several a row where a tile has few
-    const int wpr = max(1, kGradWarps / a.R), first = warp / wpr, by = kGradWarps / wpr, piece = 32 * (warp % wpr) + lane;
-    const Piece *pg = reinterpret_cast<const Piece*>(dY + (static_cast<long long>(blockIdx.x) * a.R + first) * a.lddy) + piece,
-                *ps = reinterpret_cast<const Piece*>(S + (static_cast<long long>(blockIdx.x) * a.R + first) * a.lds) + piece,
-                *pr = reinterpret_cast<const Piece*>(dR + (static_cast<long long>(blockIdx.x) * a.R + first) * a.lddr) + piece;
-    auto copy = [&](const Piece* from, long long ld, uint8_t* to, int rows) {
-        Piece* q = reinterpret_cast<Piece*>(to + first * a.pitch) + piece;
-        for (int r = first; r < rows; r += by) {
-#pragma unroll 4
-            for (int i = 0; i < np - piece; i += 32 * wpr) copy_piece(q + i, from + i);
-            q = reinterpret_cast<Piece*>(reinterpret_cast<uint8_t*>(q) + by * a.pitch);
-            from = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(from) + by * ld);
-        }
+    const float over = -1.f / static_cast<float>(a.H);
+    // slot h of array x of stage d: a piece a thread
+    Piece* slots = reinterpret_cast<Piece*>(sm) + threadIdx.x;
+    auto slot = [&](int d, int x, int h) { return slots + ((d * 3 + x) * P + h) * static_cast<int>(DEPTH > 0 ? MAXT : 0); };
+    int row = blockIdx.x * groups + mine, ahead = row;
+    const Piece *g = reinterpret_cast<const Piece*>(dY + row * a.lddy) + at, *s = reinterpret_cast<const Piece*>(S + row * a.lds) + at,
+                *r = reinterpret_cast<const Piece*>(dR + row * a.lddr) + at;
+    const long long dg = step * a.lddy, ds = step * a.lds, dr = step * a.lddr;
+    auto ahead_one = [&]() {
+        ahead += step;
+        g = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(g) + dg);
+        s = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(s) + ds);
+        r = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(r) + dr);
     };
-    int next = blockIdx.x;  // tile
-    auto fetch = [&](int b) {
-        if (next < a.tiles) {
-            const int row0 = next * a.R, rows = min(a.R, a.M - row0);
-            uint8_t* to = sm + b * stage;
-            copy(pg, a.lddy, to, rows);
-            copy(ps, a.lds, to + bytes, rows);
-            if (a.dR) copy(pr, a.lddr, to + 2 * bytes, rows);
-            if (static_cast<int>(threadIdx.x) < rows) srs[b * a.R + threadIdx.x] = load(rs + row0 + threadIdx.x);
-            next += gridDim.x;
-            const long long step = static_cast<long long>(gridDim.x) * a.R;
-            pg = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(pg) + step * a.lddy);
-            ps = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(ps) + step * a.lds);
-            pr = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(pr) + step * a.lddr);
+    auto fetch = [&](int d) {
+        if (ahead < a.M) {
+#pragma unroll
+            for (int h = 0; h < P; ++h)
+                if (at + h * G < np) {
+                    copy_piece(slot(d, 0, h), g + h * G);
+                    copy_piece(slot(d, 1, h), s + h * G);
+                    if (a.dR) copy_piece(slot(d, 2, h), r + h * G);
+                }
         }
+        ahead_one();
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(0);
-    // the weights: pair j of piece p at 2 (j np + p), so that a warp's reads share no banks
-    for (int i = threadIdx.x; i < a.H; i += kGradThreads)
-        sw[N == 1 ? i : 2 * ((i % N) / 2 * np + i / N) + (i & 1)] =
-            !a.w ? 1.f : a.wide_w ? load(static_cast<const float*>(w) + i) : to_f(load(static_cast<const V*>(w) + i));
-    for (int i = threadIdx.x; i < a.R * a.dots; i += kGradThreads) dots[i] = 0.f;
-    const int C = 1 << a.log_c, col = threadIdx.x & (C - 1), mine = threadIdx.x >> a.log_c, others = kGradThreads >> a.log_c;
-    const int L = 1 << a.log_l, at = lane & (L - 1);
-    // this warp's first stretch (of a row, or one a group of lanes) and the way to its next
-    const int u = L < 32 ? (warp << (5 - a.log_l)) + (lane >> a.log_l) : warp, du = L < 32 ? kGradWarps << (5 - a.log_l) : kGradWarps;
-    const int r_first = u / a.segs, s_first = u % a.segs, r_step = du / a.segs, s_step = du % a.segs;
-    Two acc[K], wk[K];
-    __syncthreads();
-    auto weight = [&](int p) {
-        Two f;
-        if constexpr (N == 1) {
-            f.v[0] = make_float2(sw[p], 0.f);
-        } else {
+    if constexpr (DEPTH > 0)
 #pragma unroll
-            for (int i = 0; i < X; ++i) f.v[i] = reinterpret_cast<const float2*>(sw)[i * np + p];
-        }
-        return f;
-    };
+        for (int i = 0; i < DEPTH - 1; ++i) fetch(i);
+    Floats<N> wf[P], acc[P];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int h = 0; h < P; ++h) {
 #pragma unroll
-        for (int i = 0; i < X; ++i) acc[k].v[i] = make_float2(0.f, 0.f);
-        if (col + k * C < np) wk[k] = weight(col + k * C);
+        for (int i = 0; i < X; ++i) acc[h].v[i] = make_float2(0.f, 0.f), wf[h].v[i] = make_float2(1.f, 1.f);
+        if (a.w && at + h * G < np) wf[h] = load_floats<V, N>(w, a.wide_w, static_cast<long long>(at + h * G) * N);
     }
-    const float over = -1.f / static_cast<float>(a.H);
-    V* out0 = static_cast<V*>(a.dX) + (static_cast<long long>(blockIdx.x) * a.R + mine) * a.lddx;
-    int b = 0;
-    for (int t = blockIdx.x; t < a.tiles; t += gridDim.x, b ^= 1) {
-        fetch(b ^ 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();
-        const int rows = min(a.R, a.M - t * a.R);
-        const uint8_t* tile = sm + b * stage;
-        // the stretches' sums, L lanes each; every lane of a warp goes round as often as its first
-        for (int r = r_first, seg = s_first; __any_sync(0xffffffffu, r < rows); r += r_step, seg += s_step) {
-            if (seg >= a.segs) seg -= a.segs, ++r;
-            float2 dot = make_float2(0.f, 0.f);
-            if (r < rows) {
-                const int p0 = seg * (kLaneValues / N) * L + at;
-                const Piece *g = reinterpret_cast<const Piece*>(tile + r * a.pitch), *s = reinterpret_cast<const Piece*>(tile + bytes + r * a.pitch);
+    Piece* dx = reinterpret_cast<Piece*>(static_cast<V*>(a.dX) + row * a.lddx) + at;
+    int d = 0, turn = 0;
+    for (int r0 = blockIdx.x * groups; r0 < a.M; r0 += step, row += step, turn ^= 1) {
+        const bool live = row < a.M;
+        const float rstd = live ? load(rs + row) : 0.f;
+        const float2 r2 = make_float2(rstd, rstd);
+        Piece pg[P], ps[P], pr[P];
+        if constexpr (DEPTH > 0) {
+            fetch(d == 0 ? DEPTH - 1 : d - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        } else if (live) {
 #pragma unroll
-                for (int i = 0; i < kLaneValues / N; ++i) {
-                    const int p = p0 + i * L;
-                    if (p < np) {
-                        const Two x = floats(read_piece(g + p)), y = floats(read_piece(s + p)), f = weight(p);
+            for (int h = 0; h < P; ++h)
+                if (at + h * G < np) {
+                    pg[h] = load_once(g + h * G), ps[h] = load_once(s + h * G);
+                    if (a.dR) pr[h] = load_once(r + h * G);
+                }
+        }
+        float2 dot2 = make_float2(0.f, 0.f);
+        if (live) {
 #pragma unroll
-                        for (int j = 0; j < X; ++j) dot = __ffma2_rn(__fmul2_rn(x.v[j], f.v[j]), y.v[j], dot);
-                    }
+            for (int h = 0; h < P; ++h) {
+                if (at + h * G >= np) break;
+                if constexpr (DEPTH > 0) pg[h] = read_piece(slot(d, 0, h)), ps[h] = read_piece(slot(d, 1, h));
+                const Floats<N> x = floats(pg[h]), y = floats(ps[h]);
+#pragma unroll
+                for (int i = 0; i < X; ++i) {
+                    const float2 b = __fmul2_rn(x.v[i], __fmul2_rn(y.v[i], r2));
+                    acc[h].v[i] = __fadd2_rn(acc[h].v[i], b);
+                    dot2 = __ffma2_rn(b, wf[h].v[i], dot2);
                 }
             }
-            float d = dot.x + dot.y;
-            if (L == 32) {
-#pragma unroll
-                for (int e = 16; e > 0; e >>= 1) d += __shfl_xor_sync(0xffffffffu, d, e);
-            } else {
-                for (int e = L >> 1; e > 0; e >>= 1) d += __shfl_xor_sync(0xffffffffu, d, e);
-            }
-            if (r < rows && at == 0) dots[r * a.dots + seg] = d;
         }
-        __syncthreads();
-        // the tile by columns
-        V* out = out0;
-        for (int r = mine; r < rows; r += others, out += others * a.lddx) {
-            const float rstd = srs[b * a.R + r];
-            float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i = 0; i < a.dots; i += 4) {
-                const float4 e = *reinterpret_cast<const float4*>(dots + r * a.dots + i);
-                d.x += e.x, d.y += e.y, d.z += e.z, d.w += e.w;
-            }
-            const float c = ((d.x + d.y) + (d.z + d.w)) * rstd * over;
-            const float2 r2 = make_float2(rstd, rstd), c2 = make_float2(c, c);
-            const Piece *g = reinterpret_cast<const Piece*>(tile + r * a.pitch), *s = reinterpret_cast<const Piece*>(tile + bytes + r * a.pitch),
-                        *q = reinterpret_cast<const Piece*>(tile + 2 * bytes + r * a.pitch);
+        const float dot = group_sum(dot2.x + dot2.y, G, s_sum[turn]) * over;
+        const float2 c2 = make_float2(dot, dot);
+        if (live) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int p = col + k * C;
-                if (p >= np) break;
-                const Two x = floats(read_piece(g + p)), y = floats(read_piece(s + p));
-                Two z, o;
-                if (a.dR) z = floats(read_piece(q + p));
-#pragma unroll
-                for (int j = 0; j < X; ++j) {
-                    const float2 n = __fmul2_rn(y.v[j], r2);
-                    acc[k].v[j] = __ffma2_rn(x.v[j], n, acc[k].v[j]);
-                    const float2 v = __ffma2_rn(n, c2, __fmul2_rn(x.v[j], wk[k].v[j]));
-                    o.v[j] = a.dR ? __ffma2_rn(v, r2, z.v[j]) : __fmul2_rn(v, r2);
+            for (int h = 0; h < P; ++h) {
+                if (at + h * G >= np) break;
+                if constexpr (DEPTH > 0) {  // once more, sooner than held across the sum
+                    pg[h] = read_piece(slot(d, 0, h)), ps[h] = read_piece(slot(d, 1, h));
+                    if (a.dR) pr[h] = read_piece(slot(d, 2, h));
                 }
-                write_piece(reinterpret_cast<Piece*>(out) + p, packed<V, N>(o));
+                const Floats<N> x = floats(pg[h]), y = floats(ps[h]);
+                Floats<N> z, o;
+                if (a.dR) z = floats(pr[h]);
+#pragma unroll
+                for (int i = 0; i < X; ++i) {
+                    const float2 v = __ffma2_rn(__fmul2_rn(y.v[i], r2), c2, __fmul2_rn(x.v[i], wf[h].v[i]));
+                    o.v[i] = a.dR ? __ffma2_rn(v, r2, z.v[i]) : __fmul2_rn(v, r2);
+                }
+                write_piece(dx + h * G, packed<V, N>(o));
             }
         }
-        out0 += static_cast<long long>(gridDim.x) * a.R * a.lddx;
-        __syncthreads();
+        dx = reinterpret_cast<Piece*>(reinterpret_cast<V*>(dx) + step * a.lddx);
+        if constexpr (DEPTH > 0) d = d == DEPTH - 1 ? 0 : d + 1;
+        else ahead_one();
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (DEPTH > 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.part) return;
     float* part = a.part + static_cast<long long>(blockIdx.x) * a.H;
-    float* sums = others == 1 ? part : sw;  // the weights are not needed any more
-    for (int m = 0; m < others; ++m) {  // in the rows' order
+    float* sums = groups == 1 ? part : reinterpret_cast<float*>(sm);  // where the pieces were
+    if (groups > 1) __syncthreads();
+    for (int m = 0; m < groups; ++m) {  // in the groups' order
         if (mine == m)
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int p = col + k * C;
+            for (int h = 0; h < P; ++h) {
+                const int p = at + h * G;
                 if (p >= np) break;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     float* to = sums + p * N + i;
-                    const float v = i & 1 ? acc[k].v[i / 2].y : acc[k].v[i / 2].x;
+                    const float v = i & 1 ? acc[h].v[i / 2].y : acc[h].v[i / 2].x;
                     *to = m == 0 ? v : *to + v;
                 }
             }
-        if (others > 1) __syncthreads();
+        if (groups > 1) __syncthreads();
     }
-    if (others > 1)
-        for (int c = threadIdx.x; c < a.H; c += kGradThreads) part[c] = sw[c];
+    if (groups > 1)
+        for (int c = threadIdx.x; c < a.H; c += blockDim.x) part[c] = sums[c];
 }
 
-// Rows whose tile has no room in shared memory: a block a row, read twice, the second time from L2.
+// Rows longer than a block's threads hold so: a block a row, read twice, the second time from L2.
 constexpr int kLongValues = 32;
 template <class V, int N>
 __global__ void __launch_bounds__(kMostThreads, 1) rms_norm_grad_long_kernel(GradArgs a) {
     constexpr int K = kLongValues / N;
     using Piece = Pack<V, N>;
-    __shared__ float s_sum[2][kMostThreads / 32];
+    __shared__ __align__(16) float s_sum[2][kMostThreads / 32];
     let_next_start();
     wait_for_previous();
     const int np = a.H / N;
@@ -401,8 +378,8 @@ __global__ void __launch_bounds__(kMostThreads, 1) rms_norm_grad_long_kernel(Gra
     }
 }
 
-// dw[c] = the blocks' sums, in their order within each of eight shares.
-constexpr int kAddThreads = 256;
+// dw[c] = the blocks' sums, in their order within each of 32 shares.
+constexpr int kAddThreads = 1024;
 __global__ void __launch_bounds__(kAddThreads) add_parts_kernel(int H, int blocks, const float* part, float* dw) {
     __shared__ float s[kAddThreads / 32][32];
     let_next_start();
@@ -411,7 +388,7 @@ __global__ void __launch_bounds__(kAddThreads) add_parts_kernel(int H, int block
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
     float sum = 0.f;
     if (c < H) {
-#pragma unroll 8
+#pragma unroll 16
         for (int b = w; b < blocks; b += kAddThreads / 32) sum += load(part + static_cast<long long>(b) * H + c);
     }
     s[w][threadIdx.x & 31] = sum;
@@ -468,45 +445,42 @@ spx_status norm_pieces(const NormArgs& a, cudaStream_t st) {
     return spx_cuda_status(norm_launch<V, O, 1>(a, st));
 }
 
-// Rows of a tile and the blocks of the gradient: as many rows as a stage holds, fewer where every block then has one tile.
+// Threads a row (log2), a block's threads, and the blocks of the gradient: three an SM of 256 threads, one of more.
 struct GradShape {
-    int R, tiles, blocks;
+    int log_g, threads, blocks;
 };
-constexpr int kLongRow = 32 * kGradThreads;  // longer ones go to the other kernel
+constexpr int kGradBlocks = 456, kLongRow = kHeld * kMostThreads;
 
-GradShape grad_shape(int M, int H, int row_bytes) {
+GradShape grad_shape(int M, int H) {
     GradShape g{};
-    g.R = H > kLongRow ? 1 : std::max(1, std::min({kMostRows, kStageBytes / row_bytes, (M + kGradBlocks - 1) / kGradBlocks}));
-    g.tiles = (M - 1) / g.R + 1;
-    g.blocks = std::min(g.tiles, H > kLongRow ? kGradBlocks / 2 : kGradBlocks);
+    g.log_g = 2;
+    while ((kHeld << g.log_g) < H && (1 << g.log_g) < kMostThreads) ++g.log_g;
+    g.threads = std::max(kThreads, 1 << g.log_g);
+    const int per = g.threads >> g.log_g;
+    g.blocks = std::min((M - 1) / per + 1, g.threads > kThreads ? kGradBlocks / 3 : kGradBlocks);
     return g;
 }
 
-template <class V, int N, int HELD>
-cudaError_t grad_kernel(GradArgs a, int blocks, cudaStream_t st) {
-    const int np = a.H / N;
-    a.log_c = 0;
-    while ((1 << a.log_c) < np && (1 << a.log_c) < kGradThreads) ++a.log_c;
-    a.log_l = 0;
-    while ((kLaneValues << a.log_l) < a.H && a.log_l < 5) ++a.log_l;
-    a.segs = (a.H + (kLaneValues << a.log_l) - 1) / (kLaneValues << a.log_l);
-    a.dots = (a.segs + 3) / 4 * 4;
-    const size_t smem = 2 * static_cast<size_t>(a.dR ? 3 : 2) * a.R * a.pitch + sizeof(float) * ((a.H + 3) / 4 * 4 + a.R * (a.dots + 2));
-    const cudaError_t e = spx_tc::set_smem_limit(rms_norm_grad_kernel<V, N, HELD>, 227 * 1024);
-    if (e != cudaSuccess) return e;
-    return launch_early(rms_norm_grad_kernel<V, N, HELD>, dim3(blocks), kGradThreads, smem, 1, st, a);
+template <class V, int N, int MAXT, int DEPTH>
+cudaError_t grad_kernel(const GradArgs& a, const GradShape& g, cudaStream_t st) {
+    constexpr size_t ring = static_cast<size_t>(DEPTH) * 3 * kHeld * sizeof(V) * MAXT;
+    const size_t smem = std::max(ring, a.part && g.threads > 1 << g.log_g ? sizeof(float) * a.H : 0);
+    const cudaError_t e = DEPTH > 0 ? spx_tc::set_smem_limit(rms_norm_grad_kernel<V, N, MAXT, DEPTH>, ring) : cudaSuccess;
+    return e != cudaSuccess ? e : launch_early(rms_norm_grad_kernel<V, N, MAXT, DEPTH>, dim3(g.blocks), g.threads, smem, 1, st, a);
 }
 
 template <class V, int N>
 cudaError_t grad_launch(GradArgs a, float* dw, cudaStream_t st) {
-    a.pitch = static_cast<int>((a.H * sizeof(V) + 15) / 16 * 16);
-    const GradShape g = grad_shape(a.M, a.H, (a.dR ? 3 : 2) * a.pitch);
-    a.R = g.R, a.tiles = g.tiles;
+    const GradShape g = grad_shape(a.M, a.H);
+    a.log_g = g.log_g;
     if (a.part && g.blocks == 1) a.part = dw;
     spx_note_launches(a.part && g.blocks > 1 ? 2 : 1);
-    cudaError_t e = a.H > kLongRow            ? launch_early(rms_norm_grad_long_kernel<V, N>, dim3(g.blocks), kMostThreads, 0, 1, st, a)
-                    : a.H <= 16 * kGradThreads ? grad_kernel<V, N, 16>(a, g.blocks, st)
-                                               : grad_kernel<V, N, 32>(a, g.blocks, st);
+    constexpr bool async = N * sizeof(V) >= 4;
+    cudaError_t e;
+    if (g.threads == kThreads) e = grad_kernel<V, N, kThreads, !async ? 0 : sizeof(V) == 2 ? 3 : 1>(a, g, st);
+    else if (g.threads == 512) e = grad_kernel<V, N, 512, !async ? 0 : sizeof(V) == 2 ? 3 : 2>(a, g, st);
+    else if (a.H <= kLongRow) e = grad_kernel<V, N, kMostThreads, async && sizeof(V) == 2 ? 2 : 0>(a, g, st);
+    else e = launch_early(rms_norm_grad_long_kernel<V, N>, dim3(g.blocks), kMostThreads, 0, 1, st, a);
     if (e == cudaSuccess && a.part && g.blocks > 1)
         e = launch_early(add_parts_kernel, dim3((a.H + 31) / 32), kAddThreads, 0, 1, st, a.H, g.blocks, static_cast<const float*>(a.part), dw);
     return e;
@@ -573,7 +547,7 @@ spx_status spx_rms_norm_i8(int32_t M, int32_t H, spx_type type, const void* X, i
 
 size_t spx_rms_norm_grad_scratch_bytes(int32_t M, int32_t H) {
     if (M <= 0 || H <= 0 || H > SPX_NORM_MAX_H || M > kMostIndex) return 0;
-    return M > 1 ? sizeof(float) * static_cast<size_t>(std::min(M, kGradBlocks)) * static_cast<size_t>(H) : 0;
+    return M > 1 ? sizeof(float) * static_cast<size_t>(grad_shape(M, H).blocks) * static_cast<size_t>(H) : 0;
 }
 
 spx_status spx_rms_norm_grad(int32_t M, int32_t H, spx_type type, const void* dY, int64_t lddy, const void* S, int64_t lds,

@@ -77,7 +77,8 @@ __device__ __forceinline__ Pack<V, N> packed(const Floats<N>& f) {
 // N values of type V or (wide) fp32, as fp32.
 template <class V, int N>
 __device__ __forceinline__ Floats<N> load_floats(const void* p, bool wide, long long at) {
-    if (!wide) return floats(load(reinterpret_cast<const Pack<V, N>*>(static_cast<const V*>(p) + at)));
+    if constexpr (N * sizeof(V) <= 16)
+        if (!wide) return floats(load(reinterpret_cast<const Pack<V, N>*>(static_cast<const V*>(p) + at)));
     constexpr int Q = N < 4 ? N : 4;
     Floats<N> f;
 #pragma unroll
@@ -90,16 +91,21 @@ __device__ __forceinline__ Floats<N> load_floats(const void* p, bool wide, long 
 }
 
 // Sum (or maximum, as unsigned numbers) over the G threads of a group, G a power of two; groups of several warps meet in
-// `s` (a word a warp) and the whole block has to call.
+// `s` (a word a warp, on a 16-byte boundary) and the whole block has to call.
 __device__ __forceinline__ float group_sum(float v, int G, float* s) {
     for (int d = (G < 32 ? G : 32) >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     if (G <= 32) return v;
     const int w = threadIdx.x >> 5, per = G >> 5, w0 = w & -per;
     if ((threadIdx.x & 31) == 0) s[w] = v;
     __syncthreads();
-    v = 0.f;
-    for (int i = 0; i < per; ++i) v += s[w0 + i];
-    return v;
+    if (per < 4) return per == 1 ? v : s[w0] + s[w0 + 1];
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < per; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(s + w0 + i);
+        t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+    }
+    return (t.x + t.y) + (t.z + t.w);
 }
 __device__ __forceinline__ uint32_t group_max(uint32_t v, int G, uint32_t* s) {
     for (int d = (G < 32 ? G : 32) >> 1; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
