@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "spx_rows.cuh"
+#include "spx_tc.cuh"
 
 using namespace spx_rows;
 
@@ -70,132 +71,197 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---------------------------------------------------------------- tokens by id
 
-constexpr int kOrderThreads = 512, kOrderWarps = kOrderThreads / 32;
-constexpr int kMostIds = 4096;   // ids a block owns
-constexpr int kList = 2048;      // tokens of its ids that a block holds in shared memory
+// A block owns `per` ids and looks at 16384 tokens at a time, 512 consecutive ones a warp, of which it takes those of its
+// ids: a warp's go to a list of its own, in order.  Of one id among 32 neighbours of that list match_any finds the lanes;
+// with counters per id of its own the warp so knows each token's rank in its list, and the counters of the warps before it
+// and the counts of lower ids give the place.  Of more than 16384 tokens the block's go to a list of the block first, in
+// order; where they do not fit it, all are read once more.  No floating-point and no order that depends on timing: the
+// atomics are whole sums.  Nearly all of a block's work is passing over other blocks' tokens, so that is what is kept
+// short; the other loops stay loops, since unrolled the kernel took longer to fetch its code than to run it.
+constexpr int kOrderThreads = 1024, kOrderWarps = kOrderThreads / 32, kSlots = 16, kRun = 32 * kSlots, kBatch = kOrderWarps * kRun;
+constexpr int kMostIds = 1024, kList = 4096;  // a warp's word: 10 bits of the id, 9 of the place in its run, 9 of the rank
 
 struct OrderArgs {
     Ids x;
-    int T, per, padding;       // ids a block
-    int *order, *sid, *list;   // sorted tokens and their ids; a block's tokens before they are sorted, where they do not fit
-    int* kept;                 // tokens in all that have a row
-    void* dW;                  // NULL: no zeros are written
-    long long ldw;             // bytes
-    long long row;             // bytes a row
+    int T, per, padding;
+    int *order, *sid;   // sorted tokens and their ids
+    int* kept;          // tokens in all that have a row
+    void* dW;           // NULL: no zeros are written
+    long long ldw, row; // bytes
+    int zero_bytes;     // the widest word that rows are made of
 };
 
-// Z: the widest word that rows are made of.
+// Zeros in a block's rows without tokens, a warp a row; bit i of empty[j]: row 32 j + i.
 template <class Z>
-__global__ void __launch_bounds__(kOrderThreads, 2) embed_order_kernel(OrderArgs a) {
-    __shared__ int s_at[kMostIds + 1];  // counts, then first places
-    __shared__ int s_list[kList], s_lid[kList];
-    __shared__ int s_warp[kOrderWarps], s_below[kOrderWarps], s_next;
+__device__ __forceinline__ void fill_rows(const OrderArgs& a, long long v0, int nv, const uint32_t* empty) {
+    const int lane = threadIdx.x & 31, words = static_cast<int>(a.row / sizeof(Z));
+    Z zero;
+    memset(&zero, 0, sizeof(Z));
+    for (int i = threadIdx.x >> 5; i < nv; i += kOrderWarps) {
+        if (!(empty[i >> 5] >> (i & 31) & 1u)) continue;
+        Z* q = reinterpret_cast<Z*>(static_cast<char*>(a.dW) + (v0 + i) * a.ldw);
+        for (int c = lane; c < words; c += 32) __stcs(q + c, zero);
+    }
+}
+
+// Sums of the warps before warp w and of all 32, from a word a warp.
+__device__ __forceinline__ int2 warps_before(const int* s, int w) {
+    const int own = s[threadIdx.x & 31];
+    int up = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, up, d);
+        if (static_cast<int>(threadIdx.x & 31) >= d) up += o;
+    }
+    return make_int2(__shfl_sync(0xffffffffu, up - own, w), __shfl_sync(0xffffffffu, up, 31));
+}
+
+__global__ void __launch_bounds__(kOrderThreads, 1) embed_order_kernel(OrderArgs a) {
+    // the warps' lists (kRun each), the block's list (tokens, then ids), places of the block's ids (per), a counter for each
+    // warp and id (16 bits, pitch odd)
+    extern __shared__ int sm[];
+    __shared__ int s_below[kOrderWarps], s_carry[kOrderWarps], s_found[2][kOrderWarps];
+    __shared__ uint32_t s_empty[kOrderWarps];
     let_next_start();
     wait_for_previous();
     a.x.p = behind_wait(a.x.p);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long first = static_cast<long long>(blockIdx.x) * a.per;
-    const int v0 = static_cast<int>(min(first, static_cast<long long>(a.x.V))), nv = min(a.per, a.x.V - v0);
-    for (int i = threadIdx.x; i <= nv; i += kOrderThreads) s_at[i] = 0;
-    if (threadIdx.x == 0) s_next = 0;
-    __syncthreads();
-    // each warp looks at a run of consecutive tokens
-    const int run = ((a.T + kOrderThreads - 1) / kOrderThreads) * 32, t0 = min(w * static_cast<long long>(run), static_cast<long long>(a.T)), t1 = min(static_cast<long long>(t0) + run, static_cast<long long>(a.T));
-    auto local = [&](int t) {  // the token's id in this block's range, -1: another's (lower: below the range), or none
-        const int id = t < t1 ? id_of(a.x, t) : -1;
-        return id == a.padding ? -1 : id;
+    const unsigned lower = (1u << lane) - 1u;
+    const int v0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * a.per, static_cast<long long>(a.x.V))), nv = min(a.per, a.x.V - v0);
+    int *own = sm + w * kRun, *list = sm + kBatch, *place = list + 2 * kList;
+    uint16_t* counters = reinterpret_cast<uint16_t*>(place + a.per);
+    const int pitch = (a.per + 1) | 1;
+    uint16_t* mine = counters + w * pitch;
+    int below = 0;  // this lane's tokens of lower ids
+    // the warp's tokens of this block's ids: the id, and above it the place in the run; how many
+    auto read = [&](int base, bool count) {
+        const long long t0 = static_cast<long long>(base) + w * kRun + lane;
+        constexpr int kAhead = 8;  // loads in flight; past the end the last token again: no branch between them
+        int taken = 0;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kSlots; i0 += kAhead) {
+            long long v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const long long t = min(t0 + 32 * (i0 + i), a.T - 1LL);
+                v[i] = a.x.bytes == 4 ? load(static_cast<const int*>(a.x.p) + t) : load(static_cast<const long long*>(a.x.p) + t);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) asm volatile("" : "+l"(v[i]));
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const bool on = static_cast<unsigned long long>(v[i]) < static_cast<unsigned>(a.x.V) && static_cast<int>(v[i]) != a.padding &&
+                                t0 + 32 * (i0 + i) < a.T;
+                const int id = static_cast<int>(v[i]) - v0;
+                const bool in = on && static_cast<unsigned>(id) < static_cast<unsigned>(nv);
+                below += on && id < 0 && count;
+                const unsigned who = __ballot_sync(0xffffffffu, in);
+                if (!who) continue;
+                if (in) {
+                    own[taken + __popc(who & lower)] = id | (32 * (i0 + i) + lane) << 16;
+                    if (count) atomicAdd(place + id, 1);
+                }
+                taken += __popc(who);
+            }
+        }
+        __syncwarp();
+        return taken;
     };
-    int below = 0, mine = 0;
-    for (int t = t0; t < t1; t += 128) {
-        int id[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) id[u] = local(t + 32 * u + lane);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const bool in = id[u] >= v0 && id[u] < v0 + nv;
-            if (in) atomicAdd(s_at + id[u] - v0, 1);
-            mine += in;
-            below += id[u] >= 0 && id[u] < v0;
-        }
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        mine += __shfl_xor_sync(0xffffffffu, mine, d);
-        below += __shfl_xor_sync(0xffffffffu, below, d);
-    }
-    if (lane == 0) s_warp[w] = mine, s_below[w] = below;
+    if (static_cast<int>(threadIdx.x) < nv) place[threadIdx.x] = 0;
     __syncthreads();
-    int all = 0, before = 0;
-    below = 0;
-#pragma unroll
-    for (int i = 0; i < kOrderWarps; ++i) {
-        before += i < w ? s_warp[i] : 0;
-        all += s_warp[i];
-        below += s_below[i];
-    }
-    const bool held = all <= kList;
-    if (mine) {  // this warp's tokens to the block's list, in order
-        int at = before;
-        for (int t = t0; t < t1; t += 32) {
-            const int id = local(t + lane);
-            const bool in = id >= v0 && id < v0 + nv;
-            const unsigned who = __ballot_sync(0xffffffffu, in);
-            const int to = at + __popc(who & ((1u << lane) - 1u));
-            if (in) {
-                if (held) s_list[to] = t + lane, s_lid[to] = id - v0;
-                else a.list[below + to] = t + lane;
+    const bool once = a.T <= kBatch;
+    int taken = 0, found = 0, turn = 0;  // found: tokens of this block in the batches so far
+    for (int base = 0; a.T > 0; turn ^= 1) {
+        taken = read(base, true);
+        if (!once) {
+            if (lane == 0) s_found[turn][w] = taken;
+            __syncthreads();
+            const int2 f = warps_before(s_found[turn], w);
+            for (int i = lane; i < taken; i += 32) {
+                const int to = found + f.x + i;
+                if (to < kList) list[to] = base + w * kRun + (own[i] >> 16), list[kList + to] = own[i] & 0xffff;
             }
-            at += __popc(who);
+            __syncwarp();
+            found += f.y;
         }
+        if (a.T - base <= kBatch) break;
+        base += kBatch;
     }
-    // counts to first places, by the first warp
-    __syncthreads();
-    if (w == 0) {
-        int carry = 0;
-        for (int i0 = 0; i0 <= nv; i0 += 32) {
-            const int n = i0 + lane < nv ? s_at[i0 + lane] : 0;
-            int inc = n;
+    const bool listed = !once && found <= kList;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, inc, d);
-                if (lane >= d) inc += up;
-            }
-            if (i0 + lane <= nv) s_at[i0 + lane] = carry + inc - n;
-            carry += __shfl_sync(0xffffffffu, inc, 31);
-        }
-        if (lane == 0 && blockIdx.x == gridDim.x - 1) *a.kept = below + all;
-    }
+    for (int d = 16; d > 0; d >>= 1) below += __shfl_xor_sync(0xffffffffu, below, d);
+    if (lane == 0) s_below[w] = below;
+    for (int i = threadIdx.x; i < (kOrderWarps * pitch + 1) / 2; i += kOrderThreads) reinterpret_cast<int*>(counters)[i] = 0;
     __syncthreads();
-    if (a.dW) {  // zeros, a warp a row
-        char* dW = static_cast<char*>(a.dW) + v0 * a.ldw;
-        for (int i = w; i < nv; i += kOrderWarps) {
-            if (s_at[i] != s_at[i + 1]) continue;
-            Z* q = reinterpret_cast<Z*>(dW + i * a.ldw);
-            Z zero;
-            memset(&zero, 0, sizeof(Z));
-            for (int c = lane; c < a.row / static_cast<int>(sizeof(Z)); c += 32) q[c] = zero;
+    // counts to first places: a warp's 32 ids, then the warps before it
+    const int n = static_cast<int>(threadIdx.x) < nv ? place[threadIdx.x] : 0;
+    int inc = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += up;
+    }
+    if (lane == 31) s_carry[w] = inc;
+    const uint32_t none = __ballot_sync(0xffffffffu, n == 0);
+    if (lane == 0) s_empty[w] = none;
+    __syncthreads();
+    below = warps_before(s_below, 0).y;
+    const int2 carry = warps_before(s_carry, w);
+    if (static_cast<int>(threadIdx.x) < nv) place[threadIdx.x] = below + carry.x + inc - n;
+    if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1) *a.kept = below + carry.y;
+    for (int base = 0; a.T > 0;) {
+        if (listed) {  // the block's list in runs
+            taken = max(0, min(kRun, found - w * kRun));
+            for (int i = lane; i < taken; i += 32) own[i] = list[kList + w * kRun + i] | i << 16;
+            __syncwarp();
+        } else if (!once) {
+            taken = read(base, false);
+        }
+        // the ranks among the warp's tokens of an id, above the place in the run
+#pragma unroll 1
+        for (int i0 = 0; i0 < taken; i0 += 32) {
+            const bool on = i0 + lane < taken;
+            const int word = on ? own[i0 + lane] : 0, id = on ? word & 0x3ff : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, id), before = same & lower;
+            if (on) own[i0 + lane] = word >> 16 << 10 | id | (mine[id] + __popc(before)) << 19;
+            __syncwarp();
+            if (on && before == 0) mine[id] += static_cast<uint16_t>(__popc(same));
+            __syncwarp();
         }
         __syncthreads();
-    }
-    if (w != 0) return;
-    for (int i0 = 0; i0 < all; i0 += 32) {
-        const int i = i0 + lane;
-        int t = 0, l = -1 - lane;
-        if (i < all) {
-            if (held) t = s_list[i], l = s_lid[i];
-            else t = a.list[below + i], l = id_of(a.x, t) - v0;
+        int sum = 0;  // an id's tokens in this batch
+        if (n > 0) {
+            uint16_t* c = counters + threadIdx.x;
+#pragma unroll 1
+            for (int i = 0; i < kOrderWarps; i += 8) {
+                int k[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) k[j] = c[(i + j) * pitch];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    c[(i + j) * pitch] = static_cast<uint16_t>(sum);
+                    sum += k[j];
+                }
+            }
         }
-        const unsigned same = __match_any_sync(0xffffffffu, l), lower = same & ((1u << lane) - 1u);
-        int to = 0;
-        if (i < all) to = s_at[l] + __popc(lower);
-        __syncwarp();
-        if (i < all) {
-            if (lower == 0) s_at[l] += __popc(same);
-            a.order[below + to] = t;
-            a.sid[below + to] = l + v0;
+        __syncthreads();
+        for (int i = lane; i < taken; i += 32) {
+            const int word = own[i], id = word & 0x3ff, at = word >> 10 & 0x1ff, to = place[id] + mine[id] + (word >> 19);
+            a.order[to] = listed ? list[w * kRun + at] : base + w * kRun + at;
+            a.sid[to] = id + v0;
         }
-        __syncwarp();
+        if (listed || a.T - base <= kBatch) break;
+        base += kBatch;
+        __syncthreads();
+        if (n > 0) place[threadIdx.x] += sum;
+        for (int i = threadIdx.x; i < (kOrderWarps * pitch + 1) / 2; i += kOrderThreads) reinterpret_cast<int*>(counters)[i] = 0;
+        __syncthreads();
     }
+    if (!a.dW) return;
+    if (a.zero_bytes == 16) fill_rows<uint4>(a, v0, nv, s_empty);
+    else if (a.zero_bytes == 8) fill_rows<uint2>(a, v0, nv, s_empty);
+    else if (a.zero_bytes == 4) fill_rows<uint32_t>(a, v0, nv, s_empty);
+    else fill_rows<uint16_t>(a, v0, nv, s_empty);
 }
 
 // ---------------------------------------------------------------- sums
@@ -228,75 +294,91 @@ __device__ __forceinline__ void write_sum(const SumArgs& a, int id, int v, const
     }
 }
 
-constexpr int kRows = 8;  // rows in flight
+constexpr int kRows = 8, kSets = 3, kMostChunk = 1024;
 
-// A warp's lanes hold the tokens and ids of 32 sorted places, the next 32 on their way.
+// A thread's pieces of eight rows are a set: one set is added while two are on their way into the thread's own slots of
+// shared memory (pieces of 2 bytes, which no asynchronous copy takes, through registers).  The loop over a set stays a
+// loop: with the sets in registers and the end of an id unrolled into each of their rows, the kernel fetched code for
+// longer than it added.
 template <class V, class O, int N>
-__global__ void __launch_bounds__(kThreads, 3) embed_sum_kernel(SumArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(SumArgs a) {
     constexpr int X = (N + 1) / 2;
     using Piece = Pack<V, N>;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ int s_id[kMostChunk + 2], s_at[kMostChunk];  // ids of the chunk's places, of the one before and the one after; tokens
     let_next_start();
     wait_for_previous();
     const int *order = behind_wait(a.order), *sid = behind_wait(a.sid);
-    const int lane = threadIdx.x & 31, v = min(static_cast<int>(blockIdx.y * kThreads + threadIdx.x), a.np - 1);
-    const bool mine = static_cast<int>(blockIdx.y * kThreads + threadIdx.x) < a.np;
     const long long first = static_cast<long long>(blockIdx.x) * a.chunk;
     const int p0 = static_cast<int>(first), most = static_cast<int>(min(first + a.chunk, static_cast<long long>(a.T)));
     // places past the last token's hold anything: they are looked at with the number of tokens in hand
-    int next_id = p0 + lane < most ? load(sid + p0 + lane) : -1, next_at = p0 + lane < most ? load(order + p0 + lane) : 0;
-    const int left = p0 > 0 ? load(sid + p0 - 1) : -1, right = most < a.T ? load(sid + most) : -1;
-    const int n = load(behind_wait(a.kept));
-    if (p0 >= n) return;
-    const int p1 = min(most, n);
+    for (int i = threadIdx.x; i < most - p0 + 2; i += kThreads) {
+        const int p = p0 - 1 + i;
+        s_id[i] = p >= 0 && p < a.T ? load(sid + p) : -1;
+        if (i < most - p0) s_at[i] = load(order + p0 + i);
+    }
+    const int kept = load(behind_wait(a.kept)), n = min(most, kept) - p0;  // n: places of this chunk
+    const int v = blockIdx.y * kThreads + threadIdx.x;
+    __syncthreads();
+    if (n <= 0 || v >= a.np) return;
     const V* dY = behind_wait(static_cast<const V*>(a.dY)) + static_cast<long long>(v) * N;
-    int id = __shfl_sync(0xffffffffu, next_id, 0);
-    bool open = p0 > 0 && left == id;  // the current id began before the chunk
+    O* dW = static_cast<O*>(a.dW) + static_cast<long long>(v) * N;
+    Piece* slots = reinterpret_cast<Piece*>(ring) + threadIdx.x;
+    auto fetch = [&](int p, int set) {
+        const int rows = min(kRows, n - p);
+        if constexpr (sizeof(Piece) >= 4) {
+#pragma unroll 4
+            for (int u = 0; u < rows; ++u) copy_piece(slots + (set * kRows + u) * kThreads, reinterpret_cast<const Piece*>(dY + s_at[p + u] * a.lddy));
+        } else {
+            Piece x[kRows];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) x[u] = load(reinterpret_cast<const Piece*>(dY + s_at[max(0, min(p + u, n - 1))] * a.lddy));
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) write_piece(slots + (set * kRows + u) * kThreads, stay(x[u]));
+        }
+        if (a.add)  // what the sums will be added to
+            for (int u = 0; u < rows; ++u) asm volatile("prefetch.global.L2 [%0];" ::"l"(dW + s_id[p + u + 1] * a.ldw));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    bool open = p0 > 0 && s_id[0] == s_id[1];  // the current id began before the chunk
     Floats<N> acc;
 #pragma unroll
     for (int i = 0; i < X; ++i) acc.v[i] = make_float2(0.f, 0.f);
-    auto keep = [&](int which) {
-        if (!mine) return;
-        constexpr int Q = N < 4 ? N : 4;
-        Pack<float, Q>* q = reinterpret_cast<Pack<float, Q>*>(a.part + (2LL * blockIdx.x + which) * a.ldp + static_cast<long long>(v) * N);
+    for (int i = 0; i < kSets - 1; ++i) fetch(i * kRows, i);
+    int set = 0;
+    for (int p = 0; p < n; p += kRows) {
+        fetch(p + (kSets - 1) * kRows, set == 0 ? kSets - 1 : set - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kSets - 1) : "memory");
+        const Piece* x = slots + set * kRows * kThreads;
+#pragma unroll 1
+        for (int u = 0; u < min(kRows, n - p); ++u, x += kThreads) {
+            const Floats<N> f = floats(read_piece(x));
 #pragma unroll
-        for (int i = 0; i < N / Q; ++i) {
-            Floats<Q> f;
+            for (int i = 0; i < X; ++i) acc.v[i] = __fadd2_rn(acc.v[i], f.v[i]);
+            const int id = s_id[p + u + 1], end = p + u + 1 == n;
+            if (!end && s_id[p + u + 2] == id) continue;
+            // the id ends here, or the chunk does
+            const bool on = end && p0 + n < kept && s_id[n + 1] == id;
+            if (open || on) {
+                constexpr int Q = N < 4 ? N : 4;
+                Pack<float, Q>* q = reinterpret_cast<Pack<float, Q>*>(a.part + (2LL * blockIdx.x + !open) * a.ldp + static_cast<long long>(v) * N);
 #pragma unroll
-            for (int j = 0; j < (Q + 1) / 2; ++j) f.v[j] = acc.v[(Q + 1) / 2 * i + j];
-            write_piece(q + i, packed<float, Q>(f));
-        }
-    };
-    for (int base = p0; base < p1; base += 32) {
-        const int my_id = next_id, my_at = next_at;
-        if (base + 32 + lane < p1) next_id = load(sid + base + 32 + lane), next_at = load(order + base + 32 + lane);
-        for (int u0 = 0; u0 < 32 && base + u0 < p1; u0 += kRows) {
-            Piece x[kRows];
+                for (int i = 0; i < N / Q; ++i) {
+                    Floats<Q> part;
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const int t = __shfl_sync(0xffffffffu, my_at, u0 + u);
-                if (base + u0 + u < p1) x[u] = load_once(reinterpret_cast<const Piece*>(dY + t * a.lddy));
-            }
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const int next = __shfl_sync(0xffffffffu, my_id, u0 + u);
-                if (base + u0 + u >= p1) continue;
-                if (next != id) {
-                    if (open) keep(0);
-                    else if (mine) write_sum<O, N>(a, id, v, acc);
-                    open = false;
-                    id = next;
-#pragma unroll
-                    for (int i = 0; i < X; ++i) acc.v[i] = make_float2(0.f, 0.f);
+                    for (int j = 0; j < (Q + 1) / 2; ++j) part.v[j] = acc.v[(Q + 1) / 2 * i + j];
+                    write_piece(q + i, packed<float, Q>(part));
                 }
-                const Floats<N> f = floats(x[u]);
-#pragma unroll
-                for (int i = 0; i < X; ++i) acc.v[i] = __fadd2_rn(acc.v[i], f.v[i]);
+            } else {
+                write_sum<O, N>(a, id, v, acc);
             }
+            open = false;
+#pragma unroll
+            for (int i = 0; i < X; ++i) acc.v[i] = make_float2(0.f, 0.f);
         }
+        set = set == kSets - 1 ? 0 : set + 1;
     }
-    if (open) keep(0);
-    else if (p1 < n && right == id) keep(1);
-    else if (mine) write_sum<O, N>(a, id, v, acc);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // One block for each chunk whose last id began in it and goes on after it.
@@ -326,7 +408,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(SumArgs a) {
     part += 2LL * blockIdx.x * a.ldp + static_cast<long long>(v) * N;
     auto row = [&](const float* p) { return load_floats<float, N>(p, true, 0); };
     acc = row(part + a.ldp);
-#pragma unroll 8
+#pragma unroll 16
     for (int c = 1; c <= chunks; ++c) {
         const Floats<N> f = row(part + 2LL * c * a.ldp);
 #pragma unroll
@@ -363,29 +445,38 @@ spx_status embed(int T, int H, Ids x, const void* W, int64_t ldw, float scale, v
     return spx_cuda_status(embed_launch<V, 1>(T, H, x, W, ldw, scale, Y, ldy, st));
 }
 
-// Sorted tokens a chunk: 8 to 32, so that the chunks fill the SMs, more where there would be over 4096 of them.
-int chunk_of(int T) { return std::max(std::min(32, (T / 512 + 7) / 8 * 8 + 8), (T + 4095) / 4096); }
+// Sorted tokens a chunk: as many chunks as run at once, of 8 to 1024 tokens.
+constexpr int kSumBlocks = 304;
+int chunk_of(int T, int H) {
+    const long long tiles = (H + kThreads * 8 - 1) / (kThreads * 8);  // of 16-byte pieces of two-byte values
+    return static_cast<int>(std::min<long long>(kMostChunk, std::max(8LL, (T * tiles + kSumBlocks - 1) / kSumBlocks)));
+}
 
 struct Scratch {
-    size_t order, sid, list, kept, part, bytes;
+    size_t order, sid, kept, part, bytes;
     long long ldp;
 };
 Scratch scratch_of(int T, int H) {
     Scratch s{};
     const size_t ints = (static_cast<size_t>(T) * 4 + 15) / 16 * 16;
-    s.order = 0, s.sid = ints, s.list = 2 * ints, s.kept = 3 * ints, s.part = 3 * ints + 16;
+    s.order = 0, s.sid = ints, s.kept = 2 * ints, s.part = 2 * ints + 16;
     s.ldp = (static_cast<long long>(H) + 3) / 4 * 4;
-    const size_t chunks = (static_cast<size_t>(T) + chunk_of(T) - 1) / chunk_of(T);
+    const size_t chunk = chunk_of(T, H), chunks = (T + chunk - 1) / chunk;
     s.bytes = s.part + chunks * 2 * static_cast<size_t>(s.ldp) * sizeof(float);
     return s;
 }
 
 template <class V, class O, int N>
-cudaError_t sums(const SumArgs& a, int T, cudaStream_t st) {
-    const dim3 grid((T + a.chunk - 1) / a.chunk, (a.np + kThreads - 1) / kThreads);
-    if (grid.y > 65535) return cudaErrorInvalidValue;
-    const cudaError_t e = launch_early(embed_sum_kernel<V, O, N>, grid, kThreads, 0, 1, st, a);
-    return e != cudaSuccess ? e : launch_early(embed_join_kernel<O, N>, grid, kThreads, 0, 1, st, a);
+cudaError_t sums(SumArgs a, int T, cudaStream_t st) {
+    const unsigned chunks = (T + a.chunk - 1) / a.chunk, tiles = (a.np + kThreads - 1) / kThreads;
+    constexpr size_t ring = sizeof(V) * N * kSets * kRows * kThreads;
+    cudaError_t e = spx_tc::set_smem_limit(embed_sum_kernel<V, O, N>, ring);
+    if (e == cudaSuccess) e = launch_early(embed_sum_kernel<V, O, N>, dim3(chunks, tiles), kThreads, ring, 1, st, a);
+    if (e != cudaSuccess || chunks < 2) return e;
+    // the kept sums in pieces of four: more threads, each with more of them in flight
+    constexpr int J = N < 4 ? N : 4;
+    a.np = a.np * (N / J);
+    return launch_early(embed_join_kernel<O, J>, dim3(chunks, (a.np + kThreads - 1) / kThreads), kThreads, 0, 1, st, a);
 }
 
 template <class V, class O>
@@ -437,6 +528,7 @@ spx_status spx_embed_grad(int32_t T, int32_t H, int32_t V, spx_type type, const 
     const spx_status c = check(T, H, V, type, id_bytes);
     if (c != SPX_OK) return c;
     if (w_type != type && w_type != SPX_F32) return SPX_ERR_ARG;
+    if (H > 65535 * kThreads) return SPX_ERR_UNSUPPORTED;
     if (H == 0 || V == 0 || (T == 0 && accumulate)) return SPX_OK;
     if (!dW || lddw < H || (T > 0 && (!ids || !dY || lddy < H))) return SPX_ERR_ARG;
     if (!scratch || scratch_bytes < spx_embed_grad_scratch_bytes(T, H)) return SPX_ERR_ARG;
@@ -450,21 +542,21 @@ spx_status spx_embed_grad(int32_t T, int32_t H, int32_t V, spx_type type, const 
     o.x = Ids{ids, id_bytes, V};
     o.T = T, o.padding = padding;
     o.order = reinterpret_cast<int*>(base + s.order), o.sid = reinterpret_cast<int*>(base + s.sid);
-    o.list = reinterpret_cast<int*>(base + s.list), o.kept = reinterpret_cast<int*>(base + s.kept);
+    o.kept = reinterpret_cast<int*>(base + s.kept);
     o.dW = accumulate ? nullptr : dW;
     o.ldw = static_cast<long long>(lddw * wb), o.row = static_cast<long long>(H * wb);
-    const int blocks = std::max(304, (V + kMostIds - 1) / kMostIds);
+    o.zero_bytes = copy_width(addr(dW) | static_cast<uint64_t>(o.ldw) | static_cast<uint64_t>(o.row), static_cast<int>(wb));
+    const int blocks = std::max(152, (V + kMostIds - 1) / kMostIds);
     o.per = (V + blocks - 1) / blocks;
     const dim3 grid((V + o.per - 1) / o.per);
-    const int zb = copy_width(addr(dW) | o.ldw | o.row, static_cast<int>(wb));
-    spx_note_launches(3);
-    cudaError_t e = zb == 16  ? launch_early(embed_order_kernel<uint4>, grid, kOrderThreads, 0, 1, st, o)
-                    : zb == 8 ? launch_early(embed_order_kernel<uint2>, grid, kOrderThreads, 0, 1, st, o)
-                    : zb == 4 ? launch_early(embed_order_kernel<uint32_t>, grid, kOrderThreads, 0, 1, st, o)
-                              : launch_early(embed_order_kernel<uint16_t>, grid, kOrderThreads, 0, 1, st, o);
+    const bool joins = T > chunk_of(T, H);
+    spx_note_launches(T == 0 ? 1 : joins ? 3 : 2);
+    const size_t smem = sizeof(int) * (kBatch + 2 * kList + o.per) + sizeof(uint16_t) * (kOrderWarps * ((o.per + 1) | 1) + 2);
+    cudaError_t e = spx_tc::set_smem_limit(embed_order_kernel, 200 * 1024);
+    if (e == cudaSuccess) e = launch_early(embed_order_kernel, grid, kOrderThreads, smem, 1, st, o);
     if (e != cudaSuccess || T == 0) return spx_cuda_status(e);
     SumArgs a{};
-    a.chunk = chunk_of(T), a.T = T;
+    a.chunk = chunk_of(T, H), a.T = T;
     a.order = o.order, a.sid = o.sid, a.kept = o.kept;
     a.dY = dY, a.lddy = lddy, a.dW = dW, a.ldw = lddw;
     a.part = reinterpret_cast<float*>(base + s.part), a.ldp = s.ldp;

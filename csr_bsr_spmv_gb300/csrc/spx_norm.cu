@@ -167,13 +167,6 @@ struct GradArgs {
     bool wide_w;  // the weights are fp32
 };
 
-template <class P>
-__device__ __forceinline__ void copy_piece(P* to, const P* from) {
-    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-    if constexpr (sizeof(P) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(sizeof(P) < 4 ? 4 : sizeof(P)) : "memory");
-}
-
 // DEPTH 0 (pieces of 2 bytes, which no copy takes, and rows that leave no room): loaded where they are needed.
 template <class V, int N, int MAXT, int DEPTH>
 __global__ void __launch_bounds__(MAXT, MAXT == kThreads ? 3 : 1) rms_norm_grad_kernel(GradArgs a) {

@@ -38,6 +38,33 @@ __device__ __forceinline__ void write_once(P* p, const P& v) {
     __stcs(reinterpret_cast<T*>(p), w);
 }
 
+// A piece of 4, 8 or 16 bytes to shared memory, asynchronously.
+template <class P>
+__device__ __forceinline__ void copy_piece(P* to, const P* from) {
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if constexpr (sizeof(P) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(sizeof(P) < 4 ? 4 : sizeof(P)) : "memory");
+}
+
+// The piece itself, loaded by now: the compiler would otherwise move a load down to where its value is used, and loads
+// meant to be in flight together would wait for one another.
+template <class P>
+__device__ __forceinline__ P stay(P p) {
+    if constexpr (sizeof(P) >= 4) {
+        uint32_t w[sizeof(P) / 4];
+        memcpy(w, &p, sizeof(P));
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(P) / 4); ++i) asm volatile("" : "+r"(w[i]));
+        memcpy(&p, w, sizeof(P));
+    } else {
+        uint16_t w;
+        memcpy(&w, &p, sizeof(P));
+        asm volatile("" : "+h"(w));
+        memcpy(&p, &w, sizeof(P));
+    }
+    return p;
+}
+
 // A piece's values as fp32 in pairs (N == 1: one value and a zero), and back.
 template <int N>
 struct Floats {

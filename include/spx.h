@@ -1037,9 +1037,9 @@ spx_status spx_embed(int32_t T, int32_t H, int32_t V, spx_type type, const void*
  * w_type (`type` or SPX_F32).  Ids outside [0, V), and the id `padding` (-1:
  * none), add nothing.  accumulate 0: every row of dW is written, zeros where no
  * token has its id; 1: the sums are added to dW, whose other rows are not
- * touched.
+ * touched.  Rows of up to 16776960 values (SPX_ERR_UNSUPPORTED beyond).
  *   scratch: spx_embed_grad_scratch_bytes(T, H) bytes, 16-byte aligned.
- * Launches: 3 (none for T == 0 with accumulate).
+ * Launches: 1 to 3 (none for T == 0 with accumulate).
  */
 size_t spx_embed_grad_scratch_bytes(int32_t T, int32_t H);
 spx_status spx_embed_grad(int32_t T, int32_t H, int32_t V, spx_type type, const void* ids, int32_t id_bytes, int32_t padding,

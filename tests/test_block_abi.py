@@ -53,8 +53,8 @@ def test_rms_norm_grad_refuses(change, status):
 def test_rms_norm_grad_scratch_bytes():
     need = spx._lib().spx_rms_norm_grad_scratch_bytes
     assert need(1, 4096) == need(0, 64) == need(-1, 64) == need(64, 0) == need(64, 32769) == 0
-    assert 0 < need(100000, 4096) <= 304 * 4096 * 4
-    assert 0 < need(BIG - (1 << 23), 32768) <= 304 * 32768 * 4
+    assert 0 < need(100000, 4096) <= 456 * 4096 * 4
+    assert 0 < need(BIG - (1 << 23), 32768) <= 456 * 32768 * 4
 
 
 @pytest.mark.parametrize("change,status", [
@@ -84,7 +84,7 @@ def test_embed_refuses(change, status):
 
 
 @pytest.mark.parametrize("change,status", [
-    ({0: -1}, ARG), ({1: -1}, ARG), ({2: -1}, ARG), ({2: BIG}, RANGE), ({3: 3}, ARG), ({4: None}, ARG), ({5: 2}, ARG),
+    ({0: -1}, ARG), ({1: -1}, ARG), ({2: -1}, ARG), ({2: BIG}, RANGE), ({1: 1 << 24}, UNSUP), ({3: 3}, ARG), ({4: None}, ARG), ({5: 2}, ARG),
     ({8: None}, ARG), ({9: 63}, ARG), ({10: None}, ARG), ({11: 63}, ARG), ({12: 2}, ARG), ({14: None}, ARG), ({15: 100}, ARG),
     ({4: ODD}, ALIGN), ({8: ODD}, ALIGN), ({10: ODD}, ALIGN), ({14: ODD}, ALIGN)])
 def test_embed_grad_refuses(change, status):
@@ -93,9 +93,9 @@ def test_embed_grad_refuses(change, status):
 
 def test_embed_grad_scratch_bytes():
     need = spx._lib().spx_embed_grad_scratch_bytes
-    assert need(-1, 4) == need(4, -1) == need(BIG, 4) == 0
-    assert need(0, 64) > 0 and need(16384, 2048) >= 3 * 4 * 16384
-    assert need(1 << 30, 8192) > 1 << 32
+    assert need(-1, 4) == need(4, -1) == need(BIG, 4) == need(4, BIG) == 0
+    assert need(0, 64) > 0 and need(16384, 2048) >= 2 * 4 * 16384
+    assert need(1 << 30, 8192) > 1 << 33
 
 
 def test_sizes_of_zero_launch_nothing():
