@@ -41,30 +41,40 @@ __device__ __forceinline__ int id_of(const Ids& x, int t) {
 constexpr int kTokens = 4;  // a group's tokens: their rows are in flight together
 
 // Groups of G threads, G a power of two; grid.y splits the rows.
-template <class V, int N>
+template <class V, int N, bool ANY>
 __global__ void __launch_bounds__(kThreads)
-    embed_kernel(Ids x, int T, int np, int log_g, const V* W, long long ldw, float scale, V* Y, long long ldy) {
-    using Piece = Pack<V, N>;
+    embed_kernel(Ids x, int T, int H, int log_g, const V* W, long long ldw, float scale, V* Y, long long ldy) {
     let_next_start();
     wait_for_previous();
     x.p = behind_wait(x.p);
     W = behind_wait(W);
-    const int G = 1 << log_g, t0 = (blockIdx.x * (kThreads >> log_g) + (threadIdx.x >> log_g)) * kTokens;
+    const Rows<V, N, ANY> rows{H};
+    const int G = 1 << log_g, np = rows.pieces(), at = threadIdx.x & (G - 1), t0 = (blockIdx.x * (kThreads >> log_g) + (threadIdx.x >> log_g)) * kTokens;
+    const bool left = at > 0 && (threadIdx.x & 31) > 0;
+    const V* end = W + (x.V - 1LL) * ldw + H;
     int id[kTokens];
 #pragma unroll
     for (int u = 0; u < kTokens; ++u) id[u] = t0 + u < T ? id_of(x, t0 + u) : -1;
-    for (int v = blockIdx.y * G + (threadIdx.x & (G - 1)); v < np; v += gridDim.y * G) {
-        Piece p[kTokens];
+    bool in = x.V > 0;  // all rows inside the table; of no token row 0 is read, and not used
 #pragma unroll
-        for (int u = 0; u < kTokens; ++u)
-            if (id[u] >= 0) p[u] = load(reinterpret_cast<const Piece*>(W + id[u] * ldw) + v);
+    for (int u = 0; u < kTokens; ++u) in = in && rows.inside(W + max(id[u], 0) * ldw, W, end);
+    for (int v0 = blockIdx.y * G; v0 < np; v0 += gridDim.y * G) {
+        const int v = v0 + at;
+        Pack<V, N> p[kTokens];
+        if (in) {
+#pragma unroll
+            for (int u = 0; u < kTokens; ++u) p[u] = rows.template read<true>(W + max(id[u], 0) * ldw, v);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kTokens; ++u)
+                if (id[u] >= 0 && v < np) p[u] = rows.read_edge(W + id[u] * ldw, v);
+        }
 #pragma unroll
         for (int u = 0; u < kTokens; ++u) {
-            if (t0 + u >= T) break;
             Floats<N> f = floats(p[u]);
 #pragma unroll
             for (int i = 0; i < (N + 1) / 2; ++i) f.v[i] = id[u] >= 0 ? __fmul2_rn(f.v[i], make_float2(scale, scale)) : make_float2(0.f, 0.f);
-            write_once(reinterpret_cast<Piece*>(Y + (t0 + u) * ldy) + v, packed<V, N>(f));
+            rows.write(Y + (t0 + u) * ldy, v, packed<V, N>(f), t0 + u < T, left);
         }
     }
 }
@@ -88,19 +98,20 @@ struct OrderArgs {
     int* kept;          // tokens in all that have a row
     void* dW;           // NULL: no zeros are written
     long long ldw, row; // bytes
-    int zero_bytes;     // the widest word that rows are made of
 };
 
-// Zeros in a block's rows without tokens, a warp a row; bit i of empty[j]: row 32 j + i.
-template <class Z>
+// Zeros in a block's rows without tokens, a warp a row: whole aligned words, and 2-byte values before and after them.  Bit
+// i of empty[j]: row 32 j + i.
 __device__ __forceinline__ void fill_rows(const OrderArgs& a, long long v0, int nv, const uint32_t* empty) {
-    const int lane = threadIdx.x & 31, words = static_cast<int>(a.row / sizeof(Z));
-    Z zero;
-    memset(&zero, 0, sizeof(Z));
+    const int lane = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < nv; i += kOrderWarps) {
         if (!(empty[i >> 5] >> (i & 31) & 1u)) continue;
-        Z* q = reinterpret_cast<Z*>(static_cast<char*>(a.dW) + (v0 + i) * a.ldw);
-        for (int c = lane; c < words; c += 32) __stcs(q + c, zero);
+        char* q = static_cast<char*>(a.dW) + (v0 + i) * a.ldw;
+        const int head = static_cast<int>(min(a.row, static_cast<long long>(-reinterpret_cast<intptr_t>(q) & 15)));
+        const int words = static_cast<int>((a.row - head) / 16), tail = static_cast<int>((a.row - head) % 16);
+        for (int c = lane; c < words; c += 32) __stcs(reinterpret_cast<uint4*>(q + head) + c, make_uint4(0, 0, 0, 0));
+        const int at = lane < 8 ? 2 * lane : head + 16 * words + 2 * (lane - 8);  // lanes 0 to 7: the head, 8 to 15: the tail
+        if (lane < 8 ? 2 * lane < head : 2 * (lane - 8) < tail) *reinterpret_cast<uint16_t*>(q + at) = 0;
     }
 }
 
@@ -257,11 +268,7 @@ __global__ void __launch_bounds__(kOrderThreads, 1) embed_order_kernel(OrderArgs
         for (int i = threadIdx.x; i < (kOrderWarps * pitch + 1) / 2; i += kOrderThreads) reinterpret_cast<int*>(counters)[i] = 0;
         __syncthreads();
     }
-    if (!a.dW) return;
-    if (a.zero_bytes == 16) fill_rows<uint4>(a, v0, nv, s_empty);
-    else if (a.zero_bytes == 8) fill_rows<uint2>(a, v0, nv, s_empty);
-    else if (a.zero_bytes == 4) fill_rows<uint32_t>(a, v0, nv, s_empty);
-    else fill_rows<uint16_t>(a, v0, nv, s_empty);
+    if (a.dW) fill_rows(a, v0, nv, s_empty);
 }
 
 // ---------------------------------------------------------------- sums
@@ -425,24 +432,25 @@ spx_status check(int32_t T, int32_t H, int32_t V, spx_type type, int32_t id_byte
     return SPX_OK;
 }
 
-template <class V, int N>
+template <class V, int N, bool ANY>
 cudaError_t embed_launch(int T, int H, Ids x, const void* W, int64_t ldw, float scale, void* Y, int64_t ldy, cudaStream_t st) {
-    const int np = H / N;
+    const int np = (H + N - 1) / N;
     int lg = 3;
     while (lg < 8 && (1 << lg) < np) ++lg;
-    const int per = (kThreads >> lg) * kTokens, bx = (T + per - 1) / per;
+    const int per = (kThreads >> lg) * kTokens, bx = (T - 1) / per + 1;
     const int steps = (np + (1 << lg) - 1) >> lg, by = std::min(steps, std::max(1, 1216 / bx));
-    return launch_early(embed_kernel<V, N>, dim3(bx, by), kThreads, 0, 1, st, x, T, np, lg, static_cast<const V*>(W), static_cast<long long>(ldw), scale,
+    return launch_early(embed_kernel<V, N, ANY>, dim3(bx, by), kThreads, 0, 1, st, x, T, H, lg, static_cast<const V*>(W), static_cast<long long>(ldw), scale,
                         static_cast<V*>(Y), static_cast<long long>(ldy));
 }
 
 template <class V>
 spx_status embed(int T, int H, Ids x, const void* W, int64_t ldw, float scale, void* Y, int64_t ldy, cudaStream_t st) {
-    const int vb = copy_width(addr(W) | addr(Y) | (static_cast<uint64_t>(H) | ldw | ldy) * sizeof(V), sizeof(V));
+    const uint64_t bits = addr(W) | addr(Y) | (static_cast<uint64_t>(H) | ldw | ldy) * sizeof(V);
     spx_note_launches(1);
-    if (vb == 16) return spx_cuda_status(embed_launch<V, 16 / sizeof(V)>(T, H, x, W, ldw, scale, Y, ldy, st));
-    if (sizeof(V) == 2 && vb >= 4) return spx_cuda_status(embed_launch<V, 4 / sizeof(V)>(T, H, x, W, ldw, scale, Y, ldy, st));
-    return spx_cuda_status(embed_launch<V, 1>(T, H, x, W, ldw, scale, Y, ldy, st));
+    if (bits % 16 == 0) return spx_cuda_status(embed_launch<V, 16 / sizeof(V), false>(T, H, x, W, ldw, scale, Y, ldy, st));
+    if (bits % 4 == 0) return spx_cuda_status(embed_launch<V, 4 / sizeof(V), false>(T, H, x, W, ldw, scale, Y, ldy, st));
+    if constexpr (sizeof(V) == 2) return spx_cuda_status(embed_launch<V, 8, true>(T, H, x, W, ldw, scale, Y, ldy, st));
+    return SPX_ERR_ALIGN;
 }
 
 // Sorted tokens a chunk: as many chunks as run at once, of 8 to 1024 tokens.
@@ -545,7 +553,6 @@ spx_status spx_embed_grad(int32_t T, int32_t H, int32_t V, spx_type type, const 
     o.kept = reinterpret_cast<int*>(base + s.kept);
     o.dW = accumulate ? nullptr : dW;
     o.ldw = static_cast<long long>(lddw * wb), o.row = static_cast<long long>(H * wb);
-    o.zero_bytes = copy_width(addr(dW) | static_cast<uint64_t>(o.ldw) | static_cast<uint64_t>(o.row), static_cast<int>(wb));
     const int blocks = std::max(152, (V + kMostIds - 1) / kMostIds);
     o.per = (V + blocks - 1) / blocks;
     const dim3 grid((V + o.per - 1) / o.per);

@@ -32,30 +32,39 @@ struct NormArgs {
 };
 
 // The row's quotients y / s as codes (ties to even); a row that holds an infinity or NaN has codes 0.
-template <class V, class O, int N, int HELD, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1280 / MAXT) rms_norm_kernel(NormArgs a) {
-    constexpr int P = HELD / N;
+template <class V, class O, int N, bool ANY, int HELD, int MAXT>
+__global__ void __launch_bounds__(MAXT, ANY || MAXT > kThreads ? 1024 / MAXT : 5) rms_norm_kernel(NormArgs a) {
+    constexpr int P = HELD / N, X = (N + 1) / 2;
     using Piece = Pack<V, N>;
     __shared__ __align__(16) float s_sum[MAXT / 32];
     __shared__ uint32_t s_max[MAXT / 32];
     let_next_start();
     wait_for_previous();
-    const int G = 1 << a.log_g, at = threadIdx.x & (G - 1), np = a.H / N;
+    const Rows<V, N, ANY> rows{a.H};
+    const int G = 1 << a.log_g, at = threadIdx.x & (G - 1), np = rows.pieces();
     const int row = blockIdx.x * (blockDim.x >> a.log_g) + (threadIdx.x >> a.log_g);
-    const bool live = row < a.M;
-    const Piece* x = reinterpret_cast<const Piece*>(behind_wait(static_cast<const V*>(a.X)) + row * a.ldx);
-    const Piece* r = reinterpret_cast<const Piece*>(behind_wait(static_cast<const V*>(a.R)) + row * a.ldr);
+    const bool live = row < a.M, left = at > 0 && (threadIdx.x & 31) > 0;
+    const V *x = behind_wait(static_cast<const V*>(a.X)), *r = behind_wait(static_cast<const V*>(a.R));
     const void* w = behind_wait(a.w);
-    constexpr int X = (N + 1) / 2;
     Floats<N> s[P];
     {
         Piece px[P], pr[P];
+        const V *xr = x + row * a.ldx, *rr = r + row * a.ldr;
+        if (live && rows.inside(xr, x, x + (a.M - 1) * a.ldx + a.H) && (!a.R || rows.inside(rr, r, r + (a.M - 1) * a.ldr + a.H))) {
 #pragma unroll
-        for (int h = 0; h < P; ++h)
-            if (live && at + h * G < np) {
-                px[h] = load_once(x + at + h * G);
-                if (a.R) pr[h] = load_once(r + at + h * G);
+            for (int h = 0; h < P; ++h) {
+                if (h * G >= np) break;
+                px[h] = rows.read(xr, at + h * G);
+                if (a.R) pr[h] = rows.read(rr, at + h * G);
             }
+        } else if (ANY && live) {
+#pragma unroll
+            for (int h = 0; h < P; ++h)
+                if (at + h * G < np) {
+                    px[h] = rows.read_edge(xr, at + h * G);
+                    if (a.R) pr[h] = rows.read_edge(rr, at + h * G);
+                }
+        }
 #pragma unroll
         for (int h = 0; h < P; ++h) {
             const bool on = live && at + h * G < np;
@@ -69,13 +78,10 @@ __global__ void __launch_bounds__(MAXT, 1280 / MAXT) rms_norm_kernel(NormArgs a)
     for (int h = 0; h < P; ++h)
 #pragma unroll
         for (int i = 0; i < X; ++i) sum2 = __ffma2_rn(s[h].v[i], s[h].v[i], sum2);
-    if (a.S && live) {
-        Piece* out = reinterpret_cast<Piece*>(static_cast<V*>(a.S) + row * a.lds);
+    if (a.S) {
+        V* out = static_cast<V*>(a.S) + row * a.lds;
 #pragma unroll
-        for (int h = 0; h < P; ++h) {
-            if (at + h * G >= np) break;
-            write_piece(out + at + h * G, packed<V, N>(s[h]));
-        }
+        for (int h = 0; h < P; ++h) rows.write(out, at + h * G, packed<V, N>(s[h]), live, left);
     }
     const float sum = group_sum(sum2.x + sum2.y, G, s_sum);
     const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.H) + a.eps);
@@ -85,13 +91,14 @@ __global__ void __launch_bounds__(MAXT, 1280 / MAXT) rms_norm_kernel(NormArgs a)
     for (int h = 0; h < P; ++h) {
         if (at + h * G >= np) break;
         Floats<N> f;
-        if (a.w) f = load_floats<V, N>(w, a.wide_w, static_cast<long long>(at + h * G) * N);
+        if (a.w) f = rows.weights(w, a.wide_w, at + h * G);
 #pragma unroll
         for (int i = 0; i < X; ++i) {
             s[h].v[i] = __fmul2_rn(s[h].v[i], r2);
             if (a.w) s[h].v[i] = __fmul2_rn(s[h].v[i], f.v[i]);
         }
     }
+    O* y = static_cast<O*>(a.Y) + row * a.ldy;
     if constexpr (sizeof(O) == 1) {
         uint32_t m = 0;  // the bits of an infinity or NaN are above every number's
 #pragma unroll
@@ -102,7 +109,6 @@ __global__ void __launch_bounds__(MAXT, 1280 / MAXT) rms_norm_kernel(NormArgs a)
         const bool fine = m < 0x7f800000u;
         const float q = __uint_as_float(m) / 127.f;
         if (live && at == 0) a.scale[row] = fine ? q : __int_as_float(0x7fffffff);
-        if (!live) return;
         // The quotient from the rounded reciprocal: a first one, its exact remainder, and a correction that rounds it
         // correctly (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
         // Subnormal scales, whose reciprocal may not exist, divide; they are coarse, so the quotient may pass 127.
@@ -110,10 +116,8 @@ __global__ void __launch_bounds__(MAXT, 1280 / MAXT) rms_norm_kernel(NormArgs a)
         const float inv = plain ? 1.f / q : 0.f;
         constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
         const float2 inv2 = make_float2(inv, inv), q2 = make_float2(-q, -q), whole = make_float2(kWhole, kWhole);
-        Pack<O, N>* y = reinterpret_cast<Pack<O, N>*>(static_cast<O*>(a.Y) + row * a.ldy);
 #pragma unroll
         for (int h = 0; h < P; ++h) {
-            if (at + h * G >= np) break;
             uint32_t t[2 * X];
 #pragma unroll
             for (int i = 0; i < X; ++i) {
@@ -135,19 +139,16 @@ __global__ void __launch_bounds__(MAXT, 1280 / MAXT) rms_norm_kernel(NormArgs a)
                     word[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040), __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040), 0x5410);
                 memcpy(&p, word, N);
             } else {
+                int8_t c[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) p.v[i] = static_cast<int8_t>(t[i]);
+                for (int i = 0; i < N; ++i) c[i] = static_cast<int8_t>(t[i]);
+                p.set(c);
             }
-            write_piece(y + at + h * G, p);
+            rows.write(y, at + h * G, p, live, left);
         }
     } else {
-        if (!live) return;
-        Piece* y = reinterpret_cast<Piece*>(static_cast<V*>(a.Y) + row * a.ldy);
 #pragma unroll
-        for (int h = 0; h < P; ++h) {
-            if (at + h * G >= np) break;
-            write_piece(y + at + h * G, packed<V, N>(s[h]));
-        }
+        for (int h = 0; h < P; ++h) rows.write(y, at + h * G, packed<V, N>(s[h]), live, left);
     }
 }
 
@@ -167,16 +168,19 @@ struct GradArgs {
     bool wide_w;  // the weights are fp32
 };
 
-// DEPTH 0 (pieces of 2 bytes, which no copy takes, and rows that leave no room): loaded where they are needed.
-template <class V, int N, int MAXT, int DEPTH>
-__global__ void __launch_bounds__(MAXT, MAXT == kThreads ? 3 : 1) rms_norm_grad_kernel(GradArgs a) {
+// Rows off 16-byte boundaries (ANY) bring both words around each piece.  DEPTH 0 (rows that leave no room): loaded where
+// they are needed.
+template <class V, int N, bool ANY, int MAXT, int DEPTH>
+__global__ void __launch_bounds__(MAXT, MAXT > kThreads ? 1 : ANY ? 2 : 3) rms_norm_grad_kernel(GradArgs a) {
     constexpr int P = kHeld / N, X = (N + 1) / 2;
     using Piece = Pack<V, N>;
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ __align__(16) float s_sum[2][MAXT / 32];
     let_next_start();
     wait_for_previous();
-    const int G = 1 << a.log_g, at = threadIdx.x & (G - 1), np = a.H / N;
+    const Rows<V, N, ANY> rows{a.H};
+    const int G = 1 << a.log_g, at = threadIdx.x & (G - 1), np = rows.pieces();
+    const bool left = at > 0 && (threadIdx.x & 31) > 0;
     const int groups = blockDim.x >> a.log_g, mine = threadIdx.x >> a.log_g, step = gridDim.x * groups;
     const V *dY = behind_wait(static_cast<const V*>(a.dY)), *S = behind_wait(static_cast<const V*>(a.S));
     const V* dR = behind_wait(static_cast<const V*>(a.dR));
@@ -184,27 +188,53 @@ __global__ void __launch_bounds__(MAXT, MAXT == kThreads ? 3 : 1) rms_norm_grad_
     const void* w = behind_wait(a.w);
     const float over = -1.f / static_cast<float>(a.H);
     // slot h of array x of stage d: a piece a thread
+    constexpr int E = ANY ? 2 : 1;  // words a piece
     Piece* slots = reinterpret_cast<Piece*>(sm) + threadIdx.x;
-    auto slot = [&](int d, int x, int h) { return slots + ((d * 3 + x) * P + h) * static_cast<int>(DEPTH > 0 ? MAXT : 0); };
+    auto slot = [&](int d, int x, int h) { return slots + ((d * 3 + x) * P + h) * E * static_cast<int>(DEPTH > 0 ? MAXT : 0); };
+    const V *dY1 = dY + (a.M - 1) * a.lddy + a.H, *S1 = S + (a.M - 1) * a.lds + a.H, *dR1 = dR + (a.M - 1) * a.lddr + a.H;
     int row = blockIdx.x * groups + mine, ahead = row;
-    const Piece *g = reinterpret_cast<const Piece*>(dY + row * a.lddy) + at, *s = reinterpret_cast<const Piece*>(S + row * a.lds) + at,
-                *r = reinterpret_cast<const Piece*>(dR + row * a.lddr) + at;
+    const V *g = dY + row * a.lddy, *s = S + row * a.lds, *r = dR + row * a.lddr;  // row `ahead` of each
     const long long dg = step * a.lddy, ds = step * a.lds, dr = step * a.lddr;
-    auto ahead_one = [&]() {
-        ahead += step;
-        g = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(g) + dg);
-        s = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(s) + ds);
-        r = reinterpret_cast<const Piece*>(reinterpret_cast<const V*>(r) + dr);
-    };
-    auto fetch = [&](int d) {
-        if (ahead < a.M) {
+    auto ahead_one = [&]() { ahead += step, g += dg, s += ds, r += dr; };
+    auto copy = [&](int d, int x, const V* from, const V* lo, const V* hi) {
+        if (rows.inside(from, lo, hi)) {
+            const Piece* q = reinterpret_cast<const Piece*>(reinterpret_cast<uintptr_t>(from) & ~static_cast<uintptr_t>(15)) + at;
 #pragma unroll
             for (int h = 0; h < P; ++h)
                 if (at + h * G < np) {
-                    copy_piece(slot(d, 0, h), g + h * G);
-                    copy_piece(slot(d, 1, h), s + h * G);
-                    if (a.dR) copy_piece(slot(d, 2, h), r + h * G);
+                    copy_near(slot(d, x, h), q + h * G);
+                    copy_near(slot(d, x, h) + MAXT, q + h * G + 1);
                 }
+        } else {
+#pragma unroll
+            for (int h = 0; h < P; ++h)
+                if (at + h * G < np) write_piece(slot(d, x, h), rows.read_edge(from, at + h * G));
+        }
+    };
+    auto take = [&](int d, int x, int h, int m) {  // m: bytes that the row lies off a boundary
+        const Piece p = read_piece(slot(d, x, h));
+        if constexpr (!ANY) return p;
+        else return rows.join(p, m ? read_piece(slot(d, x, h) + MAXT) : p, m, at + h * G);
+    };
+    auto off = [&](int row, const V* base, long long ld, const V* hi) {
+        const V* p = base + row * ld;
+        return ANY && rows.inside(p, base, hi) ? static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) : 0;
+    };
+    auto fetch = [&](int d) {
+        if (ahead < a.M) {
+            if constexpr (!ANY) {
+#pragma unroll
+                for (int h = 0; h < P; ++h)
+                    if (at + h * G < np) {
+                        copy_piece(slot(d, 0, h), reinterpret_cast<const Piece*>(g) + at + h * G);
+                        copy_piece(slot(d, 1, h), reinterpret_cast<const Piece*>(s) + at + h * G);
+                        if (a.dR) copy_piece(slot(d, 2, h), reinterpret_cast<const Piece*>(r) + at + h * G);
+                    }
+            } else {
+                copy(d, 0, g, dY, dY1);
+                copy(d, 1, s, S, S1);
+                if (a.dR) copy(d, 2, r, dR, dR1);
+            }
         }
         ahead_one();
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -217,9 +247,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == kThreads ? 3 : 1) rms_norm_grad_
     for (int h = 0; h < P; ++h) {
 #pragma unroll
         for (int i = 0; i < X; ++i) acc[h].v[i] = make_float2(0.f, 0.f), wf[h].v[i] = make_float2(1.f, 1.f);
-        if (a.w && at + h * G < np) wf[h] = load_floats<V, N>(w, a.wide_w, static_cast<long long>(at + h * G) * N);
+        if (a.w && at + h * G < np) wf[h] = rows.weights(w, a.wide_w, at + h * G);
     }
-    Piece* dx = reinterpret_cast<Piece*>(static_cast<V*>(a.dX) + row * a.lddx) + at;
+    V* dx = static_cast<V*>(a.dX) + row * a.lddx;
     int d = 0, turn = 0;
     for (int r0 = blockIdx.x * groups; r0 < a.M; r0 += step, row += step, turn ^= 1) {
         const bool live = row < a.M;
@@ -229,20 +259,28 @@ __global__ void __launch_bounds__(MAXT, MAXT == kThreads ? 3 : 1) rms_norm_grad_
         if constexpr (DEPTH > 0) {
             fetch(d == 0 ? DEPTH - 1 : d - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-        } else if (live) {
+        } else if (live && rows.inside(g, dY, dY1) && rows.inside(s, S, S1) && (!a.dR || rows.inside(r, dR, dR1))) {
+#pragma unroll
+            for (int h = 0; h < P; ++h) {
+                if (h * G >= np) break;
+                pg[h] = rows.read(g, at + h * G), ps[h] = rows.read(s, at + h * G);
+                if (a.dR) pr[h] = rows.read(r, at + h * G);
+            }
+        } else if (ANY && live) {
 #pragma unroll
             for (int h = 0; h < P; ++h)
                 if (at + h * G < np) {
-                    pg[h] = load_once(g + h * G), ps[h] = load_once(s + h * G);
-                    if (a.dR) pr[h] = load_once(r + h * G);
+                    pg[h] = rows.read_edge(g, at + h * G), ps[h] = rows.read_edge(s, at + h * G);
+                    if (a.dR) pr[h] = rows.read_edge(r, at + h * G);
                 }
         }
+        const int mg = DEPTH > 0 ? off(row, dY, a.lddy, dY1) : 0, ms = DEPTH > 0 ? off(row, S, a.lds, S1) : 0;
         float2 dot2 = make_float2(0.f, 0.f);
         if (live) {
 #pragma unroll
             for (int h = 0; h < P; ++h) {
                 if (at + h * G >= np) break;
-                if constexpr (DEPTH > 0) pg[h] = read_piece(slot(d, 0, h)), ps[h] = read_piece(slot(d, 1, h));
+                if constexpr (DEPTH > 0) pg[h] = take(d, 0, h, mg), ps[h] = take(d, 1, h, ms);
                 const Floats<N> x = floats(pg[h]), y = floats(ps[h]);
 #pragma unroll
                 for (int i = 0; i < X; ++i) {
@@ -254,26 +292,25 @@ __global__ void __launch_bounds__(MAXT, MAXT == kThreads ? 3 : 1) rms_norm_grad_
         }
         const float dot = group_sum(dot2.x + dot2.y, G, s_sum[turn]) * over;
         const float2 c2 = make_float2(dot, dot);
-        if (live) {
 #pragma unroll
-            for (int h = 0; h < P; ++h) {
-                if (at + h * G >= np) break;
-                if constexpr (DEPTH > 0) {  // once more, sooner than held across the sum
-                    pg[h] = read_piece(slot(d, 0, h)), ps[h] = read_piece(slot(d, 1, h));
-                    if (a.dR) pr[h] = read_piece(slot(d, 2, h));
-                }
-                const Floats<N> x = floats(pg[h]), y = floats(ps[h]);
-                Floats<N> z, o;
-                if (a.dR) z = floats(pr[h]);
-#pragma unroll
-                for (int i = 0; i < X; ++i) {
-                    const float2 v = __ffma2_rn(__fmul2_rn(y.v[i], r2), c2, __fmul2_rn(x.v[i], wf[h].v[i]));
-                    o.v[i] = a.dR ? __ffma2_rn(v, r2, z.v[i]) : __fmul2_rn(v, r2);
-                }
-                write_piece(dx + h * G, packed<V, N>(o));
+        for (int h = 0; h < P; ++h) {
+            const bool on = live && at + h * G < np;
+            if (!ANY && !on) continue;
+            if constexpr (DEPTH > 0) {  // once more, sooner than held across the sum
+                pg[h] = take(d, 0, h, mg), ps[h] = take(d, 1, h, ms);
+                if (a.dR) pr[h] = take(d, 2, h, off(row, dR, a.lddr, dR1));
             }
+            const Floats<N> x = floats(pg[h]), y = floats(ps[h]);
+            Floats<N> z, o;
+            if (a.dR) z = floats(pr[h]);
+#pragma unroll
+            for (int i = 0; i < X; ++i) {
+                const float2 v = __ffma2_rn(__fmul2_rn(y.v[i], r2), c2, __fmul2_rn(x.v[i], wf[h].v[i]));
+                o.v[i] = a.dR ? __ffma2_rn(v, r2, z.v[i]) : __fmul2_rn(v, r2);
+            }
+            rows.write(dx, at + h * G, packed<V, N>(o), on, left);
         }
-        dx = reinterpret_cast<Piece*>(reinterpret_cast<V*>(dx) + step * a.lddx);
+        dx += step * a.lddx;
         if constexpr (DEPTH > 0) d = d == DEPTH - 1 ? 0 : d + 1;
         else ahead_one();
     }
@@ -290,6 +327,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == kThreads ? 3 : 1) rms_norm_grad_
                 if (p >= np) break;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
+                    if (ANY && i >= rows.values(p)) break;
                     float* to = sums + p * N + i;
                     const float v = i & 1 ? acc[h].v[i / 2].y : acc[h].v[i / 2].x;
                     *to = m == 0 ? v : *to + v;
@@ -303,19 +341,20 @@ __global__ void __launch_bounds__(MAXT, MAXT == kThreads ? 3 : 1) rms_norm_grad_
 
 // Rows longer than a block's threads hold so: a block a row, read twice, the second time from L2.
 constexpr int kLongValues = 32;
-template <class V, int N>
+template <class V, int N, bool ANY>
 __global__ void __launch_bounds__(kMostThreads, 1) rms_norm_grad_long_kernel(GradArgs a) {
-    constexpr int K = kLongValues / N;
+    constexpr int K = kLongValues / N, X = (N + 1) / 2;
     using Piece = Pack<V, N>;
     __shared__ __align__(16) float s_sum[2][kMostThreads / 32];
     let_next_start();
     wait_for_previous();
-    const int np = a.H / N;
+    const Rows<V, N, ANY> rows{a.H};
+    const int np = rows.pieces();
     const V *dY = behind_wait(static_cast<const V*>(a.dY)), *S = behind_wait(static_cast<const V*>(a.S));
     const V* dR = behind_wait(static_cast<const V*>(a.dR));
     const float* rs = behind_wait(a.rstd);
     const void* w = behind_wait(a.w);
-    constexpr int X = (N + 1) / 2;
+    const V *dY1 = dY + (a.M - 1) * a.lddy + a.H, *S1 = S + (a.M - 1) * a.lds + a.H, *dR1 = dR + (a.M - 1) * a.lddr + a.H;
     Floats<N> acc[K];
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -323,9 +362,9 @@ __global__ void __launch_bounds__(kMostThreads, 1) rms_norm_grad_long_kernel(Gra
         for (int i = 0; i < X; ++i) acc[k].v[i] = make_float2(0.f, 0.f);
     int turn = 0;
     for (int row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
-        const Piece *g = reinterpret_cast<const Piece*>(dY + row * a.lddy), *s = reinterpret_cast<const Piece*>(S + row * a.lds);
-        const Piece* r = reinterpret_cast<const Piece*>(dR + row * a.lddr);
-        Piece* out = reinterpret_cast<Piece*>(static_cast<V*>(a.dX) + row * a.lddx);
+        const V *g = dY + row * a.lddy, *s = S + row * a.lds, *r = dR + row * a.lddr;
+        V* out = static_cast<V*>(a.dX) + row * a.lddx;
+        const bool in = rows.inside(g, dY, dY1) && rows.inside(s, S, S1) && (!a.dR || rows.inside(r, dR, dR1));
         const float rstd = load(rs + row);
         float2 dot2 = make_float2(0.f, 0.f);
         const float2 r2 = make_float2(rstd, rstd);
@@ -333,10 +372,9 @@ __global__ void __launch_bounds__(kMostThreads, 1) rms_norm_grad_long_kernel(Gra
         for (int k = 0; k < K; ++k) {
             const int p = threadIdx.x + k * kMostThreads;
             if (p >= np) break;
-            const Piece x = load(g + p), y = load(s + p);
-            const Floats<N> u = floats(x), v = floats(y);
+            const Floats<N> u = floats(in ? rows.read(g, p) : rows.read_edge(g, p)), v = floats(in ? rows.read(s, p) : rows.read_edge(s, p));
             Floats<N> f;
-            if (a.w) f = load_floats<V, N>(w, a.wide_w, static_cast<long long>(p) * N);
+            if (a.w) f = rows.weights(w, a.wide_w, p);
 #pragma unroll
             for (int i = 0; i < X; ++i) {
                 const float2 n = __fmul2_rn(v.v[i], r2);
@@ -346,18 +384,21 @@ __global__ void __launch_bounds__(kMostThreads, 1) rms_norm_grad_long_kernel(Gra
         }
         const float dot = group_sum(dot2.x + dot2.y, kMostThreads, s_sum[turn]) / -static_cast<float>(a.H);
 #pragma unroll 2
-        for (int p = threadIdx.x; p < np; p += kMostThreads) {
-            const Piece x = load(g + p), y = load(s + p);
-            const Floats<N> u = floats(x), v = floats(y);
-            Floats<N> z, f, o;
-            if (a.dR) z = floats(load_once(r + p));
-            if (a.w) f = load_floats<V, N>(w, a.wide_w, static_cast<long long>(p) * N);
+        for (int p0 = 0; p0 < np; p0 += kMostThreads) {
+            const int p = p0 + threadIdx.x;
+            const bool on = p < np;
+            Floats<N> u, v, z, f, o;
+            if (on) {
+                u = floats(in ? rows.read(g, p) : rows.read_edge(g, p)), v = floats(in ? rows.read(s, p) : rows.read_edge(s, p));
+                if (a.dR) z = floats(in ? rows.read(r, p) : rows.read_edge(r, p));
+                if (a.w) f = rows.weights(w, a.wide_w, p);
+            }
 #pragma unroll
             for (int i = 0; i < X; ++i) {
                 const float2 e = __ffma2_rn(__fmul2_rn(v.v[i], r2), make_float2(dot, dot), a.w ? __fmul2_rn(u.v[i], f.v[i]) : u.v[i]);
                 o.v[i] = a.dR ? __ffma2_rn(e, r2, z.v[i]) : __fmul2_rn(e, r2);
             }
-            write_piece(out + p, packed<V, N>(o));
+            rows.write(out, p, packed<V, N>(o), on, (threadIdx.x & 31) > 0);
         }
     }
     if (!a.part) return;
@@ -367,7 +408,8 @@ __global__ void __launch_bounds__(kMostThreads, 1) rms_norm_grad_long_kernel(Gra
         const int p = threadIdx.x + k * kMostThreads;
         if (p >= np) break;
 #pragma unroll
-        for (int i = 0; i < N; ++i) part[p * N + i] = i & 1 ? acc[k].v[i / 2].y : acc[k].v[i / 2].x;
+        for (int i = 0; i < N; ++i)
+            if (!ANY || i < rows.values(p)) part[p * N + i] = i & 1 ? acc[k].v[i / 2].y : acc[k].v[i / 2].x;
     }
 }
 
@@ -412,71 +454,71 @@ spx_status check(int32_t M, int32_t H, spx_type type, spx_type w_type) {
     return SPX_OK;
 }
 
-template <class V, class O, int N>
+template <class V, class O, int N, bool ANY>
 cudaError_t norm_launch(NormArgs a, cudaStream_t st) {
-    a.log_g = threads_log(a.M, a.H, a.H / N);
+    a.log_g = threads_log(a.M, a.H, (a.H + N - 1) / N);
     const int threads = std::max(kThreads, 1 << a.log_g), per = threads >> a.log_g;
     const dim3 grid((a.M + per - 1) / per);
-    if (threads == kThreads) return launch_early(rms_norm_kernel<V, O, N, kHeld, kThreads>, grid, threads, 0, 1, st, a);
-    return launch_early(a.H <= kHeld * kMostThreads ? rms_norm_kernel<V, O, N, kHeld, kMostThreads> : rms_norm_kernel<V, O, N, 2 * kHeld, kMostThreads>, grid,
+    if (threads == kThreads) return launch_early(rms_norm_kernel<V, O, N, ANY, kHeld, kThreads>, grid, threads, 0, 1, st, a);
+    return launch_early(a.H <= kHeld * kMostThreads ? rms_norm_kernel<V, O, N, ANY, kHeld, kMostThreads> : rms_norm_kernel<V, O, N, ANY, 2 * kHeld, kMostThreads>, grid,
                         threads, 0, 1, st, a);
 }
 
-// The widest pieces, up to 16 bytes, that every row is made of; an output in 8 bits takes as many bytes as a piece has values.
+// Rows of 16-byte pieces in every array (of codes: of as many bytes as a piece has values), else of 4-byte ones, else, 16-bit
+// rows of odd widths or bases, shifted ones.  16384 x 4096 bf16 80 us, rows of 4094 96, of 4095 161.
 template <class V, class O>
 spx_status norm_pieces(const NormArgs& a, cudaStream_t st) {
-    constexpr bool codes = sizeof(O) == 1;
     uint64_t bits = addr(a.X) | (static_cast<uint64_t>(a.H) | a.ldx) * sizeof(V);
     if (a.R) bits |= addr(a.R) | a.ldr * sizeof(V);
     if (a.S) bits |= addr(a.S) | a.lds * sizeof(V);
-    bits |= codes ? (addr(a.Y) | a.ldy) * sizeof(V) : addr(a.Y) | a.ldy * sizeof(V);
+    bits |= (addr(a.Y) | a.ldy * sizeof(O)) * (sizeof(V) / sizeof(O));
     if (a.w) bits |= a.wide_w && sizeof(V) == 2 ? (addr(a.w) % 16 ? addr(a.w) / 2 : 0) : addr(a.w);
-    const int vb = copy_width(bits, sizeof(V));
     spx_note_launches(1);
-    if (vb == 16) return spx_cuda_status(norm_launch<V, O, 16 / sizeof(V)>(a, st));
-    if (sizeof(V) == 2 && vb >= 4) return spx_cuda_status(norm_launch<V, O, 4 / sizeof(V)>(a, st));
-    return spx_cuda_status(norm_launch<V, O, 1>(a, st));
+    if (bits % 16 == 0) return spx_cuda_status(norm_launch<V, O, 16 / sizeof(V), false>(a, st));
+    if (bits % 4 == 0) return spx_cuda_status(norm_launch<V, O, 4 / sizeof(V), false>(a, st));
+    if constexpr (sizeof(V) == 2) return spx_cuda_status(norm_launch<V, O, 8, true>(a, st));
+    return SPX_ERR_ALIGN;
 }
 
-// Threads a row (log2), a block's threads, and the blocks of the gradient: three an SM of 256 threads, one of more.
+// Threads a row (log2), a block's threads, and the blocks of the gradient: as many as the SMs hold at once.
 struct GradShape {
     int log_g, threads, blocks;
 };
 constexpr int kGradBlocks = 456, kLongRow = kHeld * kMostThreads;
 
-GradShape grad_shape(int M, int H) {
+GradShape grad_shape(int M, int H, bool any) {
     GradShape g{};
     g.log_g = 2;
     while ((kHeld << g.log_g) < H && (1 << g.log_g) < kMostThreads) ++g.log_g;
     g.threads = std::max(kThreads, 1 << g.log_g);
     const int per = g.threads >> g.log_g;
-    g.blocks = std::min((M - 1) / per + 1, g.threads > kThreads ? kGradBlocks / 3 : kGradBlocks);
+    g.blocks = std::min((M - 1) / per + 1, g.threads > kThreads ? kGradBlocks / 3 : any ? kGradBlocks / 3 * 2 : kGradBlocks);
     return g;
 }
 
-template <class V, int N, int MAXT, int DEPTH>
+template <class V, int N, bool ANY, int MAXT, int DEPTH>
 cudaError_t grad_kernel(const GradArgs& a, const GradShape& g, cudaStream_t st) {
-    constexpr size_t ring = static_cast<size_t>(DEPTH) * 3 * kHeld * sizeof(V) * MAXT;
+    constexpr size_t ring = static_cast<size_t>(DEPTH) * 3 * kHeld * sizeof(V) * MAXT * (ANY ? 2 : 1);
     const size_t smem = std::max(ring, a.part && g.threads > 1 << g.log_g ? sizeof(float) * a.H : 0);
-    const cudaError_t e = DEPTH > 0 ? spx_tc::set_smem_limit(rms_norm_grad_kernel<V, N, MAXT, DEPTH>, ring) : cudaSuccess;
-    return e != cudaSuccess ? e : launch_early(rms_norm_grad_kernel<V, N, MAXT, DEPTH>, dim3(g.blocks), g.threads, smem, 1, st, a);
+    const cudaError_t e = DEPTH > 0 ? spx_tc::set_smem_limit(rms_norm_grad_kernel<V, N, ANY, MAXT, DEPTH>, ring) : cudaSuccess;
+    return e != cudaSuccess ? e : launch_early(rms_norm_grad_kernel<V, N, ANY, MAXT, DEPTH>, dim3(g.blocks), g.threads, smem, 1, st, a);
 }
 
-template <class V, int N>
-cudaError_t grad_launch(GradArgs a, float* dw, cudaStream_t st) {
-    const GradShape g = grad_shape(a.M, a.H);
+template <class V, int N, bool ANY>
+spx_status grad_launch(GradArgs a, float* dw, cudaStream_t st) {
+    const GradShape g = grad_shape(a.M, a.H, ANY);
     a.log_g = g.log_g;
     if (a.part && g.blocks == 1) a.part = dw;
     spx_note_launches(a.part && g.blocks > 1 ? 2 : 1);
-    constexpr bool async = N * sizeof(V) >= 4;
+    constexpr bool half = sizeof(V) == 2;
     cudaError_t e;
-    if (g.threads == kThreads) e = grad_kernel<V, N, kThreads, !async ? 0 : sizeof(V) == 2 ? 3 : 1>(a, g, st);
-    else if (g.threads == 512) e = grad_kernel<V, N, 512, !async ? 0 : sizeof(V) == 2 ? 3 : 2>(a, g, st);
-    else if (a.H <= kLongRow) e = grad_kernel<V, N, kMostThreads, async && sizeof(V) == 2 ? 2 : 0>(a, g, st);
-    else e = launch_early(rms_norm_grad_long_kernel<V, N>, dim3(g.blocks), kMostThreads, 0, 1, st, a);
+    if (g.threads == kThreads) e = grad_kernel<V, N, ANY, kThreads, half ? (ANY ? 2 : 3) : 1>(a, g, st);
+    else if (g.threads == 512) e = grad_kernel<V, N, ANY, 512, half ? (ANY ? 2 : 3) : ANY ? 1 : 2>(a, g, st);
+    else if (a.H <= kLongRow) e = grad_kernel<V, N, ANY, kMostThreads, half && !ANY ? 2 : 0>(a, g, st);
+    else e = launch_early(rms_norm_grad_long_kernel<V, N, ANY>, dim3(g.blocks), kMostThreads, 0, 1, st, a);
     if (e == cudaSuccess && a.part && g.blocks > 1)
         e = launch_early(add_parts_kernel, dim3((a.H + 31) / 32), kAddThreads, 0, 1, st, a.H, g.blocks, static_cast<const float*>(a.part), dw);
-    return e;
+    return spx_cuda_status(e);
 }
 
 template <class V>
@@ -484,10 +526,10 @@ spx_status grad_pieces(const GradArgs& a, float* dw, cudaStream_t st) {
     uint64_t bits = addr(a.dY) | addr(a.S) | addr(a.dX) | (static_cast<uint64_t>(a.H) | a.lddy | a.lds | a.lddx) * sizeof(V);
     if (a.dR) bits |= addr(a.dR) | a.lddr * sizeof(V);
     if (a.w) bits |= a.wide_w && sizeof(V) == 2 ? (addr(a.w) % 16 ? addr(a.w) / 2 : 0) : addr(a.w);
-    const int vb = copy_width(bits, sizeof(V));
-    if (vb == 16) return spx_cuda_status(grad_launch<V, 16 / sizeof(V)>(a, dw, st));
-    if (sizeof(V) == 2 && vb >= 4) return spx_cuda_status(grad_launch<V, 4 / sizeof(V)>(a, dw, st));
-    return spx_cuda_status(grad_launch<V, 1>(a, dw, st));
+    if (bits % 16 == 0) return grad_launch<V, 16 / sizeof(V), false>(a, dw, st);
+    if (bits % 4 == 0) return grad_launch<V, 4 / sizeof(V), false>(a, dw, st);
+    if constexpr (sizeof(V) == 2) return grad_launch<V, 8, true>(a, dw, st);
+    return SPX_ERR_ALIGN;
 }
 
 template <class V, bool CODES>
@@ -540,7 +582,7 @@ spx_status spx_rms_norm_i8(int32_t M, int32_t H, spx_type type, const void* X, i
 
 size_t spx_rms_norm_grad_scratch_bytes(int32_t M, int32_t H) {
     if (M <= 0 || H <= 0 || H > SPX_NORM_MAX_H || M > kMostIndex) return 0;
-    return M > 1 ? sizeof(float) * static_cast<size_t>(grad_shape(M, H).blocks) * static_cast<size_t>(H) : 0;
+    return M > 1 ? sizeof(float) * static_cast<size_t>(grad_shape(M, H, false).blocks) * static_cast<size_t>(H) : 0;
 }
 
 spx_status spx_rms_norm_grad(int32_t M, int32_t H, spx_type type, const void* dY, int64_t lddy, const void* S, int64_t lds,
