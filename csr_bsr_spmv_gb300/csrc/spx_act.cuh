@@ -38,50 +38,56 @@ __device__ __forceinline__ float at_most(float x, float y) {
     return r;
 }
 
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 cut(float2 x, float most) {
+    return make_float2(at_most(at_least(x.x, -most), most), at_most(at_least(x.y, -most), most));
+}
+
 // 1 / (1 + exp(-z)), z within +-88, where the exponential is finite, from the
 // hardware's 2^t and 1 / y (off by two and one units in the last place): the
-// rounding of t = z log2(e) is put back to first order, 2^(t + d) = 2^t (1 + d
-// ln 2).  Off by less than 2^-21 of itself, and 0 below 1e-38.
-__device__ __forceinline__ float logistic(float z) {
+// rounding of t = -z log2(e), which is -(z log2(e) + t), is put back to first
+// order, 2^(t + r) = 2^t (1 + r ln 2).  Off by less than 2^-21 of itself, and 0
+// below 1e-38.  Two values at a time, as everything here: most of it is one
+// instruction for both.
+__device__ __forceinline__ float2 logistic(float2 z) {
     constexpr float L = 1.44269502f, rest = 1.92596303e-8f;  // log2(e) = L + rest
-    const float t = -z * L, d = fmaf(-z, rest, fmaf(-z, L, -t));
-    float e, p;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    e = fmaf(e, d * 0.693147181f, e);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + e));
+    const float2 t = __fmul2_rn(z, both(-L)), d = __ffma2_rn(z, both(rest), __ffma2_rn(z, both(L), t));
+    float2 e, p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __fadd2_rn(__ffma2_rn(e, __fmul2_rn(d, both(-0.693147181f)), e), both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(e.y));
     return p;
 }
 
 constexpr float kTanh1 = 1.5957691216f, kTanh3 = 0.07135481628f;  // 2 sqrt(2 / pi), and that times 0.044715
 
 template <int kind>
-__device__ __forceinline__ float act_of(float x) {
-    if (kind == SPX_ACT_SILU) {
-        const float cut = at_least(x, -88.f);
-        return cut * logistic(at_most(cut, 88.f));
+__device__ __forceinline__ float2 act_of(float2 x, float2& slope) {
+    constexpr float most = kind == SPX_ACT_SILU ? 88.f : 100.f;
+    const float2 low = make_float2(at_least(x.x, -most), at_least(x.y, -most)), near = make_float2(at_most(low.x, most), at_most(low.y, most));
+    float2 z = near, dz = both(1.f), p;
+    if (kind == SPX_ACT_GELU) {
+        p = make_float2(normcdff(x.x), normcdff(x.y));
+        const float2 h = __fmul2_rn(__fmul2_rn(near, near), both(-0.5f));
+        slope = __ffma2_rn(__fmul2_rn(near, both(0.3989422804f)), make_float2(expf(h.x), expf(h.y)), p);
+        return __fmul2_rn(low, p);
     }
-    const float cut = at_least(x, -100.f);
-    if (kind == SPX_ACT_GELU) return cut * normcdff(x);
-    const float z = cut * fmaf(kTanh3, fminf(x * x, 1e4f), kTanh1);
-    return cut * logistic(at_most(at_least(z, -88.f), 88.f));
+    if (kind == SPX_ACT_GELU_TANH) {
+        const float2 xx = __fmul2_rn(near, near);
+        z = cut(__fmul2_rn(near, __ffma2_rn(both(kTanh3), xx, both(kTanh1))), 88.f);
+        dz = __ffma2_rn(both(3.f * kTanh3), xx, both(kTanh1));
+    }
+    p = logistic(z);
+    const float2 q = __ffma2_rn(p, both(-1.f), both(1.f));  // 1 - p
+    slope = __fmul2_rn(p, __ffma2_rn(kind == SPX_ACT_SILU ? near : __fmul2_rn(near, dz), q, both(1.f)));
+    return __fmul2_rn(low, p);
 }
 template <int kind>
-__device__ __forceinline__ float act_of(float x, float& slope) {
-    if (kind == SPX_ACT_SILU) {
-        const float cut = at_least(x, -88.f), z = at_most(cut, 88.f), p = logistic(z);
-        slope = p * fmaf(z, 1.f - p, 1.f);
-        return cut * p;
-    }
-    const float cut = at_least(x, -100.f), near = at_most(cut, 100.f), xx = near * near;
-    if (kind == SPX_ACT_GELU) {
-        const float p = normcdff(x);
-        slope = fmaf(near * 0.3989422804f, expf(-0.5f * xx), p);
-        return cut * p;
-    }
-    const float z = near * fmaf(kTanh3, xx, kTanh1), dz = fmaf(3.f * kTanh3, xx, kTanh1);
-    const float p = logistic(at_most(at_least(z, -88.f), 88.f));
-    slope = p * fmaf(near * dz, 1.f - p, 1.f);
-    return cut * p;
+__device__ __forceinline__ float2 act_of(float2 x) {
+    float2 slope;  // not used: its instructions go
+    return act_of<kind>(x, slope);
 }
 
 // f with the activation as a constant (a lambda over std::integral_constant): a chunk of values then runs one straight

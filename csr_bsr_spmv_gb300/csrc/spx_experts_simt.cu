@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) experts_simt_kernel(SimtGemm g, Gate
                 if constexpr (EPI == kNone) {
                     *c = from_f<O>(acc[a][b]);
                 } else if constexpr (EPI == kGate) {
-                    *c = from_f<O>(e < g.E ? act_of<ACT>(acc[a][b]) * up[a][b] : 0.f);
+                    *c = from_f<O>(e < g.E ? act_of<ACT>(make_float2(acc[a][b], 0.f)).x * up[a][b] : 0.f);
                     if (gate.H) {
                         V* h = static_cast<V*>(gate.H) + i * gate.ldh + j0 + j;
                         h[0] = from_f<V>(acc[a][b]);
@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(kThreads) experts_simt_kernel(SimtGemm g, Gate
                     float dg = 0.f, du = 0.f, out = 0.f;
                     if (e < g.E) {  // rows past the last expert's are zeros, whatever H holds there
                         const float u = to_f(load(h + g.NJ));
-                        float slope;
-                        const float act = act_of<ACT>(to_f(load(h)), slope);
-                        dg = acc[a][b] * u * slope, du = acc[a][b] * act, out = act * u;
+                        float2 slope;
+                        const float act = act_of<ACT>(make_float2(to_f(load(h)), 0.f), slope).x;
+                        dg = acc[a][b] * u * slope.x, du = acc[a][b] * act, out = act * u;
                     }
                     V* d = static_cast<V*>(gate.dH) + i * gate.lddh + j0 + j;
                     d[0] = from_f<V>(dg);

@@ -68,6 +68,8 @@ constexpr int kMaxStages = 12;
 constexpr int kExact = 1024;
 constexpr int kBand = 8;                        // row tiles that run side by side before the next lane tile
 constexpr size_t kSmemMax = 224 * 1024;         // dynamic shared memory of a CTA
+template <bool SPLIT, int EPI>
+constexpr size_t kSmemOf = EPI == kGateGrad && !SPLIT ? 226 * 1024 : kSmemMax;  // leaves the gate's gradient six stages of pairs
 // Cycles of a wait, about a second; and as some waits last as long as a tile's
 // reduction (the storing warps', a pair's second CTA's for the last stage, those
 // of CTAs that share a reduction for each other), so many more for each of its
@@ -460,7 +462,10 @@ __device__ __forceinline__ void store_gated(const TcArgs& a, const Item& it, int
     float f[16];
     with_act(a.gate.act, [&](auto kind) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = act_of<decltype(kind)::value>(v[i]) * v[16 + i];
+        for (int i = 0; i < 16; i += 2) {
+            const float2 c = __fmul2_rn(act_of<decltype(kind)::value>(make_float2(v[i], v[i + 1])), make_float2(v[16 + i], v[17 + i]));
+            f[i] = c.x, f[i + 1] = c.y;
+        }
     });
     if constexpr (sizeof(O) == 2) {
         if (a.wide_c) {
@@ -502,7 +507,10 @@ __device__ __forceinline__ void store_gate(const TcArgs& a, const Item& it, int 
 // factors are copied ahead of the sums into the warp's two patches of shared
 // memory, reach the fragments' order by ldmatrix, and what goes out takes the
 // same way back.
-constexpr uint32_t kFactorBytes = 16 * kPatchPitch;
+// A patch is 16 rows of 64 bytes; piece p of row r lies at p ^ (r / 2 % 4), so that neither eight rows of one piece nor
+// whole rows share banks.
+constexpr uint32_t kFactorPitch = 64, kFactorBytes = 16 * kFactorPitch;
+__device__ __forceinline__ uint32_t factor_at(int r, int p) { return r * kFactorPitch + 16 * (p ^ (r >> 1 & 3)); }
 
 // Where a thread reads and writes whole pieces (r = lane / 4, p = lane % 4: rows r and r + 8, columns 8 p to 8 p + 7 of
 // a warp's chunk), stepped from chunk to chunk.
@@ -529,8 +537,8 @@ struct Pieces {
         for (int i = 0; i < 2; ++i) {
             if (live && 8 * i < left) {
                 const uint16_t* q = h + i * 8 * a.gate.ldh;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 8 * kPatchPitch), "l"(q) : "memory");
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 8 * kPatchPitch + kFactorBytes), "l"(q + a.NL) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 8 * kFactorPitch), "l"(q) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 8 * kFactorPitch + kFactorBytes), "l"(q + a.NL) : "memory");
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -540,8 +548,8 @@ struct Pieces {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             uint4 w;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(from + i * 8 * kPatchPitch) : "memory");
-            if (8 * i < left) *reinterpret_cast<uint4*>(to + i * 8 * ld) = w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(from + i * 8 * kFactorPitch) : "memory");
+            if (8 * i < left) __stcs(reinterpret_cast<uint4*>(to + i * 8 * ld), w);
         }
     }
 };
@@ -560,7 +568,7 @@ __device__ __forceinline__ void load_frag16(uint32_t taddr, uint32_t (&v)[16]) {
 // Columns 16 h to 16 h + 15 of a patch's 16 rows as fragments, and back: q[m] holds rows 8 (m % 2) + 2 (t % 4) and the
 // next of column 16 h + 8 (m / 2) + t / 4.
 __device__ __forceinline__ uint32_t frag_addr(uint32_t patch, int lane, int h) {
-    return patch + ((lane >> 3 & 1) * 8 + (lane & 7)) * kPatchPitch + 32 * h + 16 * (lane >> 4);
+    return patch + factor_at((lane >> 3 & 1) * 8 + (lane & 7), 2 * h + (lane >> 4));
 }
 __device__ __forceinline__ void frag_out(uint32_t at, uint32_t (&q)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -572,20 +580,20 @@ __device__ __forceinline__ void frag_in(uint32_t at, const uint32_t (&q)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3])
                  : "memory");
 }
-// dG, dU and C of one output.
+// dG, dU and C of two outputs.
 template <int ACT>
-__device__ __forceinline__ void gate_grad(float dc, float g, float u, float& dg, float& du, float& c) {
-    float slope;
-    const float act = act_of<ACT>(g, slope);
-    dg = dc * u * slope;
-    du = dc * act;
-    c = act * u;
+__device__ __forceinline__ void gate_grad(float2 dc, float2 g, float2 u, float2& dg, float2& du, float2& c) {
+    float2 slope;
+    const float2 act = act_of<ACT>(g, slope);
+    dg = __fmul2_rn(__fmul2_rn(dc, u), slope);
+    du = __fmul2_rn(dc, act);
+    c = __fmul2_rn(act, u);
 }
 
 // 16 rows on wide rows.  The rows past the last expert's are zeros: their sums are, and so is what stands for H.
 template <class V, int ACT>
 __device__ __forceinline__ void store_gate_grad(const TcArgs& a, const Pieces& at, int lane, uint32_t patch, const uint32_t (&v)[16]) {
-    const uint32_t piece = patch + (lane >> 2) * kPatchPitch + 16 * (lane & 3);
+    const uint32_t piece = patch + factor_at(lane >> 2, lane & 3);  // rows r and r + 8 have the same place
     uint32_t c[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -597,10 +605,8 @@ __device__ __forceinline__ void store_gate_grad(const TcArgs& a, const Pieces& a
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const int i = 8 * h + 4 * (m & 1) + 2 * (m >> 1);
-            const float2 fg = widen2<V>(g[m]), fu = widen2<V>(u[m]);
             float2 a0, a1, a2;
-            gate_grad<ACT>(__uint_as_float(v[i]), fg.x, fu.x, a0.x, a1.x, a2.x);
-            gate_grad<ACT>(__uint_as_float(v[i + 1]), fg.y, fu.y, a0.y, a1.y, a2.y);
+            gate_grad<ACT>(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), widen2<V>(g[m]), widen2<V>(u[m]), a0, a1, a2);
             g[m] = pack<V>(a0.x, a0.y), u[m] = pack<V>(a1.x, a1.y), c[h][m] = pack<V>(a2.x, a2.y);
         }
         __syncwarp();
@@ -633,13 +639,14 @@ __device__ __forceinline__ void store_gate_grad_narrow(const TcArgs& a, const It
     for (int i = 0; i < 16; ++i) {
         const int n = 16 * (i >> 3) + (lane >> 2) + 8 * ((i >> 1) & 1), r = 8 * ((i >> 2) & 1) + 2 * (lane & 3) + (i & 1);
         if (n >= cols || r >= rows) continue;
-        float dg, du, c;
+        float2 dg, du, c;
         const V* p = H + r * a.gate.ldh + n;
-        gate_grad<ACT>(__uint_as_float(v[i]), live ? to_f(load(p)) : 0.f, live ? to_f(load(p + a.NL)) : 0.f, dg, du, c);
+        gate_grad<ACT>(make_float2(__uint_as_float(v[i]), 0.f), make_float2(live ? to_f(load(p)) : 0.f, 0.f),
+                       make_float2(live ? to_f(load(p + a.NL)) : 0.f, 0.f), dg, du, c);
         V* d = dH + r * a.gate.lddh + n;
-        d[0] = from_f<V>(dg);
-        d[a.NL] = from_f<V>(du);
-        if (a.C) C[r * a.ldc + n] = from_f<V>(c);
+        d[0] = from_f<V>(dg.x);
+        d[a.NL] = from_f<V>(du.x);
+        if (a.C) C[r * a.ldc + n] = from_f<V>(c.x);
     }
 }
 
@@ -677,7 +684,10 @@ __device__ __forceinline__ void gate_four(const TcArgs& a, const Item& it, int r
     for (int i = 0; i < 4; ++i) u[i] = __shfl_xor_sync(0xffffffffu, f[i], 4);
     with_act(a.gate.act, [&](auto kind) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = act_of<decltype(kind)::value>(f[i]) * u[i];
+        for (int i = 0; i < 4; i += 2) {
+            const float2 r = __fmul2_rn(act_of<decltype(kind)::value>(make_float2(f[i], f[i + 1])), make_float2(u[i], u[i + 1]));
+            c[i] = r.x, c[i + 1] = r.y;
+        }
     });
     if (a.gate.H) {
         const long long at = row * a.gate.ldh + x + (up ? a.NL : 0);
@@ -708,7 +718,11 @@ __device__ __forceinline__ void gate_grad_four(const TcArgs& a, const Item& it, 
     }
     with_act(a.gate.act, [&](auto kind) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) gate_grad<decltype(kind)::value>(f[i], g[i], u[i], dg[i], du[i], c[i]);
+        for (int i = 0; i < 4; i += 2) {
+            float2 a0, a1, a2;
+            gate_grad<decltype(kind)::value>(make_float2(f[i], f[i + 1]), make_float2(g[i], g[i + 1]), make_float2(u[i], u[i + 1]), a0, a1, a2);
+            dg[i] = a0.x, dg[i + 1] = a0.y, du[i] = a1.x, du[i + 1] = a1.y, c[i] = a2.x, c[i + 1] = a2.y;
+        }
     });
     V* d = static_cast<V*>(a.gate.dH) + row * a.gate.lddh + x;
     put_four(d, left, a.wide_h, dg);
@@ -1255,26 +1269,17 @@ __global__ void __launch_bounds__(kThreadsOf<SPLIT, FUSE, EPI>, 1)
         };
         if constexpr (EPI == kGateGrad && !SPLIT) {
             const int first = 16 * (warp >> 2), x0 = 128 * rank + 32 * (warp & 3);
-            const uint32_t piece = patch + (lane >> 2) * kPatchPitch + 16 * (lane & 3);
+            const uint32_t piece = patch + factor_at(lane >> 2, lane & 3);  // rows r and r + 8 have the same place
             Item it{};
             Pieces at{};
-            // the first rows' factors of the next tile, while this warp has none to wait for; its other rows' to L2
+            // the first rows' factors of the next tile, while this warp has none to wait for (its other rows' fetched to L2 as
+            // well: 249 us for 242)
             auto begin = [&](int t) {
                 if (t >= ntiles) return;
                 it = tile_item<MODE, CG>(a, list, t);
                 if (!a.wide_h || first >= it.rows) return;
                 at.start(a, it, it.lane0 + x0, lane, first);
                 at.fetch(a, piece);
-                if (at.live && (lane & 3) == 0)
-                    for (int i = 4 * SW; i < at.left; i += 4 * SW) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if (i + 8 * j >= at.left) break;
-                            const uint16_t* q = at.h + (i + 8 * j) * a.gate.ldh;
-                            asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
-                            asm volatile("prefetch.global.L2 [%0];" ::"l"(q + a.NL));
-                        }
-                    }
             };
             begin(me);
             for (int t = me; t < ntiles; t += G) {
@@ -1532,7 +1537,7 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
     const int team = SPLIT ? a.split : CG;  // CTAs that work on one tile
     a.part_off = static_cast<uint32_t>((list_bytes(a.E) + 15) / 16 * 16);
     const size_t list = a.part_off + (SPLIT ? a.TN * kPartPitch : kStoreWarpsOf<SPLIT, EPI> * (EPI == kGateGrad ? 2 * kFactorBytes : kPatchBytes));
-    size_t room = kSmemMax - 1024 - list;
+    size_t room = kSmemOf<SPLIT, EPI> - 1024 - list;
     if (FUSE) {  // stages for the MMAs, more than the widening warps fill at once where there is room, and raw ones
         a.stages = a.TN > 64 ? 2 : 4;
         room -= a.stages * a.stage_bytes;
@@ -1543,7 +1548,7 @@ spx_status launch(const CUtensorMap& tl, const CUtensorMap& tc, TcArgs a, long l
         room = 0;
     }
     const size_t smem = 1024 + static_cast<size_t>(a.stages) * a.stage_bytes + room + list;
-    if (set_smem_limit(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE, EPI>, kSmemMax) != cudaSuccess) return SPX_ERR_CUDA;
+    if (set_smem_limit(experts_tc_kernel<MODE, CG, I8, SPLIT, FUSE, EPI>, kSmemOf<SPLIT, EPI>) != cudaSuccess) return SPX_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreadsOf<SPLIT, FUSE, EPI>);
     cfg.dynamicSmemBytes = smem;
