@@ -1657,7 +1657,7 @@ spx_status tc_gated_grad(int E, int S, int F, int N, const int* offsets, const v
     a.gate = gate, a.h_type = type;
     a.wide_h = rows_aligned(gate.H, gate.ldh) && rows_aligned(gate.dH, gate.lddh) && F % 8 == 0 && (!C || rows_aligned(C, ldc));
     a.same_w = E == 1 || stride_w == 0;
-    const int cg = take_tile(a, kProduct, F);
+    const int cg = take_tile(a, kGateBack, F);
     a.stage_bytes = kLaneBytes + static_cast<uint32_t>(a.TN / cg) * kDepth * 2;
     a.idesc = idesc_of(type, nk ? kNK : kKN, cg);
     CUtensorMap tl, tc;

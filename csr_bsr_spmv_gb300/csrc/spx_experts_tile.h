@@ -10,7 +10,7 @@ namespace spx_exp {
 constexpr int kDepth = 64;      // reduction length of a stage: one 128-byte swizzle row of 16-bit values
 constexpr int kRawDepth = 128;  // kCodes: reduction length of a raw stage, one 128-byte row
 
-enum Kind : int { kProduct, kGradient, kCodes };  // kCodes: 8-bit factors widened on the way
+enum Kind : int { kProduct, kGradient, kCodes, kGateBack };  // kCodes: 8-bit factors widened on the way; kGateBack: the gate's gradient behind the sums
 
 struct Tile {
     int tn = 0;         // output rows
@@ -29,7 +29,8 @@ struct Tile {
 // row) run beside the next tile's MMAs; rounds of tiles count whole.  Sharing a
 // reduction costs about 1500 cycles a CTA for the exchange.  512 rows x 4096 x
 // 4096: 128-row tiles 19 us, 256-row pairs 25, 64-row tiles 30; 16 rows: one
-// CTA a tile 16.5 us, two 13.0, four 11.6, eight 16.1.
+// CTA a tile 16.5 us, two 13.0, four 11.6, eight 16.1.  The gate's gradient
+// takes 70 cycles a row for its stores, which a few tiles do not hide.
 inline Tile choose_tile(Kind kind, int E, int S, int NL, int NC, int NR, int sms) {
     const bool wgrad = kind == kGradient, fused = kind == kCodes;
     struct Shape {
@@ -58,7 +59,11 @@ inline Tile choose_tile(Kind kind, int E, int S, int NL, int NC, int NR, int sms
         for (int split = 1; split <= 8; split *= 2) {
             if (split > 1 && (wgrad || sh.cg > 1 || sh.tn > 128 || tiles * split > slots)) break;
             const double rounds = tiles * split <= slots ? 1 : tiles / slots < 4 ? static_cast<int>(tiles / slots + 0.99) : tiles / slots;
-            const double cycles = rounds * (std::max(stages / split * sh.stage, 12.0 * sh.tn) + 600) + (split > 1 ? 1500 * split : 0);
+            double cycles = rounds * (std::max(stages / split * sh.stage, 12.0 * sh.tn) + 600) + (split > 1 ? 1500 * split : 0);
+            if (kind == kGateBack) {
+                const double sums = stages / split * sh.stage, store = 70.0 * sh.tn / split;
+                cycles = rounds * (std::max(sums, store) + 600) + std::min(sums, store) + (split > 1 ? 1500 * split : 0);
+            }
             if (best == 0 || cycles < best) best = cycles, pick = sh, t.split = split;
         }
     }
