@@ -77,18 +77,27 @@ def counts_of(load, E, S):
     return list(rng.multinomial(S - S // 10, share))  # the last tenth belongs to no expert
 
 
-def check(load, E, S, F, R, dtype, act, layout, pad=0, out=None):
-    counts = counts_of(load, E, S)
+def forward(counts, F, K, dtype, act, pad=0, out=None):
+    """The product of all experts, checked; both factors."""
+    E, S = len(counts), int(sum(counts) + sum(counts) // 9)
     off = offsets_of(counts)
-    A, W = padded(normal(S, S, R, dtype=dtype), pad), padded(normal(F, E, 2 * F, R, dtype=dtype, scale=R ** -0.5), pad)
+    A, W = padded(normal(S, S, K, dtype=dtype), pad), padded(normal(F, E, 2 * F, K, dtype=dtype, scale=K ** -0.5), pad)
     C, H = spx.spx_gemm_grouped_gated(off, A, W, act=act, grad=True, dtype=out)
     c, ec, h, eh = forward64(counts, A, W, act)
     close(H, h, eh, "H")
     close(C, c, ec, "C")
     again, none = spx.spx_gemm_grouped_gated(off, A, W, act=act, dtype=out)
     assert none is None and torch.equal(again, C)
-    dY = padded(normal(R, S, R, dtype=dtype), pad)
-    W2 = normal(E, E, R, F, dtype=dtype, scale=F ** -0.5)
+    assert not C[sum(counts):].any() and not H[sum(counts):].any()
+    assert spx.spx_last_device_error() == 0
+    return H
+
+
+def backward(counts, N, dtype, act, layout, H, pad=0):
+    E, S, F = len(counts), H.shape[0], H.shape[1] // 2
+    off = offsets_of(counts)
+    dY = padded(normal(N, S, N, dtype=dtype), pad)
+    W2 = normal(E, E, N, F, dtype=dtype, scale=F ** -0.5)
     W2 = padded(W2 if layout == "kn" else W2.transpose(1, 2).contiguous(), pad)
     Hn = H.clone()
     Hn[sum(counts):] = float("nan")  # what lies behind the last expert's rows does not matter
@@ -99,8 +108,13 @@ def check(load, E, S, F, R, dtype, act, layout, pad=0, out=None):
     close(C2, c, ec, "C again")
     only, none = spx.spx_gemm_grouped_gated_grad(off, dY, W2, Hn, act=act, layout=layout, product=False)
     assert none is None and torch.equal(only, dH)
-    assert not C[sum(counts):].any() and not H[sum(counts):].any() and not dH[sum(counts):].any() and not C2[sum(counts):].any()
+    assert not dH[sum(counts):].any() and not C2[sum(counts):].any()
     assert spx.spx_last_device_error() == 0
+
+
+def check(load, E, S, F, R, dtype, act, layout, pad=0, out=None):
+    counts = counts_of(load, E, S)
+    backward(counts, R, dtype, act, layout, forward(counts, F, R, dtype, act, pad, out), pad)
 
 
 @pytest.mark.parametrize("load,E,S,F,R", [("even", 1, 1, 1, 1), ("even", 1, 11, 16, 64), ("uneven", 3, 40, 24, 72), ("one", 4, 33, 72, 64),

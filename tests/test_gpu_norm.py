@@ -34,7 +34,7 @@ def grad64(dY, S, rstd, w, dS):
 
 
 SIZES = [(1, 1), (1, 4096), (3, 7), (2, 64), (1, 128), (5, 130), (700, 128), (33, 1002), (2, 1031), (64, 2048), (3, 4096), (1217, 72),
-         (9, 4097), (2, 5000), (4, 8192), (2, 16384), (3, 16385), (2, 20000), (1, 32768), (40000, 16), (3000, 4104)]
+         (9, 4097), (2, 5000), (4, 8192), (2, 16384), (3, 16385), (2, 20000), (1, 32768), (40000, 16), (3000, 4104), (5, 8195), (500, 33), (3, 20001), (2, 9001), (2, 32767)]
 
 
 @pytest.mark.parametrize("M,H", SIZES)
@@ -76,7 +76,7 @@ def test_gradient_is_the_formula(M, H, dtype, residual):
 
 @pytest.mark.parametrize("dtype,wide", [(F32, False), (BF16, False), (BF16, True), (F16, True)])
 @pytest.mark.parametrize("pad", [1, 2, 4, 8, 24])
-@pytest.mark.parametrize("H", [264, 1002])
+@pytest.mark.parametrize("H", [264, 1002, 5, 4500])
 def test_pitches_and_bases_of_any_alignment(dtype, wide, pad, H):
     M = 37
     X, R, dY = (padded(normal(i, M, H, dtype=dtype), pad) for i in range(3))
@@ -101,10 +101,11 @@ def test_pitches_and_bases_of_any_alignment(dtype, wide, pad, H):
         assert torch.equal(between(t, pad).nan_to_num(5), e.nan_to_num(5))
 
 
-@pytest.mark.parametrize("H", [40, 1000, 6000])
+@pytest.mark.parametrize("H", [7, 40, 41, 1000, 1001, 1002, 4095, 6000, 6001, 9001, 16401, 20000])
 def test_outputs_over_their_inputs(H):
-    """S over R, Y over X; dX over dY, over dS and over S."""
-    X, R, w = normal(1, 50, H, dtype=BF16), normal(2, 50, H, dtype=BF16), normal(3, H, dtype=BF16)
+    """S over R, Y over X; dX over dY, over dS and over S: rows on 16- and 4-byte boundaries and on neither."""
+    M = 900 if H < 2000 else 320
+    X, R, w = normal(1, M, H, dtype=BF16), normal(2, M, H, dtype=BF16), normal(3, H, dtype=BF16)
     Y, S, rstd = spx.spx_rms_norm(X, w, R, grad=True)
     x, r = X.clone(), R.clone()
     spx.spx_rms_norm(x, w, r, Y=x, S=r)
@@ -115,7 +116,7 @@ def test_outputs_over_their_inputs(H):
     r = R.clone()
     Q, scale, _ = spx.spx_rms_norm_i8(X, w, r, S=r)
     assert torch.equal(r, S) and torch.equal(Q, spx.spx_rms_norm_i8(X, w, R)[0])
-    dY, dS = normal(4, 50, H, dtype=BF16), normal(5, 50, H, dtype=BF16)
+    dY, dS = normal(4, M, H, dtype=BF16), normal(5, M, H, dtype=BF16)
     dX, dw = spx.spx_rms_norm_grad(dY, S, rstd, w, dS=dS)
     for i in range(3):
         t = [dY.clone(), S.clone(), dS.clone()]
