@@ -4,7 +4,7 @@
 //   s = x + r,  rstd = 1 / sqrt(mean(s^2) + eps),  y = s rstd w
 //   d s = rstd (dy w) - s rstd^3 mean(dy w s) + dS,  d w = sum over rows of dy s rstd
 //
-// Every row is read once and stays in registers, 16 values a thread, between
+// Every row is read once and stays in registers, 16 or 32 values a thread, between
 // the sum over it and what is written from it, so both kernels are bound by
 // HBM.
 #include <algorithm>
@@ -17,7 +17,8 @@ using namespace spx_rows;
 
 namespace {
 
-// Values of a row that a thread holds; twice as many for rows longer than a CTA's threads hold so, at the cost of spills.
+// Values of a row that a thread holds; twice as many where that pays (norm_launch) and for rows longer than a CTA's threads
+// hold so.
 constexpr int kHeld = 16;
 constexpr int kThreads = 256, kMostThreads = 1024;
 
@@ -33,7 +34,7 @@ struct NormArgs {
 
 // The row's quotients y / s as codes (ties to even); a row that holds an infinity or NaN has codes 0.
 template <class V, class O, int N, bool ANY, int HELD, int MAXT>
-__global__ void __launch_bounds__(MAXT, ANY || MAXT > kThreads ? 1024 / MAXT : 5) rms_norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(MAXT, ANY || MAXT > kThreads || HELD > kHeld ? 1024 / MAXT : 5) rms_norm_kernel(NormArgs a) {
     constexpr int P = HELD / N, X = (N + 1) / 2;
     using Piece = Pack<V, N>;
     __shared__ __align__(16) float s_sum[MAXT / 32];
@@ -456,9 +457,21 @@ spx_status check(int32_t M, int32_t H, spx_type type, spx_type w_type) {
 
 template <class V, class O, int N, bool ANY>
 cudaError_t norm_launch(NormArgs a, cudaStream_t st) {
+    if constexpr (sizeof(V) == 2 && N == 8 && !ANY) {
+        // Where rows fill the SMs anyway, half the threads with twice the values each: what a thread does once a row weighs
+        // less (16384 x 4096 bf16 to 8 bits 86 us and 79, without a residual 73 and 58, 8192 x 8192 bf16 87 and 81; fp32
+        // and 4-byte pieces are faster with more threads).
+        int lg = 2;
+        while ((2 * kHeld << lg) < a.H) ++lg;
+        if ((1 << lg) <= kThreads && static_cast<long long>(a.M) << lg >= 152 * 1024) {
+            a.log_g = lg;
+            const int per = kThreads >> lg;
+            return launch_early(rms_norm_kernel<V, O, N, ANY, 2 * kHeld, kThreads>, dim3((a.M - 1) / per + 1), kThreads, 0, 1, st, a);
+        }
+    }
     a.log_g = threads_log(a.M, a.H, (a.H + N - 1) / N);
     const int threads = std::max(kThreads, 1 << a.log_g), per = threads >> a.log_g;
-    const dim3 grid((a.M + per - 1) / per);
+    const dim3 grid((a.M - 1) / per + 1);
     if (threads == kThreads) return launch_early(rms_norm_kernel<V, O, N, ANY, kHeld, kThreads>, grid, threads, 0, 1, st, a);
     return launch_early(a.H <= kHeld * kMostThreads ? rms_norm_kernel<V, O, N, ANY, kHeld, kMostThreads> : rms_norm_kernel<V, O, N, ANY, 2 * kHeld, kMostThreads>, grid,
                         threads, 0, 1, st, a);
