@@ -415,11 +415,15 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(SumArgs a) {
     part += 2LL * blockIdx.x * a.ldp + static_cast<long long>(v) * N;
     auto row = [&](const float* p) { return load_floats<float, N>(p, true, 0); };
     acc = row(part + a.ldp);
-#pragma unroll 16
-    for (int c = 1; c <= chunks; ++c) {
-        const Floats<N> f = row(part + 2LL * c * a.ldp);
+    constexpr int kAhead = 8;  // rows in flight, also where there are fewer left: past the end the last again, not added
+    for (int c0 = 1; c0 <= chunks; c0 += kAhead) {
+        Floats<N> f[kAhead];
 #pragma unroll
-        for (int i = 0; i < X; ++i) acc.v[i] = __fadd2_rn(acc.v[i], f.v[i]);
+        for (int u = 0; u < kAhead; ++u) f[u] = row(part + 2LL * min(c0 + u, chunks) * a.ldp);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int i = 0; i < X; ++i) acc.v[i] = c0 + u <= chunks ? __fadd2_rn(acc.v[i], f[u].v[i]) : acc.v[i];
     }
     write_sum<O, N>(a, id, v, acc);
 }

@@ -422,10 +422,15 @@ __global__ void __launch_bounds__(kAddThreads) add_parts_kernel(int H, int block
     wait_for_previous();
     part = behind_wait(part);
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    constexpr int kAhead = 8;  // loads in flight, also where there are fewer left: past the end the last again, not added
+    const float* q = part + min(c, H - 1);
     float sum = 0.f;
-    if (c < H) {
-#pragma unroll 16
-        for (int b = w; b < blocks; b += kAddThreads / 32) sum += load(part + static_cast<long long>(b) * H + c);
+    for (int b0 = w; b0 < blocks; b0 += kAhead * (kAddThreads / 32)) {
+        float x[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) x[i] = load(q + static_cast<long long>(min(b0 + i * (kAddThreads / 32), blocks - 1)) * H);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) sum += b0 + i * (kAddThreads / 32) < blocks ? x[i] : 0.f;
     }
     s[w][threadIdx.x & 31] = sum;
     __syncthreads();
