@@ -902,6 +902,9 @@ def _raw_stream(stream, like: torch.Tensor, *others):
     return stream.cuda_stream
 
 
+_MOST = 2 ** 31 - 1  # sizes are int32 in the library; a larger one would arrive there as another
+
+
 def _mat(t: torch.Tensor, what: str):
     """(rows, columns, row pitch, address) of a 2-D device operand whose columns are adjacent."""
     try:
@@ -911,6 +914,8 @@ def _mat(t: torch.Tensor, what: str):
     ld, unit = t.stride()
     if (unit != 1 and m > 1) or not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor with unit column stride")
+    if n > _MOST or m > _MOST:
+        raise ValueError(f"{what} has more than 2^31 - 1 rows or columns")
     return n, m, ld if n > 1 else max(m, ld), t.data_ptr() if n and m else None
 
 
@@ -1061,6 +1066,8 @@ def _experts(W: torch.Tensor, what: str):
     se, ld, unit = W.stride()
     if (unit != 1 and m > 1) or not W.is_cuda:
         raise ValueError(f"{what} must be a device tensor with unit stride in its last axis")
+    if E > _MOST or n > _MOST or m > _MOST:
+        raise ValueError(f"{what} has more than 2^31 - 1 experts, rows or columns")
     return E, n, m, ld if n > 1 else max(m, ld), se if E > 1 else 0, W.data_ptr() if E and n and m else None
 
 
@@ -1341,6 +1348,8 @@ def _ids(ids: torch.Tensor):
     if dt != torch.int64 and dt != _I32:
         raise ValueError("token ids must be int32 or int64")
     T = ids.numel()
+    if T > _MOST:
+        raise ValueError("more than 2^31 - 1 token ids")
     return T, _vec(ids, T, dt, "ids"), 4 if dt == _I32 else 8
 
 
@@ -1367,13 +1376,17 @@ def spx_embed_grad(ids: torch.Tensor, dY: torch.Tensor, V: int, scale: float = 1
         raise ValueError("dY needs one row a token")
     if accumulate and dW is None:
         raise ValueError("accumulate needs dW")
+    if not 0 <= V <= _MOST:
+        raise ValueError("V must be 0 to 2^31 - 1")
+    if padding is None or not 0 <= padding < V:
+        padding = -1
     code = _type(dY)
     dW, lddw, dw = _out(dW, V, H, (dtype or dY.dtype) if dW is None else dtype, dY, "dW", stream)
     lib = _lib()
     need = _embed_scratch(lib, T, H)
     if scratch is None:
         scratch = _new(need, torch.uint8, dY, stream)
-    rc = lib.spx_embed_grad(T, H, V, code, at, size, -1 if padding is None else padding, scale, dy, lddy, dw, lddw,
+    rc = lib.spx_embed_grad(T, H, V, code, at, size, padding, scale, dy, lddy, dw, lddw,
                             _type(dW), int(accumulate), scratch.data_ptr(), scratch.numel() * scratch.element_size(),
                             _raw_stream(stream, dY, ids, dW, scratch))
     if rc:
