@@ -50,7 +50,8 @@ __device__ __forceinline__ float2 cut(float2 x, float most) {
 // below 1e-38.  Two values at a time, as everything here: most of it is one
 // instruction for both.
 __device__ __forceinline__ float2 logistic(float2 z) {
-    constexpr float L = 1.44269502f, rest = 1.92596303e-8f;  // log2(e) = L + rest
+    constexpr double log2e = 1.4426950408889634;
+    constexpr float L = static_cast<float>(log2e), rest = static_cast<float>(log2e - static_cast<double>(L));
     const float2 t = __fmul2_rn(z, both(-L)), d = __ffma2_rn(z, both(rest), __ffma2_rn(z, both(L), t));
     float2 e, p;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
