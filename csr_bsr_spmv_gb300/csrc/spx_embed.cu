@@ -311,21 +311,23 @@ template <class V, class O, int N>
 __global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(SumArgs a) {
     constexpr int X = (N + 1) / 2;
     using Piece = Pack<V, N>;
+    // the threads' slots; the tokens of the chunk's places; the ids of them, of the one before and the one after
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ int s_id[kMostChunk + 2], s_at[kMostChunk];  // ids of the chunk's places, of the one before and the one after; tokens
+    const int threads = blockDim.x;
+    int *s_at = reinterpret_cast<int*>(ring + sizeof(Piece) * kSets * kRows * threads), *s_id = s_at + a.chunk;
     let_next_start();
     wait_for_previous();
     const int *order = behind_wait(a.order), *sid = behind_wait(a.sid);
     const long long first = static_cast<long long>(blockIdx.x) * a.chunk;
     const int p0 = static_cast<int>(first), most = static_cast<int>(min(first + a.chunk, static_cast<long long>(a.T)));
     // places past the last token's hold anything: they are looked at with the number of tokens in hand
-    for (int i = threadIdx.x; i < most - p0 + 2; i += kThreads) {
+    for (int i = threadIdx.x; i < most - p0 + 2; i += threads) {
         const int p = p0 - 1 + i;
         s_id[i] = p >= 0 && p < a.T ? load(sid + p) : -1;
         if (i < most - p0) s_at[i] = load(order + p0 + i);
     }
     const int kept = load(behind_wait(a.kept)), n = min(most, kept) - p0;  // n: places of this chunk
-    const int v = blockIdx.y * kThreads + threadIdx.x;
+    const int v = blockIdx.y * threads + threadIdx.x;
     __syncthreads();
     if (n <= 0 || v >= a.np) return;
     const V* dY = behind_wait(static_cast<const V*>(a.dY)) + static_cast<long long>(v) * N;
@@ -335,13 +337,13 @@ __global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(SumArgs a) {
         const int rows = min(kRows, n - p);
         if constexpr (sizeof(Piece) >= 4) {
 #pragma unroll 4
-            for (int u = 0; u < rows; ++u) copy_piece(slots + (set * kRows + u) * kThreads, reinterpret_cast<const Piece*>(dY + s_at[p + u] * a.lddy));
+            for (int u = 0; u < rows; ++u) copy_piece(slots + (set * kRows + u) * threads, reinterpret_cast<const Piece*>(dY + s_at[p + u] * a.lddy));
         } else {
             Piece x[kRows];
 #pragma unroll
             for (int u = 0; u < kRows; ++u) x[u] = load(reinterpret_cast<const Piece*>(dY + s_at[max(0, min(p + u, n - 1))] * a.lddy));
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) write_piece(slots + (set * kRows + u) * kThreads, stay(x[u]));
+            for (int u = 0; u < kRows; ++u) write_piece(slots + (set * kRows + u) * threads, stay(x[u]));
         }
         if (a.add)  // what the sums will be added to
             for (int u = 0; u < rows; ++u) asm volatile("prefetch.global.L2 [%0];" ::"l"(dW + s_id[p + u + 1] * a.ldw));
@@ -356,9 +358,9 @@ __global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(SumArgs a) {
     for (int p = 0; p < n; p += kRows) {
         fetch(p + (kSets - 1) * kRows, set == 0 ? kSets - 1 : set - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kSets - 1) : "memory");
-        const Piece* x = slots + set * kRows * kThreads;
+        const Piece* x = slots + set * kRows * threads;
 #pragma unroll 1
-        for (int u = 0; u < min(kRows, n - p); ++u, x += kThreads) {
+        for (int u = 0; u < min(kRows, n - p); ++u, x += threads) {
             const Floats<N> f = floats(read_piece(x));
 #pragma unroll
             for (int i = 0; i < X; ++i) acc.v[i] = __fadd2_rn(acc.v[i], f.v[i]);
@@ -388,15 +390,17 @@ __global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(SumArgs a) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// One block for each chunk whose last id began in it and goes on after it.
+// One block for each chunk whose last id began in it and goes on after it.  Groups of 2^log_g threads hold the row; where
+// that is less than a block, each takes every so many of the chunks, and they are added in the groups' order.
 template <class O, int N>
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(SumArgs a) {
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(SumArgs a, int log_g) {
     constexpr int X = (N + 1) / 2;
+    __shared__ Floats<N> s_sum[kThreads];
     let_next_start();
     wait_for_previous();
     const int* sid = behind_wait(a.sid);
     const float* part = behind_wait(static_cast<const float*>(a.part));
-    const int v = blockIdx.y * kThreads + threadIdx.x;
+    const int G = 1 << log_g, groups = kThreads >> log_g, mine = threadIdx.x >> log_g, v = blockIdx.y * G + (threadIdx.x & (G - 1));
     const long long p0 = static_cast<long long>(blockIdx.x) * a.chunk, p1 = p0 + a.chunk;
     if (p1 >= a.T) return;
     // places past the last token's hold anything
@@ -410,22 +414,32 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(SumArgs a) {
         chunks += more;
         if (more < kThreads) break;
     }
-    if (v >= a.np) return;
     Floats<N> acc;
-    part += 2LL * blockIdx.x * a.ldp + static_cast<long long>(v) * N;
-    auto row = [&](const float* p) { return load_floats<float, N>(p, true, 0); };
-    acc = row(part + a.ldp);
-    constexpr int kAhead = 8;  // rows in flight, also where there are fewer left: past the end the last again, not added
-    for (int c0 = 1; c0 <= chunks; c0 += kAhead) {
-        Floats<N> f[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) f[u] = row(part + 2LL * min(c0 + u, chunks) * a.ldp);
+    for (int i = 0; i < X; ++i) acc.v[i] = make_float2(0.f, 0.f);
+    if (v < a.np) {
+        part += 2LL * blockIdx.x * a.ldp + static_cast<long long>(v) * N;
+        auto row = [&](const float* p) { return load_floats<float, N>(p, true, 0); };
+        if (mine == 0) acc = row(part + a.ldp);
+        constexpr int kAhead = 8;  // rows in flight, also where there are fewer left: past the end the last again, not added
+        for (int c0 = 1 + mine; c0 <= chunks; c0 += kAhead * groups) {
+            Floats<N> f[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
+            for (int u = 0; u < kAhead; ++u) f[u] = row(part + 2LL * min(c0 + u * groups, chunks) * a.ldp);
 #pragma unroll
-            for (int i = 0; i < X; ++i) acc.v[i] = c0 + u <= chunks ? __fadd2_rn(acc.v[i], f[u].v[i]) : acc.v[i];
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int i = 0; i < X; ++i) acc.v[i] = c0 + u * groups <= chunks ? __fadd2_rn(acc.v[i], f[u].v[i]) : acc.v[i];
+        }
     }
-    write_sum<O, N>(a, id, v, acc);
+    if (groups > 1) {
+        s_sum[threadIdx.x] = acc;
+        __syncthreads();
+        for (int g = 1; g < groups && mine == 0; ++g)
+#pragma unroll
+            for (int i = 0; i < X; ++i) acc.v[i] = __fadd2_rn(acc.v[i], s_sum[threadIdx.x + (g << log_g)].v[i]);
+    }
+    if (mine == 0 && v < a.np) write_sum<O, N>(a, id, v, acc);
 }
 
 // ---------------------------------------------------------------- host side
@@ -457,11 +471,15 @@ spx_status embed(int T, int H, Ids x, const void* W, int64_t ldw, float scale, v
     return SPX_ERR_ALIGN;
 }
 
-// Sorted tokens a chunk: as many chunks as run at once, of 8 to 1024 tokens.
+// A block's threads for rows of np pieces.
+int sum_threads(long long np) { return static_cast<int>(std::min<long long>(kThreads, std::max(1LL, (np + 31) / 32) * 32)); }
+
+// Sorted tokens a chunk, 8 to 1024: as many chunks as run at once, of 16-byte pieces of two-byte values.  Short rows take
+// smaller blocks and so more of them (16384 tokens of 512 bf16 of 30000 ids, added: 31 us with blocks of 256, 18 so; of 1024 values 33 and 24).
 constexpr int kSumBlocks = 304;
 int chunk_of(int T, int H) {
-    const long long tiles = (H + kThreads * 8 - 1) / (kThreads * 8);  // of 16-byte pieces of two-byte values
-    return static_cast<int>(std::min<long long>(kMostChunk, std::max(8LL, (T * tiles + kSumBlocks - 1) / kSumBlocks)));
+    const long long np = (H + 7LL) / 8, tiles = (np + kThreads - 1) / kThreads, blocks = kSumBlocks * kThreads / sum_threads(np);
+    return static_cast<int>(std::min<long long>(kMostChunk, std::max(8LL, (T * tiles + blocks - 1) / blocks)));
 }
 
 struct Scratch {
@@ -480,15 +498,19 @@ Scratch scratch_of(int T, int H) {
 
 template <class V, class O, int N>
 cudaError_t sums(SumArgs a, int T, cudaStream_t st) {
-    const unsigned chunks = (T + a.chunk - 1) / a.chunk, tiles = (a.np + kThreads - 1) / kThreads;
-    constexpr size_t ring = sizeof(V) * N * kSets * kRows * kThreads;
-    cudaError_t e = spx_tc::set_smem_limit(embed_sum_kernel<V, O, N>, ring);
-    if (e == cudaSuccess) e = launch_early(embed_sum_kernel<V, O, N>, dim3(chunks, tiles), kThreads, ring, 1, st, a);
+    const unsigned chunks = (T + a.chunk - 1) / a.chunk;
+    const int threads = sum_threads(a.np);
+    constexpr size_t piece = sizeof(V) * N * kSets * kRows;
+    cudaError_t e = spx_tc::set_smem_limit(embed_sum_kernel<V, O, N>, piece * kThreads + sizeof(int) * (2 * kMostChunk + 2));
+    if (e == cudaSuccess)
+        e = launch_early(embed_sum_kernel<V, O, N>, dim3(chunks, (a.np + threads - 1) / threads), threads, piece * threads + sizeof(int) * (2 * a.chunk + 2), 1, st, a);
     if (e != cudaSuccess || chunks < 2) return e;
     // the kept sums in pieces of four: more threads, each with more of them in flight
     constexpr int J = N < 4 ? N : 4;
     a.np = a.np * (N / J);
-    return launch_early(embed_join_kernel<O, J>, dim3(chunks, (a.np + kThreads - 1) / kThreads), kThreads, 0, 1, st, a);
+    int log_g = 5;  // to 7: two shares of the chunks at least (16384 tokens of one id, 2048 bf16 105 us and 87; four shares 79, but 1 us more for ordinary ids)
+    while ((1 << log_g) < std::min(a.np, kThreads / 2)) ++log_g;
+    return launch_early(embed_join_kernel<O, J>, dim3(chunks, ((a.np - 1) >> log_g) + 1), kThreads, 0, 1, st, a, log_g);
 }
 
 template <class V, class O>
