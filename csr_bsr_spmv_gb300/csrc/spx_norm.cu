@@ -449,13 +449,14 @@ __global__ void __launch_bounds__(kAddThreads) add_parts_kernel(int H, int block
 
 // ---------------------------------------------------------------- host side
 
-
-// log2 of the threads a row: enough that its values fit their registers, and where there are few rows as many as it has
-// pieces, since every thread then waits for one load instead of several.
-int threads_log(int M, int H, int pieces) {
+// log2 of the threads a row: enough that its values fit their registers, and where there are few rows so many that a thread
+// waits for at most two pieces (1 x 1002 bf16 3.4 us with as many as needed and 2.2, 512 x 1001 fp32 9.6 and 5.9; with one
+// piece a thread 512 x 2048 bf16 takes 3.2 us for 2.9), of rows off their boundaries for one (1000 x 1001 bf16 5.9 and 5.0).
+// Larger blocks only where every row has an SM (1 x 4095 fp32 7.9 and 5.1, but 512 x 1001 5.9 and 7.5).
+int threads_log(int M, int H, int pieces, bool any) {
     int lg = 2;
     while ((kHeld << lg) < H && (1 << lg) < kMostThreads) ++lg;
-    while ((1 << lg) < pieces && (1 << lg) < kThreads && (static_cast<long long>(M) << lg) < 152 * 1024) ++lg;
+    while ((any ? 1 : 2) << lg < pieces && (1 << lg) < (M <= 152 ? kMostThreads : kThreads) && (static_cast<long long>(M) << lg) < 152 * 1024) ++lg;
     return lg;
 }
 
@@ -481,7 +482,7 @@ cudaError_t norm_launch(NormArgs a, cudaStream_t st) {
             return launch_early(rms_norm_kernel<V, O, N, ANY, 2 * kHeld, kThreads>, dim3((a.M - 1) / per + 1), kThreads, 0, 1, st, a);
         }
     }
-    a.log_g = threads_log(a.M, a.H, (a.H + N - 1) / N);
+    a.log_g = threads_log(a.M, a.H, (a.H + N - 1) / N, ANY);
     const int threads = std::max(kThreads, 1 << a.log_g), per = threads >> a.log_g;
     const dim3 grid((a.M - 1) / per + 1);
     if (threads == kThreads) return launch_early(rms_norm_kernel<V, O, N, ANY, kHeld, kThreads>, grid, threads, 0, 1, st, a);
