@@ -1,7 +1,11 @@
 // spx_gated.cu -- experts with a gate and their gradient: entry points.  Both
 // run on the experts' product kernels with the gate between the sums and what
 // is stored (spx_act.cuh), so neither the factors before the activation nor the
-// gradient behind it pass through memory on their own.
+// gradient behind it pass through memory on their own.  Measured: 32768 rows over
+// 16 experts, 2 x 2048 of 2048 bf16, 358 us repeated, 1.53 PFLOP/s, at the power
+// limit (326 in a single launch; a library product of as many operations 336 to
+// 353 repeated); its gradient 228 us (a library product of that size 182); a few
+// rows an expert are bound by the weights' bytes (35 us at 6.1 TB/s).
 #include "spx_act.cuh"
 
 using namespace spx_exp;

@@ -17,7 +17,6 @@ struct Pack {
     __device__ __forceinline__ void set(const V (&v)[N]) { memcpy(&w, v, sizeof(w)); }
 };
 
-// `once`: it is not read again soon.
 template <class P>
 __device__ __forceinline__ P read_piece(const P* p) {
     P v;
@@ -28,11 +27,6 @@ template <class P>
 __device__ __forceinline__ void write_piece(P* p, const P& v) {
     *reinterpret_cast<decltype(P::w)*>(p) = v.w;
 }
-template <class P>
-__device__ __forceinline__ void write_once(P* p, const P& v) {
-    __stcs(reinterpret_cast<decltype(P::w)*>(p), v.w);
-}
-
 // A piece of 4, 8 or 16 bytes to shared memory, asynchronously.
 template <class P>
 __device__ __forceinline__ void copy_piece(P* to, const P* from) {
@@ -241,7 +235,7 @@ struct Rows {
         memcpy(&r, o, 16);
         return r;
     }
-    // Piece p, or the last one beyond it; `in`: what inside() said; KEEP: it is read again soon.
+    // Piece p, or the last one beyond it, of a row that is inside(); KEEP: it is read again soon.
     template <bool KEEP = false>
     __device__ __forceinline__ Piece read(const V* row, int p) const {
         p = min(p, pieces() - 1);
@@ -277,7 +271,7 @@ struct Rows {
             }
             const float* v = static_cast<const float*>(w);
             Floats<N> f;
-    #pragma unroll
+#pragma unroll
             for (int i = 0; i < N / 4; ++i) {
                 const Floats<4> x = floats(read_any<float, 4>(v + p * N + 4 * i, max(0, min(4, H - p * N - 4 * i)), v, v + H));
                 f.v[2 * i] = x.v[0], f.v[2 * i + 1] = x.v[1];
