@@ -68,6 +68,16 @@ def test_gradient_sums_by_id(T, V, H, kind, dtype, out):
     assert torch.equal(acc, (want + base.double()).float().to(out))
 
 
+@pytest.mark.parametrize("H", [32, 64, 256, 258, 512, 700, 1024, 2048, 4097])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradient_of_one_id_among_others(H, dtype):
+    """An id of hundreds of chunks between ids of one token, rows from one warp's width to several blocks'."""
+    T, V = 9001, 5000
+    ids = torch.where(torch.arange(T, device="cuda") % 7 == 3, ids_of(T, V, H, "even"), 2500)
+    dY = whole(H, T, H, dtype=dtype)
+    assert torch.equal(spx.spx_embed_grad(ids, dY, V, dtype=F32), grad64(ids, dY, V, 1.0)[0].float())
+
+
 @pytest.mark.parametrize("T,V,H", [(3000, 200, 136), (16384, 5000, 264)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_gradient_of_any_values_is_the_same_every_time(T, V, H, dtype):
