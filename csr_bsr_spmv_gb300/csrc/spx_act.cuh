@@ -62,6 +62,29 @@ __device__ __forceinline__ float2 logistic(float2 z) {
     return p;
 }
 
+// Phi(-|x|), |x| at most 100, and e = exp(-x^2 / 2).  Their quotient is smooth and falls like 1 / |x|: t P(t) with t = 1 / (1 +
+// 0.35 |x|), P of degree 8 fitted in 40 digits to |x| up to 13.5, where Phi leaves fp32 (reweighted least squares, off by
+// 2^-24.9 of itself); the exponential as above, with the rounding of x^2 put back as well.  Off by less than 2^-20.5 of itself;
+// the activation of every 16-bit value comes out within 2^-20.9.  32768 x 2048 of 2048 bf16: the gate's gradient 245 us, with
+// CUDA's normcdff and expf 301 (SiLU 235); the gated product 381 and 416 (SiLU 364).
+__device__ __forceinline__ float2 normal_tail(float2 x, float2& e) {
+    constexpr double half_log2e = 1.4426950408889634 / 2;
+    constexpr float L = static_cast<float>(half_log2e), rest = static_cast<float>(half_log2e - static_cast<double>(L));
+    constexpr float P[9] = {0.1396215697f, 0.1398590851f, 0.1198524147f, 0.1054330339f, -0.0229373839f, 0.1589296681f, -0.2555049107f, 0.1438724097f, -0.0291259024f};
+    const float2 h = __fmul2_rn(x, x), low = __ffma2_rn(x, x, make_float2(-h.x, -h.y)), z = __fmul2_rn(h, both(-L));
+    const float2 d = __ffma2_rn(low, both(L), __ffma2_rn(h, both(rest), __ffma2_rn(h, both(L), z)));
+    const float2 y = __ffma2_rn(make_float2(fabsf(x.x), fabsf(x.y)), both(0.35f), both(1.f));
+    float2 t, s = both(P[8]);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(y.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(y.y));
+    e = __ffma2_rn(e, __fmul2_rn(d, both(-0.693147181f)), e);
+#pragma unroll
+    for (int i = 7; i >= 0; --i) s = __ffma2_rn(s, t, both(P[i]));
+    return __fmul2_rn(__fmul2_rn(e, t), s);
+}
+
 constexpr float kTanh1 = 1.5957691216f, kTanh3 = 0.07135481628f;  // 2 sqrt(2 / pi), and that times 0.044715
 
 template <int kind>
@@ -70,9 +93,10 @@ __device__ __forceinline__ float2 act_of(float2 x, float2& slope) {
     const float2 low = make_float2(at_least(x.x, -most), at_least(x.y, -most)), near = make_float2(at_most(low.x, most), at_most(low.y, most));
     float2 z = near, dz = both(1.f), p;
     if (kind == SPX_ACT_GELU) {
-        p = make_float2(normcdff(x.x), normcdff(x.y));
-        const float2 h = __fmul2_rn(__fmul2_rn(near, near), both(-0.5f));
-        slope = __ffma2_rn(__fmul2_rn(near, both(0.3989422804f)), make_float2(expf(h.x), expf(h.y)), p);
+        float2 e;
+        const float2 q = normal_tail(near, e);
+        p = make_float2(x.x > 0.f ? 1.f - q.x : q.x, x.y > 0.f ? 1.f - q.y : q.y);
+        slope = __ffma2_rn(__fmul2_rn(near, both(0.3989422804f)), e, p);
         return __fmul2_rn(low, p);
     }
     if (kind == SPX_ACT_GELU_TANH) {

@@ -160,6 +160,28 @@ def test_values_far_from_zero():
         assert torch.equal(C2, C)
 
 
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("K", [16, 18])
+def test_activations_of_every_16_bit_value(act, dtype, K):
+    """C in fp32 for G = x and U = 1: the activation itself, on the tensor cores and (K = 18) on the CUDA cores.  16 u of the
+    activation as above, and: p below fp32's normal numbers, 2^-126, may be 0, which is |x| 2^-126 of x p; the tanh form's z comes
+    from two rounded constants and three roundings, 5 u |z| in all, which its p = 1 / (1 + exp(-z)) passes on as 5 u |z| (1 - p) p."""
+    x = torch.arange(-2 ** 15, 2 ** 15, device="cuda", dtype=torch.int32).to(torch.int16).view(dtype)
+    x = x[x.abs().float() < 1e4]
+    x = torch.cat([x, x[:-x.numel() % 8]]).view(-1, 8)
+    A = torch.zeros(x.shape[0], K, device="cuda", dtype=dtype)
+    A[:, :8], A[:, 8:16] = x, 1
+    C, _ = spx.spx_gemm_grouped_gated(None, A, torch.eye(16, K, device="cuda", dtype=dtype), act=act, dtype=F32)
+    a = act64(act, x.double())[0]
+    err = 16 * U * a.abs() + x.double().abs() * 2.0 ** -126
+    if act == "gelu_tanh":
+        z = (8 / np.pi) ** 0.5 * (x.double() + 0.044715 * x.double() ** 3)
+        err += 5 * U * z.abs() * torch.sigmoid(-z) * a.abs()
+    close(C, a, err)
+    assert not C[x == 0].any()
+
+
 def test_no_offsets_no_rows_and_no_reduction():
     A, W = normal(1, 70, 64, dtype=BF16), normal(2, 48, 64, dtype=BF16)
     C, H = spx.spx_gemm_grouped_gated(None, A, W, grad=True)
