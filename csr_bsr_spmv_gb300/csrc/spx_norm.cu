@@ -550,13 +550,18 @@ spx_status grad_launch(GradArgs a, float* dw, cudaStream_t st) {
     a.log_g = g.log_g;
     if (a.part && g.blocks == 1) a.part = dw;
     spx_note_launches(a.part && g.blocks > 1 ? 2 : 1);
-    constexpr bool half = sizeof(V) == 2;
-    cudaError_t e;
-    if (g.threads == kThreads) e = grad_kernel<V, N, ANY, kThreads, half ? (ANY ? 2 : 3) : 1>(a, g, st);
-    else if (g.threads == 512) e = grad_kernel<V, N, ANY, 512, half ? (ANY ? 2 : 3) : ANY ? 1 : 2>(a, g, st);
-    else if (a.H <= kLongRow) e = grad_kernel<V, N, ANY, kMostThreads, half && !ANY ? 2 : 0>(a, g, st);
-    else if ((e = spx_tc::set_smem_limit(rms_norm_grad_long_kernel<V, N, ANY>, sizeof(float) * (SPX_NORM_MAX_H + kSlack))) == cudaSuccess)
-        e = launch_early(rms_norm_grad_long_kernel<V, N, ANY>, dim3(g.blocks), kMostThreads, sums_bytes(a), 1, st, a);
+    constexpr bool half = sizeof(V) == 2, shorter = half || !ANY, longer = half || N == 4;  // what grad_pieces gives these pieces
+    cudaError_t e = cudaErrorInvalidValue;
+    if (g.threads < kMostThreads) {
+        if constexpr (shorter) {
+            if (g.threads == kThreads) e = grad_kernel<V, N, ANY, kThreads, half ? (ANY ? 2 : 3) : 1>(a, g, st);
+            else e = grad_kernel<V, N, ANY, 512, half && !ANY ? 3 : 2>(a, g, st);
+        }
+    } else if constexpr (longer) {
+        if (a.H <= kLongRow) e = grad_kernel<V, N, ANY, kMostThreads, half && !ANY ? 2 : 0>(a, g, st);
+        else if ((e = spx_tc::set_smem_limit(rms_norm_grad_long_kernel<V, N, ANY>, sizeof(float) * (SPX_NORM_MAX_H + kSlack))) == cudaSuccess)
+            e = launch_early(rms_norm_grad_long_kernel<V, N, ANY>, dim3(g.blocks), kMostThreads, sums_bytes(a), 1, st, a);
+    }
     if (e == cudaSuccess && a.part && g.blocks > 1)
         e = launch_early(add_parts_kernel, dim3((a.H + 31) / 32), kAddThreads, 0, 1, st, a.H, g.blocks, static_cast<const float*>(a.part), dw);
     return spx_cuda_status(e);
@@ -568,6 +573,9 @@ spx_status grad_pieces(const GradArgs& a, float* dw, cudaStream_t st) {
     if (a.dR) bits |= addr(a.dR) | a.lddr * sizeof(V);
     if (a.w) bits |= a.wide_w && sizeof(V) == 2 ? (addr(a.w) % 16 ? addr(a.w) / 2 : 0) : addr(a.w);
     if (bits % 16 == 0) return grad_launch<V, 16 / sizeof(V), false>(a, dw, st);
+    // fp32 rows longer than 512 threads hold: shifted 16-byte pieces (2000 x 16383 409 us in 4-byte pieces and 245; of 8191
+    // values 128 and 175)
+    if (sizeof(V) == 4 && a.H > kHeld * 512) return grad_launch<V, 16 / sizeof(V), true>(a, dw, st);
     if (bits % 4 == 0) return grad_launch<V, 4 / sizeof(V), false>(a, dw, st);
     if constexpr (sizeof(V) == 2) return grad_launch<V, 8, true>(a, dw, st);
     return SPX_ERR_ALIGN;

@@ -101,6 +101,13 @@ def test_pitches_and_bases_of_any_alignment(dtype, wide, pad, H):
         assert torch.equal(between(t, pad).nan_to_num(5), e.nan_to_num(5))
 
 
+@pytest.mark.parametrize("dtype,wide", [(F32, False), (BF16, True)])
+@pytest.mark.parametrize("pad", [1, 2, 4])
+@pytest.mark.parametrize("H", [9000, 16384, 17000])
+def test_long_rows_of_any_alignment(dtype, wide, pad, H):
+    test_pitches_and_bases_of_any_alignment(dtype, wide, pad, H)
+
+
 @pytest.mark.parametrize("H", [7, 40, 41, 1000, 1001, 1002, 4095, 6000, 6001, 9001, 16401, 20000])
 def test_outputs_over_their_inputs(H):
     """S over R, Y over X; dX over dY, over dS and over S: rows on 16- and 4-byte boundaries and on neither."""
