@@ -27,7 +27,7 @@ using namespace spx_rows;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kMostGridY = 65535;
 
 // Token t's id, -1 outside [0, V).
 struct Ids {
@@ -526,6 +526,7 @@ cudaError_t sums(SumArgs a, int T, cudaStream_t st) {
     // with ordinary ids 1 us more)
     int log_g = 5;
     while ((1 << log_g) < std::min(a.np, kThreads / 2)) ++log_g;
+    while (((a.np - 1) >> log_g) >= kMostGridY) ++log_g;  // rows past 8388480 values in pieces of one: one share
     return launch_early(embed_join_kernel<O, J>, dim3(chunks, ((a.np - 1) >> log_g) + 1), kThreads, 0, 1, st, a, log_g);
 }
 
@@ -579,7 +580,7 @@ spx_status spx_embed_grad(int32_t T, int32_t H, int32_t V, spx_type type, const 
     const spx_status c = check(T, H, V, type, id_bytes);
     if (c != SPX_OK) return c;
     if (w_type != type && w_type != SPX_F32) return SPX_ERR_ARG;
-    if (H > 65535 * kThreads) return SPX_ERR_UNSUPPORTED;
+    if (H > kMostGridY * kThreads) return SPX_ERR_UNSUPPORTED;
     if (H == 0 || V == 0 || (T == 0 && accumulate)) return SPX_OK;
     if (!dW || lddw < H || (T > 0 && (!ids || !dY || lddy < H))) return SPX_ERR_ARG;
     if (!scratch || scratch_bytes < spx_embed_grad_scratch_bytes(T, H)) return SPX_ERR_ARG;
