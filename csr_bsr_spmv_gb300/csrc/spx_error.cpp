@@ -6,7 +6,8 @@
 #include "spx_internal.h"
 
 extern "C" spx_status spx_last_device_error(spx_stream_t stream) {
-    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPX_ERR_CUDA;
+    const cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return spx_cuda_status(e);
     const int timed[] = {spx_bsr_error_take(), spx_wcsr_error_take(), spx_experts_error_take()};
     const int coo = spx_coo_error_take();
     // the checked build's index errors (always 0 in the product build, which reads no word for them)

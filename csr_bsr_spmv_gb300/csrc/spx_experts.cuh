@@ -160,8 +160,7 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);  // this launch's own error, not one left by another call
 }
 
 // Slots, rows and row lengths stay below 2^31 by more than a grid's threads or

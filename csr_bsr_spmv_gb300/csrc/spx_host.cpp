@@ -564,4 +564,9 @@ spx_status spx_plan_destroy(spx_plan* P) {
 
 void spx_note_launches(uint64_t n) { g_launches.fetch_add(n); }
 
-spx_status spx_cuda_status(int cuda_error) { return cuda_error == 0 ? SPX_OK : SPX_ERR_CUDA; }
+// A refused call's error is told once: left behind, the next call would report it for its own.
+spx_status spx_cuda_status(int cuda_error) {
+    if (cuda_error == 0) return SPX_OK;
+    cudaGetLastError();
+    return SPX_ERR_CUDA;
+}
