@@ -941,8 +941,8 @@ spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t
  * (H values of `type` or fp32) may be NULL: all ones; S and rstd (fp32, for the
  * gradient) may be NULL.  S may be X or R, and Y may be any of the three, with
  * the same row pitch.  Rows of 1 to SPX_NORM_MAX_H values
- * (SPX_ERR_UNSUPPORTED beyond).  Squares whose mean passes fp32's range give
- * zeros.  Launches: 1.
+ * (SPX_ERR_UNSUPPORTED beyond).  A row whose sum of squares passes fp32's range
+ * (3.4e38, H times the mean's) has rstd 0 and a Y of zeros.  Launches: 1.
  */
 #define SPX_NORM_MAX_H 32768
 spx_status spx_rms_norm(int32_t M, int32_t H, spx_type type, const void* X, int64_t ldx, const void* R, int64_t ldr,
