@@ -942,7 +942,9 @@ spx_status spx_gemm_i8(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t
  * gradient) may be NULL.  S may be X or R, and Y may be any of the three, with
  * the same row pitch.  Rows of 1 to SPX_NORM_MAX_H values
  * (SPX_ERR_UNSUPPORTED beyond).  A row whose sum of squares passes fp32's range
- * (3.4e38, H times the mean's) has rstd 0 and a Y of zeros.  Launches: 1.
+ * (3.4e38, H times the mean's) has rstd 0 and a Y of zeros; a row of zeros, or of
+ * values whose squares all vanish in fp32, needs eps > 0 (with eps 0 its rstd is
+ * an infinity, and 0 in Y is NaN).  Launches: 1.
  */
 #define SPX_NORM_MAX_H 32768
 spx_status spx_rms_norm(int32_t M, int32_t H, spx_type type, const void* X, int64_t ldx, const void* R, int64_t ldr,
@@ -953,8 +955,9 @@ spx_status spx_rms_norm(int32_t M, int32_t H, spx_type type, const void* X, int6
  * The same with an output that spx_gemm_i8 reads: scale[m] = max_h |Y[m, h]| /
  * 127 and Q[m, h] = Y[m, h] / scale[m] rounded to the nearest whole number
  * (ties to even), from the fp32 Y that was not rounded.  A row of zeros gets
- * scale 0 and codes 0; a row whose Y holds an infinity or NaN gets scale NaN
- * and codes 0, as in spx_quant_rows_i8.  Launches: 1.
+ * scale 0 and codes 0 where eps > 0; a row whose Y holds an infinity or NaN (of
+ * zeros with eps 0 among them) gets scale NaN and codes 0, as in
+ * spx_quant_rows_i8.  Launches: 1.
  */
 spx_status spx_rms_norm_i8(int32_t M, int32_t H, spx_type type, const void* X, int64_t ldx, const void* R, int64_t ldr,
                            const void* weight, spx_type w_type, float eps, void* S, int64_t lds, int8_t* Q, int64_t ldq,

@@ -1,9 +1,9 @@
-"""Where the norm's arithmetic ends: sums of squares at fp32's largest number.  The sums lie 2% from the border, and
-fp32 sums are off by less than H u = 2^-9."""
+"""Where the norm's arithmetic ends: sums of squares at fp32's largest number, and eps 0.  No sums are compared here but those
+that are exact or lie 2% from the border, of fp32 sums that are off by less than H u = 2^-9."""
 import pytest
 import torch
 
-from block_util import BF16, F32
+from block_util import BF16, F16, F32
 from csr_bsr_spmv_gb300 import spx
 
 pytestmark = pytest.mark.gpu
@@ -24,3 +24,21 @@ def test_sums_of_squares_past_the_range_give_zeros(H, dtype):
     assert not Y[1].any() and rstd[1] == 0
     Q, scale, _ = spx.spx_rms_norm_i8(X)
     assert (Q[[0, 2]] == 127).all() and not Q[1].any() and scale[1] == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("H", [5, 520, 4097, 20000])
+def test_rows_of_zeros_need_an_eps(H, dtype):
+    """The formula divides 0 by 0 for a row of zeros and eps 0: NaN, codes 0 and a scale of NaN.  Other rows do not mind."""
+    X = torch.ones(4, H, dtype=dtype, device="cuda")
+    X[2] = 0
+    for eps in (0.0, 2.0 ** -30):
+        Y, _, rstd = spx.spx_rms_norm(X, eps=eps, grad=True)
+        Q, scale, _ = spx.spx_rms_norm_i8(X, eps=eps)
+        for i in (0, 1, 3):
+            assert (Y[i] == 1).all() and rstd[i] == 1 and (Q[i] == 127).all()
+        assert not Q[2].any()
+        if eps:
+            assert not Y[2].any() and rstd[2] == 2.0 ** 15 and scale[2] == 0
+        else:
+            assert Y[2].isnan().all() and rstd[2] == float("inf") and scale[2].isnan()
