@@ -542,9 +542,11 @@ cudaError_t sums_in_pieces(SumArgs a, int T, int H, cudaStream_t st) {
         a.np = H / N16;
         return sums<V, O, N16>(a, T, st);
     }
-    if (sizeof(V) == 2 && N >= 2 && M >= 2) {
-        a.np = H / 2;
-        return sums<V, O, 2>(a, T, st);
+    if constexpr (sizeof(V) == 2) {
+        if (N >= 2 && M >= 2) {
+            a.np = H / 2;
+            return sums<V, O, 2>(a, T, st);
+        }
     }
     a.np = H;
     return sums<V, O, 1>(a, T, st);
