@@ -140,10 +140,10 @@ spx_status launch(const SimtGemm& g, const Gate& gate, spx_type c_type, cudaStre
     }
     if (grid.y > 65535) return SPX_ERR_UNSUPPORTED;
     spx_note_launches(1);
-    return spx_cuda_status(launch_early(c_type == SPX_F32    ? experts_simt_kernel<V, float, EPI>
-                                        : c_type == SPX_BF16 ? experts_simt_kernel<V, __nv_bfloat16, EPI>
-                                                             : experts_simt_kernel<V, __half, EPI>,
-                                        grid, kThreads, 0, 1, st, g, gate));
+    auto kernel = experts_simt_kernel<V, V, EPI>;  // what is stored has the factors' type or, but for the gate's gradient, fp32
+    if constexpr (EPI != kGateGrad)
+        if (c_type == SPX_F32) kernel = experts_simt_kernel<V, float, EPI>;
+    return spx_cuda_status(launch_early(kernel, grid, kThreads, 0, 1, st, g, gate));
 }
 
 }  // namespace
