@@ -115,12 +115,11 @@ __device__ __forceinline__ void shift_words(const uint32_t (&t)[2 * W], int off,
         for (int i = 0; i < 6; ++i) v[i] = two ? t[i + 2] : t[i];
 #pragma unroll
         for (int i = 0; i < 5; ++i) u[i] = one ? v[i + 1] : v[i];
-    } else if constexpr (W == 2) {
+    } else {
+        static_assert(W == 2, "pieces of 8 and 16 bytes");
         const bool one = off & 4;
 #pragma unroll
         for (int i = 0; i < 3; ++i) u[i] = one ? t[i + 1] : t[i];
-    } else {
-        u[0] = t[0], u[1] = t[1];
     }
 #pragma unroll
     for (int i = 0; i < W; ++i) o[i] = __funnelshift_r(u[i], u[i + 1], (off & 3) * 8);
