@@ -865,8 +865,9 @@ typedef enum spx_w_layout {
  * read on the host: nothing waits for the routing.  K == 0 gives zeros.
  * Launches: 1.
  * The tensor cores run when A and W lie on 16-byte boundaries and lda, ldw and
- * (E > 1) stride_w are multiples of 8 (N and K may be any); all else runs on
- * the CUDA cores, which take about 80 times as long on large products.
+ * (E > 1) stride_w are multiples of 8 (N and K may be any but K = 0); all else
+ * runs on the CUDA cores, which take about 80 times as long on large products
+ * and give SPX_ERR_UNSUPPORTED beyond 4194240 output columns.
  */
 spx_status spx_gemm_grouped(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const void* A,
                             int64_t lda, const void* W, int64_t ldw, int64_t stride_w, spx_w_layout layout,
@@ -880,7 +881,7 @@ spx_status spx_gemm_grouped(int32_t E, int32_t S, int32_t N, int32_t K, const in
  * `w_type` (`type` or SPX_F32), rounded once from fp32.  For weights stored
  * K x N swap G and A (and N and K).  Launches: 1.
  * Alignment as above, for G and A: 16-byte bases, ldg and lda multiples of 8
- * for the tensor cores.
+ * for the tensor cores; the CUDA cores' limit holds for K.
  */
 spx_status spx_gemm_grouped_wgrad(int32_t E, int32_t S, int32_t N, int32_t K, const int32_t* offsets, const void* G,
                                   int64_t ldg, const void* A, int64_t lda, spx_type type, void* dW, int64_t ldw,
@@ -997,7 +998,8 @@ typedef enum spx_act {
  * C comes from the G and U that were not rounded.  Zeros in the rows from
  * offsets[E] on.  offsets NULL (then E must be 1): all S rows belong to the one
  * weight matrix.  type is SPX_BF16 or SPX_F16.  K == 0 gives zeros.  Launches:
- * 1.  Alignment for the tensor cores as in spx_gemm_grouped.
+ * 1.  Alignment for the tensor cores, and F's limit without it, as in
+ * spx_gemm_grouped.
  */
 spx_status spx_gemm_grouped_gated(int32_t E, int32_t S, int32_t F, int32_t K, const int32_t* offsets, const void* A,
                                   int64_t lda, const void* W, int64_t ldw, int64_t stride_w, spx_act act, spx_type type,
@@ -1015,7 +1017,7 @@ spx_status spx_gemm_grouped_gated(int32_t E, int32_t S, int32_t F, int32_t K, co
  * need not keep it.  The first weights' gradient is spx_gemm_grouped_wgrad(dH,
  * A), A's is the SPX_W_KN product of dH with the first weights.  Rows from
  * offsets[E] on are zeros, whatever H holds there.  dH may be H with the same
- * row pitch.  offsets NULL as above.  Launches: 1.
+ * row pitch.  offsets NULL and F's limit as above.  Launches: 1.
  */
 spx_status spx_gemm_grouped_gated_grad(int32_t E, int32_t S, int32_t F, int32_t N, const int32_t* offsets, const void* dY,
                                        int64_t lddy, const void* W, int64_t ldw, int64_t stride_w, spx_w_layout layout,
