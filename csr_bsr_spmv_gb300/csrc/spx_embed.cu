@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads)
 // with counters per id of its own the warp so knows each token's rank in its list, and the counters of the warps before it
 // and the counts of lower ids give the place.  Of more than 16384 tokens the block's go to a list of the block first, in
 // order (65536 tokens over 65536 rows of 128 values 48 us without the list and 40); where they do not fit it, all are read
-// once more.  No floating-point and no order that depends on timing: the atomics are whole sums.  Nearly all of a block's
+// once more.  The work so grows with tokens times blocks, of which there are 152 or one for every 1024 ids.  No floating-point and no order that depends on timing: the atomics are whole sums.  Nearly all of a block's
 // work is passing over other blocks' tokens, so that is what is kept short; the other loops stay loops, since unrolled the kernel took longer to fetch its code than to run it.
 constexpr int kOrderThreads = 1024, kOrderWarps = kOrderThreads / 32, kSlots = 16, kRun = 32 * kSlots, kBatch = kOrderWarps * kRun;
 constexpr int kMostIds = 1024, kList = 4096;  // a warp's word: 10 bits of the id, 9 of the place in its run, 9 of the rank

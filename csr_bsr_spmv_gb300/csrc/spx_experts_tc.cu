@@ -29,10 +29,10 @@
 // 128 x 64: 4.6 us), a weight gradient over few rows by its stores (64 experts of
 // 2048 x 2048, 16 or 32 rows each: 537 MB of gradients in 107 us; filling that
 // memory takes 132), or by clearing what a last step of 16 rows does not hold (12
-// rows each 111, 8 130, 1 155).  The gate costs the product little (358 us repeated
-// for 32768 rows x 2 x 2048 of 2048 over 16 experts; tensor pipe 83% active).  The
+// rows each 111, 8 130, 1 155).  The gate costs the product little (358 to 365 us
+// repeated for 32768 rows x 2 x 2048 of 2048 over 16 experts; tensor pipe 83% active).  The
 // gate's gradient is bound by what its storing warps do for each sum, beside
-// MMAs of only 2048 terms: 228 us for 32768 x 2048 of 2048 (tensor pipe 64%
+// MMAs of only 2048 terms: 228 to 237 us for 32768 x 2048 of 2048 (tensor pipe 64%
 // active, DRAM 54%), 183 with the sums stored as they are;
 // 349 with 8 storing warps that read H when a chunk's turn came.
 //

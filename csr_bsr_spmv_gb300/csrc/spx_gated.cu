@@ -2,10 +2,12 @@
 // run on the experts' product kernels with the gate between the sums and what
 // is stored (spx_act.cuh), so neither the factors before the activation nor the
 // gradient behind it pass through memory on their own.  Measured: 32768 rows over
-// 16 experts, 2 x 2048 of 2048 bf16, 358 us repeated, 1.53 PFLOP/s, at the power
-// limit (326 in a single launch; a library product of as many operations 336 to
-// 353 repeated); its gradient 228 us (a library product of that size 182); a few
-// rows an expert are bound by the weights' bytes (35 us at 6.1 TB/s).
+// 16 experts, 2 x 2048 of 2048 bf16, 358 to 365 us replayed as a graph and 377 as
+// calls, 1.46 to 1.53 PFLOP/s, at the power limit (326 in a single launch; a
+// library product of as many operations 336 to 353 repeated); its gradient 228 to
+// 237 us and 243 (a library product of that size 182); a few rows an expert are
+// bound by the weights' bytes (35 us at 6.1 TB/s).  fp32 instead of bf16 output
+// costs 3% without H, 1% with it, "nk" weights of the gradient nothing.
 #include "spx_act.cuh"
 
 using namespace spx_exp;

@@ -10,7 +10,11 @@
 // TB/s, the gradient 88 us, 6.1 TB/s (copies run at 6.8).  Few rows are bound by
 // the latency of one load, one sum and one store: a row of 4096 2.2 us, its
 // launch included.  Rows off 16-byte boundaries are bound by their instructions:
-// 4094 values 97 us (gradient 136), 4095 161 (186), of fp32 by 4-byte pieces.
+// 4-byte pieces of 4094 values 97 us (gradient 136), shifted words of 4095 161
+// (186); fp32 rows go in 4-byte pieces, in the gradient those over 8192 values in
+// shifted words.  The gradient of rows over 8192 values runs on 1024 threads of 64
+// registers and spills 100 to 770 bytes a thread (4096 x 16384 bf16 142 us for 79
+// of HBM), the norm over 16384 values 24 to 104, in fp32 pieces of one value 530.
 #include <algorithm>
 #include <type_traits>
 
@@ -165,7 +169,10 @@ __global__ void __launch_bounds__(MAXT, ANY || MAXT > kThreads || HELD > kHeld ?
 
 // A group of threads takes a row, each with columns of its own whose d w it sums over its rows.  A thread copies the
 // pieces it is going to need asynchronously into its own slots of shared memory, DEPTH rows ahead: it waits for nobody
-// else's copies, and they hold no registers.  Between the two looks at a row -- the sum of dy w s, then what is written --
+// else's copies, and they hold no registers.  That is three rows deep for 16-bit rows that need no shifting (up to 8192
+// values; two up to 16384), two for those that do and for fp32 rows over 4096 values.  fp32 rows up to 4096 have room for one, whose copies
+// are in flight beside the other blocks' rows (8192 x 4096 fp32 88 us, 90% of the copy rate, as bf16); rows in 4-byte pieces
+// spill 72 bytes a thread there.  Between the two looks at a row -- the sum of dy w s, then what is written --
 // only that sum crosses threads.  As many blocks as the SMs hold at once, three an SM, so that few rows of sums are left to
 // add (add_parts_kernel).  16384 x 4096 bf16: 94 us with a row's pieces in a thread's slots three deep (118 with tiles of
 // rows that a block waits for together; 235 with nothing ahead), 88 with the sums written in whole lines.
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > kThreads ? 1 : ANY ? 2 : 3) rms_n
 }
 
 // Rows longer than a block's threads hold so: a block a row, read twice, the second time from L2.  One row an SM in flight,
-// nothing ahead: 2048 x 20000 bf16 130 us for 48 of HBM.
+// nothing ahead, and the running sums spill (352 bytes of bf16, 548 off boundaries): 2048 x 20000 bf16 130 us for 48 of HBM.
 constexpr int kLongValues = 32;
 template <class V, int N, bool ANY>
 __global__ void __launch_bounds__(kMostThreads, 1) rms_norm_grad_long_kernel(GradArgs a) {
@@ -502,8 +509,8 @@ cudaError_t norm_launch(NormArgs a, cudaStream_t st) {
                         threads, 0, 1, st, a);
 }
 
-// Rows of 16-byte pieces in every array (of codes: of as many bytes as a piece has values), else of 4-byte ones, else, 16-bit
-// rows of odd widths or bases, shifted ones.  16384 x 4096 bf16 80 us, rows of 4094 96, of 4095 161.
+// Rows of 16-byte pieces in every array (of codes: of as many bytes as a piece has values), else of 4-byte ones (fp32 rows
+// always), else, 16-bit rows of odd widths or bases, shifted ones.  16384 x 4096 bf16 80 us, rows of 4094 96, of 4095 161.
 template <class V, class O>
 spx_status norm_pieces(const NormArgs& a, cudaStream_t st) {
     uint64_t bits = addr(a.X) | (static_cast<uint64_t>(a.H) | a.ldx) * sizeof(V);
