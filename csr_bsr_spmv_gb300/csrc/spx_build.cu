@@ -645,6 +645,7 @@ struct Pool {
     }
     ~Pool() {
         for (void* p : ptrs) cudaFreeAsync(p, st);
+        cudaGetLastError();  // what refused this call is told by its status, not by the next call's
     }
 };
 

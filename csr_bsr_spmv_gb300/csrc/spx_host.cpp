@@ -38,14 +38,14 @@ spx_status to_host(std::vector<T>& dst, const T* src, int64_t n, cudaStream_t st
     if (n == 0) return SPX_OK;
     cudaError_t e = cudaMemcpyAsync(dst.data(), src, sizeof(T) * static_cast<size_t>(n), cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    return e == cudaSuccess ? SPX_OK : SPX_ERR_CUDA;
+    return spx_cuda_status(e);
 }
 
 spx_status to_device(void* dst, const void* src, size_t bytes, cudaStream_t stream) {
     if (bytes == 0) return SPX_OK;
     cudaError_t e = cudaMemcpyAsync(dst, src, bytes, cudaMemcpyHostToDevice, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    return e == cudaSuccess ? SPX_OK : SPX_ERR_CUDA;
+    return spx_cuda_status(e);
 }
 
 bool bad_vbytes(int32_t vb) { return !(vb == 1 || vb == 2 || vb == 4 || vb == 8); }
@@ -547,7 +547,7 @@ spx_status spx_plan_upload(spx_plan* P, void* table, size_t table_bytes, spx_str
         e = cudaMemcpyAsync(dst + tb + lb, P->first.data(), P->first.size() * sizeof(uint16_t), cudaMemcpyHostToDevice,
                             st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return SPX_ERR_CUDA;
+    if (e != cudaSuccess) return spx_cuda_status(e);
     P->d_table = table;
     return SPX_OK;
 }

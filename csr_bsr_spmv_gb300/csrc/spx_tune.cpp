@@ -141,7 +141,10 @@ spx_status spx_plan_autotune(int32_t M, int32_t K, int64_t nnz, const int32_t* r
     }
     cudaEventDestroy(e0);
     cudaEventDestroy(e1);
-    if (s != SPX_OK) return s;
+    if (s != SPX_OK) {
+        cudaGetLastError();  // told by the status, not by the next call's
+        return s;
+    }
     *best = cand[pick];
     if (cached) *cached = 0;
     std::lock_guard<std::mutex> lock(g_mu);
