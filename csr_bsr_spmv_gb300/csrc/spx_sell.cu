@@ -330,8 +330,10 @@ spx_status spx_sell_get_arrays(const spx_sell* S, int32_t* slice_ptr, int32_t* p
         const size_t off[5] = {0, S->off_prow, S->off_long, S->off_col, S->off_val};
         void* dst[5] = {slice_ptr, prow, longrows, scol, sval};
         for (int i = 0; i < 5; ++i)
-            if (dst[i] && n[i] && cudaMemcpy(dst[i], dimg + off[i], n[i], cudaMemcpyDeviceToHost) != cudaSuccess)
-                return SPX_ERR_CUDA;
+            if (dst[i] && n[i]) {
+                const cudaError_t e = cudaMemcpy(dst[i], dimg + off[i], n[i], cudaMemcpyDeviceToHost);
+                if (e != cudaSuccess) return spx_cuda_status(e);
+            }
         return SPX_OK;
     }
     auto cp = [](void* dst, const void* src, size_t n) {
@@ -356,7 +358,7 @@ spx_status spx_sell_upload(spx_sell* S, void* image, size_t image_bytes, spx_str
         if (!src) return SPX_ERR_NOT_READY;
         cudaError_t e = src == image ? cudaSuccess : cudaMemcpyAsync(d, src, S->bytes, cudaMemcpyDeviceToDevice, st);
         if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-        if (e != cudaSuccess) return SPX_ERR_CUDA;
+        if (e != cudaSuccess) return spx_cuda_status(e);
         if (S->d_own) cudaFree(S->d_own);
         S->d_own = nullptr;
         S->d_image = image;
@@ -375,7 +377,7 @@ spx_status spx_sell_upload(spx_sell* S, void* image, size_t image_bytes, spx_str
     for (const Part& p : parts)
         if (e == cudaSuccess && p.n) e = cudaMemcpyAsync(d + p.off, p.src, p.n, cudaMemcpyHostToDevice, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return SPX_ERR_CUDA;
+    if (e != cudaSuccess) return spx_cuda_status(e);
     S->d_image = image;
     return SPX_OK;
 }

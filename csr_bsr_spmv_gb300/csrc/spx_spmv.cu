@@ -563,7 +563,7 @@ spx_status spx_spmv_csr_hostio(const spx_plan* plan, int32_t M, int32_t K, int64
     if (up) cudaStreamDestroy(up);
     if (down) cudaStreamDestroy(down);
     if (s != SPX_OK) return s;
-    return e == cudaSuccess ? SPX_OK : SPX_ERR_CUDA;
+    return spx_cuda_status(e);
 }
 
 spx_status spx_spmv_csr_dual(const spx_plan* pA, const spx_plan* pAt, int32_t m, int32_t n, int64_t nnz,

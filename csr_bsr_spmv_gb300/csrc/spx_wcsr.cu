@@ -518,8 +518,8 @@ spx_status spx_wcsr_plan_build(int32_t M, int64_t nchunks, const int32_t* win_pt
         return SPX_ERR_NOMEM;
     }
     if (where == SPX_DEVICE) {
-        if (cudaMemcpy(wp.data(), win_ptr, sizeof(int32_t) * wp.size(), cudaMemcpyDeviceToHost) != cudaSuccess)
-            return SPX_ERR_CUDA;
+        const cudaError_t e = cudaMemcpy(wp.data(), win_ptr, sizeof(int32_t) * wp.size(), cudaMemcpyDeviceToHost);
+        if (e != cudaSuccess) return spx_cuda_status(e);
     } else if (where == SPX_HOST) {
         std::memcpy(wp.data(), win_ptr, sizeof(int32_t) * wp.size());
     } else {
@@ -605,7 +605,7 @@ spx_status spx_wcsr_plan_upload(spx_wcsr_plan* P, void* table, size_t table_byte
         e = cudaMemcpyAsync(d + sizeof(int32_t) * P->tasks.size(), P->splits.data(), sizeof(int32_t) * P->splits.size(),
                             cudaMemcpyHostToDevice, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return SPX_ERR_CUDA;
+    if (e != cudaSuccess) return spx_cuda_status(e);
     P->d_table = table;
     return SPX_OK;
 }
